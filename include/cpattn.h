@@ -329,6 +329,62 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
                             void* stream);
 
 /*
+ * cp_qk_norm_rope_fwd / cp_qk_norm_rope_bwd -- RMS norm of every query and key
+ * head and the position rotation, in one pass over q and k, and its gradient.
+ * The pages take q and k as given; in the models they train these two steps
+ * come right before the attention.
+ *
+ *   r = 1 / sqrt(mean_e x_e^2 + eps),  z = (x r) w,  y = R z
+ *
+ * with w the weight of q or of k (shared by its heads; NULL = ones) and R the
+ * rotation of rot_dim / 2 element pairs: pair p turns by positions[a][t] *
+ * inv_freq[p], where a is the axis that pair p belongs to (sections[0] pairs
+ * read axis 0, the next sections[1] pairs axis 1, ...).  Several axes give image
+ * tokens a time, a row and a column position.  Pairs are elements (p, p +
+ * rot_dim / 2), or (2p, 2p + 1) with `interleaved`; elements from rot_dim on
+ * are normed and not rotated.  Angles are exact for every int32 position (they
+ * are reduced to turns in integers).  All arithmetic is fp32, rounded once.
+ *
+ *   q [T][H][d], k [T][H_kv][d]   strides in elements (last dimension
+ *                   contiguous), e.g. views of one projection's output; rows
+ *                   on 16-byte boundaries take vector loads, others element loads
+ *   positions       device int32 [n_axes][T]; any value
+ *   q_weight, k_weight   NULL or [d], weight_dtype
+ *   q_out, k_out    contiguous, dtype, 16-byte aligned; must not overlap an input
+ *   dq_out, dk_out  gradients of q_out, k_out: contiguous, dtype, 16-byte aligned
+ *   dq, dk          gradients of q, k: contiguous, dtype, 16-byte aligned
+ *   dq_weight, dk_weight   NULL or [d] fp32: sums over every row and head, in an
+ *                   order that does not depend on timing
+ *   workspace       backward with a weight gradient: >=
+ *                   cp_qk_norm_rope_bwd_workspace_size(desc) bytes, 256-byte
+ *                   aligned, written before it is read
+ * T == 0: no rows are touched; the weight gradients are zeroed.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE (d not 64 or 128, rot_dim, sections),
+ * CP_ERR_DTYPE, CP_ERR_ALIGNMENT, CP_ERR_WORKSPACE, CP_ERR_CUDA.
+ */
+typedef struct {
+  cp_dtype_t dtype;          /* of q, k and everything shaped like them */
+  cp_dtype_t weight_dtype;   /* of q_weight, k_weight */
+  int T, H, H_kv, d;         /* d: 64 or 128 */
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+  int rot_dim;               /* multiple of 16 in [0, d] */
+  int interleaved;
+  int n_axes;                /* 1 .. 4 */
+  int sections[4];           /* pairs of each axis; sum = rot_dim / 2 */
+  const double* inv_freq;    /* HOST array, rot_dim / 2 radians per position */
+  float eps;
+} cp_norm_rope_t;
+cp_status_t cp_qk_norm_rope_fwd(const cp_norm_rope_t* desc, const void* q, const void* k,
+                                const int32_t* positions, const void* q_weight,
+                                const void* k_weight, void* q_out, void* k_out, void* stream);
+size_t cp_qk_norm_rope_bwd_workspace_size(const cp_norm_rope_t* desc);
+cp_status_t cp_qk_norm_rope_bwd(const cp_norm_rope_t* desc, const void* q, const void* k,
+                                const int32_t* positions, const void* q_weight,
+                                const void* k_weight, const void* dq_out, const void* dk_out,
+                                void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * cp_workspace_status -- synchronise `stream` and report whether a kernel of
  * the last cp_attn_fwd / cp_attn_bwd call that used `workspace` gave up on a
  * bounded device wait (CP_ERR_TIMEOUT), met an index outside a tensor

@@ -10,6 +10,8 @@ Functions keep the names of the C entry points:
 * :func:`cp_zigzag_index`, :func:`cp_zigzag_gather`, :func:`cp_zigzag_scatter`
 * :func:`cp_attn_fwd`, :func:`cp_lse_merge`, :func:`cp_attn_bwd`
 * :func:`cp_attn_fwd_gqa`, :func:`cp_attn_bwd_gqa` -- grouped KV heads
+* :func:`cp_qk_norm_rope_fwd`, :func:`cp_qk_norm_rope_bwd` -- norm of query and key
+  heads with the position rotation
 * :func:`cp_workspace_status`, :func:`cp_set_wait_limit`, :func:`cp_plan_pairs`,
   :func:`cp_plan_unit_lists`
 * :func:`attention_host` -- end-to-end call on host (pinned) tensors.
@@ -28,7 +30,7 @@ __all__ = ["cp_zigzag_index", "cp_zigzag_gather", "cp_zigzag_scatter", "cp_attn_
            "cp_attn_fwd_noalloc", "cp_attn_fwd_gqa", "cp_attn_bwd_gqa",
            "cp_lse_merge", "cp_attn_bwd", "cp_workspace_status", "cp_set_wait_limit",
            "cp_plan_pairs", "cp_plan_unit_lists", "cp_profile_begin", "cp_profile_end", "Workspace",
-           "attention_host", "CpError"]
+           "attention_host", "CpError", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd"]
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -522,3 +524,6 @@ def attention_host(q, k, v, dout, cu_seqlens, P: int, prefix_len: int, softmax_s
     up.synchronize()
     comp.synchronize()
     return tuple(host_out[:n_res])
+
+
+from .norm_rope import cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd  # noqa: E402

@@ -27,6 +27,18 @@ STATUS = {0: "CP_OK", 1: "CP_ERR_INVALID_ARG", 2: "CP_ERR_SHAPE", 3: "CP_ERR_DTY
           8: "CP_ERR_UNSUPPORTED", 9: "CP_ERR_BOUNDS"}
 CP_F32, CP_BF16 = 0, 1
 
+
+class NormRopeDesc(ctypes.Structure):
+    """cp_norm_rope_t."""
+    _fields_ = [("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("T", ctypes.c_int),
+                ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("d", ctypes.c_int),
+                ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("eps", ctypes.c_float)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "cp_last_error": (ctypes.c_char_p, []),
@@ -76,6 +88,10 @@ SIGNATURES = {
                                    ctypes.c_int, ctypes.c_int, c_i32p, ctypes.c_int, ctypes.c_int,
                                    ctypes.c_int, ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp,
                                    ctypes.c_size_t, c_vp]),
+    "cp_qk_norm_rope_fwd": (ctypes.c_int, [ctypes.POINTER(NormRopeDesc)] + [c_vp] * 8),
+    "cp_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NormRopeDesc)]),
+    "cp_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(NormRopeDesc)] + [c_vp] * 12 +
+                            [ctypes.c_size_t, c_vp]),
     "cp_workspace_status": (ctypes.c_int, [c_vp, c_vp]),
     "cp_plan_pairs": (ctypes.c_int, [c_i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, c_i64p,
                                      c_i64p, c_i64p, c_i64p]),

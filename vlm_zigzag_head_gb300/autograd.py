@@ -21,8 +21,9 @@ from __future__ import annotations
 from typing import Callable, Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import cp_attn_bwd, cp_attn_fwd
+from . import cp_attn_bwd, cp_attn_fwd, cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd
 
 
 class CPAttention(torch.autograd.Function):
@@ -76,3 +77,45 @@ def cp_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     if softmax_scale is None:
         softmax_scale = q.shape[-1] ** -0.5
     return CPAttention.apply(q, k, v, cu_seqlens, P, prefix_len, softmax_scale, prefix_hook)
+
+
+def _dense(g: torch.Tensor) -> torch.Tensor:
+    """A contiguous, 16-byte aligned gradient (autograd may hand over any view)."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
+class QKNormRope(torch.autograd.Function):
+    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, options)``."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, q_weight, k_weight, options):
+        ctx.save_for_backward(q, k, positions, q_weight, k_weight)
+        ctx.options = options
+        return cp_qk_norm_rope_fwd(q, k, positions, q_weight, k_weight, **options)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, positions, q_weight, k_weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dq, dk, dqw, dkw = cp_qk_norm_rope_bwd(
+            q, k, positions, _dense(dq_out), _dense(dk_out), q_weight, k_weight,
+            **ctx.options)
+        return (dq if need[0] else None, dk if need[1] else None, None,
+                dqw.to(q_weight.dtype) if need[3] else None,
+                dkw.to(k_weight.dtype) if need[4] else None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
+                 q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                 theta: float = 10000.0, rot_dim: Optional[int] = None,
+                 sections: Optional[Sequence[int]] = None, interleaved: bool = False,
+                 inv_freq: Optional[Sequence[float]] = None):
+    """Differentiable :func:`cp_qk_norm_rope_fwd`: RMS norm of every head of q and k
+    and the position rotation, in one pass.  Returns contiguous ``(q_out, k_out)``,
+    ready for :func:`cp_attention`; gradients flow to q, k and the weights."""
+    options = dict(eps=eps, theta=theta, rot_dim=rot_dim, sections=sections,
+                   interleaved=interleaved, inv_freq=inv_freq)
+    return QKNormRope.apply(q, k, positions, q_weight, k_weight, options)
