@@ -385,6 +385,94 @@ cp_status_t cp_qk_norm_rope_bwd(const cp_norm_rope_t* desc, const void* q, const
                                 void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * cp_score_plan_* -- work lists of attention with modified scores.
+ * They depend on the packing alone: build the block on the host once per
+ * packing, copy it to the device (256-byte aligned) and pass both copies to
+ * every call; calls on any stream may share it, and nothing writes to it.
+ *
+ *   cu_seqlens_h   HOST, n_seqs + 1 ascending int32 from 0; samples of any
+ *                  length, empty ones too (the P ranks are partitions of one
+ *                  memory and a row sees the same keys whichever rank owns
+ *                  them: these calls take no P and no divisibility by 2P)
+ *   prefix_lens_h  NULL or HOST [n_seqs]: tokens of each sample's image prefix
+ *   bidirectional  nonzero: prefix tokens see the whole prefix of their sample
+ *                  instead of the causal part (CP-VLM page section 2's layout
+ *                  [image tokens, text tokens]; the page's own mask is causal)
+ *   n_sms          multiprocessors of the device that will run the calls
+ *   buckets_h      NULL or HOST [n_dist]: bucket of distance 0 .. n_dist - 1 of
+ *                  a learned bias; larger distances take the last entry's
+ * cp_score_plan_size returns 0 on bad arguments (cp_last_error says why);
+ * cp_score_plan_build: CP_ERR_SHAPE, CP_ERR_WORKSPACE, CP_ERR_ALIGNMENT.
+ * cp_score_plan_pairs: visible pairs per head that the forward, the backward
+ * and the fp32 work lists of a plan cover (host only, for tests).
+ */
+size_t cp_score_plan_size(const int32_t* cu_seqlens_h, int n_seqs, const int32_t* prefix_lens_h,
+                          int bidirectional, int H, int n_sms, const int32_t* buckets_h,
+                          int n_dist);
+cp_status_t cp_score_plan_build(const int32_t* cu_seqlens_h, int n_seqs,
+                                const int32_t* prefix_lens_h, int bidirectional, int H, int n_sms,
+                                const int32_t* buckets_h, int n_dist, void* block, size_t bytes);
+cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, int64_t* tiles);
+
+/*
+ * cp_attn_scored_fwd / cp_attn_scored_bwd -- packed causal attention with
+ * modified scores, and its gradient.
+ *
+ *   x_ij = softmax_scale q_i . k_j
+ *   x_ij = softcap tanh(x_ij / softcap)                       softcap > 0
+ *   x_ij -= slopes[h] |i - j|                                 slopes
+ *   x_ij += rel_bias[h][bucket(|i - j|)]                      rel_bias
+ *   out_i = sum_j softmax_j(x_ij) v_j over the visible j,  lse_i = log sum_j e^x_ij
+ *
+ * j is visible to i in the same sample when j <= i, or when both lie in a
+ * bidirectional prefix.  rel_bias entries at or below -1e37 (the type's lowest
+ * value, minus infinity) hide the pair; a row that sees no key has out 0, lse
+ * -inf and no gradient.  Entries and slopes are otherwise finite, and so are q, k, v:
+ * a NaN or infinity in a key or value row may reach every row of the 128-row
+ * tiles that hold it.
+ *
+ *   q, out, dout [T][H][d], k, v [T][H_kv][d], lse [H][T], dq, dk, dv fp32: as
+ *                cp_attn_fwd_gqa / cp_attn_bwd_gqa, with T and H those of the plan
+ *   dt           CP_BF16: tensor cores (f16 operands above softmax_scale 0.25, as
+ *                cp_attn_fwd); CP_F32: CUDA cores, fp32 throughout
+ *   score        slopes: NULL or device [H] fp32.  rel_bias: NULL or device, H x
+ *                n_buckets, any strides (in elements).  softcap: 0 or in
+ *                [1e-3, 1e4].  slopes and rel_bias exclude one another.
+ *   dbias        NULL or [H][n_buckets] fp32 contiguous: gradient of rel_bias
+ *   workspace    >= cp_attn_scored_{fwd,bwd}_workspace_size bytes, 256-byte
+ *                aligned, of this call's own while it runs; its status word is
+ *                read by cp_workspace_status
+ * Every call is launches and memsets alone (no copy from the host), so it can
+ * be captured into a graph.  dQ, dbias and, with few work items and grouped
+ * heads, dK and dV are summed by fp32 atomics: their last bits vary from run to run.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE, CP_ERR_DTYPE, CP_ERR_ALIGNMENT,
+ * CP_ERR_WORKSPACE, CP_ERR_CUDA, CP_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  float softcap;
+  const float* slopes;
+  const void* rel_bias;
+  cp_dtype_t bias_dtype;
+  int64_t bias_stride_h, bias_stride_b;
+  int n_buckets;
+} cp_score_t;
+size_t cp_attn_scored_fwd_workspace_size(const void* plan_h, cp_dtype_t dt, int H_kv, int d,
+                                         float softmax_scale);
+size_t cp_attn_scored_bwd_workspace_size(const void* plan_h, cp_dtype_t dt, int H_kv, int d,
+                                         float softmax_scale);
+cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const void* q,
+                               const void* k, const void* v, cp_dtype_t dt, int T, int H, int H_kv,
+                               int d, const cp_score_t* score, float softmax_scale, void* out,
+                               float* lse, void* out_lo, void* workspace, size_t ws_bytes,
+                               void* stream);
+cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const void* q,
+                               const void* k, const void* v, const void* out, const void* out_lo,
+                               const float* lse, const void* dout, cp_dtype_t dt, int T, int H,
+                               int H_kv, int d, const cp_score_t* score, float softmax_scale,
+                               float* dq, float* dk, float* dv, float* dbias, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
  * cp_workspace_status -- synchronise `stream` and report whether a kernel of
  * the last cp_attn_fwd / cp_attn_bwd call that used `workspace` gave up on a
  * bounded device wait (CP_ERR_TIMEOUT), met an index outside a tensor

@@ -74,8 +74,8 @@ class Scores(NamedTuple):
     bidirectional: bool = False               # the prefix attends to itself in both directions
 
 
-#: A bias at or below this hides the key, as minus infinity does.
-HIDDEN = -1e37
+#: A bias at or below this (the fp32 number nearest -1e37) hides the key, as minus infinity does.
+HIDDEN = float(np.float32(-1e37))
 
 
 def _sample_scores(q, k, scale, s: Scores, h, prefix):

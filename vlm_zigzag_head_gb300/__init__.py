@@ -12,6 +12,8 @@ Functions keep the names of the C entry points:
 * :func:`cp_attn_fwd_gqa`, :func:`cp_attn_bwd_gqa` -- grouped KV heads
 * :func:`cp_qk_norm_rope_fwd`, :func:`cp_qk_norm_rope_bwd` -- norm of query and key
   heads with the position rotation
+* :func:`cp_attn_scored_fwd`, :func:`cp_attn_scored_bwd` (plans: :class:`ScorePlan`) --
+  attention with capped or distance-biased scores
 * :func:`cp_workspace_status`, :func:`cp_set_wait_limit`, :func:`cp_plan_pairs`,
   :func:`cp_plan_unit_lists`
 * :func:`attention_host` -- end-to-end call on host (pinned) tensors.
@@ -30,7 +32,8 @@ __all__ = ["cp_zigzag_index", "cp_zigzag_gather", "cp_zigzag_scatter", "cp_attn_
            "cp_attn_fwd_noalloc", "cp_attn_fwd_gqa", "cp_attn_bwd_gqa",
            "cp_lse_merge", "cp_attn_bwd", "cp_workspace_status", "cp_set_wait_limit",
            "cp_plan_pairs", "cp_plan_unit_lists", "cp_profile_begin", "cp_profile_end", "Workspace",
-           "attention_host", "CpError", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd"]
+           "attention_host", "CpError", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd",
+           "cp_attn_scored_fwd", "cp_attn_scored_bwd", "ScorePlan", "relative_buckets"]
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -527,3 +530,5 @@ def attention_host(q, k, v, dout, cu_seqlens, P: int, prefix_len: int, softmax_s
 
 
 from .norm_rope import cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd  # noqa: E402
+from .scored import (ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd,  # noqa: E402
+                     relative_buckets)

@@ -39,6 +39,18 @@ class NormRopeDesc(ctypes.Structure):
                 ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("eps", ctypes.c_float)]
 
 
+class ScoreDesc(ctypes.Structure):
+    """cp_score_t."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", c_vp), ("rel_bias", c_vp),
+                ("bias_dtype", ctypes.c_int), ("bias_stride_h", ctypes.c_int64),
+                ("bias_stride_b", ctypes.c_int64), ("n_buckets", ctypes.c_int)]
+
+
+_PLAN = [c_i32p, ctypes.c_int, c_i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, c_i32p,
+         ctypes.c_int]
+_SCORED_WS = (ctypes.c_size_t, [c_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float])
+_SCORED_SHAPE = [ctypes.c_int] * 5 + [ctypes.POINTER(ScoreDesc), ctypes.c_float]
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "cp_last_error": (ctypes.c_char_p, []),
@@ -92,6 +104,15 @@ SIGNATURES = {
     "cp_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NormRopeDesc)]),
     "cp_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(NormRopeDesc)] + [c_vp] * 12 +
                             [ctypes.c_size_t, c_vp]),
+    "cp_score_plan_size": (ctypes.c_size_t, _PLAN),
+    "cp_score_plan_build": (ctypes.c_int, _PLAN + [c_vp, ctypes.c_size_t]),
+    "cp_score_plan_pairs": (ctypes.c_int, [c_vp, c_i64p, c_i64p, c_i64p]),
+    "cp_attn_scored_fwd_workspace_size": _SCORED_WS,
+    "cp_attn_scored_bwd_workspace_size": _SCORED_WS,
+    "cp_attn_scored_fwd": (ctypes.c_int, [c_vp] * 5 + _SCORED_SHAPE + [c_vp] * 4 +
+                           [ctypes.c_size_t, c_vp]),
+    "cp_attn_scored_bwd": (ctypes.c_int, [c_vp] * 9 + _SCORED_SHAPE + [c_vp] * 5 +
+                           [ctypes.c_size_t, c_vp]),
     "cp_workspace_status": (ctypes.c_int, [c_vp, c_vp]),
     "cp_plan_pairs": (ctypes.c_int, [c_i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, c_i64p,
                                      c_i64p, c_i64p, c_i64p]),

@@ -23,7 +23,8 @@ from typing import Callable, Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import cp_attn_bwd, cp_attn_fwd, cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd
+from . import (ScorePlan, cp_attn_bwd, cp_attn_fwd, cp_attn_scored_bwd, cp_attn_scored_fwd,
+               cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd)
 
 
 class CPAttention(torch.autograd.Function):
@@ -119,3 +120,46 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     options = dict(eps=eps, theta=theta, rot_dim=rot_dim, sections=sections,
                    interleaved=interleaved, inv_freq=inv_freq)
     return QKNormRope.apply(q, k, positions, q_weight, k_weight, options)
+
+
+class CPAttentionScored(torch.autograd.Function):
+    """``(out, lse) = CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan,
+    softmax_scale, softcap)``.  lse and slopes are not differentiable."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, rel_bias, slopes, plan, softmax_scale, softcap):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        # the bf16 remainder of the output keeps D = dO.O exact in the backward
+        train = any(ctx.needs_input_grad) and q.dtype == torch.bfloat16
+        out, lse, *lo = cp_attn_scored_fwd(q, k, v, plan, softmax_scale, softcap, slopes,
+                                           rel_bias, residual=train)
+        ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, lo[0] if lo else None)
+        ctx.meta = (plan, softmax_scale, softcap)
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, _dlse):
+        q, k, v, rel_bias, slopes, out, lse, out_lo = ctx.saved_tensors
+        plan, scale, softcap = ctx.meta
+        got = cp_attn_scored_bwd(q, k, v, out, lse, _dense(dout.to(q.dtype)), plan, scale,
+                                 softcap, slopes, rel_bias, out_lo=out_lo)
+        grads = [g.to(x.dtype) if need else None
+                 for g, x, need in zip(got, (q, k, v, rel_bias), ctx.needs_input_grad)]
+        return (*grads, *([None] * (8 - len(grads))))
+
+
+def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: ScorePlan,
+                        softmax_scale: Optional[float] = None, *, softcap: float = 0.0,
+                        slopes: Optional[torch.Tensor] = None,
+                        rel_bias: Optional[torch.Tensor] = None):
+    """Differentiable packed causal attention with modified scores (see
+    :func:`cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
+    bidirectional prefix.  Returns ``(out, lse)``; gradients flow to q, k, v and
+    ``rel_bias``.  ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the
+    backward into a graph, call :func:`cp_attn_scored_bwd`, which involves no leaves."""
+    if softmax_scale is None:
+        softmax_scale = q.shape[-1] ** -0.5
+    return CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan, float(softmax_scale),
+                                   float(softcap))

@@ -17,6 +17,7 @@
 
 #include "../../include/cpattn.h"
 #include "check.cuh"
+#include "entry.h"
 #include "kernels.h"
 #include "plan.h"
 #include "tc.h"
@@ -341,26 +342,7 @@ std::mutex g_prof_mu;
 std::atomic<bool> g_prof_on{false};
 std::vector<ProfRec> g_prof;
 
-struct ProfScope {
-  int kind;
-  cudaStream_t st;
-  cudaEvent_t a = nullptr, b = nullptr;
-  int count;
-  ProfScope(int k, cudaStream_t s, int n = 1) : kind(k), st(s), count(n) {
-    if (!g_prof_on.load()) return;
-    if (cudaEventCreate(&a) != cudaSuccess || cudaEventCreate(&b) != cudaSuccess) {
-      a = b = nullptr;
-      return;
-    }
-    cudaEventRecord(a, st);
-  }
-  ~ProfScope() {
-    if (!a) return;
-    cudaEventRecord(b, st);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof.push_back({kind, a, b, count});
-  }
-};
+using ProfScope = ProfileScope;
 
 }  // namespace
 
@@ -370,6 +352,21 @@ cudaError_t noalloc_read_status(int32_t out[2]);   // noalloc.cu
 // point): the thread-local error message and the device wait bound.
 void set_last_error(const std::string& msg) { g_err = msg; }
 long long device_wait_limit() { return wait_limit(); }
+
+ProfileScope::ProfileScope(int k, cudaStream_t s, int n) : kind(k), st(s), count(n) {
+  if (!g_prof_on.load()) return;
+  if (cudaEventCreate(&a) != cudaSuccess || cudaEventCreate(&b) != cudaSuccess) {
+    a = b = nullptr;
+    return;
+  }
+  cudaEventRecord(a, st);
+}
+ProfileScope::~ProfileScope() {
+  if (!a) return;
+  cudaEventRecord(b, st);
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  g_prof.push_back({kind, a, b, count});
+}
 }  // namespace cpattn
 
 extern "C" {
@@ -754,19 +751,12 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
   const BwdItem* items = reinterpret_cast<const BwdItem*>(w + L.items);
   if (tc) {
     CP_CUDA(cudaMemsetAsync(dq, 0, (size_t)T * H * d * sizeof(float), st), "clear dq");
-    // With grouped KV heads one CTA walks all G query heads of its KV head.
-    // When that leaves too few CTAs to fill the GPU (under ~4 per SM), the
-    // group is shared by kv_split CTAs whose partial dK / dV are reduce-added
-    // into zeroed memory.
-    const int G = H / Hkv;
-    int kv_split = 1;
-    {
-      int dev = 0, sms = 0;
-      CP_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-      CP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count");
-      const double per_launch = (double)bitems.size() * Hkv;
-      while (G % (2 * kv_split) == 0 && per_launch * kv_split < 4.0 * sms) kv_split *= 2;
-    }
+    // A group shared by kv_split CTAs reduce-adds its partial dK / dV into
+    // zeroed memory.
+    int dev = 0, sms = 0;
+    CP_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+    CP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count");
+    const int kv_split = bwd_kv_split((int64_t)bitems.size(), H, Hkv, sms);
     if (kv_split > 1) {
       CP_CUDA(cudaMemsetAsync(dk, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dk");
       CP_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");

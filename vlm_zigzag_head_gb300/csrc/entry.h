@@ -18,6 +18,21 @@ inline cp_status_t entry_fail(cp_status_t s, const std::string& msg) {
   return s;
 }
 
+// Records CUDA events around the launches of a scope while profiling is on
+// (cp_profile_begin; kinds as documented there).
+struct ProfileScope {
+  ProfileScope(int kind, cudaStream_t st, int launches = 1);
+  ~ProfileScope();
+  ProfileScope(const ProfileScope&) = delete;
+  ProfileScope& operator=(const ProfileScope&) = delete;
+
+ private:
+  int kind;
+  cudaStream_t st;
+  cudaEvent_t a = nullptr, b = nullptr;
+  int count;
+};
+
 #define ENTRY_CUDA(call, what)                                                                   \
   do {                                                                                           \
     cudaError_t e_ = (call);                                                                     \

@@ -256,7 +256,9 @@ __global__ void __launch_bounds__(kThreads) bwd_pre_kernel(const T* __restrict__
     for (int sh = lpr >> 1; sh > 0; sh >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, sh);
     if (valid && sl == 0) {
       D[(long long)h * pitch + t] = acc;
-      lse2[(long long)h * pitch + t] = lse[(long long)h * Tn + t] * 1.4426950408889634f;
+      // a row that saw no key (lse -inf) gets +inf: its probabilities are then 0
+      const float lr = lse[(long long)h * Tn + t];
+      lse2[(long long)h * pitch + t] = lr == -INFINITY ? INFINITY : lr * 1.4426950408889634f;
     }
   }
 }

@@ -31,8 +31,11 @@ enum : int32_t { DK_TEXT = 0, DK_PREFIX_SLOT = 1 };  // backward dK/dV destinati
 // A run of `len` consecutive rows starting at `row0` of tensor `src`.
 // causal != 0: key u of the key run is visible to query t of the query run
 // iff u <= t + delta (positions inside the same chunk / prefix).
+// rel: position of the query run's first row minus that of the key run's first
+// row in their sample (the scored kernels' distances; the zigzag plans, whose
+// kernels know no distances, leave it 0).
 struct Seg {
-  int32_t row0, len, src, causal, delta, pad0, pad1, pad2;
+  int32_t row0, len, src, causal, delta, rel, pad1, pad2;
 };
 
 // Forward: one query tile (<= kFwdTileQ rows) against up to kMaxSeg key runs.

@@ -1,0 +1,40 @@
+// Launchers of attention with modified scores that are not tensor-core kernels:
+// the distance tables and the fp32 path.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "scored_plan.h"
+
+namespace cpattn {
+
+// ---- learned bias by bucket <-> table by distance (scored_bias.cu) --------------
+// table[h][mid + s] = mul * bias[h][bucket[min(|s|, n_dist - 1)]] for |s| <= mid;
+// entries at or below -1e37 become -inf (the key is hidden).
+cudaError_t launch_expand_bias(const void* bias, bool bf16, int64_t stride_h, int64_t stride_b,
+                               const int32_t* buckets, int n_dist, int H, float mul, float* table,
+                               int mid, int pitch, cudaStream_t st);
+// dbias[h][b] = sum of dtable[h][t] over the distances of bucket b, in order.
+cudaError_t launch_reduce_dbias(const float* dtable, const int32_t* buckets, int n_dist,
+                                int n_buckets, int H, float* dbias, cudaStream_t st);
+
+// ---- fp32 inputs: CUDA cores (attn_f32.cu) ---------------------------------------
+struct F32Args {
+  const float *q, *k, *v, *dout;       // [T][H or Hkv][d]
+  const Tile32* tiles;
+  int n_tiles, H, Hkv;
+  int64_t T;
+  float scale, softcap;                // softcap 0: none
+  const float* slopes;                 // nullable [H]
+  const float* table;                  // nullable [H][pitch], natural units
+  int table_pitch, table_mid, n_dist;
+  float* out; float* lse;              // forward
+  const float* lse_in; const float* D; // backward; D [H][pitch_d]
+  int64_t pitch_d;
+  float *dq, *dk, *dv;
+  float* dtable;                       // nullable [H][n_dist]
+};
+cudaError_t launch_f32_fwd(const F32Args& a, int d, cudaStream_t st);
+cudaError_t launch_f32_bwd(const F32Args& a, int d, cudaStream_t st);
+
+}  // namespace cpattn

@@ -1,0 +1,52 @@
+// Work lists of attention with modified scores.
+//
+// The P simulated ranks are partitions of one memory and a query row sees the
+// same keys whichever rank owns them, so these lists walk every sample's rows in
+// natural order: no gather, one key run per query tile, one query run per key
+// tile, and distances are differences of positions.  A plan is one flat block,
+// built on the host, that the caller copies to the device once and keeps for
+// every call with the same packing.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "plan.h"
+
+namespace cpattn {
+
+constexpr int kTile32 = 64;   // rows of one tile of the fp32 kernels
+
+// One 64-row tile of a sample (fp32 kernels; queries and keys alike).
+struct Tile32 {
+  int32_t row0, len;     // natural rows [row0, row0 + len)
+  int32_t seq0, seq_len; // the sample's rows
+  int32_t prefix;        // rows that see one another in both directions (0: causal)
+  int32_t pad[3];
+};
+static_assert(sizeof(Tile32) == 32, "Tile32 layout");
+
+constexpr uint32_t kScorePlanMagic = 0x43505350u;
+constexpr int kMaxDist = 1 << 16;
+
+// At the start of the block; offsets are bytes from there.
+struct ScorePlanHeader {
+  uint32_t magic;
+  int32_t T, H, n_seqs, bidirectional;
+  int32_t n_dist, n_buckets;       // 0: no table
+  int32_t n_fwd, n_bwd, n_tiles;
+  int32_t n_units, grid;           // n_units 0: one CTA per unit
+  uint64_t fwd, bwd, runs, units, buckets, tiles, total;
+};
+static_assert(sizeof(ScorePlanHeader) <= 256, "plan header");
+
+// Checks the arguments ("" or a message) and fills `h` without building.
+std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* prefix_lens,
+                              bool bidirectional, int H, int sms, const int32_t* buckets,
+                              int n_dist, ScorePlanHeader* h);
+// Writes the block (h.total bytes).
+void score_plan_build(const ScorePlanHeader& h, const int32_t* cu, const int32_t* prefix_lens,
+                      const int32_t* buckets, void* block);
+
+}  // namespace cpattn

@@ -33,6 +33,21 @@ bool make_tmap_f32_sw128(CUtensorMap* map, void* base, int64_t rows, int H, int 
 bool make_tmap_ld(CUtensorMap* map, const void* base, int64_t pitch, int H, int box_rows,
                   const char** err);
 
+// Scores modified before the softmax (score.cuh).  kBias of the kernels:
+enum : int { SCORE_PLAIN = 0, SCORE_SLOPES = 1, SCORE_TABLE = 2 };
+struct ScoreArgs {
+  float cap_log2, inv_cap_log2;   // softcap * log2(e) and its inverse (kCap)
+  const float* slopes;            // SCORE_SLOPES: [H], natural units
+  // SCORE_TABLE: [H][table_pitch] bias * log2(e) by signed distance: entry
+  // table_mid + distance, |distance| <= table_mid; constant from n_dist - 1 on
+  const float* table;
+  int n_dist, table_pitch, table_mid;
+  float* dtable;                  // backward: [H][n_dist], sums of dS by |distance|
+};
+// Entries of the table past +-n_dist: a 128 x 128 tile that holds a distance
+// below n_dist spans 254 more, so it reads the table without bounds checks.
+constexpr int kTableSlack = 256;
+
 struct TcFwdArgs {
   CUtensorMap tm_q_text, tm_k_text, tm_v_text;  // rank-local (gathered) text rows
   CUtensorMap tm_q_nat, tm_k_nat, tm_v_nat;     // natural order (prefix rows)
@@ -56,6 +71,7 @@ struct TcFwdArgs {
   int32_t* status;            // DevStatus of the workspace
   long long wait_limit;
   int64_t text_rows;          // rows of the rank-local (gathered) tensors (index checks)
+  ScoreArgs score;            // read by the scored kernels only
 };
 cudaError_t launch_tc_fwd(const TcFwdArgs& a, cudaStream_t st);
 
@@ -80,9 +96,24 @@ struct TcBwdArgs {
   int kv_split;               // CTAs sharing one KV head's query heads (divides H / Hkv); > 1:
                               // dK / dV / prefix slots are reduce-added into zeroed memory
   int n_slots;                // prefix-gradient slots (P + 1) behind pre_k / pre_v (index checks)
+  ScoreArgs score;            // read by the scored kernels only
 };
 // The backward (tc_bwd_q128.cu): one launch over the all-steps plan, every
 // item a key tile with the query runs of all ring steps, in 128-query tiles.
 cudaError_t launch_tc_bwd_q128(const TcBwdArgs& a, cudaStream_t st);
+
+// With grouped KV heads one CTA walks all G = H / Hkv query heads of its KV
+// head.  When that leaves too few CTAs to fill the GPU (under ~4 per SM), the
+// group is shared by this many CTAs (a power of two dividing G).
+inline int bwd_kv_split(int64_t n_items, int H, int Hkv, int sms) {
+  const int G = H / Hkv;
+  int split = 1;
+  while (G % (2 * split) == 0 && (double)n_items * Hkv * split < 4.0 * sms) split *= 2;
+  return split;
+}
+// The same kernels with modified scores: items carry the distance of their
+// first query and key in Seg::rel.  score.cap_log2 > 0: capped.
+cudaError_t launch_tc_fwd_scored(const TcFwdArgs& a, int bias, cudaStream_t st);
+cudaError_t launch_tc_bwd_scored(const TcBwdArgs& a, int bias, cudaStream_t st);
 
 }  // namespace cpattn

@@ -1,0 +1,21 @@
+// Launches of the backward with modified scores (tc_bwd_q128.cuh) for one head size.
+#pragma once
+#include "tc_bwd_q128.cuh"
+
+namespace cpattn {
+
+// One instantiation serves both a whole group per CTA and shared groups: the
+// epilogue asks kv_split.
+template <int D, bool kF16>
+cudaError_t launch_bwd_scored_d(const TcBwdArgs& a, int bias, cudaStream_t st) {
+  if (a.score.cap_log2 > 0.f) {
+    if (bias == SCORE_SLOPES) return launch_q128<D, kF16, true, true, SCORE_SLOPES>(a, st);
+    if (bias == SCORE_TABLE) return launch_q128<D, kF16, true, true, SCORE_TABLE>(a, st);
+    return launch_q128<D, kF16, true, true, SCORE_PLAIN>(a, st);
+  }
+  if (bias == SCORE_SLOPES) return launch_q128<D, kF16, true, false, SCORE_SLOPES>(a, st);
+  if (bias == SCORE_TABLE) return launch_q128<D, kF16, true, false, SCORE_TABLE>(a, st);
+  return cudaErrorInvalidValue;   // plain scores: launch_tc_bwd_q128
+}
+
+}  // namespace cpattn
