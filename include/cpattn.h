@@ -347,7 +347,8 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
  *
  *   q [T][H][d], k [T][H_kv][d]   strides in elements (last dimension
  *                   contiguous), e.g. views of one projection's output; rows
- *                   on 16-byte boundaries take vector loads, others element loads
+ *                   whose groups of four elements lie on boundaries of their size
+ *                   (8 bytes of bf16) take vector loads, others element loads
  *   positions       device int32 [n_axes][T]; any value
  *   q_weight, k_weight   NULL or [d], weight_dtype
  *   q_out, k_out    contiguous, dtype, 16-byte aligned; must not overlap an input

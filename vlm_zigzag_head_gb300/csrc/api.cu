@@ -550,7 +550,7 @@ cp_status_t cp_attn_fwd_gqa(const void* q, const void* k, const void* v, cp_dtyp
   float* o_run = reinterpret_cast<float*>(w + L.o_run);
   float* lse_run = reinterpret_cast<float*>(w + L.lse_run);
   if (tc) {
-    TcFwdArgs a;
+    TcFwdArgs a{};
     const char* terr = nullptr;
     const int64_t PR = pb.text_rows;
     bool ok = make_tmap_thd(&a.tm_q_text, dst[0], PR, H, d, 128, &terr) &&
@@ -765,7 +765,7 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
                                 st),
                 "clear prefix slots");
     }
-    TcBwdArgs a;
+    TcBwdArgs a{};
     const char* terr = nullptr;
     constexpr int tq = 128;   // query rows per tile
     bool ok = make_tmap_thd(&a.tm_q, f16 ? q16 : q, T, H, d, tq, &terr, f16) &&

@@ -99,10 +99,9 @@ cp_status_t setup(const cp_norm_rope_t* p, const void* q, const void* k, const i
     const double frac = std::ldexp(turns - std::floor(turns), 64);
     a.freq[i] = frac < 18446744073709551616.0 ? (uint64_t)frac : 0;
   }
-  // 16-byte loads where every row of eight elements starts on a 16-byte boundary
-  const int64_t unit = 16 / (int64_t)elem;
-  o->vec = aligned_to(q, 16) && aligned_to(k, 16);
-  for (int i = 0; i < 2; ++i) o->vec = o->vec && a.st[i] % unit == 0 && a.sh[i] % unit == 0;
+  // vector loads where every group of four elements lies on a boundary of its size
+  o->vec = aligned_to(q, 4 * elem) && aligned_to(k, 4 * elem);
+  for (int i = 0; i < 2; ++i) o->vec = o->vec && a.st[i] % 4 == 0 && a.sh[i] % 4 == 0;
   return CP_OK;
 }
 

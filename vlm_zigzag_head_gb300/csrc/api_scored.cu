@@ -440,6 +440,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.status = reinterpret_cast<int32_t*>(w);
     a.wait_limit = device_wait_limit();
     a.kv_split = kv_split;
+    a.item_major = item_major((int64_t)c.h->n_bwd * Hkv * kv_split, sms) ? 1 : 0;
     a.f16 = c.f16 ? 1 : 0;
     a.op_scales = c.f16 ? sc : nullptr;
     a.score = s;

@@ -204,7 +204,7 @@ extern "C" cp_status_t cp_attn_fwd_noalloc(const void* q, const void* k, const v
           "zigzag gather");
   const FwdItem* items = reinterpret_cast<const FwdItem*>(w + o_items);
   if (bf16) {
-    TcFwdArgs a;
+    TcFwdArgs a{};
     const char* terr = nullptr;
     const int64_t PR = pb.text_rows;
     const bool ok = make_tmap_thd(&a.tm_q_text, dst[0], PR, H, d, 128, &terr) &&

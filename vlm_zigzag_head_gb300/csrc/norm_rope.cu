@@ -10,12 +10,17 @@
 //   dw_e = sum over rows of g_e n_e,   dx = r (g w - n mean_e(g w n)).
 //
 // The passes are bound by memory: forward reads and writes every element once,
-// backward reads x and dy and writes dx (r and the angles are recomputed).  So
-// a lane moves eight neighbouring elements (16 bytes of bf16), d / 8 lanes
-// share a head, and a warp keeps the cosines, sines and weights of its lane's
-// elements in registers while it walks the heads of one token: the angles cost
-// one evaluation per token and pair, not per head.  Several heads are loaded
-// before the first is used, to cover the memory latency.
+// backward reads x and dy and writes dx (r and the angles are recomputed).  To
+// stay there a pass has few instructions per element: a lane owns two groups of
+// four elements that rotate against one another (elements 4 l and rot / 2 + 4 l
+// on), so that the rotation needs no exchange between lanes; d / 8 lanes share a
+// head; the cosines, sines and weights of a lane's elements are multiplied once
+// per token into the coefficients that every head of the token uses; arithmetic
+// runs two elements per instruction.  Several heads are loaded before the first
+// is used, to cover the memory latency.  Measured on bf16 heads of 128: forward
+// 6.7 TB/s at 131072 tokens x 40 heads and 6.1 at 18688 x 64 (a plain copy: 6.8);
+// backward 5.8 and 5.4 with two blocks of eight warps per SM (5.5 and 5.0 with
+// three, whose 80 registers leave fewer loads in flight).
 //
 // Angles.  A 32-bit product pos * freq is off by 2^-24 of the angle, which at
 // position 100000 is 0.006 radians.  The turns per position are therefore held
@@ -26,91 +31,93 @@
 #include <type_traits>
 
 #include "norm_rope.h"
+#include "ptx.cuh"
 
 namespace cpattn {
 
 namespace {
 
+using namespace ptx;
+
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Eight elements as loaded.
+// Four elements as two pairs of floats, and their load as stored.
+struct Four {
+  uint64_t p[2];
+};
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+  uint2 v;
+  __device__ __forceinline__ void clear() { v = make_uint2(0, 0); }
   template <bool kVec>
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
     if constexpr (kVec) {
-      v = ld_stream(p);
+      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(v.x), "=r"(v.y)
+                   : "l"(p));
     } else {
       const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)s[2 * i] | ((uint32_t)s[2 * i + 1] << 16);
-      v = make_uint4(w[0], w[1], w[2], w[3]);
+      v = make_uint2((uint32_t)s[0] | ((uint32_t)s[1] << 16),
+                     (uint32_t)s[2] | ((uint32_t)s[3] << 16));
     }
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {   // a bf16 is the upper half of its fp32
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  __device__ __forceinline__ Four get() const {   // a bf16 is the upper half of its fp32
+    return {{pack2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)),
+             pack2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u))}};
   }
 };
 template <>
 struct Raw<float> {
-  uint4 v[2];
-  __device__ __forceinline__ void clear() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
+  uint4 v;
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
   template <bool kVec>
   __device__ __forceinline__ void load(const float* p) {
     if constexpr (kVec) {
-      v[0] = ld_stream(p);
-      v[1] = ld_stream(p + 4);
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "l"(p));
     } else {
       const uint32_t* s = reinterpret_cast<const uint32_t*>(p);
-      v[0] = make_uint4(s[0], s[1], s[2], s[3]);
-      v[1] = make_uint4(s[4], s[5], s[6], s[7]);
+      v = make_uint4(s[0], s[1], s[2], s[3]);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  __device__ __forceinline__ Four get() const {
+    return {{pack2(__uint_as_float(v.x), __uint_as_float(v.y)),
+             pack2(__uint_as_float(v.z), __uint_as_float(v.w))}};
   }
 };
 
 // Outputs are contiguous and 16-byte aligned.
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const Four& f) {
+  float a, b, c, d;
+  unpack2(f.p[0], a, b);
+  unpack2(f.p[1], c, d);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store4(float* p, const Four& f) {
+  float4 v;
+  unpack2(f.p[0], v.x, v.y);
+  unpack2(f.p[1], v.z, v.w);
+  *reinterpret_cast<float4*>(p) = v;
 }
 
-__device__ __forceinline__ void load_weights(const NormRopeArgs& a, int s, int e0, float (&w)[8]) {
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(b, a);
+}
+
+__device__ __forceinline__ Four load_weights(const NormRopeArgs& a, int s, int e) {
+  float w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     w[i] = a.w[s] == nullptr ? 1.f
-           : a.w_bf16        ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w[s])[e0 + i])
-                             : static_cast<const float*>(a.w[s])[e0 + i];
+           : a.w_bf16        ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.w[s])[e + i])
+                             : static_cast<const float*>(a.w[s])[e + i];
   }
+  return {{pack2(w[0], w[1]), pack2(w[2], w[3])}};
 }
 
 // Cosine and sine of every rotated pair of token t into the warp's table.
@@ -130,43 +137,49 @@ __device__ __forceinline__ void token_angles(const NormRopeArgs& a, int64_t t, i
   }
 }
 
-// The lane's rotation: element i of the rotated head is z_i c[i] + partner_i s[i].
-// Half layout: the partner elements sit `shift` lanes away (rot / 2 elements);
-// interleaved: the partner of an even element is the next one.
-template <bool kInter>
-__device__ __forceinline__ void lane_rotation(const float2* cs, int e0, int rot, float (&c)[8],
-                                              float (&s)[8]) {
-  if constexpr (kInter) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const bool in = e0 < rot;
-      const float2 v = in ? cs[(e0 + i) / 2] : make_float2(1.f, 0.f);
-      c[i] = c[i + 1] = v.x;
-      s[i] = -v.y;
-      s[i + 1] = v.y;
-    }
-  } else {
-    const int half = rot / 2;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool in = e0 < rot;
-      const float2 v = in ? cs[e0 < half ? e0 + i : e0 + i - half] : make_float2(1.f, 0.f);
-      c[i] = v.x;
-      s[i] = e0 < half ? -v.y : v.y;
+// Where a lane's elements of a head live: two groups of four, x from e0 and z
+// from e1.  Rotated lanes of the half layout hold partners, (x[i], z[i]); all
+// other lanes hold eight neighbouring elements.
+template <int D, bool kInter>
+struct Lane {
+  static constexpr int kLanes = D / 8;          // lanes of one head
+  static constexpr int kHeads = 32 / kLanes;    // heads of one warp pass
+  int e0, e1, sel, pair;   // pair: first rotated pair, or -1
+  __device__ __forceinline__ Lane(int lane, int rot) {
+    const int sub = lane % kLanes;
+    sel = lane / kLanes;
+    const bool in = sub * 8 < rot;
+    e0 = sub * 8;
+    e1 = e0 + 4;
+    pair = in ? sub * 4 : -1;
+    if (!kInter && in) {
+      e0 = sub * 4;
+      e1 = rot / 2 + sub * 4;
     }
   }
-}
-
-// y = R z, or R^T z with kBack (the sines change sign).
-template <bool kInter, bool kBack>
-__device__ __forceinline__ void rotate(const float (&z)[8], const float (&c)[8],
-                                       const float (&s)[8], int partner, float (&y)[8]) {
+  // the pairs' cosines and sines as coefficients of two elements each:
+  // half layout: of (x, z) elements 0, 1 and 2, 3; interleaved: cosine twice,
+  // and (-sine, sine), for the two elements of each of four pairs
+  __device__ __forceinline__ void coefficients(const float2* cs, uint64_t (&c)[4],
+                                               uint64_t (&s)[4]) const {
+    float2 v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float other = kInter ? z[i ^ 1] : __shfl_sync(0xffffffffu, z[i], partner);
-    y[i] = fmaf(other, kBack ? -s[i] : s[i], z[i] * c[i]);
+    for (int i = 0; i < 4; ++i) v[i] = pair >= 0 ? cs[pair + i] : make_float2(1.f, 0.f);
+    if constexpr (kInter) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = pack2(v[i].x, v[i].x);
+        s[i] = pack2(-v[i].y, v[i].y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        c[i] = pack2(v[2 * i].x, v[2 * i + 1].x);
+        s[i] = pack2(v[2 * i].y, v[2 * i + 1].y);
+      }
+    }
   }
-}
+};
 
 template <int kLanes>
 __device__ __forceinline__ float head_sum(float v) {
@@ -174,81 +187,120 @@ __device__ __forceinline__ float head_sum(float v) {
   for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
+}
 
-// Geometry shared by both directions: where lane's elements of head g live.
-template <int D>
-struct Lane {
-  static constexpr int kLanes = D / 8;          // lanes of one head
-  static constexpr int kHeads = 32 / kLanes;    // heads of one warp pass
-  int e0, sel, partner;
-  __device__ __forceinline__ Lane(int lane, int rot) {
-    const int sub = lane % kLanes;
-    e0 = sub * 8;
-    sel = lane / kLanes;
-    const int shift = rot / 16;                 // rot / 2 elements, in lanes
-    int p = e0 < rot / 2 ? sub + shift : sub - shift;
-    if (e0 >= rot) p = sub;
-    partner = sel * kLanes + p;
+// The forward's coefficients with the weights folded in: y = r (x A + other B).
+template <int D, bool kInter>
+struct Turn {
+  uint64_t A[4], B[4];
+  __device__ __forceinline__ Turn(const Lane<D, kInter>& ln, const float2* cs, const Four& wx,
+                                  const Four& wz) {
+    uint64_t c[4], s[4];
+    ln.coefficients(cs, c, s);
+    if constexpr (kInter) {
+      const uint64_t w[4] = {wx.p[0], wx.p[1], wz.p[0], wz.p[1]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        A[i] = mul2(w[i], c[i]);
+        B[i] = mul2(swap2(w[i]), s[i]);   // of the pair's other element
+      }
+    } else {
+      const uint64_t neg = pack2(-1.f, -1.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        A[i] = mul2(wx.p[i], c[i]);
+        A[2 + i] = mul2(wz.p[i], c[i]);
+        B[i] = mul2(mul2(wz.p[i], s[i]), neg);
+        B[2 + i] = mul2(wx.p[i], s[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void apply(const Four& x, const Four& z, float r, Four& y0,
+                                        Four& y1) const {
+    const uint64_t r2 = pack2(r, r);
+    const uint64_t v[4] = {x.p[0], x.p[1], z.p[0], z.p[1]};
+    uint64_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t other = kInter ? swap2(v[i]) : v[i ^ 2];
+      y[i] = mul2(fma2(other, B[i], mul2(v[i], A[i])), r2);
+    }
+    y0 = {{y[0], y[1]}};
+    y1 = {{y[2], y[3]}};
   }
 };
 
 // One warp: heads [g0, g1) of one token (query heads first, then key heads).
 template <typename T, int D, bool kInter, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 2)
     norm_rope_fwd_kernel(const __grid_constant__ NormRopeArgs a) {
   __shared__ float2 cs_all[kWarps][64];
-  using G = Lane<D>;
-  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+  using G = Lane<D, kInter>;
+  constexpr int kUnroll = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t t = unit / a.n_chunks;
   if (t >= a.T) return;   // whole warps only: the block has no barrier
-  const int total = a.heads[0] + a.heads[1];
-  const int g0 = (int)(unit % a.n_chunks) * a.chunk;
-  const int g1 = min(g0 + a.chunk, total);
+  const int g0 = (int)(unit % a.n_chunks) * a.chunk, g1 = g0 + a.chunk;
   const G ln(lane, a.rot);
-  auto src = [&](int g) {
-    const int s = g >= a.heads[0];
-    return static_cast<const T*>(a.x[s]) + t * a.st[s] +
-           (int64_t)(g - (s ? a.heads[0] : 0)) * a.sh[s] + ln.e0;
-  };
-  // the first heads' loads go out before the angles are computed
-  Raw<T> raw[kUnroll];
-#pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int g = g0 + u * G::kHeads + ln.sel;
-    raw[u].clear();
-    if (g < g1) raw[u].template load<kVec>(src(g));
-  }
   float2* cs = cs_all[warp];
-  token_angles(a, t, lane, cs);
-  __syncwarp();
-  float c[8], s[8], wq[8], wk[8];
-  lane_rotation<kInter>(cs, ln.e0, a.rot, c, s);
-  load_weights(a, 0, ln.e0, wq);
-  load_weights(a, 1, ln.e0, wk);
-  for (int gb = g0; gb < g1; gb += kUnroll * G::kHeads) {
+  bool angles = false;
+#pragma unroll 1
+  for (int s = 0; s < 2; ++s) {
+    // the chunk's heads of this tensor
+    const int h0 = max(0, g0 - (s ? a.heads[0] : 0));
+    const int h1 = min(a.heads[s], g1 - (s ? a.heads[0] : 0));
+    if (h0 >= h1) continue;
+    // running pointers to this lane's elements of the pass's head
+    const int64_t step = G::kHeads * a.sh[s];
+    const int gap = ln.e1 - ln.e0;
+    int h = h0 + ln.sel, hn = h;   // head of the pass, and of the next load
+    const T* src = static_cast<const T*>(a.x[s]) + t * a.st[s] + h * a.sh[s] + ln.e0;
+    T* dst = static_cast<T*>(a.y[s]) + (t * a.heads[s] + h) * D + ln.e0;
+    // the first heads' loads go out before the angles are computed
+    Raw<T> rx[kUnroll], rz[kUnroll];
+    auto load = [&](int u) {
+      if (hn < h1) {
+        rx[u].template load<kVec>(src);
+        rz[u].template load<kVec>(src + gap);
+      }
+      hn += G::kHeads;
+      src += step;
+    };
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int g = gb + u * G::kHeads + ln.sel;
-      float x[8];
-      raw[u].get(x);
-      const int gn = g + kUnroll * G::kHeads;
-      raw[u].clear();
-      if (gn < g1) raw[u].template load<kVec>(src(gn));
-      float ss = 0.f;
+      rx[u].clear();
+      rz[u].clear();
+      load(u);
+    }
+    if (!angles) {
+      token_angles(a, t, lane, cs);
+      __syncwarp();
+      angles = true;
+    }
+    const Turn<D, kInter> turn(ln, cs, load_weights(a, s, ln.e0), load_weights(a, s, ln.e1));
+    for (int hb = h0; hb < h1; hb += kUnroll * G::kHeads) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float r = rsqrtf(head_sum<G::kLanes>(ss) * (1.f / D) + a.eps);
-      const bool is_k = g >= a.heads[0];
-      float z[8], y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = x[i] * r * (is_k ? wk[i] : wq[i]);
-      rotate<kInter, false>(z, c, s, ln.partner, y);
-      if (g < g1) {
-        T* dst = is_k ? static_cast<T*>(a.y[1]) + (t * a.heads[1] + g - a.heads[0]) * D
-                      : static_cast<T*>(a.y[0]) + (t * a.heads[0] + g) * D;
-        store8(dst + ln.e0, y);
+      for (int u = 0; u < kUnroll; ++u) {
+        const Four x = rx[u].get(), z = rz[u].get();
+        load(u);
+        uint64_t ss = mul2(x.p[0], x.p[0]);
+        ss = fma2(x.p[1], x.p[1], ss);
+        ss = fma2(z.p[0], z.p[0], ss);
+        ss = fma2(z.p[1], z.p[1], ss);
+        const float r = rsqrtf(head_sum<G::kLanes>(sum2(ss)) * (1.f / D) + a.eps);
+        Four y0, y1;
+        turn.apply(x, z, r, y0, y1);
+        if (h < h1) {
+          store4(dst, y0);
+          store4(dst + gap, y1);
+        }
+        h += G::kHeads;
+        dst += G::kHeads * D;
       }
     }
   }
@@ -259,96 +311,129 @@ __global__ void __launch_bounds__(kWarps * 32)
 // warp order and writes one row of partial sums, which a second small launch
 // adds in block order: the result does not depend on timing.
 template <typename T, int D, bool kInter, bool kVec>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a) {
   __shared__ float2 cs_all[kWarps][64];
   __shared__ float red[kWarps][2][D];
-  using G = Lane<D>;
-  constexpr int kUnroll = sizeof(T) == 2 ? 2 : 1;
+  using G = Lane<D, kInter>;
+  constexpr int kUnroll = 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total = a.heads[0] + a.heads[1];
   const G ln(lane, a.rot);
   float2* cs = cs_all[warp];
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weights(a, 0, ln.e0, wq);
-  load_weights(a, 1, ln.e0, wk);
+  uint64_t dw[2][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int i = 0; i < 8; ++i) dw[i / 4][i % 4] = pack2(0.f, 0.f);
   const int64_t units = a.T * a.n_chunks;
   for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units;
        unit += (int64_t)gridDim.x * kWarps) {
     const int64_t t = unit / a.n_chunks;
-    const int g0 = (int)(unit % a.n_chunks) * a.chunk;
-    const int g1 = min(g0 + a.chunk, total);
-    auto load = [&](int g, Raw<T>& rx, Raw<T>& rg) {
-      rx.clear();
-      rg.clear();
-      if (g < g1) {
-        const int s = g >= a.heads[0];
-        const int h = g - (s ? a.heads[0] : 0);
-        rx.template load<kVec>(static_cast<const T*>(a.x[s]) + t * a.st[s] +
-                               (int64_t)h * a.sh[s] + ln.e0);
-        rg.template load<true>(static_cast<const T*>(a.dy[s]) +
-                               (t * a.heads[s] + h) * D + ln.e0);
-      }
-    };
-    Raw<T> rx[kUnroll], rg[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) load(g0 + u * G::kHeads + ln.sel, rx[u], rg[u]);
+    const int g0 = (int)(unit % a.n_chunks) * a.chunk, g1 = g0 + a.chunk;
     __syncwarp();   // the previous token's angles are read
-    token_angles(a, t, lane, cs);
-    __syncwarp();
-    float c[8], s[8];
-    lane_rotation<kInter>(cs, ln.e0, a.rot, c, s);
-    for (int gb = g0; gb < g1; gb += kUnroll * G::kHeads) {
+    bool angles = false;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int h0 = max(0, g0 - (s ? a.heads[0] : 0));
+      const int h1 = min(a.heads[s], g1 - (s ? a.heads[0] : 0));
+      if (h0 >= h1) continue;
+      const int64_t step = G::kHeads * a.sh[s];
+      const int gap = ln.e1 - ln.e0;
+      int h = h0 + ln.sel, hn = h;   // head of the pass, and of the next load
+      const int64_t row = (t * a.heads[s] + h) * D + ln.e0;
+      const T* src = static_cast<const T*>(a.x[s]) + t * a.st[s] + h * a.sh[s] + ln.e0;
+      const T* gsrc = static_cast<const T*>(a.dy[s]) + row;
+      T* dst = static_cast<T*>(a.y[s]) + row;
+      Raw<T> rx[kUnroll], rz[kUnroll], rgx[kUnroll], rgz[kUnroll];
+      auto load = [&](int u) {
+        if (hn < h1) {
+          rx[u].template load<kVec>(src);
+          rz[u].template load<kVec>(src + gap);
+          rgx[u].template load<true>(gsrc);
+          rgz[u].template load<true>(gsrc + gap);
+        }
+        hn += G::kHeads;
+        src += step;
+        gsrc += G::kHeads * D;
+      };
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int g = gb + u * G::kHeads + ln.sel;
-        float x[8], dy[8], gr[8];
-        rx[u].get(x);
-        rg[u].get(dy);
-        load(g + kUnroll * G::kHeads, rx[u], rg[u]);
-        rotate<kInter, true>(dy, c, s, ln.partner, gr);
-        const bool is_k = g >= a.heads[0];
-        float ss = 0.f, dot = 0.f;
+        rx[u].clear();
+        rz[u].clear();
+        rgx[u].clear();
+        rgz[u].clear();
+        load(u);
+      }
+      if (!angles) {
+        token_angles(a, t, lane, cs);
+        __syncwarp();
+        angles = true;
+      }
+      uint64_t c[4], sn[4];
+      ln.coefficients(cs, c, sn);
+      const Four wx = load_weights(a, s, ln.e0), wz = load_weights(a, s, ln.e1);
+      const uint64_t w[4] = {wx.p[0], wx.p[1], wz.p[0], wz.p[1]};
+      const uint64_t neg = pack2(-1.f, -1.f);
+      for (int hb = h0; hb < h1; hb += kUnroll * G::kHeads) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(gr[i] * (is_k ? wk[i] : wq[i]), x[i], dot);
-        }
-        const float r = rsqrtf(head_sum<G::kLanes>(ss) * (1.f / D) + a.eps);
-        // mean of (g w) n = r * mean of (g w) x
-        const float m = head_sum<G::kLanes>(dot) * (1.f / D) * r;
-        float dx[8];
+        for (int u = 0; u < kUnroll; ++u) {
+          const Four x0 = rx[u].get(), x1 = rz[u].get(), d0 = rgx[u].get(), d1 = rgz[u].get();
+          load(u);
+          const uint64_t x[4] = {x0.p[0], x0.p[1], x1.p[0], x1.p[1]};
+          const uint64_t dy[4] = {d0.p[0], d0.p[1], d1.p[0], d1.p[1]};
+          // g = R^T dy
+          uint64_t g[4], gx[4];
+          if constexpr (kInter) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float n = x[i] * r;
-          const float gn = g < g1 ? gr[i] * n : 0.f;
-          dwq[i] += is_k ? 0.f : gn;
-          dwk[i] += is_k ? gn : 0.f;
-          dx[i] = r * fmaf(gr[i], is_k ? wk[i] : wq[i], -n * m);
-        }
-        if (g < g1) {
-          T* dst = is_k ? static_cast<T*>(a.y[1]) + (t * a.heads[1] + g - a.heads[0]) * D
-                        : static_cast<T*>(a.y[0]) + (t * a.heads[0] + g) * D;
-          store8(dst + ln.e0, dx);
+            for (int i = 0; i < 4; ++i)
+              g[i] = fma2(mul2(swap2(dy[i]), sn[i]), neg, mul2(dy[i], c[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              g[i] = fma2(dy[2 + i], sn[i], mul2(dy[i], c[i]));
+              g[2 + i] = fma2(mul2(dy[i], sn[i]), neg, mul2(dy[2 + i], c[i]));
+            }
+          }
+          uint64_t ss = mul2(x[0], x[0]), dot = pack2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i > 0) ss = fma2(x[i], x[i], ss);
+            gx[i] = mul2(g[i], x[i]);
+            dot = fma2(gx[i], w[i], dot);
+          }
+          const float r = rsqrtf(head_sum<G::kLanes>(sum2(ss)) * (1.f / D) + a.eps);
+          // n mean(g w n) = x r^2 mean(g w x)
+          const float k = head_sum<G::kLanes>(sum2(dot)) * (1.f / D) * r * r;
+          if (h < h1) {
+            const uint64_t r2 = pack2(r, r), k2 = pack2(-k, -k);
+            uint64_t dx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dw[s][i] = fma2(gx[i], r2, dw[s][i]);
+              dx[i] = mul2(fma2(x[i], k2, mul2(g[i], w[i])), r2);
+            }
+            store4(dst, {{dx[0], dx[1]}});
+            store4(dst + gap, {{dx[2], dx[3]}});
+          }
+          h += G::kHeads;
+          dst += G::kHeads * D;
         }
       }
     }
   }
   if (a.partial == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int o = G::kLanes; o < 32; o <<= 1) {   // the heads of one pass
-      dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-      dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+    for (int i = 0; i < 4; ++i) {
+      float v[2];
+      unpack2(dw[s][i], v[0], v[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = G::kLanes; o < 32; o <<= 1)   // the heads of one pass
+          v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+        if (ln.sel == 0) red[warp][s][(i < 2 ? ln.e0 : ln.e1) + (i & 1) * 2 + j] = v[j];
+      }
     }
-    if (ln.sel == 0) {
-      red[warp][0][ln.e0 + i] = dwq[i];
-      red[warp][1][ln.e0 + i] = dwk[i];
-    }
-  }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
     float v = 0.f;
@@ -358,17 +443,22 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// One warp column per output: 32 columns x 8 row groups per block.
-__global__ void __launch_bounds__(256)
+// 32 outputs per block; a warp adds the rows of its share, then the warps' sums
+// meet in warp order.
+constexpr int kDwWarps = 32;
+__global__ void __launch_bounds__(kDwWarps * 32)
     norm_rope_dw_kernel(const float* partial, int blocks, int d, float* dqw, float* dkw) {
-  __shared__ float red[8][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), grp = threadIdx.x >> 5;
+  __shared__ float red[kDwWarps][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int b = grp; b < blocks; b += 8) v += partial[(int64_t)b * 2 * d + col];
-  red[grp][threadIdx.x & 31] = v;
+#pragma unroll 4
+  for (int b = warp; b < blocks; b += kDwWarps) v += partial[(int64_t)b * 2 * d + col];
+  red[warp][lane] = v;
   __syncthreads();
-  if (grp == 0) {
-    for (int g = 1; g < 8; ++g) v += red[g][threadIdx.x & 31];
+  if (warp == 0) {
+#pragma unroll
+    for (int g = 1; g < kDwWarps; ++g) v += red[g][lane];
     if (col < d) { if (dqw) dqw[col] = v; }
     else if (dkw) dkw[col - d] = v;
   }
@@ -443,7 +533,7 @@ cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, bool bf16, int d, bool i
 
 cudaError_t launch_norm_rope_dw(const float* partial, int blocks, int d, float* dqw, float* dkw,
                                 cudaStream_t st) {
-  norm_rope_dw_kernel<<<2 * d / 32, 256, 0, st>>>(partial, blocks, d, dqw, dkw);
+  norm_rope_dw_kernel<<<2 * d / 32, kDwWarps * 32, 0, st>>>(partial, blocks, d, dqw, dkw);
   return cudaGetLastError();
 }
 

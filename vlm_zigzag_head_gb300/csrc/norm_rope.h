@@ -36,7 +36,8 @@ int norm_rope_bwd_max_blocks(int sms);
 // Heads per warp and the number of such chunks.
 void norm_rope_split(int64_t T, int heads, int d, int sms, int* chunk, int* n_chunks);
 
-// vec: every row starts on a 16-byte boundary (16-byte loads), else element loads.
+// vec: every group of four elements lies on a boundary of its size (vector
+// loads), else element loads.
 cudaError_t launch_norm_rope_fwd(const NormRopeArgs& a, bool bf16, int d, bool interleaved,
                                  bool vec, cudaStream_t st);
 cudaError_t launch_norm_rope_bwd(const NormRopeArgs& a, bool bf16, int d, bool interleaved,

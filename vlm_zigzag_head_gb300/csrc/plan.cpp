@@ -229,21 +229,22 @@ void plan_forward_fused(const FwdPlan& per_step, int P, FusedFwdPlan* out) {
 }
 
 void plan_unit_lists(const std::vector<FwdItem>& items, int H, int grid,
-                     std::vector<int32_t>* units, std::vector<int32_t>* cta_off) {
+                     std::vector<int32_t>* units, std::vector<int32_t>* cta_off,
+                     bool item_major) {
   constexpr int64_t kUnitCost = 2;  // Q load and epilogue, in KV-tile equivalents
   const int n = (int)items.size();
   std::vector<std::vector<int32_t>> lists(grid);
   using Load = std::pair<int64_t, int>;  // (work so far, CTA): least work first, then lowest CTA
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> pq;
   for (int b = 0; b < grid; ++b) pq.push({0, b});
-  for (int h = 0; h < H; ++h) {
-    for (int x = 0; x < n; ++x) {
-      Load e = pq.top();
-      pq.pop();
-      lists[e.second].push_back(x + n * h);
-      e.first += items[x].n_tiles + kUnitCost;
-      pq.push(e);
-    }
+  const int64_t total = (int64_t)n * H;
+  for (int64_t u = 0; u < total; ++u) {
+    const int x = (int)(item_major ? u / H : u % n), h = (int)(item_major ? u % H : u / n);
+    Load e = pq.top();
+    pq.pop();
+    lists[e.second].push_back(x + n * h);
+    e.first += items[x].n_tiles + kUnitCost;
+    pq.push(e);
   }
   units->clear();
   cta_off->assign(1, 0);

@@ -117,8 +117,11 @@ inline long long fwd_grid(long long units, int sms) { return units < 4LL * sms ?
 // one or two heads, whose K / V stay in L2.  (A plain round robin over
 // (item, head) can give a CTA a much heavier share when n_items and grid
 // share a stride.)
+// item_major: the units are taken item by item instead, heaviest first over all
+// heads, which balances launches of few units per CTA best.
 void plan_unit_lists(const std::vector<FwdItem>& items, int H, int grid,
-                     std::vector<int32_t>* units, std::vector<int32_t>* cta_off);
+                     std::vector<int32_t>* units, std::vector<int32_t>* cta_off,
+                     bool item_major = false);
 
 // text_perm = true: text rows address the rank-local (gathered) buffer;
 // false: they address natural order (used by the fp32 dQ pass).  tile_q:

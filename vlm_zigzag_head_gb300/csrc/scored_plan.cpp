@@ -71,15 +71,15 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   p.n_fwd = (int32_t)fwd;
   p.n_bwd = (int32_t)bwd;
   p.n_tiles = (int32_t)tiles;
-  const long long units = fwd * H, grid = fwd_grid(units, sms);
-  p.grid = (int32_t)grid;
-  p.n_units = grid < units ? (int32_t)units : 0;
+  p.n_units = (int32_t)(fwd * H);
+  p.grid = std::min<int32_t>(p.n_units, sms);
+  p.item_major = item_major(p.n_units, sms) ? 1 : 0;
   uint64_t o = up256(sizeof(ScorePlanHeader));
   p.fwd = o; o = up256(o + fwd * sizeof(FwdItem));
   p.bwd = o; o = up256(o + bwd * sizeof(BwdItem));
   p.runs = o; o = up256(o + bwd * sizeof(Seg));
   p.units = o;
-  if (p.n_units > 0) o = up256(o + (uint64_t)(p.n_units + p.grid + 1) * sizeof(int32_t));
+  o = up256(o + (uint64_t)(p.n_units + p.grid + 1) * sizeof(int32_t));
   p.buckets = o; o = up256(o + (uint64_t)n_dist * sizeof(int32_t));
   p.tiles = o; o = up256(o + tiles * sizeof(Tile32));
   p.total = o;
@@ -166,7 +166,7 @@ void score_plan_build(const ScorePlanHeader& h, const int32_t* cu, const int32_t
   if (h.n_dist > 0) memcpy(b + h.buckets, buckets, h.n_dist * sizeof(int32_t));
   if (h.n_units > 0) {
     std::vector<int32_t> units, off;
-    plan_unit_lists(fwd, h.H, h.grid, &units, &off);
+    plan_unit_lists(fwd, h.H, h.grid, &units, &off, h.item_major != 0);
     memcpy(b + h.units, units.data(), units.size() * sizeof(int32_t));
     memcpy(b + h.units + units.size() * sizeof(int32_t), off.data(), off.size() * sizeof(int32_t));
   }

@@ -36,10 +36,16 @@ struct ScorePlanHeader {
   int32_t T, H, n_seqs, bidirectional;
   int32_t n_dist, n_buckets;       // 0: no table
   int32_t n_fwd, n_bwd, n_tiles;
-  int32_t n_units, grid;           // n_units 0: one CTA per unit
+  int32_t n_units, grid;           // forward: units and persistent CTAs
+  int32_t item_major;              // the forward's unit order
   uint64_t fwd, bwd, runs, units, buckets, tiles, total;
 };
 static_assert(sizeof(ScorePlanHeader) <= 256, "plan header");
+
+// Order of a launch's work units: item by item, heaviest first over all heads,
+// below 16 units per SM, where a heavy unit that starts late costs most; head by
+// head above, where K / V (or Q / dO) of one or two heads stay in L2.
+inline bool item_major(int64_t units, int sms) { return units < 16LL * sms; }
 
 // Checks the arguments ("" or a message) and fills `h` without building.
 std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* prefix_lens,

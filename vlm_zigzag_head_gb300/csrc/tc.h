@@ -95,6 +95,8 @@ struct TcBwdArgs {
   long long wait_limit;
   int kv_split;               // CTAs sharing one KV head's query heads (divides H / Hkv); > 1:
                               // dK / dV / prefix slots are reduce-added into zeroed memory
+  int item_major;             // nonzero: blocks go item by item (all heads of the heaviest
+                              // item first), else head by head
   int n_slots;                // prefix-gradient slots (P + 1) behind pre_k / pre_v (index checks)
   ScoreArgs score;            // read by the scored kernels only
 };

@@ -194,7 +194,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[2][32], uint32_t (&
                                               const score::Cap<kCap>& cap,
                                               const score::TileBias& tb, const float* ld, bool vec,
                                               int first_vis, int end_vis) {
-  const uint64_t sl2_2 = score::pack2(sl2, sl2);
+  const uint64_t sl2_2 = pack2(sl2, sl2);
   bool poly = true;
   if constexpr (kCap) {
     float big[4] = {0.f, 0.f, 0.f, 0.f};
@@ -213,13 +213,13 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[2][32], uint32_t (&
       uint32_t& e0 = rs[(x + y) >> 5][(x + y) & 31];
       uint32_t& e1 = rs[(x + y) >> 5][(x + y + 1) & 31];
       float s0, s1, w0 = 1.f, w1 = 1.f;
-      const uint64_t raw = score::pack2(__uint_as_float(e0), __uint_as_float(e1));
+      const uint64_t raw = pack2(__uint_as_float(e0), __uint_as_float(e1));
       if constexpr (kCap) {
-        const uint64_t av = score::mul2(raw, sl2_2);
+        const uint64_t av = mul2(raw, sl2_2);
         if (poly) {
-          score::unpack2(cap.poly(av), s0, s1);
+          unpack2(cap.poly(av), s0, s1);
         } else {
-          score::unpack2(av, s0, s1);
+          unpack2(av, s0, s1);
           s0 = cap.any(s0);
           s1 = cap.any(s1);
         }
@@ -229,7 +229,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[2][32], uint32_t (&
         s0 += tb.base;
         s1 += tb.base;
       } else {
-        score::unpack2(score::fma2(raw, sl2_2, score::pack2(tb.base, tb.base)), s0, s1);
+        unpack2(fma2(raw, sl2_2, pack2(tb.base, tb.base)), s0, s1);
       }
       float p0 = ex2(score::add_column<kBias, 1>(tb, x + y, s0) - l[y]);
       float p1 = ex2(score::add_column<kBias, 1>(tb, x + y + 1, s1) - l[y + 1]);
@@ -244,25 +244,26 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[2][32], uint32_t (&
 
 // Gradient of a table bias: dS summed over the pairs of each |distance|.
 //
-// In a tile near the diagonal lane u of a warp holds distance dist0 - u + x at
-// query x, so one distance moves one lane up per query: `diag` travels with it
-// and collects the whole warp's share, and lane 31 hands over one finished
-// distance per query (the rest once per tile, one per lane).  That is one
-// shuffle per dS element and 3 atomic adds per two 32-element rows, where an
-// atomic per element would be 32 times as many.  Tiles at or past the table's
-// last distance sum into one register.
+// In a tile near the diagonal lane u of a warp holds distance base + x - u at
+// query x of a block of 32.  Query x's values are turned by x lanes, lane L
+// taking u = (x - L) mod 32: it then always adds distance base + L (x >= L) or
+// base + L - 32 (x < L).  The shuffles do not wait on one another, and a warp
+// hands over 96 sums per 64 queries, one per lane in three coalesced atomics,
+// where an atomic per element would be 21 times as many.  Tiles at or past the
+// table's last distance sum into one register.
+struct Diagonals {
+  float all = 0.f, up = 0.f;   // both kinds of a block's sums; those with x >= L
+};
+__device__ __forceinline__ void bias_grad(Diagonals& g, int x, float v, int lane) {
+  const float w = __shfl_sync(0xffffffffu, v, (x - lane) & 31);
+  g.all += w;
+  if (x >= lane) g.up += w;
+}
 __device__ __forceinline__ void add_distance(const ScoreArgs& s, int h, int dist, float v,
                                              float& far_sum) {
   const int d = dist < 0 ? -dist : dist;
   if (d >= s.n_dist - 1) far_sum += v;
   else atomicAdd(s.dtable + (long long)h * s.n_dist + d, v);
-}
-__device__ __forceinline__ void bias_grad(const ScoreArgs& s, int h, int dist, float v, int lane,
-                                          float& diag, float& far_sum) {
-  // lane u takes over lane u - 1's distance; lane 31's is finished
-  const float up = __shfl_up_sync(0xffffffffu, diag, 1);
-  if (lane == 31) add_distance(s, h, dist - 1, diag, far_sum);
-  diag = (lane == 0 ? 0.f : up) + v;
 }
 __device__ __forceinline__ void flush_far(const ScoreArgs& s, int h, int lane, float& far_sum) {
   float v = far_sum;
@@ -283,15 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item_idx = blockIdx.x % a.n_items;
+  const int per_item = a.item_major ? (kShared ? a.Hkv * a.kv_split : a.Hkv) : 1;
+  const int item_idx = a.item_major ? blockIdx.x / per_item : blockIdx.x % a.n_items;
+  const int slot = a.item_major ? blockIdx.x % per_item : blockIdx.x / a.n_items;
   // KV head hk; its query heads are hk*G .. hk*G+G-1.  Shared groups
   // (kv_split > 1): kv_split CTAs take Gs = G / kv_split consecutive query
   // heads each, and their partial dK / dV meet in global memory by
   // reduce-adds.
-  const int hk = kShared ? blockIdx.x / a.n_items / a.kv_split : blockIdx.x / a.n_items;
+  const int hk = kShared ? slot / a.kv_split : slot;
   const int G = a.H / a.Hkv;
   const int Gs = kShared ? G / a.kv_split : G;   // query heads of this CTA
-  const int hq0 = hk * G + (kShared ? blockIdx.x / a.n_items % a.kv_split * Gs : 0);
+  const int hq0 = hk * G + (kShared ? slot % a.kv_split * Gs : 0);
   BwdItem& it = *reinterpret_cast<BwdItem*>(smem + L::kItem);
   if (warp == 0)  // the work item, copied once into shared memory (128 bytes)
     reinterpret_cast<uint32_t*>(&it)[lane] =
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&bars->dp_full, i & 1, lim, abort)) { ok = false; break; }
       tc_fence_after();
       uint8_t* srow = smem + L::kDS + g * L::kBox + u * 128;
-      float diag = 0.f;   // running sum of one distance (kBias: table)
+      Diagonals diag[2];   // of the two blocks of 32 queries (kBias: table)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t rd[32];
@@ -712,9 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (tb.tab == nullptr) {
                 far_sum += b0 + b1;
               } else {
-                bias_grad(a.score, hq, ti.rel + row0 - u + h * 32 + x + y, b0, lane, diag, far_sum);
-                bias_grad(a.score, hq, ti.rel + row0 - u + h * 32 + x + y + 1, b1, lane, diag,
-                          far_sum);
+                bias_grad(diag[h], x + y, b0, lane);
+                bias_grad(diag[h], x + y + 1, b1, lane);
               }
             }
             if constexpr (kF16)
@@ -735,8 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->ds_full);
       if constexpr (kBias == SCORE_TABLE) {
-        if (tb.tab != nullptr)   // the distances this warp has not finished: one per lane
-          add_distance(a.score, hq, ti.rel + row0 - u + 63, diag, far_sum);
+        if (tb.tab != nullptr) {
+          // distances base + L - 32, base + L and base + L + 32 of this warp's keys
+          const int base = ti.rel + row0 - (warp & 3) * 32 + lane;
+          add_distance(a.score, hq, base - 32, diag[0].all - diag[0].up, far_sum);
+          add_distance(a.score, hq, base, diag[0].up + (diag[1].all - diag[1].up), far_sum);
+          add_distance(a.score, hq, base + 32, diag[1].up, far_sum);
+        }
       }
       if (++jt == n_qt) {
         if constexpr (kBias == SCORE_TABLE) flush_far(a.score, hq, lane, far_sum);

@@ -144,7 +144,7 @@ template <bool kCap, int kBias>
 __device__ __forceinline__ void score_row(uint32_t (&r)[kBN / 32][32], float sl2,
                                           const score::Cap<kCap>& cap,
                                           const score::TileBias& tb) {
-  const uint64_t sl2_2 = score::pack2(sl2, sl2), base2 = score::pack2(tb.base, tb.base);
+  const uint64_t sl2_2 = pack2(sl2, sl2), base2 = pack2(tb.base, tb.base);
   bool poly = true;
   if constexpr (kCap) {
     float big[4] = {0.f, 0.f, 0.f, 0.f};
@@ -157,16 +157,16 @@ __device__ __forceinline__ void score_row(uint32_t (&r)[kBN / 32][32], float sl2
   if (!kCap || poly) {
 #pragma unroll
     for (int i = 0; i < kBN; i += 2) {
-      uint64_t y = score::pack2(__uint_as_float(r[i / 32][i % 32]),
+      uint64_t y = pack2(__uint_as_float(r[i / 32][i % 32]),
                                 __uint_as_float(r[i / 32][i % 32 + 1]));
       if constexpr (kCap) {
-        y = cap.poly(score::mul2(y, sl2_2));
-        if constexpr (kBias != SCORE_PLAIN) y = score::add2(y, base2);
+        y = cap.poly(mul2(y, sl2_2));
+        if constexpr (kBias != SCORE_PLAIN) y = add2(y, base2);
       } else {
-        y = score::fma2(y, sl2_2, base2);
+        y = fma2(y, sl2_2, base2);
       }
       float y0, y1;
-      score::unpack2(y, y0, y1);
+      unpack2(y, y0, y1);
       r[i / 32][i % 32] = __float_as_uint(score::add_column<kBias, -1>(tb, i, y0));
       r[i / 32][i % 32 + 1] = __float_as_uint(score::add_column<kBias, -1>(tb, i + 1, y1));
     }
