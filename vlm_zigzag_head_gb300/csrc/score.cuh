@@ -12,6 +12,12 @@
 // minimax coefficients on |z| <= 0.75 (off by at most 6e-7 of the value): fused
 // multiply-adds alone, two scores per instruction.  Otherwise 1 - 2 / (1 +
 // e^(2z)), two more special-function instructions per score.
+//
+// A bias costs as little as the tile allows: beyond the table's last distance it
+// is one number per row, which joins the softmax's own subtraction; slopes add one
+// multiply-add per score (their row part joins the same subtraction); only tiles
+// near the diagonal read the table (through L1, neighbouring lanes neighbouring
+// entries), and only those inside a two-way prefix take |distance|.
 #pragma once
 #include <stdint.h>
 
@@ -34,45 +40,54 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// What a thread keeps for the whole launch.
+// The cap: products s become t = tanh(s * in), in = scale / softcap; the scores
+// are then t * cap2.  (The products are scaled before the polynomial: its
+// coefficients in their units could underflow.)
 template <bool kCap>
 struct Cap {
-  float limit = 0.f, cap2 = 0.f, inv = 0.f;
-  uint64_t k[4] = {0, 0, 0, 0}, one = 0;
-  __device__ __forceinline__ explicit Cap(const ScoreArgs& s) {
+  float in = 0.f, cap2 = 0.f, inv = 0.f;
+  uint64_t in2 = 0, one = 0, neg = 0, k[4] = {0, 0, 0, 0};
+  __device__ __forceinline__ Cap(const ScoreArgs& s, float scale_log2) {
     if constexpr (kCap) {
       cap2 = s.cap_log2;
       inv = s.inv_cap_log2;
-      limit = kPolyRange * cap2;
-      const float i2 = inv * inv;
-      k[0] = pack2(kC1 * i2, kC1 * i2);
-      k[1] = pack2(kC2 * i2 * i2, kC2 * i2 * i2);
-      k[2] = pack2(kC3 * i2 * i2 * i2, kC3 * i2 * i2 * i2);
-      k[3] = pack2(kC4 * i2 * i2 * i2 * i2, kC4 * i2 * i2 * i2 * i2);
+      in = scale_log2 * inv;
+      in2 = pack2(in, in);
       one = pack2(1.f, 1.f);
+      neg = pack2(-1.f, -1.f);
+      k[0] = pack2(kC1, kC1);
+      k[1] = pack2(kC2, kC2);
+      k[2] = pack2(kC3, kC3);
+      k[3] = pack2(kC4, kC4);
     }
   }
-  // cap2 tanh(a / cap2) of two scores, |a| <= limit
-  __device__ __forceinline__ uint64_t poly(uint64_t a) const {
-    const uint64_t v = mul2(a, a);
+  // the largest |s| of a warp, times in, lets the polynomial serve
+  __device__ __forceinline__ bool in_range(float big) const {
+    return __all_sync(0xffffffffu, big * in <= kPolyRange);
+  }
+  __device__ __forceinline__ uint64_t poly(uint64_t s) const {
+    const uint64_t z = mul2(s, in2), v = mul2(z, z);
     uint64_t p = fma2(k[3], v, k[2]);
     p = fma2(p, v, k[1]);
     p = fma2(p, v, k[0]);
     p = fma2(p, v, one);
-    return mul2(a, p);
+    return mul2(z, p);
   }
-  // the same for any a: tanh z = 1 - 2 / (1 + e^(2z)), e^(2z) = 2^(2 z log2 e)
-  __device__ __forceinline__ float any(float a) const {
-    const float e = ex2(a * (inv * (2.f * kLog2e)));
-    return fmaf(-2.f * cap2, rcp_approx(1.f + e), cap2);
+  // any s: tanh z = 1 - 2 / (1 + e^(2z)), e^(2z) = 2^(2 z log2 e)
+  __device__ __forceinline__ float any(float s) const {
+    return fmaf(-2.f, rcp_approx(1.f + ex2(s * in * (2.f * kLog2e))), 1.f);
+  }
+  // 1 - t^2
+  __device__ __forceinline__ uint64_t slope(uint64_t t) const {
+    return fma2(mul2(t, neg), t, one);
   }
 };
 
 // The bias of one tile for one thread: columns run over keys (forward, the
 // distance falls by one per column) or queries (backward, it rises).
 struct TileBias {
-  float base = 0.f;    // added to every column
-  float step = 0.f;    // slopes: change per column
+  float base = 0.f;             // added to every column, log2 units
+  float step = 0.f;             // slopes: change per column, log2 units
   const float* tab = nullptr;   // near tile of a table bias: entry of column 0
   bool both = false;            // slopes: distances of both signs are visible
   float slope = 0.f, dist0 = 0.f;
@@ -100,17 +115,12 @@ __device__ __forceinline__ TileBias tile_bias(const ScoreArgs& s, int h, float s
   return b;
 }
 
-// Bias of column c that is not in `base`, added to y.
+// Slopes with both signs, or a near table: the bias of column c in log2 units.
 template <int kBias, int kSign>
-__device__ __forceinline__ float add_column(const TileBias& b, int c, float y) {
-  if constexpr (kBias == SCORE_SLOPES) {
-    if (b.both) return fmaf(-b.slope, fabsf(b.dist0 + (float)(kSign * c)), y);
-    return fmaf((float)c, b.step, y);
-  }
-  if constexpr (kBias == SCORE_TABLE) {
-    if (b.tab) return y + b.tab[kSign * c];
-  }
-  return y;
+__device__ __forceinline__ float column_bias(const TileBias& b, int c) {
+  if constexpr (kBias == SCORE_SLOPES) return -b.slope * fabsf(b.dist0 + (float)(kSign * c));
+  if constexpr (kBias == SCORE_TABLE) return b.tab[kSign * c];
+  return 0.f;
 }
 
 }  // namespace score

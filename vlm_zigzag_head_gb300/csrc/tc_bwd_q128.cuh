@@ -186,60 +186,73 @@ __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4
   }
 }
 
-// P^T of 64 queries from the products, with modified scores: the probabilities
-// as bf16 pairs in pk (the dV operand); in place over the products what dS
-// multiplies: P, or under a cap P (1 - tanh^2).
-template <bool kCap, int kBias>
-__device__ __forceinline__ void score_columns(uint32_t (&rs)[2][32], uint32_t (&pk)[32], float sl2,
-                                              const score::Cap<kCap>& cap,
-                                              const score::TileBias& tb, const float* ld, bool vec,
-                                              int first_vis, int end_vis) {
-  const uint64_t sl2_2 = pack2(sl2, sl2);
-  bool poly = true;
-  if constexpr (kCap) {
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
+// P^T of 32 queries from their products (rs), with modified scores: the
+// probabilities as bf16 pairs in pk (the dV operand); in place over the products
+// what dS multiplies: P, or under a cap P (1 - tanh^2).  kFast: every pair is
+// visible, the cap's polynomial holds and the bias is linear along the queries.
+// mul: scale or cap in log2 units, inv its inverse.  x0: the half's first query in
+// the 64; ld: its lse2.
+template <bool kCap, int kBias, bool kFast>
+__device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, int x0, float mul,
+                                              float inv, const score::Cap<kCap>& cap,
+                                              const score::TileBias& tb, bool poly,
+                                              const float* ld, bool vec, int first_vis,
+                                              int end_vis) {
+  const uint64_t mul_2 = pack2(mul, mul), base2 = pack2(tb.base, tb.base), neg = pack2(-1.f, -1.f);
+  const float step = tb.step * inv;   // slopes, before `mul`
+  const bool column = kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr);
 #pragma unroll
-    for (int x = 0; x < 64; ++x)
-      big[x & 3] = fmaxf(big[x & 3], fabsf(__uint_as_float(rs[x >> 5][x & 31])));
-    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * sl2;
-    poly = __all_sync(0xffffffffu, b <= cap.limit);
-  }
-#pragma unroll
-  for (int x = 0; x < 64; x += 4) {
+  for (int x = 0; x < 32; x += 4) {
     float l[4];
     load_row4(ld + x, vec, l);
 #pragma unroll
-    for (int y = 0; y < 4; y += 2) {
-      uint32_t& e0 = rs[(x + y) >> 5][(x + y) & 31];
-      uint32_t& e1 = rs[(x + y) >> 5][(x + y + 1) & 31];
-      float s0, s1, w0 = 1.f, w1 = 1.f;
-      const uint64_t raw = pack2(__uint_as_float(e0), __uint_as_float(e1));
+    for (int y = x; y < x + 4; y += 2) {
+      uint64_t s = pack2(__uint_as_float(rs[y]), __uint_as_float(rs[y + 1])), w = 0;
+      float s0, s1;
       if constexpr (kCap) {
-        const uint64_t av = mul2(raw, sl2_2);
-        if (poly) {
-          unpack2(cap.poly(av), s0, s1);
+        if (kFast || poly) {
+          s = cap.poly(s);
         } else {
-          unpack2(av, s0, s1);
-          s0 = cap.any(s0);
-          s1 = cap.any(s1);
+          unpack2(s, s0, s1);
+          s = pack2(cap.any(s0), cap.any(s1));
         }
-        const float t0 = s0 * cap.inv, t1 = s1 * cap.inv;
-        w0 = fmaf(-t0, t0, 1.f);
-        w1 = fmaf(-t1, t1, 1.f);
-        s0 += tb.base;
-        s1 += tb.base;
-      } else {
-        unpack2(fma2(raw, sl2_2, pack2(tb.base, tb.base)), s0, s1);
+        w = cap.slope(s);
       }
-      float p0 = ex2(score::add_column<kBias, 1>(tb, x + y, s0) - l[y]);
-      float p1 = ex2(score::add_column<kBias, 1>(tb, x + y + 1, s1) - l[y + 1]);
-      if (x + y < first_vis || x + y >= end_vis) p0 = 0.f;
-      if (x + y + 1 < first_vis || x + y + 1 >= end_vis) p1 = 0.f;
-      pk[(x + y) / 2] = pack_bf16x2(p0, p1);
-      e0 = __float_as_uint(p0 * w0);
-      e1 = __float_as_uint(p1 * w1);
+      if constexpr (kBias == SCORE_SLOPES) {
+        unpack2(s, s0, s1);
+        s = pack2(fmaf((float)y, step, s0), fmaf((float)(y + 1), step, s1));
+      }
+      uint64_t add = fma2(pack2(l[y - x], l[y - x + 1]), neg, base2);
+      if (!kFast && column)
+        add = add2(add, pack2(score::column_bias<kBias, 1>(tb, x0 + y),
+                              score::column_bias<kBias, 1>(tb, x0 + y + 1)));
+      float p0, p1;
+      unpack2(fma2(s, mul_2, add), p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      if constexpr (!kFast) {
+        if (x0 + y < first_vis || x0 + y >= end_vis) p0 = 0.f;
+        if (x0 + y + 1 < first_vis || x0 + y + 1 >= end_vis) p1 = 0.f;
+      }
+      pk[y / 2] = pack_bf16x2(p0, p1);
+      if constexpr (kCap) unpack2(mul2(pack2(p0, p1), w), p0, p1);
+      rs[y] = __float_as_uint(p0);
+      rs[y + 1] = __float_as_uint(p1);
     }
   }
+}
+
+// Whether a warp's 64 products per lane all lie in the polynomial's range.
+template <bool kCap>
+__device__ __forceinline__ bool in_poly_range(const uint32_t (&rs)[2][32],
+                                              const score::Cap<kCap>& cap) {
+  if constexpr (!kCap) return true;
+  float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int x = 0; x < 64; x += 2)
+    big[(x >> 1) & 3] = fmaxf(fmaxf(big[(x >> 1) & 3], fabsf(__uint_as_float(rs[x >> 5][x & 31]))),
+                              fabsf(__uint_as_float(rs[x >> 5][(x & 31) + 1])));
+  return cap.in_range(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])));
 }
 
 // Gradient of a table bias: dS summed over the pairs of each |distance|.
@@ -617,9 +630,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sw = u & 7;
     bool ok = true;
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const score::Cap<kCap> cap(a.score);
+    const score::Cap<kCap> cap(a.score, sl2);
+    const float s_mul = kCap ? cap.cap2 : sl2, s_inv = kScored ? 1.f / s_mul : 0.f;
     int jt = 0, hq = hq0;       // tile and query head, as the producers walk them
-    float far_sum = 0.f;        // this thread's dS beyond the table (kBias: table)
+    float far_sum = 0.f;        // this thread's dS beyond the table (kBias: table),
+    uint64_t far2 = 0;          // and the same by even and odd queries
     for (int i = 0; ok && i < n_all; ++i) {
       const int st = i % kQStages;
       if (!mbar_wait(&bars->s_full, i & 1, lim, abort) ||
@@ -650,35 +665,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- P^T: probabilities of the 64 queries, computed in place over S and
       // kept in fp32 for dS; bf16 pairs into the first 32 of this warpgroup's
       // S columns
-      uint32_t pk[32];
       score::TileBias tb;
-      if constexpr (kScored) {
-        // distances rise along the queries; the half tile's span over its 128 keys
-        const int first = ti.rel + row0;
-        const float slope2 =
-            kBias == SCORE_SLOPES ? a.score.slopes[hq] * score::kLog2e : 0.f;
-        tb = score::tile_bias<kBias, 1>(a.score, hq, slope2, first - u, first - (kBK - 1),
-                                        first + 63, ti.causal != 0);
-        score_columns<kCap, kBias>(rs, pk, sl2, cap, tb, ld, vec, first_vis, end_vis);
-      } else {
+      uint32_t pk[2][16];   // P^T as bf16 pairs, 32 queries each
+      // distances rise along the queries; the half tile's span over its 128 keys
+      const int first = ti.rel + row0;
+      const float slope2 = kBias == SCORE_SLOPES ? a.score.slopes[hq] * score::kLog2e : 0.f;
+      tb = score::tile_bias<kBias, 1>(a.score, hq, slope2, first - u, first - (kBK - 1),
+                                      first + 63, ti.causal != 0);
+      const bool poly = in_poly_range<kCap>(rs, cap);
+      auto p_tile = [&](auto fast) {
+        constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        float l[4];
-        load_row4(ld + x, vec, l);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t& e = rs[(x + y) >> 5][(x + y) & 31];
-          float pv = ex2(fmaf(__uint_as_float(e), sl2, -l[y]));
-          if (!whole && (x + y < first_vis || x + y >= end_vis)) pv = 0.f;
-          e = __float_as_uint(pv);
+        for (int h = 0; h < 2; ++h) {
+          score::TileBias th = tb;
+          th.base += 32 * h * tb.step;
+          score_columns<kCap, kBias, kFast>(rs[h], pk[h], 32 * h, s_mul, s_inv, cap, th, poly,
+                                            ld + 32 * h, vec, first_vis, end_vis);
+          tmem_st16(tmem + lane_off + kColS + g * 64 + 16 * h, pk[h]);
         }
-      }
-#pragma unroll
-        for (int x = 0; x < 32; ++x)
-          pk[x] = pack_bf16x2(__uint_as_float(rs[x >> 4][(2 * x) & 31]),
-                              __uint_as_float(rs[x >> 4][(2 * x + 1) & 31]));
-      }
-      tmem_st32(tmem + lane_off + kColS + g * 64, pk);
+      };
+      if (whole && poly && !tb.both && tb.tab == nullptr) p_tile(std::true_type{});
+      else p_tile(std::false_type{});
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -689,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint8_t* srow = smem + L::kDS + g * L::kBox + u * 128;
       Diagonals diag[2];   // of the two blocks of 32 queries (kBias: table)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      auto ds_half = [&](int h, auto near_tile) {
+        [[maybe_unused]] constexpr bool kNear = decltype(near_tile)::value;
         uint32_t rd[32];
         tmem_ld32(tmem + lane_off + kColDP + g * 64 + h * 32, rd);
         tmem_ld_wait();
@@ -702,23 +709,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_row4(ld + kLdRows + h * 32 + x, vec, dd);
 #pragma unroll
           for (int y = 0; y < 4; y += 2) {
-            const float d0 = __uint_as_float(rs[h][x + y]) * (__uint_as_float(rd[x + y]) - dd[y]);
-            const float d1 =
-                __uint_as_float(rs[h][x + y + 1]) * (__uint_as_float(rd[x + y + 1]) - dd[y + 1]);
+            float d0, d1;
+            const uint64_t diff = fma2(pack2(dd[y], dd[y + 1]), pack2(-1.f, -1.f),
+                                       pack2(__uint_as_float(rd[x + y]),
+                                             __uint_as_float(rd[x + y + 1])));
+            const uint64_t ds = mul2(pack2(__uint_as_float(rs[h][x + y]),
+                                           __uint_as_float(rs[h][x + y + 1])), diff);
             if constexpr (kBias == SCORE_TABLE) {
-              float b0 = d0, b1 = d1;
+              uint64_t b = ds;
               if constexpr (kCap) {   // the bias is added behind the cap: P alone, from P^T
-                const uint32_t p2 = pk[(h * 32 + x + y) / 2];
-                b0 = __uint_as_float(p2 << 16) * (__uint_as_float(rd[x + y]) - dd[y]);
-                b1 = __uint_as_float(p2 & 0xffff0000u) * (__uint_as_float(rd[x + y + 1]) - dd[y + 1]);
+                const uint32_t p2 = pk[h][(x + y) / 2];
+                b = mul2(pack2(__uint_as_float(p2 << 16), __uint_as_float(p2 & 0xffff0000u)),
+                         diff);
               }
-              if (tb.tab == nullptr) {
-                far_sum += b0 + b1;
-              } else {
+              if constexpr (kNear) {
+                float b0, b1;
+                unpack2(b, b0, b1);
                 bias_grad(diag[h], x + y, b0, lane);
                 bias_grad(diag[h], x + y + 1, b1, lane);
+              } else {
+                far2 = add2(far2, b);
               }
             }
+            unpack2(ds, d0, d1);
             if constexpr (kF16)
               hk[(x + y) / 2] = pack_f16x2(d0 * ds_inv, d1 * ds_inv);
             else
@@ -731,6 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(srow + off) =
               make_uint4(hk[c * 4], hk[c * 4 + 1], hk[c * 4 + 2], hk[c * 4 + 3]);
         }
+      };
+      if (kBias == SCORE_TABLE && tb.tab != nullptr) {
+        ds_half(0, std::true_type{});
+        ds_half(1, std::true_type{});
+      } else {
+        ds_half(0, std::false_type{});
+        ds_half(1, std::false_type{});
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -746,7 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (++jt == n_qt) {
-        if constexpr (kBias == SCORE_TABLE) flush_far(a.score, hq, lane, far_sum);
+        if constexpr (kBias == SCORE_TABLE) {
+          float f0, f1;
+          unpack2(far2, f0, f1);
+          far_sum += f0 + f1;
+          flush_far(a.score, hq, lane, far_sum);
+          far2 = 0;
+        }
         jt = 0;
         ++hq;
       }

@@ -45,6 +45,8 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "check.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -139,44 +141,57 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-// The row's 128 products become modified scores (log2 units).
+// Modifies the row's 128 products in place; the scores in log2 units are then
+// r * mul + add.  mul comes in as the factor without a near bias (scale, or the
+// cap), inv as its inverse.  A cap without a bias keeps the order of the scores, so
+// while its polynomial serves the products stay as they are: returns true, and
+// the caller caps the row's maximum, and each product beside its exponential.
 template <bool kCap, int kBias>
-__device__ __forceinline__ void score_row(uint32_t (&r)[kBN / 32][32], float sl2,
-                                          const score::Cap<kCap>& cap,
-                                          const score::TileBias& tb) {
-  const uint64_t sl2_2 = pack2(sl2, sl2), base2 = pack2(tb.base, tb.base);
-  bool poly = true;
+__device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv,
+                                          const score::Cap<kCap>& cap, const score::TileBias& tb,
+                                          float& mul, float& add) {
+  add = tb.base;
+  bool lazy = false;
   if constexpr (kCap) {
     float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kBN; ++i)
-      big[i & 3] = fmaxf(big[i & 3], fabsf(__uint_as_float(r[i / 32][i % 32])));
-    const float b = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * sl2;
-    poly = __all_sync(0xffffffffu, b <= cap.limit);
-  }
-  if (!kCap || poly) {
+    for (int i = 0; i < kBN; i += 2)
+      big[(i >> 1) & 3] = fmaxf(fmaxf(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i / 32][i % 32]))),
+                                fabsf(__uint_as_float(r[i / 32][i % 32 + 1])));
+    if (cap.in_range(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])))) {
+      lazy = kBias == SCORE_PLAIN;
 #pragma unroll
-    for (int i = 0; i < kBN; i += 2) {
-      uint64_t y = pack2(__uint_as_float(r[i / 32][i % 32]),
-                                __uint_as_float(r[i / 32][i % 32 + 1]));
-      if constexpr (kCap) {
-        y = cap.poly(mul2(y, sl2_2));
-        if constexpr (kBias != SCORE_PLAIN) y = add2(y, base2);
-      } else {
-        y = fma2(y, sl2_2, base2);
+      for (int i = 0; i < (kBias == SCORE_PLAIN ? 0 : kBN); i += 2) {
+        float y0, y1;
+        unpack2(cap.poly(pack2(__uint_as_float(r[i / 32][i % 32]),
+                               __uint_as_float(r[i / 32][i % 32 + 1]))),
+                y0, y1);
+        r[i / 32][i % 32] = __float_as_uint(y0);
+        r[i / 32][i % 32 + 1] = __float_as_uint(y1);
       }
-      float y0, y1;
-      unpack2(y, y0, y1);
-      r[i / 32][i % 32] = __float_as_uint(score::add_column<kBias, -1>(tb, i, y0));
-      r[i / 32][i % 32 + 1] = __float_as_uint(score::add_column<kBias, -1>(tb, i + 1, y1));
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int i = 0; i < kBN; ++i) {
-      const float y = cap.any(__uint_as_float(r[i / 32][i % 32]) * sl2) + tb.base;
-      r[i / 32][i % 32] = __float_as_uint(score::add_column<kBias, -1>(tb, i, y));
+      for (int i = 0; i < kBN; ++i)
+        r[i / 32][i % 32] = __float_as_uint(cap.any(__uint_as_float(r[i / 32][i % 32])));
     }
   }
+  if constexpr (kBias == SCORE_SLOPES) {
+    if (!tb.both) {
+      const float step = tb.step * inv;   // in the row's present units
+#pragma unroll
+      for (int i = 0; i < kBN; ++i)
+        r[i / 32][i % 32] =
+            __float_as_uint(fmaf((float)i, step, __uint_as_float(r[i / 32][i % 32])));
+    }
+  }
+  if (kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr)) {
+#pragma unroll
+    for (int i = 0; i < kBN; ++i)
+      r[i / 32][i % 32] = __float_as_uint(
+          fmaf(__uint_as_float(r[i / 32][i % 32]), mul, score::column_bias<kBias, -1>(tb, i)));
+    mul = 1.f;
+  }
+  return lazy;
 }
 
 template <int D, bool kF16P, bool kCap, int kBias>
@@ -398,10 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     const int tq = x * kBM + t;                // query row of the item
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_off + col_s(x);
-    // modified scores replace the products (scale included): then no factor
+    // scores in log2 units: products (or what score_row makes of them) times sl2,
+    // plus s_add
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const float sl2 = kScored ? 1.f : a.scale_log2;
-    const score::Cap<kCap> cap(a.score);
+    const score::Cap<kCap> cap(a.score, a.scale_log2);
+    const float s_mul = kCap ? cap.cap2 : a.scale_log2, s_inv = kScored ? 1.f / s_mul : 0.f;
+    float sl2 = s_mul, s_add = 0.f;
     const float vmul = kF16P ? a.op_scales->v_mul : 1.f;   // V = V16 * vmul
     bool ok = true;
     int j = 0;   // KV tile counter across units
@@ -433,12 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < kBN / 32; ++c) reg_fence32(r[c]);
+        bool lazy = false;   // the products are still to be capped
         if constexpr (kScored) {
           // distances fall along the row; the tile's span is that of its 128 rows
           const int first = sg.rel + x * kBM - tt * kBN;
           const score::TileBias tb = score::tile_bias<kBias, -1>(
               a.score, h, slope2, first + t, first - (kBN - 1), first + kBM - 1, sg.causal != 0);
-          score_row<kCap, kBias>(r, a.scale_log2, cap, tb);
+          sl2 = s_mul;
+          lazy = score_row<kCap, kBias>(r, s_inv, cap, tb, sl2, s_add);
         }
         // keys at or past `vis` (tile-relative) are masked for this row
         const int vis = lim_u - tt * kBN;
@@ -456,8 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
             mp[i & 7] = fmaxf(mp[i & 7], i < vis ? __uint_as_float(r[i / 32][i % 32]) : -INFINITY);
         }
         // max of the raw scores, then to scaled log2 units (scale > 0)
-        const float mt = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+        const float mr = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+        const float mt = !kScored ? mr * sl2
+                         : lazy && mr != -INFINITY ? cap.any(mr) * sl2
+                                                   : fmaf(mr, sl2, s_add);
         const float m_new = fmaxf(m, mt);
         const bool need = m_new > m + kRescaleThreshold || (m == -INFINITY && m_new != -INFINITY);
         if (__any_sync(0xffffffffu, need)) {
@@ -485,29 +507,41 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
         }
         // probabilities, row sum, and P (bf16 pairs, or f16 pairs for the f16 PV
         // product) over S columns [0, 64)
-        const float mu = m == -INFINITY ? 0.f : m;
+        const float mu = (m == -INFINITY ? 0.f : m) - (kScored ? s_add : 0.f);
         float sp[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) sp[i] = 0.f;
         uint32_t pk[2][32];
-        if (whole) {
+        const uint64_t mul_2 = pack2(sl2, sl2), sub2 = pack2(-mu, -mu);
+        auto exponentials = [&](auto all_seen, auto to_cap) {
+          constexpr bool kWhole = decltype(all_seen)::value, kLazy = decltype(to_cap)::value;
 #pragma unroll
           for (int i = 0; i < kBN; i += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(r[i / 32][i % 32]), sl2, -mu));
-            const float p1 = ex2(fmaf(__uint_as_float(r[i / 32][i % 32 + 1]), sl2, -mu));
+            uint64_t y = pack2(__uint_as_float(r[i / 32][i % 32]),
+                               __uint_as_float(r[i / 32][i % 32 + 1]));
+            if constexpr (kLazy) y = cap.poly(y);
+            float p0, p1;
+            unpack2(fma2(y, mul_2, sub2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            if constexpr (!kWhole) {
+              if (i >= vis) p0 = 0.f;
+              if (i + 1 >= vis) p1 = 0.f;
+            }
             sp[(i >> 1) & 7] += p0 + p1;
             pk[i / 64][(i / 2) % 32] = pack_op2<kF16P>(p0, p1);
+          }
+        };
+        if constexpr (kCap && kBias == SCORE_PLAIN) {
+          if (lazy) {
+            if (whole) exponentials(std::true_type{}, std::true_type{});
+            else exponentials(std::false_type{}, std::true_type{});
+          } else {
+            exponentials(std::false_type{}, std::false_type{});
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < kBN; i += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(r[i / 32][i % 32]), sl2, -mu));
-            float p1 = ex2(fmaf(__uint_as_float(r[i / 32][i % 32 + 1]), sl2, -mu));
-            if (i >= vis) p0 = 0.f;
-            if (i + 1 >= vis) p1 = 0.f;
-            sp[(i >> 1) & 7] += p0 + p1;
-            pk[i / 64][(i / 2) % 32] = pack_op2<kF16P>(p0, p1);
-          }
+          if (whole) exponentials(std::true_type{}, std::false_type{});
+          else exponentials(std::false_type{}, std::false_type{});
         }
         tmem_st32(s_col, pk[0]);
         tmem_st32(s_col + 32, pk[1]);
