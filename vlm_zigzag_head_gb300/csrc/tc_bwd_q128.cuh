@@ -637,21 +637,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t far2 = 0;          // and the same by even and odd queries
     for (int i = 0; ok && i < n_all; ++i) {
       const int st = i % kQStages;
-      if (!mbar_wait(&bars->s_full, i & 1, lim, abort) ||
-          !mbar_wait(&bars->q_full[st], (i / kQStages) & 1, lim, abort)) {
+      if (!mbar_wait(&bars->q_full[st], (i / kQStages) & 1, lim, abort)) {
         ok = false;
         break;
       }
-      tc_fence_after();
-      // the slot is rewritten only after this tile's dK product, which waits
-      // for this warpgroup's dS
+      // Everything that follows from the tile's place is worked out before its
+      // products are ready.  The slot is rewritten only after this tile's dK
+      // product, which waits for this warpgroup's dS.
       const TileInfo ti = reinterpret_cast<const TileInfo*>(smem + L::kInfo)[st];
-      uint32_t rs[2][32];
-      tmem_ld32(tmem + lane_off + kColS + g * 64, rs[0]);
-      tmem_ld32(tmem + lane_off + kColS + g * 64 + 32, rs[1]);
-      tmem_ld_wait();
-      reg_fence32(rs[0]);
-      reg_fence32(rs[1]);
       const int tile_row = ti.tile_row;                     // natural row of the tile's first query
       const int row0 = ti.row_in + g * 64;                  // first query of this half (inside the run)
       const float* ld = reinterpret_cast<const float*>(smem + L::kLd + st * L::kLdStride) +
@@ -662,16 +655,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end_vis = key_ok ? ti.len - row0 : 0;
       const bool whole = __all_sync(0xffffffffu, first_vis <= 0 && end_vis >= 64);
       const bool vec = (tile_row & 3) == 0;
-      // ---- P^T: probabilities of the 64 queries, computed in place over S and
-      // kept in fp32 for dS; bf16 pairs into the first 32 of this warpgroup's
-      // S columns
-      score::TileBias tb;
-      uint32_t pk[2][16];   // P^T as bf16 pairs, 32 queries each
       // distances rise along the queries; the half tile's span over its 128 keys
       const int first = ti.rel + row0;
-      const float slope2 = kBias == SCORE_SLOPES ? a.score.slopes[hq] * score::kLog2e : 0.f;
-      tb = score::tile_bias<kBias, 1>(a.score, hq, slope2, first - u, first - (kBK - 1),
-                                      first + 63, ti.causal != 0);
+      score::TileBias tb;
+      if constexpr (kBias != SCORE_PLAIN) {
+        const float slope2 = kBias == SCORE_SLOPES ? a.score.slopes[hq] * score::kLog2e : 0.f;
+        tb = score::tile_bias<kBias, 1>(a.score, hq, slope2, first - u, first - (kBK - 1),
+                                        first + 63, ti.causal != 0);
+      }
+      if (!mbar_wait(&bars->s_full, i & 1, lim, abort)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t rs[2][32];
+      tmem_ld32(tmem + lane_off + kColS + g * 64, rs[0]);
+      tmem_ld32(tmem + lane_off + kColS + g * 64 + 32, rs[1]);
+      tmem_ld_wait();
+      reg_fence32(rs[0]);
+      reg_fence32(rs[1]);
+      // ---- P^T: probabilities of the 64 queries, computed in place over S and
+      // kept in fp32 for dS; bf16 pairs into the first 32 of this warpgroup's
+      // S columns, in halves
+      uint32_t pk[2][16];   // P^T as bf16 pairs, 32 queries each
       const bool poly = in_poly_range<kCap>(rs, cap);
       auto p_tile = [&](auto fast) {
         constexpr bool kFast = decltype(fast)::value;

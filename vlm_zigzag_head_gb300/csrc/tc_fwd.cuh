@@ -440,6 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       // key u of the run is visible to this row iff u < lim_u
       const int lim_u = sg.causal ? min(sg.len, tq + sg.delta + 1) : sg.len;
       for (int tt = 0; tt < nt; ++tt, ++j) {
+        // the tile's bias, worked out before its products are ready: distances fall
+        // along the row; the tile's span is that of its 128 rows
+        const int first = sg.rel + x * kBM - tt * kBN;
+        score::TileBias tb;
+        if constexpr (kBias != SCORE_PLAIN)
+          tb = score::tile_bias<kBias, -1>(a.score, h, slope2, first + t, first - (kBN - 1),
+                                           first + kBM - 1, sg.causal != 0);
         if (!mbar_wait(&bars->s_full[x], j & 1, lim, abort)) { ok = false; break; }
         tc_fence_after();
         // the whole 128-column S row of this thread in registers: one TMEM
@@ -452,10 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
         for (int c = 0; c < kBN / 32; ++c) reg_fence32(r[c]);
         bool lazy = false;   // the products are still to be capped
         if constexpr (kScored) {
-          // distances fall along the row; the tile's span is that of its 128 rows
-          const int first = sg.rel + x * kBM - tt * kBN;
-          const score::TileBias tb = score::tile_bias<kBias, -1>(
-              a.score, h, slope2, first + t, first - (kBN - 1), first + kBM - 1, sg.causal != 0);
           sl2 = s_mul;
           lazy = score_row<kCap, kBias>(r, s_inv, cap, tb, sl2, s_add);
         }
