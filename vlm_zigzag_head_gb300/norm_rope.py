@@ -12,19 +12,11 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import CP_F32, CpError, _binding as _b, _dt, _ptr, _stream
+from . import CP_F32, CpError, _binding as _b, _dt
 
 
-@functools.lru_cache(maxsize=64)
-def _freq_array(theta: float, rot_dim: int, inv_freq: Optional[tuple]):
-    """Radians per position of every rotated pair, as a C array of doubles."""
-    if inv_freq is None:
-        if not theta > 0:
-            raise CpError(1, "theta must be positive")
-        inv_freq = tuple(theta ** (-2.0 * p / rot_dim) for p in range(rot_dim // 2))
-    elif len(inv_freq) != rot_dim // 2:
-        raise CpError(2, "inv_freq must have rot_dim / 2 entries")
-    return (ctypes.c_double * max(1, len(inv_freq)))(*inv_freq)
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _check_heads(x, name, like=None):
@@ -32,27 +24,24 @@ def _check_heads(x, name, like=None):
         raise CpError(2, "%s must be [T, heads, d]" % name)
     if not x.is_cuda:
         raise CpError(1, "tensors must live on a CUDA device")
-    if x.shape[2] > 1 and x.stride(2) != 1:
-        raise CpError(1, "the last dimension of %s must be contiguous" % name)
-    if like is not None and (x.device != like.device or x.dtype != like.dtype or
-                             x.shape[0] != like.shape[0] or x.shape[2] != like.shape[2]):
-        raise CpError(2, "q and k must share device, dtype, tokens and head size")
+    if like is not None and (x.device != like.device or x.dtype != like.dtype):
+        raise CpError(2, "q and k must share device and dtype")
 
 
-def _desc(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections, interleaved,
-          inv_freq):
-    """Checked descriptor and the tensors' pointers."""
-    _check_heads(q, "q")
-    _check_heads(k, "k", q)
-    T, H, d = q.shape
+@functools.lru_cache(maxsize=256)
+def _desc(dtype, q_shape, q_stride, k_shape, k_stride, pos_shape, w_dtype, eps, theta, rot_dim,
+          sections, interleaved, inv_freq):
+    """The checked descriptor of one set of shapes and options."""
+    T, H, d = q_shape
+    if k_shape[0] != T or k_shape[2] != d:
+        raise CpError(2, "q and k must share tokens and head size")
+    if d > 1 and (q_stride[2] != 1 or k_stride[2] != 1):
+        raise CpError(1, "the last dimension of q and k must be contiguous")
     rot = d if rot_dim is None else int(rot_dim)
     if rot < 0 or rot > d or rot % 16:
         raise CpError(2, "rot_dim must be a multiple of 16 in [0, head_dim]")
-    if positions.dtype != torch.int32 or not positions.is_contiguous() or \
-            positions.device != q.device:
-        raise CpError(3, "positions must be a contiguous int32 tensor on q's device")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dim() not in (1, 2) or positions.shape[-1] != T or not 1 <= axes <= 4:
+    axes = 1 if len(pos_shape) == 1 else pos_shape[0]
+    if len(pos_shape) not in (1, 2) or pos_shape[-1] != T or not 1 <= axes <= 4:
         raise CpError(2, "positions must be [T] or [axes, T] with at most 4 axes")
     if sections is None:
         if axes != 1:
@@ -60,26 +49,46 @@ def _desc(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections, in
         sections = (rot // 2,)
     if len(sections) != axes:
         raise CpError(2, "sections must have one entry per position axis")
-    ws = [w for w in (q_weight, k_weight) if w is not None]
-    for w in ws:
-        if w.shape != (d,) or not w.is_contiguous() or w.device != q.device or \
-                w.dtype != ws[0].dtype:
-            raise CpError(2, "norm weights must be contiguous [head_dim] tensors of one dtype "
-                             "on q's device")
+    if inv_freq is None:
+        if not theta > 0:
+            raise CpError(1, "theta must be positive")
+        inv_freq = [theta ** (-2.0 * p / rot) for p in range(rot // 2)]
+    elif len(inv_freq) != rot // 2:
+        raise CpError(2, "inv_freq must have rot_dim / 2 entries")
     f = _b.NormRopeDesc()
-    f.dtype = _dt(q)
-    f.weight_dtype = _dt(ws[0]) if ws else CP_F32
-    f.T, f.H, f.H_kv, f.d = T, H, k.shape[1], d
+    f.dtype, f.weight_dtype = dtype, w_dtype
+    f.T, f.H, f.H_kv, f.d = T, H, k_shape[1], d
     # the stride of a dimension of one element is never used
-    f.q_stride_t, f.q_stride_h = (s if n > 1 else 0 for s, n in zip(q.stride(), q.shape[:2]))
-    f.k_stride_t, f.k_stride_h = (s if n > 1 else 0 for s, n in zip(k.stride(), k.shape[:2]))
-    f.rot_dim, f.interleaved, f.n_axes = rot, int(bool(interleaved)), axes
+    f.q_stride_t, f.q_stride_h = (s if n > 1 else 0 for s, n in zip(q_stride, q_shape[:2]))
+    f.k_stride_t, f.k_stride_h = (s if n > 1 else 0 for s, n in zip(k_stride, k_shape[:2]))
+    f.rot_dim, f.interleaved, f.n_axes = rot, int(interleaved), axes
     for i, n in enumerate(sections):
-        f.sections[i] = int(n)
-    f.inv_freq = _freq_array(float(theta), rot, None if inv_freq is None else
-                             tuple(float(x) for x in inv_freq))
-    f.eps = float(eps)
+        f.sections[i] = n
+    f.inv_freq = (ctypes.c_double * max(1, len(inv_freq)))(*inv_freq)
+    f.eps = eps
     return f
+
+
+def _prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections, interleaved,
+             inv_freq):
+    _check_heads(q, "q")
+    _check_heads(k, "k", q)
+    if positions.dtype != torch.int32 or positions.device != q.device or \
+            not positions.is_contiguous():
+        raise CpError(3, "positions must be a contiguous int32 tensor on q's device")
+    w_dtype = CP_F32
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        if w.shape != q.shape[2:] or w.device != q.device or not w.is_contiguous():
+            raise CpError(2, "norm weights must be contiguous [head_dim] tensors on q's device")
+        w_dtype = _dt(w)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise CpError(3, "the norm weights must share a dtype")
+    return _desc(_dt(q), tuple(q.shape), q.stride(), tuple(k.shape), k.stride(),
+                 tuple(positions.shape), w_dtype, float(eps), float(theta), rot_dim,
+                 None if sections is None else tuple(int(n) for n in sections), bool(interleaved),
+                 None if inv_freq is None else tuple(float(x) for x in inv_freq))
 
 
 def cp_qk_norm_rope_fwd(q, k, positions, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -95,14 +104,15 @@ def cp_qk_norm_rope_fwd(q, k, positions, q_weight=None, k_weight=None, eps: floa
     times ``inv_freq[p]`` (default ``theta ** (-2 p / rot_dim)``).
     ``q_weight`` / ``k_weight``: norm weights ``[d]`` (bf16 or fp32) or None.
     Returns contiguous ``(q_out, k_out)``."""
-    f = _desc(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections, interleaved,
-              inv_freq)
+    f = _prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections,
+                 interleaved, inv_freq)
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     with torch.cuda.device(q.device):
         _b.check(_b.lib().cp_qk_norm_rope_fwd(
-            ctypes.byref(f), _ptr(q), _ptr(k), _ptr(positions), _ptr(q_weight), _ptr(k_weight),
-            _ptr(q_out), _ptr(k_out), _stream(q.device)))
+            ctypes.byref(f), q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight),
+            _at(k_weight), q_out.data_ptr(), k_out.data_ptr(),
+            torch.cuda.current_stream().cuda_stream))
     return q_out, k_out
 
 
@@ -114,8 +124,8 @@ def cp_qk_norm_rope_bwd(q, k, positions, dq_out, dk_out, q_weight=None, k_weight
     gradients of its outputs: contiguous, q's dtype).  Returns ``(dq, dk,
     dq_weight, dk_weight)``: dq, dk contiguous in q's dtype; the weight
     gradients fp32 ``[d]``, or None for a weight that is None."""
-    f = _desc(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections, interleaved,
-              inv_freq)
+    f = _prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections,
+                 interleaved, inv_freq)
     for g, x in ((dq_out, q), (dk_out, k)):
         if g.shape != x.shape or g.dtype != x.dtype or g.device != x.device or \
                 not g.is_contiguous():
@@ -131,7 +141,7 @@ def cp_qk_norm_rope_bwd(q, k, positions, dq_out, dk_out, q_weight=None, k_weight
             nbytes = _b.lib().cp_qk_norm_rope_bwd_workspace_size(ctypes.byref(f))
             ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
         _b.check(_b.lib().cp_qk_norm_rope_bwd(
-            ctypes.byref(f), _ptr(q), _ptr(k), _ptr(positions), _ptr(q_weight), _ptr(k_weight),
-            _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(ws),
-            nbytes, _stream(q.device)))
+            ctypes.byref(f), q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight),
+            _at(k_weight), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+            _at(dqw), _at(dkw), _at(ws), nbytes, torch.cuda.current_stream().cuda_stream))
     return dq, dk, dqw, dkw

@@ -14,7 +14,8 @@ from typing import List, Optional, Sequence, Union
 
 import torch
 
-from . import CP_BF16, CpError, Workspace, _binding as _b, _dt, _need_cuda, _ptr, _stream
+from . import CP_BF16, CpError, Workspace, _binding as _b, _dt, _need_cuda
+from .norm_rope import _at
 
 
 def relative_buckets(n_buckets: int, max_distance: int) -> List[int]:
@@ -65,13 +66,23 @@ class ScorePlan:
             self.dev = torch.frombuffer(self.host, dtype=torch.uint8).to(device)
             self._stream = torch.cuda.current_stream(device)
         self.device = device
+        self._block = (ctypes.c_char * len(self.host)).from_buffer(self.host)
+        self._sizes = {}   # workspace bytes by direction, dtype, KV heads, head size and scale
 
-    def _use(self):
-        """The device copy, kept from reuse until the current stream is done with it."""
-        stream = torch.cuda.current_stream(self.device)
+    def _use(self, stream):
+        """The device copy, kept from reuse until ``stream`` is done with it."""
         if stream != self._stream and not torch.cuda.is_current_stream_capturing():
             self.dev.record_stream(stream)
-        return _ptr(self.dev)
+        return self.dev.data_ptr()
+
+    def _workspace_bytes(self, backward, dt, H_kv, d, scale):
+        key = (backward, dt, H_kv, d, scale)
+        if key not in self._sizes:
+            L = _b.lib()
+            size = L.cp_attn_scored_bwd_workspace_size if backward else \
+                L.cp_attn_scored_fwd_workspace_size
+            self._sizes[key] = size(self._block, dt, H_kv, d, scale)
+        return self._sizes[key]
 
 
 def build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix, rel_buckets, n_sms):
@@ -139,9 +150,9 @@ def _space(workspace, nbytes, device):
     """(holder, pointer, bytes): the caller's workspace, or a new one for this call alone."""
     if workspace is None:
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return buf, _ptr(buf), nbytes
+        return buf, buf.data_ptr(), nbytes
     workspace.get(nbytes, device)
-    return workspace, ctypes.c_void_p(workspace.ptr()), workspace.nbytes()
+    return workspace, workspace.ptr(), workspace.nbytes()
 
 
 def cp_attn_scored_fwd(q, k, v, plan: ScorePlan, softmax_scale: float, softcap: float = 0.0,
@@ -165,15 +176,15 @@ def cp_attn_scored_fwd(q, k, v, plan: ScorePlan, softmax_scale: float, softcap: 
     if out_lo is not None or (residual and dt == CP_BF16):
         out_lo = _like(out_lo, q.shape, q.dtype, q.device, "out_lo")
     s = _scores(q, plan, softcap, slopes, rel_bias)
-    L = _b.lib()
-    host = (ctypes.c_char * len(plan.host)).from_buffer(plan.host)
+    scale = float(softmax_scale)
     with torch.cuda.device(q.device):
-        nbytes = L.cp_attn_scored_fwd_workspace_size(host, dt, k.shape[1], d, float(softmax_scale))
+        nbytes = plan._workspace_bytes(False, dt, k.shape[1], d, scale)
         ws, ptr, size = _space(workspace, nbytes, q.device)
-        _b.check(L.cp_attn_scored_fwd(host, plan._use(), _ptr(q), _ptr(k), _ptr(v), dt, T, H,
-                                      k.shape[1], d, ctypes.byref(s), float(softmax_scale),
-                                      _ptr(out), _ptr(lse), _ptr(out_lo), ptr, size,
-                                      _stream(q.device)))
+        stream = torch.cuda.current_stream()
+        _b.check(_b.lib().cp_attn_scored_fwd(
+            plan._block, plan._use(stream), q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, T, H,
+            k.shape[1], d, ctypes.byref(s), scale, out.data_ptr(), lse.data_ptr(), _at(out_lo),
+            ptr, size, stream.cuda_stream))
     return (out, lse, out_lo) if residual else (out, lse)
 
 
@@ -198,13 +209,14 @@ def cp_attn_scored_bwd(q, k, v, out, lse, dout, plan: ScorePlan, softmax_scale: 
     dbias = None
     if rel_bias is not None:
         dbias = torch.empty(rel_bias.shape, dtype=torch.float32, device=q.device)
-    L = _b.lib()
-    host = (ctypes.c_char * len(plan.host)).from_buffer(plan.host)
+    scale = float(softmax_scale)
     with torch.cuda.device(q.device):
-        nbytes = L.cp_attn_scored_bwd_workspace_size(host, dt, k.shape[1], d, float(softmax_scale))
+        nbytes = plan._workspace_bytes(True, dt, k.shape[1], d, scale)
         ws, ptr, size = _space(workspace, nbytes, q.device)
-        _b.check(L.cp_attn_scored_bwd(host, plan._use(), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                      _ptr(out_lo), _ptr(lse), _ptr(dout), dt, T, H, k.shape[1], d,
-                                      ctypes.byref(s), float(softmax_scale), _ptr(dq), _ptr(dk),
-                                      _ptr(dv), _ptr(dbias), ptr, size, _stream(q.device)))
+        stream = torch.cuda.current_stream()
+        _b.check(_b.lib().cp_attn_scored_bwd(
+            plan._block, plan._use(stream), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            out.data_ptr(), _at(out_lo), lse.data_ptr(), dout.data_ptr(), dt, T, H, k.shape[1], d,
+            ctypes.byref(s), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _at(dbias), ptr,
+            size, stream.cuda_stream))
     return (dq, dk, dv) if dbias is None else (dq, dk, dv, dbias)
