@@ -36,11 +36,18 @@ const ScorePlanHeader* header(const void* plan_h) {
 // Offsets into the workspace of either direction.
 struct Ws {
   size_t status = 0, table = 0, scales = 0, v16 = 0;                   // forward
+  size_t part_out = 0, part_lse = 0;                                   // forward, fp32
   size_t lse2 = 0, D = 0, q16 = 0, k16 = 0, dtable = 0;                // backward
   size_t total = 0;
 };
 
 inline int64_t ld_pitch(int64_t T) { return (T + 3) / 4 * 4; }
+
+// The forward's partial results live in the workspace, so its split follows from
+// the plan alone (n_sms is the plan's).
+int f32_fwd_splits(const ScorePlanHeader& h) {
+  return f32_splits((int64_t)h.n_tiles * h.H, h.max_walk, h.n_sms);
+}
 
 Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward) {
   Ws w;
@@ -54,6 +61,11 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
   if (!backward) {
     w.v16 = o;
     if (f16) o = up256(o + T * Hkv * d * 2);
+    const size_t parts = dt == CP_F32 ? f32_fwd_splits(h) : 1;
+    w.part_out = o;
+    if (parts > 1) o = up256(o + parts * T * h.H * d * sizeof(float));
+    w.part_lse = o;
+    if (parts > 1) o = up256(o + parts * T * h.H * sizeof(float));
   } else {
     w.lse2 = o;
     w.D = o + (size_t)ld_pitch(T) * h.H * sizeof(float);   // plane 1 directly after plane 0
@@ -178,6 +190,7 @@ F32Args f32_args(const Call& c, const cp_score_t* sc, const char* plan, const Sc
   a.T = c.h->T;
   a.scale = scale;
   a.softcap = sc->softcap;
+  a.inv_cap = sc->softcap > 0.f ? 1.f / sc->softcap : 0.f;
   a.slopes = sc->slopes;
   a.table = s.table;
   a.table_pitch = s.table_pitch;
@@ -287,10 +300,15 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
     a.q = static_cast<const float*>(q);
     a.k = static_cast<const float*>(k);
     a.v = static_cast<const float*>(v);
-    a.out = static_cast<float*>(out);
-    a.lse = lse;
-    ProfileScope prof(6, st);
+    a.splits = f32_fwd_splits(*c.h);
+    const bool parts = a.splits > 1;
+    a.out = parts ? reinterpret_cast<float*>(w + c.ws.part_out) : static_cast<float*>(out);
+    a.lse = parts ? reinterpret_cast<float*>(w + c.ws.part_lse) : lse;
+    ProfileScope prof(6, st, parts ? 2 : 1);
     ENTRY_CUDA(launch_f32_fwd(a, d, st), "fp32 scored forward");
+    if (parts)
+      ENTRY_CUDA(launch_lse_merge(a.splits, a.out, a.lse, T, H, d, out, false, lse, st),
+                 "merge of partial results");
     return CP_OK;
   }
   const void* vsrc = v;
@@ -407,6 +425,15 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.dk = dk;
     a.dv = dv;
     a.dtable = s.dtable;
+    a.splits = f32_splits((int64_t)a.n_tiles * H, c.h->max_walk, sms);
+    a.add_dq = a.splits > 1;
+    a.add_dkdv = a.splits > 1 || H > Hkv;
+    if (a.add_dq)
+      ENTRY_CUDA(cudaMemsetAsync(dq, 0, (size_t)T * H * d * sizeof(float), st), "clear dq");
+    if (a.add_dkdv) {
+      ENTRY_CUDA(cudaMemsetAsync(dk, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dk");
+      ENTRY_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");
+    }
     ProfileScope prof(7, st, 2);
     ENTRY_CUDA(launch_f32_bwd(a, d, st), "fp32 scored backward");
   } else {

@@ -8,8 +8,11 @@
 //   scores   16 fused multiply-adds per two 16-byte shared loads,
 //   outputs  4 d / 4 of them per d / 16 + 4 such loads (contraction in fours),
 // so the products are bound by fp32 arithmetic, not by shared memory.
-// Backward: one kernel per output side (dQ by query tiles; dK, dV by key tiles,
-// summed over the query heads that share a KV head), each result written once.
+// Backward: one kernel per output side (dQ by query tiles; dK, dV by key tiles and
+// query heads).  These inputs are short as a rule, so a tile's walk is what bounds
+// a launch: several blocks share it (f32_splits), forward by the log-sum-exp merge
+// of their partial results, backward by fp32 adds into zeroed gradients, as for
+// the query heads that share a KV head.
 #include "scored.h"
 
 namespace cpattn {
@@ -101,7 +104,7 @@ __device__ __forceinline__ float score(const F32Args& a, int h, float s, int i, 
   float x = s * a.scale;
   t = 0.f;
   if (a.softcap > 0.f) {
-    t = tanhf(x / a.softcap);
+    t = tanhf(x * a.inv_cap);
     x = a.softcap * t;
   }
   const int dist = i - j;
@@ -123,6 +126,12 @@ __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// The tiles [first, last) of a walk of n that fall to this block.
+__device__ __forceinline__ void my_tiles(const F32Args& a, int n, int& first, int& last) {
+  first = (int)((int64_t)n * blockIdx.z / a.splits);
+  last = (int)((int64_t)n * (blockIdx.z + 1) / a.splits);
 }
 
 // Keys a query tile sees: up to its last row, or the whole both-way prefix.
@@ -152,7 +161,9 @@ __global__ void __launch_bounds__(kThreads) f32_fwd_kernel(const F32Args a) {
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) o[i][j] = 0.f;
   }
-  for (int u0 = 0; u0 < nkeys; u0 += kT) {
+  int first, last;
+  my_tiles(a, (nkeys + kT - 1) / kT, first, last);
+  for (int u0 = first * kT; u0 < last * kT; u0 += kT) {
     const int n = min(kT, nkeys - u0);
     __syncthreads();
     stage<D>(K, a.k + (tl.seq0 + u0) * ks + hk * D, n, ks);
@@ -192,10 +203,12 @@ __global__ void __launch_bounds__(kThreads) f32_fwd_kernel(const F32Args a) {
     const int r = 4 * ty + i;
     if (r >= tl.len) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-    float* dst = a.out + (tl.row0 + r) * qs + h * D;
+    float* dst = a.out + (blockIdx.z * a.T + tl.row0 + r) * qs + h * D;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) dst[tx + 16 * j] = o[i][j] * inv;
-    if (tx == 0) a.lse[h * a.T + tl.row0 + r] = l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+    if (tx == 0)
+      a.lse[((int64_t)blockIdx.z * a.H + h) * a.T + tl.row0 + r] =
+          l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
   }
 }
 
@@ -223,7 +236,10 @@ __global__ void __launch_bounds__(kThreads) f32_dq_kernel(const F32Args a) {
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) dq[i][j] = 0.f;
   }
-  for (int u0 = 0; u0 < nkeys; u0 += kT) {
+  int first, last;
+  my_tiles(a, (nkeys + kT - 1) / kT, first, last);
+  if (first >= last) return;
+  for (int u0 = first * kT; u0 < last * kT; u0 += kT) {
     const int n = min(kT, nkeys - u0);
     __syncthreads();
     stage<D>(K, a.k + (tl.seq0 + u0) * ks + hk * D, n, ks);
@@ -266,7 +282,10 @@ __global__ void __launch_bounds__(kThreads) f32_dq_kernel(const F32Args a) {
     if (r >= tl.len) continue;
     float* dst = a.dq + (tl.row0 + r) * qs + h * D;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) dst[tx + 16 * j] = dq[i][j];
+    for (int j = 0; j < D / 16; ++j) {
+      if (a.add_dq) atomicAdd(dst + tx + 16 * j, dq[i][j]);
+      else dst[tx + 16 * j] = dq[i][j];
+    }
   }
 }
 
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) f32_dkdv_kernel(const F32Args a) {
   float* P = dO + tile_floats<D>();
   float* S = P + kPFloats;
   const Tile32 tl = a.tiles[blockIdx.x];
-  const int hk = blockIdx.y, G = a.H / a.Hkv;
+  const int h = blockIdx.y, hk = h / (a.H / a.Hkv);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int u0 = tl.row0 - tl.seq0;
   const int64_t qs = (int64_t)a.H * D, ks = (int64_t)a.Hkv * D;
@@ -291,9 +310,13 @@ __global__ void __launch_bounds__(kThreads) f32_dkdv_kernel(const F32Args a) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) dk[i][j] = dv[i][j] = 0.f;
-  for (int h = hk * G; h < (hk + 1) * G; ++h) {
+  {
     // queries that see this tile: its own rows on, or all for a both-way prefix
-    for (int t0 = u0 < tl.prefix ? 0 : u0; t0 < tl.seq_len; t0 += kT) {
+    const int start = u0 < tl.prefix ? 0 : u0;
+    int first, last;
+    my_tiles(a, (tl.seq_len - start + kT - 1) / kT, first, last);
+    if (first >= last) return;
+    for (int t0 = start + first * kT; t0 < start + last * kT; t0 += kT) {
       const int n = min(kT, tl.seq_len - t0);
       __syncthreads();
       stage<D>(Q, a.q + (tl.seq0 + t0) * qs + h * D, n, qs);
@@ -332,18 +355,23 @@ __global__ void __launch_bounds__(kThreads) f32_dkdv_kernel(const F32Args a) {
     const int64_t at = (tl.row0 + r) * ks + hk * D;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-      a.dk[at + tx + 16 * j] = dk[i][j];
-      a.dv[at + tx + 16 * j] = dv[i][j];
+      if (a.add_dkdv) {
+        atomicAdd(a.dk + at + tx + 16 * j, dk[i][j]);
+        atomicAdd(a.dv + at + tx + 16 * j, dv[i][j]);
+      } else {
+        a.dk[at + tx + 16 * j] = dk[i][j];
+        a.dv[at + tx + 16 * j] = dv[i][j];
+      }
     }
   }
 }
 
 template <typename K>
-cudaError_t run(K kernel, int tiles, int heads, int floats, const F32Args& a, cudaStream_t st) {
+cudaError_t run(K kernel, int floats, const F32Args& a, cudaStream_t st) {
   const int bytes = floats * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kernel<<<dim3(tiles, heads), kThreads, bytes, st>>>(a);
+  kernel<<<dim3(a.n_tiles, a.H, a.splits), kThreads, bytes, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -351,17 +379,17 @@ template <int D>
 cudaError_t bwd_d(const F32Args& a, cudaStream_t st) {
   constexpr int t = tile_floats<D>();
   static_assert((4 * t + 2 * kPFloats) * 4 <= 227 * 1024, "shared memory budget");
-  cudaError_t e = run(f32_dq_kernel<D>, a.n_tiles, a.H, 4 * t + kPFloats, a, st);
+  cudaError_t e = run(f32_dq_kernel<D>, 4 * t + kPFloats, a, st);
   if (e != cudaSuccess) return e;
-  return run(f32_dkdv_kernel<D>, a.n_tiles, a.Hkv, 4 * t + 2 * kPFloats, a, st);
+  return run(f32_dkdv_kernel<D>, 4 * t + 2 * kPFloats, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_f32_fwd(const F32Args& a, int d, cudaStream_t st) {
   if (a.n_tiles == 0) return cudaSuccess;
-  return d == 64 ? run(f32_fwd_kernel<64>, a.n_tiles, a.H, 3 * tile_floats<64>() + kPFloats, a, st)
-                 : run(f32_fwd_kernel<128>, a.n_tiles, a.H, 3 * tile_floats<128>() + kPFloats, a, st);
+  return d == 64 ? run(f32_fwd_kernel<64>, 3 * tile_floats<64>() + kPFloats, a, st)
+                 : run(f32_fwd_kernel<128>, 3 * tile_floats<128>() + kPFloats, a, st);
 }
 
 cudaError_t launch_f32_bwd(const F32Args& a, int d, cudaStream_t st) {

@@ -24,16 +24,27 @@ struct F32Args {
   const Tile32* tiles;
   int n_tiles, H, Hkv;
   int64_t T;
-  float scale, softcap;                // softcap 0: none
+  float scale, softcap, inv_cap;       // softcap 0: none
   const float* slopes;                 // nullable [H]
   const float* table;                  // nullable [H][pitch], natural units
   int table_pitch, table_mid, n_dist;
-  float* out; float* lse;              // forward
+  int splits;                          // blocks that share the tiles one block would walk
+  float* out; float* lse;              // forward; splits > 1: partial results [splits][T][H][d],
+                                       // [splits][H][T] for the log-sum-exp merge
   const float* lse_in; const float* D; // backward; D [H][pitch_d]
   int64_t pitch_d;
   float *dq, *dk, *dv;
   float* dtable;                       // nullable [H][n_dist]
+  bool add_dq, add_dkdv;               // add into zeroed dq / dk and dv instead of storing
 };
+// Blocks along a walk of up to `walk` tiles: as many as keep two tiles each and
+// the launch within two blocks per SM.  (768 tokens, 8 heads over 2, d = 128, one
+// block per walk against six: forward 168 -> 67 us, backward 1201 -> 333 us.)
+inline int f32_splits(int64_t blocks, int walk, int sms) {
+  int64_t s = 2LL * sms / (blocks > 0 ? blocks : 1);
+  if (s > walk / 2) s = walk / 2;
+  return s < 1 ? 1 : (int)s;
+}
 cudaError_t launch_f32_fwd(const F32Args& a, int d, cudaStream_t st);
 cudaError_t launch_f32_bwd(const F32Args& a, int d, cudaStream_t st);
 

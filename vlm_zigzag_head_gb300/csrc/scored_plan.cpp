@@ -36,7 +36,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   if (cu[0] != 0) return "cu_seqlens[0] must be 0";
   if (n_dist < 0 || n_dist > kMaxDist) return "n_dist must be in [0, 65536]";
   if (n_dist > 0 && !buckets) return "buckets is NULL";
-  int64_t fwd = 0, bwd = 0, tiles = 0;
+  int64_t fwd = 0, bwd = 0, tiles = 0, walk = 0;
   for (int i = 0; i < n_seqs; ++i) {
     const int64_t len = (int64_t)cu[i + 1] - cu[i];
     if (len < 0) {
@@ -53,6 +53,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
       bwd += cdiv(rows, kBwdTileK);
     });
     tiles += cdiv(len, kTile32);
+    walk = std::max(walk, cdiv(len, kTile32));
   }
   int nb = 0;
   for (int i = 0; i < n_dist; ++i) {
@@ -65,12 +66,14 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   p.T = cu[n_seqs];
   p.H = H;
   p.n_seqs = n_seqs;
+  p.n_sms = sms;
   p.bidirectional = bidirectional ? 1 : 0;
   p.n_dist = n_dist;
   p.n_buckets = nb;
   p.n_fwd = (int32_t)fwd;
   p.n_bwd = (int32_t)bwd;
   p.n_tiles = (int32_t)tiles;
+  p.max_walk = (int32_t)walk;
   p.n_units = (int32_t)(fwd * H);
   p.grid = std::min<int32_t>(p.n_units, sms);
   p.item_major = item_major(p.n_units, sms) ? 1 : 0;

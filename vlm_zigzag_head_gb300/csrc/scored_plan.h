@@ -36,8 +36,10 @@ struct ScorePlanHeader {
   int32_t T, H, n_seqs, bidirectional;
   int32_t n_dist, n_buckets;       // 0: no table
   int32_t n_fwd, n_bwd, n_tiles;
+  int32_t max_walk;                // tiles of the longest sample (fp32 kernels)
   int32_t n_units, grid;           // forward: units and persistent CTAs
   int32_t item_major;              // the forward's unit order
+  int32_t n_sms;
   uint64_t fwd, bwd, runs, units, buckets, tiles, total;
 };
 static_assert(sizeof(ScorePlanHeader) <= 256, "plan header");
