@@ -432,14 +432,16 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  * a NaN or infinity in a key or value row may reach every row of the 128-row
  * tiles that hold it.
  *
- *   q, out, dout [T][H][d], k, v [T][H_kv][d], lse [H][T], dq, dk, dv fp32: as
+ *   q, out, dout [T][H][d], k, v [T][H_kv][d], lse [H][T], dq, dk, dv: as
  *                cp_attn_fwd_gqa / cp_attn_bwd_gqa, with T and H those of the plan
+ *   grad_dtype   of dq, dk, dv: CP_F32, or CP_BF16 with bf16 inputs (summed in
+ *                fp32 in the workspace, rounded once)
  *   dt           CP_BF16: tensor cores (f16 operands above softmax_scale 0.25, as
  *                cp_attn_fwd); CP_F32: CUDA cores, fp32 throughout
  *   score        slopes: NULL or device [H] fp32.  rel_bias: NULL or device, H x
  *                n_buckets, any strides (in elements).  softcap: 0 or in
  *                [1e-3, 1e4].  slopes and rel_bias exclude one another.
- *   dbias        NULL or [H][n_buckets] fp32 contiguous: gradient of rel_bias
+ *   dbias        NULL or [H][n_buckets] contiguous, dbias_dtype: gradient of rel_bias
  *   workspace    >= cp_attn_scored_{fwd,bwd}_workspace_size bytes, 256-byte
  *                aligned, of this call's own while it runs; its status word is
  *                read by cp_workspace_status
@@ -460,7 +462,7 @@ typedef struct {
 size_t cp_attn_scored_fwd_workspace_size(const void* plan_h, cp_dtype_t dt, int H_kv, int d,
                                          float softmax_scale);
 size_t cp_attn_scored_bwd_workspace_size(const void* plan_h, cp_dtype_t dt, int H_kv, int d,
-                                         float softmax_scale);
+                                         float softmax_scale, cp_dtype_t grad_dtype);
 cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const void* q,
                                const void* k, const void* v, cp_dtype_t dt, int T, int H, int H_kv,
                                int d, const cp_score_t* score, float softmax_scale, void* out,
@@ -470,8 +472,9 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
                                const void* k, const void* v, const void* out, const void* out_lo,
                                const float* lse, const void* dout, cp_dtype_t dt, int T, int H,
                                int H_kv, int d, const cp_score_t* score, float softmax_scale,
-                               float* dq, float* dk, float* dv, float* dbias, void* workspace,
-                               size_t ws_bytes, void* stream);
+                               void* dq, void* dk, void* dv, cp_dtype_t grad_dtype, void* dbias,
+                               cp_dtype_t dbias_dtype, void* workspace, size_t ws_bytes,
+                               void* stream);
 
 /*
  * cp_workspace_status -- synchronise `stream` and report whether a kernel of

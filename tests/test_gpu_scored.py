@@ -150,6 +150,26 @@ def test_bias_strides_and_types():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv", [(4, 1), (3, 1), (2, 2)])
+def test_bf16_gradients_are_the_rounded_fp32_ones(H, Hkv):
+    """Shared groups (summed by atomics: up to the order of fp32 sums) and whole ones."""
+    from vlm_zigzag_head_gb300 import CpError, ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    q, k, v, dout = (x.to(DEV) for x in _inputs(333, H, Hkv, 64, "bf16", 3))
+    plan = ScorePlan([0, 200, 333], H, rel_buckets=[0, 1, 2], device=DEV)
+    bias = torch.randn(H, 3, device=DEV).to(torch.bfloat16)
+    out, lse, lo = cp_attn_scored_fwd(q, k, v, plan, R64, rel_bias=bias, residual=True)
+    a = cp_attn_scored_bwd(q, k, v, out, lse, dout, plan, R64, rel_bias=bias, out_lo=lo)
+    b = cp_attn_scored_bwd(q, k, v, out, lse, dout, plan, R64, rel_bias=bias, out_lo=lo, grad_dtype=torch.bfloat16)
+    for x, y in zip(a, b):
+        assert x.dtype == torch.float32 and y.dtype == torch.bfloat16
+        # half a step of bf16, and the sums' own variation (1e-5 of the largest)
+        assert torch.all((x - y.float()).abs() <= 2.0 ** -8 * x.abs() + 1e-5 * x.abs().max())
+    with pytest.raises(CpError):
+        cp_attn_scored_bwd(q.float(), k.float(), v.float(), out.float(), lse, dout.float(), plan, R64,
+                           grad_dtype=torch.bfloat16)
+
+
+@pytest.mark.gpu
 def test_plain_scores_equal_the_unmodified_attention():
     """Without cap and bias the causal result is cp_attn_fwd's, up to its summation order."""
     from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_bwd, cp_attn_fwd, cp_attn_scored_bwd, cp_attn_scored_fwd

@@ -56,7 +56,7 @@ A, ODD = 4096, 4097
 
 
 def _call(direction="fwd", plan=None, plan_d=A, dt=1, T=5, H=2, Hkv=1, d=64, scale=0.125, ws=A, ws_bytes=1 << 20,
-          out_lo=None, dbias=None, score=None, null_score=False, swap=None, **over):
+          out_lo=None, dbias=None, score=None, null_score=False, swap=None, grad_dt=0, dbias_dt=0, **over):
     """Status of a call on stand-in pointers; a refused call never touches them."""
     plan = build_plan([0, 5], 2, 0, False, [0, 1, 1, 2], 152)[0] if plan is None else plan
     s = B.ScoreDesc()
@@ -72,8 +72,8 @@ def _call(direction="fwd", plan=None, plan_d=A, dt=1, T=5, H=2, Hkv=1, d=64, sca
     host = _host(plan) if not isinstance(plan, int) else ctypes.c_void_p(plan)
     if direction == "fwd":
         return B.lib().cp_attn_scored_fwd(host, plan_d, *vp[:3], *shape, *vp[3:], out_lo, ws, ws_bytes, None)
-    return B.lib().cp_attn_scored_bwd(host, plan_d, *vp[:4], out_lo, *vp[4:6], *shape, *vp[6:], dbias, ws, ws_bytes,
-                                      None)
+    return B.lib().cp_attn_scored_bwd(host, plan_d, *vp[:4], out_lo, *vp[4:6], *shape, *vp[6:], grad_dt, dbias, dbias_dt,
+                                      ws, ws_bytes, None)
 
 
 BAD = [(dict(plan=bytearray(256)), 1), (dict(null_score=True), 1), (dict(dt=5), 3), (dict(T=6), 2), (dict(H=4), 2),
@@ -99,6 +99,12 @@ def test_bad_pointers(cplib):
             assert _call(direction, swap=(i, A + 8)) == 4
     assert _call("bwd", dbias=A) == 1                       # no rel_bias to differentiate
     assert _call("bwd", rel_bias=A, dbias=ODD) == 4
+    assert _call("bwd", grad_dt=7) == 3
+    assert _call("bwd", dt=0, grad_dt=1) == 3               # bf16 gradients of fp32 inputs
+    assert _call("bwd", rel_bias=A, dbias=A, dbias_dt=5) == 3
+    need = B.lib().cp_attn_scored_bwd_workspace_size(_host(build_plan([0, 5], 2, 0, False, [0, 1, 1, 2], 152)[0]),
+                                                     1, 1, 64, 0.125, 1)
+    assert _call("bwd", grad_dt=1, ws_bytes=need - 1) == 5
     plain = build_plan([0, 5], 2, 0, False, None, 152)[0]
     assert _call("fwd", plan=plain, rel_bias=A) == 1        # a plan without buckets
     assert _call("fwd", plan=0) == 1

@@ -108,11 +108,11 @@ SIGNATURES = {
     "cp_score_plan_build": (ctypes.c_int, _PLAN + [c_vp, ctypes.c_size_t]),
     "cp_score_plan_pairs": (ctypes.c_int, [c_vp, c_i64p, c_i64p, c_i64p]),
     "cp_attn_scored_fwd_workspace_size": _SCORED_WS,
-    "cp_attn_scored_bwd_workspace_size": _SCORED_WS,
+    "cp_attn_scored_bwd_workspace_size": (ctypes.c_size_t, _SCORED_WS[1] + [ctypes.c_int]),
     "cp_attn_scored_fwd": (ctypes.c_int, [c_vp] * 5 + _SCORED_SHAPE + [c_vp] * 4 +
                            [ctypes.c_size_t, c_vp]),
-    "cp_attn_scored_bwd": (ctypes.c_int, [c_vp] * 9 + _SCORED_SHAPE + [c_vp] * 5 +
-                           [ctypes.c_size_t, c_vp]),
+    "cp_attn_scored_bwd": (ctypes.c_int, [c_vp] * 9 + _SCORED_SHAPE + [c_vp] * 3 +
+                           [ctypes.c_int, c_vp, ctypes.c_int, c_vp, ctypes.c_size_t, c_vp]),
     "cp_workspace_status": (ctypes.c_int, [c_vp, c_vp]),
     "cp_plan_pairs": (ctypes.c_int, [c_i32p, ctypes.c_int, ctypes.c_int, ctypes.c_int, c_i64p,
                                      c_i64p, c_i64p, c_i64p]),

@@ -144,7 +144,8 @@ class CPAttentionScored(torch.autograd.Function):
         q, k, v, rel_bias, slopes, out, lse, out_lo = ctx.saved_tensors
         plan, scale, softcap = ctx.meta
         got = cp_attn_scored_bwd(q, k, v, out, lse, _dense(dout.to(q.dtype)), plan, scale,
-                                 softcap, slopes, rel_bias, out_lo=out_lo)
+                                 softcap, slopes, rel_bias, out_lo=out_lo, grad_dtype=q.dtype)
+        # (a bias of another dtype than fp32 q, k, v gets its fp32 gradient rounded here)
         grads = [g.to(x.dtype) if need else None
                  for g, x, need in zip(got, (q, k, v, rel_bias), ctx.needs_input_grad)]
         return (*grads, *([None] * (8 - len(grads))))

@@ -33,11 +33,14 @@ const ScorePlanHeader* header(const void* plan_h) {
   return h->magic == kScorePlanMagic ? h : nullptr;
 }
 
-// Offsets into the workspace of either direction.
+// Offsets into the workspace of either direction.  What has to start at zero
+// comes first, so that one memset clears it.
 struct Ws {
-  size_t status = 0, table = 0, scales = 0, v16 = 0;                   // forward
-  size_t part_out = 0, part_lse = 0;                                   // forward, fp32
-  size_t lse2 = 0, D = 0, q16 = 0, k16 = 0, dtable = 0;                // backward
+  size_t status = 0, scales = 0;
+  size_t dtable = 0, dq = 0, dk = 0, dv = 0;   // backward (dq, dk, dv: bf16 results)
+  size_t table = 0;
+  size_t v16 = 0, part_out = 0, part_lse = 0;  // forward
+  size_t lse2 = 0, D = 0, q16 = 0, k16 = 0;    // backward
   size_t total = 0;
 };
 
@@ -49,33 +52,33 @@ int f32_fwd_splits(const ScorePlanHeader& h) {
   return f32_splits((int64_t)h.n_tiles * h.H, h.max_walk, h.n_sms);
 }
 
-Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward) {
+Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward,
+          bool bf16_grads) {
   Ws w;
   const bool f16 = dt == CP_BF16 && uses_f16_operands(scale);
   const size_t T = h.T;
   size_t o = kStatusBytes;
-  w.table = o;
-  if (h.n_dist > 0) o = up256(o + (size_t)h.H * table_pitch(h.n_dist) * sizeof(float));
-  w.scales = o;
-  if (f16) o = up256(o + sizeof(OpScales));
+  auto take = [&](size_t* at, bool need, size_t bytes) {
+    *at = o;
+    if (need) o = up256(o + bytes);
+  };
+  take(&w.scales, f16, sizeof(OpScales));
+  take(&w.dtable, backward && h.n_dist > 0, (size_t)h.H * h.n_dist * sizeof(float));
+  take(&w.dq, backward && bf16_grads, T * h.H * d * sizeof(float));
+  take(&w.dk, backward && bf16_grads, T * Hkv * d * sizeof(float));
+  take(&w.dv, backward && bf16_grads, T * Hkv * d * sizeof(float));
+  take(&w.table, h.n_dist > 0, (size_t)h.H * table_pitch(h.n_dist) * sizeof(float));
   if (!backward) {
-    w.v16 = o;
-    if (f16) o = up256(o + T * Hkv * d * 2);
     const size_t parts = dt == CP_F32 ? f32_fwd_splits(h) : 1;
-    w.part_out = o;
-    if (parts > 1) o = up256(o + parts * T * h.H * d * sizeof(float));
-    w.part_lse = o;
-    if (parts > 1) o = up256(o + parts * T * h.H * sizeof(float));
+    take(&w.v16, f16, T * Hkv * d * 2);
+    take(&w.part_out, parts > 1, parts * T * h.H * d * sizeof(float));
+    take(&w.part_lse, parts > 1, parts * T * h.H * sizeof(float));
   } else {
-    w.lse2 = o;
-    w.D = o + (size_t)ld_pitch(T) * h.H * sizeof(float);   // plane 1 directly after plane 0
-    o = up256(o + 2 * (size_t)ld_pitch(T) * h.H * sizeof(float));
-    w.q16 = o;
-    if (f16) o = up256(o + T * h.H * d * 2);
-    w.k16 = o;
-    if (f16) o = up256(o + T * Hkv * d * 2);
-    w.dtable = o;
-    if (h.n_dist > 0) o = up256(o + (size_t)h.H * h.n_dist * sizeof(float));
+    const size_t plane = (size_t)ld_pitch(T) * h.H * sizeof(float);
+    take(&w.lse2, true, 2 * plane);
+    w.D = w.lse2 + plane;   // plane 1 directly after plane 0
+    take(&w.q16, f16, T * h.H * d * 2);
+    take(&w.k16, f16, T * Hkv * d * 2);
   }
   w.total = o;
   return w;
@@ -91,7 +94,8 @@ struct Call {
 // Checks everything that does not need a GPU.
 cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptrs, int n_ptrs,
                   cp_dtype_t dt, int T, int H, int Hkv, int d, const cp_score_t* sc, float scale,
-                  const void* out_lo, const void* ws, size_t ws_bytes, bool backward, Call* c) {
+                  const void* out_lo, const void* ws, size_t ws_bytes, bool backward,
+                  bool bf16_grads, Call* c) {
   c->h = header(plan_h);
   if (!c->h) return entry_fail(CP_ERR_INVALID_ARG, "plan_h is not a score plan");
   if (!sc) return entry_fail(CP_ERR_INVALID_ARG, "score is NULL");
@@ -126,7 +130,7 @@ cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptr
   c->bias = sc->slopes ? SCORE_SLOPES : sc->rel_bias ? SCORE_TABLE : SCORE_PLAIN;
   c->bf16 = dt == CP_BF16;
   c->f16 = c->bf16 && uses_f16_operands(scale);
-  c->ws = layout(*c->h, dt, Hkv, d, scale, backward);
+  c->ws = layout(*c->h, dt, Hkv, d, scale, backward, bf16_grads);
   if (out_lo && !c->bf16) return entry_fail(CP_ERR_DTYPE, "out_lo is for bf16 outputs only");
   if (T == 0) return CP_OK;
   if (!plan_d) return entry_fail(CP_ERR_INVALID_ARG, "plan_d is NULL");
@@ -266,14 +270,14 @@ size_t cp_attn_scored_fwd_workspace_size(const void* plan_h, cp_dtype_t dt, int 
                                          float scale) {
   const ScorePlanHeader* h = header(plan_h);
   if (!h || Hkv < 1 || d < 1) return 0;
-  return layout(*h, dt, Hkv, d, scale, false).total;
+  return layout(*h, dt, Hkv, d, scale, false, false).total;
 }
 
 size_t cp_attn_scored_bwd_workspace_size(const void* plan_h, cp_dtype_t dt, int Hkv, int d,
-                                         float scale) {
+                                         float scale, cp_dtype_t grad_dt) {
   const ScorePlanHeader* h = header(plan_h);
   if (!h || Hkv < 1 || d < 1) return 0;
-  return layout(*h, dt, Hkv, d, scale, true).total;
+  return layout(*h, dt, Hkv, d, scale, true, grad_dt == CP_BF16).total;
 }
 
 cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const void* q,
@@ -284,7 +288,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   const void* ptrs[5] = {q, k, v, out, lse};
   Call c;
   cp_status_t e = check(plan_h, plan_d, ptrs, 5, dt, T, H, Hkv, d, score, scale, out_lo, ws,
-                        ws_bytes, false, &c);
+                        ws_bytes, false, false, &c);
   if (e != CP_OK) return e;
   if (T == 0) return CP_OK;
   int sms = 0;
@@ -292,7 +296,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* w = static_cast<char*>(ws);
   const char* plan = static_cast<const char*>(plan_d);
-  ENTRY_CUDA(cudaMemsetAsync(w, 0, kStatusBytes, st), "clear status");
+  ENTRY_CUDA(cudaMemsetAsync(w, 0, c.ws.dtable, st), "clear status and operand scales");
   ScoreArgs s;
   if ((e = prepare_scores(c, score, plan, w, &s, st)) != CP_OK) return e;
   if (!c.bf16) {
@@ -317,7 +321,6 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
     const int64_t n = (int64_t)T * Hkv * d;
     void* v16 = w + c.ws.v16;
     ProfileScope prof(1, st, 2);
-    ENTRY_CUDA(cudaMemsetAsync(sc, 0, sizeof(OpScales), st), "clear operand scales");
     ENTRY_CUDA(launch_absmax_bf16(&v, &n, 1, sc, st), "max |V|");
     ENTRY_CUDA(launch_to_f16_scaled(&v, &v16, &n, 1, sc, false, d, st), "f16 copy of V");
     vsrc = v16;
@@ -361,22 +364,28 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
 cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const void* q,
                                const void* k, const void* v, const void* out, const void* out_lo,
                                const float* lse, const void* dout, cp_dtype_t dt, int T, int H,
-                               int Hkv, int d, const cp_score_t* score, float scale, float* dq,
-                               float* dk, float* dv, float* dbias, void* ws, size_t ws_bytes,
-                               void* stream) {
+                               int Hkv, int d, const cp_score_t* score, float scale, void* dq_out,
+                               void* dk_out, void* dv_out, cp_dtype_t grad_dt, void* dbias,
+                               cp_dtype_t dbias_dt, void* ws, size_t ws_bytes, void* stream) {
   ENTRY_TRY
-  const void* ptrs[9] = {q, k, v, out, lse, dout, dq, dk, dv};
+  const void* ptrs[9] = {q, k, v, out, lse, dout, dq_out, dk_out, dv_out};
   Call c;
   cp_status_t e = check(plan_h, plan_d, ptrs, 9, dt, T, H, Hkv, d, score, scale, out_lo, ws,
-                        ws_bytes, true, &c);
+                        ws_bytes, true, grad_dt == CP_BF16, &c);
   if (e != CP_OK) return e;
+  if (grad_dt != CP_F32 && (grad_dt != CP_BF16 || dt != CP_BF16))
+    return entry_fail(CP_ERR_DTYPE, "grad_dtype must be CP_F32, or CP_BF16 for bf16 inputs");
+  if (dbias && dbias_dt != CP_F32 && dbias_dt != CP_BF16)
+    return entry_fail(CP_ERR_DTYPE, "dbias_dtype must be CP_F32 or CP_BF16");
   if (dbias && c.bias != SCORE_TABLE)
     return entry_fail(CP_ERR_INVALID_ARG, "dbias without rel_bias");
-  if (!aligned_to(dbias, 4)) return entry_fail(CP_ERR_ALIGNMENT, "dbias alignment");
+  if (!aligned_to(dbias, dbias_dt == CP_BF16 ? 2 : 4))
+    return entry_fail(CP_ERR_ALIGNMENT, "dbias alignment");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (T == 0) {
     if (dbias)
-      ENTRY_CUDA(cudaMemsetAsync(dbias, 0, (size_t)H * score->n_buckets * sizeof(float), st),
+      ENTRY_CUDA(cudaMemsetAsync(dbias, 0,
+                                 (size_t)H * score->n_buckets * (dbias_dt == CP_BF16 ? 2 : 4), st),
                  "clear dbias");
     return CP_OK;
   }
@@ -384,14 +393,31 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   if ((e = check_gpu(c.bf16, &sms)) != CP_OK) return e;
   char* w = static_cast<char*>(ws);
   const char* plan = static_cast<const char*>(plan_d);
-  ENTRY_CUDA(cudaMemsetAsync(w, 0, kStatusBytes, st), "clear status");
+  // bf16 gradients are summed in fp32 in the workspace and rounded at the end
+  const bool bf16_grads = grad_dt == CP_BF16;
+  float* dq = static_cast<float*>(dq_out);
+  float* dk = static_cast<float*>(dk_out);
+  float* dv = static_cast<float*>(dv_out);
+  if (bf16_grads) {
+    dq = reinterpret_cast<float*>(w + c.ws.dq);
+    dk = reinterpret_cast<float*>(w + c.ws.dk);
+    dv = reinterpret_cast<float*>(w + c.ws.dv);
+  }
+  const int kv_split = c.bf16 ? bwd_kv_split(c.h->n_bwd, H, Hkv, sms) : 1;
+  const int f32_split = c.bf16 ? 1 : f32_splits((int64_t)c.h->n_tiles * H, c.h->max_walk, sms);
+  const bool add_dq = c.bf16 || f32_split > 1;
+  const bool add_dkdv = c.bf16 ? kv_split > 1 : f32_split > 1 || H > Hkv;
+  const size_t zero = !bf16_grads ? c.ws.dq : add_dkdv ? c.ws.table : c.ws.dk;
+  ENTRY_CUDA(cudaMemsetAsync(w, 0, zero, st), "clear status and sums");
+  if (!bf16_grads && add_dq)
+    ENTRY_CUDA(cudaMemsetAsync(dq, 0, (size_t)T * H * d * sizeof(float), st), "clear dq");
+  if (!bf16_grads && add_dkdv) {
+    ENTRY_CUDA(cudaMemsetAsync(dk, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dk");
+    ENTRY_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");
+  }
   ScoreArgs s;
   if ((e = prepare_scores(c, score, plan, w, &s, st)) != CP_OK) return e;
-  if (c.bias == SCORE_TABLE) {
-    s.dtable = reinterpret_cast<float*>(w + c.ws.dtable);
-    ENTRY_CUDA(cudaMemsetAsync(s.dtable, 0, (size_t)H * s.n_dist * sizeof(float), st),
-               "clear distance gradients");
-  }
+  if (c.bias == SCORE_TABLE) s.dtable = reinterpret_cast<float*>(w + c.ws.dtable);
   float* Dd = reinterpret_cast<float*>(w + c.ws.D);
   float* lse2 = reinterpret_cast<float*>(w + c.ws.lse2);
   const int64_t pitch = ld_pitch(T);
@@ -407,7 +433,6 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
       void* dsts[2] = {q16, k16};
       const int64_t n[4] = {(int64_t)T * H * d, (int64_t)T * Hkv * d, (int64_t)T * Hkv * d,
                             (int64_t)T * H * d};
-      ENTRY_CUDA(cudaMemsetAsync(sc, 0, sizeof(OpScales), st), "clear operand scales");
       ENTRY_CUDA(launch_absmax_bf16(srcs, n, 4, sc, st), "max |Q|, |K|, |V|, |dO|");
       ENTRY_CUDA(launch_to_f16_scaled(srcs, dsts, n, 2, sc, true, d, st), "f16 copies of Q, K");
     }
@@ -425,24 +450,12 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.dk = dk;
     a.dv = dv;
     a.dtable = s.dtable;
-    a.splits = f32_splits((int64_t)a.n_tiles * H, c.h->max_walk, sms);
-    a.add_dq = a.splits > 1;
-    a.add_dkdv = a.splits > 1 || H > Hkv;
-    if (a.add_dq)
-      ENTRY_CUDA(cudaMemsetAsync(dq, 0, (size_t)T * H * d * sizeof(float), st), "clear dq");
-    if (a.add_dkdv) {
-      ENTRY_CUDA(cudaMemsetAsync(dk, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dk");
-      ENTRY_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");
-    }
+    a.splits = f32_split;
+    a.add_dq = add_dq;
+    a.add_dkdv = add_dkdv;
     ProfileScope prof(7, st, 2);
     ENTRY_CUDA(launch_f32_bwd(a, d, st), "fp32 scored backward");
   } else {
-    ENTRY_CUDA(cudaMemsetAsync(dq, 0, (size_t)T * H * d * sizeof(float), st), "clear dq");
-    const int kv_split = bwd_kv_split(c.h->n_bwd, H, Hkv, sms);
-    if (kv_split > 1) {
-      ENTRY_CUDA(cudaMemsetAsync(dk, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dk");
-      ENTRY_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");
-    }
     TcBwdArgs a{};
     const char* terr = nullptr;
     if (!make_tmap_thd(&a.tm_q, c.f16 ? q16 : q, T, H, d, 128, &terr, c.f16) ||
@@ -474,9 +487,15 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     ProfileScope prof(4, st);
     ENTRY_CUDA(launch_tc_bwd_scored(a, c.bias, st), "tensor-core scored backward");
   }
+  if (bf16_grads) {
+    const float* const src[3] = {dq, dk, dv};
+    void* const dst[3] = {dq_out, dk_out, dv_out};
+    const int64_t n[3] = {(int64_t)T * H * d, (int64_t)T * Hkv * d, (int64_t)T * Hkv * d};
+    ENTRY_CUDA(launch_cast_bf16(src, dst, n, sms, st), "bf16 gradients");
+  }
   if (dbias)
     ENTRY_CUDA(launch_reduce_dbias(s.dtable, reinterpret_cast<const int32_t*>(plan + c.h->buckets),
-                                   s.n_dist, score->n_buckets, H, dbias, st),
+                                   s.n_dist, score->n_buckets, H, dbias, dbias_dt == CP_BF16, st),
                "bias gradient by bucket");
   return CP_OK;
   ENTRY_CATCH

@@ -27,14 +27,15 @@ template <int D>
 constexpr int tile_floats() { return D * kPad; }
 constexpr int kPFloats = kT * kPad;
 
-// dst[e][row] = src[row][e] for row < rows, 0 beyond.  Neighbouring threads take
-// neighbouring rows: conflict-free stores; the two halves of a 32-byte sector
-// are read close together.
+// dst[e][row] = src[row][e] for row < rows, 0 beyond.  A warp takes 8 rows x 64
+// bytes at a time: half as many lines per load as one row per lane, at the price of
+// two-way conflicts among its stores.
 template <int D>
 __device__ __forceinline__ void stage(float* dst, const float* src, int rows, int64_t stride) {
-  const int row = threadIdx.x & (kT - 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = warp * 8 + (lane >> 2);
 #pragma unroll
-  for (int e = (threadIdx.x / kT) * 4; e < D; e += kThreads / kT * 4) {
+  for (int e = (lane & 3) * 4; e < D; e += 16) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) v = *reinterpret_cast<const float4*>(src + row * stride + e);
     dst[e * kPad + row] = v.x;
@@ -43,6 +44,7 @@ __device__ __forceinline__ void stage(float* dst, const float* src, int rows, in
     dst[(e + 3) * kPad + row] = v.w;
   }
 }
+static_assert(kThreads == 8 * 32 && kT == 64, "eight warps stage eight rows each");
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -310,43 +312,41 @@ __global__ void __launch_bounds__(kThreads) f32_dkdv_kernel(const F32Args a) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) dk[i][j] = dv[i][j] = 0.f;
-  {
-    // queries that see this tile: its own rows on, or all for a both-way prefix
-    const int start = u0 < tl.prefix ? 0 : u0;
-    int first, last;
-    my_tiles(a, (tl.seq_len - start + kT - 1) / kT, first, last);
-    if (first >= last) return;
-    for (int t0 = start + first * kT; t0 < start + last * kT; t0 += kT) {
-      const int n = min(kT, tl.seq_len - t0);
-      __syncthreads();
-      stage<D>(Q, a.q + (tl.seq0 + t0) * qs + h * D, n, qs);
-      stage<D>(dO, a.dout + (tl.seq0 + t0) * qs + h * D, n, qs);
-      __syncthreads();
-      float c[4][4], g[4][4];        // [key][query]
-      outer<D>(K, Q, ty, tx, c);
-      outer<D>(V, dO, ty, tx, g);
+  // queries that see this tile: its own rows on, or all for a both-way prefix
+  const int start = u0 < tl.prefix ? 0 : u0;
+  int first, last;
+  my_tiles(a, (tl.seq_len - start + kT - 1) / kT, first, last);
+  if (first >= last) return;
+  for (int t0 = start + first * kT; t0 < start + last * kT; t0 += kT) {
+    const int n = min(kT, tl.seq_len - t0);
+    __syncthreads();
+    stage<D>(Q, a.q + (tl.seq0 + t0) * qs + h * D, n, qs);
+    stage<D>(dO, a.dout + (tl.seq0 + t0) * qs + h * D, n, qs);
+    __syncthreads();
+    float c[4][4], g[4][4];        // [key][query]
+    outer<D>(K, Q, ty, tx, c);
+    outer<D>(V, dO, ty, tx, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 4 * tx + j, pos = t0 + r;
-        const float lse = r < n ? a.lse_in[h * a.T + tl.seq0 + pos] : -INFINITY;
-        const float Dr = r < n ? a.D[h * a.pitch_d + tl.seq0 + pos] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * tx + j, pos = t0 + r;
+      const float lse = r < n ? a.lse_in[h * a.T + tl.seq0 + pos] : -INFINITY;
+      const float Dr = r < n ? a.D[h * a.pitch_d + tl.seq0 + pos] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = u0 + 4 * ty + i;
-          float t;
-          const float x = score(a, h, c[i][j], pos, u, tl.prefix, t);
-          const bool live = lse != -INFINITY && 4 * ty + i < tl.len && x != -INFINITY;
-          const float p = live ? expf(x - lse) : 0.f;
-          c[i][j] = p;
-          g[i][j] = live ? p * (g[i][j] - Dr) * (1.f - t * t) * a.scale : 0.f;
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + 4 * ty + i;
+        float t;
+        const float x = score(a, h, c[i][j], pos, u, tl.prefix, t);
+        const bool live = lse != -INFINITY && 4 * ty + i < tl.len && x != -INFINITY;
+        const float p = live ? expf(x - lse) : 0.f;
+        c[i][j] = p;
+        g[i][j] = live ? p * (g[i][j] - Dr) * (1.f - t * t) * a.scale : 0.f;
       }
-      put(P, ty, tx, c);
-      put(S, ty, tx, g);
-      __syncthreads();
-      accumulate<D>(P, dO, ty, tx, dv);
-      accumulate<D>(S, Q, ty, tx, dk);
     }
+    put(P, ty, tx, c);
+    put(S, ty, tx, g);
+    __syncthreads();
+    accumulate<D>(P, dO, ty, tx, dv);
+    accumulate<D>(S, Q, ty, tx, dk);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -8,7 +8,7 @@
 
 namespace cpattn {
 
-// ---- learned bias by bucket <-> table by distance (scored_bias.cu) --------------
+// ---- learned bias by bucket <-> table by distance (scored_aux.cu) --------------
 // table[h][mid + s] = mul * bias[h][bucket[min(|s|, n_dist - 1)]] for |s| <= mid;
 // entries at or below -1e37 become -inf (the key is hidden).
 cudaError_t launch_expand_bias(const void* bias, bool bf16, int64_t stride_h, int64_t stride_b,
@@ -16,7 +16,10 @@ cudaError_t launch_expand_bias(const void* bias, bool bf16, int64_t stride_h, in
                                int mid, int pitch, cudaStream_t st);
 // dbias[h][b] = sum of dtable[h][t] over the distances of bucket b, in order.
 cudaError_t launch_reduce_dbias(const float* dtable, const int32_t* buckets, int n_dist,
-                                int n_buckets, int H, float* dbias, cudaStream_t st);
+                                int n_buckets, int H, void* dbias, bool bf16, cudaStream_t st);
+// dst[i] = bf16(src[i]) for three tensors of n[i] elements (multiples of 4).
+cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3],
+                             const int64_t (&n)[3], int sms, cudaStream_t st);
 
 // ---- fp32 inputs: CUDA cores (attn_f32.cu) ---------------------------------------
 struct F32Args {

@@ -1,0 +1,99 @@
+// The small kernels around attention with modified scores: the learned bias laid
+// out by distance and its gradient summed back (a few KB a head: bound by the
+// launch), and the gradients' rounding to bf16 (one pass, bound by memory).
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+#include "scored.h"
+
+namespace cpattn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__global__ void __launch_bounds__(kThreads)
+    expand_bias_kernel(const void* bias, int bf16, int64_t sh, int64_t sb, const int32_t* buckets,
+                       int n_dist, float mul, float* table, int mid, int pitch) {
+  const int h = blockIdx.y;
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < pitch; i += gridDim.x * kThreads) {
+    const int s = i - mid;
+    const int64_t at = h * sh + buckets[min(s < 0 ? -s : s, n_dist - 1)] * sb;
+    const float b = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[at])
+                         : static_cast<const float*>(bias)[at];
+    table[(int64_t)h * pitch + i] = b <= -1e37f ? -INFINITY : b * mul;
+  }
+}
+
+// One block per head, one warp per bucket at a time; lanes take the distances
+// 32 apart and meet in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+    reduce_dbias_kernel(const float* dtable, const int32_t* buckets, int n_dist, int n_buckets,
+                        void* dbias, int bf16) {
+  const int h = blockIdx.x, lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < n_buckets; b += kThreads / 32) {
+    float v = 0.f;
+    for (int t = lane; t < n_dist; t += 32)
+      if (buckets[t] == b) v += dtable[(int64_t)h * n_dist + t];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane != 0) continue;
+    const int64_t at = (int64_t)h * n_buckets + b;
+    if (bf16) static_cast<__nv_bfloat16*>(dbias)[at] = __float2bfloat16_rn(v);
+    else static_cast<float*>(dbias)[at] = v;
+  }
+}
+
+struct Cast3 {
+  const float4* src[3];
+  uint2* dst[3];
+  int64_t n[3];   // groups of four elements
+};
+
+// Block row blockIdx.y: tensor; four elements per thread and step.
+__global__ void __launch_bounds__(kThreads) cast_bf16_kernel(const Cast3 c) {
+  const int t = blockIdx.y;
+  const float4* src = t == 0 ? c.src[0] : t == 1 ? c.src[1] : c.src[2];
+  uint2* dst = t == 0 ? c.dst[0] : t == 1 ? c.dst[1] : c.dst[2];
+  const int64_t n = t == 0 ? c.n[0] : t == 1 ? c.n[1] : c.n[2];
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * kThreads) {
+    const float4 v = src[i];
+    dst[i] = make_uint2(ptx::pack_bf16x2(v.x, v.y), ptx::pack_bf16x2(v.z, v.w));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3],
+                             const int64_t (&n)[3], int sms, cudaStream_t st) {
+  Cast3 c;
+  int64_t most = 0;
+  for (int i = 0; i < 3; ++i) {
+    c.src[i] = reinterpret_cast<const float4*>(src[i]);
+    c.dst[i] = static_cast<uint2*>(dst[i]);
+    c.n[i] = n[i] / 4;
+    most = c.n[i] > most ? c.n[i] : most;
+  }
+  const int64_t want = (most + 4 * kThreads - 1) / (4 * kThreads), cap = 8LL * sms;
+  const unsigned blocks = (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
+  cast_bf16_kernel<<<dim3(blocks, 3), kThreads, 0, st>>>(c);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_expand_bias(const void* bias, bool bf16, int64_t stride_h, int64_t stride_b,
+                               const int32_t* buckets, int n_dist, int H, float mul, float* table,
+                               int mid, int pitch, cudaStream_t st) {
+  expand_bias_kernel<<<dim3((pitch + kThreads - 1) / kThreads, H), kThreads, 0, st>>>(
+      bias, bf16 ? 1 : 0, stride_h, stride_b, buckets, n_dist, mul, table, mid, pitch);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_reduce_dbias(const float* dtable, const int32_t* buckets, int n_dist,
+                                int n_buckets, int H, void* dbias, bool bf16, cudaStream_t st) {
+  reduce_dbias_kernel<<<H, kThreads, 0, st>>>(dtable, buckets, n_dist, n_buckets, dbias,
+                                              bf16 ? 1 : 0);
+  return cudaGetLastError();
+}
+
+}  // namespace cpattn

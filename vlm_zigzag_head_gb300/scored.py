@@ -67,7 +67,7 @@ class ScorePlan:
             self._stream = torch.cuda.current_stream(device)
         self.device = device
         self._block = (ctypes.c_char * len(self.host)).from_buffer(self.host)
-        self._sizes = {}   # workspace bytes by direction, dtype, KV heads, head size and scale
+        self._sizes = {}   # workspace bytes by dtypes, KV heads, head size and scale
 
     def _use(self, stream):
         """The device copy, kept from reuse until ``stream`` is done with it."""
@@ -75,14 +75,15 @@ class ScorePlan:
             self.dev.record_stream(stream)
         return self.dev.data_ptr()
 
-    def _workspace_bytes(self, backward, dt, H_kv, d, scale):
-        key = (backward, dt, H_kv, d, scale)
-        if key not in self._sizes:
+    def _workspace_bytes(self, *shape):
+        """Of the forward (dtype, KV heads, head size, scale), or with the gradients'
+        dtype as a fifth of the backward."""
+        if shape not in self._sizes:
             L = _b.lib()
-            size = L.cp_attn_scored_bwd_workspace_size if backward else \
+            size = L.cp_attn_scored_bwd_workspace_size if len(shape) == 5 else \
                 L.cp_attn_scored_fwd_workspace_size
-            self._sizes[key] = size(self._block, dt, H_kv, d, scale)
-        return self._sizes[key]
+            self._sizes[shape] = size(self._block, *shape)
+        return self._sizes[shape]
 
 
 def build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix, rel_buckets, n_sms):
@@ -178,7 +179,7 @@ def cp_attn_scored_fwd(q, k, v, plan: ScorePlan, softmax_scale: float, softcap: 
     s = _scores(q, plan, softcap, slopes, rel_bias)
     scale = float(softmax_scale)
     with torch.cuda.device(q.device):
-        nbytes = plan._workspace_bytes(False, dt, k.shape[1], d, scale)
+        nbytes = plan._workspace_bytes(dt, k.shape[1], d, scale)
         ws, ptr, size = _space(workspace, nbytes, q.device)
         stream = torch.cuda.current_stream()
         _b.check(_b.lib().cp_attn_scored_fwd(
@@ -190,9 +191,11 @@ def cp_attn_scored_fwd(q, k, v, plan: ScorePlan, softmax_scale: float, softcap: 
 
 def cp_attn_scored_bwd(q, k, v, out, lse, dout, plan: ScorePlan, softmax_scale: float,
                        softcap: float = 0.0, slopes=None, rel_bias=None,
-                       workspace: Optional[Workspace] = None, grads=None, out_lo=None):
-    """Gradient of :func:`cp_attn_scored_fwd`: ``(dq, dk, dv)`` fp32, and with
-    ``rel_bias`` a fourth, ``dbias [H, n_buckets]`` fp32.  ``grads`` may supply dq, dk, dv."""
+                       workspace: Optional[Workspace] = None, grads=None, out_lo=None,
+                       grad_dtype=torch.float32):
+    """Gradient of :func:`cp_attn_scored_fwd`: ``(dq, dk, dv)``, and with ``rel_bias`` a
+    fourth, ``dbias [H, n_buckets]``.  ``grad_dtype``: fp32, or bf16 for bf16 inputs
+    (dbias is then in rel_bias's dtype).  ``grads`` may supply dq, dk, dv."""
     _need_cuda(q, k, v, out, lse, dout, out_lo, *(grads or ()))
     _check(q, k, v, plan)
     T, H, d = q.shape
@@ -202,21 +205,24 @@ def cp_attn_scored_bwd(q, k, v, out, lse, dout, plan: ScorePlan, softmax_scale: 
             _like(t, q.shape, q.dtype, q.device, name)
     _like(lse, (H, T), torch.float32, q.device, "lse")
     dq, dk, dv = grads or (None, None, None)
-    dq = _like(dq, q.shape, torch.float32, q.device, "dq")
-    dk = _like(dk, k.shape, torch.float32, q.device, "dk")
-    dv = _like(dv, k.shape, torch.float32, q.device, "dv")
+    dq = _like(dq, q.shape, grad_dtype, q.device, "dq")
+    dk = _like(dk, k.shape, grad_dtype, q.device, "dk")
+    dv = _like(dv, k.shape, grad_dtype, q.device, "dv")
+    gdt = _dt(dq)
     s = _scores(q, plan, softcap, slopes, rel_bias)
-    dbias = None
+    dbias, bdt = None, gdt
     if rel_bias is not None:
-        dbias = torch.empty(rel_bias.shape, dtype=torch.float32, device=q.device)
+        dbias = torch.empty(rel_bias.shape, device=q.device, dtype=torch.float32
+                            if grad_dtype == torch.float32 else rel_bias.dtype)
+        bdt = _dt(dbias)
     scale = float(softmax_scale)
     with torch.cuda.device(q.device):
-        nbytes = plan._workspace_bytes(True, dt, k.shape[1], d, scale)
+        nbytes = plan._workspace_bytes(dt, k.shape[1], d, scale, gdt)
         ws, ptr, size = _space(workspace, nbytes, q.device)
         stream = torch.cuda.current_stream()
         _b.check(_b.lib().cp_attn_scored_bwd(
             plan._block, plan._use(stream), q.data_ptr(), k.data_ptr(), v.data_ptr(),
             out.data_ptr(), _at(out_lo), lse.data_ptr(), dout.data_ptr(), dt, T, H, k.shape[1], d,
-            ctypes.byref(s), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _at(dbias), ptr,
-            size, stream.cuda_stream))
+            ctypes.byref(s), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), gdt, _at(dbias),
+            bdt, ptr, size, stream.cuda_stream))
     return (dq, dk, dv) if dbias is None else (dq, dk, dv, dbias)
