@@ -428,9 +428,10 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  * j is visible to i in the same sample when j <= i, or when both lie in a
  * bidirectional prefix.  rel_bias entries at or below -1e37 (the type's lowest
  * value, minus infinity) hide the pair; a row that sees no key has out 0, lse
- * -inf and no gradient.  Entries and slopes are otherwise finite, and so are q, k, v:
- * a NaN or infinity in a key or value row may reach every row of the 128-row
- * tiles that hold it.
+ * -inf and no gradient.  Entries and slopes are otherwise finite.  A NaN or
+ * infinity in q, k, v or dout stays within its sample; there it may reach every
+ * row of the 128-row tiles that hold it, before the causal mask's rows too.
+ * softmax_scale lies in [1e-10, 1e10].
  *
  *   q, out, dout [T][H][d], k, v [T][H_kv][d], lse [H][T], dq, dk, dv: as
  *                cp_attn_fwd_gqa / cp_attn_bwd_gqa, with T and H those of the plan

@@ -286,6 +286,48 @@ def test_streams_graphs_and_shared_plans():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=4.0), dict(slopes=True), dict(bias=True),
+                                dict(softcap=4.0, bias=True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_and_infinity_stay_in_their_sample(dtype, kw, d):
+    """A sample of NaN and infinities between two others: those get the bits they get beside a finite
+    one (gradients up to the order of fp32 sums; under a cap an infinity in a shared tile may select
+    the other evaluation of tanh, 1e-6 apart, which can turn a rounding to bf16).  Lengths end inside
+    tiles; the prefix is two-way."""
+    from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    lens, H = [150, 70, 131], 4
+    cu, opt = _cu(lens), {}
+    plan = ScorePlan(cu, H, prefix_len=[40, 70, 5], bidirectional_prefix=True, rel_buckets=[0, 1, 2, 2, 3], device=DEV)
+    if "softcap" in kw:
+        opt["softcap"] = kw["softcap"]
+    if "slopes" in kw:
+        opt["slopes"] = torch.tensor([0.5, 0.25, 0.1, 0.01], device=DEV)
+    if "bias" in kw:
+        opt["rel_bias"] = torch.randn(H, 4, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+
+    def run(x):
+        out, lse, *lo = cp_attn_scored_fwd(*x[:3], plan, R64, residual=dtype == "bf16", **opt)
+        return [out, lse.t()] + list(cp_attn_scored_bwd(*x[:3], out, lse, x[3], plan, R64,
+                                                        out_lo=lo[0] if lo else None, **opt))[:3]
+    clean = [x.to(DEV) for x in _inputs(cu[-1], H, 2, d, dtype, 6)]
+    dirty = [x.clone() for x in clean]
+    for i, x in enumerate(dirty):
+        x[150:220] = float("nan")
+        x[150 + 7 * i:220:13] = float("inf")
+    for i, (a, b) in enumerate(zip(run(clean), run(dirty))):
+        for rows in (slice(0, 150), slice(220, 351)):
+            x, y = a[rows].float(), b[rows].float()
+            assert torch.isfinite(y).all(), i
+            if "softcap" in kw and i < 2:
+                assert torch.all((x - y).abs() <= 2.0 ** -7 * x.abs() + 1e-5), i
+            elif i < 2:
+                assert torch.equal(x, y), i
+            else:   # dS rounded to bf16 on the other side of a border: one step of 2^-8 in few places
+                assert (x - y).norm() <= (2.0 ** -10 if "softcap" in kw else 1e-5) * x.norm(), i
+
+
+@pytest.mark.gpu
 def test_no_tokens_and_given_outputs():
     from vlm_zigzag_head_gb300 import CpError, ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
     H, d = 2, 64

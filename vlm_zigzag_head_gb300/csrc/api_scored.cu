@@ -106,8 +106,9 @@ cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptr
   if (Hkv < 1 || H % Hkv != 0)
     return entry_fail(CP_ERR_SHAPE, "H must be a positive multiple of H_kv");
   if (d != 64 && d != 128) return entry_fail(CP_ERR_SHAPE, "head_dim must be 64 or 128");
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return entry_fail(CP_ERR_INVALID_ARG, "softmax_scale must be positive and finite");
+  // its inverse, and its quotients with the cap and the slopes, stay normal numbers
+  if (!(scale >= 1e-10f && scale <= 1e10f))
+    return entry_fail(CP_ERR_INVALID_ARG, "softmax_scale must be in [1e-10, 1e10]");
   if (!(sc->softcap >= 0.f) || !std::isfinite(sc->softcap))
     return entry_fail(CP_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: none)");
   // cap * log2(e), its inverse and that inverse's eighth power stay normal numbers
@@ -354,6 +355,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   a.status = reinterpret_cast<int32_t*>(w);
   a.wait_limit = device_wait_limit();
   a.text_rows = T;
+  a.isolate = 1;
   a.score = s;
   ProfileScope prof(2, st);
   ENTRY_CUDA(launch_tc_fwd_scored(a, c.bias, st), "tensor-core scored forward");
@@ -480,6 +482,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.status = reinterpret_cast<int32_t*>(w);
     a.wait_limit = device_wait_limit();
     a.kv_split = kv_split;
+    a.isolate = 1;
     a.item_major = item_major((int64_t)c.h->n_bwd * Hkv * kv_split, sms) ? 1 : 0;
     a.f16 = c.f16 ? 1 : 0;
     a.op_scales = c.f16 ? sc : nullptr;

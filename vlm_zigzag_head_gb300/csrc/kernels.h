@@ -38,6 +38,8 @@ cudaError_t launch_lse_merge(int n_parts, const float* part_out, const float* pa
                              int H, int d, void* out, bool out_bf16, float* lse, cudaStream_t st);
 // D[h*pitch + t] = sum_e dO[t][h][e] * O[t][h][e];  lse2[h*pitch + t] = lse[h][t] * log2(e)
 // (out_lo nullable, bf16 only: D uses out + out_lo)
+// bf16 (the tensor-core backward): both negated, so that the kernel adds them;
+// a row that saw no key (lse -inf) counts as lse +inf.
 cudaError_t launch_bwd_preprocess(const void* out, const void* out_lo, const void* dout, bool bf16,
                                   const float* lse, int T, int H, int d, float* D, float* lse2,
                                   int64_t pitch, cudaStream_t st);

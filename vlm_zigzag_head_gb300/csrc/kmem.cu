@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) bwd_pre_kernel(const T* __restrict__
                                                            const T* __restrict__ dout,
                                                            const float* __restrict__ lse, int Tn,
                                                            int H, int d, float* D, float* lse2,
-                                                           long long pitch) {
+                                                           long long pitch, float sign) {
   const int lane = threadIdx.x & 31;
   const int lpr = d * (int)sizeof(T) / 16;          // lanes per row: 8, 16 or 32
   const int rpw = 32 / lpr;                          // rows per warp pass
@@ -255,10 +255,11 @@ __global__ void __launch_bounds__(kThreads) bwd_pre_kernel(const T* __restrict__
     if (valid) add_dot16(o + off, o_lo ? o_lo + off : nullptr, dout + off, acc);
     for (int sh = lpr >> 1; sh > 0; sh >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, sh);
     if (valid && sl == 0) {
-      D[(long long)h * pitch + t] = acc;
+      D[(long long)h * pitch + t] = sign * acc;
       // a row that saw no key (lse -inf) gets +inf: its probabilities are then 0
       const float lr = lse[(long long)h * Tn + t];
-      lse2[(long long)h * pitch + t] = lr == -INFINITY ? INFINITY : lr * 1.4426950408889634f;
+      lse2[(long long)h * pitch + t] =
+          sign * (lr == -INFINITY ? INFINITY : lr * 1.4426950408889634f);
     }
   }
 }
@@ -503,11 +504,11 @@ cudaError_t launch_bwd_preprocess(const void* out, const void* out_lo, const voi
     bwd_pre_kernel<__nv_bfloat16><<<g, kThreads, 0, st>>>(
         static_cast<const __nv_bfloat16*>(out), static_cast<const __nv_bfloat16*>(out_lo),
         static_cast<const __nv_bfloat16*>(dout), lse, T,
-        H, d, D, lse2, pitch);
+        H, d, D, lse2, pitch, -1.f);
   else
     bwd_pre_kernel<float><<<g, kThreads, 0, st>>>(static_cast<const float*>(out), nullptr,
                                                   static_cast<const float*>(dout), lse, T, H, d,
-                                                  D, lse2, pitch);
+                                                  D, lse2, pitch, 1.f);
   return cudaGetLastError();
 }
 

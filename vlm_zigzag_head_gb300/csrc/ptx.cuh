@@ -279,6 +279,18 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// Rows [first, 128) of an operand tile become zero: D / 64 boxes of 128 rows x 128
+// bytes (a row keeps its 128 bytes under the swizzle).  kThreads threads call it
+// with their number t; a fence.proxy.async and a barrier arrival must follow.
+template <int D, int kThreads>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int first, int t) {
+  constexpr int kPieces = D / 8;   // 16-byte pieces of one row
+  const int piece = t % kPieces;
+  uint8_t* p = tile + (piece >> 3) * (128 * 128) + (piece & 7) * 16;
+#pragma unroll 1
+  for (int row = first + t / kPieces; row < 128; row += kThreads / kPieces)
+    *reinterpret_cast<uint4*>(p + row * 128) = make_uint4(0, 0, 0, 0);
+}
 // Vector fp32 reduce-add into global memory (16-byte aligned address).
 __device__ __forceinline__ void red_add_v4(float4* p, float4 v) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y),

@@ -40,25 +40,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The cap: products s become t = tanh(s * in), in = scale / softcap; the scores
-// are then t * cap2.  (The products are scaled before the polynomial: its
-// coefficients in their units could underflow.)
-template <bool kCap>
+// The cap: products s become t = tanh(s * in), in = scale / softcap, or with kNeg
+// (the backward) minus that; the scores are t * mul, mul = cap2 or -cap2.  (With
+// the sign reversed one constant, -1, serves the polynomial and the slope.  The
+// products are scaled before the polynomial: its coefficients in their units could
+// underflow.)
+template <bool kCap, bool kNeg>
 struct Cap {
-  float in = 0.f, cap2 = 0.f, inv = 0.f;
-  uint64_t in2 = 0, one = 0, neg = 0, k[4] = {0, 0, 0, 0};
+  static constexpr float kUnit = kNeg ? -1.f : 1.f;
+  float in = 0.f, mul = 0.f;
+  uint64_t in2 = 0, unit = 0, k[4] = {0, 0, 0, 0};
   __device__ __forceinline__ Cap(const ScoreArgs& s, float scale_log2) {
     if constexpr (kCap) {
-      cap2 = s.cap_log2;
-      inv = s.inv_cap_log2;
-      in = scale_log2 * inv;
+      mul = kUnit * s.cap_log2;
+      in = scale_log2 * s.inv_cap_log2;
       in2 = pack2(in, in);
-      one = pack2(1.f, 1.f);
-      neg = pack2(-1.f, -1.f);
-      k[0] = pack2(kC1, kC1);
-      k[1] = pack2(kC2, kC2);
-      k[2] = pack2(kC3, kC3);
-      k[3] = pack2(kC4, kC4);
+      unit = pack2(kUnit, kUnit);
+      k[0] = pack2(kUnit * kC1, kUnit * kC1);
+      k[1] = pack2(kUnit * kC2, kUnit * kC2);
+      k[2] = pack2(kUnit * kC3, kUnit * kC3);
+      k[3] = pack2(kUnit * kC4, kUnit * kC4);
     }
   }
   // the largest |s| of a warp, times in, lets the polynomial serve
@@ -70,16 +71,17 @@ struct Cap {
     uint64_t p = fma2(k[3], v, k[2]);
     p = fma2(p, v, k[1]);
     p = fma2(p, v, k[0]);
-    p = fma2(p, v, one);
+    p = fma2(p, v, unit);
     return mul2(z, p);
   }
   // any s: tanh z = 1 - 2 / (1 + e^(2z)), e^(2z) = 2^(2 z log2 e)
   __device__ __forceinline__ float any(float s) const {
-    return fmaf(-2.f, rcp_approx(1.f + ex2(s * in * (2.f * kLog2e))), 1.f);
+    return fmaf(-2.f * kUnit, rcp_approx(1.f + ex2(s * in * (2.f * kLog2e))), kUnit);
   }
-  // 1 - t^2
-  __device__ __forceinline__ uint64_t slope(uint64_t t) const {
-    return fma2(mul2(t, neg), t, one);
+  // t^2 - 1
+  __device__ __forceinline__ uint64_t minus_slope(uint64_t t) const {
+    static_assert(kNeg, "the constant is -1");
+    return fma2(t, t, unit);
   }
 };
 

@@ -71,6 +71,8 @@ struct TcFwdArgs {
   int32_t* status;            // DevStatus of the workspace
   long long wait_limit;
   int64_t text_rows;          // rows of the rank-local (gathered) tensors (index checks)
+  int isolate;                // nonzero: rows past a run's end are cleared before a product
+                              // reads them (0 * NaN of a neighbouring sample is NaN)
   ScoreArgs score;            // read by the scored kernels only
 };
 cudaError_t launch_tc_fwd(const TcFwdArgs& a, cudaStream_t st);
@@ -95,6 +97,7 @@ struct TcBwdArgs {
   long long wait_limit;
   int kv_split;               // CTAs sharing one KV head's query heads (divides H / Hkv); > 1:
                               // dK / dV / prefix slots are reduce-added into zeroed memory
+  int isolate;                // as TcFwdArgs::isolate, for query and key rows
   int item_major;             // nonzero: blocks go item by item (all heads of the heaviest
                               // item first), else head by head
   int n_slots;                // prefix-gradient slots (P + 1) behind pre_k / pre_v (index checks)

@@ -39,14 +39,16 @@
 //   warp 0       TMA producer: K, V once; Q and the lse2 / D rows per tile
 //   warp 1       TMEM allocation; lane 0 issues every tcgen05.mma
 //   warp 2       TMA producer: dO per tile
-//   warp 3       idle
+//   warp 3       clears rows of another sample in the tiles that hold some (isolate)
 //   warps 4..11  P / dS (two warpgroups, 64 query columns each; thread = key
 //                row), then the dK / dV epilogue
 //   warps 12..15 dQ drain; thread = query row (TMEM lane of dQ)
 // Registers: warpgroup 0 drops to 64 (the least that leaves its MMA and
 // producer code without spills), the P / dS warpgroups rise to 136 and the
 // drain warpgroup to 168 (128 * 64 + 256 * 136 + 128 * 168 <= 512 * 128), so a
-// drain thread can hold its whole dQ row and free the TMEM at once.
+// drain thread can hold its whole dQ row and free the TMEM at once.  Modified
+// scores need more: 144 and 152 (the same sum; 18688 tokens, 8 heads, capped: 1688
+// us against 1819; plain scores are better off with the first split, 1491 to 1527).
 //
 // With kCap or kBias (score.cuh) the P / dS warps recompute the modified scores
 // from S^T; under a cap dS also takes the factor 1 - tanh^2.  A table bias's
@@ -126,6 +128,7 @@ static_assert(sizeof(TileInfo) == 32, "TileInfo layout");
 
 struct Bars {
   uint64_t kv_full;
+  uint64_t kv_raw, q_raw[kQStages], do_raw[2];   // tiles cleared before their *_full (isolate)
   uint64_t q_full[kQStages], q_empty[kQStages];
   uint64_t do_full[2], do_empty[2];
   uint64_t s_full, p_full, dp_full, ds_full;
@@ -175,7 +178,34 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-// Four neighbouring per-query values (lse2 or D); vec: 16-byte aligned.
+// The barriers of a producer's loads over N stages: a stage's own one, or its raw
+// one for a tile that warp 3 clears first.  Bit st of each word belongs to stage st.
+template <int N>
+struct Loads {
+  uint32_t used = 0, raw = 0;                  // the stage has a load; it is on the raw barrier
+  uint32_t full_phase = 0, raw_phase = 0;      // phases of the next load
+  uint32_t last = 0;                           // phase of the last load
+  __device__ __forceinline__ uint64_t* next(int st, bool on_raw, uint64_t* full, uint64_t* rawb) {
+    const uint32_t bit = 1u << st;
+    // a stage's own barrier completes once per tile, whoever publishes it
+    last = (last & ~bit) | ((on_raw ? raw_phase : full_phase) & bit);
+    used |= bit;
+    raw = on_raw ? raw | bit : raw & ~bit;
+    if (on_raw) raw_phase ^= bit;
+    full_phase ^= bit;
+    return on_raw ? rawb + st : full + st;
+  }
+  // every load must have landed before the CTA exits (normally the consumers
+  // already waited for them and these waits return at once)
+  __device__ __forceinline__ void drain(uint64_t* full, uint64_t* rawb) const {
+    int zero = 0;
+    for (int st = 0; st < N; ++st)
+      if (used >> st & 1)
+        mbar_wait(raw >> st & 1 ? rawb + st : full + st, last >> st & 1, kDrainLimit, &zero);
+  }
+};
+
+// Four neighbouring per-query values (minus lse2 or minus D); vec: 16-byte aligned.
 __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4]) {
   if (vec) {
     const float4 q = *reinterpret_cast<const float4*>(p);
@@ -188,17 +218,18 @@ __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4
 
 // P^T of 32 queries from their products (rs), with modified scores: the
 // probabilities as bf16 pairs in pk (the dV operand); in place over the products
-// what dS multiplies: P, or under a cap P (1 - tanh^2).  kFast: every pair is
+// what dS multiplies: P, or under a cap -P (1 - tanh^2), whose sign the factors of
+// dQ and dK undo.  kFast: every pair is
 // visible, the cap's polynomial holds and the bias is linear along the queries.
 // mul: scale or cap in log2 units, inv its inverse.  x0: the half's first query in
 // the 64; ld: its lse2.
 template <bool kCap, int kBias, bool kFast>
 __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, int x0, float mul,
-                                              float inv, const score::Cap<kCap>& cap,
+                                              float inv, const score::Cap<kCap, true>& cap,
                                               const score::TileBias& tb, bool poly,
                                               const float* ld, bool vec, int first_vis,
                                               int end_vis) {
-  const uint64_t mul_2 = pack2(mul, mul), base2 = pack2(tb.base, tb.base), neg = pack2(-1.f, -1.f);
+  const uint64_t mul_2 = pack2(mul, mul), base2 = pack2(tb.base, tb.base);
   const float step = tb.step * inv;   // slopes, before `mul`
   const bool column = kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr);
 #pragma unroll
@@ -216,13 +247,14 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, 
           unpack2(s, s0, s1);
           s = pack2(cap.any(s0), cap.any(s1));
         }
-        w = cap.slope(s);
+        w = cap.minus_slope(s);
       }
       if constexpr (kBias == SCORE_SLOPES) {
         unpack2(s, s0, s1);
         s = pack2(fmaf((float)y, step, s0), fmaf((float)(y + 1), step, s1));
       }
-      uint64_t add = fma2(pack2(l[y - x], l[y - x + 1]), neg, base2);
+      uint64_t add = pack2(l[y - x], l[y - x + 1]);   // minus lse2
+      if constexpr (kBias != SCORE_PLAIN) add = add2(add, base2);
       if (!kFast && column)
         add = add2(add, pack2(score::column_bias<kBias, 1>(tb, x0 + y),
                               score::column_bias<kBias, 1>(tb, x0 + y + 1)));
@@ -235,7 +267,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, 
         if (x0 + y + 1 < first_vis || x0 + y + 1 >= end_vis) p1 = 0.f;
       }
       pk[y / 2] = pack_bf16x2(p0, p1);
-      if constexpr (kCap) unpack2(mul2(pack2(p0, p1), w), p0, p1);
+      if constexpr (kCap) unpack2(mul2(pack2(p0, p1), w), p0, p1);   // -P (1 - tanh^2)
       rs[y] = __float_as_uint(p0);
       rs[y + 1] = __float_as_uint(p1);
     }
@@ -245,7 +277,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, 
 // Whether a warp's 64 products per lane all lie in the polynomial's range.
 template <bool kCap>
 __device__ __forceinline__ bool in_poly_range(const uint32_t (&rs)[2][32],
-                                              const score::Cap<kCap>& cap) {
+                                              const score::Cap<kCap, true>& cap) {
   if constexpr (!kCap) return true;
   float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -317,6 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->kv_full, 1);
+    mbar_init(&bars->kv_raw, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_raw[s], 1);
+      mbar_init(&bars->do_raw[s], 1);
+    }
     for (int s = 0; s < kQStages; ++s) {
       mbar_init(&bars->q_full[s], 1);
       mbar_init(&bars->q_empty[s], 1);
@@ -356,22 +393,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Concurrent CTAs are neighbouring key tiles that meet the same queries in
   // the same order, so the Q / dO tiles they load are shared through L2.
   const int n_all = Gs * n_qt;
+  // isolate: K / V rows past the item's keys and Q / dO rows (and lse2, D) past a
+  // run's end are another sample's and may be NaN.  Their P and dS are 0; so that 0
+  // meets 0, the loads of such a tile complete on a raw barrier, and warp 3 clears
+  // the foreign rows before it publishes the tile.
+  const bool clear_kv = a.isolate && it.k_len < kBK && n_all > 0;
 
   if (warp < 4) {
     setmaxnreg_dec<64>();
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer: K, V, Q, lse2 / D
       if (lane == 0) {
-        int issued = 0;
+        Loads<kQStages> loads;
         bool kv_issued = false;
         if (n_all > 0 && !(CP_IN_RANGE(it.k_row0, 0, a.T, a.status, 201) &&
                            CP_IN_RANGE(hk, 0, a.Hkv, a.status, 202))) {
           *abort = 1;
         } else if (n_all > 0) {
-          mbar_expect_tx(&bars->kv_full, 2 * L::kTile);
+          uint64_t* landed = clear_kv ? &bars->kv_raw : &bars->kv_full;
+          mbar_expect_tx(landed, 2 * L::kTile);
           for (int b = 0; b < D / 64; ++b) {
-            tma_load_3d(&a.tm_k, &bars->kv_full, smem + L::kK + b * L::kBox, b * 64, hk, it.k_row0);
-            tma_load_3d(&a.tm_v, &bars->kv_full, smem + L::kV + b * L::kBox, b * 64, hk, it.k_row0);
+            tma_load_3d(&a.tm_k, landed, smem + L::kK + b * L::kBox, b * 64, hk, it.k_row0);
+            tma_load_3d(&a.tm_v, landed, smem + L::kV + b * L::kBox, b * 64, hk, it.k_row0);
           }
           kv_issued = true;
         }
@@ -399,29 +442,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           info->delta = sg.delta;
           info->len = sg.len;
           info->rel = sg.rel;
-          mbar_expect_tx(&bars->q_full[st], L::kTile + L::kLdBytes);
+          uint64_t* landed = loads.next(st, a.isolate && sg.len - q0 - t * kBQ < kBQ, bars->q_full,
+                                        bars->q_raw);
+          mbar_expect_tx(landed, L::kTile + L::kLdBytes);
           for (int b = 0; b < D / 64; ++b)
-            tma_load_3d(&a.tm_q, &bars->q_full[st], smem + L::kQ + st * L::kTile + b * L::kBox,
-                        b * 64, hq, grow);
+            tma_load_3d(&a.tm_q, landed, smem + L::kQ + st * L::kTile + b * L::kBox, b * 64, hq,
+                        grow);
           // the lse2 / D box starts at the row rounded down to 4 (16-byte TMA alignment)
-          tma_load_3d(&a.tm_ld, &bars->q_full[st], smem + L::kLd + st * L::kLdStride, grow & ~3,
-                      hq, 0);
-          issued = j + 1;
+          tma_load_3d(&a.tm_ld, landed, smem + L::kLd + st * L::kLdStride, grow & ~3, hq, 0);
         }
         // every load issued here must land before the CTA exits (normally the
         // consumers already waited for them and these waits return at once)
         int zero = 0;
-        if (kv_issued) mbar_wait(&bars->kv_full, 0, kDrainLimit, &zero);
-        for (int x = issued - kQStages; x < issued; ++x) {
-          if (x < 0) continue;
-          mbar_wait(&bars->q_full[x % kQStages], (x / kQStages) & 1, kDrainLimit, &zero);
-        }
+        if (kv_issued) mbar_wait(clear_kv ? &bars->kv_raw : &bars->kv_full, 0, kDrainLimit, &zero);
+        loads.drain(bars->q_full, bars->q_raw);
       }
     } else if (warp == 2) {
       // ---------------------------------------------------------- TMA producer: dO
       if (lane == 0) {
         constexpr int S = L::kDOStages;
-        int issued = 0;
+        Loads<S> loads;
         TileWalk walk;
         int jt = 0, hq = hq0;
         for (int j = 0; j < n_all; ++j, jt = jt + 1 == n_qt ? 0 : jt + 1, hq += jt == 0) {
@@ -438,17 +478,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             *abort = 1;
             break;
           }
-          mbar_expect_tx(&bars->do_full[st], L::kTile);
+          uint64_t* landed = loads.next(st, a.isolate && sg.len - q0 - t * kBQ < kBQ, bars->do_full,
+                                        bars->do_raw);
+          mbar_expect_tx(landed, L::kTile);
           for (int b = 0; b < D / 64; ++b)
-            tma_load_3d(&a.tm_do, &bars->do_full[st], smem + L::kDO + st * L::kTile + b * L::kBox,
-                        b * 64, hq, grow);
-          issued = j + 1;
+            tma_load_3d(&a.tm_do, landed, smem + L::kDO + st * L::kTile + b * L::kBox, b * 64, hq,
+                        grow);
         }
-        int zero = 0;
-        for (int x = issued - S; x < issued; ++x) {
-          if (x < 0) continue;
-          mbar_wait(&bars->do_full[x % S], (x / S) & 1, kDrainLimit, &zero);
+        loads.drain(bars->do_full, bars->do_raw);
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- rows of another sample
+      // Clears them in the tiles that landed on a raw barrier, then publishes the
+      // tile; in the order in which the MMA issuer takes the tiles.
+      if (clear_kv) {
+        if (__all_sync(0xffffffffu, mbar_wait(&bars->kv_raw, 0, lim, abort))) {
+          clear_rows<D, 32>(smem + L::kK, it.k_len, lane);
+          clear_rows<D, 32>(smem + L::kV, it.k_len, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->kv_full);
         }
+      }
+      TileWalk walk;
+      uint32_t q_phase = 0, do_phase = 0;   // bit st: phase of the stage's raw barrier
+      int jt = 0;
+      for (int j = 0; a.isolate && j < n_all; ++j, jt = jt + 1 == n_qt ? 0 : jt + 1) {
+        Seg sg;
+        int q0, t;
+        tile_of(runs, nseg, jt, walk, sg, q0, t);
+        const int tail = sg.len - q0 - t * kBQ;
+        if (tail >= kBQ) continue;
+        const int st = j % kQStages, so = j % L::kDOStages;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&bars->q_raw[st], q_phase >> st & 1, lim, abort)))
+          break;
+        q_phase ^= 1u << st;
+        clear_rows<D, 32>(smem + L::kQ + st * L::kTile, tail, lane);
+        float* ld = reinterpret_cast<float*>(smem + L::kLd + st * L::kLdStride) +
+                    ((sg.row0 + q0 + t * kBQ) & 3);
+        for (int x = tail + lane; x < kBQ; x += 32) ld[x] = ld[kLdRows + x] = 0.f;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full[st]);
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&bars->do_raw[so], do_phase >> so & 1, lim, abort)))
+          break;
+        do_phase ^= 1u << so;
+        clear_rows<D, 32>(smem + L::kDO + so * L::kTile, tail, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->do_full[so]);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
@@ -476,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         bool ok = true;
         if (n_all > 0) {
-          ok = mbar_wait(&bars->kv_full, 0, lim, abort) && mbar_wait(&bars->q_full[0], 0, lim, abort);
+          ok = mbar_wait(&bars->kv_full, 0, lim, abort) &&
+               mbar_wait(&bars->q_full[0], 0, lim, abort);
           if (ok) {
             tc_fence_after();
             issue_s(0);
@@ -554,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    setmaxnreg_inc<168>();
+    setmaxnreg_inc<kCap || kBias != SCORE_PLAIN ? 152 : 168>();
     // ------------------------------------------------------------ dQ drain
     // thread = query row wq * 32 + lane of the tile (TMEM lane of dQ).  The
     // whole row comes out of TMEM first (its columns are free again for the
@@ -566,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     // dQ = scale * (dS K); with f16 operands also undo the dS and K factors
-    const float dq_mul = kF16 ? a.scale * a.op_scales->dq_mul : a.scale;
+    const float dq_scale = kCap ? -a.scale : a.scale;   // dS comes negated under a cap
+    const float dq_mul = kF16 ? dq_scale * a.op_scales->dq_mul : dq_scale;
     uint8_t* stg = smem + L::kStg + wq * L::kStgWarp;
     uint8_t* my_row = stg + lane * 128;
     const int sw = lane & 7;
@@ -590,6 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->dq_free);
+      // rows past the run's end are another sample's: what this sample's keys (NaN,
+      // it may be) give them is replaced by zero
+      const bool foreign = a.isolate && lane >= sg.len - q0 - t * kBQ - wq * 32;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         // the previous reduce of this warp must have read the buffer
@@ -602,6 +687,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        __uint_as_float(r[c][4 * x + 2]) * dq_mul,
                                        __uint_as_float(r[c][4 * x + 3]) * dq_mul);
           *reinterpret_cast<float4*>(my_row + ((x ^ sw) << 4)) = v;
+        }
+        if (foreign) {
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<float4*>(my_row + x * 16) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -616,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) bulk_wait_all();   // every reduce-add finished before exit
     if (!ok) record_timeout(a.status, abort, 24);
   } else {
-    setmaxnreg_inc<136>();
+    setmaxnreg_inc<kCap || kBias != SCORE_PLAIN ? 144 : 136>();
     // ------------------------------------------------------------ P / dS
     // Two warpgroups share every query tile: warpgroup g (warps 4+4g .. 7+4g)
     // computes P^T / dS^T for query columns [64g, 64g + 64) of its key rows.
@@ -630,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sw = u & 7;
     bool ok = true;
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const score::Cap<kCap> cap(a.score, sl2);
-    const float s_mul = kCap ? cap.cap2 : sl2, s_inv = kScored ? 1.f / s_mul : 0.f;
+    const score::Cap<kCap, true> cap(a.score, sl2);
+    const float s_mul = kCap ? cap.mul : sl2, s_inv = kScored ? 1.f / s_mul : 0.f;
     int jt = 0, hq = hq0;       // tile and query head, as the producers walk them
     float far_sum = 0.f;        // this thread's dS beyond the table (kBias: table),
     uint64_t far2 = 0;          // and the same by even and odd queries
@@ -716,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; y += 2) {
             float d0, d1;
-            const uint64_t diff = fma2(pack2(dd[y], dd[y + 1]), pack2(-1.f, -1.f),
+            const uint64_t diff = add2(pack2(dd[y], dd[y + 1]),   // minus D
                                        pack2(__uint_as_float(rd[x + y]),
                                              __uint_as_float(rd[x + y + 1])));
             const uint64_t ds = mul2(pack2(__uint_as_float(rs[h][x + y]),
@@ -802,7 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         dst = (g == 0 ? a.pre_k : a.pre_v) + (row * a.Hkv + hk) * D;
       }
       const bool first = (it.flags & F_FIRST) != 0;
-      const float mul = g == 0 ? (kF16 ? a.scale * a.op_scales->dk_mul : a.scale) : 1.f;
+      const float dk_scale = kCap ? -a.scale : a.scale;
+      const float mul = g == 0 ? (kF16 ? dk_scale * a.op_scales->dk_mul : dk_scale) : 1.f;
       const uint32_t col = g == 0 ? C::kDK : C::kDV;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {

@@ -148,7 +148,7 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
 // the caller caps the row's maximum, and each product beside its exponential.
 template <bool kCap, int kBias>
 __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv,
-                                          const score::Cap<kCap>& cap, const score::TileBias& tb,
+                                          const score::Cap<kCap, false>& cap, const score::TileBias& tb,
                                           float& mul, float& add) {
   add = tb.base;
   bool lazy = false;
@@ -416,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     // scores in log2 units: products (or what score_row makes of them) times sl2,
     // plus s_add
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const score::Cap<kCap> cap(a.score, a.scale_log2);
-    const float s_mul = kCap ? cap.cap2 : a.scale_log2, s_inv = kScored ? 1.f / s_mul : 0.f;
+    const score::Cap<kCap, false> cap(a.score, a.scale_log2);
+    const float s_mul = kCap ? cap.mul : a.scale_log2, s_inv = kScored ? 1.f / s_mul : 0.f;
     float sl2 = s_mul, s_add = 0.f;
     const float vmul = kF16P ? a.op_scales->v_mul : 1.f;   // V = V16 * vmul
     bool ok = true;
@@ -549,6 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
         tmem_st32(s_col, pk[0]);
         tmem_st32(s_col + 32, pk[1]);
         l += ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
+        // V rows past the run's end (another sample's) meet probabilities of 0;
+        // tile A's warps clear them, as its PV is the first to read V
+        const int tail = sg.len - tt * kBN;
+        if (a.isolate && x == 0 && tail < kBN) {
+          const int vs = j % kStages;
+          if (!mbar_wait(&bars->v_full[vs], (j / kStages) & 1, lim, abort)) { ok = false; break; }
+          clear_rows<D, 128>(smem + L::kV + vs * L::kTile, tail, t);
+          fence_proxy_async_smem();
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import numbers
 from typing import List, Optional, Sequence, Union
 
 import torch
@@ -56,11 +57,14 @@ class ScorePlan:
             device = torch.device("cuda", torch.cuda.current_device())
         if torch.cuda.is_current_stream_capturing():
             raise CpError(1, "make the plan before the capture")
+        if rel_buckets is not None:
+            rel_buckets = [int(b) for b in rel_buckets]
+            if not rel_buckets:
+                raise CpError(1, "rel_buckets is empty")
         sms = torch.cuda.get_device_properties(device).multi_processor_count
         self.host, self.T = build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix,
                                        rel_buckets, sms)
         self.heads = int(heads)
-        self.n_buckets = max(rel_buckets) + 1 if rel_buckets else 0
         with torch.cuda.device(device):
             # a blocking copy: the lists are on the device before any stream uses them
             self.dev = torch.frombuffer(self.host, dtype=torch.uint8).to(device)
@@ -92,7 +96,8 @@ def build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix, rel_buckets,
     n = len(cu_seqlens) - 1
     if n < 1:
         raise CpError(1, "cu_seqlens needs at least two entries")
-    lens = [int(prefix_len)] * n if isinstance(prefix_len, int) else [int(x) for x in prefix_len]
+    one = isinstance(prefix_len, numbers.Integral)
+    lens = [int(prefix_len)] * n if one else [int(x) for x in prefix_len]
     if len(lens) != n:
         raise CpError(2, "prefix_len needs one entry per sample")
     pre = _b.cu_array(lens)
