@@ -231,13 +231,6 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
-// The same without swizzle, for a K-major operand in core matrices (8 rows x 16
-// bytes, contiguous): lbo = distance between core matrices along K, sbo = between
-// groups of 8 rows.
-__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61);
-}
-
 // Instruction descriptor of kind::f16: bf16 A and B, fp32 accumulator,
 // M x N tile, A / B K-major (0) or MN-major (1).
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn_major, int b_mn_major) {
@@ -269,10 +262,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-// x rounded to bf16.
-__device__ __forceinline__ float bf16_part(float x) {
-  return __uint_as_float(pack_bf16x2(x, 0.f) << 16);
 }
 // Operand pairs for kind::f16 MMAs: bf16, or f16 when kF16.
 template <bool kF16>

@@ -78,9 +78,7 @@ struct Smem {
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kStages * kTile;
   static constexpr int kBars = kV + kStages * kTile;
-  static constexpr int kAx = kBars + 256;          // slopes: w of the rows, 0..127 of the keys
-  static constexpr int kBx = kAx + kBM * 32;       // (128 x 16 bf16, core-matrix layout)
-  static constexpr int kBytes = kBx + kBN * 32;
+  static constexpr int kBytes = kBars + 256;
   static constexpr int kAlloc = kBytes + 1024;     // slack for 1024-byte alignment
 };
 static_assert(Smem<128>::kAlloc <= 227 * 1024, "shared memory budget");
@@ -111,7 +109,9 @@ __device__ __forceinline__ int run_tiles(const Seg& s, int q_len) {
 // The n-th KV tile a unit visits of a run's nt.  With slopes the nearest come first:
 // their scores are the largest, so the running maximum settles at once, where from
 // the far end it would rise by 128 slopes a tile and O be rescaled every time
-// (18688 tokens, 8 heads: 704 us from the far end, 585 from the near one).
+// (18688 tokens, 8 heads: 725 us from the far end, 602 from the near one; plain
+// scores 575).  The bias itself costs one multiply-add per score; carried by one more
+// MMA step instead it measured 592, not worth the operand tiles it needs.
 template <int kBias>
 __device__ __forceinline__ int tile_at(int n, int nt) {
   return kBias == SCORE_SLOPES ? nt - 1 - n : n;
@@ -186,19 +186,6 @@ __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv
         r[i / 32][i % 32] = __float_as_uint(cap.any(__uint_as_float(r[i / 32][i % 32])));
     }
   }
-  if constexpr (kBias == SCORE_SLOPES && !kCap) {
-    // the products hold the linear bias already; keys ahead of the query (a two-way
-    // prefix) get twice their distance back
-    add = -tb.slope * tb.dist0;
-    if (tb.both) {
-      const float back = 2.f * tb.slope * inv;
-#pragma unroll
-      for (int i = 0; i < kBN; ++i)
-        r[i / 32][i % 32] = __float_as_uint(
-            fmaf(fminf(tb.dist0 - (float)i, 0.f), back, __uint_as_float(r[i / 32][i % 32])));
-    }
-    return false;
-  }
   if constexpr (kBias == SCORE_SLOPES) {
     if (!tb.both) {
       const float step = tb.step * inv;   // in the row's present units
@@ -236,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
   const long long lim = a.wait_limit;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, kBias == SCORE_SLOPES && !kCap ? 2 : 1);   // Q, and w (slopes)
+    mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->k_full[s], 1);
@@ -253,23 +240,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
-  }
-  // Slopes without a cap: the bias grows by w = slope / scale (in units of the
-  // products) from key to key, the same for every row.  One more MMA step adds it to
-  // S: three columns of A hold w in bf16 pieces (24 bits), three of B the key's place
-  // in the tile, exact in bf16; what is left is one number per row and tile.
-  constexpr bool kFold = kBias == SCORE_SLOPES && !kCap;
-  if constexpr (kFold) {
-    for (int i = threadIdx.x; i < kBM * 2; i += kThreads) {   // 16-byte pieces
-      const int row = i >> 1;
-      const uint32_t c = pack_bf16x2((float)row, (float)row);
-      reinterpret_cast<uint4*>(smem + L::kAx)[i] = make_uint4(0, 0, 0, 0);
-      // piece 0 of a row: columns 0..7, piece 1: columns 8..15 (core matrices of 8 rows)
-      uint4* b = reinterpret_cast<uint4*>(smem + L::kBx + (row >> 3) * 256 + (i & 1) * 128) +
-                 (row & 7);
-      *b = (i & 1) ? make_uint4(0, 0, 0, 0) : make_uint4(c, c & 0xffffu, 0, 0);
-    }
-    fence_proxy_async_smem();
   }
   if (warp == 1) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
@@ -363,16 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           for (int b = 0; b < D / 64; ++b)
             tma_load_3d(qm, &bars->q_full, smem + L::kQ + x * L::kTile + b * L::kBox, b * 64,
                         uid / a.n_items, it.q_row0 + x * kBM);
-        if constexpr (kFold) {   // the previous unit's S products are done with A's columns
-          const float w = a.score.slopes[uid / a.n_items] * score::kLog2e / a.scale_log2;
-          const float hi = bf16_part(w), mid = bf16_part(w - hi), lo = w - hi - mid;
-          const uint4 v = make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0, 0);
-#pragma unroll 4
-          for (int row = 0; row < kBM; ++row)
-            *(reinterpret_cast<uint4*>(smem + L::kAx + (row >> 3) * 256) + (row & 7)) = v;
-          fence_proxy_async_smem();
-          mbar_arrive(&bars->q_full);
-        }
         ++n;
       }
       int zero = 0;
@@ -394,9 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           mma_bf16(tmem + col_s(x), sdesc_sw128(qx + off, 16, 1024),
                    sdesc_sw128(k_addr + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
         }
-        if constexpr (kFold)
-          mma_bf16(tmem + col_s(x), sdesc_plain(smem_u32(smem + L::kAx), 128, 256),
-                   sdesc_plain(smem_u32(smem + L::kBx), 128, 256), idesc_qk, 1u);
         mma_commit(&bars->s_full[x]);
       };
       // O_x += P_x(j) V_j, P from TMEM (keys 16kk.. 16kk+15: columns 8kk .. 8kk+7);
