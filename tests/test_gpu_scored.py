@@ -364,6 +364,79 @@ def test_bounds_checked_build_meets_no_index_outside_a_tensor():
 
 
 @pytest.mark.gpu
+def test_waits_that_give_up_on_tiles_with_foreign_rows():
+    """The same with tiles that end inside a sample (their loads land on barriers of their own), forward
+    and backward; the next calls are exact again."""
+    from vlm_zigzag_head_gb300 import ScorePlan, Workspace, cp_attn_scored_bwd, cp_attn_scored_fwd, cp_set_wait_limit
+    from vlm_zigzag_head_gb300 import cp_workspace_status
+    cu = _cu([300, 77, 500, 1])
+    q, k, v, dout = (x.to(DEV) for x in _inputs(cu[-1], 4, 2, 128, "bf16", 1))
+    plan = ScorePlan(cu, 4, prefix_len=1, bidirectional_prefix=True, device=DEV)
+    ws = Workspace(DEV)
+
+    def both():
+        out, lse, lo = cp_attn_scored_fwd(q, k, v, plan, R128, softcap=5.0, workspace=ws, residual=True)
+        a = cp_workspace_status(ws)
+        g = cp_attn_scored_bwd(q, k, v, out, lse, dout, plan, R128, softcap=5.0, workspace=ws, out_lo=lo)
+        return a, cp_workspace_status(ws), (out, lse) + g
+    want = both()
+    assert want[:2] == (0, 0)
+    cp_set_wait_limit(1)
+    try:
+        seen = [both()[:2] for _ in range(3)]
+    finally:
+        cp_set_wait_limit(0)
+    assert any(7 in s for s in seen) and all(x in (0, 7) for s in seen for x in s)
+    got = both()
+    assert got[:2] == (0, 0) and torch.equal(got[2][0], want[2][0]) and torch.equal(got[2][1], want[2][1])
+    for x, y in zip(got[2][2:], want[2][2:]):
+        assert (x - y).norm() <= 1e-5 * y.norm()
+
+
+@pytest.mark.gpu
+def test_strided_inputs_and_broadcast_bias_through_autograd():
+    """q, k, v as slices of one tensor that start off the 16-byte grid, a bias row shared by all heads
+    (expanded), and slopes that ask for a gradient."""
+    from vlm_zigzag_head_gb300 import CpError, ScorePlan
+    from vlm_zigzag_head_gb300.autograd import cp_attention_scored
+    H, Hkv, d, T = 4, 2, 64, 150
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(T, H + 2 * Hkv, d + 3, generator=g).to(torch.bfloat16).to(DEV)[..., 1:d + 1].requires_grad_(True)
+    row = torch.randn(1, 3, generator=g).to(DEV).requires_grad_(True)
+    plan = ScorePlan([0, 90, T], H, rel_buckets=[0, 1, 2], device=DEV)
+    dout = torch.randn(T, H, d, generator=g).to(torch.bfloat16).to(DEV)
+    out, _ = cp_attention_scored(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], plan, rel_bias=row.expand(H, 3))
+    dx, drow = torch.autograd.grad(out, (x, row), dout)
+    ops = [t.detach().contiguous().requires_grad_(True) for t in (x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:])]
+    full = row.detach().expand(H, 3).contiguous().requires_grad_(True)
+    out2, _ = cp_attention_scored(*ops, plan, rel_bias=full)
+    got = torch.autograd.grad(out2, ops + [full], dout)
+    assert torch.equal(out, out2)
+    for a, b in ((dx, torch.cat(got[:3], dim=1)), (drow, got[3].sum(0, keepdim=True))):
+        assert (a.float() - b.float()).norm() <= 2.0 ** -8 * b.float().norm()
+    with pytest.raises(CpError):
+        cp_attention_scored(*ops, plan, slopes=torch.ones(H, device=DEV, requires_grad=True))
+
+
+@pytest.mark.gpu
+def test_fp32_bias_of_bf16_inputs_and_back():
+    """The bias keeps its own dtype, in its gradient too."""
+    from vlm_zigzag_head_gb300 import ScorePlan
+    from vlm_zigzag_head_gb300.autograd import cp_attention_scored
+    plan = ScorePlan([0, 70], 2, rel_buckets=[0, 1, 2], device=DEV)
+    for dtype, bdtype in (("bf16", torch.float32), ("f32", torch.bfloat16)):
+        q, k, v, dout = (x.to(DEV) for x in _inputs(70, 2, 2, 64, dtype, 2))
+        bias = torch.randn(2, 3, device=DEV).to(bdtype).requires_grad_(True)
+        out, _ = cp_attention_scored(q, k, v, plan, rel_bias=bias)
+        (db,) = torch.autograd.grad(out, bias, dout)
+        s = O.Scores(bias=bias.detach().cpu(), buckets=[0, 1, 2])
+        vals, tol = reference(q, k, v, [0, 70], 64 ** -0.5, s, dout, HALF_STEP["bf16"] if dtype == "bf16" else 0.0,
+                              HALF_STEP[dtype])
+        assert db.dtype == bdtype
+        check("dbias", db, vals["dbias"], tol["dbias"], extra=torch.finfo(bdtype).eps / 2)
+
+
+@pytest.mark.gpu
 def test_wait_that_gives_up_is_reported():
     """With the shortest wait limit the kernels leave early and the status says so."""
     from vlm_zigzag_head_gb300 import ScorePlan, Workspace, cp_attn_scored_fwd, cp_set_wait_limit, cp_workspace_status

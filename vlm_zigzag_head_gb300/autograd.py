@@ -23,7 +23,7 @@ from typing import Callable, Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (ScorePlan, cp_attn_bwd, cp_attn_fwd, cp_attn_scored_bwd, cp_attn_scored_fwd,
+from . import (CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, cp_attn_scored_bwd, cp_attn_scored_fwd,
                cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd)
 
 
@@ -80,10 +80,10 @@ def cp_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     return CPAttention.apply(q, k, v, cu_seqlens, P, prefix_len, softmax_scale, prefix_hook)
 
 
-def _dense(g: torch.Tensor) -> torch.Tensor:
-    """A contiguous, 16-byte aligned gradient (autograd may hand over any view)."""
-    g = g.contiguous()
-    return g if g.data_ptr() % 16 == 0 else g.clone()
+def _dense(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous, 16-byte aligned tensor (a copy of any other view)."""
+    x = x.contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
 
 
 class QKNormRope(torch.autograd.Function):
@@ -128,7 +128,7 @@ class CPAttentionScored(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, rel_bias, slopes, plan, softmax_scale, softcap):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q, k, v = _dense(q), _dense(k), _dense(v)
         # the bf16 remainder of the output keeps D = dO.O exact in the backward
         train = any(ctx.needs_input_grad) and q.dtype == torch.bfloat16
         out, lse, *lo = cp_attn_scored_fwd(q, k, v, plan, softmax_scale, softcap, slopes,
@@ -157,10 +157,12 @@ def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan:
                         rel_bias: Optional[torch.Tensor] = None):
     """Differentiable packed causal attention with modified scores (see
     :func:`cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
-    bidirectional prefix.  Returns ``(out, lse)``; gradients flow to q, k, v and
-    ``rel_bias``.  ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the
+    bidirectional prefix.  q, k and v of any strides (copied where not contiguous).
+    Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias``.  ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the
     backward into a graph, call :func:`cp_attn_scored_bwd`, which involves no leaves."""
     if softmax_scale is None:
         softmax_scale = q.shape[-1] ** -0.5
+    if slopes is not None and slopes.requires_grad:
+        raise CpError(8, "slopes have no gradient here; a learned bias goes in rel_bias")
     return CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan, float(softmax_scale),
                                    float(softcap))
