@@ -23,8 +23,7 @@ from typing import Callable, Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, cp_attn_scored_bwd, cp_attn_scored_fwd,
-               cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd)
+from . import CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
 
 
 class CPAttention(torch.autograd.Function):
@@ -86,23 +85,26 @@ def _dense(x: torch.Tensor) -> torch.Tensor:
     return x if x.data_ptr() % 16 == 0 else x.clone()
 
 
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 class QKNormRope(torch.autograd.Function):
-    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, options)``."""
+    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, desc)``."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, q_weight, k_weight, options):
+    def forward(ctx, q, k, positions, q_weight, k_weight, desc):
         ctx.save_for_backward(q, k, positions, q_weight, k_weight)
-        ctx.options = options
-        return cp_qk_norm_rope_fwd(q, k, positions, q_weight, k_weight, **options)
+        ctx.desc = desc
+        return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dq, dk, dqw, dkw = cp_qk_norm_rope_bwd(
-            q, k, positions, _dense(dq_out), _dense(dk_out), q_weight, k_weight,
-            **ctx.options)
+        dq, dk, dqw, dkw = norm_rope._launch_bwd(ctx.desc, q, k, positions, _dense(dq_out),
+                                                 _dense(dk_out), q_weight, k_weight)
         return (dq if need[0] else None, dk if need[1] else None, None,
                 dqw.to(q_weight.dtype) if need[3] else None,
                 dkw.to(k_weight.dtype) if need[4] else None, None)
@@ -114,27 +116,26 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
                  theta: float = 10000.0, rot_dim: Optional[int] = None,
                  sections: Optional[Sequence[int]] = None, interleaved: bool = False,
                  inv_freq: Optional[Sequence[float]] = None):
-    """Differentiable :func:`cp_qk_norm_rope_fwd`: RMS norm of every head of q and k
+    """Differentiable :func:`~vlm_zigzag_head_gb300.cp_qk_norm_rope_fwd`: RMS norm of every head of q and k
     and the position rotation, in one pass.  Returns contiguous ``(q_out, k_out)``,
     ready for :func:`cp_attention`; gradients flow to q, k and the weights."""
-    options = dict(eps=eps, theta=theta, rot_dim=rot_dim, sections=sections,
-                   interleaved=interleaved, inv_freq=inv_freq)
-    return QKNormRope.apply(q, k, positions, q_weight, k_weight, options)
+    desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections,
+                              interleaved, inv_freq)
+    if not _wants_grad(q, k, q_weight, k_weight):
+        return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
+    return QKNormRope.apply(q, k, positions, q_weight, k_weight, desc)
 
 
 class CPAttentionScored(torch.autograd.Function):
     """``(out, lse) = CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan,
-    softmax_scale, softcap)``.  lse and slopes are not differentiable."""
+    softmax_scale, desc)`` on checked tensors.  lse and slopes are not differentiable."""
 
     @staticmethod
-    def forward(ctx, q, k, v, rel_bias, slopes, plan, softmax_scale, softcap):
-        q, k, v = _dense(q), _dense(k), _dense(v)
+    def forward(ctx, q, k, v, rel_bias, slopes, plan, softmax_scale, desc):
         # the bf16 remainder of the output keeps D = dO.O exact in the backward
-        train = any(ctx.needs_input_grad) and q.dtype == torch.bfloat16
-        out, lse, *lo = cp_attn_scored_fwd(q, k, v, plan, softmax_scale, softcap, slopes,
-                                           rel_bias, residual=train)
-        ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, lo[0] if lo else None)
-        ctx.meta = (plan, softmax_scale, softcap)
+        out, lse, out_lo = scored._launch_fwd(desc, q, k, v, plan, softmax_scale, residual=True)
+        ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, out_lo)
+        ctx.meta = (plan, softmax_scale, desc)
         ctx.mark_non_differentiable(lse)
         return out, lse
 
@@ -142,13 +143,15 @@ class CPAttentionScored(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout, _dlse):
         q, k, v, rel_bias, slopes, out, lse, out_lo = ctx.saved_tensors
-        plan, scale, softcap = ctx.meta
-        got = cp_attn_scored_bwd(q, k, v, out, lse, _dense(dout.to(q.dtype)), plan, scale,
-                                 softcap, slopes, rel_bias, out_lo=out_lo, grad_dtype=q.dtype)
-        # (a bias of another dtype than fp32 q, k, v gets its fp32 gradient rounded here)
-        grads = [g.to(x.dtype) if need else None
-                 for g, x, need in zip(got, (q, k, v, rel_bias), ctx.needs_input_grad)]
-        return (*grads, *([None] * (8 - len(grads))))
+        plan, scale, desc = ctx.meta
+        # saved tensors may have moved (offloaded and brought back)
+        desc.rel_bias = None if rel_bias is None else rel_bias.data_ptr()
+        desc.slopes = None if slopes is None else slopes.data_ptr()
+        got = scored._launch_bwd(desc, q, k, v, out, lse, _dense(dout), plan, scale, rel_bias,
+                                 None, None, out_lo, q.dtype)
+        need = ctx.needs_input_grad
+        dbias = got[3].to(rel_bias.dtype) if need[3] else None
+        return (*(g if n else None for g, n in zip(got[:3], need)), dbias, None, None, None, None)
 
 
 def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan: ScorePlan,
@@ -156,13 +159,19 @@ def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan:
                         slopes: Optional[torch.Tensor] = None,
                         rel_bias: Optional[torch.Tensor] = None):
     """Differentiable packed causal attention with modified scores (see
-    :func:`cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
+    :func:`~vlm_zigzag_head_gb300.cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
     bidirectional prefix.  q, k and v of any strides (copied where not contiguous).
     Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias``.  ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the
-    backward into a graph, call :func:`cp_attn_scored_bwd`, which involves no leaves."""
+    backward into a graph, call :func:`~vlm_zigzag_head_gb300.cp_attn_scored_bwd`, which involves no leaves."""
     if softmax_scale is None:
         softmax_scale = q.shape[-1] ** -0.5
     if slopes is not None and slopes.requires_grad:
         raise CpError(8, "slopes have no gradient here; a learned bias goes in rel_bias")
-    return CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan, float(softmax_scale),
-                                   float(softcap))
+    if not (q.is_cuda and k.is_cuda and v.is_cuda):
+        raise CpError(1, "tensors must live on a CUDA device")
+    scored._check(q, k, v, plan)
+    q, k, v = _dense(q), _dense(k), _dense(v)
+    desc = scored._scores(q, softcap, slopes, rel_bias)
+    if not _wants_grad(q, k, v, rel_bias):
+        return scored._launch_fwd(desc, q, k, v, plan, float(softmax_scale))
+    return CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan, float(softmax_scale), desc)

@@ -19,6 +19,27 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(device) -> int:
+    """The current stream's handle (without building a Stream object per call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+class _on_device:
+    """``torch.cuda.device``, free of charge where the device is current already."""
+
+    def __init__(self, device):
+        other = torch.cuda.current_device() != device.index
+        self._guard = torch.cuda.device(device) if other else None
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
 def _check_heads(x, name, like=None):
     if x.dim() != 3:
         raise CpError(2, "%s must be [T, heads, d]" % name)
@@ -106,13 +127,17 @@ def cp_qk_norm_rope_fwd(q, k, positions, q_weight=None, k_weight=None, eps: floa
     Returns contiguous ``(q_out, k_out)``."""
     f = _prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections,
                  interleaved, inv_freq)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    with torch.cuda.device(q.device):
+    return _launch_fwd(f, q, k, positions, q_weight, k_weight)
+
+
+def _launch_fwd(f, q, k, positions, q_weight, k_weight):
+    device = q.device
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=device)
+    with _on_device(device):
         _b.check(_b.lib().cp_qk_norm_rope_fwd(
-            ctypes.byref(f), q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight),
-            _at(k_weight), q_out.data_ptr(), k_out.data_ptr(),
-            torch.cuda.current_stream().cuda_stream))
+            f, q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight), _at(k_weight),
+            q_out.data_ptr(), k_out.data_ptr(), _raw_stream(device)))
     return q_out, k_out
 
 
@@ -130,18 +155,23 @@ def cp_qk_norm_rope_bwd(q, k, positions, dq_out, dk_out, q_weight=None, k_weight
         if g.shape != x.shape or g.dtype != x.dtype or g.device != x.device or \
                 not g.is_contiguous():
             raise CpError(2, "output gradients must be contiguous and match q and k")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    d = q.shape[2]
-    dqw, dkw = (None if w is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    return _launch_bwd(f, q, k, positions, dq_out, dk_out, q_weight, k_weight)
+
+
+def _launch_bwd(f, q, k, positions, dq_out, dk_out, q_weight, k_weight):
+    device, d = q.device, q.shape[2]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=device)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=device)
+    dqw, dkw = (None if w is None else torch.empty(d, dtype=torch.float32, device=device)
                 for w in (q_weight, k_weight))
-    with torch.cuda.device(q.device):
+    lib = _b.lib()
+    with _on_device(device):
         ws, nbytes = None, 0
         if dqw is not None or dkw is not None:
-            nbytes = _b.lib().cp_qk_norm_rope_bwd_workspace_size(ctypes.byref(f))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        _b.check(_b.lib().cp_qk_norm_rope_bwd(
-            ctypes.byref(f), q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight),
-            _at(k_weight), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-            _at(dqw), _at(dkw), _at(ws), nbytes, torch.cuda.current_stream().cuda_stream))
+            nbytes = lib.cp_qk_norm_rope_bwd_workspace_size(f)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _b.check(lib.cp_qk_norm_rope_bwd(
+            f, q.data_ptr(), k.data_ptr(), positions.data_ptr(), _at(q_weight), _at(k_weight),
+            dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _at(dqw),
+            _at(dkw), _at(ws), nbytes, _raw_stream(device)))
     return dq, dk, dqw, dkw

@@ -16,7 +16,7 @@ from typing import List, Optional, Sequence, Union
 import torch
 
 from . import CP_BF16, CpError, Workspace, _binding as _b, _dt, _need_cuda
-from .norm_rope import _at
+from .norm_rope import _at, _on_device, _raw_stream
 
 
 def relative_buckets(n_buckets: int, max_distance: int) -> List[int]:
@@ -68,16 +68,17 @@ class ScorePlan:
         with torch.cuda.device(device):
             # a blocking copy: the lists are on the device before any stream uses them
             self.dev = torch.frombuffer(self.host, dtype=torch.uint8).to(device)
-            self._stream = torch.cuda.current_stream(device)
+            self._stream = _raw_stream(device)
         self.device = device
+        self._at = self.dev.data_ptr()
         self._block = (ctypes.c_char * len(self.host)).from_buffer(self.host)
         self._sizes = {}   # workspace bytes by dtypes, KV heads, head size and scale
 
-    def _use(self, stream):
-        """The device copy, kept from reuse until ``stream`` is done with it."""
+    def _use(self, stream: int):
+        """The device copy, kept from reuse until ``stream``, the current one, is done with it."""
         if stream != self._stream and not torch.cuda.is_current_stream_capturing():
-            self.dev.record_stream(stream)
-        return self.dev.data_ptr()
+            self.dev.record_stream(torch.cuda.current_stream(self.device))
+        return self._at
 
     def _workspace_bytes(self, *shape):
         """Of the forward (dtype, KV heads, head size, scale), or with the gradients'
@@ -113,7 +114,7 @@ def build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix, rel_buckets,
     return host, int(cu[n])
 
 
-def _scores(q, plan, softcap, slopes, rel_bias):
+def _scores(q, softcap, slopes, rel_bias):
     s = _b.ScoreDesc()
     s.softcap = float(softcap)
     H = q.shape[1]
@@ -144,12 +145,8 @@ def _check(q, k, v, plan):
 
 
 def _like(t, shape, dtype, device, name):
-    """``t``, checked, or a new tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
         raise CpError(2, "%s has another shape, dtype or device" % name)
-    return t
 
 
 def _space(workspace, nbytes, device):
@@ -175,22 +172,35 @@ def cp_attn_scored_fwd(q, k, v, plan: ScorePlan, softmax_scale: float, softcap: 
     call takes one of its own, so calls on several streams may overlap."""
     _need_cuda(q, k, v, out, lse, out_lo)
     _check(q, k, v, plan)
+    T, H, _ = q.shape
+    if out is not None:
+        _like(out, q.shape, q.dtype, q.device, "out")
+    if lse is not None:
+        _like(lse, (H, T), torch.float32, q.device, "lse")
+    if out_lo is not None:
+        _like(out_lo, q.shape, q.dtype, q.device, "out_lo")
+    s = _scores(q, softcap, slopes, rel_bias)
+    return _launch_fwd(s, q, k, v, plan, float(softmax_scale), out, lse, workspace, residual,
+                       out_lo)
+
+
+def _launch_fwd(s, q, k, v, plan, scale, out=None, lse=None, workspace=None, residual=False,
+                out_lo=None):
+    """The forward on checked tensors."""
     T, H, d = q.shape
-    dt = _dt(q)
-    out = _like(out, q.shape, q.dtype, q.device, "out")
-    lse = _like(lse, (H, T), torch.float32, q.device, "lse")
-    if out_lo is not None or (residual and dt == CP_BF16):
-        out_lo = _like(out_lo, q.shape, q.dtype, q.device, "out_lo")
-    s = _scores(q, plan, softcap, slopes, rel_bias)
-    scale = float(softmax_scale)
-    with torch.cuda.device(q.device):
-        nbytes = plan._workspace_bytes(dt, k.shape[1], d, scale)
-        ws, ptr, size = _space(workspace, nbytes, q.device)
-        stream = torch.cuda.current_stream()
+    H_kv, device, dt = k.shape[1], q.device, _dt(q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=device)
+    if lse is None:
+        lse = torch.empty((H, T), dtype=torch.float32, device=device)
+    if out_lo is None and residual and dt == CP_BF16:
+        out_lo = torch.empty(q.shape, dtype=q.dtype, device=device)
+    with _on_device(device):
+        ws, ptr, size = _space(workspace, plan._workspace_bytes(dt, H_kv, d, scale), device)
+        stream = _raw_stream(device)
         _b.check(_b.lib().cp_attn_scored_fwd(
             plan._block, plan._use(stream), q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, T, H,
-            k.shape[1], d, ctypes.byref(s), scale, out.data_ptr(), lse.data_ptr(), _at(out_lo),
-            ptr, size, stream.cuda_stream))
+            H_kv, d, s, scale, out.data_ptr(), lse.data_ptr(), _at(out_lo), ptr, size, stream))
     return (out, lse, out_lo) if residual else (out, lse)
 
 
@@ -203,31 +213,38 @@ def cp_attn_scored_bwd(q, k, v, out, lse, dout, plan: ScorePlan, softmax_scale: 
     (dbias is then in rel_bias's dtype).  ``grads`` may supply dq, dk, dv."""
     _need_cuda(q, k, v, out, lse, dout, out_lo, *(grads or ()))
     _check(q, k, v, plan)
-    T, H, d = q.shape
-    dt = _dt(q)
+    T, H, _ = q.shape
     for t, name in ((out, "out"), (dout, "dout"), (out_lo, "out_lo")):
         if t is not None:
             _like(t, q.shape, q.dtype, q.device, name)
     _like(lse, (H, T), torch.float32, q.device, "lse")
-    dq, dk, dv = grads or (None, None, None)
-    dq = _like(dq, q.shape, grad_dtype, q.device, "dq")
-    dk = _like(dk, k.shape, grad_dtype, q.device, "dk")
-    dv = _like(dv, k.shape, grad_dtype, q.device, "dv")
-    gdt = _dt(dq)
-    s = _scores(q, plan, softcap, slopes, rel_bias)
-    dbias, bdt = None, gdt
+    for t, x, name in zip(grads or (), (q, k, v), ("dq", "dk", "dv")):
+        _like(t, x.shape, grad_dtype, q.device, name)
+    s = _scores(q, softcap, slopes, rel_bias)
+    got = _launch_bwd(s, q, k, v, out, lse, dout, plan, float(softmax_scale), rel_bias,
+                      workspace, grads, out_lo, grad_dtype)
+    return got if rel_bias is not None else got[:3]
+
+
+def _launch_bwd(s, q, k, v, out, lse, dout, plan, scale, rel_bias, workspace, grads, out_lo,
+                grad_dtype):
+    """The backward on checked tensors; dbias is None without a bias."""
+    T, H, d = q.shape
+    H_kv, device, dt = k.shape[1], q.device, _dt(q)
+    dq, dk, dv = grads or (torch.empty(x.shape, dtype=grad_dtype, device=device)
+                           for x in (q, k, v))
+    gdt = bdt = _dt(dq)
+    dbias = None
     if rel_bias is not None:
-        dbias = torch.empty(rel_bias.shape, device=q.device, dtype=torch.float32
+        dbias = torch.empty(rel_bias.shape, device=device, dtype=torch.float32
                             if grad_dtype == torch.float32 else rel_bias.dtype)
         bdt = _dt(dbias)
-    scale = float(softmax_scale)
-    with torch.cuda.device(q.device):
-        nbytes = plan._workspace_bytes(dt, k.shape[1], d, scale, gdt)
-        ws, ptr, size = _space(workspace, nbytes, q.device)
-        stream = torch.cuda.current_stream()
+    with _on_device(device):
+        ws, ptr, size = _space(workspace, plan._workspace_bytes(dt, H_kv, d, scale, gdt), device)
+        stream = _raw_stream(device)
         _b.check(_b.lib().cp_attn_scored_bwd(
             plan._block, plan._use(stream), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            out.data_ptr(), _at(out_lo), lse.data_ptr(), dout.data_ptr(), dt, T, H, k.shape[1], d,
-            ctypes.byref(s), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), gdt, _at(dbias),
-            bdt, ptr, size, stream.cuda_stream))
-    return (dq, dk, dv) if dbias is None else (dq, dk, dv, dbias)
+            out.data_ptr(), _at(out_lo), lse.data_ptr(), dout.data_ptr(), dt, T, H, H_kv, d, s,
+            scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), gdt, _at(dbias), bdt, ptr, size,
+            stream))
+    return dq, dk, dv, dbias
