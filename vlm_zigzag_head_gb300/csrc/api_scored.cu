@@ -62,7 +62,9 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
     *at = o;
     if (need) o = up256(o + bytes);
   };
-  take(&w.scales, f16, sizeof(OpScales));
+  // a learned bias's gradient wants a more exact forward (below): V's f16 copy too
+  const bool v16 = f16 || (dt == CP_BF16 && h.n_dist > 0 && !backward);
+  take(&w.scales, f16 || v16, sizeof(OpScales));
   take(&w.dtable, backward && h.n_dist > 0, (size_t)h.H * h.n_dist * sizeof(float));
   take(&w.dq, backward && bf16_grads, T * h.H * d * sizeof(float));
   take(&w.dk, backward && bf16_grads, T * Hkv * d * sizeof(float));
@@ -70,7 +72,7 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
   take(&w.table, h.n_dist > 0, (size_t)h.H * table_pitch(h.n_dist) * sizeof(float));
   if (!backward) {
     const size_t parts = dt == CP_F32 ? f32_fwd_splits(h) : 1;
-    take(&w.v16, f16, T * Hkv * d * 2);
+    take(&w.v16, v16, T * Hkv * d * 2);
     take(&w.part_out, parts > 1, parts * T * h.H * d * sizeof(float));
     take(&w.part_lse, parts > 1, parts * T * h.H * sizeof(float));
   } else {
@@ -316,9 +318,14 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
                  "merge of partial results");
     return CP_OK;
   }
+  // PV on f16 operands above softmax scale 0.25, as cp_attn_fwd; and, where a
+  // backward will follow (out_lo), with a learned bias: its gradient is a sum of dS =
+  // P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  P in bf16
+  // leaves 2.4e-3 to 3.7e-3 on dbias, P in f16 1.7e-3, mostly its own rounding.
+  const bool f16 = c.f16 || (c.bias == SCORE_TABLE && out_lo != nullptr);
   const void* vsrc = v;
   OpScales* sc = reinterpret_cast<OpScales*>(w + c.ws.scales);
-  if (c.f16) {   // PV on f16 operands: V's scaled copy
+  if (f16) {   // V's scaled copy
     const int64_t n = (int64_t)T * Hkv * d;
     void* v16 = w + c.ws.v16;
     ProfileScope prof(1, st, 2);
@@ -330,7 +337,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   const char* terr = nullptr;
   if (!make_tmap_thd(&a.tm_q_nat, q, T, H, d, 128, &terr) ||
       !make_tmap_thd(&a.tm_k_nat, k, T, Hkv, d, 128, &terr) ||
-      !make_tmap_thd(&a.tm_v_nat, vsrc, T, Hkv, d, 128, &terr, c.f16))
+      !make_tmap_thd(&a.tm_v_nat, vsrc, T, Hkv, d, 128, &terr, f16))
     return entry_fail(CP_ERR_CUDA, std::string("tensor map: ") + (terr ? terr : "?"));
   a.tm_q_text = a.tm_q_nat;   // no run of these plans is rank-local
   a.tm_k_text = a.tm_k_nat;
@@ -346,8 +353,8 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   a.Hkv = Hkv;
   a.d = d;
   a.scale_log2 = scale * kLog2e;
-  a.f16_pv = c.f16 ? 1 : 0;
-  a.op_scales = c.f16 ? sc : nullptr;
+  a.f16_pv = f16 ? 1 : 0;
+  a.op_scales = f16 ? sc : nullptr;
   a.out = out;
   a.lse = lse;
   a.T = T;

@@ -221,10 +221,13 @@ __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4
 // what dS multiplies: P, or under a cap -P (1 - tanh^2), whose sign the factors of
 // dQ and dK undo.  kFast: every pair is
 // visible, the cap's polynomial holds and the bias is linear along the queries.
+// With a cap and a table, ph: P alone as f16 pairs, for the bias's gradient (2^-12 of
+// the value where registers for fp32 are lacking; bf16 pairs would show in it).
 // mul: scale or cap in log2 units, inv its inverse.  x0: the half's first query in
 // the 64; ld: its lse2.
 template <bool kCap, int kBias, bool kFast>
-__device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, int x0, float mul,
+__device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t (&pk)[16],
+                                              uint32_t* ph, int x0, float mul,
                                               float inv, const score::Cap<kCap, true>& cap,
                                               const score::TileBias& tb, bool poly,
                                               const float* ld, bool vec, int first_vis,
@@ -267,6 +270,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t* pk, 
         if (x0 + y + 1 < first_vis || x0 + y + 1 >= end_vis) p1 = 0.f;
       }
       pk[y / 2] = pack_bf16x2(p0, p1);
+      if constexpr (kCap && kBias == SCORE_TABLE) ph[y / 2] = pack_f16x2(p0, p1);
       if constexpr (kCap) unpack2(mul2(pack2(p0, p1), w), p0, p1);   // -P (1 - tanh^2)
       rs[y] = __float_as_uint(p0);
       rs[y + 1] = __float_as_uint(p1);
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- P^T: probabilities of the 64 queries, computed in place over S and
       // kept in fp32 for dS; bf16 pairs into the first 32 of this warpgroup's
       // S columns, in halves
-      uint32_t pk[2][16];   // P^T as bf16 pairs, 32 queries each
+      uint32_t ph[2][16];   // P^T as f16 pairs (cap and table), 32 queries each
       const bool poly = in_poly_range<kCap>(rs, cap);
       auto p_tile = [&](auto fast) {
         constexpr bool kFast = decltype(fast)::value;
@@ -775,9 +779,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < 2; ++h) {
           score::TileBias th = tb;
           th.base += 32 * h * tb.step;
-          score_columns<kCap, kBias, kFast>(rs[h], pk[h], 32 * h, s_mul, s_inv, cap, th, poly,
+          uint32_t pk[16];   // P^T as bf16 pairs
+          score_columns<kCap, kBias, kFast>(rs[h], pk, ph[h], 32 * h, s_mul, s_inv, cap, th, poly,
                                             ld + 32 * h, vec, first_vis, end_vis);
-          tmem_st16(tmem + lane_off + kColS + g * 64 + 16 * h, pk[h]);
+          tmem_st16(tmem + lane_off + kColS + g * 64 + 16 * h, pk);
         }
       };
       if (whole && poly && !tb.both && tb.tab == nullptr) p_tile(std::true_type{});
@@ -813,10 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            __uint_as_float(rs[h][x + y + 1])), diff);
             if constexpr (kBias == SCORE_TABLE) {
               uint64_t b = ds;
-              if constexpr (kCap) {   // the bias is added behind the cap: P alone, from P^T
-                const uint32_t p2 = pk[h][(x + y) / 2];
-                b = mul2(pack2(__uint_as_float(p2 << 16), __uint_as_float(p2 & 0xffff0000u)),
-                         diff);
+              if constexpr (kCap) {   // the bias is added behind the cap: P alone
+                float p0, p1;
+                unpack_f16x2(ph[h][(x + y) / 2], p0, p1);
+                b = mul2(pack2(p0, p1), diff);
               }
               if constexpr (kNear) {
                 float b0, b1;
