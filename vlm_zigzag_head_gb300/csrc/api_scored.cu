@@ -407,15 +407,19 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   float* dq = static_cast<float*>(dq_out);
   float* dk = static_cast<float*>(dk_out);
   float* dv = static_cast<float*>(dv_out);
-  if (bf16_grads) {
-    dq = reinterpret_cast<float*>(w + c.ws.dq);
-    dk = reinterpret_cast<float*>(w + c.ws.dk);
-    dv = reinterpret_cast<float*>(w + c.ws.dv);
-  }
   const int kv_split = c.bf16 ? bwd_kv_split(c.h->n_bwd, H, Hkv, sms) : 1;
   const int f32_split = c.bf16 ? 1 : f32_splits((int64_t)c.h->n_tiles * H, c.h->max_walk, sms);
   const bool add_dq = c.bf16 || f32_split > 1;
   const bool add_dkdv = c.bf16 ? kv_split > 1 : f32_split > 1 || H > Hkv;
+  // (dK and dV of whole groups come out of the tensor cores complete: straight to bf16)
+  const bool bf16_dkdv = bf16_grads && !add_dkdv;
+  if (bf16_grads) {
+    dq = reinterpret_cast<float*>(w + c.ws.dq);
+    if (add_dkdv) {
+      dk = reinterpret_cast<float*>(w + c.ws.dk);
+      dv = reinterpret_cast<float*>(w + c.ws.dv);
+    }
+  }
   const size_t zero = !bf16_grads ? c.ws.dq : add_dkdv ? c.ws.table : c.ws.dk;
   ENTRY_CUDA(cudaMemsetAsync(w, 0, zero, st), "clear status and sums");
   if (!bf16_grads && add_dq)
@@ -486,6 +490,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;
+    a.dkv_bf16 = bf16_dkdv ? 1 : 0;
     a.status = reinterpret_cast<int32_t*>(w);
     a.wait_limit = device_wait_limit();
     a.kv_split = kv_split;
@@ -500,7 +505,8 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   if (bf16_grads) {
     const float* const src[3] = {dq, dk, dv};
     void* const dst[3] = {dq_out, dk_out, dv_out};
-    const int64_t n[3] = {(int64_t)T * H * d, (int64_t)T * Hkv * d, (int64_t)T * Hkv * d};
+    const int64_t nkv = bf16_dkdv ? 0 : (int64_t)T * Hkv * d;
+    const int64_t n[3] = {(int64_t)T * H * d, nkv, nkv};
     ENTRY_CUDA(launch_cast_bf16(src, dst, n, sms, st), "bf16 gradients");
   }
   if (dbias)

@@ -27,11 +27,12 @@ __global__ void __launch_bounds__(kThreads)
 
 // One block per head, one warp per bucket at a time; lanes take the distances
 // 32 apart and meet in a fixed order.
-__global__ void __launch_bounds__(kThreads)
+constexpr int kReduceThreads = 1024;
+__global__ void __launch_bounds__(kReduceThreads)
     reduce_dbias_kernel(const float* dtable, const int32_t* buckets, int n_dist, int n_buckets,
                         void* dbias, int bf16) {
   const int h = blockIdx.x, lane = threadIdx.x & 31;
-  for (int b = threadIdx.x >> 5; b < n_buckets; b += kThreads / 32) {
+  for (int b = threadIdx.x >> 5; b < n_buckets; b += kReduceThreads / 32) {
     float v = 0.f;
     for (int t = lane; t < n_dist; t += 32)
       if (buckets[t] == b) v += dtable[(int64_t)h * n_dist + t];
@@ -77,7 +78,7 @@ cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3]
   }
   const int64_t want = (most + 4 * kThreads - 1) / (4 * kThreads), cap = 8LL * sms;
   const unsigned blocks = (unsigned)(want < 1 ? 1 : want < cap ? want : cap);
-  cast_bf16_kernel<<<dim3(blocks, 3), kThreads, 0, st>>>(c);
+  cast_bf16_kernel<<<dim3(blocks, n[1] > 0 || n[2] > 0 ? 3 : 1), kThreads, 0, st>>>(c);
   return cudaGetLastError();
 }
 
@@ -91,7 +92,7 @@ cudaError_t launch_expand_bias(const void* bias, bool bf16, int64_t stride_h, in
 
 cudaError_t launch_reduce_dbias(const float* dtable, const int32_t* buckets, int n_dist,
                                 int n_buckets, int H, void* dbias, bool bf16, cudaStream_t st) {
-  reduce_dbias_kernel<<<H, kThreads, 0, st>>>(dtable, buckets, n_dist, n_buckets, dbias,
+  reduce_dbias_kernel<<<H, kReduceThreads, 0, st>>>(dtable, buckets, n_dist, n_buckets, dbias,
                                               bf16 ? 1 : 0);
   return cudaGetLastError();
 }

@@ -92,6 +92,7 @@ struct TcBwdArgs {
   float scale, scale_log2;
   int64_t T;
   float* dq; float* dk; float* dv;
+  int dkv_bf16;               // dk, dv point to bf16 (scored plans, kv_split 1)
   float* pre_k; float* pre_v; int64_t pre_rows;
   int32_t* status;
   long long wait_limit;

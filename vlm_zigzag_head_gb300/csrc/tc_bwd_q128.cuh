@@ -896,6 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long row = (long long)it.slot * a.pre_rows + it.dk_row0 + u;
         dst = (g == 0 ? a.pre_k : a.pre_v) + (row * a.Hkv + hk) * D;
       }
+      __nv_bfloat16* dst16 =
+          reinterpret_cast<__nv_bfloat16*>(g == 0 ? a.dk : a.dv) +
+          ((long long)(it.k_row0 + u) * a.Hkv + hk) * D;   // dkv_bf16: DK_TEXT items only
       const bool first = (it.flags & F_FIRST) != 0;
       const float dk_scale = kCap ? -a.scale : a.scale;
       const float mul = g == 0 ? (kF16 ? dk_scale * a.op_scales->dk_mul : dk_scale) : 1.f;
@@ -916,6 +919,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 32; x += 4) {
           float4 v = make_float4(__uint_as_float(r[x]) * mul, __uint_as_float(r[x + 1]) * mul,
                                  __uint_as_float(r[x + 2]) * mul, __uint_as_float(r[x + 3]) * mul);
+          if (a.dkv_bf16) {
+            *reinterpret_cast<uint2*>(dst16 + c * 32 + x) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            continue;
+          }
           float4* d4 = reinterpret_cast<float4*>(dst + c * 32 + x);
           if (kShared && (!kScored || a.kv_split > 1)) {   // sub-CTAs of one group meet here (zeroed first)
             red_add_v4(d4, v);
