@@ -238,3 +238,23 @@ def test_python_refusals_on_device():
         with pytest.raises(CpError):
             call()
             pytest.fail("call %d was not refused" % i)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["fused", "heads", "odd"])
+def test_saved_tensors_that_come_back_with_other_strides(layout):
+    """Offloading keeps contiguous copies of the strided q and k: the backward reads those."""
+    from vlm_zigzag_head_gb300.autograd import qk_norm_rope
+    q, k, pos, qw, kw, dqo, dko = _inputs(19, 4, 2, 64, torch.bfloat16, layout, 2, axes=2)
+    leaves = [t.detach().requires_grad_(True) for t in (q, k, qw, kw)]
+    sections = [20, 12]
+
+    def run():
+        qo, ko = qk_norm_rope(leaves[0], leaves[1], pos, leaves[2], leaves[3], sections=sections)
+        return qo, ko
+    want = torch.autograd.grad(run(), leaves, (dqo, dko))
+    with torch.autograd.graph.save_on_cpu():
+        outs = run()
+    sections.clear()   # the options are those of the forward
+    got = torch.autograd.grad(outs, leaves, (dqo, dko))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

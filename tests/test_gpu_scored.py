@@ -451,3 +451,26 @@ def test_wait_that_gives_up_is_reported():
         cp_set_wait_limit(0)
     cp_attn_scored_fwd(q, k, v, plan, R128, softcap=5.0, workspace=ws)
     assert cp_workspace_status(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["slopes", "bias"])
+def test_saved_tensors_that_come_back_with_other_strides(kind):
+    """Offloading moves what the backward needs and keeps contiguous copies: a transposed bias too."""
+    from vlm_zigzag_head_gb300 import ScorePlan
+    from vlm_zigzag_head_gb300.autograd import cp_attention_scored
+    H, d, T = 3, 64, 75
+    plan = ScorePlan([0, 40, T], H, rel_buckets=[0, 1, 2, 2, 3], device=DEV)
+    q, k, v, dout = (x.to(DEV) for x in _inputs(T, H, H, d, "f32", 7))
+    leaves = [x.requires_grad_(True) for x in (q, k, v)]
+    opt = dict(slopes=torch.tensor([0.5, 0.25, 0.1], device=DEV))
+    if kind == "bias":
+        bias = torch.randn(4, H, device=DEV, generator=torch.Generator(DEV).manual_seed(2)).t().requires_grad_(True)
+        leaves.append(bias)
+        opt = dict(rel_bias=bias)
+    want = torch.autograd.grad(cp_attention_scored(q, k, v, plan, **opt)[0], leaves, dout)
+    with torch.autograd.graph.save_on_cpu():
+        out, _ = cp_attention_scored(q, k, v, plan, **opt)
+    got = torch.autograd.grad(out, leaves, dout)
+    # equal up to the order of the atomic sums
+    assert all((a - b).norm() <= 1e-5 * b.norm() for a, b in zip(got, want))

@@ -90,12 +90,13 @@ def _wants_grad(*tensors) -> bool:
 
 
 class QKNormRope(torch.autograd.Function):
-    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, desc)``."""
+    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, options)``."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, q_weight, k_weight, desc):
+    def forward(ctx, q, k, positions, q_weight, k_weight, options):
         ctx.save_for_backward(q, k, positions, q_weight, k_weight)
-        ctx.desc = desc
+        ctx.options = options
+        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
 
     @staticmethod
@@ -103,7 +104,9 @@ class QKNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dq, dk, dqw, dkw = norm_rope._launch_bwd(ctx.desc, q, k, positions, _dense(dq_out),
+        # saved tensors may come back with other strides (offloaded, recomputed)
+        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *ctx.options)
+        dq, dk, dqw, dkw = norm_rope._launch_bwd(desc, q, k, positions, _dense(dq_out),
                                                  _dense(dk_out), q_weight, k_weight)
         return (dq if need[0] else None, dk if need[1] else None, None,
                 dqw.to(q_weight.dtype) if need[3] else None,
@@ -119,11 +122,13 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     """Differentiable :func:`~vlm_zigzag_head_gb300.cp_qk_norm_rope_fwd`: RMS norm of every head of q and k
     and the position rotation, in one pass.  Returns contiguous ``(q_out, k_out)``,
     ready for :func:`cp_attention`; gradients flow to q, k and the weights."""
-    desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, eps, theta, rot_dim, sections,
-                              interleaved, inv_freq)
+    sections = None if sections is None else tuple(sections)
+    inv_freq = None if inv_freq is None else tuple(inv_freq)
+    options = (eps, theta, rot_dim, sections, interleaved, inv_freq)
     if not _wants_grad(q, k, q_weight, k_weight):
+        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
-    return QKNormRope.apply(q, k, positions, q_weight, k_weight, desc)
+    return QKNormRope.apply(q, k, positions, q_weight, k_weight, options)
 
 
 class CPAttentionScored(torch.autograd.Function):
@@ -135,7 +140,7 @@ class CPAttentionScored(torch.autograd.Function):
         # the bf16 remainder of the output keeps D = dO.O exact in the backward
         out, lse, out_lo = scored._launch_fwd(desc, q, k, v, plan, softmax_scale, residual=True)
         ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, out_lo)
-        ctx.meta = (plan, softmax_scale, desc)
+        ctx.meta = (plan, softmax_scale, desc.softcap)
         ctx.mark_non_differentiable(lse)
         return out, lse
 
@@ -143,10 +148,12 @@ class CPAttentionScored(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout, _dlse):
         q, k, v, rel_bias, slopes, out, lse, out_lo = ctx.saved_tensors
-        plan, scale, desc = ctx.meta
-        # saved tensors may have moved (offloaded and brought back)
-        desc.rel_bias = None if rel_bias is None else rel_bias.data_ptr()
-        desc.slopes = None if slopes is None else slopes.data_ptr()
+        plan, scale, softcap = ctx.meta
+        # saved tensors may come back elsewhere and with other strides (offloaded, recomputed)
+        q, k, v, out, lse = (_dense(x) for x in (q, k, v, out, lse))
+        out_lo = None if out_lo is None else _dense(out_lo)
+        scored._check(q, k, v, plan)
+        desc = scored._scores(q, softcap, slopes, rel_bias)
         got = scored._launch_bwd(desc, q, k, v, out, lse, _dense(dout), plan, scale, rel_bias,
                                  None, None, out_lo, q.dtype)
         need = ctx.needs_input_grad
@@ -161,8 +168,9 @@ def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan:
     """Differentiable packed causal attention with modified scores (see
     :func:`~vlm_zigzag_head_gb300.cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
     bidirectional prefix.  q, k and v of any strides (copied where not contiguous).
-    Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias``.  ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the
-    backward into a graph, call :func:`~vlm_zigzag_head_gb300.cp_attn_scored_bwd`, which involves no leaves."""
+    Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias``.
+    ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the backward into a graph, call
+    :func:`~vlm_zigzag_head_gb300.cp_attn_scored_bwd`, which involves no leaves."""
     if softmax_scale is None:
         softmax_scale = q.shape[-1] ** -0.5
     if slopes is not None and slopes.requires_grad:
