@@ -258,3 +258,27 @@ def test_saved_tensors_that_come_back_with_other_strides(layout):
     sections.clear()   # the options are those of the forward
     got = torch.autograd.grad(outs, leaves, (dqo, dko))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_offsets_past_32_bits(dtype):
+    """The last rows of tensors with more than 2^31 elements get the bits that they get alone."""
+    from vlm_zigzag_head_gb300 import cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd
+    H, d, n = 64, 64, 70
+    T = 2 ** 31 // (H * d) + n
+    x = torch.zeros((T, H + 1, d), dtype=dtype, device=DEV)
+    tail = torch.randn((n, H + 1, d), device=DEV, generator=torch.Generator(DEV).manual_seed(3)).to(dtype)
+    x[-n:] = tail
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    w = torch.linspace(0.5, 1.5, d, device=DEV)
+    ends = []
+    for y, p in ((x, pos), (tail, pos[-n:].contiguous())):
+        q, k = y[:, :H], y[:, H:]
+        qo, ko = cp_qk_norm_rope_fwd(q, k, p, w, w)
+        dq, dk, dw, _ = cp_qk_norm_rope_bwd(q, k, p, qo, ko, w, w)
+        ends.append([t[-n:].clone() for t in (qo, ko, dq, dk)])
+        assert torch.isfinite(dw).all()
+    assert all(torch.equal(a, b) for a, b in zip(*ends))
+    del x, y, q, k, qo, ko, dq, dk
+    torch.cuda.empty_cache()

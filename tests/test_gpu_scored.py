@@ -474,3 +474,61 @@ def test_saved_tensors_that_come_back_with_other_strides(kind):
     got = torch.autograd.grad(out, leaves, dout)
     # equal up to the order of the atomic sums
     assert all((a - b).norm() <= 1e-5 * b.norm() for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(dtype):
+    """The last sample of tensors with more than 2^31 elements gets the bits that it gets alone
+    (two key tiles at most add to a row of dq, and two addends have one sum)."""
+    from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    H, d, n, m = 64, 64, 120, 512
+    before = 2 ** 31 // (H * d)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(DEV).manual_seed(3)
+    tails = [torch.randn((n, H, d), device=DEV, generator=g).to(dt) for _ in range(4)]
+    slopes = torch.linspace(0.01, 0.5, H, device=DEV)
+    ends = []
+    for T in (before + n, n):
+        plan = ScorePlan(list(range(0, T - n + 1, m)) + [T], H, device=DEV)
+        x = [torch.zeros((T, H, d), dtype=dt, device=DEV) for _ in range(4)]
+        for a, b in zip(x, tails):
+            a[-n:] = b
+        out, lse, lo = cp_attn_scored_fwd(*x[:3], plan, R64, slopes=slopes, residual=True)
+        got = cp_attn_scored_bwd(*x[:3], out, lse, x[3], plan, R64, slopes=slopes, out_lo=lo, grad_dtype=dt)
+        ends.append([t[-n:].clone() for t in (out, lse.t(), *got)])
+    for a, b in zip(*ends):
+        assert torch.isfinite(a).all()
+        if dtype == "bf16":
+            assert torch.equal(a, b)
+        else:   # the walk of the sample alone may be shared between blocks
+            assert (a - b).norm() <= 1e-5 * b.norm()
+    del x, out, lse, lo, got, plan
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+def test_small_gradients_beside_a_sample_that_is_not_finite(bias):
+    """f16 operands are scaled by their tensor's largest finite value: gradients of 1e-7 beside a
+    sample of NaN and infinities equal those beside a finite one."""
+    from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    cu, H, d = [0, 140, 210, 300], 2, 64
+    plan = ScorePlan(cu, H, rel_buckets=[0, 1, 2], device=DEV)
+    opt = dict(rel_bias=torch.randn(H, 3, device=DEV, generator=torch.Generator(DEV).manual_seed(1))) if bias else {}
+    clean = [x.to(DEV) for x in _inputs(cu[-1], H, 1, d, "bf16", 8)]
+    for x, f in zip(clean, (1e-2, 1e-2, 1e-6, 1e-7)):
+        x *= f
+    dirty = [x.clone() for x in clean]
+    for x in clean:
+        x[140:210] = 0
+    for i, x in enumerate(dirty):
+        x[140:210] = float("nan")
+        x[140 + i:210:9] = float("-inf")
+    ends = []
+    for x in (clean, dirty):
+        out, lse, lo = cp_attn_scored_fwd(*x[:3], plan, 1.0, residual=True, **opt)
+        got = cp_attn_scored_bwd(*x[:3], out, lse, x[3], plan, 1.0, out_lo=lo, **opt)
+        ends.append([torch.cat([t[:140], t[210:]]).float() for t in (out, lse.t(), *got[:3])])
+    for a, b in zip(*ends):
+        assert a.norm() > 0 and (a - b).norm() <= 1e-5 * a.norm()
