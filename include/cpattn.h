@@ -428,7 +428,8 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  * j is visible to i in the same sample when j <= i, or when both lie in a
  * bidirectional prefix.  rel_bias entries at or below -1e37 (the type's lowest
  * value, minus infinity) hide the pair; a row that sees no key has out 0, lse
- * -inf and no gradient.  Entries and slopes are otherwise finite.  A NaN or
+ * -inf and no gradient.  Entries and slopes are otherwise finite; a slope adds up
+ * to 2e-5 of itself to the rounding of a score.  A NaN or
  * infinity in q, k, v or dout stays within its sample; there it may reach every
  * row of the 128-row tiles that hold it, before the causal mask's rows too.
  * softmax_scale lies in [1e-10, 1e10].
@@ -437,8 +438,10 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  *                cp_attn_fwd_gqa / cp_attn_bwd_gqa, with T and H those of the plan
  *   grad_dtype   of dq, dk, dv: CP_F32, or CP_BF16 with bf16 inputs (summed in
  *                fp32 in the workspace, rounded once)
- *   dt           CP_BF16: tensor cores (f16 operands above softmax_scale 0.25, as
- *                cp_attn_fwd); CP_F32: CUDA cores, fp32 throughout
+ *   dt           CP_BF16: tensor cores; CP_F32: CUDA cores, fp32 throughout.  Above
+ *                softmax_scale 0.25 (as cp_attn_fwd), and in a forward with rel_bias
+ *                and out_lo, bf16 operands become f16, scaled by their tensor's largest
+ *                finite magnitude: values below 2^-28 of it lose bits, below 2^-40 all
  *   score        slopes: NULL or device [H] fp32.  rel_bias: NULL or device, H x
  *                n_buckets, any strides (in elements).  softcap: 0 or in
  *                [1e-3, 1e4].  slopes and rel_bias exclude one another.
@@ -542,6 +545,9 @@ cp_status_t cp_plan_unit_lists(const int32_t* cu_seqlens_h, int n_seqs, int pref
  *   0 zigzag index   1 zigzag gather   2 tensor-core forward (ring steps)
  *   3 backward preprocess   4 tensor-core backward (ring steps)
  *   5 prefix-gradient sum   6 CUDA-core forward step   7 CUDA-core backward step
+ * The scored attention counts its kernels among these (1: f16 copy of V; 2, 3, 4,
+ * 6, 7) without the ones that move its bias and gradients; cp_qk_norm_rope_* is
+ * not recorded.
  * Errors: CP_ERR_CUDA.
  */
 void cp_profile_begin(void);

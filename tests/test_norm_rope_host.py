@@ -73,3 +73,11 @@ def test_python_refusals():
         cp_qk_norm_rope_fwd(x, x, torch.zeros(4, dtype=torch.int32))
     with pytest.raises(CpError):
         cp_qk_norm_rope_fwd(x[0], x, torch.zeros(4, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("pos_shape", [(), (3,), (1, 4, 1), (0, 4), (5, 4)])
+def test_position_shapes(pos_shape):
+    from vlm_zigzag_head_gb300 import norm_rope
+    with pytest.raises(CpError):
+        norm_rope._desc(1, (4, 2, 64), (128, 64, 1), (4, 1, 64), (64, 64, 1), pos_shape, 0, 1e-6, 1e4, None, None,
+                        False, None)

@@ -123,3 +123,9 @@ def test_python_refuses_cpu_tensors():
     q = torch.zeros(4, 2, 64)
     with pytest.raises(CpError):
         cp_attn_scored_fwd(q, q, q, None, 0.125)
+
+
+def test_more_heads_than_a_grid_holds(cplib):
+    assert build_plan([0, 5], 65535, 0, False, None, 152)[1] == 5
+    with pytest.raises(CpError):
+        build_plan([0, 5], 65536, 0, False, None, 152)

@@ -320,8 +320,9 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   }
   // PV on f16 operands above softmax scale 0.25, as cp_attn_fwd; and, where a
   // backward will follow (out_lo), with a learned bias: its gradient is a sum of dS =
-  // P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  P in bf16
-  // leaves 2.4e-3 to 3.7e-3 on dbias, P in f16 1.7e-3, mostly its own rounding.
+  // P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  Before its
+  // own rounding dbias is off by 1e-3 to 3e-3 (relative) with P in bf16, by 1e-4 to
+  // 2e-4 with P in f16.
   const bool f16 = c.f16 || (c.bias == SCORE_TABLE && out_lo != nullptr);
   const void* vsrc = v;
   OpScales* sc = reinterpret_cast<OpScales*>(w + c.ws.scales);

@@ -42,7 +42,7 @@ struct F32Args {
 };
 // Blocks along a walk of up to `walk` tiles: as many as keep two tiles each and
 // the launch within two blocks per SM.  (768 tokens, 8 heads over 2, d = 128, one
-// block per walk against six: forward 168 -> 67 us, backward 1201 -> 333 us.)
+// block per walk against six: forward 168 -> 117 us, backward 1201 -> 276 us.)
 inline int f32_splits(int64_t blocks, int walk, int sms) {
   int64_t s = 2LL * sms / (blocks > 0 ? blocks : 1);
   if (s > walk / 2) s = walk / 2;

@@ -31,7 +31,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   char buf[160];
   if (!cu) return "cu_seqlens is NULL";
   if (n_seqs < 1) return "n_seqs must be >= 1";
-  if (H < 1) return "H must be >= 1";
+  if (H < 1 || H > 65535) return "H must be in [1, 65535]";
   if (sms < 1) return "n_sms must be >= 1";
   if (cu[0] != 0) return "cu_seqlens[0] must be 0";
   if (n_dist < 0 || n_dist > kMaxDist) return "n_dist must be in [0, 65536]";

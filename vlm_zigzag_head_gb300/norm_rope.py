@@ -61,7 +61,7 @@ def _desc(dtype, q_shape, q_stride, k_shape, k_stride, pos_shape, w_dtype, eps, 
     rot = d if rot_dim is None else int(rot_dim)
     if rot < 0 or rot > d or rot % 16:
         raise CpError(2, "rot_dim must be a multiple of 16 in [0, head_dim]")
-    axes = 1 if len(pos_shape) == 1 else pos_shape[0]
+    axes = pos_shape[0] if len(pos_shape) == 2 else 1
     if len(pos_shape) not in (1, 2) or pos_shape[-1] != T or not 1 <= axes <= 4:
         raise CpError(2, "positions must be [T] or [axes, T] with at most 4 axes")
     if sections is None:
