@@ -399,7 +399,9 @@ cp_status_t cp_qk_norm_rope_bwd(const cp_norm_rope_t* desc, const void* q, const
  *   bidirectional  nonzero: prefix tokens see the whole prefix of their sample
  *                  instead of the causal part (CP-VLM page section 2's layout
  *                  [image tokens, text tokens]; the page's own mask is causal)
- *   n_sms          multiprocessors of the device that will run the calls
+ *   n_sms          multiprocessors of the device that will run the calls (at most
+ *                  4096): with few heads and samples long runs are cut into parts
+ *                  for them
  *   buckets_h      NULL or HOST [n_dist]: bucket of distance 0 .. n_dist - 1 of
  *                  a learned bias; larger distances take the last entry's
  * cp_score_plan_size returns 0 on bad arguments (cp_last_error says why);
@@ -450,8 +452,9 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  *                aligned, of this call's own while it runs; its status word is
  *                read by cp_workspace_status
  * Every call is launches and memsets alone (no copy from the host), so it can
- * be captured into a graph.  dQ, dbias and, with few work items and grouped
- * heads, dK and dV are summed by fp32 atomics: their last bits vary from run to run.
+ * be captured into a graph.  dQ, dbias and, where few heads and tiles leave SMs
+ * to share a key tile, dK and dV are summed by fp32 atomics: their last bits
+ * vary from run to run.  The forward's bits do not.
  * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE, CP_ERR_DTYPE, CP_ERR_ALIGNMENT,
  * CP_ERR_WORKSPACE, CP_ERR_CUDA, CP_ERR_UNSUPPORTED.
  */

@@ -532,3 +532,85 @@ def test_small_gradients_beside_a_sample_that_is_not_finite(bias):
         ends.append([torch.cat([t[:140], t[210:]]).float() for t in (out, lse.t(), *got[:3])])
     for a, b in zip(*ends):
         assert a.norm() > 0 and (a - b).norm() <= 1e-5 * a.norm()
+
+
+CUT = [   # one or two heads: runs of more than three tiles are cut into parts
+    ([1500], 0, False, 1, 1, 64, R64, 0.0, "slopes"),
+    ([1111, 130], 0, False, 2, 1, 128, R128, 20.0, None),
+    ([1300, 77], [300, 77], True, 2, 2, 64, R64, 0.0, (32, 1000)),
+    ([1200], 700, True, 1, 1, 128, R128, 5.0, "slopes"),
+    ([1025, 0, 1], [1, 0, 1], True, 3, 1, 64, 1.0, 4.0, (8, 32)),      # f16 operands
+    ([1400], 0, False, 1, 1, 128, R128, 0.0, (8, 16)),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,prefix,both,H,Hkv,d,scale,cap,kind", CUT)
+def test_cut_runs_match_oracle(lens, prefix, both, H, Hkv, d, scale, cap, kind):
+    gain = 1.0 if scale < 0.5 else d ** -0.5
+    _run(lens, prefix, both, H, Hkv, d, "bf16", scale, cap, kind, gain, seed=len(lens))
+
+
+@pytest.mark.gpu
+def test_cut_runs_whose_parts_see_nothing():
+    """A bias that hides near or far keys leaves whole parts, and some rows, without a key."""
+    from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    H, d, cu = 3, 64, [0, 1290]
+    buckets = [0] * 200 + [1] * 200 + [2]
+    bias = torch.zeros(H, 3)
+    bias[0, 1:] = float("-inf")     # the last parts alone
+    bias[1, :2] = float("-inf")     # the first parts; rows below 400 see nothing
+    bias[2, :] = float("-inf")
+    q, k, v, dout = _inputs(cu[-1], H, 1, d, "bf16", 5)
+    plan = ScorePlan(cu, H, rel_buckets=buckets, device=DEV)
+    dv = [x.to(DEV) for x in (q, k, v, dout)]
+    out, lse, lo = cp_attn_scored_fwd(*dv[:3], plan, R64, rel_bias=bias.to(DEV), residual=True)
+    got = cp_attn_scored_bwd(*dv[:3], out, lse, dv[3], plan, R64, rel_bias=bias.to(DEV), out_lo=lo)
+    s = O.Scores(bias=bias.clamp(min=-1e38), buckets=buckets)
+    vals, tol = reference(q, k, v, cu, R64, s, dout, HALF_STEP["bf16"], HALF_STEP["bf16"])
+    assert not out[:400, 1].any() and not out[:, 2].any()
+    assert torch.all(lse[1, :400] == -torch.inf) and torch.all(lse[2] == -torch.inf)
+    for name, g in zip(("out", "lse", "dq", "dk", "dv", "dbias"), (out, lse, *got)):
+        check(name, g, vals[name], tol[name])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["cap", "slopes", "bias"])
+def test_cut_runs_keep_samples_apart(kind):
+    """NaN in the samples around a cut one, a captured call, and bf16 gradients."""
+    from vlm_zigzag_head_gb300 import ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd
+    H, d, cu = 2, 64, [0, 70, 1270, 1500]
+    plan = ScorePlan(cu, H, rel_buckets=[0, 1, 2], device=DEV)
+    opt = {"cap": dict(softcap=6.0), "slopes": dict(slopes=torch.tensor([0.1, 0.02], device=DEV)),
+           "bias": dict(rel_bias=torch.randn(H, 3, device=DEV, generator=torch.Generator(DEV).manual_seed(1)))}[kind]
+    x = [t.to(DEV) for t in _inputs(cu[-1], H, 1, d, "bf16", 8)]
+
+    def run():
+        out, lse, lo = cp_attn_scored_fwd(*x[:3], plan, R64, residual=True, **opt)
+        return (out, lse.t()) + cp_attn_scored_bwd(*x[:3], out, lse, x[3], plan, R64, out_lo=lo,
+                                                   grad_dtype=torch.bfloat16, **opt)[:3]
+    want = [t.clone() for t in run()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = run()
+    for t in x:
+        t[:70] = float("nan")
+        t[1270:] = float("inf")
+    g.replay()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(want, held)):
+        a, b = a[70:1270].float(), b[70:1270].float()
+        assert torch.isfinite(b).all(), i
+        # an infinity in a shared tile may select the other evaluation of tanh; sums in another order turn
+        # a rounding to bf16 in few places
+        assert (a - b).norm() <= 2.0 ** -10 * a.norm(), i
+
+
+@pytest.mark.gpu
+def test_bounds_checked_build_meets_no_index_outside_a_tensor_in_cut_runs():
+    from vlm_zigzag_head_gb300 import build
+    from vlm_zigzag_head_gb300._binding import bounds_checked
+    build.build(checked=True)
+    with bounds_checked():
+        _run([1300, 1, 129], [40, 0, 129], True, 2, 1, 64, "bf16", R64, 8.0, "slopes", seed=1)
+        _run([1060], 0, False, 1, 1, 128, "bf16", R128, 0.0, (8, 64), seed=2)

@@ -129,3 +129,32 @@ def test_more_heads_than_a_grid_holds(cplib):
     assert build_plan([0, 5], 65535, 0, False, None, 152)[1] == 5
     with pytest.raises(CpError):
         build_plan([0, 5], 65536, 0, False, None, 152)
+
+
+def _cut(plan, dtype, d=64):
+    """Bytes that a forward needs for partial results, per element of a row."""
+    block = (ctypes.c_char * len(plan)).from_buffer(plan)
+    return B.lib().cp_attn_scored_fwd_workspace_size(block, dtype, 1, d, 0.125)
+
+
+@pytest.mark.parametrize("lens,prefix,H", [([3000], 0, 1), ([1025, 0, 2000], 300, 2), ([4999, 1], 1, 4),
+                                           ([2048, 130], [2048, 5], 1), ([129] * 20 + [5000], 7, 3)])
+@pytest.mark.parametrize("both", [False, True])
+def test_cut_plans_cover_the_visible_pairs(cplib, lens, prefix, H, both):
+    """Few heads: long runs are cut into parts, which still meet every pair once."""
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    pre = [min(prefix, n) for n in lens] if isinstance(prefix, int) else prefix
+    want = sum(n * (n + 1) // 2 + (p * (p - 1) // 2 if both else 0) for n, p in zip(lens, pre))
+    for sms in (1, 16, 152, 4096):
+        plan, T = build_plan(cu, H, pre, both, None, sms)
+        assert _pairs(plan) == [want] * 3
+        if sms != 16:   # one multiprocessor has nobody to share with
+            assert (_cut(plan, 1) > 256) == (sms > 16)
+    with pytest.raises(CpError):
+        build_plan(cu, H, pre, both, None, 4097)
+
+
+def test_plans_that_fill_the_gpu_are_not_cut(cplib):
+    for lens, H in (([4096], 16), ([8192], 8), ([2048, 1531, 700], 12), ([512], 8), ([40] * 300, 4)):
+        plan, _ = build_plan(np.concatenate([[0], np.cumsum(lens)]).tolist(), H, 0, False, None, 152)
+        assert _cut(plan, 1) == 256   # the status alone

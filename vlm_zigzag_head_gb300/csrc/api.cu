@@ -775,7 +775,7 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
               make_tmap_ld(&a.tm_ld, lse2, pitch, H, tq + 4, &terr) &&
               make_tmap_f32_sw128(&a.tm_dq, dq, T, H, d, 32, &terr);
     if (!ok) return fail(CP_ERR_CUDA, std::string("tensor map: ") + (terr ? terr : "?"));
-    a.H = H; a.Hkv = Hkv; a.kv_split = kv_split; a.d = d; a.scale = scale;
+    a.H = H; a.Hkv = Hkv; a.kv_split = kv_split; a.add_dkdv = kv_split > 1; a.d = d; a.scale = scale;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.T = T;
     a.dq = dq; a.dk = dk; a.dv = dv;

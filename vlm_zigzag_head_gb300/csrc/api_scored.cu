@@ -39,7 +39,7 @@ struct Ws {
   size_t status = 0, scales = 0;
   size_t dtable = 0, dq = 0, dk = 0, dv = 0;   // backward (dq, dk, dv: bf16 results)
   size_t table = 0;
-  size_t v16 = 0, part_out = 0, part_lse = 0;  // forward
+  size_t v16 = 0, part_out = 0, part_lse = 0;  // forward (parts: fp32 results)
   size_t lse2 = 0, D = 0, q16 = 0, k16 = 0;    // backward
   size_t total = 0;
 };
@@ -71,10 +71,11 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
   take(&w.dv, backward && bf16_grads, T * Hkv * d * sizeof(float));
   take(&w.table, h.n_dist > 0, (size_t)h.H * table_pitch(h.n_dist) * sizeof(float));
   if (!backward) {
-    const size_t parts = dt == CP_F32 ? f32_fwd_splits(h) : 1;
+    const size_t splits = dt == CP_F32 ? f32_fwd_splits(h) : 1;
+    const size_t rows = dt == CP_BF16 ? h.run_rows : splits > 1 ? splits * T : 0;
     take(&w.v16, v16, T * Hkv * d * 2);
-    take(&w.part_out, parts > 1, parts * T * h.H * d * sizeof(float));
-    take(&w.part_lse, parts > 1, parts * T * h.H * sizeof(float));
+    take(&w.part_out, rows > 0, rows * h.H * d * sizeof(float));
+    take(&w.part_lse, rows > 0, rows * h.H * sizeof(float));
   } else {
     const size_t plane = (size_t)ld_pitch(T) * h.H * sizeof(float);
     take(&w.lse2, true, 2 * plane);
@@ -248,14 +249,16 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
   for (int i = 0; i < h->n_fwd; ++i)
     for (int t = 0; t < fi[i].q_len; ++t) {
       const Seg& s = fi[i].seg[0];
-      nf += s.causal ? std::min<int64_t>(s.len, (int64_t)t + s.delta + 1) : s.len;
+      nf += s.causal ? std::max<int64_t>(0, std::min<int64_t>(s.len, (int64_t)t + s.delta + 1))
+                     : s.len;
     }
   const BwdItem* bi = reinterpret_cast<const BwdItem*>(b + h->bwd);
   const Seg* runs = reinterpret_cast<const Seg*>(b + h->runs);
   for (int i = 0; i < h->n_bwd; ++i)
     for (int u = 0; u < bi[i].k_len; ++u) {
       const Seg& s = runs[bi[i].run0];
-      nb += s.causal ? std::max<int64_t>(0, (int64_t)s.len - (u - s.delta)) : s.len;
+      nb += s.causal ? std::min<int64_t>(s.len, std::max<int64_t>(0, (int64_t)s.len - (u - s.delta)))
+                     : s.len;
     }
   const Tile32* ti = reinterpret_cast<const Tile32*>(b + h->tiles);
   for (int i = 0; i < h->n_tiles; ++i)
@@ -365,8 +368,15 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   a.text_rows = T;
   a.isolate = 1;
   a.score = s;
-  ProfileScope prof(2, st);
+  a.o_run = reinterpret_cast<float*>(w + c.ws.part_out);
+  a.lse_run = reinterpret_cast<float*>(w + c.ws.part_lse);
+  a.run_rows = c.h->run_rows;
+  ProfileScope prof(2, st, c.h->n_joins > 0 ? 2 : 1);
   ENTRY_CUDA(launch_tc_fwd_scored(a, c.bias, st), "tensor-core scored forward");
+  if (c.h->n_joins > 0)
+    ENTRY_CUDA(launch_join_parts(reinterpret_cast<const Join*>(plan + c.h->joins), c.h->n_joins,
+                                 a.o_run, a.lse_run, a.run_rows, H, d, T, out, out_lo, lse, st),
+               "join of partial results");
   return CP_OK;
   ENTRY_CATCH
 }
@@ -411,7 +421,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   const int kv_split = c.bf16 ? bwd_kv_split(c.h->n_bwd, H, Hkv, sms) : 1;
   const int f32_split = c.bf16 ? 1 : f32_splits((int64_t)c.h->n_tiles * H, c.h->max_walk, sms);
   const bool add_dq = c.bf16 || f32_split > 1;
-  const bool add_dkdv = c.bf16 ? kv_split > 1 : f32_split > 1 || H > Hkv;
+  const bool add_dkdv = c.bf16 ? kv_split > 1 || c.h->bwd_cut : f32_split > 1 || H > Hkv;
   // (dK and dV of whole groups come out of the tensor cores complete: straight to bf16)
   const bool bf16_dkdv = bf16_grads && !add_dkdv;
   if (bf16_grads) {
@@ -495,6 +505,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.status = reinterpret_cast<int32_t*>(w);
     a.wait_limit = device_wait_limit();
     a.kv_split = kv_split;
+    a.add_dkdv = add_dkdv ? 1 : 0;
     a.isolate = 1;
     a.item_major = item_major((int64_t)c.h->n_bwd * Hkv * kv_split, sms) ? 1 : 0;
     a.f16 = c.f16 ? 1 : 0;

@@ -20,6 +20,11 @@ cudaError_t launch_reduce_dbias(const float* dtable, const int32_t* buckets, int
 // dst[i] = bf16(src[i]) for three tensors of n[i] elements (multiples of 4).
 cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3],
                              const int64_t (&n)[3], int sms, cudaStream_t st);
+// out, lse (and out_lo, nullable) of the rows of cut tiles from their partial
+// results po [H][run_rows][d], pl [H][run_rows].
+cudaError_t launch_join_parts(const Join* joins, int n_joins, const float* po, const float* pl,
+                              int64_t run_rows, int H, int d, int64_t T, void* out, void* out_lo,
+                              float* lse, cudaStream_t st);
 
 // ---- fp32 inputs: CUDA cores (attn_f32.cu) ---------------------------------------
 struct F32Args {

@@ -1,6 +1,7 @@
 // The small kernels around attention with modified scores: the learned bias laid
 // out by distance and its gradient summed back (a few KB a head: bound by the
-// launch), and the gradients' rounding to bf16 (one pass, bound by memory).
+// launch), the join of partial results, and the gradients' rounding to bf16 (one
+// pass each, bound by memory).
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
@@ -64,7 +65,66 @@ __global__ void __launch_bounds__(kThreads) cast_bf16_kernel(const Cast3 c) {
   }
 }
 
+// Softmax parts: out = sum_p e^(lse_p - m) out_p / sum_p e^(lse_p - m), m the largest
+// lse_p.  Block (join, piece of its rows, head); D / 4 lanes per row.
+constexpr int kJoinRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    join_parts_kernel(const Join* joins, const float* po, const float* pl, int64_t run_rows, int H,
+                      int64_t T, __nv_bfloat16* out, __nv_bfloat16* out_lo, float* lse) {
+  constexpr int kLanes = D / 4, kPass = kThreads / kLanes;
+  const Join jn = joins[blockIdx.x];
+  const int h = blockIdx.z, lane = threadIdx.x % kLanes;
+  const int end = min(jn.len, ((int)blockIdx.y + 1) * kJoinRows);
+  for (int t = blockIdx.y * kJoinRows + threadIdx.x / kLanes; t < end; t += kPass) {
+    const int64_t row0 = h * run_rows + jn.run_row0 + t;
+    float m = -INFINITY;
+    for (int p = 0; p < jn.parts; ++p) m = fmaxf(m, pl[row0 + (int64_t)p * jn.len]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    if (m != -INFINITY) {
+#pragma unroll 4
+      for (int p = 0; p < jn.parts; ++p) {
+        const int64_t row = row0 + (int64_t)p * jn.len;
+        const float w = expf(pl[row] - m);
+        const float4 v = *reinterpret_cast<const float4*>(po + row * D + lane * 4);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+        sum += w;
+      }
+      const float inv = 1.f / sum;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+    const uint2 hi = make_uint2(ptx::pack_bf16x2(acc.x, acc.y), ptx::pack_bf16x2(acc.z, acc.w));
+    const int64_t at = ((jn.out_row0 + t) * (int64_t)H + h) * D + lane * 4;
+    *reinterpret_cast<uint2*>(out + at) = hi;
+    if (out_lo != nullptr)   // the remainder, itself rounded to bf16
+      *reinterpret_cast<uint2*>(out_lo + at) = make_uint2(
+          ptx::pack_bf16x2(acc.x - __uint_as_float(hi.x << 16),
+                           acc.y - __uint_as_float(hi.x & 0xffff0000u)),
+          ptx::pack_bf16x2(acc.z - __uint_as_float(hi.y << 16),
+                           acc.w - __uint_as_float(hi.y & 0xffff0000u)));
+    if (lane == 0)
+      lse[h * T + jn.out_row0 + t] = m == -INFINITY ? -INFINITY : m + logf(sum);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_join_parts(const Join* joins, int n_joins, const float* po, const float* pl,
+                              int64_t run_rows, int H, int d, int64_t T, void* out, void* out_lo,
+                              float* lse, cudaStream_t st) {
+  const dim3 grid(n_joins, kFwdPairQ / kJoinRows, H);
+  auto* o = static_cast<__nv_bfloat16*>(out);
+  auto* lo = static_cast<__nv_bfloat16*>(out_lo);
+  if (d == 64)
+    join_parts_kernel<64><<<grid, kThreads, 0, st>>>(joins, po, pl, run_rows, H, T, o, lo, lse);
+  else
+    join_parts_kernel<128><<<grid, kThreads, 0, st>>>(joins, po, pl, run_rows, H, T, o, lo, lse);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3],
                              const int64_t (&n)[3], int sms, cudaStream_t st) {

@@ -3,7 +3,10 @@
 // The P simulated ranks are partitions of one memory and a query row sees the
 // same keys whichever rank owns them, so these lists walk every sample's rows in
 // natural order: no gather, one key run per query tile, one query run per key
-// tile, and distances are differences of positions.  A plan is one flat block,
+// tile, and distances are differences of positions.  Where few tiles would leave
+// SMs idle behind the longest of them, long runs are cut into parts (part_limit):
+// the forward's parts leave fp32 results that a last kernel joins, the backward's
+// add their dK and dV.  A plan is one flat block,
 // built on the host, that the caller copies to the device once and keeps for
 // every call with the same packing.
 #pragma once
@@ -27,6 +30,13 @@ struct Tile32 {
 };
 static_assert(sizeof(Tile32) == 32, "Tile32 layout");
 
+// A forward tile whose keys were cut: its rows, and the first row of its `parts`
+// partial results, each `len` rows long.
+struct Join {
+  int32_t out_row0, len, run_row0, parts;
+};
+static_assert(sizeof(Join) == 16, "Join layout");
+
 constexpr uint32_t kScorePlanMagic = 0x43505350u;
 constexpr int kMaxDist = 1 << 16;
 
@@ -36,11 +46,14 @@ struct ScorePlanHeader {
   int32_t T, H, n_seqs, bidirectional;
   int32_t n_dist, n_buckets;       // 0: no table
   int32_t n_fwd, n_bwd, n_tiles;
+  int32_t fwd_part, bwd_part;      // tiles of the longest part of a cut run (0: none cut)
+  int32_t n_joins, run_rows;       // forward: cut tiles and their partial rows per head
+  int32_t bwd_cut;                 // nonzero: several backward items share a key tile
   int32_t max_walk;                // tiles of the longest sample (fp32 kernels)
   int32_t n_units, grid;           // forward: units and persistent CTAs
   int32_t item_major;              // the forward's unit order
   int32_t n_sms;
-  uint64_t fwd, bwd, runs, units, buckets, tiles, total;
+  uint64_t fwd, bwd, runs, units, buckets, tiles, joins, total;
 };
 static_assert(sizeof(ScorePlanHeader) <= 256, "plan header");
 

@@ -92,11 +92,12 @@ struct TcBwdArgs {
   float scale, scale_log2;
   int64_t T;
   float* dq; float* dk; float* dv;
-  int dkv_bf16;               // dk, dv point to bf16 (scored plans, kv_split 1)
+  int dkv_bf16;               // dk, dv point to bf16 (scored plans, not add_dkdv)
   float* pre_k; float* pre_v; int64_t pre_rows;
   int32_t* status;
   long long wait_limit;
-  int kv_split;               // CTAs sharing one KV head's query heads (divides H / Hkv); > 1:
+  int kv_split;               // CTAs sharing one KV head's query heads (divides H / Hkv)
+  int add_dkdv;               // several CTAs share a key tile (kv_split > 1, or cut query runs):
                               // dK / dV / prefix slots are reduce-added into zeroed memory
   int isolate;                // as TcFwdArgs::isolate, for query and key rows
   int item_major;             // nonzero: blocks go item by item (all heads of the heaviest
@@ -104,7 +105,7 @@ struct TcBwdArgs {
   int n_slots;                // prefix-gradient slots (P + 1) behind pre_k / pre_v (index checks)
   ScoreArgs score;            // read by the scored kernels only
 };
-// The backward (tc_bwd_q128.cu): one launch over the all-steps plan, every
+// The backward (tc_bwd_q128.cuh): one launch over the all-steps plan, every
 // item a key tile with the query runs of all ring steps, in 128-query tiles.
 cudaError_t launch_tc_bwd_q128(const TcBwdArgs& a, cudaStream_t st);
 

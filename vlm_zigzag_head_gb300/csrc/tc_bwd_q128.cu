@@ -7,7 +7,7 @@ namespace {
 
 template <int D, bool kF16>
 cudaError_t launch_plain(const TcBwdArgs& a, cudaStream_t st) {
-  return a.kv_split > 1 ? launch_q128<D, kF16, true, false, SCORE_PLAIN>(a, st)
+  return a.add_dkdv ? launch_q128<D, kF16, true, false, SCORE_PLAIN>(a, st)
                         : launch_q128<D, kF16, false, false, SCORE_PLAIN>(a, st);
 }
 

@@ -4,8 +4,8 @@
 
 namespace cpattn {
 
-// One instantiation serves both a whole group per CTA and shared groups: the
-// epilogue asks kv_split.
+// One instantiation serves key tiles of one CTA and shared ones: the epilogue asks
+// add_dkdv.
 template <int D, bool kF16>
 cudaError_t launch_bwd_scored_d(const TcBwdArgs& a, int bias, cudaStream_t st) {
   if (a.score.cap_log2 > 0.f) {
