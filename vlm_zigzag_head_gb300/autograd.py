@@ -90,13 +90,12 @@ def _wants_grad(*tensors) -> bool:
 
 
 class QKNormRope(torch.autograd.Function):
-    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, options)``."""
+    """``(q_out, k_out) = QKNormRope.apply(q, k, positions, q_weight, k_weight, desc, options)``."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, q_weight, k_weight, options):
+    def forward(ctx, q, k, positions, q_weight, k_weight, desc, options):
         ctx.save_for_backward(q, k, positions, q_weight, k_weight)
-        ctx.options = options
-        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
+        ctx.meta = (desc, options, q.stride(), k.stride())
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
 
     @staticmethod
@@ -104,13 +103,15 @@ class QKNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
         need = ctx.needs_input_grad
+        desc, options, q_stride, k_stride = ctx.meta
         # saved tensors may come back with other strides (offloaded, recomputed)
-        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *ctx.options)
+        if q.stride() != q_stride or k.stride() != k_stride:
+            desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
         dq, dk, dqw, dkw = norm_rope._launch_bwd(desc, q, k, positions, _dense(dq_out),
                                                  _dense(dk_out), q_weight, k_weight)
         return (dq if need[0] else None, dk if need[1] else None, None,
                 dqw.to(q_weight.dtype) if need[3] else None,
-                dkw.to(k_weight.dtype) if need[4] else None, None)
+                dkw.to(k_weight.dtype) if need[4] else None, None, None)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
@@ -125,10 +126,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     sections = None if sections is None else tuple(sections)
     inv_freq = None if inv_freq is None else tuple(inv_freq)
     options = (eps, theta, rot_dim, sections, interleaved, inv_freq)
+    desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
     if not _wants_grad(q, k, q_weight, k_weight):
-        desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
-    return QKNormRope.apply(q, k, positions, q_weight, k_weight, options)
+    return QKNormRope.apply(q, k, positions, q_weight, k_weight, desc, options)
 
 
 class CPAttentionScored(torch.autograd.Function):
@@ -152,7 +153,6 @@ class CPAttentionScored(torch.autograd.Function):
         # saved tensors may come back elsewhere and with other strides (offloaded, recomputed)
         q, k, v, out, lse = (_dense(x) for x in (q, k, v, out, lse))
         out_lo = None if out_lo is None else _dense(out_lo)
-        scored._check(q, k, v, plan)
         desc = scored._scores(q, softcap, slopes, rel_bias)
         got = scored._launch_bwd(desc, q, k, v, out, lse, _dense(dout), plan, scale, rel_bias,
                                  None, None, out_lo, q.dtype)
