@@ -8,6 +8,8 @@ half step of the 16-bit operands (2^-8 for bf16 P and dS; 0 on the fp32 path):
 * a probability by e = 2 max delta + 2^-20 of its value (its row's normaliser errs as much; exp2);
 * out by (r + e) sum p|v|, plus half a step of the output type;
 * D = dout . out by eD = sum |dout| (r + e + 2^-16) sum p|v|: out is kept to 16 bits by its remainder;
+* with f16 operands (softmax scale above 1/4) dS is kept as an f16 multiple of 2^es, which ends at steps
+  of 2^(es - 24): half a step, `ds_floor`, on every visible pair;
 * dS = p (dP - D) w by (r + 2 e + 4e-6) |dS| + p (eD + d u sum|dout v|) + 4e-6 |p (dP - D)|;
 * products of these with k, q and dout sum the bounds, and n u of the magnitudes for n summed terms.
 """
@@ -18,7 +20,13 @@ from oracle import scored as O
 U = 2.0 ** -24
 
 
-def reference(q, k, v, cu, scale, s, dout, r_op, r_out):
+def f16_ds_floor(v, dout):
+    """es = 1 + log2 d + E_v + E_dout - 15, with E the exponents of the largest magnitudes."""
+    es = 1 + np.log2(v.shape[-1]) + sum(np.frexp(np.abs(O._f64(x)).max())[1] for x in (v, dout)) - 15
+    return 2.0 ** (es - 25)
+
+
+def reference(q, k, v, cu, scale, s, dout, r_op, r_out, ds_floor=0.0):
     """({name: value}, {name: bound}) of out, lse, dq, dk, dv and dbias."""
     q, k, v, dout = (O._f64(x) for x in (q, k, v, dout))
     T, H, d = q.shape
@@ -52,6 +60,7 @@ def reference(q, k, v, cu, scale, s, dout, r_op, r_out):
             raw = np.abs(p * g)
             part = p * (eD + d * U * (np.abs(do) @ np.abs(vh).T))
             eS = (r_op + 2 * e + 4e-6) * raw * w + part + 4e-6 * raw
+            eS = eS + ds_floor * seen
             mag = raw * w
             tol["dq"][rows, h] = scale * (eS @ np.abs(kh) + m * U * (mag @ np.abs(kh)))
             tol["dk"][rows, hk] += scale * (eS.T @ np.abs(qh) + G * m * U * (mag.T @ np.abs(qh)))

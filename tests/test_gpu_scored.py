@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import scored as O
-from scored_util import check, reference
+from scored_util import check, f16_ds_floor, reference
 
 DEV = "cuda:0"
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -51,7 +51,7 @@ def _run(lens, prefix, both, H, Hkv, d, dtype, scale, cap, kind, gain=1.0, bias_
     pre = [prefix] * len(lens) if isinstance(prefix, int) else prefix
     s = O.Scores(softcap=cap, slopes=slopes, bias=bias, buckets=buckets, prefix_lens=pre, bidirectional=both)
     vals, tol = reference(q, k, v, cu, scale, s, dout, HALF_STEP[dtype] if dtype == "bf16" else 0.0,
-                          HALF_STEP[dtype])
+                          HALF_STEP[dtype], f16_ds_floor(v, dout) if dtype == "bf16" and scale > 0.25 else 0.0)
     check("out", out, vals["out"], tol["out"])
     check("lse", lse, vals["lse"], tol["lse"])
     for name, g in zip(("dq", "dk", "dv", "dbias"), got):
@@ -614,3 +614,11 @@ def test_bounds_checked_build_meets_no_index_outside_a_tensor_in_cut_runs():
     with bounds_checked():
         _run([1300, 1, 129], [40, 0, 129], True, 2, 1, 64, "bf16", R64, 8.0, "slopes", seed=1)
         _run([1060], 0, False, 1, 1, 128, "bf16", R128, 0.0, (8, 64), seed=2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,cap", [(1e-8, 1e-3), (1e-8, 1e4), (0.2, 1e4), (0.2, 1e-3), (20.0, 1e4), (1e-3, 1e-3)])
+@pytest.mark.parametrize("kind", [None, "slopes", (8, 32)])
+def test_ends_of_the_cap_and_scale_ranges(scale, cap, kind):
+    """Coefficients of the cap's polynomial that would leave the range of normal numbers."""
+    _run([150, 33], 0, False, 2, 1, 64, "bf16", scale, cap, kind, 1.0 if scale < 1 else 0.125, seed=3)

@@ -166,11 +166,12 @@ cp_status_t check_gpu(bool bf16, int* sms) {
 }
 
 // The tensor-core kernels' view of the scores; lays the table out by distance.
-cp_status_t prepare_scores(const Call& c, const cp_score_t* sc, const char* plan, char* w,
-                           ScoreArgs* s, cudaStream_t st) {
+cp_status_t prepare_scores(const Call& c, const cp_score_t* sc, float scale, const char* plan,
+                           char* w, ScoreArgs* s, cudaStream_t st) {
   *s = ScoreArgs{};
   s->cap_log2 = sc->softcap * kLog2e;
   s->inv_cap_log2 = sc->softcap > 0.f ? 1.f / s->cap_log2 : 0.f;
+  if (sc->softcap > 0.f) fill_cap_polynomial(s, scale * kLog2e);
   s->slopes = sc->slopes;
   if (c.bias == SCORE_TABLE) {
     s->n_dist = c.h->n_dist;
@@ -304,7 +305,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   const char* plan = static_cast<const char*>(plan_d);
   ENTRY_CUDA(cudaMemsetAsync(w, 0, c.ws.dtable, st), "clear status and operand scales");
   ScoreArgs s;
-  if ((e = prepare_scores(c, score, plan, w, &s, st)) != CP_OK) return e;
+  if ((e = prepare_scores(c, score, scale, plan, w, &s, st)) != CP_OK) return e;
   if (!c.bf16) {
     F32Args a = f32_args(c, score, plan, s, Hkv, scale);
     a.q = static_cast<const float*>(q);
@@ -440,7 +441,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     ENTRY_CUDA(cudaMemsetAsync(dv, 0, (size_t)T * Hkv * d * sizeof(float), st), "clear dv");
   }
   ScoreArgs s;
-  if ((e = prepare_scores(c, score, plan, w, &s, st)) != CP_OK) return e;
+  if ((e = prepare_scores(c, score, scale, plan, w, &s, st)) != CP_OK) return e;
   if (c.bias == SCORE_TABLE) s.dtable = reinterpret_cast<float*>(w + c.ws.dtable);
   float* Dd = reinterpret_cast<float*>(w + c.ws.D);
   float* lse2 = reinterpret_cast<float*>(w + c.ws.lse2);

@@ -30,9 +30,8 @@ namespace score {
 using namespace ptx;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPolyRange = 0.75f;
-constexpr float kC1 = -0.33329880795843986f, kC2 = 0.13270406554292946f,
-                kC3 = -0.050340821426050376f, kC4 = 0.013161359006389609f;
+constexpr float kPolyRange = kCapPolyRange;
+constexpr float kC1 = kCapPoly[0], kC2 = kCapPoly[1], kC3 = kCapPoly[2], kC4 = kCapPoly[3];
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -40,17 +39,51 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The cap: products s become t = tanh(s * in), in = scale / softcap, or with kNeg
-// (the backward) minus that; the scores are t * mul, mul = cap2 or -cap2.  (With
-// the sign reversed one constant, -1, serves the polynomial and the slope.  The
-// products are scaled before the polynomial: its coefficients in their units could
-// underflow.)
-template <bool kCap, bool kNeg>
-struct Cap {
-  static constexpr float kUnit = kNeg ? -1.f : 1.f;
+// The forward's cap: products s become scores s * factor(s), a polynomial in s^2
+// with the scale and the cap in its coefficients (six fused operations a score
+// with the softmax's own subtraction, where scaling, tanh and scaling back take
+// eight: 18 688 tokens x 8 of 128 812 -> 780 us, with slopes 890 -> 815, with a
+// table 863 -> 796), or any(s) * mul.
+template <bool kCap>
+struct FwdCap {
+  float in = 0.f, mul = 0.f, reach = -1.f;
+  uint64_t k[5] = {0, 0, 0, 0, 0};
+  __device__ __forceinline__ FwdCap(const ScoreArgs& s, float scale_log2) {
+    if constexpr (kCap) {
+      mul = s.cap_log2;
+      in = scale_log2 * s.inv_cap_log2;
+      reach = s.cap_reach;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) k[i] = pack2(s.cap_k[i], s.cap_k[i]);
+    }
+  }
+  // the largest |s| of a warp lets the polynomial serve
+  __device__ __forceinline__ bool in_range(float big) const {
+    return __all_sync(0xffffffffu, big <= reach);
+  }
+  __device__ __forceinline__ uint64_t factor(uint64_t s) const {
+    const uint64_t v = mul2(s, s);
+    uint64_t p = fma2(k[4], v, k[3]);
+    p = fma2(p, v, k[2]);
+    p = fma2(p, v, k[1]);
+    return fma2(p, v, k[0]);
+  }
+  // any s: tanh z = 1 - 2 / (1 + e^(2z)), e^(2z) = 2^(2 z log2 e)
+  __device__ __forceinline__ float any(float s) const {
+    return fmaf(-2.f, rcp_approx(1.f + ex2(s * in * (2.f * kLog2e))), 1.f);
+  }
+};
+
+// The backward's cap: products s become t = -tanh(s * in), in = scale / softcap; the
+// scores are t * mul, mul = -cap2.  (With the sign reversed one constant, -1, serves
+// the polynomial and the slope.  The products are scaled before the polynomial, as
+// tanh itself is wanted.)
+template <bool kCap>
+struct BwdCap {
+  static constexpr float kUnit = -1.f;
   float in = 0.f, mul = 0.f;
   uint64_t in2 = 0, unit = 0, k[4] = {0, 0, 0, 0};
-  __device__ __forceinline__ Cap(const ScoreArgs& s, float scale_log2) {
+  __device__ __forceinline__ BwdCap(const ScoreArgs& s, float scale_log2) {
     if constexpr (kCap) {
       mul = kUnit * s.cap_log2;
       in = scale_log2 * s.inv_cap_log2;
@@ -74,13 +107,11 @@ struct Cap {
     p = fma2(p, v, unit);
     return mul2(z, p);
   }
-  // any s: tanh z = 1 - 2 / (1 + e^(2z)), e^(2z) = 2^(2 z log2 e)
   __device__ __forceinline__ float any(float s) const {
     return fmaf(-2.f * kUnit, rcp_approx(1.f + ex2(s * in * (2.f * kLog2e))), kUnit);
   }
   // t^2 - 1
   __device__ __forceinline__ uint64_t minus_slope(uint64_t t) const {
-    static_assert(kNeg, "the constant is -1");
     return fma2(t, t, unit);
   }
 };

@@ -37,6 +37,9 @@ bool make_tmap_ld(CUtensorMap* map, const void* base, int64_t pitch, int H, int 
 enum : int { SCORE_PLAIN = 0, SCORE_SLOPES = 1, SCORE_TABLE = 2 };
 struct ScoreArgs {
   float cap_log2, inv_cap_log2;   // softcap * log2(e) and its inverse (kCap)
+  // the forward's cap: scores are s (k0 + k1 s^2 + .. + k4 s^8) for |s| <= cap_reach
+  float cap_k[5];
+  float cap_reach;
   const float* slopes;            // SCORE_SLOPES: [H], natural units
   // SCORE_TABLE: [H][table_pitch] bias * log2(e) by signed distance: entry
   // table_mid + distance, |distance| <= table_mid; constant from n_dist - 1 on
@@ -44,6 +47,14 @@ struct ScoreArgs {
   int n_dist, table_pitch, table_mid;
   float* dtable;                  // backward: [H][n_dist], sums of dS by |distance|
 };
+// tanh(z) = z (1 + c1 z^2 + .. + c4 z^8) for |z| <= 0.75, minimax (off by at most
+// 6e-7 of the value)
+constexpr float kCapPolyRange = 0.75f;
+constexpr float kCapPoly[4] = {-0.33329880795843986f, 0.13270406554292946f,
+                               -0.050340821426050376f, 0.013161359006389609f};
+// Fills cap_k and cap_reach from the caps and the scale.  A coefficient that is no
+// normal number is left out, and the reach ends where its term passes 3e-7.
+void fill_cap_polynomial(ScoreArgs* s, float scale_log2);
 // Entries of the table past +-n_dist: a 128 x 128 tile that holds a distance
 // below n_dist spans 254 more, so it reads the table without bounds checks.
 constexpr int kTableSlack = 256;

@@ -228,7 +228,7 @@ __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4
 template <bool kCap, int kBias, bool kFast>
 __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t (&pk)[16],
                                               uint32_t* ph, int x0, float mul,
-                                              float inv, const score::Cap<kCap, true>& cap,
+                                              float inv, const score::BwdCap<kCap>& cap,
                                               const score::TileBias& tb, bool poly,
                                               const float* ld, bool vec, int first_vis,
                                               int end_vis) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t (&pk)
 // Whether a warp's 64 products per lane all lie in the polynomial's range.
 template <bool kCap>
 __device__ __forceinline__ bool in_poly_range(const uint32_t (&rs)[2][32],
-                                              const score::Cap<kCap, true>& cap) {
+                                              const score::BwdCap<kCap>& cap) {
   if constexpr (!kCap) return true;
   float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sw = u & 7;
     bool ok = true;
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const score::Cap<kCap, true> cap(a.score, sl2);
+    const score::BwdCap<kCap> cap(a.score, sl2);
     const float s_mul = kCap ? cap.mul : sl2, s_inv = kScored ? 1.f / s_mul : 0.f;
     int jt = 0, hq = hq0;       // tile and query head, as the producers walk them
     float far_sum = 0.f;        // this thread's dS beyond the table (kBias: table),

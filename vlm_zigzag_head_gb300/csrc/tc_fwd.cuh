@@ -159,10 +159,10 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
 // the caller caps the row's maximum, and each product beside its exponential.
 template <bool kCap, int kBias>
 __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv,
-                                          const score::Cap<kCap, false>& cap, const score::TileBias& tb,
+                                          const score::FwdCap<kCap>& cap, const score::TileBias& tb,
                                           float& mul, float& add) {
   add = tb.base;
-  bool lazy = false;
+  const bool near = kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr);
   if constexpr (kCap) {
     float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -170,16 +170,35 @@ __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv
       big[(i >> 1) & 3] = fmaxf(fmaxf(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i / 32][i % 32]))),
                                 fabsf(__uint_as_float(r[i / 32][i % 32 + 1])));
     if (cap.in_range(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])))) {
-      lazy = kBias == SCORE_PLAIN;
+      if constexpr (kBias == SCORE_PLAIN) return true;
+      auto poly = [&](auto bias) {
 #pragma unroll
-      for (int i = 0; i < (kBias == SCORE_PLAIN ? 0 : kBN); i += 2) {
-        float y0, y1;
-        unpack2(cap.poly(pack2(__uint_as_float(r[i / 32][i % 32]),
-                               __uint_as_float(r[i / 32][i % 32 + 1]))),
-                y0, y1);
-        r[i / 32][i % 32] = __float_as_uint(y0);
-        r[i / 32][i % 32 + 1] = __float_as_uint(y1);
+        for (int i = 0; i < kBN; i += 2) {
+          const uint64_t s = pack2(__uint_as_float(r[i / 32][i % 32]),
+                                   __uint_as_float(r[i / 32][i % 32 + 1]));
+          float y0, y1;
+          unpack2(bias(i, s, cap.factor(s)), y0, y1);
+          r[i / 32][i % 32] = __float_as_uint(y0);
+          r[i / 32][i % 32 + 1] = __float_as_uint(y1);
+        }
+      };
+      mul = 1.f;
+      if constexpr (kBias == SCORE_SLOPES) {
+        if (near) {
+          poly([&](int i, uint64_t s, uint64_t f) {
+            return fma2(s, f, pack2(score::column_bias<kBias, -1>(tb, i),
+                                    score::column_bias<kBias, -1>(tb, i + 1)));
+          });
+          return false;
+        }
+        poly([&](int, uint64_t s, uint64_t f) { return mul2(s, f); });
+#pragma unroll
+        for (int i = 0; i < kBN; ++i)
+          r[i / 32][i % 32] =
+              __float_as_uint(fmaf((float)i, tb.step, __uint_as_float(r[i / 32][i % 32])));
+        return false;
       }
+      poly([&](int, uint64_t s, uint64_t f) { return mul2(s, f); });   // a near table follows
     } else {
 #pragma unroll
       for (int i = 0; i < kBN; ++i)
@@ -187,7 +206,7 @@ __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv
     }
   }
   if constexpr (kBias == SCORE_SLOPES) {
-    if (!tb.both) {
+    if (!near) {
       const float step = tb.step * inv;   // in the row's present units
 #pragma unroll
       for (int i = 0; i < kBN; ++i)
@@ -195,14 +214,14 @@ __device__ __forceinline__ bool score_row(uint32_t (&r)[kBN / 32][32], float inv
             __float_as_uint(fmaf((float)i, step, __uint_as_float(r[i / 32][i % 32])));
     }
   }
-  if (kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr)) {
+  if (near) {
 #pragma unroll
     for (int i = 0; i < kBN; ++i)
       r[i / 32][i % 32] = __float_as_uint(
           fmaf(__uint_as_float(r[i / 32][i % 32]), mul, score::column_bias<kBias, -1>(tb, i)));
     mul = 1.f;
   }
-  return lazy;
+  return false;
 }
 
 template <int D, bool kF16P, bool kCap, int kBias>
@@ -428,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     // scores in log2 units: products (or what score_row makes of them) times sl2,
     // plus s_add
     constexpr bool kScored = kCap || kBias != SCORE_PLAIN;
-    const score::Cap<kCap, false> cap(a.score, a.scale_log2);
+    const score::FwdCap<kCap> cap(a.score, a.scale_log2);
     const float s_mul = kCap ? cap.mul : a.scale_log2, s_inv = kScored ? 1.f / s_mul : 0.f;
     float sl2 = s_mul, s_add = 0.f;
     const float vmul = kF16P ? a.op_scales->v_mul : 1.f;   // V = V16 * vmul
@@ -533,11 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           constexpr bool kWhole = decltype(all_seen)::value, kLazy = decltype(to_cap)::value;
 #pragma unroll
           for (int i = 0; i < kBN; i += 2) {
-            uint64_t y = pack2(__uint_as_float(r[i / 32][i % 32]),
+            const uint64_t y = pack2(__uint_as_float(r[i / 32][i % 32]),
                                __uint_as_float(r[i / 32][i % 32 + 1]));
-            if constexpr (kLazy) y = cap.poly(y);
             float p0, p1;
-            unpack2(fma2(y, mul_2, sub2), p0, p1);
+            unpack2(fma2(y, kLazy ? cap.factor(y) : mul_2, sub2), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
             if constexpr (!kWhole) {

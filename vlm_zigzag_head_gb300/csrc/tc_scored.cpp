@@ -2,7 +2,27 @@
 // direction, head size and operand type.
 #include "tc.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace cpattn {
+
+void fill_cap_polynomial(ScoreArgs* s, float scale_log2) {
+  // |z| up to which the terms from this one on are below 3e-7
+  constexpr float without[4] = {9e-4f, 0.038f, 0.13f, 0.26f};
+  const float in = scale_log2 * s->inv_cap_log2;
+  double a = scale_log2;
+  float z = kCapPolyRange;
+  s->cap_k[0] = scale_log2;
+  for (int i = 0; i < 4; ++i) {
+    a *= (double)in * in;
+    const float k = (float)(a * kCapPoly[i]);
+    const bool normal = std::fabs(k) >= 1e-36f && std::fabs(k) <= 1e36f;
+    if (!normal) z = std::min(z, without[i]);
+    s->cap_k[i + 1] = normal ? k : 0.f;
+  }
+  s->cap_reach = z / in;
+}
 
 #define CP_SCORED(dir, Args)                                                       \
   cudaError_t launch_##dir##_scored_64_bf16(const Args&, int, cudaStream_t);       \
