@@ -353,7 +353,8 @@ cp_status_t cp_attn_bwd_gqa(const void* q, const void* k, const void* v, const v
  *   q_weight, k_weight   NULL or [d], weight_dtype
  *   q_out, k_out    contiguous, dtype, 16-byte aligned; must not overlap an input
  *   dq_out, dk_out  gradients of q_out, k_out: contiguous, dtype, 16-byte aligned
- *   dq, dk          gradients of q, k: contiguous, dtype, 16-byte aligned
+ *   dq, dk          gradients of q, k: contiguous, dtype, 16-byte aligned; must not
+ *                   overlap an input
  *   dq_weight, dk_weight   NULL or [d] fp32: sums over every row and head, in an
  *                   order that does not depend on timing
  *   workspace       backward with a weight gradient: >=
