@@ -158,3 +158,22 @@ def test_plans_that_fill_the_gpu_are_not_cut(cplib):
     for lens, H in (([4096], 16), ([8192], 8), ([2048, 1531, 700], 12), ([512], 8), ([40] * 300, 4)):
         plan, _ = build_plan(np.concatenate([[0], np.cumsum(lens)]).tolist(), H, 0, False, None, 152)
         assert _cut(plan, 1) == 256   # the status alone
+
+
+def test_buckets_of_any_whole_numbers(cplib):
+    want, _ = build_plan([0, 9], 1, 0, False, [0, 1, 1, 2], 152)
+    for same in (np.array([0, 1, 1, 2]), torch.tensor([0, 1, 1, 2]), (0, True, 1, 2)):
+        assert build_plan([0, 9], 1, 0, False, list(same), 152)[0] == want
+    for bad in ([0, 0.5], [0, 1 << 40], ["0"]):
+        with pytest.raises(CpError):
+            build_plan([0, 9], 1, 0, False, bad, 152)
+
+
+@pytest.mark.parametrize("n,far", [(2, 2), (3, 9), (8, 16), (32, 128), (33, 100), (64, 4096)])
+def test_relative_buckets_equal_their_formula(n, far):
+    import math
+    exact = n // 2
+    want = [d if d < exact else
+            min(n - 1, exact + int(math.log(d / exact) / math.log(far / exact) * (n - exact) + 1e-9))
+            for d in range(far + 1)]
+    assert relative_buckets(n, far) == want

@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cstdio>
 #include <map>
-#include <queue>
 #include <tuple>
 
 namespace cpattn {
@@ -233,24 +232,24 @@ void plan_unit_lists(const std::vector<FwdItem>& items, int H, int grid,
                      bool item_major) {
   constexpr int64_t kUnitCost = 2;  // Q load and epilogue, in KV-tile equivalents
   const int n = (int)items.size();
-  std::vector<std::vector<int32_t>> lists(grid);
   using Load = std::pair<int64_t, int>;  // (work so far, CTA): least work first, then lowest CTA
-  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> pq;
-  for (int b = 0; b < grid; ++b) pq.push({0, b});
+  std::vector<Load> least(grid);
+  for (int b = 0; b < grid; ++b) least[b] = {0, b};
   const int64_t total = (int64_t)n * H;
+  std::vector<int32_t> owner(total);
+  cta_off->assign(grid + 1, 0);
   for (int64_t u = 0; u < total; ++u) {
-    const int x = (int)(item_major ? u / H : u % n), h = (int)(item_major ? u % H : u / n);
-    Load e = pq.top();
-    pq.pop();
-    lists[e.second].push_back(x + n * h);
-    e.first += items[x].n_tiles + kUnitCost;
-    pq.push(e);
+    const Load e = least[0];
+    owner[u] = e.second;
+    ++(*cta_off)[e.second + 1];
+    replace_least(least, {e.first + items[item_major ? u / H : u % n].n_tiles + kUnitCost, e.second});
   }
-  units->clear();
-  cta_off->assign(1, 0);
-  for (const auto& l : lists) {
-    units->insert(units->end(), l.begin(), l.end());
-    cta_off->push_back((int32_t)units->size());
+  for (int b = 0; b < grid; ++b) (*cta_off)[b + 1] += (*cta_off)[b];
+  units->resize(total);
+  std::vector<int32_t> at(cta_off->begin(), cta_off->end() - 1);
+  for (int64_t u = 0; u < total; ++u) {
+    const int64_t x = item_major ? u / H : u % n, h = item_major ? u % H : u / n;
+    (*units)[at[owner[u]]++] = (int32_t)(x + n * h);
   }
 }
 

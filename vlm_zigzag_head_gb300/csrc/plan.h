@@ -108,6 +108,20 @@ void plan_forward_fused(const FwdPlan& per_step, int P, FusedFwdPlan* out);
 // per unit below four units per SM, else one persistent CTA per SM.
 inline long long fwd_grid(long long units, int sms) { return units < 4LL * sms ? units : sms; }
 
+// Puts v in the place of the least element, heap[0], of a min-heap.
+template <typename T>
+inline void replace_least(std::vector<T>& heap, const T& v) {
+  const size_t n = heap.size();
+  size_t i = 0;
+  for (size_t c = 1; c < n; c = 2 * i + 1) {
+    if (c + 1 < n && heap[c + 1] < heap[c]) ++c;
+    if (!(heap[c] < v)) break;
+    heap[i] = heap[c];
+    i = c;
+  }
+  heap[i] = v;
+}
+
 // Unit lists of a persistent forward launch with `grid` CTAs: CTA b walks
 // units[cta_off[b] .. cta_off[b + 1]), each entry item + n_items * head.
 // Units are taken head by head, items heaviest first (the plan's order), and

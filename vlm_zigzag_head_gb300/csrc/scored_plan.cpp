@@ -4,8 +4,6 @@
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
-#include <functional>
-#include <queue>
 #include <vector>
 
 namespace cpattn {
@@ -45,14 +43,12 @@ int64_t makespan(const std::vector<int64_t>& runs, int64_t limit, int sms) {
       (np > 1 ? cut : units)[tiles] += runs[n];
     }
   }
-  std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> free_at;
-  for (int b = 0; b < sms; ++b) free_at.push(0);
+  std::vector<int64_t> free_at(sms, 0);
   int64_t last = 0;
   for (size_t n = runs.size(); n-- > 1;)
     for (int64_t x = 0; x < units[n] + cut[n]; ++x) {
-      const int64_t t = free_at.top() + 2 * (int64_t)n + kUnitCost + (x < cut[n] ? kPartCost : 0);
-      free_at.pop();
-      free_at.push(t);
+      const int64_t t = free_at[0] + 2 * (int64_t)n + kUnitCost + (x < cut[n] ? kPartCost : 0);
+      replace_least(free_at, t);
       last = std::max(last, t);
     }
   return last + (any ? kJoinCost : 0);

@@ -8,6 +8,7 @@ Plans, tensor checks and workspaces for ``cp_attn_scored_fwd`` /
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import numbers
@@ -25,11 +26,22 @@ def relative_buckets(n_buckets: int, max_distance: int) -> List[int]:
     exact = n_buckets // 2
     if n_buckets < 2 or max_distance <= exact:
         raise CpError(1, "relative_buckets needs n_buckets >= 2 and max_distance > n_buckets / 2")
-    out = list(range(exact))
-    for dist in range(exact, max_distance + 1):
-        ratio = math.log(dist / exact) / math.log(max_distance / exact)
+    span = math.log(max_distance / exact)
+
+    def bucket(dist):
+        ratio = math.log(dist / exact) / span
         # the nudge keeps exact powers, whose quotient may fall just short, in their bucket
-        out.append(min(n_buckets - 1, exact + int(ratio * (n_buckets - exact) + 1e-9)))
+        return min(n_buckets - 1, exact + int(ratio * (n_buckets - exact) + 1e-9))
+    out = list(range(exact))
+    for b in range(exact, n_buckets):   # its distances: up to the first one of the next bucket
+        end = max_distance + 1
+        if b < n_buckets - 1:
+            end = min(end, int(exact * math.exp(span * (b + 1 - exact) / (n_buckets - exact))))
+            while end > len(out) and bucket(end - 1) > b:
+                end -= 1
+            while end <= max_distance and bucket(end) <= b:
+                end += 1
+        out += [b] * (end - len(out))
     return out
 
 
@@ -58,7 +70,7 @@ class ScorePlan:
         if torch.cuda.is_current_stream_capturing():
             raise CpError(1, "make the plan before the capture")
         if rel_buckets is not None:
-            rel_buckets = [int(b) for b in rel_buckets]
+            rel_buckets = list(rel_buckets)
             if not rel_buckets:
                 raise CpError(1, "rel_buckets is empty")
         sms = torch.cuda.get_device_properties(device).multi_processor_count
@@ -103,7 +115,12 @@ def build_plan(cu_seqlens, heads, prefix_len, bidirectional_prefix, rel_buckets,
         raise CpError(2, "prefix_len needs one entry per sample")
     pre = _b.cu_array(lens)
     nb = len(rel_buckets) if rel_buckets else 0
-    buckets = _b.cu_array(rel_buckets) if nb else None
+    buckets = None
+    if nb:
+        try:   # array copies whole numbers of any kind several times faster than ctypes
+            buckets = (ctypes.c_int32 * nb).from_buffer(array.array("i", rel_buckets))
+        except (TypeError, OverflowError):
+            raise CpError(1, "rel_buckets must be whole numbers of 32 bits") from None
     args = (cu, n, pre, int(bool(bidirectional_prefix)), int(heads), int(n_sms), buckets, nb)
     size = _b.lib().cp_score_plan_size(*args)
     if size == 0:
