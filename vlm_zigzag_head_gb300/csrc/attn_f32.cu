@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) f32_fwd_kernel(const F32Args a) {
   float* K = Q + tile_floats<D>();
   float* V = K + tile_floats<D>();
   float* P = V + tile_floats<D>();
-  const Tile32 tl = a.tiles[blockIdx.x];
+  const Tile32 tl = a.tiles[gridDim.x - 1 - blockIdx.x];   // longest walks first
   const int h = blockIdx.y, hk = h / (a.H / a.Hkv);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int t0 = tl.row0 - tl.seq0, nkeys = visible_keys(tl);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) f32_dq_kernel(const F32Args a) {
   float* K = dO + tile_floats<D>();
   float* V = K + tile_floats<D>();
   float* P = V + tile_floats<D>();
-  const Tile32 tl = a.tiles[blockIdx.x];
+  const Tile32 tl = a.tiles[gridDim.x - 1 - blockIdx.x];   // longest walks first
   const int h = blockIdx.y, hk = h / (a.H / a.Hkv);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int t0 = tl.row0 - tl.seq0, nkeys = visible_keys(tl);

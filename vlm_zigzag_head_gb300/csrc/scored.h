@@ -45,12 +45,14 @@ struct F32Args {
   float* dtable;                       // nullable [H][n_dist]
   bool add_dq, add_dkdv;               // add into zeroed dq / dk and dv instead of storing
 };
-// Blocks along a walk of up to `walk` tiles: as many as keep two tiles each and
-// the launch within two blocks per SM.  (768 tokens, 8 heads over 2, d = 128, one
-// block per walk against six: forward 168 -> 117 us, backward 1201 -> 276 us.)
+// Blocks along a walk of up to `walk` tiles: as many as keep the launch within four
+// blocks per SM, down to a tile each.  (Forward / backward us with one block per
+// walk, two blocks per SM and two tiles each, and this: 768 tokens, 8 heads over 2,
+// d = 128: 168 / 1201, 94 / 237, 79 / 191; 273 + 146 tokens, 4 over 2, d = 64: 29 / 70
+// and 21 / 46.  Six per SM: 88 / 203 for the former.)
 inline int f32_splits(int64_t blocks, int walk, int sms) {
-  int64_t s = 2LL * sms / (blocks > 0 ? blocks : 1);
-  if (s > walk / 2) s = walk / 2;
+  int64_t s = 4LL * sms / (blocks > 0 ? blocks : 1);
+  if (s > walk) s = walk;
   return s < 1 ? 1 : (int)s;
 }
 cudaError_t launch_f32_fwd(const F32Args& a, int d, cudaStream_t st);
