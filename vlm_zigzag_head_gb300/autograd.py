@@ -96,6 +96,7 @@ class QKNormRope(torch.autograd.Function):
     def forward(ctx, q, k, positions, q_weight, k_weight, desc, options):
         ctx.save_for_backward(q, k, positions, q_weight, k_weight)
         ctx.meta = (desc, options, q.stride(), k.stride())
+        ctx.set_materialize_grads(False)
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
 
     @staticmethod
@@ -107,8 +108,13 @@ class QKNormRope(torch.autograd.Function):
         # saved tensors may come back with other strides (offloaded, recomputed)
         if q.stride() != q_stride or k.stride() != k_stride:
             desc = norm_rope._prepare(q, k, positions, q_weight, k_weight, *options)
-        dq, dk, dqw, dkw = norm_rope._launch_bwd(desc, q, k, positions, _dense(dq_out),
-                                                 _dense(dk_out), q_weight, k_weight)
+        # an output that nothing used has no gradient
+        dq_out = torch.zeros_like(q, memory_format=torch.contiguous_format) if dq_out is None \
+            else _dense(dq_out)
+        dk_out = torch.zeros_like(k, memory_format=torch.contiguous_format) if dk_out is None \
+            else _dense(dk_out)
+        dq, dk, dqw, dkw = norm_rope._launch_bwd(desc, q, k, positions, dq_out, dk_out, q_weight,
+                                                 k_weight)
         return (dq if need[0] else None, dk if need[1] else None, None,
                 dqw.to(q_weight.dtype) if need[3] else None,
                 dkw.to(k_weight.dtype) if need[4] else None, None, None)
@@ -142,6 +148,7 @@ class CPAttentionScored(torch.autograd.Function):
         out, lse, out_lo = scored._launch_fwd(desc, q, k, v, plan, softmax_scale, residual=True)
         ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, out_lo)
         ctx.meta = (plan, softmax_scale, desc.softcap)
+        ctx.set_materialize_grads(False)   # lse's would be zeros to fill
         ctx.mark_non_differentiable(lse)
         return out, lse
 
