@@ -48,7 +48,9 @@
 // drain warpgroup to 168 (128 * 64 + 256 * 136 + 128 * 168 <= 512 * 128), so a
 // drain thread can hold its whole dQ row and free the TMEM at once.  Modified
 // scores need more: 144 and 152 (the same sum; 18688 tokens, 8 heads, capped: 1688
-// us against 1819; plain scores are better off with the first split, 1491 to 1527).
+// us against 1819; plain scores are better off with the first split, 1491 to 1527);
+// a table 152 and 144, the launch's total (1633 -> 1605, 12 288 tokens x 8 of 64
+// 595 -> 577; a cap without one 1642 -> 1654).
 //
 // With kCap or kBias (score.cuh) the P / dS warps recompute the modified scores
 // from S^T; under a cap dS also takes the factor 1 - tanh^2.  A table bias's
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 12) {
-    setmaxnreg_inc<kCap || kBias != SCORE_PLAIN ? 152 : 168>();
+    setmaxnreg_inc<kBias == SCORE_TABLE ? 144 : kCap || kBias != SCORE_PLAIN ? 152 : 168>();
     // ------------------------------------------------------------ dQ drain
     // thread = query row wq * 32 + lane of the tile (TMEM lane of dQ).  The
     // whole row comes out of TMEM first (its columns are free again for the
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) bulk_wait_all();   // every reduce-add finished before exit
     if (!ok) record_timeout(a.status, abort, 24);
   } else {
-    setmaxnreg_inc<kCap || kBias != SCORE_PLAIN ? 144 : 136>();
+    setmaxnreg_inc<kBias == SCORE_TABLE ? 152 : kCap || kBias != SCORE_PLAIN ? 144 : 136>();
     // ------------------------------------------------------------ P / dS
     // Two warpgroups share every query tile: warpgroup g (warps 4+4g .. 7+4g)
     // computes P^T / dS^T for query columns [64g, 64g + 64) of its key rows.
