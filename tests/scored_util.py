@@ -8,7 +8,7 @@ half step of the 16-bit operands (2^-8 for bf16 P and dS; 0 on the fp32 path):
 * a probability by e = 2 max delta + 2^-20 of its value (its row's normaliser errs as much; exp2);
 * out by (r + e) sum p|v|, plus half a step of the output type;
 * D = dout . out by eD = sum |dout| (r + e + 2^-16) sum p|v|: out is kept to 16 bits by its remainder;
-* with f16 operands (softmax scale above 1/4) dS is kept as an f16 multiple of 2^es, which ends at steps
+* with f16 operands (softmax scale above 1/4, or short samples) dS is kept as an f16 multiple of 2^es, which ends at steps
   of 2^(es - 24): half a step, `ds_floor`, on every visible pair;
 * dS = p (dP - D) w by (r + 2 e + 4e-6) |dS| + p (eD + d u sum|dout v|) + 4e-6 |p (dP - D)|;
 * products of these with k, q and dout sum the bounds, and n u of the magnitudes for n summed terms.

@@ -51,7 +51,7 @@ def _run(lens, prefix, both, H, Hkv, d, dtype, scale, cap, kind, gain=1.0, bias_
     pre = [prefix] * len(lens) if isinstance(prefix, int) else prefix
     s = O.Scores(softcap=cap, slopes=slopes, bias=bias, buckets=buckets, prefix_lens=pre, bidirectional=both)
     vals, tol = reference(q, k, v, cu, scale, s, dout, HALF_STEP[dtype] if dtype == "bf16" else 0.0,
-                          HALF_STEP[dtype], f16_ds_floor(v, dout) if dtype == "bf16" and scale > 0.25 else 0.0)
+                          HALF_STEP[dtype], f16_ds_floor(v, dout) if dtype == "bf16" else 0.0)
     check("out", out, vals["out"], tol["out"])
     check("lse", lse, vals["lse"], tol["lse"])
     for name, g in zip(("dq", "dk", "dv", "dbias"), got):

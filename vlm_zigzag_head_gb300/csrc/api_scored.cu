@@ -52,19 +52,36 @@ int f32_fwd_splits(const ScorePlanHeader& h) {
   return f32_splits((int64_t)h.n_tiles * h.H, h.max_walk, h.n_sms);
 }
 
+// f16 operands, above softmax scale 0.25 as cp_attn_fwd and cp_attn_bwd, and
+// - in a forward with a learned bias that a backward will follow (out_lo): the
+//   bias's gradient is a sum of dS = P (dP - D) in which rows cancel, so that an error
+//   of D = dO . O shows.  Before its own rounding dbias is off by 1e-3 to 3e-3
+//   (relative) with P in bf16, by 1e-4 to 2e-4 with P in f16.
+// - in a backward whose samples have at most 1024 tokens: few terms meet in a row of
+//   dq or dk, and f16 has the range for them (P of a row is 2^-10 or more on average).
+//   Errors against 64 bits, in units of the results' own rounding, over 120 packings:
+//   dq up to 2.1, 1.3 on average with dS in bf16, up to 1.5 and 1.06 on average so; it
+//   takes 4 to 5 us of launches (1024 tokens x 8 of 64: 23 -> 28; at 4096 x 16 223 ->
+//   249, for dq from 1.09 to 1.04 on average).  Longer rows keep
+//   bf16 and its range.
+constexpr int kF16Tokens = 1024;
+bool f16_operands(const ScorePlanHeader& h, cp_dtype_t dt, float scale, bool backward,
+                  bool bias_gradient) {
+  return dt == CP_BF16 && (uses_f16_operands(scale) ||
+                           (backward ? h.max_walk * kTile32 <= kF16Tokens : bias_gradient));
+}
+
 Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward,
           bool bf16_grads) {
   Ws w;
-  const bool f16 = dt == CP_BF16 && uses_f16_operands(scale);
+  const bool f16 = f16_operands(h, dt, scale, backward, h.n_dist > 0);
   const size_t T = h.T;
   size_t o = kStatusBytes;
   auto take = [&](size_t* at, bool need, size_t bytes) {
     *at = o;
     if (need) o = up256(o + bytes);
   };
-  // a learned bias's gradient wants a more exact forward (below): V's f16 copy too
-  const bool v16 = f16 || (dt == CP_BF16 && h.n_dist > 0 && !backward);
-  take(&w.scales, f16 || v16, sizeof(OpScales));
+  take(&w.scales, f16, sizeof(OpScales));
   take(&w.dtable, backward && h.n_dist > 0, (size_t)h.H * h.n_dist * sizeof(float));
   take(&w.dq, backward && bf16_grads, T * h.H * d * sizeof(float));
   take(&w.dk, backward && bf16_grads, T * Hkv * d * sizeof(float));
@@ -73,7 +90,7 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
   if (!backward) {
     const size_t splits = dt == CP_F32 ? f32_fwd_splits(h) : 1;
     const size_t rows = dt == CP_BF16 ? h.run_rows : splits > 1 ? splits * T : 0;
-    take(&w.v16, v16, T * Hkv * d * 2);
+    take(&w.v16, f16, T * Hkv * d * 2);
     take(&w.part_out, rows > 0, rows * h.H * d * sizeof(float));
     take(&w.part_lse, rows > 0, rows * h.H * sizeof(float));
   } else {
@@ -133,7 +150,7 @@ cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptr
   }
   c->bias = sc->slopes ? SCORE_SLOPES : sc->rel_bias ? SCORE_TABLE : SCORE_PLAIN;
   c->bf16 = dt == CP_BF16;
-  c->f16 = c->bf16 && uses_f16_operands(scale);
+  c->f16 = f16_operands(*c->h, dt, scale, backward, out_lo != nullptr && c->bias == SCORE_TABLE);
   c->ws = layout(*c->h, dt, Hkv, d, scale, backward, bf16_grads);
   if (out_lo && !c->bf16) return entry_fail(CP_ERR_DTYPE, "out_lo is for bf16 outputs only");
   if (T == 0) return CP_OK;
@@ -151,6 +168,16 @@ cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptr
   if (!aligned_to(ws, 256))
     return entry_fail(CP_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   return CP_OK;
+}
+
+// As bwd_kv_split, for groups of any size: CTAs that share a group of query heads.
+// (4096 tokens of 128, 6 heads over 2: 264 us with powers of two alone, 107 so;
+// 8192, 5 over 1: 826 and 234.)
+int group_split(int64_t n_items, int H, int Hkv, int sms) {
+  const int G = H / Hkv;
+  for (int s = 1; s < G; ++s)
+    if (G % s == 0 && n_items * Hkv * s >= 4LL * sms) return s;
+  return G;
 }
 
 cp_status_t check_gpu(bool bf16, int* sms) {
@@ -258,7 +285,7 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
   for (int i = 0; i < h->n_bwd; ++i)
     for (int u = 0; u < bi[i].k_len; ++u) {
       const Seg& s = runs[bi[i].run0];
-      nb += s.causal ? std::min<int64_t>(s.len, std::max<int64_t>(0, (int64_t)s.len - (u - s.delta)))
+      nb += s.causal ? std::min<int64_t>(s.len, std::max<int64_t>(0, s.len - (u - s.delta)))
                      : s.len;
     }
   const Tile32* ti = reinterpret_cast<const Tile32*>(b + h->tiles);
@@ -322,15 +349,9 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
                  "merge of partial results");
     return CP_OK;
   }
-  // PV on f16 operands above softmax scale 0.25, as cp_attn_fwd; and, where a
-  // backward will follow (out_lo), with a learned bias: its gradient is a sum of dS =
-  // P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  Before its
-  // own rounding dbias is off by 1e-3 to 3e-3 (relative) with P in bf16, by 1e-4 to
-  // 2e-4 with P in f16.
-  const bool f16 = c.f16 || (c.bias == SCORE_TABLE && out_lo != nullptr);
   const void* vsrc = v;
   OpScales* sc = reinterpret_cast<OpScales*>(w + c.ws.scales);
-  if (f16) {   // V's scaled copy
+  if (c.f16) {   // V's scaled copy
     const int64_t n = (int64_t)T * Hkv * d;
     void* v16 = w + c.ws.v16;
     ProfileScope prof(1, st, 2);
@@ -342,7 +363,7 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   const char* terr = nullptr;
   if (!make_tmap_thd(&a.tm_q_nat, q, T, H, d, 128, &terr) ||
       !make_tmap_thd(&a.tm_k_nat, k, T, Hkv, d, 128, &terr) ||
-      !make_tmap_thd(&a.tm_v_nat, vsrc, T, Hkv, d, 128, &terr, f16))
+      !make_tmap_thd(&a.tm_v_nat, vsrc, T, Hkv, d, 128, &terr, c.f16))
     return entry_fail(CP_ERR_CUDA, std::string("tensor map: ") + (terr ? terr : "?"));
   a.tm_q_text = a.tm_q_nat;   // no run of these plans is rank-local
   a.tm_k_text = a.tm_k_nat;
@@ -358,8 +379,8 @@ cp_status_t cp_attn_scored_fwd(const void* plan_h, const void* plan_d, const voi
   a.Hkv = Hkv;
   a.d = d;
   a.scale_log2 = scale * kLog2e;
-  a.f16_pv = f16 ? 1 : 0;
-  a.op_scales = f16 ? sc : nullptr;
+  a.f16_pv = c.f16 ? 1 : 0;
+  a.op_scales = c.f16 ? sc : nullptr;
   a.out = out;
   a.lse = lse;
   a.T = T;
@@ -419,7 +440,7 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   float* dq = static_cast<float*>(dq_out);
   float* dk = static_cast<float*>(dk_out);
   float* dv = static_cast<float*>(dv_out);
-  const int kv_split = c.bf16 ? bwd_kv_split(c.h->n_bwd, H, Hkv, sms) : 1;
+  const int kv_split = c.bf16 ? group_split(c.h->n_bwd, H, Hkv, sms) : 1;
   const int f32_split = c.bf16 ? 1 : f32_splits((int64_t)c.h->n_tiles * H, c.h->max_walk, sms);
   const bool add_dq = c.bf16 || f32_split > 1;
   const bool add_dkdv = c.bf16 ? kv_split > 1 || c.h->bwd_cut : f32_split > 1 || H > Hkv;
