@@ -622,3 +622,16 @@ def test_bounds_checked_build_meets_no_index_outside_a_tensor_in_cut_runs():
 def test_ends_of_the_cap_and_scale_ranges(scale, cap, kind):
     """Coefficients of the cap's polynomial that would leave the range of normal numbers."""
     _run([150, 33], 0, False, 2, 1, 64, "bf16", scale, cap, kind, 1.0 if scale < 1 else 0.125, seed=3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,H,Hkv", [([130], 6, 2), ([200, 40], 5, 1), ([1100], 6, 1), ([90], 12, 2)])
+def test_groups_that_are_no_power_of_two(lens, H, Hkv):
+    _run(lens, 0, False, H, Hkv, 64, "bf16", R64, 20.0, "slopes", seed=H)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("longest", [1024, 1025])
+def test_both_operand_types_of_the_backward(longest):
+    """The longest sample decides between f16 and bf16 dS: both within the bounds, with a short one beside."""
+    _run([longest, 60], [9, 5], True, 4, 2, 64, "bf16", R64, 0.0, (8, 32), seed=2)

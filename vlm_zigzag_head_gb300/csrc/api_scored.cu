@@ -61,9 +61,8 @@ int f32_fwd_splits(const ScorePlanHeader& h) {
 //   dq or dk, and f16 has the range for them (P of a row is 2^-10 or more on average).
 //   Errors against 64 bits, in units of the results' own rounding, over 120 packings:
 //   dq up to 2.1, 1.3 on average with dS in bf16, up to 1.5 and 1.06 on average so; it
-//   takes 4 to 5 us of launches (1024 tokens x 8 of 64: 23 -> 28; at 4096 x 16 223 ->
-//   249, for dq from 1.09 to 1.04 on average).  Longer rows keep
-//   bf16 and its range.
+//   takes 4 to 5 us of launches (1024 tokens x 8 of 64: 23 -> 28).  Longer rows keep
+//   bf16 and its range (4096 x 16 would go from 223 to 249 us).
 constexpr int kF16Tokens = 1024;
 bool f16_operands(const ScorePlanHeader& h, cp_dtype_t dt, float scale, bool backward,
                   bool bias_gradient) {
