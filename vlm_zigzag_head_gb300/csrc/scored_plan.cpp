@@ -160,7 +160,8 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
     if (buckets[i] < 0 || buckets[i] >= kMaxDist) return "a bucket is not in [0, 65536)";
     nb = std::max(nb, buckets[i] + 1);
   }
-  if (fwd * H > 0x7fffffffLL || bwd > 0x7fffffffLL || run_rows > 0x7fffffffLL) return "too many work units";
+  if (fwd * H > 0x7fffffffLL || bwd > 0x7fffffffLL || run_rows > 0x7fffffffLL)
+    return "too many work units";
   p.magic = kScorePlanMagic;
   p.T = cu[n_seqs];
   p.H = H;

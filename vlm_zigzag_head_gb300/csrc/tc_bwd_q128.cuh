@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           float4* d4 = reinterpret_cast<float4*>(dst + c * 32 + x);
-          if (kShared && (!kScored || a.add_dkdv)) {   // sub-CTAs of one group meet here (zeroed first)
+          if (kShared && (!kScored || a.add_dkdv)) {   // CTAs of one key tile meet (zeroed)
             red_add_v4(d4, v);
             continue;
           }
