@@ -443,10 +443,11 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  *   grad_dtype   of dq, dk, dv: CP_F32, or CP_BF16 with bf16 inputs (summed in
  *                fp32 in the workspace, rounded once)
  *   dt           CP_BF16: tensor cores; CP_F32: CUDA cores, fp32 throughout.  Above
- *                softmax_scale 0.25 (as cp_attn_fwd), in a forward with rel_bias and
- *                out_lo, and in a backward whose longest sample has at most 1024
- *                tokens, bf16 operands become f16, scaled by their tensor's largest
- *                finite magnitude: values below 2^-28 of it lose bits, below 2^-40 all
+ *                softmax_scale 0.25 (as cp_attn_fwd), and with rel_bias and out_lo, the
+ *                forward takes its probabilities and v as f16, v scaled by its largest
+ *                finite magnitude: values below 2^-28 of it lose bits, below 2^-40 all.
+ *                The backward keeps bf16 operands at any scale, so that a gradient's
+ *                relative error does not depend on the size of others
  *   score        slopes: NULL or device [H] fp32.  rel_bias: NULL or device, H x
  *                n_buckets, any strides (in elements).  softcap: 0 or in
  *                [1e-3, 1e4].  slopes and rel_bias exclude one another.

@@ -40,7 +40,7 @@ struct Ws {
   size_t dtable = 0, dq = 0, dk = 0, dv = 0;   // backward (dq, dk, dv: bf16 results)
   size_t table = 0;
   size_t v16 = 0, part_out = 0, part_lse = 0;  // forward (parts: fp32 results)
-  size_t lse2 = 0, D = 0, q16 = 0, k16 = 0;    // backward
+  size_t lse2 = 0, D = 0;                      // backward
   size_t total = 0;
 };
 
@@ -52,28 +52,23 @@ int f32_fwd_splits(const ScorePlanHeader& h) {
   return f32_splits((int64_t)h.n_tiles * h.H, h.max_walk, h.n_sms);
 }
 
-// f16 operands, above softmax scale 0.25 as cp_attn_fwd and cp_attn_bwd, and
-// - in a forward with a learned bias that a backward will follow (out_lo): the
-//   bias's gradient is a sum of dS = P (dP - D) in which rows cancel, so that an error
-//   of D = dO . O shows.  Before its own rounding dbias is off by 1e-3 to 3e-3
-//   (relative) with P in bf16, by 1e-4 to 2e-4 with P in f16.
-// - in a backward whose samples have at most 1024 tokens: few terms meet in a row of
-//   dq or dk, and f16 has the range for them (P of a row is 2^-10 or more on average).
-//   Errors against 64 bits, in units of the results' own rounding, over 120 packings:
-//   dq up to 2.1, 1.3 on average with dS in bf16, up to 1.5 and 1.06 on average so; it
-//   takes 4 to 5 us of launches (1024 tokens x 8 of 64: 23 -> 28).  Longer rows keep
-//   bf16 and its range (4096 x 16 would go from 223 to 249 us).
-constexpr int kF16Tokens = 1024;
-bool f16_operands(const ScorePlanHeader& h, cp_dtype_t dt, float scale, bool backward,
-                  bool bias_gradient) {
-  return dt == CP_BF16 && (uses_f16_operands(scale) ||
-                           (backward ? h.max_walk * kTile32 <= kF16Tokens : bias_gradient));
+// The forward's P V on f16 operands, above softmax scale 0.25 as cp_attn_fwd, and with a
+// learned bias that a backward will follow (out_lo): the bias's gradient is a sum of
+// dS = P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  Before
+// its own rounding dbias is off by 1e-3 to 3e-3 (relative) with P in bf16, by 1e-4 to
+// 2e-4 with P in f16.
+// The backward keeps bf16 at any scale.  dS follows the gradient's size, which differs
+// from sample to sample and from token to token; f16 with one power of two for the call
+// would leave a sample whose dout is 2^-14 of another's the bits of bf16, and one of
+// 2^-20 none (dq off by 8e-2 at 1e-6, 1.6e-3 so at any ratio).
+bool f16_operands(cp_dtype_t dt, float scale, bool bias_gradient) {
+  return dt == CP_BF16 && (uses_f16_operands(scale) || bias_gradient);
 }
 
 Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward,
           bool bf16_grads) {
   Ws w;
-  const bool f16 = f16_operands(h, dt, scale, backward, h.n_dist > 0);
+  const bool f16 = !backward && f16_operands(dt, scale, h.n_dist > 0);
   const size_t T = h.T;
   size_t o = kStatusBytes;
   auto take = [&](size_t* at, bool need, size_t bytes) {
@@ -96,8 +91,6 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
     const size_t plane = (size_t)ld_pitch(T) * h.H * sizeof(float);
     take(&w.lse2, true, 2 * plane);
     w.D = w.lse2 + plane;   // plane 1 directly after plane 0
-    take(&w.q16, f16, T * h.H * d * 2);
-    take(&w.k16, f16, T * Hkv * d * 2);
   }
   w.total = o;
   return w;
@@ -105,7 +98,7 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
 
 struct Call {
   const ScorePlanHeader* h = nullptr;
-  bool bf16 = false, f16 = false;
+  bool bf16 = false, f16 = false;   // f16: the forward's P V on f16 operands
   int bias = SCORE_PLAIN;
   Ws ws;
 };
@@ -149,7 +142,8 @@ cp_status_t check(const void* plan_h, const void* plan_d, const void* const* ptr
   }
   c->bias = sc->slopes ? SCORE_SLOPES : sc->rel_bias ? SCORE_TABLE : SCORE_PLAIN;
   c->bf16 = dt == CP_BF16;
-  c->f16 = f16_operands(*c->h, dt, scale, backward, out_lo != nullptr && c->bias == SCORE_TABLE);
+  c->f16 = !backward &&
+           f16_operands(dt, scale, out_lo != nullptr && c->bias == SCORE_TABLE);
   c->ws = layout(*c->h, dt, Hkv, d, scale, backward, bf16_grads);
   if (out_lo && !c->bf16) return entry_fail(CP_ERR_DTYPE, "out_lo is for bf16 outputs only");
   if (T == 0) return CP_OK;
@@ -466,21 +460,10 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   float* Dd = reinterpret_cast<float*>(w + c.ws.D);
   float* lse2 = reinterpret_cast<float*>(w + c.ws.lse2);
   const int64_t pitch = ld_pitch(T);
-  OpScales* sc = reinterpret_cast<OpScales*>(w + c.ws.scales);
-  void* q16 = w + c.ws.q16;
-  void* k16 = w + c.ws.k16;
   {
-    ProfileScope prof(3, st, c.f16 ? 3 : 1);
+    ProfileScope prof(3, st);
     ENTRY_CUDA(launch_bwd_preprocess(out, out_lo, dout, c.bf16, lse, T, H, d, Dd, lse2, pitch, st),
                "bwd preprocess");
-    if (c.f16) {   // S, dQ and dK on f16 operands
-      const void* srcs[4] = {q, k, v, dout};
-      void* dsts[2] = {q16, k16};
-      const int64_t n[4] = {(int64_t)T * H * d, (int64_t)T * Hkv * d, (int64_t)T * Hkv * d,
-                            (int64_t)T * H * d};
-      ENTRY_CUDA(launch_absmax_bf16(srcs, n, 4, sc, st), "max |Q|, |K|, |V|, |dO|");
-      ENTRY_CUDA(launch_to_f16_scaled(srcs, dsts, n, 2, sc, true, d, st), "f16 copies of Q, K");
-    }
   }
   if (!c.bf16) {
     F32Args a = f32_args(c, score, plan, s, Hkv, scale);
@@ -503,8 +486,8 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   } else {
     TcBwdArgs a{};
     const char* terr = nullptr;
-    if (!make_tmap_thd(&a.tm_q, c.f16 ? q16 : q, T, H, d, 128, &terr, c.f16) ||
-        !make_tmap_thd(&a.tm_k, c.f16 ? k16 : k, T, Hkv, d, kBwdTileK, &terr, c.f16) ||
+    if (!make_tmap_thd(&a.tm_q, q, T, H, d, 128, &terr) ||
+        !make_tmap_thd(&a.tm_k, k, T, Hkv, d, kBwdTileK, &terr) ||
         !make_tmap_thd(&a.tm_v, v, T, Hkv, d, kBwdTileK, &terr) ||
         !make_tmap_thd(&a.tm_do, dout, T, H, d, 128, &terr) ||
         !make_tmap_ld(&a.tm_ld, lse2, pitch, H, 128 + 4, &terr) ||
@@ -529,8 +512,6 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.add_dkdv = add_dkdv ? 1 : 0;
     a.isolate = 1;
     a.item_major = item_major((int64_t)c.h->n_bwd * Hkv * kv_split, sms) ? 1 : 0;
-    a.f16 = c.f16 ? 1 : 0;
-    a.op_scales = c.f16 ? sc : nullptr;
     a.score = s;
     ProfileScope prof(4, st);
     ENTRY_CUDA(launch_tc_bwd_scored(a, c.bias, st), "tensor-core scored backward");

@@ -34,6 +34,8 @@
 // then run on f16 operands: the host-made copies Q * 2^-eQ and K * 2^-eK, and
 // dS^T * 2^-eS rounded to f16 (three more mantissa bits than bf16); the
 // factors are undone in fp32 (OpScales).  dP^T and dV keep bf16 V, dO and P^T.
+// Modified scores keep bf16 throughout (kF16 = false): one power of two for all of a
+// call's dS would take the bits of samples and tokens with small gradients.
 //
 // Warp roles (512 threads; TMEM lane quarter of warp w is w % 4):
 //   warp 0       TMA producer: K, V once; Q and the lse2 / D rows per tile

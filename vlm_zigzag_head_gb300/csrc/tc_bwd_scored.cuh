@@ -6,15 +6,15 @@ namespace cpattn {
 
 // One instantiation serves key tiles of one CTA and shared ones: the epilogue asks
 // add_dkdv.
-template <int D, bool kF16>
+template <int D>
 cudaError_t launch_bwd_scored_d(const TcBwdArgs& a, int bias, cudaStream_t st) {
   if (a.score.cap_log2 > 0.f) {
-    if (bias == SCORE_SLOPES) return launch_q128<D, kF16, true, true, SCORE_SLOPES>(a, st);
-    if (bias == SCORE_TABLE) return launch_q128<D, kF16, true, true, SCORE_TABLE>(a, st);
-    return launch_q128<D, kF16, true, true, SCORE_PLAIN>(a, st);
+    if (bias == SCORE_SLOPES) return launch_q128<D, false, true, true, SCORE_SLOPES>(a, st);
+    if (bias == SCORE_TABLE) return launch_q128<D, false, true, true, SCORE_TABLE>(a, st);
+    return launch_q128<D, false, true, true, SCORE_PLAIN>(a, st);
   }
-  if (bias == SCORE_SLOPES) return launch_q128<D, kF16, true, false, SCORE_SLOPES>(a, st);
-  if (bias == SCORE_TABLE) return launch_q128<D, kF16, true, false, SCORE_TABLE>(a, st);
+  if (bias == SCORE_SLOPES) return launch_q128<D, false, true, false, SCORE_SLOPES>(a, st);
+  if (bias == SCORE_TABLE) return launch_q128<D, false, true, false, SCORE_TABLE>(a, st);
   return cudaErrorInvalidValue;   // plain scores: launch_tc_bwd_q128
 }
 

@@ -1,5 +1,5 @@
 // Picks the kernel of a launch with modified scores: one translation unit per
-// direction, head size and operand type.
+// direction, head size and (forward) operand type.
 #include "tc.h"
 
 #include <algorithm>
@@ -24,13 +24,13 @@ void fill_cap_polynomial(ScoreArgs* s, float scale_log2) {
   s->cap_reach = z / in;
 }
 
-#define CP_SCORED(dir, Args)                                                       \
-  cudaError_t launch_##dir##_scored_64_bf16(const Args&, int, cudaStream_t);       \
-  cudaError_t launch_##dir##_scored_64_f16(const Args&, int, cudaStream_t);        \
-  cudaError_t launch_##dir##_scored_128_bf16(const Args&, int, cudaStream_t);      \
-  cudaError_t launch_##dir##_scored_128_f16(const Args&, int, cudaStream_t);
-CP_SCORED(fwd, TcFwdArgs)
-CP_SCORED(bwd, TcBwdArgs)
+#define CP_SCORED(name, Args) cudaError_t launch_##name(const Args&, int, cudaStream_t);
+CP_SCORED(fwd_scored_64_bf16, TcFwdArgs)
+CP_SCORED(fwd_scored_64_f16, TcFwdArgs)
+CP_SCORED(fwd_scored_128_bf16, TcFwdArgs)
+CP_SCORED(fwd_scored_128_f16, TcFwdArgs)
+CP_SCORED(bwd_scored_64, TcBwdArgs)
+CP_SCORED(bwd_scored_128, TcBwdArgs)
 #undef CP_SCORED
 
 cudaError_t launch_tc_fwd_scored(const TcFwdArgs& a, int bias, cudaStream_t st) {
@@ -45,13 +45,12 @@ cudaError_t launch_tc_fwd_scored(const TcFwdArgs& a, int bias, cudaStream_t st) 
 cudaError_t launch_tc_bwd_scored(const TcBwdArgs& a, int bias, cudaStream_t st) {
   if (a.n_items == 0) return cudaSuccess;
   if (a.runs == nullptr || a.kv_split < 1 || (a.H / a.Hkv) % a.kv_split != 0 ||
-      (a.f16 && a.op_scales == nullptr))
+      a.f16)   // bf16 operands alone
     return cudaErrorInvalidValue;
   if (bias == SCORE_PLAIN && !(a.score.cap_log2 > 0.f)) return launch_tc_bwd_q128(a, st);
-  if (a.d == 64)
-    return a.f16 ? launch_bwd_scored_64_f16(a, bias, st) : launch_bwd_scored_64_bf16(a, bias, st);
+  if (a.d == 64) return launch_bwd_scored_64(a, bias, st);
   if (a.d != 128) return cudaErrorNotSupported;
-  return a.f16 ? launch_bwd_scored_128_f16(a, bias, st) : launch_bwd_scored_128_bf16(a, bias, st);
+  return launch_bwd_scored_128(a, bias, st);
 }
 
 }  // namespace cpattn
