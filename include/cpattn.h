@@ -236,9 +236,10 @@ cp_status_t cp_attn_fwd_noalloc(const void* q, const void* k, const void* v, cp_
  * on in §1 and §4.1 step 5):
  *     lse = log sum_p exp(lse_p),   out = sum_p exp(lse_p - lse) * out_p.
  * A part with lse = -inf contributes nothing; if every part is -inf the row
- * gets lse = -inf and out = 0.  The merged lse comes first (the largest
- * lse_p, then the sum of exp(lse_p - max)); out then sums the parts in index
- * order, each read once (16-byte loads when d is a multiple of 4).
+ * gets lse = -inf and out = 0; if one is NaN the row gets NaN.  The merged lse
+ * comes first (the largest lse_p, then the sum of exp(lse_p - max)); out then
+ * sums the parts in index order, each read once (16-byte loads when d is a
+ * multiple of 4).
  *
  *   part_out  [n_parts][rows][H][d] fp32       part_lse [n_parts][H][rows] fp32
  *   out       [rows][H][d], dtype out_dt       lse      [H][rows] fp32
@@ -434,7 +435,9 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  * -inf and no gradient.  Entries and slopes are otherwise finite; a slope adds up
  * to 2e-5 of itself to the rounding of a score.  A NaN or
  * infinity in q, k, v or dout stays within its sample; there it may reach every
- * row of the 128-row tiles that hold it, before the causal mask's rows too.
+ * row of the tiles that hold it (256 rows forward, 128 backward; 64 with CP_F32),
+ * before the causal mask's rows too.  A row with a score of NaN or plus infinity
+ * gets NaN in out, lse and dq; a score of minus infinity hides its key.
  * softmax_scale lies in [1e-10, 1e10].  tanh is off by at most 1e-6 of its value,
  * or by 2.5e-7 where scores of the same tile exceed three quarters of the cap.
  *

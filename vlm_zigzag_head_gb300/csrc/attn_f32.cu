@@ -204,13 +204,14 @@ __global__ void __launch_bounds__(kThreads) f32_fwd_kernel(const F32Args a) {
   for (int i = 0; i < 4; ++i) {
     const int r = 4 * ty + i;
     if (r >= tl.len) continue;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    // 0: no key seen; NaN: a score was, or overflowed, and out and lse are too
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     float* dst = a.out + (blockIdx.z * a.T + tl.row0 + r) * qs + h * D;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) dst[tx + 16 * j] = o[i][j] * inv;
     if (tx == 0)
       a.lse[((int64_t)blockIdx.z * a.H + h) * a.T + tl.row0 + r] =
-          l[i] > 0.f ? m[i] + logf(l[i]) : -INFINITY;
+          l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
   }
 }
 

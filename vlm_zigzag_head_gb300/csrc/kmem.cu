@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace cpattn {
 
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) lse_merge_kernel(int n_parts,
     float l_run = -INFINITY;
     for (int p = 0; p < n_parts; ++p) {
       const float lp = pl[p * stride_part_l + (long long)h * rows + row];
-      const float m = fmaxf(l_run, lp);
+      const float m = ptx::max_nan(l_run, lp);   // a NaN part makes the row NaN
       if (m == -INFINITY) continue;
       const float wa = expf(l_run - m), wb = expf(lp - m);
       const float tot = wa + wb;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) lse_merge_kernel(int n_parts,
 
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int o = 16; o > 0; o >>= 1) x = ptx::max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 __device__ __forceinline__ float warp_sum(float x) {
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) lse_merge_v4_kernel(int n_parts,
     const long long row = w - (long long)h * rows;
     const float* lp = pl + (long long)h * rows + row;
     float m = -INFINITY;
-    for (int p = lane; p < n_parts; p += 32) m = fmaxf(m, lp[p * stride_l]);
+    for (int p = lane; p < n_parts; p += 32) m = ptx::max_nan(m, lp[p * stride_l]);
     m = warp_max(m);
     const long long o = (row * H + h) * (long long)d + lane * 4;
     if (m == -INFINITY) {   // no part saw a key

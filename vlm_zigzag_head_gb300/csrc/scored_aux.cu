@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) cast_bf16_kernel(const Cast3 c) {
 }
 
 // Softmax parts: out = sum_p e^(lse_p - m) out_p / sum_p e^(lse_p - m), m the largest
-// lse_p.  Block (join, piece of its rows, head); D / 4 lanes per row.
+// lse_p (NaN if one is).  Block (join, piece of its rows, head); D / 4 lanes per row.
 constexpr int kJoinRows = 32;
 template <int D>
 __global__ void __launch_bounds__(kThreads)
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int t = blockIdx.y * kJoinRows + threadIdx.x / kLanes; t < end; t += kPass) {
     const int64_t row0 = h * run_rows + jn.run_row0 + t;
     float m = -INFINITY;
-    for (int p = 0; p < jn.parts; ++p) m = fmaxf(m, pl[row0 + (int64_t)p * jn.len]);
+    for (int p = 0; p < jn.parts; ++p) m = ptx::max_nan(m, pl[row0 + (int64_t)p * jn.len]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     if (m != -INFINITY) {

@@ -615,15 +615,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       if (valid && it.run_row0 >= 0 && a.runs == nullptr &&
           !CP_IN_RANGE(it.run_row0 + tq, 0, a.run_rows, a.status, 108))
         valid = false;
-      float lse_s = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-      const float inv = l > 0.f ? vmul / l : 0.f;
+      // l is 0 for a row that saw no key, and NaN where a score was (or overflowed):
+      // then lse is too, so that no merge or backward takes the row for an empty one
+      float lse_s = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+      const float inv = l == 0.f ? 0.f : vmul / l;
       const int flags = it.flags;
       const long long rrow =
           it.run_row0 >= 0 && a.runs == nullptr ? (long long)h * a.run_rows + it.run_row0 + tq : 0;
       float ca = 0.f, cb = 1.f;
       if (valid && !(flags & F_FIRST)) {
         const float lr = a.lse_run[rrow];
-        const float mm = fmaxf(lr, lse_s);
+        const float mm = max_nan(lr, lse_s);
         if (mm != -INFINITY) {
           const float wa = expf(lr - mm), wb = expf(lse_s - mm), tot = wa + wb;
           ca = wa / tot;
