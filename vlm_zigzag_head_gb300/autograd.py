@@ -148,13 +148,15 @@ class CPAttentionScored(torch.autograd.Function):
         out, lse, out_lo = scored._launch_fwd(desc, q, k, v, plan, softmax_scale, residual=True)
         ctx.save_for_backward(q, k, v, rel_bias, slopes, out, lse, out_lo)
         ctx.meta = (plan, softmax_scale, desc.softcap)
-        ctx.set_materialize_grads(False)   # lse's would be zeros to fill
+        ctx.set_materialize_grads(False)   # lse's would be zeros to fill; dout may be None
         ctx.mark_non_differentiable(lse)
         return out, lse
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout, _dlse):
+        if dout is None:   # what used out has no gradient for it
+            return (None,) * 8
         q, k, v, rel_bias, slopes, out, lse, out_lo = ctx.saved_tensors
         plan, scale, softcap = ctx.meta
         # saved tensors may come back elsewhere and with other strides (offloaded, recomputed)
