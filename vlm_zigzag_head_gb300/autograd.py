@@ -21,6 +21,7 @@ from __future__ import annotations
 from typing import Callable, Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
@@ -86,7 +87,14 @@ def _dense(x: torch.Tensor) -> torch.Tensor:
 
 
 def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether the call goes through its autograd function: for a backward to follow, or, with
+    a dual tensor, for the function to say that it has no forward-mode rule (a plain call would
+    drop the tangent, which reads as a derivative of zero)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    # no dual tensor outside a level; the private number saves a query per tensor
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 class QKNormRope(torch.autograd.Function):
@@ -128,7 +136,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
                  inv_freq: Optional[Sequence[float]] = None):
     """Differentiable :func:`~vlm_zigzag_head_gb300.cp_qk_norm_rope_fwd`: RMS norm of every head of q and k
     and the position rotation, in one pass.  Returns contiguous ``(q_out, k_out)``,
-    ready for :func:`cp_attention`; gradients flow to q, k and the weights."""
+    ready for :func:`cp_attention`; gradients flow to q, k and the weights (backward only:
+    forward mode raises).  To capture the backward into a graph, call
+    :func:`~vlm_zigzag_head_gb300.cp_qk_norm_rope_bwd`, which involves no leaves."""
     sections = None if sections is None else tuple(sections)
     inv_freq = None if inv_freq is None else tuple(inv_freq)
     options = (eps, theta, rot_dim, sections, interleaved, inv_freq)
@@ -177,7 +187,8 @@ def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan:
     """Differentiable packed causal attention with modified scores (see
     :func:`~vlm_zigzag_head_gb300.cp_attn_scored_fwd`): a tanh cap, a bias by distance, and the plan's
     bidirectional prefix.  q, k and v of any strides (copied where not contiguous).
-    Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias``.
+    Returns ``(out, lse)``; gradients flow to q, k, v and ``rel_bias`` (backward only: forward
+    mode raises).
     ``softmax_scale`` defaults to ``1/sqrt(d)``.  To capture the backward into a graph, call
     :func:`~vlm_zigzag_head_gb300.cp_attn_scored_bwd`, which involves no leaves."""
     if softmax_scale is None:
@@ -189,6 +200,6 @@ def cp_attention_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, plan:
     scored._check(q, k, v, plan)
     q, k, v = _dense(q), _dense(k), _dense(v)
     desc = scored._scores(q, softcap, slopes, rel_bias)
-    if not _wants_grad(q, k, v, rel_bias):
+    if not _wants_grad(q, k, v, rel_bias, slopes):
         return scored._launch_fwd(desc, q, k, v, plan, float(softmax_scale))
     return CPAttentionScored.apply(q, k, v, rel_bias, slopes, plan, float(softmax_scale), desc)
