@@ -220,13 +220,25 @@ __device__ __forceinline__ void load_row4(const float* p, bool vec, float (&v)[4
   }
 }
 
+// With a cap and a table P is kept as f16 for the bias's gradient.  P is a probability,
+// about 1 at most, and far keys of a long row have 2^-17 and less: f16 holds P 2^14 to
+// 2^-11 of its value from P = 2^-28 on, P itself from 2^-14 (2048 tokens, far buckets held
+// down to P of 2^-26: dbias off by 28 % and 5e-6).  The factor is a term of the exponent,
+// so it costs nothing; bf16 and fp32 round alike at any power of two, and it is taken out
+// where dQ, dK, dV and the sums of dS leave.
+template <bool kCap, int kBias>
+constexpr int kPLog2 = kCap && kBias == SCORE_TABLE ? 14 : 0;
+template <bool kCap, int kBias>
+constexpr float kPUnit = 1.f / (1 << kPLog2<kCap, kBias>);   // 1 / 2^kPLog2
+
 // P^T of 32 queries from their products (rs), with modified scores: the
 // probabilities as bf16 pairs in pk (the dV operand); in place over the products
 // what dS multiplies: P, or under a cap -P (1 - tanh^2), whose sign the factors of
 // dQ and dK undo.  kFast: every pair is
 // visible, the cap's polynomial holds and the bias is linear along the queries.
-// With a cap and a table, ph: P alone as f16 pairs, for the bias's gradient (2^-12 of
-// the value where registers for fp32 are lacking; bf16 pairs would show in it).
+// With a cap and a table, ph: P alone as f16 pairs, for the bias's gradient (registers
+// for fp32 are lacking; bf16 pairs would show in it).  All of these are then P times
+// 2^kPLog2.
 // mul: scale or cap in log2 units, inv its inverse.  x0: the half's first query in
 // the 64; ld: its lse2.
 template <bool kCap, int kBias, bool kFast>
@@ -236,7 +248,9 @@ __device__ __forceinline__ void score_columns(uint32_t (&rs)[32], uint32_t (&pk)
                                               const score::TileBias& tb, bool poly,
                                               const float* ld, bool vec, int first_vis,
                                               int end_vis) {
-  const uint64_t mul_2 = pack2(mul, mul), base2 = pack2(tb.base, tb.base);
+  float base = tb.base;
+  if constexpr (kPLog2<kCap, kBias> != 0) base += kPLog2<kCap, kBias>;
+  const uint64_t mul_2 = pack2(mul, mul), base2 = pack2(base, base);
   const float step = tb.step * inv;   // slopes, before `mul`
   const bool column = kBias != SCORE_PLAIN && (tb.both || tb.tab != nullptr);
 #pragma unroll
@@ -312,17 +326,19 @@ __device__ __forceinline__ void bias_grad(Diagonals& g, int x, float v, int lane
   g.all += w;
   if (x >= lane) g.up += w;
 }
+// mul: kPUnit (the far sums keep the factor to the end).
 __device__ __forceinline__ void add_distance(const ScoreArgs& s, int h, int dist, float v,
-                                             float& far_sum) {
+                                             float mul, float& far_sum) {
   const int d = dist < 0 ? -dist : dist;
   if (d >= s.n_dist - 1) far_sum += v;
-  else atomicAdd(s.dtable + (long long)h * s.n_dist + d, v);
+  else atomicAdd(s.dtable + (long long)h * s.n_dist + d, v * mul);
 }
-__device__ __forceinline__ void flush_far(const ScoreArgs& s, int h, int lane, float& far_sum) {
+__device__ __forceinline__ void flush_far(const ScoreArgs& s, int h, int lane, float mul,
+                                          float& far_sum) {
   float v = far_sum;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) atomicAdd(s.dtable + (long long)h * s.n_dist + s.n_dist - 1, v);
+  if (lane == 0) atomicAdd(s.dtable + (long long)h * s.n_dist + s.n_dist - 1, v * mul);
   far_sum = 0.f;
 }
 
@@ -655,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     // dQ = scale * (dS K); with f16 operands also undo the dS and K factors
-    const float dq_scale = kCap ? -a.scale : a.scale;   // dS comes negated under a cap
+    // dS comes negated under a cap, and times 2^kPLog2
+    const float dq_scale = (kCap ? -a.scale : a.scale) * kPUnit<kCap, kBias>;
     const float dq_mul = kF16 ? dq_scale * a.op_scales->dq_mul : dq_scale;
     uint8_t* stg = smem + L::kStg + wq * L::kStgWarp;
     uint8_t* my_row = stg + lane * 128;
@@ -733,6 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int jt = 0, hq = hq0;       // tile and query head, as the producers walk them
     float far_sum = 0.f;        // this thread's dS beyond the table (kBias: table),
     uint64_t far2 = 0;          // and the same by even and odd queries
+    [[maybe_unused]] constexpr float bias_mul = kPUnit<kCap, kBias>;
     for (int i = 0; ok && i < n_all; ++i) {
       const int st = i % kQStages;
       if (!mbar_wait(&bars->q_full[st], (i / kQStages) & 1, lim, abort)) {
@@ -865,9 +883,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tb.tab != nullptr) {
           // distances base + L - 32, base + L and base + L + 32 of this warp's keys
           const int base = ti.rel + row0 - (warp & 3) * 32 + lane;
-          add_distance(a.score, hq, base - 32, diag[0].all - diag[0].up, far_sum);
-          add_distance(a.score, hq, base, diag[0].up + (diag[1].all - diag[1].up), far_sum);
-          add_distance(a.score, hq, base + 32, diag[1].up, far_sum);
+          add_distance(a.score, hq, base - 32, diag[0].all - diag[0].up, bias_mul, far_sum);
+          add_distance(a.score, hq, base, diag[0].up + (diag[1].all - diag[1].up), bias_mul,
+                       far_sum);
+          add_distance(a.score, hq, base + 32, diag[1].up, bias_mul, far_sum);
         }
       }
       if (++jt == n_qt) {
@@ -875,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float f0, f1;
           unpack2(far2, f0, f1);
           far_sum += f0 + f1;
-          flush_far(a.score, hq, lane, far_sum);
+          flush_far(a.score, hq, lane, bias_mul, far_sum);
           far2 = 0;
         }
         jt = 0;
@@ -904,8 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<__nv_bfloat16*>(g == 0 ? a.dk : a.dv) +
           ((long long)(it.k_row0 + u) * a.Hkv + hk) * D;   // dkv_bf16: DK_TEXT items only
       const bool first = (it.flags & F_FIRST) != 0;
-      const float dk_scale = kCap ? -a.scale : a.scale;
-      const float mul = g == 0 ? (kF16 ? dk_scale * a.op_scales->dk_mul : dk_scale) : 1.f;
+      constexpr float p_unit = kPUnit<kCap, kBias>;
+      const float dk_scale = (kCap ? -a.scale : a.scale) * p_unit;
+      const float mul = g == 0 ? (kF16 ? dk_scale * a.op_scales->dk_mul : dk_scale) : p_unit;
       const uint32_t col = g == 0 ? C::kDK : C::kDV;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
