@@ -184,7 +184,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   p.bwd = o; o = up256(o + bwd * sizeof(BwdItem));
   p.runs = o; o = up256(o + bwd * sizeof(Seg));
   p.units = o;
-  o = up256(o + (uint64_t)(p.n_units + p.grid + 1) * sizeof(int32_t));
+  o = up256(o + ((uint64_t)p.n_units + p.grid + 1) * sizeof(int32_t));
   p.buckets = o; o = up256(o + (uint64_t)n_dist * sizeof(int32_t));
   p.tiles = o; o = up256(o + tiles * sizeof(Tile32));
   p.joins = o; o = up256(o + joins * sizeof(Join));
