@@ -1,5 +1,7 @@
 """Score plans at the ends of what their sizes can hold (host only)."""
 import ctypes
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -30,3 +32,32 @@ def test_more_units_than_32_bits_hold(cplib):
     n = (2 ** 31 - 1) // 127 + 1
     assert _size(np.arange(n + 1, dtype=np.int32), 127, 152) == 0
     assert b"too many work units" in B.lib().cp_last_error()
+
+
+CHILD = """
+import ctypes, resource, sys
+lib = ctypes.CDLL(sys.argv[1])
+lib.cp_score_plan_size.restype = ctypes.c_size_t
+lib.cp_last_error.restype = ctypes.c_char_p
+def size():
+    cu = (ctypes.c_int32 * 2)(0, 2 ** 31 - 1)
+    return lib.cp_score_plan_size(cu, 1, None, 0, 1, 152, None, 0)
+if sys.argv[2] == "free":
+    assert size() > 0
+else:   # no room for the lists of tiles by length (16 million entries)
+    with open("/proc/self/statm") as f:
+        used = int(f.read().split()[0]) * resource.getpagesize()
+    soft, hard = resource.getrlimit(resource.RLIMIT_AS)
+    resource.setrlimit(resource.RLIMIT_AS, (used + (32 << 20), hard))
+    assert size() == 0 and lib.cp_last_error()
+    resource.setrlimit(resource.RLIMIT_AS, (soft, hard))
+    assert size() > 0
+"""
+
+
+@pytest.mark.parametrize("memory", ["free", "short"])
+def test_no_exception_leaves_the_size_query(cplib, memory):
+    """Out of memory is an error like any other: 0 and a message."""
+    r = subprocess.run([sys.executable, "-c", CHILD, B.lib_path(), memory], capture_output=True, text=True,
+                       timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stderr[-1000:])

@@ -235,14 +235,16 @@ extern "C" {
 size_t cp_score_plan_size(const int32_t* cu, int n_seqs, const int32_t* prefix_lens,
                           int bidirectional, int H, int n_sms, const int32_t* buckets,
                           int n_dist) {
-  ScorePlanHeader h;
-  const std::string err = score_plan_layout(cu, n_seqs, prefix_lens, bidirectional != 0, H, n_sms,
-                                            buckets, n_dist, &h);
-  if (!err.empty()) {
+  try {
+    ScorePlanHeader h;
+    const std::string err = score_plan_layout(cu, n_seqs, prefix_lens, bidirectional != 0, H, n_sms,
+                                              buckets, n_dist, &h);
+    if (err.empty()) return h.total;
     set_last_error(err);
-    return 0;
+  } catch (const std::exception& ex) {   // its lists may not fit in memory
+    set_last_error(ex.what());
   }
-  return h.total;
+  return 0;
 }
 
 cp_status_t cp_score_plan_build(const int32_t* cu, int n_seqs, const int32_t* prefix_lens,
