@@ -64,9 +64,10 @@ struct OpScales {
   float pad[3];
 };
 static_assert(sizeof(OpScales) == 64, "OpScales layout");
-// max |x| of up to 4 bf16 tensors of n[t] elements (multiples of 8, 16-byte
-// aligned) into sc->amax[t] (atomic max over the bit patterns; NaN counts as
-// the largest, and then gives the factor 1).
+// max |x| over the finite elements of up to 4 bf16 tensors of n[t] elements
+// (multiples of 8, 16-byte aligned) into sc->amax[t] (atomic max over the bit
+// patterns; NaN and infinities are left out, and a tensor without a normal
+// number gives the factor 1).
 cudaError_t launch_absmax_bf16(const void* const* src, const int64_t* n, int n_tensors,
                                OpScales* sc, cudaStream_t st);
 // dst[t] = f16(src[t] * 2^-e_t) for up to 2 bf16 tensors of n[t] elements,

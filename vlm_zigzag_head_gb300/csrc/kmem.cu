@@ -316,9 +316,10 @@ __device__ __forceinline__ T pick4(const T (&x)[4], int t) {
 }
 
 // Per block (tensor blockIdx.y): max over the finite |x| of its share, as the bit
-// pattern of a non-negative float (bf16 bits shifted into the high half; a NaN or
-// an infinity would take the scale from every other row), then one atomic max (one per warp, all on one address, took 30 us on four tensors of
-// 6.6 MB; one per block takes 7).
+// pattern of a non-negative float (bf16 bits shifted into the high half), then one
+// atomic max.  A NaN or an infinity would take the scale from every other row.  One
+// atomic per warp, all on one address, took 30 us on four tensors of 6.6 MB; one per
+// block takes 7.
 __global__ void __launch_bounds__(kThreads) absmax_bf16_kernel(Ptrs4 p, uint32_t* amax) {
   const int t = blockIdx.y;
   const uint4* s = pick4(p.s, t);
