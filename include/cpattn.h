@@ -449,8 +449,10 @@ cp_status_t cp_score_plan_pairs(const void* plan_h, int64_t* fwd, int64_t* bwd, 
  *                softmax_scale 0.25 (as cp_attn_fwd), and with rel_bias and out_lo, the
  *                forward takes its probabilities and v as f16, v scaled by its largest
  *                finite magnitude: values below 2^-28 of it lose bits, below 2^-40 all.
- *                The backward keeps bf16 operands at any scale, so that a gradient's
- *                relative error does not depend on the size of others
+ *                The backward keeps bf16 operands at any scale, or f16 in samples of up to
+ *                1024 tokens whose non-zero rows of dout lie within 2^8 of one another in
+ *                norm, scaled by the sample's own magnitudes: a sample's gradients do not
+ *                depend on others, nor a small gradient's precision on larger ones
  *   score        slopes: NULL or device [H] fp32.  rel_bias: NULL or device, H x
  *                n_buckets, any strides (in elements).  softcap: 0 or in
  *                [1e-3, 1e4].  slopes and rel_bias exclude one another.

@@ -36,11 +36,11 @@ const ScorePlanHeader* header(const void* plan_h) {
 // Offsets into the workspace of either direction.  What has to start at zero
 // comes first, so that one memset clears it.
 struct Ws {
-  size_t status = 0, scales = 0;
+  size_t status = 0, scales = 0, ranges = 0;
   size_t dtable = 0, dq = 0, dk = 0, dv = 0;   // backward (dq, dk, dv: bf16 results)
   size_t table = 0;
   size_t v16 = 0, part_out = 0, part_lse = 0;  // forward (parts: fp32 results)
-  size_t lse2 = 0, D = 0;                      // backward
+  size_t lse2 = 0, D = 0, q16 = 0, k16 = 0;    // backward
   size_t total = 0;
 };
 
@@ -57,13 +57,14 @@ int f32_fwd_splits(const ScorePlanHeader& h) {
 // dS = P (dP - D) in which rows cancel, so that an error of D = dO . O shows.  Before
 // its own rounding dbias is off by 1e-3 to 3e-3 (relative) with P in bf16, by 1e-4 to
 // 2e-4 with P in f16.
-// The backward keeps bf16 at any scale.  dS follows the gradient's size, which differs
-// from sample to sample and from token to token; f16 with one power of two for the call
-// would leave a sample whose dout is 2^-14 of another's the bits of bf16, and one of
-// 2^-20 none (dq off by 8e-2 at 1e-6, 1.6e-3 so at any ratio).
+// The backward's types do not follow the scale: dS is bf16, but f16 in the short samples
+// whose range allows it (operand_range.cuh).  One power of two for all of a call's dS
+// would leave a sample whose dout is 2^-20 of another's next to none of f16's bits (512
+// tokens of 128: dq off by 8e-2 at 1e-6; in bf16 by 1.8e-3 at any ratio).
 bool f16_operands(cp_dtype_t dt, float scale, bool bias_gradient) {
   return dt == CP_BF16 && (uses_f16_operands(scale) || bias_gradient);
 }
+bool has_ranges(const ScorePlanHeader& h, cp_dtype_t dt) { return dt == CP_BF16 && h.n_short > 0; }
 
 Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, bool backward,
           bool bf16_grads) {
@@ -75,7 +76,9 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
     *at = o;
     if (need) o = up256(o + bytes);
   };
+  const bool ranges = backward && has_ranges(h, dt);
   take(&w.scales, f16, sizeof(OpScales));
+  take(&w.ranges, ranges, (size_t)h.n_seqs * Hkv * sizeof(OperandRange));
   take(&w.dtable, backward && h.n_dist > 0, (size_t)h.H * h.n_dist * sizeof(float));
   take(&w.dq, backward && bf16_grads, T * h.H * d * sizeof(float));
   take(&w.dk, backward && bf16_grads, T * Hkv * d * sizeof(float));
@@ -91,6 +94,8 @@ Ws layout(const ScorePlanHeader& h, cp_dtype_t dt, int Hkv, int d, float scale, 
     const size_t plane = (size_t)ld_pitch(T) * h.H * sizeof(float);
     take(&w.lse2, true, 2 * plane);
     w.D = w.lse2 + plane;   // plane 1 directly after plane 0
+    take(&w.q16, ranges, T * h.H * d * 2);
+    take(&w.k16, ranges, T * Hkv * d * 2);
   }
   w.total = o;
   return w;
@@ -462,10 +467,21 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
   float* Dd = reinterpret_cast<float*>(w + c.ws.D);
   float* lse2 = reinterpret_cast<float*>(w + c.ws.lse2);
   const int64_t pitch = ld_pitch(T);
+  const bool item_types = has_ranges(*c.h, dt);
+  OperandRange* ranges = reinterpret_cast<OperandRange*>(w + c.ws.ranges);
+  void* q16 = w + c.ws.q16;
+  void* k16 = w + c.ws.k16;
   {
-    ProfileScope prof(3, st);
+    ProfileScope prof(3, st, item_types ? 3 : 1);
     ENTRY_CUDA(launch_bwd_preprocess(out, out_lo, dout, c.bf16, lse, T, H, d, Dd, lse2, pitch, st),
                "bwd preprocess");
+    if (item_types) {   // S, dQ and dK of short samples on f16 operands
+      const Tile32* tiles = reinterpret_cast<const Tile32*>(plan + c.h->tiles);
+      ENTRY_CUDA(launch_operand_ranges(tiles, c.h->n_tiles, q, k, v, dout, H, Hkv, d, ranges, st),
+                 "ranges of short samples");
+      ENTRY_CUDA(launch_f16_operands(tiles, c.h->n_tiles, q, k, H, Hkv, d, ranges, q16, k16, st),
+                 "f16 copies of short samples");
+    }
   }
   if (!c.bf16) {
     F32Args a = f32_args(c, score, plan, s, Hkv, scale);
@@ -490,6 +506,8 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     const char* terr = nullptr;
     if (!make_tmap_thd(&a.tm_q, q, T, H, d, 128, &terr) ||
         !make_tmap_thd(&a.tm_k, k, T, Hkv, d, kBwdTileK, &terr) ||
+        (item_types && (!make_tmap_thd(&a.tm_q16, q16, T, H, d, 128, &terr, true) ||
+                        !make_tmap_thd(&a.tm_k16, k16, T, Hkv, d, kBwdTileK, &terr, true))) ||
         !make_tmap_thd(&a.tm_v, v, T, Hkv, d, kBwdTileK, &terr) ||
         !make_tmap_thd(&a.tm_do, dout, T, H, d, 128, &terr) ||
         !make_tmap_ld(&a.tm_ld, lse2, pitch, H, 128 + 4, &terr) ||
@@ -514,6 +532,8 @@ cp_status_t cp_attn_scored_bwd(const void* plan_h, const void* plan_d, const voi
     a.add_dkdv = add_dkdv ? 1 : 0;
     a.isolate = 1;
     a.item_major = item_major((int64_t)c.h->n_bwd * Hkv * kv_split, sms) ? 1 : 0;
+    a.ranges = item_types ? ranges : nullptr;
+    a.n_samples = c.h->n_seqs;
     a.score = s;
     ProfileScope prof(4, st);
     ENTRY_CUDA(launch_tc_bwd_scored(a, c.bias, st), "tensor-core scored backward");

@@ -56,6 +56,7 @@ struct BwdItem {
   int32_t dk_mode;  // DK_TEXT: dk/dv natural rows k_row0..; DK_PREFIX_SLOT: slot buffer
   int32_t dk_row0;  // row inside the prefix slot buffer (DK_PREFIX_SLOT)
   int32_t slot;     // prefix slot: rank 0..P-1, or P for the prefix queries' own term
+                    // (scored plans, DK_TEXT alone: the item's sample)
   int32_t flags;    // F_FIRST: overwrite the destination, else accumulate
   int32_t run0;     // all-steps plans: index of the first run in the run list; else -1
   int32_t pad[7];

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "scored_plan.h"
+#include "tc.h"
 
 namespace cpattn {
 
@@ -25,6 +26,17 @@ cudaError_t launch_cast_bf16(const float* const (&src)[3], void* const (&dst)[3]
 cudaError_t launch_join_parts(const Join* joins, int n_joins, const float* po, const float* pl,
                               int64_t run_rows, int H, int d, int64_t T, void* out, void* out_lo,
                               float* lse, cudaStream_t st);
+
+// ---- f16 operands of short samples' backward (scored_aux.cu, operand_range.cuh) ----
+// One block per 64-row tile and KV head; tiles of samples of more than kF16Tokens
+// tokens are passed over.  ranges [n_samples][Hkv], zeroed before.
+cudaError_t launch_operand_ranges(const Tile32* tiles, int n_tiles, const void* q, const void* k,
+                                  const void* v, const void* dout, int H, int Hkv, int d,
+                                  OperandRange* ranges, cudaStream_t st);
+// Scaled f16 copies of the rows of Q and K whose sample and KV head take f16.
+cudaError_t launch_f16_operands(const Tile32* tiles, int n_tiles, const void* q, const void* k,
+                                int H, int Hkv, int d, const OperandRange* ranges, void* q16,
+                                void* k16, cudaStream_t st);
 
 // ---- fp32 inputs: CUDA cores (attn_f32.cu) ---------------------------------------
 struct F32Args {

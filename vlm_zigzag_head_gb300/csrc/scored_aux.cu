@@ -1,9 +1,10 @@
 // The small kernels around attention with modified scores: the learned bias laid
 // out by distance and its gradient summed back (a few KB a head: bound by the
-// launch), the join of partial results, and the gradients' rounding to bf16 (one
-// pass each, bound by memory).
+// launch), the join of partial results, the gradients' rounding to bf16, and the
+// ranges and f16 copies of short samples (one pass each, bound by memory).
 #include <cuda_bf16.h>
 
+#include "operand_range.cuh"
 #include "ptx.cuh"
 #include "scored.h"
 
@@ -111,7 +112,154 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Eight bf16 of one row's piece.
+struct Piece {
+  uint32_t w[4];
+  __device__ __forceinline__ explicit Piece(const __nv_bfloat16* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  // bit pattern of the largest finite magnitude, as fp32
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = (w[i] & 0x7fffu) << 16, hi = w[i] & 0x7fff0000u;
+      m = max(m, lo < 0x7f800000u ? lo : 0u);
+      m = max(m, hi < 0x7f800000u ? hi : 0u);
+    }
+    return m;
+  }
+  __device__ __forceinline__ bool any() const {
+    return ((w[0] | w[1] | w[2] | w[3]) & 0x7fff7fffu) != 0;
+  }
+  __device__ __forceinline__ float squares() const {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+      s = fmaf(lo, lo, fmaf(hi, hi, s));
+    }
+    return s;
+  }
+};
+
+// D / 8 lanes per row; block: a tile's rows for one KV head.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    operand_range_kernel(const Tile32* tiles, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                         const __nv_bfloat16* v, const __nv_bfloat16* dout, int H, int Hkv,
+                         OperandRange* ranges) {
+  constexpr int kLanes = D / 8, kRows = kThreads / kLanes;
+  const Tile32 tl = tiles[blockIdx.x];
+  if (tl.seq_len > kF16Tokens) return;
+  const int hk = blockIdx.y, G = H / Hkv;
+  const int e = threadIdx.x % kLanes * 8, r0 = threadIdx.x / kLanes;
+  // the row's sum of squares in all its lanes; rows that are not there count as zero
+  auto row_squares = [&](const Piece& p, bool there, bool& any) {
+    float s = there ? p.squares() : 0.f;
+    int a = there && p.any();
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      a |= __shfl_xor_sync(0xffffffffu, a, o);
+    }
+    any = a != 0;
+    return s;
+  };
+  uint32_t m[5] = {0, 0, 0, 0, 0};   // q, k, v2, g2, g2_least
+  bool any;
+  for (int base = 0; base < tl.len; base += kRows) {
+    const bool there = base + r0 < tl.len;
+    const int64_t at = ((int64_t)(tl.row0 + min(base + r0, tl.len - 1)) * Hkv + hk) * D + e;
+    if (there) m[1] = max(m[1], Piece(k + at).largest());
+    m[2] = max(m[2], __float_as_uint(row_squares(Piece(v + at), there, any)));
+  }
+  const int rows = tl.len * G;   // (token, query head) pairs
+  for (int base = 0; base < rows; base += kRows) {
+    const int x = min(base + r0, rows - 1);
+    const bool there = base + r0 < rows;
+    const int64_t at = ((int64_t)(tl.row0 + x / G) * H + hk * G + x % G) * D + e;
+    if (there) m[0] = max(m[0], Piece(q + at).largest());
+    const float s = row_squares(Piece(dout + at), there, any);
+    m[3] = max(m[3], __float_as_uint(s));
+    // a row whose squares underflow is not zero: it counts as the smallest number
+    if (any) m[4] = max(m[4], ~__float_as_uint(fmaxf(s, 1e-38f)));
+  }
+  __shared__ uint32_t part[kThreads / 32][5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    m[i] = __reduce_max_sync(0xffffffffu, m[i]);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][i] = m[i];
+  }
+  __syncthreads();
+  if (threadIdx.x >= 5) return;
+  uint32_t top = 0;
+  for (int w = 0; w < kThreads / 32; ++w) top = max(top, part[w][threadIdx.x]);
+  // the fields q, k, v2, g2, g2_least lie in this order
+  uint32_t* dst = &ranges[(int64_t)tl.sample * Hkv + hk].q + threadIdx.x;
+  if (top != 0) atomicMax(dst, top);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+    f16_operands_kernel(const Tile32* tiles, const __nv_bfloat16* q, const __nv_bfloat16* k, int H,
+                        int Hkv, const OperandRange* ranges, uint4* q16, uint4* k16) {
+  constexpr int kPieces = D / 8;
+  const Tile32 tl = tiles[blockIdx.x];
+  if (tl.seq_len > kF16Tokens) return;
+  const int hk = blockIdx.y, G = H / Hkv;
+  const Operands ops = choose_operands(ranges[(int64_t)tl.sample * Hkv + hk]);
+  if (!ops.f16) return;
+  auto copy = [](const __nv_bfloat16* src, uint4* dst, int64_t piece, float f) {
+    const Piece p(src + piece * 8);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = ptx::pack_f16x2(__uint_as_float(p.w[i] << 16) * f,
+                             __uint_as_float(p.w[i] & 0xffff0000u) * f);
+    dst[piece] = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+  const float fq = range_pow2(-ops.eq), fk = range_pow2(-ops.ek);
+  for (int i = threadIdx.x; i < tl.len * G * kPieces; i += kThreads) {
+    const int x = i / kPieces;
+    copy(q, q16, ((int64_t)(tl.row0 + x / G) * H + hk * G + x % G) * kPieces + i % kPieces, fq);
+  }
+  for (int i = threadIdx.x; i < tl.len * kPieces; i += kThreads)
+    copy(k, k16, ((int64_t)(tl.row0 + i / kPieces) * Hkv + hk) * kPieces + i % kPieces, fk);
+}
+
 }  // namespace
+
+cudaError_t launch_operand_ranges(const Tile32* tiles, int n_tiles, const void* q, const void* k,
+                                  const void* v, const void* dout, int H, int Hkv, int d,
+                                  OperandRange* ranges, cudaStream_t st) {
+  const auto* qb = static_cast<const __nv_bfloat16*>(q);
+  const auto* kb = static_cast<const __nv_bfloat16*>(k);
+  const auto* vb = static_cast<const __nv_bfloat16*>(v);
+  const auto* gb = static_cast<const __nv_bfloat16*>(dout);
+  const dim3 grid(n_tiles, Hkv);
+  if (d == 64)
+    operand_range_kernel<64><<<grid, kThreads, 0, st>>>(tiles, qb, kb, vb, gb, H, Hkv, ranges);
+  else
+    operand_range_kernel<128><<<grid, kThreads, 0, st>>>(tiles, qb, kb, vb, gb, H, Hkv, ranges);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_f16_operands(const Tile32* tiles, int n_tiles, const void* q, const void* k,
+                                int H, int Hkv, int d, const OperandRange* ranges, void* q16,
+                                void* k16, cudaStream_t st) {
+  const auto* qb = static_cast<const __nv_bfloat16*>(q);
+  const auto* kb = static_cast<const __nv_bfloat16*>(k);
+  auto* qo = static_cast<uint4*>(q16);
+  auto* ko = static_cast<uint4*>(k16);
+  const dim3 grid(n_tiles, Hkv);
+  if (d == 64)
+    f16_operands_kernel<64><<<grid, kThreads, 0, st>>>(tiles, qb, kb, H, Hkv, ranges, qo, ko);
+  else
+    f16_operands_kernel<128><<<grid, kThreads, 0, st>>>(tiles, qb, kb, H, Hkv, ranges, qo, ko);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_join_parts(const Join* joins, int n_joins, const float* po, const float* pl,
                               int64_t run_rows, int H, int d, int64_t T, void* out, void* out_lo,

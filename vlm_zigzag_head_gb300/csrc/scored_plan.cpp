@@ -124,6 +124,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   if (n_dist < 0 || n_dist > kMaxDist) return "n_dist must be in [0, 65536]";
   if (n_dist > 0 && !buckets) return "buckets is NULL";
   int64_t fwd = 0, bwd = 0, tiles = 0, walk = 0, joins = 0, run_rows = 0, key_tiles = 0;
+  int64_t n_short = 0;
   for (int i = 0; i < n_seqs; ++i) {
     const int64_t len = (int64_t)cu[i + 1] - cu[i];
     if (len < 0) {
@@ -136,6 +137,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
       return buf;
     }
     tiles += cdiv(len, kTile32);
+    if (len <= kF16Tokens) n_short += cdiv(len, kTile32);
     walk = std::max(walk, cdiv(len, kTile32));
   }
   ScorePlanHeader p{};
@@ -176,6 +178,7 @@ std::string score_plan_layout(const int32_t* cu, int n_seqs, const int32_t* pref
   p.run_rows = (int32_t)run_rows;
   p.bwd_cut = bwd > key_tiles ? 1 : 0;
   p.max_walk = (int32_t)walk;
+  p.n_short = (int32_t)n_short;
   p.n_units = (int32_t)(fwd * H);
   p.grid = std::min<int32_t>(p.n_units, sms);
   p.item_major = item_major(p.n_units, sms) ? 1 : 0;
@@ -252,6 +255,7 @@ void score_plan_build(const ScorePlanHeader& h, const int32_t* cu, const int32_t
         it.k_len = (int32_t)std::min<int64_t>(kBwdTileK, first + rows - u0);
         it.nseg = 1;
         it.dk_mode = DK_TEXT;
+        it.slot = i;
         it.flags = F_FIRST;
         Seg& s = it.seg[0];
         const int64_t q0 = both ? 0 : u0;
@@ -279,6 +283,7 @@ void score_plan_build(const ScorePlanHeader& h, const int32_t* cu, const int32_t
       t.len = (int32_t)std::min<int64_t>(kTile32, len - t0);
       t.seq0 = (int32_t)s0;
       t.seq_len = (int32_t)len;
+      t.sample = i;
       t.prefix = bidir && prefix_lens ? prefix_lens[i] : 0;
       tiles.push_back(t);
     }

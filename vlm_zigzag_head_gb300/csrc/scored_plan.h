@@ -21,12 +21,14 @@ namespace cpattn {
 
 constexpr int kTile32 = 64;   // rows of one tile of the fp32 kernels
 
-// One 64-row tile of a sample (fp32 kernels; queries and keys alike).
+// One 64-row tile of a sample (fp32 kernels, queries and keys alike, and the passes
+// over the rows of short samples).
 struct Tile32 {
   int32_t row0, len;     // natural rows [row0, row0 + len)
   int32_t seq0, seq_len; // the sample's rows
   int32_t prefix;        // rows that see one another in both directions (0: causal)
-  int32_t pad[3];
+  int32_t sample;
+  int32_t pad[2];
 };
 static_assert(sizeof(Tile32) == 32, "Tile32 layout");
 
@@ -39,6 +41,8 @@ static_assert(sizeof(Join) == 16, "Join layout");
 
 constexpr uint32_t kScorePlanMagic = 0x43505350u;
 constexpr int kMaxDist = 1 << 16;
+// Longest sample whose backward may take f16 operands (operand_range.cuh).
+constexpr int kF16Tokens = 1024;
 
 // At the start of the block; offsets are bytes from there.
 struct ScorePlanHeader {
@@ -53,6 +57,7 @@ struct ScorePlanHeader {
   int32_t n_units, grid;           // forward: units and persistent CTAs
   int32_t item_major;              // the forward's unit order
   int32_t n_sms;
+  int32_t n_short;                 // tiles of samples of up to kF16Tokens tokens
   uint64_t fwd, bwd, runs, units, buckets, tiles, joins, total;
 };
 static_assert(sizeof(ScorePlanHeader) <= 256, "plan header");

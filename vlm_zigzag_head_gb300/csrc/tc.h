@@ -88,8 +88,26 @@ struct TcFwdArgs {
 };
 cudaError_t launch_tc_fwd(const TcFwdArgs& a, cudaStream_t st);
 
+// Largest magnitudes of one sample's rows for one KV head and its query heads (bit
+// patterns, which order as integers; all 0 at first).
+struct OperandRange {
+  uint32_t q, k;        // max |x| over the finite elements
+  uint32_t v2, g2;      // largest sum of squares of a row of V and dO
+  uint32_t g2_least;    // complement of the least one of a row of dO that is not zero
+  uint32_t pad[3];
+};
+static_assert(sizeof(OperandRange) == 32, "OperandRange layout");
+
+// Operand types of S, dQ and dK (dP and dV: bf16).
+enum : int {
+  OPS_BF16 = 0,
+  OPS_F16 = 1,    // f16 with the factors of op_scales
+  OPS_ITEM = 2,   // each item's own choice (operand_range.cuh) from `ranges`
+};
+
 struct TcBwdArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // natural order (Q, K: the f16 copies when f16)
+  CUtensorMap tm_q16, tm_k16;            // f16 copies of the samples that take them (ranges)
   CUtensorMap tm_ld;                     // [2][H][pitch] fp32: lse2, D
   CUtensorMap tm_dq;                     // dq fp32 [T][H][d], box {32, 1, 32}, 128-byte swizzle:
                                          // reduce-add target
@@ -98,6 +116,9 @@ struct TcBwdArgs {
                               // runs[items[i].run0 .. + nseg)
   int f16;                    // S, dQ and dK on f16 operands (scaled Q, K copies; dS in f16)
   const OpScales* op_scales;  // device; read when f16
+  const OperandRange* ranges; // scored kernels, nullable: [n_samples][Hkv], each item's choice
+                              // of operand types (item.slot: its sample)
+  int n_samples;
   int n_items, H, d;
   int Hkv;                    // KV heads; one CTA per (key tile, KV head) walks its H / Hkv query heads
   float scale, scale_log2;

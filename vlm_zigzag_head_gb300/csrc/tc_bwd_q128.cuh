@@ -34,8 +34,9 @@
 // then run on f16 operands: the host-made copies Q * 2^-eQ and K * 2^-eK, and
 // dS^T * 2^-eS rounded to f16 (three more mantissa bits than bf16); the
 // factors are undone in fp32 (OpScales).  dP^T and dV keep bf16 V, dO and P^T.
-// Modified scores keep bf16 throughout (kF16 = false): one power of two for all of a
-// call's dS would take the bits of samples and tokens with small gradients.
+// Modified scores choose the types item by item, from the range of the item's sample
+// (OPS_ITEM, operand_range.cuh): one power of two for all of a call's dS would take the
+// bits of samples and tokens with small gradients.
 //
 // Warp roles (512 threads; TMEM lane quarter of warp w is w % 4):
 //   warp 0       TMA producer: K, V once; Q and the lse2 / D rows per tile
@@ -64,6 +65,7 @@
 
 #include "check.cuh"
 #include "kernels.h"
+#include "operand_range.cuh"
 #include "ptx.cuh"
 #include "score.cuh"
 #include "tc.h"
@@ -141,6 +143,7 @@ struct Bars {
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  Operands ops;   // OPS_ITEM
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
@@ -342,7 +345,7 @@ __device__ __forceinline__ void flush_far(const ScoreArgs& s, int h, int lane, f
   far_sum = 0.f;
 }
 
-template <int D, bool kF16, bool kShared, bool kCap, int kBias>
+template <int D, int kOps, bool kShared, bool kCap, int kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_bwd_q128_kernel(const __grid_constant__ TcBwdArgs a) {
   using L = Lay<D>;
@@ -395,6 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->dkv_done, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
+    if constexpr (kOps == OPS_ITEM) {
+      const int sample = a.items[item_idx].slot;
+      bars->ops = choose_operands(CP_IN_RANGE(sample, 0, a.n_samples, a.status, 213) &&
+                                          CP_IN_RANGE(hk, 0, a.Hkv, a.status, 214)
+                                      ? a.ranges[(long long)sample * a.Hkv + hk]
+                                      : OperandRange{});
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -405,6 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  // S, dQ and dK of this item on f16 operands
+  const bool f16 = kOps == OPS_F16 || (kOps == OPS_ITEM && bars->ops.f16 != 0);
 
   // the item's query runs, in ring-step order, from the plan's run list
   const int nseg = it.nseg;
@@ -436,12 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (n_all > 0) {
           uint64_t* landed = clear_kv ? &bars->kv_raw : &bars->kv_full;
           mbar_expect_tx(landed, 2 * L::kTile);
+          const CUtensorMap* mk = kOps == OPS_ITEM && f16 ? &a.tm_k16 : &a.tm_k;
           for (int b = 0; b < D / 64; ++b) {
-            tma_load_3d(&a.tm_k, landed, smem + L::kK + b * L::kBox, b * 64, hk, it.k_row0);
+            tma_load_3d(mk, landed, smem + L::kK + b * L::kBox, b * 64, hk, it.k_row0);
             tma_load_3d(&a.tm_v, landed, smem + L::kV + b * L::kBox, b * 64, hk, it.k_row0);
           }
           kv_issued = true;
         }
+        const CUtensorMap* mq = kOps == OPS_ITEM && f16 ? &a.tm_q16 : &a.tm_q;
         TileWalk walk;
         int jt = 0, hq = hq0;
         for (int j = 0; j < n_all; ++j, jt = jt + 1 == n_qt ? 0 : jt + 1, hq += jt == 0) {
@@ -470,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         bars->q_raw);
           mbar_expect_tx(landed, L::kTile + L::kLdBytes);
           for (int b = 0; b < D / 64; ++b)
-            tma_load_3d(&a.tm_q, landed, smem + L::kQ + st * L::kTile + b * L::kBox, b * 64, hq,
+            tma_load_3d(mq, landed, smem + L::kQ + st * L::kTile + b * L::kBox, b * 64, hq,
                         grow);
           // the lse2 / D box starts at the row rounded down to 4 (16-byte TMA alignment)
           tma_load_3d(&a.tm_ld, landed, smem + L::kLd + st * L::kLdStride, grow & ~3, hq, 0);
@@ -558,13 +572,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0) {
         // K-major A and B; B (Q, dO) MN-major; A (dS), B (K) MN-major.  S^T, dQ
-        // and dK take f16 operands when kF16 (K, Q copies and dS^T all f16);
+        // and dK take f16 operands when f16 (K, Q copies and dS^T all f16);
         // dP^T and dV always bf16 (V, dO, P^T)
-        constexpr uint32_t idesc_s = kF16 ? idesc_f16(kBK, kBQ, 0, 0) : idesc_bf16(kBK, kBQ, 0, 0);
+        const uint32_t idesc_s = f16 ? idesc_f16(kBK, kBQ, 0, 0) : idesc_bf16(kBK, kBQ, 0, 0);
         constexpr uint32_t idesc_dp = idesc_bf16(kBK, kBQ, 0, 0);
         constexpr uint32_t idesc_dv = idesc_bf16(kBK, D, 0, 1);
-        constexpr uint32_t idesc_dk = kF16 ? idesc_f16(kBK, D, 0, 1) : idesc_bf16(kBK, D, 0, 1);
-        constexpr uint32_t idesc_dq = kF16 ? idesc_f16(kBQ, D, 1, 1) : idesc_bf16(kBQ, D, 1, 1);
+        const uint32_t idesc_dk = f16 ? idesc_f16(kBK, D, 0, 1) : idesc_bf16(kBK, D, 0, 1);
+        const uint32_t idesc_dq = f16 ? idesc_f16(kBQ, D, 1, 1) : idesc_bf16(kBQ, D, 1, 1);
         const uint32_t k_addr = smem_u32(smem + L::kK), v_addr = smem_u32(smem + L::kV);
         const uint32_t ds_addr = smem_u32(smem + L::kDS);
         // S^T (into the S columns) from K and Q stage st
@@ -671,9 +685,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3;
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     // dQ = scale * (dS K); with f16 operands also undo the dS and K factors
-    // dS comes negated under a cap, and times 2^kPLog2
-    const float dq_scale = (kCap ? -a.scale : a.scale) * kPUnit<kCap, kBias>;
-    const float dq_mul = kF16 ? dq_scale * a.op_scales->dq_mul : dq_scale;
+    // dS comes negated under a cap, and times 2^kPLog2 (in f16: taken out before it is
+    // rounded)
+    const float dq_scale = (kCap ? -a.scale : a.scale) * (f16 ? 1.f : kPUnit<kCap, kBias>);
+    const float dq_mul = kOps == OPS_F16    ? dq_scale * a.op_scales->dq_mul
+                         : kOps == OPS_ITEM ? dq_scale * bars->ops.dq_mul
+                                            : dq_scale;
     uint8_t* stg = smem + L::kStg + wq * L::kStgWarp;
     uint8_t* my_row = stg + lane * 128;
     const int sw = lane & 7;
@@ -739,8 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int u = (warp & 3) * 32 + lane;        // key row == TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     // S^T = (K16 Q16^T) * qk_mul and dS16 = dS * ds_inv with f16 operands
-    const float sl2 = kF16 ? a.scale_log2 * a.op_scales->qk_mul : a.scale_log2;
-    const float ds_inv = kF16 ? a.op_scales->ds_inv : 1.f;
+    const float sl2 = kOps == OPS_F16    ? a.scale_log2 * a.op_scales->qk_mul
+                      : kOps == OPS_ITEM ? a.scale_log2 * bars->ops.qk_mul
+                                         : a.scale_log2;
+    const float ds_inv = kOps == OPS_F16    ? a.op_scales->ds_inv
+                         : kOps == OPS_ITEM ? bars->ops.ds_inv * kPUnit<kCap, kBias>
+                                            : 1.f;
     const bool key_ok = u < it.k_len;
     const int sw = u & 7;
     bool ok = true;
@@ -819,8 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       uint8_t* srow = smem + L::kDS + g * L::kBox + u * 128;
       Diagonals diag[2];   // of the two blocks of 32 queries (kBias: table)
-      auto ds_half = [&](int h, auto near_tile) {
+      auto ds_half = [&](int h, auto near_tile, auto in_f16) {
         [[maybe_unused]] constexpr bool kNear = decltype(near_tile)::value;
+        constexpr bool kF16 = decltype(in_f16)::value;
         uint32_t rd[32];
         tmem_ld32(tmem + lane_off + kColDP + g * 64 + h * 32, rd);
         tmem_ld_wait();
@@ -868,12 +890,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(hk[c * 4], hk[c * 4 + 1], hk[c * 4 + 2], hk[c * 4 + 3]);
         }
       };
-      if (kBias == SCORE_TABLE && tb.tab != nullptr) {
-        ds_half(0, std::true_type{});
-        ds_half(1, std::true_type{});
+      auto ds_tile = [&](auto in_f16) {
+        if (kBias == SCORE_TABLE && tb.tab != nullptr) {
+          ds_half(0, std::true_type{}, in_f16);
+          ds_half(1, std::true_type{}, in_f16);
+        } else {
+          ds_half(0, std::false_type{}, in_f16);
+          ds_half(1, std::false_type{}, in_f16);
+        }
+      };
+      if constexpr (kOps == OPS_ITEM) {
+        if (f16) ds_tile(std::true_type{});
+        else ds_tile(std::false_type{});
       } else {
-        ds_half(0, std::false_type{});
-        ds_half(1, std::false_type{});
+        ds_tile(std::bool_constant<kOps == OPS_F16>{});
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -924,8 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ((long long)(it.k_row0 + u) * a.Hkv + hk) * D;   // dkv_bf16: DK_TEXT items only
       const bool first = (it.flags & F_FIRST) != 0;
       constexpr float p_unit = kPUnit<kCap, kBias>;
-      const float dk_scale = (kCap ? -a.scale : a.scale) * p_unit;
-      const float mul = g == 0 ? (kF16 ? dk_scale * a.op_scales->dk_mul : dk_scale) : p_unit;
+      float dk_mul = (kCap ? -a.scale : a.scale) * (f16 ? 1.f : p_unit);
+      if constexpr (kOps == OPS_F16) dk_mul *= a.op_scales->dk_mul;
+      if constexpr (kOps == OPS_ITEM) dk_mul *= bars->ops.dk_mul;
+      const float mul = g == 0 ? dk_mul : p_unit;
       const uint32_t col = g == 0 ? C::kDK : C::kDV;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -970,15 +1002,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool kF16, bool kShared, bool kCap, int kBias>
+template <int D, int kOps, bool kShared, bool kCap, int kBias>
 cudaError_t launch_q128(const TcBwdArgs& a, cudaStream_t st) {
   constexpr int smem = Lay<D>::kAlloc;
-  cudaError_t e = cudaFuncSetAttribute(tc_bwd_q128_kernel<D, kF16, kShared, kCap, kBias>,
+  cudaError_t e = cudaFuncSetAttribute(tc_bwd_q128_kernel<D, kOps, kShared, kCap, kBias>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const long long blocks = (long long)a.n_items * a.Hkv * a.kv_split;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  tc_bwd_q128_kernel<D, kF16, kShared, kCap, kBias><<<(unsigned)blocks, kThreads, smem, st>>>(a);
+  tc_bwd_q128_kernel<D, kOps, kShared, kCap, kBias><<<(unsigned)blocks, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -1,5 +1,5 @@
 // Picks the kernel of a launch with modified scores: one translation unit per
-// direction, head size and (forward) operand type.
+// direction, head size and operand type.
 #include "tc.h"
 
 #include <algorithm>
@@ -29,8 +29,10 @@ CP_SCORED(fwd_scored_64_bf16, TcFwdArgs)
 CP_SCORED(fwd_scored_64_f16, TcFwdArgs)
 CP_SCORED(fwd_scored_128_bf16, TcFwdArgs)
 CP_SCORED(fwd_scored_128_f16, TcFwdArgs)
-CP_SCORED(bwd_scored_64, TcBwdArgs)
-CP_SCORED(bwd_scored_128, TcBwdArgs)
+CP_SCORED(bwd_scored_64_bf16, TcBwdArgs)
+CP_SCORED(bwd_scored_64_item, TcBwdArgs)
+CP_SCORED(bwd_scored_128_bf16, TcBwdArgs)
+CP_SCORED(bwd_scored_128_item, TcBwdArgs)
 #undef CP_SCORED
 
 cudaError_t launch_tc_fwd_scored(const TcFwdArgs& a, int bias, cudaStream_t st) {
@@ -45,12 +47,14 @@ cudaError_t launch_tc_fwd_scored(const TcFwdArgs& a, int bias, cudaStream_t st) 
 cudaError_t launch_tc_bwd_scored(const TcBwdArgs& a, int bias, cudaStream_t st) {
   if (a.n_items == 0) return cudaSuccess;
   if (a.runs == nullptr || a.kv_split < 1 || (a.H / a.Hkv) % a.kv_split != 0 ||
-      a.f16)   // bf16 operands alone
+      a.f16)   // one choice for all items: the plain kernels'
     return cudaErrorInvalidValue;
-  if (bias == SCORE_PLAIN && !(a.score.cap_log2 > 0.f)) return launch_tc_bwd_q128(a, st);
-  if (a.d == 64) return launch_bwd_scored_64(a, bias, st);
+  const bool item = a.ranges != nullptr;
+  if (!item && bias == SCORE_PLAIN && !(a.score.cap_log2 > 0.f)) return launch_tc_bwd_q128(a, st);
+  if (a.d == 64)
+    return item ? launch_bwd_scored_64_item(a, bias, st) : launch_bwd_scored_64_bf16(a, bias, st);
   if (a.d != 128) return cudaErrorNotSupported;
-  return launch_bwd_scored_128(a, bias, st);
+  return item ? launch_bwd_scored_128_item(a, bias, st) : launch_bwd_scored_128_bf16(a, bias, st);
 }
 
 }  // namespace cpattn
