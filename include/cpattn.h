@@ -388,6 +388,87 @@ cp_status_t cp_qk_norm_rope_bwd(const cp_norm_rope_t* desc, const void* q, const
                                 void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * cp_rope_fwd / cp_rope_bwd -- rotation of every query and key head by its
+ * position, without a norm, and its gradient: for models whose heads are not
+ * normed (those that are take cp_qk_norm_rope_fwd).
+ *
+ *   (y_i, y_j) = amplitude (x_i cos t - x_j sin t, x_j cos t + x_i sin t)
+ *
+ * for rotated pair p = (i, j) with t = positions[a][t] * inv_freq[p]; axes,
+ * sections, interleaved, rot_dim and the exactness of the angles are those of
+ * cp_qk_norm_rope_fwd.  Elements from rot_dim on are copied bit for bit.  Contexts
+ * longer than those a model was trained on take scaled inv_freq and, with some
+ * methods, an amplitude other than 1.
+ *
+ *   q [T][H][d], k [T][H_kv][d], q_out, k_out, and backward dq_out, dk_out (in),
+ *   dq, dk (out)    strides in elements (last dimension contiguous).  An output
+ *                   may be its input (same pointer and strides: in place); else
+ *                   outputs overlap neither an input nor one another
+ *   positions       device int32 [n_axes][T]; any value
+ * Backward: the strides of `desc` named q, k are those of dq_out, dk_out, the ones
+ * named q_out, k_out those of dq, dk.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE (d not 64 or 128, rot_dim, sections),
+ * CP_ERR_DTYPE, CP_ERR_ALIGNMENT, CP_ERR_CUDA.
+ */
+typedef struct {
+  cp_dtype_t dtype;
+  int T, H, H_kv, d;         /* d: 64 or 128 */
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h;
+  int64_t q_out_stride_t, q_out_stride_h, k_out_stride_t, k_out_stride_h;
+  int rot_dim;               /* multiple of 16 in [0, d] */
+  int interleaved;
+  int n_axes;                /* 1 .. 4 */
+  int sections[4];           /* pairs of each axis; sum = rot_dim / 2 */
+  const double* inv_freq;    /* HOST array, rot_dim / 2 radians per position */
+  float amplitude;           /* finite */
+} cp_rope_t;
+cp_status_t cp_rope_fwd(const cp_rope_t* desc, const void* q, const void* k,
+                        const int32_t* positions, void* q_out, void* k_out, void* stream);
+cp_status_t cp_rope_bwd(const cp_rope_t* desc, const void* dq_out, const void* dk_out,
+                        const int32_t* positions, void* dq, void* dk, void* stream);
+
+/*
+ * cp_layer_norm_fwd / cp_layer_norm_bwd -- layer norm of token rows and its
+ * gradient: the norm before the projections to q, k, v and before the
+ * feed-forward block.
+ *
+ *   n = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps),  y = n weight + bias
+ *
+ * fp32 throughout, the mean taken out before the squares are summed; rounded once.
+ * A NaN or infinity reaches its own row, and through it dweight and dbias.
+ *
+ *   x, dy [T][D]    row strides in elements; rows on 16-byte boundaries that are
+ *                   whole 16-byte pieces take vector loads, others element loads
+ *   weight, bias    NULL (ones, zeros) or [D], weight_dtype
+ *   y, dx           [T][D] contiguous, dtype, 16-byte aligned; must not overlap an
+ *                   input.  dx NULL: not wanted
+ *   mean, rstd      [T] fp32: forward: written where not NULL; backward: read
+ *   dweight, dbias  NULL or [D] fp32: sums over the rows, in an order that does not
+ *                   depend on timing
+ *   workspace       backward with dweight or dbias: >=
+ *                   cp_layer_norm_bwd_workspace_size(desc) bytes, 256-byte aligned,
+ *                   written before it is read
+ * T == 0: no rows are touched; dweight and dbias are zeroed.
+ * cp_layer_norm_bwd_workspace_size returns 0 on a bad descriptor.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE (D not in [1, 16384]), CP_ERR_DTYPE,
+ * CP_ERR_ALIGNMENT, CP_ERR_WORKSPACE, CP_ERR_CUDA.
+ */
+typedef struct {
+  cp_dtype_t dtype;          /* of x, y, dy, dx */
+  cp_dtype_t weight_dtype;   /* of weight, bias */
+  int T, D;
+  int64_t x_stride, dy_stride;
+  float eps;
+} cp_layer_norm_t;
+cp_status_t cp_layer_norm_fwd(const cp_layer_norm_t* desc, const void* x, const void* weight,
+                              const void* bias, void* y, float* mean, float* rstd, void* stream);
+size_t cp_layer_norm_bwd_workspace_size(const cp_layer_norm_t* desc);
+cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const void* dy,
+                              const void* weight, const float* mean, const float* rstd, void* dx,
+                              float* dweight, float* dbias, void* workspace, size_t ws_bytes,
+                              void* stream);
+
+/*
  * cp_score_plan_* -- work lists of attention with modified scores.
  * They depend on the packing alone: build the block on the host once per
  * packing, copy it to the device (256-byte aligned) and pass both copies to

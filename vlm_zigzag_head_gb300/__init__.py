@@ -12,6 +12,9 @@ Functions keep the names of the C entry points:
 * :func:`cp_attn_fwd_gqa`, :func:`cp_attn_bwd_gqa` -- grouped KV heads
 * :func:`cp_qk_norm_rope_fwd`, :func:`cp_qk_norm_rope_bwd` -- norm of query and key
   heads with the position rotation
+* :func:`cp_rope_fwd`, :func:`cp_rope_bwd` (frequencies: :func:`rope_frequencies`) -- the
+  rotation alone, for long contexts too
+* :func:`cp_layer_norm_fwd`, :func:`cp_layer_norm_bwd` -- layer norm of token rows
 * :func:`cp_attn_scored_fwd`, :func:`cp_attn_scored_bwd` (plans: :class:`ScorePlan`) --
   attention with capped or distance-biased scores
 * :func:`cp_workspace_status`, :func:`cp_set_wait_limit`, :func:`cp_plan_pairs`,
@@ -33,7 +36,9 @@ __all__ = ["cp_zigzag_index", "cp_zigzag_gather", "cp_zigzag_scatter", "cp_attn_
            "cp_lse_merge", "cp_attn_bwd", "cp_workspace_status", "cp_set_wait_limit",
            "cp_plan_pairs", "cp_plan_unit_lists", "cp_profile_begin", "cp_profile_end", "Workspace",
            "attention_host", "CpError", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd",
-           "cp_attn_scored_fwd", "cp_attn_scored_bwd", "ScorePlan", "relative_buckets"]
+           "cp_attn_scored_fwd", "cp_attn_scored_bwd", "ScorePlan", "relative_buckets",
+           "cp_layer_norm_fwd", "cp_layer_norm_bwd", "cp_rope_fwd", "cp_rope_bwd",
+           "rope_frequencies"]
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -529,6 +534,8 @@ def attention_host(q, k, v, dout, cu_seqlens, P: int, prefix_len: int, softmax_s
     return tuple(host_out[:n_res])
 
 
+from .layer_norm import cp_layer_norm_bwd, cp_layer_norm_fwd  # noqa: E402
 from .norm_rope import cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd  # noqa: E402
+from .rope import cp_rope_bwd, cp_rope_fwd, rope_frequencies  # noqa: E402
 from .scored import (ScorePlan, cp_attn_scored_bwd, cp_attn_scored_fwd,  # noqa: E402
                      relative_buckets)

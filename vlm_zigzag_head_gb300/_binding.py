@@ -39,6 +39,25 @@ class NormRopeDesc(ctypes.Structure):
                 ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("eps", ctypes.c_float)]
 
 
+class RopeDesc(ctypes.Structure):
+    """cp_rope_t."""
+    _fields_ = [("dtype", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("d", ctypes.c_int)] + \
+               [(n, ctypes.c_int64) for n in ("q_stride_t", "q_stride_h", "k_stride_t",
+                                              "k_stride_h", "q_out_stride_t", "q_out_stride_h",
+                                              "k_out_stride_t", "k_out_stride_h")] + \
+               [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("sections", ctypes.c_int * 4),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("amplitude", ctypes.c_float)]
+
+
+class LayerNormDesc(ctypes.Structure):
+    """cp_layer_norm_t."""
+    _fields_ = [("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("T", ctypes.c_int),
+                ("D", ctypes.c_int), ("x_stride", ctypes.c_int64), ("dy_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
 class ScoreDesc(ctypes.Structure):
     """cp_score_t."""
     _fields_ = [("softcap", ctypes.c_float), ("slopes", c_vp), ("rel_bias", c_vp),
@@ -104,6 +123,12 @@ SIGNATURES = {
     "cp_qk_norm_rope_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NormRopeDesc)]),
     "cp_qk_norm_rope_bwd": (ctypes.c_int, [ctypes.POINTER(NormRopeDesc)] + [c_vp] * 12 +
                             [ctypes.c_size_t, c_vp]),
+    "cp_rope_fwd": (ctypes.c_int, [ctypes.POINTER(RopeDesc)] + [c_vp] * 6),
+    "cp_rope_bwd": (ctypes.c_int, [ctypes.POINTER(RopeDesc)] + [c_vp] * 6),
+    "cp_layer_norm_fwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 7),
+    "cp_layer_norm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerNormDesc)]),
+    "cp_layer_norm_bwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 9 +
+                          [ctypes.c_size_t, c_vp]),
     "cp_score_plan_size": (ctypes.c_size_t, _PLAN),
     "cp_score_plan_build": (ctypes.c_int, _PLAN + [c_vp, ctypes.c_size_t]),
     "cp_score_plan_pairs": (ctypes.c_int, [c_vp, c_i64p, c_i64p, c_i64p]),

@@ -25,6 +25,9 @@ from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
+from . import _binding as _b
+from . import layer_norm as _layer_norm
+from . import rope as _rope
 
 
 class CPAttention(torch.autograd.Function):
@@ -146,6 +149,88 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor,
     if not _wants_grad(q, k, q_weight, k_weight):
         return norm_rope._launch_fwd(desc, q, k, positions, q_weight, k_weight)
     return QKNormRope.apply(q, k, positions, q_weight, k_weight, desc, options)
+
+
+class Rope(torch.autograd.Function):
+    """``(q_out, k_out) = Rope.apply(q, k, positions, desc, options)``."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, desc, options):
+        ctx.save_for_backward(positions)
+        ctx.meta = options, q.shape, k.shape, q.dtype
+        ctx.set_materialize_grads(False)
+        return _rope._launch(_b.lib().cp_rope_fwd, desc, q, k, positions)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        positions, = ctx.saved_tensors
+        options, q_shape, k_shape, dtype = ctx.meta
+        if dq_out is None and dk_out is None:
+            return (None,) * 5
+        # an output that nothing used has no gradient
+        dq_out, dk_out = (torch.zeros(shape, dtype=dtype, device=positions.device) if g is None
+                          else g if g.stride(-1) == 1 else g.contiguous()
+                          for g, shape in ((dq_out, q_shape), (dk_out, k_shape)))
+        desc = _rope._prepare(dq_out, dk_out, positions, *options)
+        dq, dk = _rope._launch(_b.lib().cp_rope_bwd, desc, dq_out, dk_out, positions)
+        need = ctx.needs_input_grad
+        return dq if need[0] else None, dk if need[1] else None, None, None, None
+
+
+def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, theta: float = 10000.0,
+         rot_dim: Optional[int] = None, sections: Optional[Sequence[int]] = None,
+         interleaved: bool = False, inv_freq: Optional[Sequence[float]] = None,
+         amplitude: float = 1.0):
+    """Differentiable :func:`~vlm_zigzag_head_gb300.cp_rope_fwd`: every head of q and k turned by
+    its position.  Returns contiguous ``(q_out, k_out)``, ready for :func:`cp_attention`;
+    gradients flow to q and k (backward only: forward mode raises).  To capture the backward
+    into a graph, call :func:`~vlm_zigzag_head_gb300.cp_rope_bwd`, which involves no leaves."""
+    options = (theta, rot_dim, None if sections is None else tuple(sections), interleaved,
+               None if inv_freq is None else tuple(inv_freq), amplitude)
+    desc = _rope._prepare(q, k, positions, *options)
+    if not _wants_grad(q, k):
+        return _rope._launch(_b.lib().cp_rope_fwd, desc, q, k, positions)
+    return Rope.apply(q, k, positions, desc, options)
+
+
+class LayerNorm(torch.autograd.Function):
+    """``y = LayerNorm.apply(x, weight, bias, eps)``."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        rows = _layer_norm._rows(x, "x")
+        desc = _layer_norm._prepare(rows, weight, bias, eps)
+        y, mean, rstd = _layer_norm._launch_fwd(desc, rows, weight, bias, x.shape)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.set_materialize_grads(False)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        if dy is None:   # what used y has no gradient for it
+            return (None,) * 4
+        x, weight, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = _layer_norm.cp_layer_norm_bwd(x, dy, mean, rstd, weight, input_grad=need[0],
+                                                   weight_grad=need[1], bias_grad=need[2])
+        return (dx, dw.to(weight.dtype) if need[1] else None,
+                db.to(ctx.bias_dtype) if need[2] else None, None)
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+               bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5):
+    """Differentiable :func:`~vlm_zigzag_head_gb300.cp_layer_norm_fwd` of the last dimension of
+    ``x [..., D]``.  Returns y, contiguous; gradients flow to x, weight and bias (backward
+    only: forward mode raises).  To capture the backward into a graph, call
+    :func:`~vlm_zigzag_head_gb300.cp_layer_norm_bwd`, which involves no leaves."""
+    if not _wants_grad(x, weight, bias):
+        rows = _layer_norm._rows(x, "x")
+        desc = _layer_norm._prepare(rows, weight, bias, eps)
+        return _layer_norm._launch_fwd(desc, rows, weight, bias, x.shape)[0]
+    return LayerNorm.apply(x, weight, bias, eps)
 
 
 class CPAttentionScored(torch.autograd.Function):

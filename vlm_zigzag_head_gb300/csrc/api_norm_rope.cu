@@ -8,6 +8,7 @@
 #include "../../include/cpattn.h"
 #include "entry.h"
 #include "norm_rope.h"
+#include "rope_desc.h"
 
 using namespace cpattn;
 
@@ -18,8 +19,6 @@ struct Setup {
   bool bf16 = false, vec = false;
   int sms = 0;
 };
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Everything that does not look at a tensor pointer.
 cp_status_t check_desc(const cp_norm_rope_t* p) {
@@ -33,26 +32,9 @@ cp_status_t check_desc(const cp_norm_rope_t* p) {
   if (p->H > (1 << 20) || p->H_kv > (1 << 20))
     return entry_fail(CP_ERR_SHAPE, "at most 2^20 heads");
   if (p->d != 64 && p->d != 128) return entry_fail(CP_ERR_SHAPE, "head_dim must be 64 or 128");
-  if (p->rot_dim < 0 || p->rot_dim > p->d || p->rot_dim % 16 != 0)
-    return entry_fail(CP_ERR_SHAPE, "rot_dim must be a multiple of 16 in [0, head_dim]");
-  if (p->n_axes < 1 || p->n_axes > kRopeMaxAxes)
-    return entry_fail(CP_ERR_SHAPE, "n_axes must be in [1, 4]");
-  int pairs = 0;
-  for (int i = 0; i < p->n_axes; ++i) {
-    if (p->sections[i] < 0 || p->sections[i] > 64)
-      return entry_fail(CP_ERR_SHAPE, "a section is negative or larger than the head");
-    pairs += p->sections[i];
-  }
-  if (pairs != p->rot_dim / 2)
-    return entry_fail(CP_ERR_SHAPE, "sections must add up to rot_dim / 2");
   if (!(p->eps >= 0.f) || !std::isfinite(p->eps))
     return entry_fail(CP_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  if (p->rot_dim > 0 && !p->inv_freq)
-    return entry_fail(CP_ERR_INVALID_ARG, "inv_freq is NULL");
-  for (int i = 0; i < p->rot_dim / 2; ++i)
-    if (!std::isfinite(p->inv_freq[i]))
-      return entry_fail(CP_ERR_INVALID_ARG, "inv_freq must be finite");
-  return CP_OK;
+  return rope_check_angles(p);
 }
 
 cp_status_t setup(const cp_norm_rope_t* p, const void* q, const void* k, const int32_t* pos,
@@ -82,23 +64,9 @@ cp_status_t setup(const cp_norm_rope_t* p, const void* q, const void* k, const i
   a.w[0] = qw;
   a.w[1] = kw;
   a.w_bf16 = p->weight_dtype == CP_BF16;
-  a.pos = pos;
-  int end = 0;
-  for (int i = 0; i < kRopeMaxAxes; ++i) {
-    if (i < p->n_axes) end += p->sections[i];
-    a.sec_end[i] = end;
-  }
-  a.n_axes = p->n_axes;
-  a.T = p->T;
-  a.rot = p->rot_dim;
   a.eps = p->eps;
   a.partial = nullptr;
-  for (int i = 0; i < 64; ++i) a.freq[i] = 0;
-  for (int i = 0; i < p->rot_dim / 2; ++i) {
-    const double turns = p->inv_freq[i] / 6.283185307179586476925;
-    const double frac = std::ldexp(turns - std::floor(turns), 64);
-    a.freq[i] = frac < 18446744073709551616.0 ? (uint64_t)frac : 0;
-  }
+  rope_fill_angles(p, pos, &a);
   // vector loads where every group of four elements lies on a boundary of its size
   o->vec = aligned_to(q, 4 * elem) && aligned_to(k, 4 * elem);
   for (int i = 0; i < 2; ++i) o->vec = o->vec && a.st[i] % 4 == 0 && a.sh[i] % 4 == 0;
@@ -110,7 +78,7 @@ cp_status_t shape_launch(const cp_norm_rope_t* p, Setup* o) {
   int dev = 0;
   ENTRY_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   ENTRY_CUDA(cudaDeviceGetAttribute(&o->sms, cudaDevAttrMultiProcessorCount, dev), "SM count");
-  norm_rope_split(p->T, p->H + p->H_kv, p->d, o->sms, &o->a.chunk, &o->a.n_chunks);
+  rope_split(p->T, p->H + p->H_kv, p->d, o->sms, &o->a.chunk, &o->a.n_chunks);
   return CP_OK;
 }
 

@@ -22,7 +22,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int table_mid(int n_dist) { return n_dist + kTableSlack; }
 int table_pitch(int n_dist) { return 2 * table_mid(n_dist) + 1; }

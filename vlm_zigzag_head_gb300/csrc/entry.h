@@ -13,6 +13,8 @@ namespace cpattn {
 void set_last_error(const std::string& msg);   // api.cu
 long long device_wait_limit();                 // api.cu
 
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 inline cp_status_t entry_fail(cp_status_t s, const std::string& msg) {
   set_last_error(msg);
   return s;
