@@ -72,7 +72,11 @@ cp_status_t cp_layer_norm_fwd(const cp_layer_norm_t* desc, const void* x, const 
   a.rstd = rstd;
   const bool vec = aligned_to(x, 16) && (desc->T == 1 || desc->x_stride * elem % 16 == 0) &&
                    desc->D * elem % 16 == 0 && aligned_to(weight, 16) && aligned_to(bias, 16);
-  ENTRY_CUDA(launch_layer_norm_fwd(a, bf16, vec, static_cast<cudaStream_t>(stream)), "layer norm");
+  int dev = 0, sms = 0;
+  ENTRY_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+  ENTRY_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "SM count");
+  ENTRY_CUDA(launch_layer_norm_fwd(a, bf16, vec, sms, static_cast<cudaStream_t>(stream)),
+             "layer norm");
   return CP_OK;
   ENTRY_CATCH
 }

@@ -51,27 +51,45 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
   return v;
 }
 
-__device__ __forceinline__ void widen(const uint4& v, float (&f)[8]) {
+// A piece's elements as pairs of floats.
+template <typename T>
+__device__ __forceinline__ void widen(const uint4& v, uint64_t (&f)[kPiece<T> / 2]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {   // a bf16 is the upper half of its fp32
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i)   // a bf16 is the upper half of its fp32
+      f[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      f[i] = pack2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
   }
 }
-__device__ __forceinline__ void widen(const uint4& v, float (&f)[4]) {
-  f[0] = __uint_as_float(v.x);
-  f[1] = __uint_as_float(v.y);
-  f[2] = __uint_as_float(v.z);
-  f[3] = __uint_as_float(v.w);
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const uint64_t (&f)[kPiece<T> / 2]) {
+  uint32_t u[4];
+  float a, b;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack2(f[i], a, b);
+      u[i] = pack_bf16x2(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      unpack2(f[i], a, b);
+      u[2 * i] = __float_as_uint(a);
+      u[2 * i + 1] = __float_as_uint(b);
+    }
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ uint4 narrow(const float (&f)[4]) {
-  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                    __float_as_uint(f[3]));
+
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
 }
 
 // One piece of a row as stored (16 bytes); elements past the row are zero.
@@ -82,77 +100,89 @@ __device__ __forceinline__ uint4 load_piece(const T* row, int t, int i, int D) {
     const int c = column<T, TPR, true>(t, i, 0);
     return c < D ? load_once(row + c) : make_uint4(0, 0, 0, 0);
   } else {
-    float f[E];
+    uint64_t f[E / 2];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int c = column<T, TPR, false>(t, i, j);
-      f[j] = c < D ? as_float(row[c]) : 0.f;
+    for (int j = 0; j < E; j += 2) {
+      const int c = column<T, TPR, false>(t, i, j), d = column<T, TPR, false>(t, i, j + 1);
+      f[j / 2] = pack2(c < D ? as_float(row[c]) : 0.f, d < D ? as_float(row[d]) : 0.f);
     }
-    return narrow(f);   // exact: the values come from this type
+    return narrow<T>(f);   // exact: the values come from this type
   }
 }
 
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void store_piece(T* row, int t, int i, int D,
-                                            const float (&f)[kPiece<T>]) {
+                                            const uint64_t (&f)[kPiece<T> / 2]) {
   constexpr int E = kPiece<T>;
   if constexpr (kVec) {
     const int c = column<T, TPR, true>(t, i, 0);
-    if (c < D) *reinterpret_cast<uint4*>(row + c) = narrow(f);
+    if (c < D) *reinterpret_cast<uint4*>(row + c) = narrow<T>(f);
   } else {
 #pragma unroll
     for (int j = 0; j < E; ++j) {
       const int c = column<T, TPR, false>(t, i, j);
+      float v[2];
+      unpack2(f[j / 2], v[0], v[1]);
       if (c < D) {
-        if constexpr (sizeof(T) == 2) row[c] = __float2bfloat16_rn(f[j]);
-        else row[c] = f[j];
+        if constexpr (sizeof(T) == 2) row[c] = __float2bfloat16_rn(v[j & 1]);
+        else row[c] = v[j & 1];
       }
     }
   }
 }
 
-// Weights or biases of one piece's columns (`none` where the pointer is null).
+// Weights or biases of one piece's columns (`none` where the pointer is null, zero
+// past the row).
 template <typename T, int TPR, bool kVec>
 __device__ __forceinline__ void load_weights(const void* w, bool bf16, float none, int t, int i,
-                                             int D, float (&f)[kPiece<T>]) {
+                                             int D, uint64_t (&f)[kPiece<T> / 2]) {
   constexpr int E = kPiece<T>;
   if (w == nullptr) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] = none;
+    for (int j = 0; j < E / 2; ++j) f[j] = pack2(none, none);
     return;
   }
   const int c0 = column<T, TPR, kVec>(t, i, 0);
   if (kVec && c0 < D) {   // pieces lie within the row
     if (bf16) {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w) + c0;
-      if constexpr (E == 8) {
-        widen(*reinterpret_cast<const uint4*>(p), f);
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        f[0] = __uint_as_float(v.x << 16);
-        f[1] = __uint_as_float(v.x & 0xffff0000u);
-        f[2] = __uint_as_float(v.y << 16);
-        f[3] = __uint_as_float(v.y & 0xffff0000u);
-      }
+      const uint32_t* p =
+          reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(w) + c0);
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j)
+        f[j] = pack2(__uint_as_float(p[j] << 16), __uint_as_float(p[j] & 0xffff0000u));
     } else {
       const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c0);
 #pragma unroll
       for (int j = 0; j < E / 4; ++j) {
         const float4 v = p[j];
-        f[4 * j] = v.x;
-        f[4 * j + 1] = v.y;
-        f[4 * j + 2] = v.z;
-        f[4 * j + 3] = v.w;
+        f[2 * j] = pack2(v.x, v.y);
+        f[2 * j + 1] = pack2(v.z, v.w);
       }
     }
     return;
   }
+  float v[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) {
     const int c = column<T, TPR, kVec>(t, i, j);
-    f[j] = c >= D  ? 0.f
+    v[j] = c >= D  ? 0.f
            : bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c])
                   : static_cast<const float*>(w)[c];
+  }
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) f[j] = pack2(v[2 * j], v[2 * j + 1]);
+}
+
+// A pair with zeros in place of elements past the row (all other values kept).
+template <typename T, int TPR, bool kVec>
+__device__ __forceinline__ uint64_t inside(uint64_t v, int t, int i, int j, int D) {
+  if constexpr (kVec) {
+    return column<T, TPR, true>(t, i, 0) < D ? v : 0ull;
+  } else {
+    float a, b;
+    unpack2(v, a, b);
+    return pack2(column<T, TPR, false>(t, i, 2 * j) < D ? a : 0.f,
+                 column<T, TPR, false>(t, i, 2 * j + 1) < D ? b : 0.f);
   }
 }
 
@@ -162,93 +192,128 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-template <typename T, int TPR, int NV, bool kVec>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
+constexpr int kMinThreads = 256;   // of a block whose rows take fewer
+constexpr int block_threads(int tpr) { return tpr > kMinThreads ? tpr : kMinThreads; }
+
+// Persistent blocks: a group of TPR threads takes rows gridDim.x * G apart with its
+// columns' weights in registers (read per row they were twice the traffic of bf16
+// rows, from L1) and the next row's loads in flight.  A warp takes the squares about
+// its own mean, and the warps' means and squares are then joined: one barrier a row.
+template <typename T, int TPR, int NV, bool kVec, int kBlocks>
+__global__ void __launch_bounds__(block_threads(TPR), kBlocks)
     layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a) {
-  constexpr int E = kPiece<T>;
-  constexpr int kWarps = TPR / 32;
-  __shared__ float red[2][kWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = TPR == 32 ? lane : threadIdx.x;
-  const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 8 + warp : (int64_t)blockIdx.x;
-  if (row >= a.T) return;   // whole warps, and only where a row is one warp's
-  auto row_sum = [&](float v, int which) {
-    v = warp_sum(v);
-    if constexpr (kWarps > 1) {
-      if (lane == 0) red[which][warp] = v;
-      __syncthreads();
-      v = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) v += red[which][i];
+  constexpr int E2 = kPiece<T> / 2;
+  constexpr int G = block_threads(TPR) / TPR;   // rows of one pass
+  constexpr int kWarps = TPR / 32;              // of one row
+  __shared__ float2 red[2][G][kWarps];          // a warp's mean, sum of squares about it
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const int warp = t >> 5, lane = threadIdx.x & 31;
+  // columns of warp w of the row
+  auto columns_of = [&](int w) {
+    int n = 0;
+    for (int i = 0; i < NV; ++i) {
+      if (kVec) {
+        const int c = (i * TPR + w * 32) * 2 * E2;
+        n += min(max(a.D - c, 0), 32 * 2 * E2);
+      } else {
+        for (int j = 0; j < 2 * E2; ++j) n += min(max(a.D - (i * 2 * E2 + j) * TPR - w * 32, 0), 32);
+      }
     }
-    return v;
+    return n;
   };
-  const T* src = static_cast<const T*>(a.x) + row * a.x_stride;
+  const int mine = columns_of(warp);
+  const float inv_mine = mine > 0 ? 1.f / (float)mine : 0.f;
+  const float lane_cols = kWarps > 1 && lane < kWarps ? (float)columns_of(lane) : 0.f;
+  uint64_t w[NV][E2], b[NV][E2];
   uint4 raw[NV];
+  auto load = [&](int64_t row) {
+    const T* src = static_cast<const T*>(a.x) + row * a.x_stride;
+    if (row < a.T) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) raw[i] = load_piece<T, TPR, kVec>(src, t, i, a.D);
-  float x[NV][E];
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    widen(raw[i], x[i]);
-#pragma unroll
-    for (int j = 0; j < E; ++j) sum += x[i][j];
-  }
-  const float mean = row_sum(sum, 0) * a.inv_D;
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      x[i][j] -= mean;
-      if (column<T, TPR, kVec>(t, i, j) < a.D) ss = fmaf(x[i][j], x[i][j], ss);
+      for (int i = 0; i < NV; ++i) raw[i] = load_piece<T, TPR, kVec>(src, t, i, a.D);
     }
-  const float r = rsqrtf(row_sum(ss, 1) * a.inv_D + a.eps);
-  T* dst = static_cast<T*>(a.y) + row * a.D;
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + grp;
+  load(row);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float w[E], b[E];
-    load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, w);
-    load_weights<T, TPR, kVec>(a.b, a.w_bf16, 0.f, t, i, a.D, b);
-#pragma unroll
-    for (int j = 0; j < E; ++j) x[i][j] = fmaf(x[i][j] * r, w[j], b[j]);
-    store_piece<T, TPR, kVec>(dst, t, i, a.D, x[i]);
+    load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, w[i]);
+    load_weights<T, TPR, kVec>(a.b, a.w_bf16, 0.f, t, i, a.D, b[i]);
   }
-  if (t == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = r;
+  int slot = 0;
+  // a warp that is a row's only one leaves when its rows are done; with several the
+  // whole block walks alike
+  for (int64_t first = (int64_t)blockIdx.x * G; kWarps > 1 ? first < a.T : row < a.T;
+       first += step, row += step) {
+    uint64_t x[NV][E2];
+    uint64_t s2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      widen<T>(raw[i], x[i]);
+#pragma unroll
+      for (int j = 0; j < E2; ++j) s2 = add2(s2, x[i][j]);
+    }
+    load(row + step);
+    float mean = warp_sum(sum2(s2)) * inv_mine;
+    const uint64_t neg = pack2(-mean, -mean);
+    uint64_t ss = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < E2; ++j) {
+        const uint64_t d = inside<T, TPR, kVec>(add2(x[i][j], neg), t, i, j, a.D);
+        ss = fma2(d, d, ss);
+      }
+    float squares = warp_sum(sum2(ss));
+    if constexpr (kWarps > 1) {
+      if (lane == 0) red[slot][grp][warp] = make_float2(mean, squares);
+      __syncthreads();
+      // lane i has warp i's: the mean of all, then the squares about that (each
+      // thread adding all warps' from shared memory measured 3 to 15 % slower)
+      const float2 v = lane < kWarps ? red[slot][grp][lane] : make_float2(0.f, 0.f);
+      mean = warp_sum(v.x * lane_cols) * a.inv_D;
+      const float d = v.x - mean;
+      squares = warp_sum(lane_cols > 0.f ? fmaf(lane_cols * d, d, v.y) : 0.f);
+      slot ^= 1;   // the next pass writes the other slot: one barrier a pass
+    }
+    const float r = rsqrtf(squares * a.inv_D + a.eps);
+    if (row < a.T) {
+      T* dst = static_cast<T*>(a.y) + row * a.D;
+      const uint64_t m2 = pack2(-mean, -mean), r2 = pack2(r, r);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < E2; ++j)
+          x[i][j] = fma2(mul2(add2(x[i][j], m2), r2), w[i][j], b[i][j]);
+        store_piece<T, TPR, kVec>(dst, t, i, a.D, x[i]);
+      }
+      if (t == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = r;
+      }
+    }
   }
 }
 
-constexpr int kBwdThreads = 256;   // of a block whose rows take fewer
-
 // kWide (rows of more than 1024 threads' 8 elements): sums of dw and db in shared
 // memory and no row read ahead, so that a thread's row fits 64 registers.
-template <typename T, int TPR, int NV, bool kVec, bool kWide>
-__global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
+template <typename T, int TPR, int NV, bool kVec, bool kWide, int kBlocks>
+__global__ void __launch_bounds__(block_threads(TPR), kBlocks)
     layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a) {
-  constexpr int E = kPiece<T>;
-  constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
+  constexpr int E = kPiece<T>, E2 = E / 2;
+  constexpr int kThreads = block_threads(TPR);
   constexpr int G = kThreads / TPR;        // rows of one pass
   constexpr int kWarps = TPR / 32;         // of one row
   constexpr int kCols = TPR * NV * E;
+  constexpr int kHeld = kWide ? 1 : NV;
   extern __shared__ float acc[];           // kWide: [2][kCols]; else [G][2][kCols] at the end
   __shared__ float2 red[2][G][kWarps];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int warp = t >> 5, lane = threadIdx.x & 31;
-  float dw[kWide ? 1 : NV][E], db[kWide ? 1 : NV][E], w[kWide ? 1 : NV][E];
-  if constexpr (kWide) {
-    for (int c = threadIdx.x; c < 2 * kCols; c += kThreads) acc[c] = 0.f;
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, w[i]);
-#pragma unroll
-      for (int j = 0; j < E; ++j) dw[i][j] = db[i][j] = 0.f;
-    }
-  }
+  uint64_t dw[kHeld][E2], db[kHeld][E2], w[kHeld][E2];
   uint4 rx[NV], rd[NV];
   float mean = 0.f, r = 0.f;
   auto load = [&](int64_t row) {
@@ -271,112 +336,135 @@ __global__ void __launch_bounds__(TPR > kBwdThreads ? TPR : kBwdThreads)
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t row = (int64_t)blockIdx.x * G + grp;
   if constexpr (!kWide) load(row);
+  if constexpr (kWide) {
+    for (int c = threadIdx.x; c < 2 * kCols; c += kThreads) acc[c] = 0.f;
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, w[i]);
+#pragma unroll
+      for (int j = 0; j < E2; ++j) dw[i][j] = db[i][j] = 0ull;
+    }
+  }
   int slot = 0;
   for (int64_t first = (int64_t)blockIdx.x * G; first < a.T; first += step, row += step) {
     if constexpr (kWide) load(row);
-    float s1 = 0.f, s2 = 0.f;
-    float n[kWide ? 1 : NV][E], g[kWide ? 1 : NV][E];
-    const float rc = r, mc = mean;
-    auto widen_piece = [&](int i, float (&ni)[E], float (&gi)[E], const float (&wi)[E], bool sums) {
-      float d[E];
-      widen(rx[i], ni);
-      widen(rd[i], d);
+    uint64_t s1 = 0ull, s2 = 0ull;
+    uint64_t n[kHeld][E2], g[kHeld][E2];
+    const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
+    // n and g of a piece; the first time its share of the sums too
+    auto take = [&](int i, uint64_t (&ni)[E2], uint64_t (&gi)[E2], const uint64_t (&wi)[E2],
+                    bool sums) {
+      uint64_t d[E2];
+      widen<T>(rx[i], ni);
+      widen<T>(rd[i], d);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const bool in = column<T, TPR, kVec>(t, i, j) < a.D;
-        ni[j] = in ? (ni[j] - mc) * rc : 0.f;
-        gi[j] = in ? d[j] * wi[j] : 0.f;
+      for (int j = 0; j < E2; ++j) {
+        ni[j] = inside<T, TPR, kVec>(mul2(add2(ni[j], m2), r2), t, i, j, a.D);
+        gi[j] = mul2(d[j], wi[j]);   // past the row: zeros
         if (!sums) continue;
-        s1 += gi[j];
-        s2 = fmaf(gi[j], ni[j], s2);
+        s1 = add2(s1, gi[j]);
+        s2 = fma2(gi[j], ni[j], s2);
         if constexpr (kWide) {
-          if (in && a.partial) {
-            const int c = (i * E + j) * TPR + t;   // no two lanes on one bank
-            acc[c] = fmaf(d[j], ni[j], acc[c]);
-            acc[kCols + c] += d[j];
+          if (a.partial) {
+            uint64_t* p = reinterpret_cast<uint64_t*>(acc) + (i * E2 + j) * TPR + t;
+            p[0] = fma2(d[j], ni[j], p[0]);
+            p[kCols / 2] = add2(p[kCols / 2], d[j]);
           }
         } else {
-          dw[i][j] = fmaf(d[j], ni[j], dw[i][j]);
-          db[i][j] += d[j];
+          dw[i][j] = fma2(d[j], ni[j], dw[i][j]);
+          db[i][j] = add2(db[i][j], d[j]);
         }
       }
     };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if constexpr (kWide) {
-        float wi[E];
+        uint64_t wi[E2];
         load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, wi);
-        widen_piece(i, n[0], g[0], wi, true);
+        take(i, n[0], g[0], wi, true);
       } else {
-        widen_piece(i, n[i], g[i], w[i], true);
+        take(i, n[i], g[i], w[i], true);
       }
     }
+    const float rc = r;
     if constexpr (!kWide) load(row + step);   // in flight during the sums
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+    float c1 = warp_sum(sum2(s1)), c2 = warp_sum(sum2(s2));
     if constexpr (kWarps > 1) {
-      if (lane == 0) red[slot][grp][warp] = make_float2(s1, s2);
+      if (lane == 0) red[slot][grp][warp] = make_float2(c1, c2);
       __syncthreads();
-      s1 = s2 = 0.f;
+      c1 = c2 = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        s1 += red[slot][grp][i].x;
-        s2 += red[slot][grp][i].y;
+        c1 += red[slot][grp][i].x;
+        c2 += red[slot][grp][i].y;
       }
       slot ^= 1;   // the next pass writes the other slot: one barrier a pass
     }
     if (a.y != nullptr && row < a.T) {
-      const float c1 = s1 * a.inv_D, c2 = s2 * a.inv_D;
+      c1 *= -a.inv_D * rc;
+      c2 *= -a.inv_D;
+      const uint64_t k1 = pack2(c1, c1), k2 = pack2(c2, c2), kr = pack2(rc, rc);
       T* dst = static_cast<T*>(a.y) + row * a.D;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        constexpr int kOne = 0;
-        const int k = kWide ? kOne : i;
+        const int k = kWide ? 0 : i;
         if constexpr (kWide) {
-          float wi[E];
+          uint64_t wi[E2];
           load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, wi);
-          widen_piece(i, n[0], g[0], wi, false);
+          take(i, n[0], g[0], wi, false);
         }
-        float dx[E];
+        uint64_t dx[E2];
 #pragma unroll
-        for (int j = 0; j < E; ++j) dx[j] = rc * (fmaf(-n[k][j], c2, g[k][j]) - c1);
+        for (int j = 0; j < E2; ++j) dx[j] = fma2(fma2(n[k][j], k2, g[k][j]), kr, k1);
         store_piece<T, TPR, kVec>(dst, t, i, a.D, dx);
       }
     }
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
-  if constexpr (kWide) {   // a thread's own columns: no barrier
+  if constexpr (kWide || G == 1) {   // a thread's own columns: no barrier
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = column<T, TPR, kVec>(t, i, j), s = (i * E + j) * TPR + t;
-        if (c < a.D) {
-          out[c] = acc[s];
-          out[a.D + c] = acc[kCols + s];
+      for (int j = 0; j < E2; ++j) {
+        uint64_t vw, vb;
+        if constexpr (kWide) {
+          const uint64_t* p = reinterpret_cast<const uint64_t*>(acc) + (i * E2 + j) * TPR + t;
+          vw = p[0];
+          vb = p[kCols / 2];
+        } else {
+          vw = dw[i][j];
+          vb = db[i][j];
         }
-      }
-  } else if constexpr (G == 1) {
+        float fw[2], fb[2];
+        unpack2(vw, fw[0], fw[1]);
+        unpack2(vb, fb[0], fb[1]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = column<T, TPR, kVec>(t, i, j);
-        if (c < a.D) {
-          out[c] = dw[i][j];
-          out[a.D + c] = db[i][j];
+        for (int e = 0; e < 2; ++e) {
+          const int c = column<T, TPR, kVec>(t, i, 2 * j + e);
+          if (c < a.D) {
+            out[c] = fw[e];
+            out[a.D + c] = fb[e];
+          }
         }
       }
   } else {
-    float* mine = acc + grp * 2 * kCols;
+    float* own = acc + grp * 2 * kCols;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int c = column<T, TPR, kVec>(t, i, j);
-        mine[c] = dw[i][j];
-        mine[kCols + c] = db[i][j];
+      for (int j = 0; j < E2; ++j) {
+        float fw[2], fb[2];
+        unpack2(dw[i][j], fw[0], fw[1]);
+        unpack2(db[i][j], fb[0], fb[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int c = column<T, TPR, kVec>(t, i, 2 * j + e);
+          own[c] = fw[e];
+          own[kCols + c] = fb[e];
+        }
       }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * kCols; c += kThreads) {
@@ -412,55 +500,60 @@ __global__ void __launch_bounds__(kDwWarps * 32)
   }
 }
 
-template <int V>
-using Int = std::integral_constant<int, V>;
+// Threads per row, 16-byte pieces per thread and blocks per SM of a launch.
+struct Shape {
+  int tpr, nv, blocks;
+};
+constexpr Shape kFwdShapes[] = {{32, 1, 4},  {32, 2, 3},  {64, 2, 3},  {128, 2, 3},
+                                {256, 2, 3}, {256, 4, 2}, {512, 4, 1}, {1024, 4, 1}};
+// fp32: half the elements a piece, so fewer registers
+constexpr Shape kFwdShapesF32[] = {{32, 1, 4},  {32, 2, 4},  {64, 2, 4},   {128, 2, 4},
+                                   {256, 2, 4}, {512, 2, 2}, {1024, 2, 1}, {1024, 4, 1}};
+constexpr Shape kBwdShapes[] = {{32, 1, 3},  {32, 2, 2},  {64, 2, 2},   {128, 2, 2},
+                                {256, 2, 2}, {512, 2, 1}, {1024, 2, 1}, {1024, 4, 1}};
+constexpr int kBwdWideFrom = 6;   // shapes with sums in shared memory
 
-// f(threads per row, pieces per thread) for a row of `pieces` 16-byte pieces
-template <typename F>
-cudaError_t by_width_fwd(int pieces, F f) {
-  if (pieces <= 32) return f(Int<32>{}, Int<1>{});
-  if (pieces <= 64) return f(Int<32>{}, Int<2>{});
-  if (pieces <= 128) return f(Int<32>{}, Int<4>{});
-  if (pieces <= 256) return f(Int<32>{}, Int<8>{});
-  if (pieces <= 512) return f(Int<128>{}, Int<4>{});
-  if (pieces <= 1024) return f(Int<256>{}, Int<4>{});
-  if (pieces <= 2048) return f(Int<512>{}, Int<4>{});
-  return f(Int<1024>{}, Int<4>{});
+// The shape of rows of `pieces` 16-byte pieces: 32, 64, 128, ... at most.
+int shape_of(int pieces) {
+  int i = 0;
+  while ((32 << i) < pieces) ++i;
+  return i;
 }
-template <typename F>
-cudaError_t by_width_bwd(int pieces, F f) {
-  if (pieces <= 32) return f(Int<32>{}, Int<1>{}, Int<0>{});
-  if (pieces <= 64) return f(Int<32>{}, Int<2>{}, Int<0>{});
-  if (pieces <= 128) return f(Int<64>{}, Int<2>{}, Int<0>{});
-  if (pieces <= 256) return f(Int<128>{}, Int<2>{}, Int<0>{});
-  if (pieces <= 512) return f(Int<256>{}, Int<2>{}, Int<0>{});
-  if (pieces <= 1024) return f(Int<512>{}, Int<2>{}, Int<0>{});
-  if (pieces <= 2048) return f(Int<1024>{}, Int<2>{}, Int<1>{});
-  return f(Int<1024>{}, Int<4>{}, Int<1>{});
+
+// f(the shape's number as an integral constant)
+template <int I = 0, typename F>
+cudaError_t by_shape(int i, F f) {
+  if constexpr (I < 8) return i == I ? f(std::integral_constant<int, I>{}) : by_shape<I + 1>(i, f);
+  else return cudaErrorInvalidValue;
 }
 
 int pieces_of(int D, bool bf16) { return bf16 ? (D + 7) / 8 : (D + 3) / 4; }
 
+int blocks_of(const Shape& s, int64_t T, int sms) {
+  const int rows = block_threads(s.tpr) / s.tpr;
+  const int64_t need = (T + rows - 1) / rows, most = (int64_t)s.blocks * sms;
+  return (int)(need < most ? need : most);
+}
+
 template <typename T, bool kVec>
-cudaError_t fwd_t(const LayerNormArgs& a, cudaStream_t st) {
-  return by_width_fwd(pieces_of(a.D, sizeof(T) == 2), [&](auto tpr, auto nv) {
-    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    const int64_t blocks = TPR == 32 ? (a.T + 7) / 8 : a.T;
-    layer_norm_fwd_kernel<T, TPR, NV, kVec>
-        <<<(unsigned)blocks, TPR == 32 ? 256 : TPR, 0, st>>>(a);
+cudaError_t fwd_t(const LayerNormArgs& a, int sms, cudaStream_t st) {
+  return by_shape(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
+    constexpr Shape s = sizeof(T) == 2 ? kFwdShapes[decltype(i)::value]
+                                       : kFwdShapesF32[decltype(i)::value];
+    layer_norm_fwd_kernel<T, s.tpr, s.nv, kVec, s.blocks>
+        <<<blocks_of(s, a.T, sms), block_threads(s.tpr), 0, st>>>(a);
     return cudaGetLastError();
   });
 }
 
 template <typename T, bool kVec>
 cudaError_t bwd_t(const LayerNormArgs& a, int blocks, cudaStream_t st) {
-  return by_width_bwd(pieces_of(a.D, sizeof(T) == 2), [&](auto tpr, auto nv, auto wide) {
-    constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-    constexpr bool kWide = decltype(wide)::value != 0;
-    constexpr int kThreads = TPR > kBwdThreads ? TPR : kBwdThreads;
-    constexpr int G = kThreads / TPR;
-    constexpr int smem = (kWide || G > 1) ? G * 2 * TPR * NV * kPiece<T> * 4 : 0;
-    auto kernel = layer_norm_bwd_kernel<T, TPR, NV, kVec, kWide>;
+  return by_shape(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
+    constexpr Shape s = kBwdShapes[decltype(i)::value];
+    constexpr bool kWide = decltype(i)::value >= kBwdWideFrom;
+    constexpr int kThreads = block_threads(s.tpr), G = kThreads / s.tpr;
+    constexpr int smem = (kWide || G > 1) ? G * 2 * s.tpr * s.nv * kPiece<T> * 4 : 0;
+    auto kernel = layer_norm_bwd_kernel<T, s.tpr, s.nv, kVec, kWide, s.blocks>;
     if (smem > 48 * 1024) {
       cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -474,20 +567,14 @@ cudaError_t bwd_t(const LayerNormArgs& a, int blocks, cudaStream_t st) {
 }  // namespace
 
 int layer_norm_bwd_blocks(int64_t T, int D, bool bf16, int sms) {
-  const int pieces = pieces_of(D, bf16);
-  int64_t rows = 1, per_sm = 1;   // rows of one pass, blocks that fit an SM
-  if (pieces <= 64) rows = 8;
-  else if (pieces <= 128) rows = 4;
-  else if (pieces <= 256) rows = 2;
-  if (pieces <= 512) per_sm = 2;
-  const int64_t need = (T + rows - 1) / rows;
-  const int64_t most = per_sm * sms;
-  return (int)(need < most ? need : most);
+  return blocks_of(kBwdShapes[shape_of(pieces_of(D, bf16))], T, sms);
 }
 
-cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, bool bf16, bool vec, cudaStream_t st) {
-  if (bf16) return vec ? fwd_t<__nv_bfloat16, true>(a, st) : fwd_t<__nv_bfloat16, false>(a, st);
-  return vec ? fwd_t<float, true>(a, st) : fwd_t<float, false>(a, st);
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, bool bf16, bool vec, int sms,
+                                  cudaStream_t st) {
+  if (bf16)
+    return vec ? fwd_t<__nv_bfloat16, true>(a, sms, st) : fwd_t<__nv_bfloat16, false>(a, sms, st);
+  return vec ? fwd_t<float, true>(a, sms, st) : fwd_t<float, false>(a, sms, st);
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, bool bf16, bool vec, int blocks,

@@ -29,7 +29,8 @@ int layer_norm_bwd_blocks(int64_t T, int D, bool bf16, int sms);
 
 // vec: rows, weights and outputs lie on 16-byte boundaries and D is whole 16-byte
 // pieces (vector loads), else element loads.
-cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, bool bf16, bool vec, cudaStream_t st);
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a, bool bf16, bool vec, int sms,
+                                  cudaStream_t st);
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, bool bf16, bool vec, int blocks,
                                   cudaStream_t st);
 // dw[e], db[e]: sums of partial[b][0][e], partial[b][1][e] over the blocks, in a fixed order.
