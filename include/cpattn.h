@@ -469,6 +469,59 @@ cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const 
                               void* stream);
 
 /*
+ * cp_gated_ffn_fwd / cp_gated_ffn_bwd -- the gated feed-forward block that follows
+ * the attention in a transformer layer, and its gradient.
+ *
+ *   g = x w_gate^T,  u = x w_up^T,  h = a(g) u,  y = h w_down^T
+ *   dh = dy w_down,  dg = dh u a'(g),  du = dh a(g),  dx = dg w_gate + du w_up,
+ *   dw_gate = dg^T x,  dw_up = du^T x,  dw_down = dy^T h
+ *
+ * CP_BF16: tensor cores, sums and activation in fp32; g and u where kept, h, dg and
+ * du are rounded to bf16 once, as operands of the next product, and the results
+ * once.  CP_F32: CUDA cores, fp32 throughout.  A NaN or infinity reaches the rows of
+ * y, dx and the parts of the weights' gradients that the formulas give it.
+ *
+ *   x [T][D], dy [T][D_out], w_gate, w_up [F][D], w_down [D_out][F]   row strides in
+ *                   elements; rows do not overlap (e.g. halves of one [2 F][D] weight)
+ *   y [T][D_out], gate, up [T][F], dx [T][D]   contiguous, dtype; must not overlap an
+ *                   input.  Forward: gate, up: g and u for the backward, or both NULL
+ *   dw_gate, dw_up [F][D], dw_down [D_out][F]   contiguous, grad_dtype (CP_F32, or
+ *                   CP_BF16 with bf16 inputs), summed over all rows in fp32
+ *   dx, dw_*        NULL: not wanted, and its product is left out
+ *   workspace       >= cp_gated_ffn_{fwd,bwd}_workspace_size(desc) bytes, 256-byte
+ *                   aligned, of this call's own while it runs; its status word is
+ *                   read by cp_workspace_status
+ * Every pointer 16-byte aligned, row strides whole 16-byte pieces.  D, F and D_out are
+ * multiples of 8; T is any number.  Sums do not depend on timing.  Every call is
+ * launches and memsets alone, so it can be captured into a graph.  T == 0: no rows are
+ * touched; the weights' gradients are zeroed.
+ * The *_workspace_size functions return 0 on a bad descriptor or without a device.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_SHAPE, CP_ERR_DTYPE, CP_ERR_ALIGNMENT,
+ * CP_ERR_WORKSPACE, CP_ERR_CUDA.
+ */
+typedef enum {
+  CP_ACT_SILU = 0,       /* g / (1 + e^-g) */
+  CP_ACT_GELU = 1,       /* g (1 + erf(g / sqrt 2)) / 2 */
+  CP_ACT_GELU_TANH = 2   /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+} cp_activation_t;
+typedef struct {
+  cp_dtype_t dtype;
+  cp_dtype_t grad_dtype;     /* of dw_gate, dw_up, dw_down */
+  cp_activation_t activation;
+  int T, D, F, D_out;
+  int64_t x_stride, w_gate_stride, w_up_stride, w_down_stride, dy_stride;
+} cp_gated_ffn_t;
+size_t cp_gated_ffn_fwd_workspace_size(const cp_gated_ffn_t* desc);
+size_t cp_gated_ffn_bwd_workspace_size(const cp_gated_ffn_t* desc);
+cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+                             const void* w_up, const void* w_down, void* y, void* gate, void* up,
+                             void* workspace, size_t ws_bytes, void* stream);
+cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+                             const void* w_up, const void* w_down, const void* gate,
+                             const void* up, const void* dy, void* dx, void* dw_gate, void* dw_up,
+                             void* dw_down, void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * cp_score_plan_* -- work lists of attention with modified scores.
  * They depend on the packing alone: build the block on the host once per
  * packing, copy it to the device (256-byte aligned) and pass both copies to

@@ -130,3 +130,60 @@ def test_heads_that_share_memory_are_seen():
     assert not rope._disjoint(x[:, :4], x[:, 3:6]) and not rope._disjoint(x, x)
     assert not rope._disjoint(x[:, ::2], x[:, 1::2])   # apart, but not seen to be: refused
     assert rope._disjoint(x[:1, :4], x[:1, 4:6])
+
+
+def _ffn_desc(**over):
+    f = B.GatedFfnDesc()
+    f.dtype, f.grad_dtype, f.activation, f.T, f.D, f.F, f.D_out = 1, 1, 0, 4, 64, 128, 32
+    f.x_stride, f.w_gate_stride, f.w_up_stride, f.w_down_stride, f.dy_stride = 64, 64, 64, 128, 32
+    for k, v in over.items():
+        setattr(f, k, v)
+    return f
+
+
+def _ffn_fwd(f, x=A, wg=A, wu=A, wd=A, y=A, gate=A, up=A, ws=A, n=0):
+    return B.lib().cp_gated_ffn_fwd(f, x, wg, wu, wd, y, gate, up, ws, n, None)
+
+
+def _ffn_bwd(f, x=A, wg=A, wu=A, wd=A, gate=A, up=A, dy=A, dx=A, dwg=A, dwu=A, dwd=A, ws=A, n=0):
+    return B.lib().cp_gated_ffn_bwd(f, x, wg, wu, wd, gate, up, dy, dx, dwg, dwu, dwd, ws, n, None)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(dtype=7), 3), (dict(grad_dtype=5), 3), (dict(dtype=0, grad_dtype=1), 3), (dict(activation=3), 1),
+    (dict(activation=-1), 1), (dict(T=-1), 1), (dict(D=0), 2), (dict(D=60), 2), (dict(F=4), 2), (dict(D_out=12), 2),
+    (dict(F=(1 << 20) + 8), 2), (dict(x_stride=56), 2), (dict(dy_stride=0), 2), (dict(w_gate_stride=-64), 2),
+    (dict(w_down_stride=120), 2), (dict(x_stride=68), 4), (dict(w_up_stride=66), 4), (dict(x_stride=1 << 40), 2)])
+def test_gated_ffn_descriptors(cplib, over, status):
+    f = _ffn_desc(**over)
+    assert _ffn_fwd(f) == status and _ffn_bwd(f) == status
+    assert B.lib().cp_last_error()
+    assert B.lib().cp_gated_ffn_fwd_workspace_size(f) == 0 and B.lib().cp_gated_ffn_bwd_workspace_size(f) == 0
+
+
+def test_gated_ffn_pointers(cplib):
+    f = _ffn_desc()
+    assert _ffn_fwd(None) == 1 and _ffn_bwd(None) == 1
+    for name in ("x", "wg", "wu", "wd", "y", "gate", "up"):
+        assert _ffn_fwd(f, **{name: None}) == 1, name
+        assert _ffn_fwd(f, **{name: A8}) == 4, name
+    for name in ("x", "wg", "wu", "wd", "gate", "up", "dy"):
+        assert _ffn_bwd(f, **{name: None}) == 1, name
+    for name in ("x", "wg", "wu", "wd", "gate", "up", "dy", "dx", "dwg", "dwu", "dwd"):
+        assert _ffn_bwd(f, **{name: A8}) == 4, name
+    assert _ffn_fwd(f, ws=None) == 5 and _ffn_bwd(f, ws=None) == 5
+    # nothing to do
+    assert _ffn_fwd(_ffn_desc(T=0), None, None, None, None, None, None, None, None) == 0
+    assert _ffn_bwd(_ffn_desc(T=0), dx=None, dwg=None, dwu=None, dwd=None, ws=None) == 0
+    assert _ffn_bwd(f, dx=None, dwg=None, dwu=None, dwd=None, ws=None) == 0
+
+
+def test_rows_that_need_a_copy():
+    from vlm_zigzag_head_gb300.ffn import _aligned
+    x = torch.zeros(6, 64, dtype=torch.bfloat16)
+    assert _aligned(x) is x and _aligned(x[:, :32]).data_ptr() == x.data_ptr()
+    for view in (x[:, 1:9], x[:1].expand(6, 64), x.t(), torch.zeros(6, 36, dtype=torch.bfloat16)[:, :32],
+                 x[:, :1].expand(6, 64)):
+        got = _aligned(view)
+        assert got.data_ptr() % 16 == 0 and got.is_contiguous() and torch.equal(got, view)
+    assert _aligned(x[2]).data_ptr() == x[2].data_ptr()

@@ -15,6 +15,7 @@ Functions keep the names of the C entry points:
 * :func:`cp_rope_fwd`, :func:`cp_rope_bwd` (frequencies: :func:`rope_frequencies`) -- the
   rotation alone, for long contexts too
 * :func:`cp_layer_norm_fwd`, :func:`cp_layer_norm_bwd` -- layer norm of token rows
+* :func:`cp_gated_ffn_fwd`, :func:`cp_gated_ffn_bwd` -- the gated feed-forward block
 * :func:`cp_attn_scored_fwd`, :func:`cp_attn_scored_bwd` (plans: :class:`ScorePlan`) --
   attention with capped or distance-biased scores
 * :func:`cp_workspace_status`, :func:`cp_set_wait_limit`, :func:`cp_plan_pairs`,
@@ -38,7 +39,7 @@ __all__ = ["cp_zigzag_index", "cp_zigzag_gather", "cp_zigzag_scatter", "cp_attn_
            "attention_host", "CpError", "cp_qk_norm_rope_fwd", "cp_qk_norm_rope_bwd",
            "cp_attn_scored_fwd", "cp_attn_scored_bwd", "ScorePlan", "relative_buckets",
            "cp_layer_norm_fwd", "cp_layer_norm_bwd", "cp_rope_fwd", "cp_rope_bwd",
-           "rope_frequencies"]
+           "rope_frequencies", "cp_gated_ffn_fwd", "cp_gated_ffn_bwd"]
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -534,6 +535,7 @@ def attention_host(q, k, v, dout, cu_seqlens, P: int, prefix_len: int, softmax_s
     return tuple(host_out[:n_res])
 
 
+from .ffn import cp_gated_ffn_bwd, cp_gated_ffn_fwd  # noqa: E402
 from .layer_norm import cp_layer_norm_bwd, cp_layer_norm_fwd  # noqa: E402
 from .norm_rope import cp_qk_norm_rope_bwd, cp_qk_norm_rope_fwd  # noqa: E402
 from .rope import cp_rope_bwd, cp_rope_fwd, rope_frequencies  # noqa: E402

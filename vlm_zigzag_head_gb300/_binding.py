@@ -58,6 +58,14 @@ class LayerNormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class GatedFfnDesc(ctypes.Structure):
+    """cp_gated_ffn_t."""
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "grad_dtype", "activation", "T", "D", "F",
+                                            "D_out")] + \
+               [(n, ctypes.c_int64) for n in ("x_stride", "w_gate_stride", "w_up_stride",
+                                              "w_down_stride", "dy_stride")]
+
+
 class ScoreDesc(ctypes.Structure):
     """cp_score_t."""
     _fields_ = [("softcap", ctypes.c_float), ("slopes", c_vp), ("rel_bias", c_vp),
@@ -129,6 +137,12 @@ SIGNATURES = {
     "cp_layer_norm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerNormDesc)]),
     "cp_layer_norm_bwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 9 +
                           [ctypes.c_size_t, c_vp]),
+    "cp_gated_ffn_fwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GatedFfnDesc)]),
+    "cp_gated_ffn_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GatedFfnDesc)]),
+    "cp_gated_ffn_fwd": (ctypes.c_int, [ctypes.POINTER(GatedFfnDesc)] + [c_vp] * 8 +
+                         [ctypes.c_size_t, c_vp]),
+    "cp_gated_ffn_bwd": (ctypes.c_int, [ctypes.POINTER(GatedFfnDesc)] + [c_vp] * 12 +
+                         [ctypes.c_size_t, c_vp]),
     "cp_score_plan_size": (ctypes.c_size_t, _PLAN),
     "cp_score_plan_build": (ctypes.c_int, _PLAN + [c_vp, ctypes.c_size_t]),
     "cp_score_plan_pairs": (ctypes.c_int, [c_vp, c_i64p, c_i64p, c_i64p]),

@@ -1,0 +1,496 @@
+// C ABI of the gated feed-forward block: argument checks, work split and the launch
+// sequence.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "../../include/cpattn.h"
+#include "entry.h"
+#include "ffn.h"
+
+using namespace cpattn;
+
+namespace {
+
+constexpr int kMaxWidth = 1 << 20;
+constexpr size_t kStatusBytes = 256;   // status word at the start of a workspace
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline int tiles(int64_t n, int tile) { return (int)((n + tile - 1) / tile); }
+
+cp_status_t check_desc(const cp_gated_ffn_t* p) {
+  if (!p) return entry_fail(CP_ERR_INVALID_ARG, "desc is NULL");
+  if (p->dtype != CP_F32 && p->dtype != CP_BF16)
+    return entry_fail(CP_ERR_DTYPE, "dtype must be CP_F32 or CP_BF16");
+  if (p->grad_dtype != CP_F32 && !(p->grad_dtype == CP_BF16 && p->dtype == CP_BF16))
+    return entry_fail(CP_ERR_DTYPE, "grad_dtype must be CP_F32, or CP_BF16 with bf16 inputs");
+  if (p->activation < CP_ACT_SILU || p->activation > CP_ACT_GELU_TANH)
+    return entry_fail(CP_ERR_INVALID_ARG, "unknown activation");
+  if (p->T < 0) return entry_fail(CP_ERR_INVALID_ARG, "T >= 0");
+  for (int n : {p->D, p->F, p->D_out})
+    if (n < 8 || n > kMaxWidth || n % 8 != 0)
+      return entry_fail(CP_ERR_SHAPE, "D, F and D_out must be multiples of 8 in [8, 2^20]");
+  const int per16 = p->dtype == CP_BF16 ? 8 : 4;
+  const struct { int64_t stride, rows, width; } m[5] = {
+      {p->x_stride, p->T, p->D},         {p->w_gate_stride, p->F, p->D},
+      {p->w_up_stride, p->F, p->D},      {p->w_down_stride, p->D_out, p->F},
+      {p->dy_stride, p->T, p->D_out}};
+  for (int i = 0; i < 5; ++i) {
+    if (m[i].rows <= 1) continue;   // never used
+    if (m[i].stride < m[i].width)
+      return entry_fail(CP_ERR_SHAPE, "rows must not overlap");
+    if (m[i].stride % per16 != 0)
+      return entry_fail(CP_ERR_ALIGNMENT, "row strides must be whole 16-byte pieces");
+    if (m[i].stride >= (int64_t)1 << 36)
+      return entry_fail(CP_ERR_SHAPE, "a row stride is too large");
+  }
+  return CP_OK;
+}
+
+// 16-byte aligned and not NULL.
+cp_status_t check_ptr(const void* p, const char* name) {
+  if (!p) return entry_fail(CP_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (!aligned_to(p, 16))
+    return entry_fail(CP_ERR_ALIGNMENT, std::string(name) + " must be 16-byte aligned");
+  return CP_OK;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Shares of k that a product's tiles are cut into: as many as fit the SMs at once,
+// each of at least four k tiles.
+int share_k(int64_t n_tiles, int k_tiles, int at_once) {
+  if (2 * n_tiles > at_once) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(at_once / n_tiles, k_tiles / 4));
+}
+
+constexpr int kF32K = 16;   // the fp32 kernel's k step; 128 x 128 tiles, two blocks an SM
+int share_k_f32(int64_t M, int64_t N, int64_t K, int sms) {
+  return share_k((int64_t)tiles(M, 128) * tiles(N, 128), tiles(K, 4 * kF32K), 2 * sms);
+}
+
+// How each product is cut, and what of the workspace it takes.
+struct Plan {
+  int sms = 0;
+  int gate_up = 1, down = 1;                 // forward
+  int dh = 1, d_down = 1, d_in = 1, dx = 1;  // backward
+  size_t fwd_partial = 0, bwd_partial = 0;   // bytes
+};
+
+Plan make_plan(const cp_gated_ffn_t* p, int sms) {
+  Plan r;
+  r.sms = sms;
+  const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
+  if (p->dtype == CP_BF16) {
+    const int64_t mt = tiles(T, kGemmM);
+    r.gate_up = share_k(mt * tiles(F, kGemmN / 2), tiles(D, kGemmK), sms);
+    r.down = share_k(mt * tiles(O, kGemmN), tiles(F, kGemmK), sms);
+    r.dh = share_k(mt * tiles(F, kGemmN), tiles(O, kGemmK), sms);
+    r.dx = share_k(mt * tiles(D, kGemmN), 2 * tiles(F, kGemmK), sms);
+    r.d_down = share_k((int64_t)tiles(O, kGemmM) * tiles(F, kGemmN), tiles(T, kGemmK), sms);
+    r.d_in = share_k((int64_t)2 * tiles(F, kGemmM) * tiles(D, kGemmN), tiles(T, kGemmK), sms);
+  } else {
+    r.gate_up = share_k_f32(T, F, D, sms);
+    r.down = share_k_f32(T, O, F, sms);
+    r.dh = share_k_f32(T, F, O, sms);
+    r.dx = share_k_f32(T, D, F, sms);
+    r.d_down = share_k_f32(O, F, T, sms);
+    r.d_in = share_k_f32(F, D, T, sms);
+  }
+  const bool f32 = p->dtype == CP_F32;
+  auto bytes = [](int shares, int64_t n) { return shares > 1 ? (size_t)shares * n * 4 : 0; };
+  // fp32: gate and up always go through the workspace, and so does dh
+  const size_t gu = f32 ? (size_t)r.gate_up * 2 * T * F * 4 : bytes(r.gate_up, 2 * T * F);
+  const size_t dh = f32 ? (size_t)r.dh * T * F * 4 : bytes(r.dh, T * F);
+  r.fwd_partial = std::max(gu, bytes(r.down, T * O));
+  r.bwd_partial = std::max(std::max(dh, bytes(r.dx, (f32 ? 2 : 1) * T * D)),
+                           std::max(bytes(r.d_down, O * F), bytes(r.d_in, 2 * F * D)));
+  return r;
+}
+
+size_t hidden_bytes(const cp_gated_ffn_t* p) {
+  return up256((size_t)p->T * p->F * (p->dtype == CP_BF16 ? 2 : 4));
+}
+
+size_t fwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
+  return kStatusBytes + hidden_bytes(p) + up256(plan.fwd_partial);
+}
+size_t bwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
+  return kStatusBytes + 3 * hidden_bytes(p) + up256(plan.bwd_partial);
+}
+
+cp_status_t check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned_to(ws, 256))
+    return entry_fail(CP_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  if (have < need)
+    return entry_fail(CP_ERR_WORKSPACE, "workspace smaller than cp_gated_ffn_*_workspace_size()");
+  return CP_OK;
+}
+
+// One operand of a bf16 product: an [rows][cols] matrix in memory.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, stride;
+};
+
+// A product under construction; failures stick.
+struct Product {
+  GemmArgs g = {};
+  int epilogue;
+  bool a_mn, b_mn;
+  const char* err = nullptr;
+
+  Product(int epi, bool amn, bool bmn, int M, int N, int splits, int32_t* status, void* partial)
+      : epilogue(epi), a_mn(amn), b_mn(bmn) {
+    g.M = M;
+    g.N = N;
+    g.m_tiles = g.m_split = tiles(M, kGemmM);
+    g.n_tiles = tiles(N, epi == GEMM_GLU ? kGemmN / 2 : kGemmN);
+    g.splits = splits;
+    g.partial = static_cast<float*>(partial);
+    g.status = status;
+    g.wait_limit = device_wait_limit();
+  }
+  void operand(CUtensorMap* map, const Matrix& m, bool mn) {
+    const char* e = nullptr;
+    if (!make_tmap_matrix(map, m.p, m.rows, m.cols, m.rows > 1 ? m.stride : m.cols, mn ? 64 : 128,
+                          &e) && !err)
+      err = e;
+  }
+  void a(int i, const Matrix& m) { operand(&g.a[i], m, a_mn); }
+  void b(int i, const Matrix& m) { operand(&g.b[i], m, b_mn); }
+  void k(int64_t K, int phases = 1) {
+    g.k_split = tiles(K, kGemmK);
+    g.k_tiles = phases * g.k_split;
+  }
+};
+
+cp_status_t run(const Product& p, const Plan& plan, cudaStream_t st, const char* what) {
+  if (p.err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + p.err);
+  ENTRY_CUDA(launch_gemm_bf16(p.g, p.epilogue, p.a_mn, p.b_mn, plan.sms, st), what);
+  return CP_OK;
+}
+
+cp_status_t join(const GemmArgs& g, int epilogue, int output, int64_t n, bool bf16,
+                 cudaStream_t st, const char* what) {
+  JoinArgs j = {};
+  j.splits = g.splits;
+  j.n = n;
+  j.partial = g.partial + (int64_t)output * g.splits * n;
+  j.out = g.out[output];
+  j.act = g.act;
+  j.gate = g.gate;
+  j.up = g.up;
+  j.dgate = g.dgate;
+  j.dup = g.dup;
+  ENTRY_CUDA(launch_ffn_join(j, epilogue, bf16, st), what);
+  return CP_OK;
+}
+
+cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                     const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
+                     cudaStream_t st) {
+  int32_t* status = reinterpret_cast<int32_t*>(ws);
+  void* h = ws + kStatusBytes;
+  void* partial = ws + kStatusBytes + hidden_bytes(p);
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  cp_status_t e;
+  Product gu(GEMM_GLU, false, false, T, F, plan.gate_up, status, partial);
+  gu.a(0, {x, T, D, p->x_stride});
+  gu.b(0, {wg, F, D, p->w_gate_stride});
+  gu.b(1, {wu, F, D, p->w_up_stride});
+  gu.k(D);
+  gu.g.out[0] = h;
+  gu.g.act = p->activation;
+  gu.g.gate = gate;
+  gu.g.up = up;
+  if ((e = run(gu, plan, st, "gate and up projections")) != CP_OK) return e;
+  if (gu.g.splits > 1 &&
+      (e = join(gu.g, GEMM_GLU, 0, (int64_t)T * F, true, st, "gate and up sums")) != CP_OK)
+    return e;
+  Product down(GEMM_STORE, false, false, T, O, plan.down, status, partial);
+  down.a(0, {h, T, F, F});
+  down.b(0, {wd, O, F, p->w_down_stride});
+  down.k(F);
+  down.g.out[0] = y;
+  if ((e = run(down, plan, st, "down projection")) != CP_OK) return e;
+  if (down.g.splits > 1)
+    return join(down.g, GEMM_STORE, 0, (int64_t)T * O, true, st, "down projection's sums");
+  return CP_OK;
+}
+
+cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                     const void* wu, const void* wd, const void* gate, const void* up,
+                     const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
+                     cudaStream_t st) {
+  int32_t* status = reinterpret_cast<int32_t*>(ws);
+  uint8_t* at = ws + kStatusBytes;
+  void *dg = at, *du = at + hidden_bytes(p), *h = at + 2 * hidden_bytes(p);
+  void* partial = at + 3 * hidden_bytes(p);
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  const bool wide = p->grad_dtype == CP_F32;
+  cp_status_t e;
+  Product dh(GEMM_DGLU, false, true, T, F, plan.dh, status, partial);
+  dh.a(0, {dy, T, O, p->dy_stride});
+  dh.b(0, {wd, O, F, p->w_down_stride});
+  dh.k(O);
+  dh.g.out[0] = h;
+  dh.g.act = p->activation;
+  dh.g.gate = const_cast<void*>(gate);
+  dh.g.up = const_cast<void*>(up);
+  dh.g.dgate = dg;
+  dh.g.dup = du;
+  if ((e = run(dh, plan, st, "hidden gradients")) != CP_OK) return e;
+  if (dh.g.splits > 1 &&
+      (e = join(dh.g, GEMM_DGLU, 0, (int64_t)T * F, true, st, "hidden gradients' sums")) != CP_OK)
+    return e;
+  if (dx) {   // dg Wg + du Wu as one product, k running through both
+    Product q(GEMM_STORE, false, true, T, D, plan.dx, status, partial);
+    q.a(0, {dg, T, F, F});
+    q.a(1, {du, T, F, F});
+    q.b(0, {wg, F, D, p->w_gate_stride});
+    q.b(1, {wu, F, D, p->w_up_stride});
+    q.k(F, 2);
+    q.g.out[0] = dx;
+    if ((e = run(q, plan, st, "input gradient")) != CP_OK) return e;
+    if (q.g.splits > 1 &&
+        (e = join(q.g, GEMM_STORE, 0, (int64_t)T * D, true, st, "input gradient's sums")) != CP_OK)
+      return e;
+  }
+  if (dwd) {
+    Product q(GEMM_STORE, true, true, O, F, plan.d_down, status, partial);
+    q.a(0, {dy, T, O, p->dy_stride});
+    q.b(0, {h, T, F, F});
+    q.k(T);
+    q.g.out[0] = dwd;
+    q.g.out_f32 = wide;
+    if ((e = run(q, plan, st, "down weight's gradient")) != CP_OK) return e;
+    if (q.g.splits > 1 && (e = join(q.g, GEMM_STORE, 0, (int64_t)O * F, !wide, st,
+                                    "down weight gradient's sums")) != CP_OK)
+      return e;
+  }
+  if (dwg || dwu) {   // both as one product, m running through both
+    const bool both = dwg && dwu;
+    Product q(GEMM_STORE, true, true, F, D, plan.d_in, status, partial);
+    q.a(0, {dwg ? dg : du, T, F, F});
+    if (both) {
+      q.a(1, {du, T, F, F});
+      q.g.m_tiles *= 2;
+    }
+    q.b(0, {x, T, D, p->x_stride});
+    q.k(T);
+    q.g.out[0] = dwg ? dwg : dwu;
+    q.g.out[1] = dwu;
+    q.g.out_f32 = wide;
+    if ((e = run(q, plan, st, "gate and up weights' gradients")) != CP_OK) return e;
+    for (int i = 0; i < (both ? 2 : 1) && q.g.splits > 1; ++i)
+      if ((e = join(q.g, GEMM_STORE, i, (int64_t)F * D, !wide, st,
+                    "gate and up weight gradients' sums")) != CP_OK)
+        return e;
+  }
+  return CP_OK;
+}
+
+// fp32: out = A B^T over element strides, its shares joined when there are several.
+struct F32 {
+  float* partial;
+  cudaStream_t st;
+
+  cp_status_t shares(const void* a, int64_t sam, int64_t sak, const void* b, int64_t sbn,
+                     int64_t sbk, int M, int N, int K, int splits, float* out, bool accumulate,
+                     const char* what) const {
+    GemmF32Args g;
+    g.a = static_cast<const float*>(a);
+    g.b = static_cast<const float*>(b);
+    g.sam = sam;
+    g.sak = sak;
+    g.sbn = sbn;
+    g.sbk = sbk;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.splits = splits;
+    g.accumulate = accumulate;
+    g.out = out;
+    ENTRY_CUDA(launch_gemm_f32(g, st), what);
+    return CP_OK;
+  }
+  cp_status_t sum(int splits, int64_t n, void* out, const char* what) const {
+    JoinArgs j = {};
+    j.partial = partial;
+    j.splits = splits;
+    j.n = n;
+    j.out = out;
+    ENTRY_CUDA(launch_ffn_join(j, GEMM_STORE, false, st), what);
+    return CP_OK;
+  }
+  cp_status_t product(const void* a, int64_t sam, int64_t sak, const void* b, int64_t sbn,
+                      int64_t sbk, int M, int N, int K, int splits, void* out,
+                      const char* what) const {
+    float* to = splits > 1 ? partial : static_cast<float*>(out);
+    cp_status_t e = shares(a, sam, sak, b, sbn, sbk, M, N, K, splits, to, false, what);
+    if (e != CP_OK || splits == 1) return e;
+    return sum(splits, (int64_t)M * N, out, what);
+  }
+};
+
+cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                    const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
+                    cudaStream_t st) {
+  void* h = ws + kStatusBytes;
+  const F32 f{reinterpret_cast<float*>(ws + kStatusBytes + hidden_bytes(p)), st};
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  const int64_t n = (int64_t)T * F;
+  cp_status_t e;
+  if ((e = f.shares(x, p->x_stride, 1, wg, p->w_gate_stride, 1, T, F, D, plan.gate_up, f.partial,
+                    false, "gate projection")) != CP_OK ||
+      (e = f.shares(x, p->x_stride, 1, wu, p->w_up_stride, 1, T, F, D, plan.gate_up,
+                    f.partial + plan.gate_up * n, false, "up projection")) != CP_OK)
+    return e;
+  JoinArgs j = {};
+  j.partial = f.partial;
+  j.splits = plan.gate_up;
+  j.n = n;
+  j.out = h;
+  j.act = p->activation;
+  j.gate = gate;
+  j.up = up;
+  ENTRY_CUDA(launch_ffn_join(j, GEMM_GLU, false, st), "activation");
+  return f.product(h, F, 1, wd, p->w_down_stride, 1, T, O, F, plan.down, y, "down projection");
+}
+
+cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                    const void* wu, const void* wd, const void* gate, const void* up,
+                    const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
+                    cudaStream_t st) {
+  uint8_t* at = ws + kStatusBytes;
+  void *dg = at, *du = at + hidden_bytes(p), *h = at + 2 * hidden_bytes(p);
+  const F32 f{reinterpret_cast<float*>(at + 3 * hidden_bytes(p)), st};
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  cp_status_t e;
+  if ((e = f.shares(dy, p->dy_stride, 1, wd, 1, p->w_down_stride, T, F, O, plan.dh, f.partial,
+                    false, "hidden gradients")) != CP_OK)
+    return e;
+  JoinArgs j = {};
+  j.partial = f.partial;
+  j.splits = plan.dh;
+  j.n = (int64_t)T * F;
+  j.out = h;
+  j.act = p->activation;
+  j.gate = const_cast<void*>(gate);
+  j.up = const_cast<void*>(up);
+  j.dgate = dg;
+  j.dup = du;
+  ENTRY_CUDA(launch_ffn_join(j, GEMM_DGLU, false, st), "activation's gradient");
+  if (dx) {
+    const int s = plan.dx;
+    const int64_t n = (int64_t)T * D;
+    float* to = s > 1 ? f.partial : static_cast<float*>(dx);
+    if ((e = f.shares(dg, F, 1, wg, 1, p->w_gate_stride, T, D, F, s, to, false,
+                      "input gradient")) != CP_OK ||
+        (e = f.shares(du, F, 1, wu, 1, p->w_up_stride, T, D, F, s, s > 1 ? to + s * n : to, s == 1,
+                      "input gradient")) != CP_OK ||
+        (s > 1 && (e = f.sum(2 * s, n, dx, "input gradient's sums")) != CP_OK))
+      return e;
+  }
+  if (dwd && (e = f.product(dy, 1, p->dy_stride, h, 1, F, O, F, T, plan.d_down, dwd,
+                            "down weight's gradient")) != CP_OK)
+    return e;
+  if (dwg && (e = f.product(dg, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in, dwg,
+                            "gate weight's gradient")) != CP_OK)
+    return e;
+  if (dwu && (e = f.product(du, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in, dwu,
+                            "up weight's gradient")) != CP_OK)
+    return e;
+  return CP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cp_gated_ffn_fwd_workspace_size(const cp_gated_ffn_t* desc) {
+  const int sms = check_desc(desc) == CP_OK ? sm_count() : 0;
+  return sms > 0 ? fwd_bytes(desc, make_plan(desc, sms)) : 0;
+}
+
+size_t cp_gated_ffn_bwd_workspace_size(const cp_gated_ffn_t* desc) {
+  const int sms = check_desc(desc) == CP_OK ? sm_count() : 0;
+  return sms > 0 ? bwd_bytes(desc, make_plan(desc, sms)) : 0;
+}
+
+cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+                             const void* w_up, const void* w_down, void* y, void* gate, void* up,
+                             void* workspace, size_t ws_bytes, void* stream) {
+  ENTRY_TRY
+  cp_status_t e = check_desc(desc);
+  if (e != CP_OK) return e;
+  if (desc->T == 0) return CP_OK;
+  if ((e = check_ptr(x, "x")) != CP_OK || (e = check_ptr(w_gate, "w_gate")) != CP_OK ||
+      (e = check_ptr(w_up, "w_up")) != CP_OK || (e = check_ptr(w_down, "w_down")) != CP_OK ||
+      (e = check_ptr(y, "y")) != CP_OK)
+    return e;
+  if ((gate == nullptr) != (up == nullptr))
+    return entry_fail(CP_ERR_INVALID_ARG, "gate and up are kept together or not at all");
+  if (!aligned_to(gate, 16) || !aligned_to(up, 16))
+    return entry_fail(CP_ERR_ALIGNMENT, "gate and up must be 16-byte aligned");
+  if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
+  const Plan plan = make_plan(desc, sm_count());
+  if (plan.sms < 1) return entry_fail(CP_ERR_CUDA, "no CUDA device");
+  if ((e = check_workspace(workspace, ws_bytes, fwd_bytes(desc, plan))) != CP_OK) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ENTRY_CUDA(cudaMemsetAsync(ws, 0, 8, st), "clear the status word");
+  return desc->dtype == CP_BF16 ? fwd_bf16(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st)
+                                : fwd_f32(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
+  ENTRY_CATCH
+}
+
+cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+                             const void* w_up, const void* w_down, const void* gate,
+                             const void* up, const void* dy, void* dx, void* dw_gate, void* dw_up,
+                             void* dw_down, void* workspace, size_t ws_bytes, void* stream) {
+  ENTRY_TRY
+  cp_status_t e = check_desc(desc);
+  if (e != CP_OK) return e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  for (const void* p : {(const void*)dx, (const void*)dw_gate, (const void*)dw_up,
+                        (const void*)dw_down})
+    if (!aligned_to(p, 16)) return entry_fail(CP_ERR_ALIGNMENT, "gradients must be 16-byte aligned");
+  if (desc->T == 0) {   // no rows: the weights' gradients are zero
+    const size_t elem = desc->grad_dtype == CP_BF16 ? 2 : 4;
+    const size_t in = (size_t)desc->F * desc->D * elem, out = (size_t)desc->F * desc->D_out * elem;
+    if (dw_gate) ENTRY_CUDA(cudaMemsetAsync(dw_gate, 0, in, st), "clear gradients");
+    if (dw_up) ENTRY_CUDA(cudaMemsetAsync(dw_up, 0, in, st), "clear gradients");
+    if (dw_down) ENTRY_CUDA(cudaMemsetAsync(dw_down, 0, out, st), "clear gradients");
+    return CP_OK;
+  }
+  if ((e = check_ptr(x, "x")) != CP_OK || (e = check_ptr(w_gate, "w_gate")) != CP_OK ||
+      (e = check_ptr(w_up, "w_up")) != CP_OK || (e = check_ptr(w_down, "w_down")) != CP_OK ||
+      (e = check_ptr(gate, "gate")) != CP_OK || (e = check_ptr(up, "up")) != CP_OK ||
+      (e = check_ptr(dy, "dy")) != CP_OK)
+    return e;
+  if (!dx && !dw_gate && !dw_up && !dw_down) return CP_OK;   // nothing is wanted
+  if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
+  const Plan plan = make_plan(desc, sm_count());
+  if (plan.sms < 1) return entry_fail(CP_ERR_CUDA, "no CUDA device");
+  if ((e = check_workspace(workspace, ws_bytes, bwd_bytes(desc, plan))) != CP_OK) return e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ENTRY_CUDA(cudaMemsetAsync(ws, 0, 8, st), "clear the status word");
+  return desc->dtype == CP_BF16
+             ? bwd_bf16(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
+                        dw_down, ws, st)
+             : bwd_f32(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
+                       dw_down, ws, st);
+  ENTRY_CATCH
+}
+
+}  // extern "C"
