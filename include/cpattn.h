@@ -476,15 +476,17 @@ cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const 
  *   dh = dy w_down,  dg = dh u a'(g),  du = dh a(g),  dx = dg w_gate + du w_up,
  *   dw_gate = dg^T x,  dw_up = du^T x,  dw_down = dy^T h
  *
- * CP_BF16: tensor cores, sums and activation in fp32; g and u where kept, h, dg and
- * du are rounded to bf16 once, as operands of the next product, and the results
- * once.  CP_F32: CUDA cores, fp32 throughout.  A NaN or infinity reaches the rows of
+ * CP_BF16: tensor cores, sums and activation in fp32; h, dg and du are rounded to
+ * bf16 once, as operands of the next product, and the results once; g and u are
+ * kept for the backward to 24 bits (2^-17 of the value).  CP_F32: CUDA cores, fp32 throughout.  A NaN or infinity reaches the rows of
  * y, dx and the parts of the weights' gradients that the formulas give it.
  *
  *   x [T][D], dy [T][D_out], w_gate, w_up [F][D], w_down [D_out][F]   row strides in
  *                   elements; rows do not overlap (e.g. halves of one [2 F][D] weight)
- *   y [T][D_out], gate, up [T][F], dx [T][D]   contiguous, dtype; must not overlap an
- *                   input.  Forward: gate, up: g and u for the backward, or both NULL
+ *   y [T][D_out], dx [T][D]   contiguous, dtype; must not overlap an input
+ *   gate, up        cp_gated_ffn_kept_size(desc) bytes each: g and u for the backward,
+ *                   in the library's own layout, written by the forward (both, or both
+ *                   NULL: not kept) and read by the backward
  *   dw_gate, dw_up [F][D], dw_down [D_out][F]   contiguous, grad_dtype (CP_F32, or
  *                   CP_BF16 with bf16 inputs), summed over all rows in fp32
  *   dx, dw_*        NULL: not wanted, and its product is left out
@@ -511,6 +513,7 @@ typedef struct {
   int T, D, F, D_out;
   int64_t x_stride, w_gate_stride, w_up_stride, w_down_stride, dy_stride;
 } cp_gated_ffn_t;
+size_t cp_gated_ffn_kept_size(const cp_gated_ffn_t* desc);   /* 0: bad descriptor, T == 0 */
 size_t cp_gated_ffn_fwd_workspace_size(const cp_gated_ffn_t* desc);
 size_t cp_gated_ffn_bwd_workspace_size(const cp_gated_ffn_t* desc);
 cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,

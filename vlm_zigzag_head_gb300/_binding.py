@@ -137,6 +137,7 @@ SIGNATURES = {
     "cp_layer_norm_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerNormDesc)]),
     "cp_layer_norm_bwd": (ctypes.c_int, [ctypes.POINTER(LayerNormDesc)] + [c_vp] * 9 +
                           [ctypes.c_size_t, c_vp]),
+    "cp_gated_ffn_kept_size": (ctypes.c_size_t, [ctypes.POINTER(GatedFfnDesc)]),
     "cp_gated_ffn_fwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GatedFfnDesc)]),
     "cp_gated_ffn_bwd_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GatedFfnDesc)]),
     "cp_gated_ffn_fwd": (ctypes.c_int, [ctypes.POINTER(GatedFfnDesc)] + [c_vp] * 8 +

@@ -90,12 +90,13 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
   if (p->dtype == CP_BF16) {
     const int64_t mt = tiles(T, kGemmM);
-    r.gate_up = share_k(mt * tiles(F, kGemmN / 2), tiles(D, kGemmK), sms);
-    r.down = share_k(mt * tiles(O, kGemmN), tiles(F, kGemmK), sms);
-    r.dh = share_k(mt * tiles(F, kGemmN), tiles(O, kGemmK), sms);
-    r.dx = share_k(mt * tiles(D, kGemmN), 2 * tiles(F, kGemmK), sms);
-    r.d_down = share_k((int64_t)tiles(O, kGemmM) * tiles(F, kGemmN), tiles(T, kGemmK), sms);
-    r.d_in = share_k((int64_t)2 * tiles(F, kGemmM) * tiles(D, kGemmN), tiles(T, kGemmK), sms);
+    const int pairs = sms / 2;
+    r.gate_up = share_k(mt * tiles(F, kGemmN / 2), tiles(D, kGemmK), pairs);
+    r.down = share_k(mt * tiles(O, kGemmN), tiles(F, kGemmK), pairs);
+    r.dh = share_k(mt * tiles(F, kGemmN), tiles(O, kGemmK), pairs);
+    r.dx = share_k(mt * tiles(D, kGemmN), 2 * tiles(F, kGemmK), pairs);
+    r.d_down = share_k((int64_t)tiles(O, kGemmM) * tiles(F, kGemmN), tiles(T, kGemmK), pairs);
+    r.d_in = share_k((int64_t)2 * tiles(F, kGemmM) * tiles(D, kGemmN), tiles(T, kGemmK), pairs);
   } else {
     r.gate_up = share_k_f32(T, F, D, sms);
     r.down = share_k_f32(T, O, F, sms);
@@ -144,6 +145,8 @@ struct Matrix {
 // A product under construction; failures stick.
 struct Product {
   GemmArgs g = {};
+  JoinArgs j = {};       // what its shares become
+  void* outputs[2] = {};
   int epilogue;
   bool a_mn, b_mn;
   const char* err = nullptr;
@@ -154,46 +157,67 @@ struct Product {
     g.N = N;
     g.m_tiles = g.m_split = tiles(M, kGemmM);
     g.n_tiles = tiles(N, epi == GEMM_GLU ? kGemmN / 2 : kGemmN);
-    g.splits = splits;
+    g.splits = j.splits = splits;
     g.partial = static_cast<float*>(partial);
     g.status = status;
     g.wait_limit = device_wait_limit();
+    j.M = M;
+    j.N = N;
   }
-  void operand(CUtensorMap* map, const Matrix& m, bool mn) {
+  void map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows) {
     const char* e = nullptr;
-    if (!make_tmap_matrix(map, m.p, m.rows, m.cols, m.rows > 1 ? m.stride : m.cols, mn ? 64 : 128,
+    if (!make_tmap_matrix(m, x.p, x.rows, x.cols, x.rows > 1 ? x.stride : x.cols, elem, cols, rows,
                           &e) && !err)
       err = e;
   }
-  void a(int i, const Matrix& m) { operand(&g.a[i], m, a_mn); }
-  void b(int i, const Matrix& m) { operand(&g.b[i], m, b_mn); }
+  void a(int i, const Matrix& m) { map(&g.a[i], m, 2, kGemmK, a_mn ? 64 : kGemmM / 2); }
+  void b(int i, const Matrix& m) { map(&g.b[i], m, 2, kGemmK, b_mn ? 64 : kGemmN / 2); }
   void k(int64_t K, int phases = 1) {
     g.k_split = tiles(K, kGemmK);
     g.k_tiles = phases * g.k_split;
   }
+  void box(CUtensorMap* m, void* p, int elem, int64_t stride) {   // what an epilogue moves
+    if (g.splits == 1) map(m, {p, g.M, g.N, stride}, elem, kGemmBox, kGemmBox);
+  }
+  void out(int i, void* p, bool f32 = false) {
+    outputs[i] = p;
+    g.out_f32 = f32;
+    box(&g.out[i], p, f32 ? 4 : 2, g.N);
+  }
+  void act(int activation) { g.act = j.act = activation; }
+  void kept(void* gate, void* up) {
+    j.gate = gate;
+    j.up = up;
+    g.keep = gate != nullptr;
+    if (!gate) return;
+    for (int i = 0; i < 2; ++i) {
+      uint8_t* p = static_cast<uint8_t*>(i ? up : gate);
+      CUtensorMap* m = i ? g.up : g.gate;
+      box(&m[0], p, 2, g.N);
+      if (g.splits == 1)
+        map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, kGemmBox, kGemmBox);
+    }
+  }
+  void gradients(void* dgate, void* dup) {
+    j.dgate = dgate;
+    j.dup = dup;
+    box(&g.dgate, dgate, 2, g.N);
+    box(&g.dup, dup, 2, g.N);
+  }
+
+  cp_status_t run(const Plan& plan, cudaStream_t st, const char* what) {
+    if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
+    ENTRY_CUDA(launch_gemm_bf16(g, epilogue, a_mn, b_mn, plan.sms, st), what);
+    if (g.splits == 1) return CP_OK;
+    const int n = g.m_split < g.m_tiles ? 2 : 1;   // outputs
+    for (int i = 0; i < n; ++i) {
+      j.partial = g.partial + (int64_t)i * g.splits * g.M * g.N;
+      j.out = outputs[i];
+      ENTRY_CUDA(launch_ffn_join(j, epilogue, !g.out_f32, st), what);
+    }
+    return CP_OK;
+  }
 };
-
-cp_status_t run(const Product& p, const Plan& plan, cudaStream_t st, const char* what) {
-  if (p.err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + p.err);
-  ENTRY_CUDA(launch_gemm_bf16(p.g, p.epilogue, p.a_mn, p.b_mn, plan.sms, st), what);
-  return CP_OK;
-}
-
-cp_status_t join(const GemmArgs& g, int epilogue, int output, int64_t n, bool bf16,
-                 cudaStream_t st, const char* what) {
-  JoinArgs j = {};
-  j.splits = g.splits;
-  j.n = n;
-  j.partial = g.partial + (int64_t)output * g.splits * n;
-  j.out = g.out[output];
-  j.act = g.act;
-  j.gate = g.gate;
-  j.up = g.up;
-  j.dgate = g.dgate;
-  j.dup = g.dup;
-  ENTRY_CUDA(launch_ffn_join(j, epilogue, bf16, st), what);
-  return CP_OK;
-}
 
 cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
                      const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
@@ -208,23 +232,16 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   gu.b(0, {wg, F, D, p->w_gate_stride});
   gu.b(1, {wu, F, D, p->w_up_stride});
   gu.k(D);
-  gu.g.out[0] = h;
-  gu.g.act = p->activation;
-  gu.g.gate = gate;
-  gu.g.up = up;
-  if ((e = run(gu, plan, st, "gate and up projections")) != CP_OK) return e;
-  if (gu.g.splits > 1 &&
-      (e = join(gu.g, GEMM_GLU, 0, (int64_t)T * F, true, st, "gate and up sums")) != CP_OK)
-    return e;
+  gu.out(0, h);
+  gu.act(p->activation);
+  gu.kept(gate, up);
+  if ((e = gu.run(plan, st, "gate and up projections")) != CP_OK) return e;
   Product down(GEMM_STORE, false, false, T, O, plan.down, status, partial);
   down.a(0, {h, T, F, F});
   down.b(0, {wd, O, F, p->w_down_stride});
   down.k(F);
-  down.g.out[0] = y;
-  if ((e = run(down, plan, st, "down projection")) != CP_OK) return e;
-  if (down.g.splits > 1)
-    return join(down.g, GEMM_STORE, 0, (int64_t)T * O, true, st, "down projection's sums");
-  return CP_OK;
+  down.out(0, y);
+  return down.run(plan, st, "down projection");
 }
 
 cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
@@ -242,16 +259,11 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   dh.a(0, {dy, T, O, p->dy_stride});
   dh.b(0, {wd, O, F, p->w_down_stride});
   dh.k(O);
-  dh.g.out[0] = h;
-  dh.g.act = p->activation;
-  dh.g.gate = const_cast<void*>(gate);
-  dh.g.up = const_cast<void*>(up);
-  dh.g.dgate = dg;
-  dh.g.dup = du;
-  if ((e = run(dh, plan, st, "hidden gradients")) != CP_OK) return e;
-  if (dh.g.splits > 1 &&
-      (e = join(dh.g, GEMM_DGLU, 0, (int64_t)T * F, true, st, "hidden gradients' sums")) != CP_OK)
-    return e;
+  dh.out(0, h);
+  dh.act(p->activation);
+  dh.kept(const_cast<void*>(gate), const_cast<void*>(up));
+  dh.gradients(dg, du);
+  if ((e = dh.run(plan, st, "hidden gradients")) != CP_OK) return e;
   if (dx) {   // dg Wg + du Wu as one product, k running through both
     Product q(GEMM_STORE, false, true, T, D, plan.dx, status, partial);
     q.a(0, {dg, T, F, F});
@@ -259,42 +271,30 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
     q.b(0, {wg, F, D, p->w_gate_stride});
     q.b(1, {wu, F, D, p->w_up_stride});
     q.k(F, 2);
-    q.g.out[0] = dx;
-    if ((e = run(q, plan, st, "input gradient")) != CP_OK) return e;
-    if (q.g.splits > 1 &&
-        (e = join(q.g, GEMM_STORE, 0, (int64_t)T * D, true, st, "input gradient's sums")) != CP_OK)
-      return e;
+    q.out(0, dx);
+    if ((e = q.run(plan, st, "input gradient")) != CP_OK) return e;
   }
   if (dwd) {
     Product q(GEMM_STORE, true, true, O, F, plan.d_down, status, partial);
     q.a(0, {dy, T, O, p->dy_stride});
     q.b(0, {h, T, F, F});
     q.k(T);
-    q.g.out[0] = dwd;
-    q.g.out_f32 = wide;
-    if ((e = run(q, plan, st, "down weight's gradient")) != CP_OK) return e;
-    if (q.g.splits > 1 && (e = join(q.g, GEMM_STORE, 0, (int64_t)O * F, !wide, st,
-                                    "down weight gradient's sums")) != CP_OK)
-      return e;
+    q.out(0, dwd, wide);
+    if ((e = q.run(plan, st, "down weight's gradient")) != CP_OK) return e;
   }
   if (dwg || dwu) {   // both as one product, m running through both
     const bool both = dwg && dwu;
     Product q(GEMM_STORE, true, true, F, D, plan.d_in, status, partial);
     q.a(0, {dwg ? dg : du, T, F, F});
+    q.out(0, dwg ? dwg : dwu, wide);
     if (both) {
       q.a(1, {du, T, F, F});
+      q.out(1, dwu, wide);
       q.g.m_tiles *= 2;
     }
     q.b(0, {x, T, D, p->x_stride});
     q.k(T);
-    q.g.out[0] = dwg ? dwg : dwu;
-    q.g.out[1] = dwu;
-    q.g.out_f32 = wide;
-    if ((e = run(q, plan, st, "gate and up weights' gradients")) != CP_OK) return e;
-    for (int i = 0; i < (both ? 2 : 1) && q.g.splits > 1; ++i)
-      if ((e = join(q.g, GEMM_STORE, i, (int64_t)F * D, !wide, st,
-                    "gate and up weight gradients' sums")) != CP_OK)
-        return e;
+    if ((e = q.run(plan, st, "gate and up weights' gradients")) != CP_OK) return e;
   }
   return CP_OK;
 }
@@ -323,11 +323,12 @@ struct F32 {
     ENTRY_CUDA(launch_gemm_f32(g, st), what);
     return CP_OK;
   }
-  cp_status_t sum(int splits, int64_t n, void* out, const char* what) const {
+  cp_status_t sum(int splits, int M, int N, void* out, const char* what) const {
     JoinArgs j = {};
     j.partial = partial;
     j.splits = splits;
-    j.n = n;
+    j.M = M;
+    j.N = N;
     j.out = out;
     ENTRY_CUDA(launch_ffn_join(j, GEMM_STORE, false, st), what);
     return CP_OK;
@@ -338,7 +339,7 @@ struct F32 {
     float* to = splits > 1 ? partial : static_cast<float*>(out);
     cp_status_t e = shares(a, sam, sak, b, sbn, sbk, M, N, K, splits, to, false, what);
     if (e != CP_OK || splits == 1) return e;
-    return sum(splits, (int64_t)M * N, out, what);
+    return sum(splits, M, N, out, what);
   }
 };
 
@@ -358,7 +359,8 @@ cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   JoinArgs j = {};
   j.partial = f.partial;
   j.splits = plan.gate_up;
-  j.n = n;
+  j.M = T;
+  j.N = F;
   j.out = h;
   j.act = p->activation;
   j.gate = gate;
@@ -382,7 +384,8 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   JoinArgs j = {};
   j.partial = f.partial;
   j.splits = plan.dh;
-  j.n = (int64_t)T * F;
+  j.M = T;
+  j.N = F;
   j.out = h;
   j.act = p->activation;
   j.gate = const_cast<void*>(gate);
@@ -398,7 +401,7 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
                       "input gradient")) != CP_OK ||
         (e = f.shares(du, F, 1, wu, 1, p->w_up_stride, T, D, F, s, s > 1 ? to + s * n : to, s == 1,
                       "input gradient")) != CP_OK ||
-        (s > 1 && (e = f.sum(2 * s, n, dx, "input gradient's sums")) != CP_OK))
+        (s > 1 && (e = f.sum(2 * s, T, D, dx, "input gradient's sums")) != CP_OK))
       return e;
   }
   if (dwd && (e = f.product(dy, 1, p->dy_stride, h, 1, F, O, F, T, plan.d_down, dwd,
@@ -416,6 +419,12 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
 }  // namespace
 
 extern "C" {
+
+size_t cp_gated_ffn_kept_size(const cp_gated_ffn_t* desc) {
+  if (check_desc(desc) != CP_OK) return 0;
+  return desc->dtype == CP_BF16 ? (size_t)kept_bytes(desc->T, desc->F)
+                                : (size_t)desc->T * desc->F * 4;
+}
 
 size_t cp_gated_ffn_fwd_workspace_size(const cp_gated_ffn_t* desc) {
   const int sms = check_desc(desc) == CP_OK ? sm_count() : 0;

@@ -9,12 +9,23 @@ namespace cpattn {
 
 enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
-// 2-D tensor map over a bf16 [rows][cols] matrix with a row stride in elements (a
-// multiple of 8), box {64, box_rows}, 128-byte swizzle.
+// 2-D tensor map over an [rows][cols] matrix of elements of 1, 2 (bf16) or 4 (fp32)
+// bytes with a row stride in elements (whole 16-byte pieces), box rows of 32, 64 or 128
+// bytes in the swizzle of that size.
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
-                      int64_t stride, int box_rows, const char** err);
+                      int64_t stride, int elem, int box_cols, int box_rows, const char** err);
 
-constexpr int kGemmM = 128, kGemmN = 256, kGemmK = 64;   // tile
+// The projections kept for a bf16 backward hold 24 bits of their fp32 values: a bf16
+// plane [M][N], then a plane of signed bytes, row pitch kept_pitch(N), that say how far
+// the value lies from its bf16 in steps of 2^-8 of a bf16 step.  With bf16 alone their
+// rounding passes into every gradient (dw_down off by 3.5e-3 in relative L2, 2.4e-3
+// so, 1.7e-3 its own rounding).
+inline __host__ __device__ int64_t kept_pitch(int64_t N) { return (N + 15) / 16 * 16; }
+inline __host__ __device__ int64_t kept_low(int64_t M, int64_t N) { return M * N * 2; }  // bytes
+inline int64_t kept_bytes(int64_t M, int64_t N) { return kept_low(M, N) + M * kept_pitch(N); }
+
+// Tile of a CTA pair, k step, and the boxes an epilogue warp moves.
+constexpr int kGemmM = 256, kGemmN = 256, kGemmK = 64, kGemmBox = 32;
 
 // What becomes of a tile of products.
 enum : int {
@@ -26,7 +37,10 @@ enum : int {
 // C[M][N] = sum over k of A(m, k) B(n, k).  A tile of either operand is loaded from
 // memory where k runs along a row (K-major) or where m (n) does (MN-major).
 struct GemmArgs {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a[2], b[2];      // box {64, 128} K-major, {64, 64} MN-major
+  CUtensorMap out[2];          // box {32, 32}; unused where splits > 1
+  CUtensorMap gate[2], up[2];  // the kept planes, box {32, 32}
+  CUtensorMap dgate, dup;      // GEMM_DGLU: written; h goes to out[0]
   int M, N;            // of one output
   int m_tiles, n_tiles;
   int m_split;         // m tiles from here on: a[1], out[1] (m_tiles: none)
@@ -34,13 +48,9 @@ struct GemmArgs {
   int k_split;         // k tiles from here on: a[1], b[1] (k_tiles: none)
   int splits;          // > 1: that many units share a tile's k; sums go to `partial`
   float* partial;      // [splits][M][N], once for each output (GEMM_GLU: gate, up)
-  void* out[2];        // row stride N
   int out_f32;
   int act;
-  void* gate;          // [M][N]; GEMM_GLU: written (nullable), GEMM_DGLU: read
-  void* up;
-  void* dgate;         // GEMM_DGLU: written; h goes to out[0]
-  void* dup;
+  int keep;            // GEMM_GLU: write gate and up
   int32_t* status;
   long long wait_limit;
 };
@@ -50,17 +60,18 @@ cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, bool a_mn, bool b_
 
 // The sums of the shares of a product, and what its epilogue would have done.
 struct JoinArgs {
-  const float* partial;   // [splits][n]; gate and up: [2][splits][n]
+  const float* partial;   // [splits][M][N]; gate and up: [2][splits][M][N]
   int splits;
-  int64_t n;              // elements of the output
-  void* out;              // sum; act(gate) up; h
+  int64_t M;
+  int N;
+  void* out;              // [M][N]: sum; act(gate) up; h
   int act;
-  void* gate;             // as GemmArgs
+  void* gate;             // GEMM_GLU: written (nullable), GEMM_DGLU: read; bf16: both planes
   void* up;
-  void* dgate;
+  void* dgate;            // [M][N]
   void* dup;
 };
-// bf16: out, gate, up, dgate, dup are bf16 (else fp32).
+// bf16: out, dgate, dup are bf16 (else all fp32).
 cudaError_t launch_ffn_join(const JoinArgs& j, int epilogue, bool bf16, cudaStream_t st);
 
 // fp32 products on CUDA cores: partial[split][m][n] = sum over the split's k of

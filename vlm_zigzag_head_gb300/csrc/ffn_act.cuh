@@ -42,6 +42,21 @@ __device__ __forceinline__ float activation(float g, int act, float& da) {
   return g * s;
 }
 
+// The 24 bits kept of v: a bf16 (rounded to nearest) and the rest in steps of 2^-8 of
+// its step.  The sum of bit patterns carries across powers of two.
+__device__ __forceinline__ void split24(float v, uint32_t& hi, uint32_t& lo) {
+  const uint32_t r = __float_as_uint(v) + 0x80u;   // rounded to 24 bits
+  hi = (r + 0x8000u) >> 16;
+  lo = ((r - (hi << 16)) >> 8) & 0xffu;
+  if (v != v) {
+    hi = 0x7fc0u;
+    lo = 0u;
+  }
+}
+__device__ __forceinline__ float join24(uint32_t hi, uint32_t lo) {   // lo: any upper bits
+  return __uint_as_float((hi << 16) + (uint32_t)((int32_t)(lo << 24) >> 16));
+}
+
 }  // namespace
 
 }  // namespace cpattn

@@ -31,17 +31,50 @@ __device__ __forceinline__ void store4(void* p, int64_t i, float4 v) {
         make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
+// Four elements, from column c of row m on, of a kept projection.
+template <typename T>
+__device__ __forceinline__ void keep4(void* p, int64_t m, int c, int64_t M, int N, float4 v) {
+  if constexpr (sizeof(T) == 4) {
+    store4<float>(p, m * N + c, v);
+  } else {
+    uint32_t hi[4], lo[4];
+    split24(v.x, hi[0], lo[0]);
+    split24(v.y, hi[1], lo[1]);
+    split24(v.z, hi[2], lo[2]);
+    split24(v.w, hi[3], lo[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + m * N + c) =
+        make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + kept_low(M, N) + m * kept_pitch(N) +
+                                 c) = lo[0] | lo[1] << 8 | lo[2] << 16 | lo[3] << 24;
+  }
+}
+template <typename T>
+__device__ __forceinline__ float4 kept4(const void* p, int64_t m, int c, int64_t M, int N) {
+  if constexpr (sizeof(T) == 4) {
+    return load4<float>(p, m * N + c);
+  } else {
+    const uint2 h =
+        *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + m * N + c);
+    const uint32_t l = *reinterpret_cast<const uint32_t*>(
+        static_cast<const uint8_t*>(p) + kept_low(M, N) + m * kept_pitch(N) + c);
+    return make_float4(join24(h.x & 0xffffu, l), join24(h.x >> 16, l >> 8),
+                       join24(h.y & 0xffffu, l >> 16), join24(h.y >> 16, l >> 24));
+  }
+}
+
 // Bound by memory: reads every share once.  Shares are added in order, so the sums do
 // not depend on timing.
 template <typename T, int kEpi>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs j) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= j.n) return;   // n is a multiple of 4
+  const int64_t n = j.M * j.N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;   // N is a multiple of 8
+  const int64_t row = i / j.N;
+  const int col = (int)(i - row * j.N);
   auto sum = [&](const float* p) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = 0; s < j.splits; ++s) {
-      const float4 w = *reinterpret_cast<const float4*>(p + s * j.n + i);
+      const float4 w = *reinterpret_cast<const float4*>(p + s * n + i);
       v.x += w.x;
       v.y += w.y;
       v.z += w.z;
@@ -53,10 +86,10 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
   if constexpr (kEpi == GEMM_STORE) {
     store4<T>(j.out, i, x);
   } else if constexpr (kEpi == GEMM_GLU) {
-    const float4 u = sum(j.partial + j.splits * j.n);
+    const float4 u = sum(j.partial + j.splits * n);
     if (j.gate != nullptr) {
-      store4<T>(j.gate, i, x);
-      store4<T>(j.up, i, u);
+      keep4<T>(j.gate, row, col, j.M, j.N, x);
+      keep4<T>(j.up, row, col, j.M, j.N, u);
     }
     float d;
     x.x = activation<false>(x.x, j.act, d) * u.x;
@@ -65,7 +98,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     x.w = activation<false>(x.w, j.act, d) * u.w;
     store4<T>(j.out, i, x);
   } else {
-    const float4 g = load4<T>(j.gate, i), u = load4<T>(j.up, i);
+    const float4 g = kept4<T>(j.gate, row, col, j.M, j.N);
+    const float4 u = kept4<T>(j.up, row, col, j.M, j.N);
     const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
     const float dh[4] = {x.x, x.y, x.z, x.w};
     float h[4], dg[4], du[4];
@@ -177,7 +211,7 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(const __grid_constant__ G
 
 template <typename T>
 cudaError_t join_t(const JoinArgs& j, int epilogue, cudaStream_t st) {
-  const int64_t blocks = (j.n / 4 + 255) / 256;
+  const int64_t blocks = (j.M * j.N / 4 + 255) / 256;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (epilogue == GEMM_STORE) join_kernel<T, GEMM_STORE><<<(unsigned)blocks, 256, 0, st>>>(j);
   else if (epilogue == GEMM_GLU) join_kernel<T, GEMM_GLU><<<(unsigned)blocks, 256, 0, st>>>(j);

@@ -3,16 +3,22 @@
 //
 //   C[m][n] = sum_k A(m, k) B(n, k),  bf16 operands, fp32 sums in tensor memory
 //
-// A tile is 128 x 256 (gate and up: 128 x 128 of each, so that both halves of a pair
-// meet in one epilogue), k goes by 64.  Operands come by TMA in the 128-byte swizzle,
-// K-major or MN-major as they lie in memory: no product needs a transposed copy.  The
-// kernel is persistent: CTAs walk (tile, share of k) units, and the two accumulators
-// in tensor memory let a tile's epilogue run under the next one's products.
+// A pair of CTAs shares a tile of 256 x 256 (gate and up: 256 x 128 of each, so that
+// both halves of a pair of columns meet in one epilogue), k goes by 64: each CTA
+// loads 128 rows of A and of B, and the pair's MMAs read both.  Operands come by TMA
+// in the 128-byte swizzle, K-major or MN-major as they lie in memory: no product needs
+// a transposed copy.  The kernel is persistent: pairs walk (tile, share of k) units,
+// and two accumulators in tensor memory let a tile's epilogue run under the next one's
+// products.
 //
 // Warp roles (384 threads):
-//   warp 0       TMA producer (one lane)
-//   warp 1       TMEM allocation; lane 0 issues every tcgen05.mma
+//   warp 0       TMA producer (one lane): this CTA's rows of A and B
+//   warp 1       TMEM allocation; in the first CTA lane 0 issues every MMA
 //   warps 4..11  epilogue: TMEM lane quarter w % 4, column half (w - 4) / 4
+//
+// The epilogue moves boxes of 32 x 32 through shared memory by TMA, a warp its own:
+// a thread holds one row, and rows read and written straight from it (16 bytes in
+// each of 32 lines) took longer than the products.
 //
 // Rows and columns past the matrices' ends are zeros by TMA's fill and are not
 // stored.
@@ -30,21 +36,38 @@ namespace {
 using namespace ptx;
 
 constexpr int kThreads = 384;
-constexpr int kStages = 4;
 constexpr int kEpiWarps = 8;
-constexpr int kTileA = kGemmM * kGemmK * 2, kTileB = kGemmN * kGemmK * 2;   // bytes
-constexpr int kStage = kTileA + kTileB;
-constexpr int kSmem = kStages * kStage + 256 + 1024;   // barriers; slack for alignment
+constexpr int kRows = kGemmM / 2;                   // of A and B in one CTA
+constexpr int kTile = kRows * kGemmK * 2;           // bytes of one operand's part of a stage
+constexpr int kBf16Box = 32 * 32 * 2, kByteBox = 32 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kDrainLimit = 1LL << 24;
 // m tiles whose n tiles are walked together: about square patches of tiles run at a
 // time, which reads the least of A and B
-constexpr int kGroupM = 16;
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+constexpr int kGroupM = 8;
+
+// Stages, and a warp's boxes: two bf16 or one fp32; h, gate, up and the low bytes;
+// gate, up, low bytes in, dgate, dup, h out.
+template <int kEpi>
+struct Layout {
+  static constexpr int kStages = kEpi == GEMM_STORE ? 6 : kEpi == GEMM_GLU ? 5 : 4;
+  static constexpr int kWarpBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
+                                    : kEpi == GEMM_GLU ? 3 * kBf16Box + 2 * kByteBox
+                                                       : 5 * kBf16Box + 2 * kByteBox;
+  static constexpr int kBoxes = kStages * 2 * kTile;
+  static constexpr int kBars = kBoxes + kEpiWarps * kWarpBytes;
+  static constexpr int kSmem = kBars + 256 + 1024;   // slack for alignment
+};
+static_assert(Layout<GEMM_STORE>::kSmem <= 227 * 1024, "shared memory budget");
+static_assert(Layout<GEMM_GLU>::kSmem <= 227 * 1024, "shared memory budget");
+static_assert(Layout<GEMM_DGLU>::kSmem <= 227 * 1024, "shared memory budget");
 
 struct Bars {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
+  uint64_t full[6];        // first CTA: both CTAs' loads of a stage have landed
+  uint64_t empty[6];       // both: the stage's MMAs are done
+  uint64_t acc_full[2];    // both: a tile's products are done
+  uint64_t acc_empty[2];   // first CTA: both CTAs' epilogues have read them
+  uint64_t box[kEpiWarps];   // GEMM_DGLU: a warp's boxes have landed
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -73,31 +96,11 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-}
-
-// 32 columns of one row, from column n on (N is a multiple of 8).
-__device__ __forceinline__ void store_bf16(void* out, int64_t at, int n, int N, const float* f) {
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(out) + at;
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    if (n + i < N) *reinterpret_cast<uint4*>(p + i) = pack8(f + i);
-}
-__device__ __forceinline__ void store_f32(float* out, int64_t at, int n, int N, const float* f) {
+__device__ __forceinline__ void store_f32(float* out, int n, int N, const float (&f)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4)
-    if (n + i < N)
-      *reinterpret_cast<float4*>(out + at + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    if (n + i < N)   // N is a multiple of 8
+      *reinterpret_cast<float4*>(out + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
 }
 
 __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
@@ -109,37 +112,59 @@ __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
 }
 
-// dgate, dup and h of 32 columns of one row, from dh and the kept gate and up.
-__device__ __forceinline__ void hidden_gradients(const GemmArgs& g, int64_t at, int n,
-                                                 const float* dh) {
-  const __nv_bfloat16* pg = static_cast<const __nv_bfloat16*>(g.gate) + at;
-  const __nv_bfloat16* pu = static_cast<const __nv_bfloat16*>(g.up) + at;
+// 16-byte piece p of a lane's row in a 32 x 32 box of 32-, 64- or 128-byte rows, as
+// TMA's swizzle of that size places it; the eight lanes of a pass meet no bank twice.
+template <int kRowBytes>
+__device__ __forceinline__ uint4* piece(uint8_t* box, int lane, int p) {
+  constexpr int kSwap = kRowBytes / 16 - 1;
+  return reinterpret_cast<uint4*>(box + lane * kRowBytes +
+                                  ((p ^ (lane * kRowBytes / 128 & kSwap)) << 4));
+}
+
+__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, const float (&f)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    if (n + i >= g.N) continue;
-    float gate[8], up[8], h[8];
-    unpack8(*reinterpret_cast<const uint4*>(pg + i), gate);
-    unpack8(*reinterpret_cast<const uint4*>(pu + i), up);
+  for (int p = 0; p < 4; ++p)
+    *piece<64>(box, lane, p) =
+        make_uint4(pack_bf16x2(f[8 * p], f[8 * p + 1]), pack_bf16x2(f[8 * p + 2], f[8 * p + 3]),
+                   pack_bf16x2(f[8 * p + 4], f[8 * p + 5]), pack_bf16x2(f[8 * p + 6], f[8 * p + 7]));
+}
+__device__ __forceinline__ void put_f32(uint8_t* box, int lane, const float (&f)[32]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float da;
-      const float a = activation<true>(gate[e], g.act, da), d = dh[i + e];
-      h[e] = a * up[e];
-      gate[e] = d * up[e] * da;
-      up[e] = d * a;
+  for (int p = 0; p < 8; ++p)
+    *piece<128>(box, lane, p) =
+        make_uint4(__float_as_uint(f[4 * p]), __float_as_uint(f[4 * p + 1]),
+                   __float_as_uint(f[4 * p + 2]), __float_as_uint(f[4 * p + 3]));
+}
+__device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, const float (&f)[32]) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint32_t h[8], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split24(f[16 * p + 4 * i + e], a[e], b[e]);
+      h[2 * i] = a[0] | a[1] << 16;
+      h[2 * i + 1] = a[2] | a[3] << 16;
+      l[i] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
     }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.dgate) + at + i) = pack8(gate);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.dup) + at + i) = pack8(up);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.out[0]) + at + i) = pack8(h);
+    *piece<64>(hi, lane, 2 * p) = make_uint4(h[0], h[1], h[2], h[3]);
+    *piece<64>(hi, lane, 2 * p + 1) = make_uint4(h[4], h[5], h[6], h[7]);
+    *piece<32>(lo, lane, p) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
 template <bool kAMN, bool kBMN, int kEpi>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Bars* bars = reinterpret_cast<Bars*>(smem + kStages * kStage);
+  using L = Layout<kEpi>;
+  constexpr int kStages = L::kStages;
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int units = g.m_tiles * g.n_tiles * g.splits;
   volatile int* abort = &bars->abort;
   const long long lim = g.wait_limit;
@@ -151,18 +176,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->acc_full[s], 1);
-      mbar_init(&bars->acc_empty[s], kEpiWarps);
+      mbar_init(&bars->acc_empty[s], 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&bars->box[w], 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&bars->tmem_base, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // the other CTA's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
@@ -170,75 +197,73 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       int j = 0;   // k tiles so far, across units
-      for (int u = blockIdx.x; u < units && !*abort; u += gridDim.x) {
+      for (int u = pair; u < units && !*abort; u += pairs) {
         const Unit t = unit_at(g, u);
         const bool second = t.m >= g.m_split;
-        const int m0 = (t.m - (second ? g.m_split : 0)) * kGemmM;
-        const int n0 = t.n * (kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN);
-        if (!CP_IN_RANGE(m0, 0, g.M, g.status, 301) || !CP_IN_RANGE(n0, 0, g.N, g.status, 302)) {
+        const int m0 = (t.m - (second ? g.m_split : 0)) * kGemmM + rank * kRows;
+        const int n0 = kEpi == GEMM_GLU ? t.n * kRows : t.n * kGemmN + rank * kRows;
+        if (!CP_IN_RANGE(m0, 0, g.M + kRows, g.status, 301) ||
+            !CP_IN_RANGE(n0, 0, g.N + kRows, g.status, 302)) {
           *abort = 1;
           break;
         }
         for (int k = t.k0; k < t.k1; ++k, ++j) {
           const int st = j % kStages;
-          if (j >= kStages && !mbar_wait(&bars->empty[st], ((j / kStages) - 1) & 1, lim, abort)) {
+          if (j >= kStages &&
+              !mbar_wait_cluster(&bars->empty[st], ((j / kStages) - 1) & 1, lim, abort)) {
             record_timeout(g.status, abort, 31);
             break;
           }
           const int src = k >= g.k_split;
           const int kk = (k - (src ? g.k_split : 0)) * kGemmK;
           const CUtensorMap* ma = &g.a[second || src];
-          const CUtensorMap* mb = &g.b[src];
-          uint8_t* pa = smem + st * kStage;
-          uint8_t* pb = pa + kTileA;
-          uint64_t* full = &bars->full[st];
-          mbar_expect_tx(full, kStage);
+          const CUtensorMap* mb = &g.b[kEpi == GEMM_GLU ? rank : src];   // gate or up
+          uint8_t* pa = smem + st * 2 * kTile;
+          uint8_t* pb = pa + kTile;
+          if (rank == 0) mbar_expect_tx(&bars->full[st], 4 * kTile);   // both CTAs' parts
+          const uint32_t full = in_first_cta(&bars->full[st]);
           if constexpr (kAMN) {
-            for (int i = 0; i < kGemmM / 64; ++i)
-              tma_load_2d(ma, full, pa + i * 64 * kGemmK * 2, m0 + i * 64, kk);
+            for (int i = 0; i < kRows / 64; ++i)
+              tma_load_2d_pair(ma, full, pa + i * 64 * kGemmK * 2, m0 + i * 64, kk);
           } else {
-            tma_load_2d(ma, full, pa, kk, m0);
+            tma_load_2d_pair(ma, full, pa, kk, m0);
           }
-          if constexpr (kEpi == GEMM_GLU) {   // 128 rows of each weight
-            tma_load_2d(&g.b[0], full, pb, kk, n0);
-            tma_load_2d(&g.b[1], full, pb + kTileB / 2, kk, n0);
-          } else if constexpr (kBMN) {
-            for (int i = 0; i < kGemmN / 64; ++i)
-              tma_load_2d(mb, full, pb + i * 64 * kGemmK * 2, n0 + i * 64, kk);
+          if constexpr (kBMN) {
+            for (int i = 0; i < kRows / 64; ++i)
+              tma_load_2d_pair(mb, full, pb + i * 64 * kGemmK * 2, n0 + i * 64, kk);
           } else {
-            tma_load_2d(mb, full, pb, kk, n0);
-            tma_load_2d(mb, full, pb + kTileB / 2, kk, n0 + kGemmN / 2);
+            tma_load_2d_pair(mb, full, pb, kk, n0);
           }
         }
       }
-      // every load must land before the CTA exits (normally they have: the MMA
-      // issuer waited for them)
+      // every load must have been read before the CTA exits
       int zero = 0;
       for (int x = j - kStages; x < j; ++x)
-        if (x >= 0) mbar_wait(&bars->full[x % kStages], (x / kStages) & 1, kDrainLimit, &zero);
+        if (x >= 0)
+          mbar_wait_cluster(&bars->empty[x % kStages], (x / kStages) & 1, kDrainLimit, &zero);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_bf16(kGemmM, kGemmN, kAMN, kBMN);
       bool ok = true;
       int j = 0, n = 0;   // k tiles and units so far
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++n) {
+      for (int u = pair; ok && u < units; u += pairs, ++n) {
         const Unit t = unit_at(g, u);
         const int s = n & 1;
-        if (n >= 2 && !mbar_wait(&bars->acc_empty[s], ((n >> 1) - 1) & 1, lim, abort)) {
+        if (n >= 2 && !mbar_wait_cluster(&bars->acc_empty[s], ((n >> 1) - 1) & 1, lim, abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
         for (int k = t.k0; k < t.k1; ++k, ++j) {
           const int st = j % kStages;
-          if (!mbar_wait(&bars->full[st], (j / kStages) & 1, lim, abort)) {
+          if (!mbar_wait_cluster(&bars->full[st], (j / kStages) & 1, lim, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t pa = smem_u32(smem + st * kStage), pb = pa + kTileA;
+          const uint32_t pa = smem_u32(smem + st * 2 * kTile), pb = pa + kTile;
 #pragma unroll
           for (int i = 0; i < kGemmK / 16; ++i) {
             // 16 k further: 32 bytes along a K-major row, 16 rows of an MN-major box
@@ -246,100 +271,225 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                                      : sdesc_sw128(pa + i * 32, 16, 1024);
             const uint64_t db = kBMN ? sdesc_sw128(pb + i * 2048, 64 * kGemmK * 2, 1024)
                                      : sdesc_sw128(pb + i * 32, 16, 1024);
-            mma_bf16(tmem + s * kGemmN, da, db, idesc, (k > t.k0 || i > 0) ? 1u : 0u);
+            mma_bf16_pair(tmem + s * kGemmN, da, db, idesc, (k > t.k0 || i > 0) ? 1u : 0u);
           }
-          mma_commit(&bars->empty[st]);
+          mma_commit_pair(&bars->empty[st]);
         }
         if (!ok) break;
-        mma_commit(&bars->acc_full[s]);
+        mma_commit_pair(&bars->acc_full[s]);
       }
       if (!ok) {
         record_timeout(g.status, abort, 32);
         // nothing issued by this thread may still be running at exit
-        mma_commit(&bars->drain);
+        mma_commit_pair(&bars->drain);
         int zero = 0;
-        mbar_wait(&bars->drain, 0, kDrainLimit, &zero);
+        mbar_wait_cluster(&bars->drain, 0, kDrainLimit, &zero);
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    int n = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+    const int quarter = warp & 3, half = (warp - 4) >> 2, w = warp - 4;
+    uint8_t* boxes = smem + L::kBoxes + w * L::kWarpBytes;
+    // columns of a warp: 128 of one product, or 64 of gate and of up
+    constexpr int kChunks = kEpi == GEMM_GLU ? 2 : 4;
+    constexpr int kTileN = kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN;
+    auto first_row = [&](const Unit& t) {
+      return (t.m - (t.m >= g.m_split ? g.m_split : 0)) * kGemmM + rank * kRows + quarter * 32;
+    };
+    auto first_col = [&](const Unit& t, int c) {
+      return t.n * kTileN + half * (kTileN / 2) + c * kGemmBox;
+    };
+    // GEMM_DGLU: the kept gate and up of a chunk, on their way while the one before
+    // is worked on
+    auto fetch = [&](const Unit& t, int c) {
+      if (lane != 0) return;
+      const int row = first_row(t), col = first_col(t, c);
+      mbar_expect_tx(&bars->box[w], 2 * (kBf16Box + kByteBox));
+      tma_load_2d(&g.gate[0], &bars->box[w], boxes, col, row);
+      tma_load_2d(&g.up[0], &bars->box[w], boxes + kBf16Box, col, row);
+      tma_load_2d(&g.gate[1], &bars->box[w], boxes + 2 * kBf16Box, col, row);
+      tma_load_2d(&g.up[1], &bars->box[w], boxes + 2 * kBf16Box + kByteBox, col, row);
+    };
+    const bool fetches = kEpi == GEMM_DGLU && g.splits == 1;
+    int n = 0, fetched = 0, got = 0;
+    if (fetches && pair < units) {
+      fetch(unit_at(g, pair), 0);
+      ++fetched;
+    }
+    bool ok = true;
+    for (int u = pair; ok && u < units; u += pairs, ++n) {
       const Unit t = unit_at(g, u);
       const int s = n & 1;
-      if (!mbar_wait(&bars->acc_full[s], (n >> 1) & 1, lim, abort)) {
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_cluster(&bars->acc_full[s], (n >> 1) & 1, lim, abort))) {
         if (lane == 0) record_timeout(g.status, abort, 33);
         break;
       }
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kGemmN;
-      const bool second = t.m >= g.m_split;
-      const int row = (t.m - (second ? g.m_split : 0)) * kGemmM + quarter * 32 + lane;
-      const bool in = row < g.M;
-      const int64_t at = (int64_t)row * g.N;
-      if constexpr (kEpi == GEMM_GLU) {
-        const int64_t share = (int64_t)g.M * g.N;
+      const int second = t.m >= g.m_split;
+      const int row0 = first_row(t), row = row0 + lane;
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int col = half * 64 + c * 32, nc = t.n * (kGemmN / 2) + col;
-          float x[32], v[32];
-          load_acc(acc + col, x);
-          load_acc(acc + kGemmN / 2 + col, v);
-          if (in && g.splits > 1) {
-            store_f32(g.partial + t.split * share, at + nc, nc, g.N, x);
-            store_f32(g.partial + (g.splits + t.split) * share, at + nc, nc, g.N, v);
-          } else if (in) {
-            if (g.gate != nullptr) {
-              store_bf16(g.gate, at + nc, nc, g.N, x);
-              store_bf16(g.up, at + nc, nc, g.N, v);
+      for (int c = 0; c < kChunks; ++c) {
+        const int col = half * (kTileN / 2) + c * kGemmBox, nc = first_col(t, c);
+        const bool stores = row0 < g.M && nc < g.N;   // the box is not wholly past the end
+        const int64_t at = (int64_t)row * g.N + nc;
+        float x[32];
+        load_acc(acc + col, x);
+        if constexpr (kEpi == GEMM_GLU) {
+          float v[32];
+          load_acc(acc + kTileN + col, v);
+          if (g.splits > 1) {
+            const int64_t share = (int64_t)g.M * g.N;
+            if (row < g.M) {
+              store_f32(g.partial + t.split * share + at, nc, g.N, x);
+              store_f32(g.partial + (g.splits + t.split) * share + at, nc, g.N, v);
             }
-            float unused;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = activation<false>(x[i], g.act, unused) * v[i];
-            store_bf16(g.out[0], at + nc, nc, g.N, x);
+            __syncwarp();   // the next load of the accumulator is the whole warp's
+            continue;
           }
-          __syncwarp();   // the next load of the accumulator is the whole warp's
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col = half * 128 + c * 32, nc = t.n * kGemmN + col;
-          float x[32];
-          load_acc(acc + col, x);
-          if (in && g.splits > 1) {
-            store_f32(g.partial + (int64_t)(t.split + (second ? g.splits : 0)) * g.M * g.N, at + nc,
-                      nc, g.N, x);
-          } else if (in && kEpi == GEMM_STORE) {
-            if (g.out_f32) store_f32(static_cast<float*>(g.out[second]), at + nc, nc, g.N, x);
-            else store_bf16(g.out[second], at + nc, nc, g.N, x);
-          } else if (in) {
-            hidden_gradients(g, at + nc, nc, x);
-          }
+          if (lane == 0) bulk_wait_read<0>();   // the boxes' last stores have read them
           __syncwarp();
+          if (g.keep) {
+            put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, x);
+            put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, v);
+          }
+          float unused;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = activation<false>(x[i], g.act, unused) * v[i];
+          put_bf16(boxes, lane, x);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && stores) {
+            tma_store_2d(&g.out[0], boxes, nc, row0);
+            if (g.keep) {
+              tma_store_2d(&g.gate[0], boxes + kBf16Box, nc, row0);
+              tma_store_2d(&g.up[0], boxes + 2 * kBf16Box, nc, row0);
+              tma_store_2d(&g.gate[1], boxes + 3 * kBf16Box, nc, row0);
+              tma_store_2d(&g.up[1], boxes + 3 * kBf16Box + kByteBox, nc, row0);
+            }
+            bulk_commit();
+          }
+        } else {
+          if (g.splits > 1) {
+            if (row < g.M)
+              store_f32(g.partial + (int64_t)(t.split + second * g.splits) * g.M * g.N + at, nc,
+                        g.N, x);
+            __syncwarp();
+            continue;
+          }
+          if constexpr (kEpi == GEMM_STORE) {
+            uint8_t* box = boxes + (g.out_f32 ? 0 : (c & 1) * kBf16Box);
+            if (lane == 0) {
+              if (g.out_f32) bulk_wait_read<0>();
+              else bulk_wait_read<1>();
+            }
+            __syncwarp();
+            if (g.out_f32) put_f32(box, lane, x);
+            else put_bf16(box, lane, x);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (stores) tma_store_2d(&g.out[second], box, nc, row0);
+              bulk_commit();   // one group a chunk, so that the count holds
+            }
+          } else {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->box[w], got & 1, lim, abort))) {
+              if (lane == 0) record_timeout(g.status, abort, 34);
+              ok = false;
+              break;
+            }
+            ++got;
+            uint4 kg[4], ku[4], lg[2], lu[2];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              kg[p] = *piece<64>(boxes, lane, p);
+              ku[p] = *piece<64>(boxes + kBf16Box, lane, p);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              lg[p] = *piece<32>(boxes + 2 * kBf16Box, lane, p);
+              lu[p] = *piece<32>(boxes + 2 * kBf16Box + kByteBox, lane, p);
+            }
+            __syncwarp();   // all have read: the next chunk may land
+            if (c + 1 < kChunks) {
+              fetch(t, c + 1);
+              ++fetched;
+            } else if (u + pairs < units) {
+              fetch(unit_at(g, u + pairs), 0);
+              ++fetched;
+            }
+            uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            const uint32_t* wg = reinterpret_cast<const uint32_t*>(kg);
+            const uint32_t* wu = reinterpret_cast<const uint32_t*>(ku);
+            const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
+            const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {   // eight columns at a time
+              float dg[8], du[8], h[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int i = 8 * p + e;
+                const float gate = join24(wg[i / 2] >> (i % 2 * 16) & 0xffffu, bg[i / 4] >> (i % 4 * 8));
+                const float up = join24(wu[i / 2] >> (i % 2 * 16) & 0xffffu, bu[i / 4] >> (i % 4 * 8));
+                float da;
+                const float a = activation<true>(gate, g.act, da);
+                h[e] = a * up;
+                dg[e] = x[i] * up * da;
+                du[e] = x[i] * a;
+              }
+              auto put = [&](int which, const float (&f)[8]) {
+                *piece<64>(out + which * kBf16Box, lane, p) =
+                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+              };
+              put(0, dg);
+              put(1, du);
+              put(2, h);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && stores) {
+              tma_store_2d(&g.dgate, out, nc, row0);
+              tma_store_2d(&g.dup, out + kBf16Box, nc, row0);
+              tma_store_2d(&g.out[0], out + 2 * kBf16Box, nc, row0);
+              bulk_commit();
+            }
+          }
         }
       }
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->acc_empty[s]);
+      if (lane == 0) mbar_arrive_cluster(in_first_cta(&bars->acc_empty[s]));
+    }
+    if (lane == 0) {
+      int zero = 0;   // a load that nobody waited for (after a wait gave up)
+      for (; got < fetched; ++got) mbar_wait(&bars->box[w], got & 1, kDrainLimit, &zero);
+      bulk_wait_all();
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // the other CTA's MMAs and arrivals no longer need this one
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
 template <bool kAMN, bool kBMN, int kEpi>
 cudaError_t launch_t(const GemmArgs& g, int sms, cudaStream_t st) {
   auto kernel = gemm_kernel<kAMN, kBMN, kEpi>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  constexpr int smem = Layout<kEpi>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)g.m_tiles * g.n_tiles * g.splits;
   if (units < 1 || units > 0x3fffffff) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, st>>>(g);
+  const int64_t pairs = units < sms / 2 ? units : sms / 2;
+  kernel<<<(unsigned)(2 * pairs), kThreads, smem, st>>>(g);
   return cudaGetLastError();
 }
 

@@ -97,22 +97,29 @@ bool make_tmap_ld(CUtensorMap* map, const void* base, int64_t pitch, int H, int 
   return true;
 }
 
-// dims (innermost first): {cols, rows}; box {64, box_rows}: 128-byte rows in the 128-byte
-// swizzle.
+// dims (innermost first): {cols, rows}; box {box_cols, box_rows}, whose rows are laid out
+// in the swizzle of their size (32, 64 or 128 bytes).
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
-                      int64_t stride, int box_rows, const char** err) {
+                      int64_t stride, int elem, int box_cols, int box_rows, const char** err) {
   auto fn = encode_fn();
   if (!fn) {
     *err = "cuTensorMapEncodeTiled unavailable";
     return false;
   }
+  const CUtensorMapDataType type = elem == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const int row = box_cols * elem;
+  const CUtensorMapSwizzle swizzle = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)stride * elem};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     *err = "cuTensorMapEncodeTiled failed (matrix)";
     return false;

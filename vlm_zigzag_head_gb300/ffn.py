@@ -33,7 +33,7 @@ def _aligned(x: torch.Tensor) -> torch.Tensor:
 @functools.lru_cache(maxsize=256)
 def _desc(dtype, grad_dtype, activation, T, D, F, D_out, x_stride, wg_stride, wu_stride,
           wd_stride, dy_stride):
-    """The descriptor, and the workspaces of forward and backward by device."""
+    """The descriptor, and its workspace and kept sizes as they get known."""
     if T > 0x7fffffff:
         raise CpError(2, "at most 2^31 - 1 rows")
     f = _b.GatedFfnDesc()
@@ -42,6 +42,12 @@ def _desc(dtype, grad_dtype, activation, T, D, F, D_out, x_stride, wg_stride, wu
     f.x_stride, f.dy_stride = (x_stride, dy_stride) if T > 1 else (D, D_out)
     f.w_gate_stride, f.w_up_stride, f.w_down_stride = wg_stride, wu_stride, wd_stride
     return f, {}
+
+
+def _kept_bytes(f, sizes):
+    if "kept" not in sizes:
+        sizes["kept"] = _b.lib().cp_gated_ffn_kept_size(f)
+    return sizes["kept"]
 
 
 def _workspace_bytes(f, sizes, device, backward):
@@ -87,15 +93,17 @@ def cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", *, keep:
     (bf16: tensor cores; fp32: CUDA cores), with ``w_gate``/``w_up [F, D]``, ``w_down [D_out,
     F]`` and ``a`` one of ``"silu"``, ``"gelu"``, ``"gelu_tanh"``.  D, F, D_out: multiples of
     8; rows of any stride that lie on 16-byte boundaries.  With ``keep`` returns ``(y, gate,
-    up)``, the two projections ``[..., F]`` for :func:`cp_gated_ffn_bwd`.  Without
-    ``workspace`` each call takes one of its own, so calls on several streams may overlap."""
+    up)``, the two projections for :func:`cp_gated_ffn_bwd` as byte tensors in the library's
+    layout (bf16: to 24 bits).  Without ``workspace`` each call takes one of its own, so calls
+    on several streams may overlap."""
     rows = _rows(x, "x")
     f, sizes = _prepare(rows, w_gate, w_up, w_down, activation, _dt(rows))
     device, lead = x.device, x.shape[:-1]
     y = torch.empty((*lead, f.D_out), dtype=x.dtype, device=device)
     gate = up = None
     if keep:
-        gate, up = (torch.empty((*lead, f.F), dtype=x.dtype, device=device) for _ in range(2))
+        gate, up = (torch.empty(_kept_bytes(f, sizes), dtype=torch.uint8, device=device)
+                    for _ in range(2))
     with _on_device(device):
         ws, ptr, size = _space(workspace, _workspace_bytes(f, sizes, device, False), device)
         _b.check(_b.lib().cp_gated_ffn_fwd(
@@ -115,7 +123,7 @@ def cp_gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, dy, activation: str = "s
                         _dt(torch.empty(0, dtype=grad_dtype)), g)
     device = x.device
     for t, name in ((gate, "gate"), (up, "up")):
-        _like(t, (*x.shape[:-1], f.F), x.dtype, device, name)
+        _like(t, (_kept_bytes(f, sizes),), torch.uint8, device, name)
         if not t.is_contiguous():
             raise CpError(1, "%s must be contiguous" % name)
     like = ((x, x.dtype), (w_gate, grad_dtype), (w_up, grad_dtype), (w_down, grad_dtype))
