@@ -83,7 +83,7 @@ CASES = [(1, 64, 128, 64, "bf16", "silu"), (128, 64, 128, 256, "bf16", "silu"), 
          (257, 520, 1032, 264, "bf16", "silu"), (37, 1024, 2816, 1024, "bf16", "gelu_tanh"),
          (3, 2048, 512, 1000, "bf16", "silu"), (16, 264, 4104, 264, "bf16", "gelu"),
          (1000, 512, 1360, 512, "bf16", "silu"), (3000, 64, 2048, 64, "bf16", "silu"),
-         (2500, 1536, 768, 1280, "bf16", "gelu_tanh"),
+         (2500, 1536, 768, 1280, "bf16", "gelu_tanh"), (5000, 1024, 1280, 1024, "bf16", "silu"),
          (1, 32, 64, 32, "f32", "silu"), (5, 8, 16, 24, "f32", "gelu"), (129, 136, 264, 72, "f32", "gelu_tanh"),
          (300, 256, 512, 256, "f32", "silu"), (17, 512, 1360, 512, "f32", "gelu"),
          (1030, 96, 200, 104, "f32", "silu")]
@@ -105,3 +105,165 @@ def test_matches_oracle(T, D, F, D_out, dtype, act):
         _check((y, *grads), x, wg, wu, wd, dy, act, dt, grad_dtype)
         again = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, grad_dtype=grad_dtype)
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def _call(seed=1, T=70, D=72, F=136, D_out=40, dtype=torch.bfloat16):
+    import vlm_zigzag_head_gb300 as cp
+    x, wg, wu, wd, dy = _inputs(T, D, F, D_out, dtype, seed)
+    y, gate, up = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+    return cp, x, wg, wu, wd, dy, y, gate, up
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,F", [(70, 72, 136), (700, 2048, 2304)])   # the second: shared last tiles
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_parts_that_are_wanted(T, D, F, dtype):
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(2, T, D, F, 104, dtype)
+    ws = cp.Workspace()
+    full = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, grad_dtype=dtype)
+    for bits in range(16):
+        wanted = [bool(bits >> i & 1) for i in range(4)]
+        got = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, grad_dtype=dtype, wanted=wanted, workspace=ws)
+        for have, want, on in zip(got, full, wanted):
+            assert (have is None) == (not on)
+            # one weight alone shares its k otherwise than both: other roundings of the sums
+            assert not on or rel_l2(have, want) <= 2 * (F32_REL if dtype == torch.float32 else 2.0 ** -8)
+    if ws.buf is not None:
+        assert cp.cp_workspace_status(ws) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_strided_rows_halves_of_one_weight_and_no_rows(dtype):
+    """Rows out of wider ones and one [2 F][D] weight give the bits of contiguous copies; nothing beside
+    the outputs is written."""
+    import vlm_zigzag_head_gb300 as cp
+    T, D, F, Do = 150, 72, 136, 40
+    x, wg, wu, wd, dy = _inputs(T, D, F, Do, dtype, 3)
+    both = torch.cat([wg, wu])
+    xs = torch.full((T, D + 24), float("nan"), dtype=dtype, device=DEV)[:, 8:8 + D]
+    dys = torch.full((T, Do + 16), float("nan"), dtype=dtype, device=DEV)[:, 16:]
+    wds = torch.full((Do, F + 8), float("nan"), dtype=dtype, device=DEV)[:, :F]
+    for to, frm in ((xs, x), (dys, dy), (wds, wd)):
+        to.copy_(frm)
+    y, g, u = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+    grads = cp.cp_gated_ffn_bwd(x, wg, wu, wd, g, u, dy)
+    ys, gs, us = cp.cp_gated_ffn_fwd(xs, both[:F], both[F:], wds, keep=True)
+    assert torch.equal(y, ys)
+    for a, b in zip(grads, cp.cp_gated_ffn_bwd(xs, both[:F], both[F:], wds, gs, us, dys)):
+        assert torch.equal(a, b)
+    # leading dimensions, and none
+    y3, g3, u3 = cp.cp_gated_ffn_fwd(x.view(5, 30, D), wg, wu, wd, keep=True)
+    assert y3.shape == (5, 30, Do) and torch.equal(y3.view(T, Do), y)
+    dx3 = cp.cp_gated_ffn_bwd(x.view(5, 30, D), wg, wu, wd, g3, u3, dy.view(5, 30, Do))[0]
+    assert dx3.shape == (5, 30, D) and torch.equal(dx3.view(T, D), grads[0])
+    assert cp.cp_gated_ffn_fwd(x[7], wg, wu, wd).shape == (Do,)
+    y0, g0, u0 = cp.cp_gated_ffn_fwd(x[:0], wg, wu, wd, keep=True)
+    assert y0.shape == (0, Do)
+    zero = cp.cp_gated_ffn_bwd(x[:0], wg, wu, wd, g0, u0, dy[:0])
+    assert zero[0].shape == (0, D) and not any(z.any() for z in zero[1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,act", [(torch.bfloat16, "silu"), (torch.float32, "gelu"), (torch.float32, "gelu_tanh")])
+def test_autograd_against_formula_and_differences(dtype, act):
+    from vlm_zigzag_head_gb300.autograd import gated_ffn
+    T, D, F, Do = 60, 64, 128, 48
+    x, wg, wu, wd, dy = _inputs(T, D, F, Do, dtype, 4)
+    leaves = [t.clone().requires_grad_(True) for t in (x, wg, wu, wd)]
+    y = gated_ffn(*leaves, activation=act)
+    grads = torch.autograd.grad(y, leaves, dy)
+    _check((y, *grads), x, wg, wu, wd, dy, act, dtype, dtype)
+    # a central difference along a random direction of all inputs, in 64 bits by the oracle
+    rng, h = np.random.default_rng(0), 1e-5
+    args = [to64(t) for t in (x, wg, wu, wd)]
+    dirs = [rng.standard_normal(a.shape) * np.abs(a).mean() for a in args]
+    plus, minus = (O.gated_ffn(*(a + s * h * v for a, v in zip(args, dirs)), act) for s in (1, -1))
+    slope = ((plus - minus) / (2 * h) * to64(dy)).sum()
+    got = sum((to64(g) * v).sum() for g, v in zip(grads, dirs))
+    size = sum(np.linalg.norm(to64(g)) * np.linalg.norm(v) for g, v in zip(grads, dirs))
+    assert abs(got - slope) <= (BF16_REL if dtype == torch.bfloat16 else 2 * F32_REL) * size
+    # frozen weights, rows off the 16-byte grid, an expanded gradient
+    odd = torch.zeros((T, D + 1), dtype=dtype, device=DEV)[:, 1:]
+    odd.copy_(x)
+    odd.requires_grad_(True)
+    dx, = torch.autograd.grad(gated_ffn(odd, wg, wu, wd, activation=act), odd, dy[:1].expand(T, Do))
+    dx2, = torch.autograd.grad(gated_ffn(leaves[0], wg, wu, wd, activation=act), leaves[0],
+                               dy[:1].expand(T, Do).contiguous())
+    assert torch.equal(dx, dx2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,F", [(60, 64, 128), (1, 256, 512), (400, 1024, 768)])
+def test_streams_and_graphs(T, D, F):
+    """Calls on several streams at once, and captured ones replayed, give the same bits."""
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(5, T, D, F, 128)
+    grads = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy)
+    sides, got = [torch.cuda.Stream() for _ in range(3)], []
+    torch.cuda.synchronize()
+    for s in sides:
+        with torch.cuda.stream(s):
+            r = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+            got.append((r, cp.cp_gated_ffn_bwd(x, wg, wu, wd, r[1], r[2], dy)))
+    torch.cuda.synchronize()
+    for r, g in got:
+        assert torch.equal(r[0], y) and all(torch.equal(a, b) for a, b in zip(g, grads))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        yg, gg, ug = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+        out = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gg, ug, dy)
+    for _ in range(2):
+        for t in (yg, *out):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, y) and all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 7, 300])
+def test_nonfinite_rows_stay_rows(T):
+    """A NaN in one row of x reaches that row of y and dx alone, and every weight gradient."""
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(6, T)
+    clean = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy)
+    row = T // 2
+    bad = x.clone()
+    bad[row, 3] = float("nan")
+    yb, gb, ub = cp.cp_gated_ffn_fwd(bad, wg, wu, wd, keep=True)
+    db = cp.cp_gated_ffn_bwd(bad, wg, wu, wd, gb, ub, dy)
+    keep = torch.arange(T, device=DEV) != row
+    assert yb[row].isnan().all() and torch.equal(yb[keep], y[keep])
+    assert db[0][row].isnan().all() and torch.equal(db[0][keep], clean[0][keep])
+    assert all(d.isnan().any() for d in db[1:])
+
+
+@pytest.mark.gpu
+def test_large_and_tiny_values():
+    """Projections far from 1 keep their digits: 24 bits at any exponent."""
+    import vlm_zigzag_head_gb300 as cp
+    for size in (1e-18, 1e-6, 1e6, 1e12):
+        x, wg, wu, wd, dy = _inputs(40, 64, 128, 64, torch.bfloat16, 7)
+        wu = (wu.float() * size).to(torch.bfloat16)
+        y, g, u = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+        grads = cp.cp_gated_ffn_bwd(x, wg, wu, wd, g, u, dy)
+        _check((y, *grads), x, wg, wu, wd, dy, "silu", torch.bfloat16, torch.float32)
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_are_reported():
+    """A bounded wait cut to one polling round gives up; the status says so and the next call is exact."""
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(8, 600, 512, 1024, 512)
+    ws, seen = cp.Workspace(), []
+    cp.cp_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws)
+            try:
+                seen.append(cp.cp_workspace_status(ws))
+            except cp.CpError as e:
+                seen.append(e.status)
+    finally:
+        cp.cp_set_wait_limit(0)
+    assert all(s in (0, 7) for s in seen) and 7 in seen, seen
+    assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws), y)
+    assert cp.cp_workspace_status(ws) == 0

@@ -76,43 +76,51 @@ int share_k_f32(int64_t M, int64_t N, int64_t K, int sms) {
   return share_k((int64_t)tiles(M, 128) * tiles(N, 128), tiles(K, 4 * kF32K), 2 * sms);
 }
 
-// How each product is cut, and what of the workspace it takes.
+// How the bf16 products' last tiles and the fp32 products' k are shared, and what of
+// the workspace that takes.
+struct Share {
+  int whole, shares;
+};
 struct Plan {
   int sms = 0;
-  int gate_up = 1, down = 1;                 // forward
-  int dh = 1, d_down = 1, d_in = 1, dx = 1;  // backward
+  Share gate_up, down, dh, d_down, d_in, d_both, dx;   // d_both: d_in of both weights at once
   size_t fwd_partial = 0, bwd_partial = 0;   // bytes
 };
 
 Plan make_plan(const cp_gated_ffn_t* p, int sms) {
   Plan r;
   r.sms = sms;
+  if (sms < 2) return r;
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
   if (p->dtype == CP_BF16) {
-    const int64_t mt = tiles(T, kGemmM);
-    const int pairs = sms / 2;
-    r.gate_up = share_k(mt * tiles(F, kGemmN / 2), tiles(D, kGemmK), pairs);
-    r.down = share_k(mt * tiles(O, kGemmN), tiles(F, kGemmK), pairs);
-    r.dh = share_k(mt * tiles(F, kGemmN), tiles(O, kGemmK), pairs);
-    r.dx = share_k(mt * tiles(D, kGemmN), 2 * tiles(F, kGemmK), pairs);
-    r.d_down = share_k((int64_t)tiles(O, kGemmM) * tiles(F, kGemmN), tiles(T, kGemmK), pairs);
-    r.d_in = share_k((int64_t)2 * tiles(F, kGemmM) * tiles(D, kGemmN), tiles(T, kGemmK), pairs);
-  } else {
-    r.gate_up = share_k_f32(T, F, D, sms);
-    r.down = share_k_f32(T, O, F, sms);
-    r.dh = share_k_f32(T, F, O, sms);
-    r.dx = share_k_f32(T, D, F, sms);
-    r.d_down = share_k_f32(O, F, T, sms);
-    r.d_in = share_k_f32(F, D, T, sms);
+    auto share = [&](int64_t M, int64_t N, int tile_n, int k_tiles, int outputs, size_t* most) {
+      const int64_t n = (int64_t)outputs * tiles(M, kGemmM) * tiles(N, tile_n);
+      Share s;
+      share_tail(n, k_tiles, sms / 2, &s.whole, &s.shares);
+      *most = std::max(*most, s.shares > 1 ? partial_bytes(n, s.whole, s.shares) : 0);
+      return s;
+    };
+    r.gate_up = share(T, F, kGemmN / 2, tiles(D, kGemmK), 1, &r.fwd_partial);
+    r.down = share(T, O, kGemmN, tiles(F, kGemmK), 1, &r.fwd_partial);
+    r.dh = share(T, F, kGemmN, tiles(O, kGemmK), 1, &r.bwd_partial);
+    r.dx = share(T, D, kGemmN, 2 * tiles(F, kGemmK), 1, &r.bwd_partial);
+    r.d_down = share(O, F, kGemmN, tiles(T, kGemmK), 1, &r.bwd_partial);
+    r.d_in = share(F, D, kGemmN, tiles(T, kGemmK), 1, &r.bwd_partial);
+    r.d_both = share(F, D, kGemmN, tiles(T, kGemmK), 2, &r.bwd_partial);
+    return r;
   }
-  const bool f32 = p->dtype == CP_F32;
-  auto bytes = [](int shares, int64_t n) { return shares > 1 ? (size_t)shares * n * 4 : 0; };
-  // fp32: gate and up always go through the workspace, and so does dh
-  const size_t gu = f32 ? (size_t)r.gate_up * 2 * T * F * 4 : bytes(r.gate_up, 2 * T * F);
-  const size_t dh = f32 ? (size_t)r.dh * T * F * 4 : bytes(r.dh, T * F);
-  r.fwd_partial = std::max(gu, bytes(r.down, T * O));
-  r.bwd_partial = std::max(std::max(dh, bytes(r.dx, (f32 ? 2 : 1) * T * D)),
-                           std::max(bytes(r.d_down, O * F), bytes(r.d_in, 2 * F * D)));
+  // gate and up always go through the workspace, and so does dh
+  auto share = [&](int64_t M, int64_t N, int64_t K, int outputs, bool always, size_t* most) {
+    const Share s{0, share_k_f32(M, N, K, sms)};
+    if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
+    return s;
+  };
+  r.gate_up = share(T, F, D, 2, true, &r.fwd_partial);
+  r.down = share(T, O, F, 1, false, &r.fwd_partial);
+  r.dh = share(T, F, O, 1, true, &r.bwd_partial);
+  r.dx = share(T, D, F, 2, false, &r.bwd_partial);
+  r.d_down = share(O, F, T, 1, false, &r.bwd_partial);
+  r.d_in = share(F, D, T, 1, false, &r.bwd_partial);
   return r;
 }
 
@@ -145,30 +153,28 @@ struct Matrix {
 // A product under construction; failures stick.
 struct Product {
   GemmArgs g = {};
-  JoinArgs j = {};       // what its shares become
-  void* outputs[2] = {};
+  JoinArgs j = {};       // what becomes of its shared tiles
   int epilogue;
   bool a_mn, b_mn;
   const char* err = nullptr;
 
-  Product(int epi, bool amn, bool bmn, int M, int N, int splits, int32_t* status, void* partial)
+  Product(int epi, bool amn, bool bmn, int M, int N, Share s, int32_t* status, void* partial)
       : epilogue(epi), a_mn(amn), b_mn(bmn) {
     g.M = M;
     g.N = N;
     g.m_tiles = g.m_split = tiles(M, kGemmM);
     g.n_tiles = tiles(N, epi == GEMM_GLU ? kGemmN / 2 : kGemmN);
-    g.splits = j.splits = splits;
+    g.whole = s.whole;
+    g.shares = s.shares;
     g.partial = static_cast<float*>(partial);
     g.status = status;
     g.wait_limit = device_wait_limit();
-    j.M = M;
-    j.N = N;
   }
   void map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows) {
     const char* e = nullptr;
-    if (!make_tmap_matrix(m, x.p, x.rows, x.cols, x.rows > 1 ? x.stride : x.cols, elem, cols, rows,
-                          &e) && !err)
-      err = e;
+    // a single row's stride is never used, but has to be whole 16-byte pieces
+    const int64_t stride = x.rows > 1 ? x.stride : (x.cols + 15) / 16 * 16;
+    if (!make_tmap_matrix(m, x.p, x.rows, x.cols, stride, elem, cols, rows, &e) && !err) err = e;
   }
   void a(int i, const Matrix& m) { map(&g.a[i], m, 2, kGemmK, a_mn ? 64 : kGemmM / 2); }
   void b(int i, const Matrix& m) { map(&g.b[i], m, 2, kGemmK, b_mn ? 64 : kGemmN / 2); }
@@ -177,14 +183,13 @@ struct Product {
     g.k_tiles = phases * g.k_split;
   }
   void box(CUtensorMap* m, void* p, int elem, int64_t stride) {   // what an epilogue moves
-    if (g.splits == 1) map(m, {p, g.M, g.N, stride}, elem, kGemmBox, kGemmBox);
+    map(m, {p, g.M, g.N, stride}, elem, kGemmBox, kGemmBox);
   }
   void out(int i, void* p, bool f32 = false) {
-    outputs[i] = p;
+    j.out[i] = p;
     g.out_f32 = f32;
     box(&g.out[i], p, f32 ? 4 : 2, g.N);
   }
-  void act(int activation) { g.act = j.act = activation; }
   void kept(void* gate, void* up) {
     j.gate = gate;
     j.up = up;
@@ -194,8 +199,7 @@ struct Product {
       uint8_t* p = static_cast<uint8_t*>(i ? up : gate);
       CUtensorMap* m = i ? g.up : g.gate;
       box(&m[0], p, 2, g.N);
-      if (g.splits == 1)
-        map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, kGemmBox, kGemmBox);
+      map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, kGemmBox, kGemmBox);
     }
   }
   void gradients(void* dgate, void* dup) {
@@ -208,13 +212,7 @@ struct Product {
   cp_status_t run(const Plan& plan, cudaStream_t st, const char* what) {
     if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
     ENTRY_CUDA(launch_gemm_bf16(g, epilogue, a_mn, b_mn, plan.sms, st), what);
-    if (g.splits == 1) return CP_OK;
-    const int n = g.m_split < g.m_tiles ? 2 : 1;   // outputs
-    for (int i = 0; i < n; ++i) {
-      j.partial = g.partial + (int64_t)i * g.splits * g.M * g.N;
-      j.out = outputs[i];
-      ENTRY_CUDA(launch_ffn_join(j, epilogue, !g.out_f32, st), what);
-    }
+    if (g.shares > 1) ENTRY_CUDA(launch_gemm_join(g, j, epilogue, st), what);
     return CP_OK;
   }
 };
@@ -233,7 +231,7 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   gu.b(1, {wu, F, D, p->w_up_stride});
   gu.k(D);
   gu.out(0, h);
-  gu.act(p->activation);
+  gu.g.act = p->activation;
   gu.kept(gate, up);
   if ((e = gu.run(plan, st, "gate and up projections")) != CP_OK) return e;
   Product down(GEMM_STORE, false, false, T, O, plan.down, status, partial);
@@ -260,7 +258,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   dh.b(0, {wd, O, F, p->w_down_stride});
   dh.k(O);
   dh.out(0, h);
-  dh.act(p->activation);
+  dh.g.act = p->activation;
   dh.kept(const_cast<void*>(gate), const_cast<void*>(up));
   dh.gradients(dg, du);
   if ((e = dh.run(plan, st, "hidden gradients")) != CP_OK) return e;
@@ -284,7 +282,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   }
   if (dwg || dwu) {   // both as one product, m running through both
     const bool both = dwg && dwu;
-    Product q(GEMM_STORE, true, true, F, D, plan.d_in, status, partial);
+    Product q(GEMM_STORE, true, true, F, D, both ? plan.d_both : plan.d_in, status, partial);
     q.a(0, {dwg ? dg : du, T, F, F});
     q.out(0, dwg ? dwg : dwu, wide);
     if (both) {
@@ -324,13 +322,12 @@ struct F32 {
     return CP_OK;
   }
   cp_status_t sum(int splits, int M, int N, void* out, const char* what) const {
-    JoinArgs j = {};
+    F32JoinArgs j = {};
     j.partial = partial;
     j.splits = splits;
-    j.M = M;
-    j.N = N;
-    j.out = out;
-    ENTRY_CUDA(launch_ffn_join(j, GEMM_STORE, false, st), what);
+    j.n = (int64_t)M * N;
+    j.out = static_cast<float*>(out);
+    ENTRY_CUDA(launch_f32_join(j, GEMM_STORE, st), what);
     return CP_OK;
   }
   cp_status_t product(const void* a, int64_t sam, int64_t sak, const void* b, int64_t sbn,
@@ -351,22 +348,21 @@ cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   const int64_t n = (int64_t)T * F;
   cp_status_t e;
-  if ((e = f.shares(x, p->x_stride, 1, wg, p->w_gate_stride, 1, T, F, D, plan.gate_up, f.partial,
+  if ((e = f.shares(x, p->x_stride, 1, wg, p->w_gate_stride, 1, T, F, D, plan.gate_up.shares, f.partial,
                     false, "gate projection")) != CP_OK ||
-      (e = f.shares(x, p->x_stride, 1, wu, p->w_up_stride, 1, T, F, D, plan.gate_up,
-                    f.partial + plan.gate_up * n, false, "up projection")) != CP_OK)
+      (e = f.shares(x, p->x_stride, 1, wu, p->w_up_stride, 1, T, F, D, plan.gate_up.shares,
+                    f.partial + plan.gate_up.shares * n, false, "up projection")) != CP_OK)
     return e;
-  JoinArgs j = {};
+  F32JoinArgs j = {};
   j.partial = f.partial;
-  j.splits = plan.gate_up;
-  j.M = T;
-  j.N = F;
-  j.out = h;
+  j.splits = plan.gate_up.shares;
+  j.n = (int64_t)T * F;
+  j.out = static_cast<float*>(h);
   j.act = p->activation;
-  j.gate = gate;
-  j.up = up;
-  ENTRY_CUDA(launch_ffn_join(j, GEMM_GLU, false, st), "activation");
-  return f.product(h, F, 1, wd, p->w_down_stride, 1, T, O, F, plan.down, y, "down projection");
+  j.gate = static_cast<float*>(gate);
+  j.up = static_cast<float*>(up);
+  ENTRY_CUDA(launch_f32_join(j, GEMM_GLU, st), "activation");
+  return f.product(h, F, 1, wd, p->w_down_stride, 1, T, O, F, plan.down.shares, y, "down projection");
 }
 
 cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
@@ -378,23 +374,22 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   const F32 f{reinterpret_cast<float*>(at + 3 * hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  if ((e = f.shares(dy, p->dy_stride, 1, wd, 1, p->w_down_stride, T, F, O, plan.dh, f.partial,
+  if ((e = f.shares(dy, p->dy_stride, 1, wd, 1, p->w_down_stride, T, F, O, plan.dh.shares, f.partial,
                     false, "hidden gradients")) != CP_OK)
     return e;
-  JoinArgs j = {};
+  F32JoinArgs j = {};
   j.partial = f.partial;
-  j.splits = plan.dh;
-  j.M = T;
-  j.N = F;
-  j.out = h;
+  j.splits = plan.dh.shares;
+  j.n = (int64_t)T * F;
+  j.out = static_cast<float*>(h);
   j.act = p->activation;
-  j.gate = const_cast<void*>(gate);
-  j.up = const_cast<void*>(up);
-  j.dgate = dg;
-  j.dup = du;
-  ENTRY_CUDA(launch_ffn_join(j, GEMM_DGLU, false, st), "activation's gradient");
+  j.gate = static_cast<float*>(const_cast<void*>(gate));
+  j.up = static_cast<float*>(const_cast<void*>(up));
+  j.dgate = static_cast<float*>(dg);
+  j.dup = static_cast<float*>(du);
+  ENTRY_CUDA(launch_f32_join(j, GEMM_DGLU, st), "activation's gradient");
   if (dx) {
-    const int s = plan.dx;
+    const int s = plan.dx.shares;
     const int64_t n = (int64_t)T * D;
     float* to = s > 1 ? f.partial : static_cast<float*>(dx);
     if ((e = f.shares(dg, F, 1, wg, 1, p->w_gate_stride, T, D, F, s, to, false,
@@ -404,13 +399,13 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
         (s > 1 && (e = f.sum(2 * s, T, D, dx, "input gradient's sums")) != CP_OK))
       return e;
   }
-  if (dwd && (e = f.product(dy, 1, p->dy_stride, h, 1, F, O, F, T, plan.d_down, dwd,
+  if (dwd && (e = f.product(dy, 1, p->dy_stride, h, 1, F, O, F, T, plan.d_down.shares, dwd,
                             "down weight's gradient")) != CP_OK)
     return e;
-  if (dwg && (e = f.product(dg, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in, dwg,
+  if (dwg && (e = f.product(dg, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in.shares, dwg,
                             "gate weight's gradient")) != CP_OK)
     return e;
-  if (dwu && (e = f.product(du, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in, dwu,
+  if (dwu && (e = f.product(du, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in.shares, dwu,
                             "up weight's gradient")) != CP_OK)
     return e;
   return CP_OK;
@@ -453,7 +448,7 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
     return entry_fail(CP_ERR_ALIGNMENT, "gate and up must be 16-byte aligned");
   if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
   const Plan plan = make_plan(desc, sm_count());
-  if (plan.sms < 1) return entry_fail(CP_ERR_CUDA, "no CUDA device");
+  if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, fwd_bytes(desc, plan))) != CP_OK) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -490,7 +485,7 @@ cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if (!dx && !dw_gate && !dw_up && !dw_down) return CP_OK;   // nothing is wanted
   if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
   const Plan plan = make_plan(desc, sm_count());
-  if (plan.sms < 1) return entry_fail(CP_ERR_CUDA, "no CUDA device");
+  if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, bwd_bytes(desc, plan))) != CP_OK) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   ENTRY_CUDA(cudaMemsetAsync(ws, 0, 8, st), "clear the status word");

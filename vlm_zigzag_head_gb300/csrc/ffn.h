@@ -46,8 +46,9 @@ struct GemmArgs {
   int m_split;         // m tiles from here on: a[1], out[1] (m_tiles: none)
   int k_tiles;         // all k tiles
   int k_split;         // k tiles from here on: a[1], b[1] (k_tiles: none)
-  int splits;          // > 1: that many units share a tile's k; sums go to `partial`
-  float* partial;      // [splits][M][N], once for each output (GEMM_GLU: gate, up)
+  int whole;           // tiles of one unit; each tile after them is `shares` units,
+  int shares;          // which share its k and leave their sums in `partial`
+  float* partial;      // [tile - whole][share][64][256][4]: columns 4 c .. 4 c + 3 of a row
   int out_f32;
   int act;
   int keep;            // GEMM_GLU: write gate and up
@@ -58,21 +59,37 @@ struct GemmArgs {
 cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, bool a_mn, bool b_mn, int sms,
                              cudaStream_t st);
 
-// The sums of the shares of a product, and what its epilogue would have done.
+// How many of n tiles run as one unit each, and the shares of the others: the last
+// tiles, too few for all pairs of CTAs at once, are cut along k where that saves time.
+void share_tail(int64_t n, int k_tiles, int pairs, int* whole, int* shares);
+inline size_t partial_bytes(int64_t n, int whole, int shares) {
+  return (size_t)(n - whole) * shares * kGemmM * kGemmN * sizeof(float);
+}
+
+// What the epilogue would have done with the tiles that are shared, from their sums.
 struct JoinArgs {
-  const float* partial;   // [splits][M][N]; gate and up: [2][splits][M][N]
-  int splits;
-  int64_t M;
-  int N;
-  void* out;              // [M][N]: sum; act(gate) up; h
-  int act;
-  void* gate;             // GEMM_GLU: written (nullable), GEMM_DGLU: read; bf16: both planes
+  void* out[2];        // [M][N]; two where m_split < m_tiles
+  void* gate;          // GEMM_GLU: written (nullable), GEMM_DGLU: read; both planes
   void* up;
-  void* dgate;            // [M][N]
+  void* dgate;         // [M][N]
   void* dup;
 };
-// bf16: out, dgate, dup are bf16 (else all fp32).
-cudaError_t launch_ffn_join(const JoinArgs& j, int epilogue, bool bf16, cudaStream_t st);
+cudaError_t launch_gemm_join(const GemmArgs& g, const JoinArgs& j, int epilogue, cudaStream_t st);
+
+// fp32: the sums of the shares of a product (partial [splits][M][N]; gate and up:
+// [2][splits][M][N]) and what its epilogue does.  All arrays [M][N] fp32.
+struct F32JoinArgs {
+  const float* partial;
+  int splits;
+  int64_t n;           // M N
+  float* out;          // sum; act(gate) up; h
+  int act;
+  float* gate;         // GEMM_GLU: written (nullable), GEMM_DGLU: read
+  float* up;
+  float* dgate;
+  float* dup;
+};
+cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st);
 
 // fp32 products on CUDA cores: partial[split][m][n] = sum over the split's k of
 // A(m, k) B(n, k), an element of A at m * sam + k * sak (one of the strides is 1).

@@ -1,9 +1,10 @@
-// The gated feed-forward block beside its tensor-core products: sums of the shares of
-// a product with what its epilogue does, and the fp32 products on CUDA cores.
+// The gated feed-forward block beside its tensor-core products: what becomes of tiles
+// whose k was shared, and the fp32 products on CUDA cores.
 #include <cuda_bf16.h>
 
 #include "ffn.h"
 #include "ffn_act.cuh"
+#include "ffn_tiles.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -12,108 +13,151 @@ namespace {
 
 using namespace ptx;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const void* p, int64_t i) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+// A thread has eight columns of one row of a tile (GEMM_GLU: of gate and of up) and
+// adds their shares in order, so the sums do not depend on timing.  Bound by memory:
+// neighbouring threads read neighbouring rows' 16 bytes.
+template <int kEpi>
+__global__ void __launch_bounds__(256)
+    tile_join_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ JoinArgs j) {
+  constexpr int kTileN = kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN;
+  const TilePlace t = tile_place(g, g.whole + blockIdx.x);
+  const int second = t.m >= g.m_split;
+  const int row = (t.m - (second ? g.m_split : 0)) * kGemmM + threadIdx.x;
+  const int col = t.n * kTileN + blockIdx.y * 8;
+  if (row >= g.M || col >= g.N) return;   // N is a multiple of 8
+  const float4* part = reinterpret_cast<const float4*>(g.partial) +
+                       (int64_t)blockIdx.x * g.shares * (64 * kGemmM) + threadIdx.x;
+  auto sum = [&](int piece, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < g.shares; ++s) {
+      const float4 a = part[(s * 64 + piece) * kGemmM], b = part[(s * 64 + piece + 1) * kGemmM];
+      f[0] += a.x;
+      f[1] += a.y;
+      f[2] += a.z;
+      f[3] += a.w;
+      f[4] += b.x;
+      f[5] += b.y;
+      f[6] += b.z;
+      f[7] += b.w;
+    }
+  };
+  const int64_t at = (int64_t)row * g.N + col;
+  auto put = [&](void* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
+        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                   pack_bf16x2(f[6], f[7]));
+  };
+  const int64_t low = kept_low(g.M, g.N) + row * kept_pitch(g.N) + col;
+  float x[8];
+  sum(blockIdx.y * 2, x);
+  if constexpr (kEpi == GEMM_STORE) {
+    if (g.out_f32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(j.out[second]) + at);
+      p[0] = make_float4(x[0], x[1], x[2], x[3]);
+      p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      put(j.out[second], x);
+    }
+  } else if constexpr (kEpi == GEMM_GLU) {
+    float u[8], h[8], unused;
+    sum(32 + blockIdx.y * 2, u);
+    if (j.gate != nullptr) {
+      auto keep = [&](void* p, const float (&f)[8]) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split24(f[i], hi[i], lo[i]);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
+            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16,
+                       hi[6] | hi[7] << 16);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + low) =
+            make_uint2(lo[0] | lo[1] << 8 | lo[2] << 16 | lo[3] << 24,
+                       lo[4] | lo[5] << 8 | lo[6] << 16 | lo[7] << 24);
+      };
+      keep(j.gate, x);
+      keep(j.up, u);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = activation<false>(x[i], g.act, unused) * u[i];
+    put(j.out[0], h);
   } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+    auto kept = [&](const void* p, float (&f)[8]) {
+      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
+      const uint2 l = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + low);
+      const uint32_t hi[4] = {v.x, v.y, v.z, v.w}, lo[2] = {l.x, l.y};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        f[i] = join24(hi[i / 2] >> (i % 2 * 16) & 0xffffu, lo[i / 4] >> (i % 4 * 8));
+    };
+    float gate[8], up[8], h[8];
+    kept(j.gate, gate);
+    kept(j.up, up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float da;
+      const float a = activation<true>(gate[i], g.act, da);
+      h[i] = a * up[i];
+      gate[i] = x[i] * up[i] * da;
+      up[i] = x[i] * a;
+    }
+    put(j.dgate, gate);
+    put(j.dup, up);
+    put(j.out[0], h);
   }
-}
-template <typename T>
-__device__ __forceinline__ void store4(void* p, int64_t i, float4 v) {
-  if constexpr (sizeof(T) == 4)
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
-        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-// Four elements, from column c of row m on, of a kept projection.
-template <typename T>
-__device__ __forceinline__ void keep4(void* p, int64_t m, int c, int64_t M, int N, float4 v) {
-  if constexpr (sizeof(T) == 4) {
-    store4<float>(p, m * N + c, v);
-  } else {
-    uint32_t hi[4], lo[4];
-    split24(v.x, hi[0], lo[0]);
-    split24(v.y, hi[1], lo[1]);
-    split24(v.z, hi[2], lo[2]);
-    split24(v.w, hi[3], lo[3]);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + m * N + c) =
-        make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + kept_low(M, N) + m * kept_pitch(N) +
-                                 c) = lo[0] | lo[1] << 8 | lo[2] << 16 | lo[3] << 24;
-  }
-}
-template <typename T>
-__device__ __forceinline__ float4 kept4(const void* p, int64_t m, int c, int64_t M, int N) {
-  if constexpr (sizeof(T) == 4) {
-    return load4<float>(p, m * N + c);
-  } else {
-    const uint2 h =
-        *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + m * N + c);
-    const uint32_t l = *reinterpret_cast<const uint32_t*>(
-        static_cast<const uint8_t*>(p) + kept_low(M, N) + m * kept_pitch(N) + c);
-    return make_float4(join24(h.x & 0xffffu, l), join24(h.x >> 16, l >> 8),
-                       join24(h.y & 0xffffu, l >> 16), join24(h.y >> 16, l >> 24));
-  }
+__device__ __forceinline__ void add4(float4& v, const float4& w) {
+  v.x += w.x;
+  v.y += w.y;
+  v.z += w.z;
+  v.w += w.w;
 }
 
-// Bound by memory: reads every share once.  Shares are added in order, so the sums do
-// not depend on timing.
-template <typename T, int kEpi>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs j) {
-  const int64_t n = j.M * j.N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;   // N is a multiple of 8
-  const int64_t row = i / j.N;
-  const int col = (int)(i - row * j.N);
+template <int kEpi>
+__global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F32JoinArgs j) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= j.n) return;   // n is a multiple of 8
   auto sum = [&](const float* p) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int s = 0; s < j.splits; ++s) {
-      const float4 w = *reinterpret_cast<const float4*>(p + s * n + i);
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
-    }
+    for (int s = 0; s < j.splits; ++s) add4(v, *reinterpret_cast<const float4*>(p + s * j.n + i));
     return v;
   };
-  float4 x = sum(j.partial);
+  auto put = [&](float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p + i) = make_float4(f[0], f[1], f[2], f[3]);
+  };
+  const float4 v = sum(j.partial);
+  const float x[4] = {v.x, v.y, v.z, v.w};
   if constexpr (kEpi == GEMM_STORE) {
-    store4<T>(j.out, i, x);
+    put(j.out, x);
   } else if constexpr (kEpi == GEMM_GLU) {
-    const float4 u = sum(j.partial + j.splits * n);
+    const float4 w = sum(j.partial + j.splits * j.n);
+    const float u[4] = {w.x, w.y, w.z, w.w};
     if (j.gate != nullptr) {
-      keep4<T>(j.gate, row, col, j.M, j.N, x);
-      keep4<T>(j.up, row, col, j.M, j.N, u);
+      put(j.gate, x);
+      put(j.up, u);
     }
-    float d;
-    x.x = activation<false>(x.x, j.act, d) * u.x;
-    x.y = activation<false>(x.y, j.act, d) * u.y;
-    x.z = activation<false>(x.z, j.act, d) * u.z;
-    x.w = activation<false>(x.w, j.act, d) * u.w;
-    store4<T>(j.out, i, x);
+    float h[4], unused;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = activation<false>(x[e], j.act, unused) * u[e];
+    put(j.out, h);
   } else {
-    const float4 g = kept4<T>(j.gate, row, col, j.M, j.N);
-    const float4 u = kept4<T>(j.up, row, col, j.M, j.N);
-    const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-    const float dh[4] = {x.x, x.y, x.z, x.w};
+    const float4 a4 = *reinterpret_cast<const float4*>(j.gate + i);
+    const float4 u4 = *reinterpret_cast<const float4*>(j.up + i);
+    const float gs[4] = {a4.x, a4.y, a4.z, a4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
     float h[4], dg[4], du[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float da;
       const float a = activation<true>(gs[e], j.act, da);
       h[e] = a * us[e];
-      dg[e] = dh[e] * us[e] * da;
-      du[e] = dh[e] * a;
+      dg[e] = x[e] * us[e] * da;
+      du[e] = x[e] * a;
     }
-    store4<T>(j.dgate, i, make_float4(dg[0], dg[1], dg[2], dg[3]));
-    store4<T>(j.dup, i, make_float4(du[0], du[1], du[2], du[3]));
-    store4<T>(j.out, i, make_float4(h[0], h[1], h[2], h[3]));
+    put(j.dgate, dg);
+    put(j.dup, du);
+    put(j.out, h);
   }
 }
 
@@ -209,20 +253,36 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(const __grid_constant__ G
   }
 }
 
-template <typename T>
-cudaError_t join_t(const JoinArgs& j, int epilogue, cudaStream_t st) {
-  const int64_t blocks = (j.M * j.N / 4 + 255) / 256;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (epilogue == GEMM_STORE) join_kernel<T, GEMM_STORE><<<(unsigned)blocks, 256, 0, st>>>(j);
-  else if (epilogue == GEMM_GLU) join_kernel<T, GEMM_GLU><<<(unsigned)blocks, 256, 0, st>>>(j);
-  else join_kernel<T, GEMM_DGLU><<<(unsigned)blocks, 256, 0, st>>>(j);
+}  // namespace
+
+void share_tail(int64_t n, int k_tiles, int pairs, int* whole, int* shares) {
+  *whole = (int)n;
+  *shares = 1;
+  const int tail = (int)(n % pairs);
+  if (tail == 0) return;
+  // at least four k tiles a share, and twelve saved: joining costs a launch
+  const int s = pairs / tail < k_tiles / 4 ? pairs / tail : k_tiles / 4;
+  if (s < 2 || k_tiles - (k_tiles + s - 1) / s < 12) return;
+  *whole = (int)(n - tail);
+  *shares = s;
+}
+
+cudaError_t launch_gemm_join(const GemmArgs& g, const JoinArgs& j, int epilogue, cudaStream_t st) {
+  const int tail = g.m_tiles * g.n_tiles - g.whole;
+  const dim3 grid((unsigned)tail, epilogue == GEMM_GLU ? 16 : 32);
+  if (epilogue == GEMM_STORE) tile_join_kernel<GEMM_STORE><<<grid, kGemmM, 0, st>>>(g, j);
+  else if (epilogue == GEMM_GLU) tile_join_kernel<GEMM_GLU><<<grid, kGemmM, 0, st>>>(g, j);
+  else tile_join_kernel<GEMM_DGLU><<<grid, kGemmM, 0, st>>>(g, j);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_ffn_join(const JoinArgs& j, int epilogue, bool bf16, cudaStream_t st) {
-  return bf16 ? join_t<__nv_bfloat16>(j, epilogue, st) : join_t<float>(j, epilogue, st);
+cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st) {
+  const int64_t blocks = (j.n / 4 + 255) / 256;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (epilogue == GEMM_STORE) f32_join_kernel<GEMM_STORE><<<(unsigned)blocks, 256, 0, st>>>(j);
+  else if (epilogue == GEMM_GLU) f32_join_kernel<GEMM_GLU><<<(unsigned)blocks, 256, 0, st>>>(j);
+  else f32_join_kernel<GEMM_DGLU><<<(unsigned)blocks, 256, 0, st>>>(j);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_gemm_f32(const GemmF32Args& g, cudaStream_t st) {

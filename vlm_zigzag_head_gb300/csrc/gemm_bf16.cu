@@ -27,6 +27,7 @@
 #include "check.cuh"
 #include "ffn.h"
 #include "ffn_act.cuh"
+#include "ffn_tiles.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -42,10 +43,7 @@ constexpr int kTile = kRows * kGemmK * 2;           // bytes of one operand's pa
 constexpr int kBf16Box = 32 * 32 * 2, kByteBox = 32 * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kDrainLimit = 1LL << 24;
-// m tiles whose n tiles are walked together: about square patches of tiles run at a
-// time, which reads the least of A and B
-constexpr int kGroupM = 8;
-
+constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 // Stages, and a warp's boxes: two bf16 or one fp32; h, gate, up and the low bytes;
 // gate, up, low bytes in, dgate, dup, h out.
 template <int kEpi>
@@ -74,21 +72,24 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
+// Unit u: a tile, and which of its k tiles.  The issuing thread asks for the k tiles
+// alone: between two tiles the tensor core waits for it.
+struct Work {
+  int tile, slot, k0, k1;   // slot: of the partial sums, -1 for a whole tile
+};
+__device__ __forceinline__ Work work_at(const GemmArgs& g, int u) {
+  if (u < g.whole) return {u, -1, 0, g.k_tiles};
+  const unsigned v = u - g.whole, tail = v / g.shares, share = v % g.shares;
+  return {(int)(g.whole + tail), (int)v, (int)(g.k_tiles * share / g.shares),
+          (int)(g.k_tiles * (share + 1) / g.shares)};
+}
 struct Unit {
-  int m, n, split, k0, k1;   // tile, share of k, its k tiles
+  int m, n, slot, k0, k1;
 };
 __device__ __forceinline__ Unit unit_at(const GemmArgs& g, int u) {
-  Unit r;
-  const int tile = u / g.splits;
-  r.split = u % g.splits;
-  const int per_group = kGroupM * g.n_tiles;
-  const int first = tile / per_group * kGroupM, in = tile % per_group;
-  const int rows = min(kGroupM, g.m_tiles - first);
-  r.m = first + in % rows;
-  r.n = in / rows;
-  r.k0 = (int)((long long)g.k_tiles * r.split / g.splits);
-  r.k1 = (int)((long long)g.k_tiles * (r.split + 1) / g.splits);
-  return r;
+  const Work w = work_at(g, u);
+  const TilePlace t = tile_place(g, w.tile);
+  return {t.m, t.n, w.slot, w.k0, w.k1};
 }
 
 __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
@@ -96,11 +97,14 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-__device__ __forceinline__ void store_f32(float* out, int n, int N, const float (&f)[32]) {
+// 32 columns (pieces 8 c .. 8 c + 7) of tile row `row` into a shared tile's sums.
+__device__ __forceinline__ void store_partial(const GemmArgs& g, int slot, int col, int row,
+                                              const float (&f)[32]) {
+  float4* p = reinterpret_cast<float4*>(g.partial) +
+              ((int64_t)slot * (kGemmN / 4) + col / 4) * kGemmM + row;
 #pragma unroll
-  for (int i = 0; i < 32; i += 4)
-    if (n + i < N)   // N is a multiple of 8
-      *reinterpret_cast<float4*>(out + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  for (int i = 0; i < 8; ++i)
+    p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
 __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
@@ -165,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int units = g.m_tiles * g.n_tiles * g.splits;
+  const int units = g.whole + (g.m_tiles * g.n_tiles - g.whole) * g.shares;
   volatile int* abort = &bars->abort;
   const long long lim = g.wait_limit;
 
@@ -236,11 +240,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every load must have been read before the CTA exits
+      // no load may be on its way when the CTA exits (none is once its tiles' epilogues
+      // are done; after a wait gave up, nobody may be reading the stages any more)
       int zero = 0;
       for (int x = j - kStages; x < j; ++x)
         if (x >= 0)
-          mbar_wait_cluster(&bars->empty[x % kStages], (x / kStages) & 1, kDrainLimit, &zero);
+          mbar_wait_cluster(&bars->empty[x % kStages], (x / kStages) & 1, kLandLimit, &zero);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -248,8 +253,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16(kGemmM, kGemmN, kAMN, kBMN);
       bool ok = true;
       int j = 0, n = 0;   // k tiles and units so far
-      for (int u = pair; ok && u < units; u += pairs, ++n) {
-        const Unit t = unit_at(g, u);
+      Work t = work_at(g, pair), next = t;
+      for (int u = pair; ok && u < units; u += pairs, ++n, t = next) {
+        if (u + pairs < units) next = work_at(g, u + pairs);
         const int s = n & 1;
         if (n >= 2 && !mbar_wait_cluster(&bars->acc_empty[s], ((n >> 1) - 1) & 1, lim, abort)) {
           ok = false;
@@ -310,12 +316,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tma_load_2d(&g.gate[1], &bars->box[w], boxes + 2 * kBf16Box, col, row);
       tma_load_2d(&g.up[1], &bars->box[w], boxes + 2 * kBf16Box + kByteBox, col, row);
     };
-    const bool fetches = kEpi == GEMM_DGLU && g.splits == 1;
     int n = 0, fetched = 0, got = 0;
-    if (fetches && pair < units) {
-      fetch(unit_at(g, pair), 0);
+    auto fetch_first = [&](int u) {   // the first chunk of unit u, where it is a whole tile
+      if (kEpi != GEMM_DGLU || u >= g.whole) return;
+      fetch(unit_at(g, u), 0);
       ++fetched;
-    }
+    };
+    fetch_first(pair);
     bool ok = true;
     for (int u = pair; ok && u < units; u += pairs, ++n) {
       const Unit t = unit_at(g, u);
@@ -328,22 +335,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kGemmN;
       const int second = t.m >= g.m_split;
-      const int row0 = first_row(t), row = row0 + lane;
+      const int row0 = first_row(t), tile_row = rank * kRows + quarter * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         const int col = half * (kTileN / 2) + c * kGemmBox, nc = first_col(t, c);
         const bool stores = row0 < g.M && nc < g.N;   // the box is not wholly past the end
-        const int64_t at = (int64_t)row * g.N + nc;
         float x[32];
         load_acc(acc + col, x);
         if constexpr (kEpi == GEMM_GLU) {
           float v[32];
           load_acc(acc + kTileN + col, v);
-          if (g.splits > 1) {
-            const int64_t share = (int64_t)g.M * g.N;
-            if (row < g.M) {
-              store_f32(g.partial + t.split * share + at, nc, g.N, x);
-              store_f32(g.partial + (g.splits + t.split) * share + at, nc, g.N, v);
+          if (t.slot >= 0) {
+            if (row0 + lane < g.M) {
+              store_partial(g, t.slot, col, tile_row, x);
+              store_partial(g, t.slot, kTileN + col, tile_row, v);
             }
             __syncwarp();   // the next load of the accumulator is the whole warp's
             continue;
@@ -371,10 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         } else {
-          if (g.splits > 1) {
-            if (row < g.M)
-              store_f32(g.partial + (int64_t)(t.split + second * g.splits) * g.M * g.N + at, nc,
-                        g.N, x);
+          if (t.slot >= 0) {
+            if (row0 + lane < g.M) store_partial(g, t.slot, col, tile_row, x);
             __syncwarp();
             continue;
           }
@@ -415,9 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (c + 1 < kChunks) {
               fetch(t, c + 1);
               ++fetched;
-            } else if (u + pairs < units) {
-              fetch(unit_at(g, u + pairs), 0);
-              ++fetched;
+            } else {
+              fetch_first(u + pairs);
             }
             uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
             if (lane == 0) bulk_wait_read<0>();
@@ -486,7 +488,7 @@ cudaError_t launch_t(const GemmArgs& g, int sms, cudaStream_t st) {
   constexpr int smem = Layout<kEpi>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)g.m_tiles * g.n_tiles * g.splits;
+  const int64_t units = g.whole + ((int64_t)g.m_tiles * g.n_tiles - g.whole) * g.shares;
   if (units < 1 || units > 0x3fffffff) return cudaErrorInvalidConfiguration;
   const int64_t pairs = units < sms / 2 ? units : sms / 2;
   kernel<<<(unsigned)(2 * pairs), kThreads, smem, st>>>(g);
