@@ -6,7 +6,7 @@ off by at most a step (the tensor core may cut off): 2 (K + 8) u times the sum o
 activation is off by 2^-20 of its value (exponential 2 u, its argument's rounding times up to 32,
 division 2 u).  Slopes: |a'| <= 1.13, |a''| <= 1.  With e_z the error of z, forward:
     e_h <= 1.13 e_g |u| + |a| (e_u + 2^-20 |u|) + r |h|,  e_y = e_h |Wd| + sum error + r |y|;
-backward, from g and u kept to 24 bits (e_g + k |g|, e_u + k |u|; k = 2^-17 in bf16, 0 in fp32):
+backward, from g and u kept to 24 bits (e_g + k |g|, e_u + k |u|; k = 2^-15 in bf16, 0 in fp32):
     e_dg <= |u a'| e_dh + |dh a'| e_u + |dh u| (e_g + 2^-20) + r |dg|,
     e_du <= |a| e_dh + |dh| (1.13 e_g + 2^-20 |a|) + r |du|,
 and the last products pass these on as y does.  Terms of second order: 10 % more.  These bounds
@@ -48,7 +48,7 @@ def _bounds(x, wg, wu, wd, dy, act, r):
     eg, eu = summed(D) * (ax @ awg.T), summed(D) * (ax @ awu.T)
     eh = 1.13 * eg * np.abs(u) + np.abs(a) * (eu + 2 ** -20 * np.abs(u)) + r * np.abs(h)
     ey = eh @ awd.T + summed(F) * (np.abs(h) @ awd.T)
-    k = 0.0 if r == U else 2.0 ** -17
+    k = 0.0 if r == U else 2.0 ** -15
     eg, eu = eg + k * np.abs(g), eu + k * np.abs(u)
     dh = dy @ wd
     edh = summed(Do) * (ady @ awd)

@@ -183,7 +183,7 @@ struct Product {
     g.k_tiles = phases * g.k_split;
   }
   void box(CUtensorMap* m, void* p, int elem, int64_t stride) {   // what an epilogue moves
-    map(m, {p, g.M, g.N, stride}, elem, kGemmBox, kGemmBox);
+    map(m, {p, g.M, g.N, stride}, elem, elem == 4 ? 32 : 64, 32);
   }
   void out(int i, void* p, bool f32 = false) {
     j.out[i] = p;
@@ -199,7 +199,7 @@ struct Product {
       uint8_t* p = static_cast<uint8_t*>(i ? up : gate);
       CUtensorMap* m = i ? g.up : g.gate;
       box(&m[0], p, 2, g.N);
-      map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, kGemmBox, kGemmBox);
+      map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, 64, 32);
     }
   }
   void gradients(void* dgate, void* dup) {

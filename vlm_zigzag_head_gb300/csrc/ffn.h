@@ -15,17 +15,17 @@ enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                       int64_t stride, int elem, int box_cols, int box_rows, const char** err);
 
-// The projections kept for a bf16 backward hold 24 bits of their fp32 values: a bf16
-// plane [M][N], then a plane of signed bytes, row pitch kept_pitch(N), that say how far
-// the value lies from its bf16 in steps of 2^-8 of a bf16 step.  With bf16 alone their
-// rounding passes into every gradient (dw_down off by 3.5e-3 in relative L2, 2.4e-3
-// so, 1.7e-3 its own rounding).
+// The projections kept for a bf16 backward are the upper 24 bits of their fp32 values:
+// a plane [M][N] of upper halves (bf16, cut off), then a plane of the bytes below them,
+// row pitch kept_pitch(N).  With bf16 alone their rounding passes into every gradient
+// (dw_down off by 3.5e-3 in relative L2; 2.4e-3 so, 1.7e-3 its own rounding).
 inline __host__ __device__ int64_t kept_pitch(int64_t N) { return (N + 15) / 16 * 16; }
 inline __host__ __device__ int64_t kept_low(int64_t M, int64_t N) { return M * N * 2; }  // bytes
 inline int64_t kept_bytes(int64_t M, int64_t N) { return kept_low(M, N) + M * kept_pitch(N); }
 
-// Tile of a CTA pair, k step, and the boxes an epilogue warp moves.
-constexpr int kGemmM = 256, kGemmN = 256, kGemmK = 64, kGemmBox = 32;
+// Tile of a CTA pair and k step; an epilogue moves boxes of 32 rows and 64 columns (fp32:
+// 32).
+constexpr int kGemmM = 256, kGemmN = 256, kGemmK = 64;
 
 // What becomes of a tile of products.
 enum : int {
@@ -38,8 +38,8 @@ enum : int {
 // memory where k runs along a row (K-major) or where m (n) does (MN-major).
 struct GemmArgs {
   CUtensorMap a[2], b[2];      // box {64, 128} K-major, {64, 64} MN-major
-  CUtensorMap out[2];          // box {32, 32}; unused where splits > 1
-  CUtensorMap gate[2], up[2];  // the kept planes, box {32, 32}
+  CUtensorMap out[2];          // box {64, 32} bf16, {32, 32} fp32
+  CUtensorMap gate[2], up[2];  // the kept planes, box {64, 32}
   CUtensorMap dgate, dup;      // GEMM_DGLU: written; h goes to out[0]
   int M, N;            // of one output
   int m_tiles, n_tiles;

@@ -9,23 +9,48 @@ namespace cpattn {
 
 namespace {
 
+__device__ __forceinline__ float inverse(float x) {   // 1 unit in the last place; 0 of infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 1 / (1 + e^-z); e^-z overflows to infinity, whose inverse is 0.
 __device__ __forceinline__ float sigmoid(float z) {
-  return __fdividef(1.f, 1.f + ptx::ex2(-1.4426950408889634f * z));
+  return inverse(1.f + ptx::ex2(-1.4426950408889634f * z));
+}
+
+// The normal distribution at g, where e = e^(-g^2 / 2).  To the left of 0 it is e t P(t),
+// t = 1 / (1 + 0.3 |g|), P of degree 7 fitted to the least relative error over |g| <= 14
+// (1.5e-7, 3.5e-7 in fp32), so the far tail keeps its digits; to the right 1 minus that.
+// kFast = false takes erfc of the math library, for fp32 results.
+template <bool kFast>
+__device__ __forceinline__ float normal(float g, float e) {
+  if constexpr (!kFast) return 0.5f * erfcf(-0.70710678118654752f * g);
+  constexpr float c[8] = {1.196293011e-01f, 1.207539588e-01f,
+                          9.991349280e-02f, 1.285616159e-01f,
+                          -5.368362367e-02f, 2.063534856e-01f,
+                          -1.572030634e-01f, 3.567476943e-02f};
+  const float t = inverse(fmaf(0.3f, fabsf(g), 1.f));
+  float p = c[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) p = fmaf(p, t, c[i]);
+  const float q = e * (p * t);
+  return g < 0.f ? q : 1.f - q;
 }
 
 // a(g), and its derivative where asked for.
 //   silu        g s(g),                 s the sigmoid
-//   gelu        g F(g),                 F the normal distribution, by erfc so that the
-//               far left tail keeps its digits
+//   gelu        g F(g),                 F the normal distribution
 //   gelu_tanh   g s(2 z),  z = sqrt(2 / pi) (g + 0.044715 g^3): 0.5 (1 + tanh z) is
 //               s(2 z), without the difference of two ones at the left
-template <bool kDerivative>
+// With a = g s: a' = s + a (1 - s) (2 z)'.
+template <bool kDerivative, bool kFast>
 __device__ __forceinline__ float activation(float g, int act, float& da) {
   if (act == ACT_GELU) {
-    const float f = 0.5f * erfcf(-0.70710678118654752f * g);
-    if constexpr (kDerivative)
-      da = fmaf(g, 0.3989422804014327f * ptx::ex2(-0.72134752044448170f * g * g), f);
+    const float e = ptx::ex2(-0.72134752044448170f * (g * g));
+    const float f = normal<kFast>(g, e);
+    if constexpr (kDerivative) da = fmaf(g, 0.3989422804014327f * e, f);
     return g * f;
   }
   float s, slope;   // slope of the sigmoid's argument
@@ -38,23 +63,42 @@ __device__ __forceinline__ float activation(float g, int act, float& da) {
     s = sigmoid(k * g * fmaf(0.044715f, g2, 1.f));
     slope = k * fmaf(0.134145f, g2, 1.f);
   }
-  if constexpr (kDerivative) da = fmaf(g * s * (1.f - s), slope, s);
-  return g * s;
+  const float a = g * s;
+  if constexpr (kDerivative) da = fmaf(a - a * s, slope, s);
+  return a;
 }
 
-// The 24 bits kept of v: a bf16 (rounded to nearest) and the rest in steps of 2^-8 of
-// its step.  The sum of bit patterns carries across powers of two.
-__device__ __forceinline__ void split24(float v, uint32_t& hi, uint32_t& lo) {
-  const uint32_t r = __float_as_uint(v) + 0x80u;   // rounded to 24 bits
-  hi = (r + 0x8000u) >> 16;
-  lo = ((r - (hi << 16)) >> 8) & 0xffu;
-  if (v != v) {
-    hi = 0x7fc0u;
-    lo = 0u;
-  }
+// The upper 24 bits of two or four fp32 values, in memory order: their upper halves
+// (bf16 planes), and the bytes below them.  Byte permutations alone: rounding to 24
+// bits instead took six instructions a value, and with it the gradient's epilogue
+// longer than its products.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float join24(uint32_t hi, uint32_t lo) {   // lo: any upper bits
-  return __uint_as_float((hi << 16) + (uint32_t)((int32_t)(lo << 24) >> 16));
+__device__ __forceinline__ uint32_t next_bytes(float a, float b, float c, float d) {
+  return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0051),
+                     __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0051), 0x5410);
+}
+// Value i of a pair of upper halves, and its byte, number k of four.  The lowest eight
+// bits, of which nothing was kept, repeat that byte: off by at most 2^-15 of the value,
+// zeros and infinities are exact.
+template <int i, int k>
+__device__ __forceinline__ float rejoin(uint32_t halves, uint32_t bytes) {
+  return __uint_as_float(
+      __byte_perm(halves, bytes, (4 + k) | (4 + k) << 4 | (2 * i) << 8 | (2 * i + 1) << 12));
+}
+
+// Eight values from four pairs of halves and two words of bytes.
+__device__ __forceinline__ void rejoin8(const uint32_t* halves, const uint32_t* bytes,
+                                        float (&f)[8]) {
+  f[0] = rejoin<0, 0>(halves[0], bytes[0]);
+  f[1] = rejoin<1, 1>(halves[0], bytes[0]);
+  f[2] = rejoin<0, 2>(halves[1], bytes[0]);
+  f[3] = rejoin<1, 3>(halves[1], bytes[0]);
+  f[4] = rejoin<0, 0>(halves[2], bytes[1]);
+  f[5] = rejoin<1, 1>(halves[2], bytes[1]);
+  f[6] = rejoin<0, 2>(halves[3], bytes[1]);
+  f[7] = rejoin<1, 3>(halves[3], bytes[1]);
 }
 
 }  // namespace

@@ -65,30 +65,24 @@ __global__ void __launch_bounds__(256)
     sum(32 + blockIdx.y * 2, u);
     if (j.gate != nullptr) {
       auto keep = [&](void* p, const float (&f)[8]) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) split24(f[i], hi[i], lo[i]);
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
-            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16,
-                       hi[6] | hi[7] << 16);
+            make_uint4(upper_halves(f[0], f[1]), upper_halves(f[2], f[3]),
+                       upper_halves(f[4], f[5]), upper_halves(f[6], f[7]));
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + low) =
-            make_uint2(lo[0] | lo[1] << 8 | lo[2] << 16 | lo[3] << 24,
-                       lo[4] | lo[5] << 8 | lo[6] << 16 | lo[7] << 24);
+            make_uint2(next_bytes(f[0], f[1], f[2], f[3]), next_bytes(f[4], f[5], f[6], f[7]));
       };
       keep(j.gate, x);
       keep(j.up, u);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = activation<false>(x[i], g.act, unused) * u[i];
+    for (int i = 0; i < 8; ++i) h[i] = activation<false, true>(x[i], g.act, unused) * u[i];
     put(j.out[0], h);
   } else {
     auto kept = [&](const void* p, float (&f)[8]) {
       const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
       const uint2 l = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + low);
       const uint32_t hi[4] = {v.x, v.y, v.z, v.w}, lo[2] = {l.x, l.y};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[i] = join24(hi[i / 2] >> (i % 2 * 16) & 0xffffu, lo[i / 4] >> (i % 4 * 8));
+      rejoin8(hi, lo, f);
     };
     float gate[8], up[8], h[8];
     kept(j.gate, gate);
@@ -96,7 +90,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float da;
-      const float a = activation<true>(gate[i], g.act, da);
+      const float a = activation<true, true>(gate[i], g.act, da);
       h[i] = a * up[i];
       gate[i] = x[i] * up[i] * da;
       up[i] = x[i] * a;
@@ -140,7 +134,7 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
     }
     float h[4], unused;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = activation<false>(x[e], j.act, unused) * u[e];
+    for (int e = 0; e < 4; ++e) h[e] = activation<false, false>(x[e], j.act, unused) * u[e];
     put(j.out, h);
   } else {
     const float4 a4 = *reinterpret_cast<const float4*>(j.gate + i);
@@ -150,7 +144,7 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float da;
-      const float a = activation<true>(gs[e], j.act, da);
+      const float a = activation<true, false>(gs[e], j.act, da);
       h[e] = a * us[e];
       dg[e] = x[e] * us[e] * da;
       du[e] = x[e] * a;

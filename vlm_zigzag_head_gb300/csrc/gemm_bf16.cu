@@ -14,11 +14,12 @@
 // Warp roles (384 threads):
 //   warp 0       TMA producer (one lane): this CTA's rows of A and B
 //   warp 1       TMEM allocation; in the first CTA lane 0 issues every MMA
-//   warps 4..11  epilogue: TMEM lane quarter w % 4, column half (w - 4) / 4
+//   warps 4..11  epilogue: TMEM lane quarter w % 4; the two warps of a quarter have
+//                halves of each 64 columns
 //
-// The epilogue moves boxes of 32 x 32 through shared memory by TMA, a warp its own:
-// a thread holds one row, and rows read and written straight from it (16 bytes in
-// each of 32 lines) took longer than the products.
+// The epilogue moves boxes of 32 rows x 64 columns through shared memory by TMA, two
+// warps to a box: a thread holds one row, and rows read and written straight from it
+// (16 bytes in each of 32 lines) took longer than the products.
 //
 // Rows and columns past the matrices' ends are zeros by TMA's fill and are not
 // stored.
@@ -40,20 +41,20 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kRows = kGemmM / 2;                   // of A and B in one CTA
 constexpr int kTile = kRows * kGemmK * 2;           // bytes of one operand's part of a stage
-constexpr int kBf16Box = 32 * 32 * 2, kByteBox = 32 * 32;
+constexpr int kBf16Box = 32 * 64 * 2, kByteBox = 32 * 64;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kDrainLimit = 1LL << 24;
 constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
-// Stages, and a warp's boxes: two bf16 or one fp32; h, gate, up and the low bytes;
-// gate, up, low bytes in, dgate, dup, h out.
+// Stages, and the boxes of two warps: two of bf16 (or two halves of fp32); h, gate, up
+// and the low bytes; gate, up, low bytes in, dgate, dup, h out.
 template <int kEpi>
 struct Layout {
   static constexpr int kStages = kEpi == GEMM_STORE ? 6 : kEpi == GEMM_GLU ? 5 : 4;
-  static constexpr int kWarpBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
+  static constexpr int kPairBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
                                     : kEpi == GEMM_GLU ? 3 * kBf16Box + 2 * kByteBox
                                                        : 5 * kBf16Box + 2 * kByteBox;
   static constexpr int kBoxes = kStages * 2 * kTile;
-  static constexpr int kBars = kBoxes + kEpiWarps * kWarpBytes;
+  static constexpr int kBars = kBoxes + kEpiWarps / 2 * kPairBytes;
   static constexpr int kSmem = kBars + 256 + 1024;   // slack for alignment
 };
 static_assert(Layout<GEMM_STORE>::kSmem <= 227 * 1024, "shared memory budget");
@@ -65,7 +66,7 @@ struct Bars {
   uint64_t empty[6];       // both: the stage's MMAs are done
   uint64_t acc_full[2];    // both: a tile's products are done
   uint64_t acc_empty[2];   // first CTA: both CTAs' epilogues have read them
-  uint64_t box[kEpiWarps];   // GEMM_DGLU: a warp's boxes have landed
+  uint64_t box[4];         // GEMM_DGLU: a quarter's boxes have landed
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -116,8 +117,8 @@ __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
 }
 
-// 16-byte piece p of a lane's row in a 32 x 32 box of 32-, 64- or 128-byte rows, as
-// TMA's swizzle of that size places it; the eight lanes of a pass meet no bank twice.
+// 16-byte piece p of a lane's row in a box of 64- or 128-byte rows, as TMA's swizzle
+// of that size places it; the eight lanes of a pass meet no bank twice.
 template <int kRowBytes>
 __device__ __forceinline__ uint4* piece(uint8_t* box, int lane, int p) {
   constexpr int kSwap = kRowBytes / 16 - 1;
@@ -125,10 +126,11 @@ __device__ __forceinline__ uint4* piece(uint8_t* box, int lane, int p) {
                                   ((p ^ (lane * kRowBytes / 128 & kSwap)) << 4));
 }
 
-__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, const float (&f)[32]) {
+// A lane's 32 columns, the first or second half of a box's (fp32: a box of their own).
+__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, int half, const float (&f)[32]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p)
-    *piece<64>(box, lane, p) =
+    *piece<128>(box, lane, half * 4 + p) =
         make_uint4(pack_bf16x2(f[8 * p], f[8 * p + 1]), pack_bf16x2(f[8 * p + 2], f[8 * p + 3]),
                    pack_bf16x2(f[8 * p + 4], f[8 * p + 5]), pack_bf16x2(f[8 * p + 6], f[8 * p + 7]));
 }
@@ -139,22 +141,21 @@ __device__ __forceinline__ void put_f32(uint8_t* box, int lane, const float (&f)
         make_uint4(__float_as_uint(f[4 * p]), __float_as_uint(f[4 * p + 1]),
                    __float_as_uint(f[4 * p + 2]), __float_as_uint(f[4 * p + 3]));
 }
-__device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, const float (&f)[32]) {
+__device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, int half,
+                                         const float (&f)[32]) {
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     uint32_t h[8], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t a[4], b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) split24(f[16 * p + 4 * i + e], a[e], b[e]);
-      h[2 * i] = a[0] | a[1] << 16;
-      h[2 * i + 1] = a[2] | a[3] << 16;
-      l[i] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+      const float* v = f + 16 * p + 4 * i;
+      h[2 * i] = upper_halves(v[0], v[1]);
+      h[2 * i + 1] = upper_halves(v[2], v[3]);
+      l[i] = next_bytes(v[0], v[1], v[2], v[3]);
     }
-    *piece<64>(hi, lane, 2 * p) = make_uint4(h[0], h[1], h[2], h[3]);
-    *piece<64>(hi, lane, 2 * p + 1) = make_uint4(h[4], h[5], h[6], h[7]);
-    *piece<32>(lo, lane, p) = make_uint4(l[0], l[1], l[2], l[3]);
+    *piece<128>(hi, lane, half * 4 + 2 * p) = make_uint4(h[0], h[1], h[2], h[3]);
+    *piece<128>(hi, lane, half * 4 + 2 * p + 1) = make_uint4(h[4], h[5], h[6], h[7]);
+    *piece<64>(lo, lane, half * 2 + p) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -182,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars->acc_full[s], 1);
       mbar_init(&bars->acc_empty[s], 2 * kEpiWarps);
     }
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&bars->box[w], 1);
+    for (int q = 0; q < 4; ++q) mbar_init(&bars->box[q], 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -294,41 +295,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, half = (warp - 4) >> 2, w = warp - 4;
-    uint8_t* boxes = smem + L::kBoxes + w * L::kWarpBytes;
-    // columns of a warp: 128 of one product, or 64 of gate and of up
-    constexpr int kChunks = kEpi == GEMM_GLU ? 2 : 4;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const bool issues = half == 0 && lane == 0;   // of the two warps' boxes
+    const int pair_bar = 1 + quarter;
+    auto pair_sync = [&] { named_sync(pair_bar, 64); };
+    uint8_t* boxes = smem + L::kBoxes + quarter * L::kPairBytes;
     constexpr int kTileN = kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN;
+    constexpr int kChunks = kTileN / 64;
     auto first_row = [&](const Unit& t) {
       return (t.m - (t.m >= g.m_split ? g.m_split : 0)) * kGemmM + rank * kRows + quarter * 32;
     };
-    auto first_col = [&](const Unit& t, int c) {
-      return t.n * kTileN + half * (kTileN / 2) + c * kGemmBox;
-    };
     // GEMM_DGLU: the kept gate and up of a chunk, on their way while the one before
     // is worked on
-    auto fetch = [&](const Unit& t, int c) {
-      if (lane != 0) return;
-      const int row = first_row(t), col = first_col(t, c);
-      mbar_expect_tx(&bars->box[w], 2 * (kBf16Box + kByteBox));
-      tma_load_2d(&g.gate[0], &bars->box[w], boxes, col, row);
-      tma_load_2d(&g.up[0], &bars->box[w], boxes + kBf16Box, col, row);
-      tma_load_2d(&g.gate[1], &bars->box[w], boxes + 2 * kBf16Box, col, row);
-      tma_load_2d(&g.up[1], &bars->box[w], boxes + 2 * kBf16Box + kByteBox, col, row);
+    [[maybe_unused]] auto fetch = [&](const Unit& t, int c) {
+      if (!issues) return;
+      const int row = first_row(t), col = t.n * kTileN + c * 64;
+      uint64_t* bar = &bars->box[quarter];
+      mbar_expect_tx(bar, 2 * (kBf16Box + kByteBox));
+      tma_load_2d(&g.gate[0], bar, boxes, col, row);
+      tma_load_2d(&g.up[0], bar, boxes + kBf16Box, col, row);
+      tma_load_2d(&g.gate[1], bar, boxes + 2 * kBf16Box, col, row);
+      tma_load_2d(&g.up[1], bar, boxes + 2 * kBf16Box + kByteBox, col, row);
     };
     int n = 0, fetched = 0, got = 0;
     auto fetch_first = [&](int u) {   // the first chunk of unit u, where it is a whole tile
-      if (kEpi != GEMM_DGLU || u >= g.whole) return;
-      fetch(unit_at(g, u), 0);
-      ++fetched;
+      if constexpr (kEpi == GEMM_DGLU) {
+        if (u >= g.whole) return;
+        fetch(unit_at(g, u), 0);
+        ++fetched;
+      }
     };
     fetch_first(pair);
     bool ok = true;
     for (int u = pair; ok && u < units; u += pairs, ++n) {
       const Unit t = unit_at(g, u);
       const int s = n & 1;
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait_cluster(&bars->acc_full[s], (n >> 1) & 1, lim, abort))) {
+      // both warps of a box go on, or neither
+      if (!named_all(pair_bar, 64,
+                     mbar_wait_cluster(&bars->acc_full[s], (n >> 1) & 1, lim, abort))) {
         if (lane == 0) record_timeout(g.status, abort, 33);
         break;
       }
@@ -338,8 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row0 = first_row(t), tile_row = rank * kRows + quarter * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
-        const int col = half * (kTileN / 2) + c * kGemmBox, nc = first_col(t, c);
-        const bool stores = row0 < g.M && nc < g.N;   // the box is not wholly past the end
+        const int col = c * 64 + half * 32, box_col = t.n * kTileN + c * 64;
+        const bool stores = row0 < g.M && box_col < g.N;   // the box is not wholly past the end
         float x[32];
         load_acc(acc + col, x);
         if constexpr (kEpi == GEMM_GLU) {
@@ -353,25 +357,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();   // the next load of the accumulator is the whole warp's
             continue;
           }
-          if (lane == 0) bulk_wait_read<0>();   // the boxes' last stores have read them
-          __syncwarp();
+          if (issues) bulk_wait_read<0>();   // the boxes' last stores have read them
+          pair_sync();
           if (g.keep) {
-            put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, x);
-            put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, v);
+            put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, half, x);
+            put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, half, v);
           }
           float unused;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = activation<false>(x[i], g.act, unused) * v[i];
-          put_bf16(boxes, lane, x);
+          for (int i = 0; i < 32; ++i) x[i] = activation<false, true>(x[i], g.act, unused) * v[i];
+          put_bf16(boxes, lane, half, x);
           fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && stores) {
-            tma_store_2d(&g.out[0], boxes, nc, row0);
+          pair_sync();
+          if (issues && stores) {
+            tma_store_2d(&g.out[0], boxes, box_col, row0);
             if (g.keep) {
-              tma_store_2d(&g.gate[0], boxes + kBf16Box, nc, row0);
-              tma_store_2d(&g.up[0], boxes + 2 * kBf16Box, nc, row0);
-              tma_store_2d(&g.gate[1], boxes + 3 * kBf16Box, nc, row0);
-              tma_store_2d(&g.up[1], boxes + 3 * kBf16Box + kByteBox, nc, row0);
+              tma_store_2d(&g.gate[0], boxes + kBf16Box, box_col, row0);
+              tma_store_2d(&g.up[0], boxes + 2 * kBf16Box, box_col, row0);
+              tma_store_2d(&g.gate[1], boxes + 3 * kBf16Box, box_col, row0);
+              tma_store_2d(&g.up[1], boxes + 3 * kBf16Box + kByteBox, box_col, row0);
             }
             bulk_commit();
           }
@@ -382,22 +386,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             continue;
           }
           if constexpr (kEpi == GEMM_STORE) {
-            uint8_t* box = boxes + (g.out_f32 ? 0 : (c & 1) * kBf16Box);
-            if (lane == 0) {
+            uint8_t* box = boxes + (g.out_f32 ? half : c & 1) * kBf16Box;
+            if (issues) {
               if (g.out_f32) bulk_wait_read<0>();
               else bulk_wait_read<1>();
             }
-            __syncwarp();
+            pair_sync();
             if (g.out_f32) put_f32(box, lane, x);
-            else put_bf16(box, lane, x);
+            else put_bf16(box, lane, half, x);
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (stores) tma_store_2d(&g.out[second], box, nc, row0);
+            pair_sync();
+            if (issues) {
+              if (stores) tma_store_2d(&g.out[second], box, box_col, row0);
+              if (stores && g.out_f32 && box_col + 32 < g.N)
+                tma_store_2d(&g.out[second], box + kBf16Box, box_col + 32, row0);
               bulk_commit();   // one group a chunk, so that the count holds
             }
           } else {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->box[w], got & 1, lim, abort))) {
+            if (!named_all(pair_bar, 64, mbar_wait(&bars->box[quarter], got & 1, lim, abort))) {
               if (lane == 0) record_timeout(g.status, abort, 34);
               ok = false;
               break;
@@ -406,15 +412,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint4 kg[4], ku[4], lg[2], lu[2];
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-              kg[p] = *piece<64>(boxes, lane, p);
-              ku[p] = *piece<64>(boxes + kBf16Box, lane, p);
+              kg[p] = *piece<128>(boxes, lane, half * 4 + p);
+              ku[p] = *piece<128>(boxes + kBf16Box, lane, half * 4 + p);
             }
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              lg[p] = *piece<32>(boxes + 2 * kBf16Box, lane, p);
-              lu[p] = *piece<32>(boxes + 2 * kBf16Box + kByteBox, lane, p);
+              lg[p] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + p);
+              lu[p] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + p);
             }
-            __syncwarp();   // all have read: the next chunk may land
+            if (issues) bulk_wait_read<0>();   // the last stores have read their boxes
+            pair_sync();   // all have read: the next chunk may land
             if (c + 1 < kChunks) {
               fetch(t, c + 1);
               ++fetched;
@@ -422,41 +429,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               fetch_first(u + pairs);
             }
             uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
-            if (lane == 0) bulk_wait_read<0>();
-            __syncwarp();
             const uint32_t* wg = reinterpret_cast<const uint32_t*>(kg);
             const uint32_t* wu = reinterpret_cast<const uint32_t*>(ku);
             const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
             const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {   // eight columns at a time
-              float dg[8], du[8], h[8];
+              float gate[8], up[8], h[8];
+              rejoin8(wg + 4 * p, bg + 2 * p, gate);
+              rejoin8(wu + 4 * p, bu + 2 * p, up);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int i = 8 * p + e;
-                const float gate = join24(wg[i / 2] >> (i % 2 * 16) & 0xffffu, bg[i / 4] >> (i % 4 * 8));
-                const float up = join24(wu[i / 2] >> (i % 2 * 16) & 0xffffu, bu[i / 4] >> (i % 4 * 8));
                 float da;
-                const float a = activation<true>(gate, g.act, da);
-                h[e] = a * up;
-                dg[e] = x[i] * up * da;
-                du[e] = x[i] * a;
+                const float a = activation<true, true>(gate[e], g.act, da), dh = x[8 * p + e];
+                h[e] = a * up[e];
+                gate[e] = dh * up[e] * da;
+                up[e] = dh * a;
               }
               auto put = [&](int which, const float (&f)[8]) {
-                *piece<64>(out + which * kBf16Box, lane, p) =
+                *piece<128>(out + which * kBf16Box, lane, half * 4 + p) =
                     make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
               };
-              put(0, dg);
-              put(1, du);
+              put(0, gate);
+              put(1, up);
               put(2, h);
             }
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && stores) {
-              tma_store_2d(&g.dgate, out, nc, row0);
-              tma_store_2d(&g.dup, out + kBf16Box, nc, row0);
-              tma_store_2d(&g.out[0], out + 2 * kBf16Box, nc, row0);
+            pair_sync();
+            if (issues && stores) {
+              tma_store_2d(&g.dgate, out, box_col, row0);
+              tma_store_2d(&g.dup, out + kBf16Box, box_col, row0);
+              tma_store_2d(&g.out[0], out + 2 * kBf16Box, box_col, row0);
               bulk_commit();
             }
           }
@@ -467,9 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(in_first_cta(&bars->acc_empty[s]));
     }
-    if (lane == 0) {
+    if (issues) {
       int zero = 0;   // a load that nobody waited for (after a wait gave up)
-      for (; got < fetched; ++got) mbar_wait(&bars->box[w], got & 1, kDrainLimit, &zero);
+      for (; got < fetched; ++got) mbar_wait(&bars->box[quarter], got & 1, kDrainLimit, &zero);
       bulk_wait_all();
     }
   }
