@@ -14,7 +14,6 @@ using namespace cpattn;
 namespace {
 
 constexpr int kMaxWidth = 1 << 20;
-constexpr size_t kStatusBytes = 256;   // status word at the start of a workspace
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline int tiles(int64_t n, int tile) { return (int)((n + tile - 1) / tile); }
@@ -76,6 +75,12 @@ int share_k_f32(int64_t M, int64_t N, int64_t K, int sms) {
   return share_k((int64_t)tiles(M, 128) * tiles(N, 128), tiles(K, 4 * kF32K), 2 * sms);
 }
 
+// Forward calls that the kernels for few rows take, and for a batch of them.
+bool few_rows(const cp_gated_ffn_t* p) { return p->dtype == CP_BF16 && p->T <= kFewRows; }
+bool batch_rows(const cp_gated_ffn_t* p) {
+  return p->dtype == CP_BF16 && p->T > kFewRows && p->T <= kBatchRows;
+}
+
 // How the bf16 products' last tiles and the fp32 products' k are shared, and what of
 // the workspace that takes.
 struct Share {
@@ -124,15 +129,20 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
   return r;
 }
 
+// At the start of a workspace, cleared by every call: the status word, and the tickets
+// of shared tiles (fewer than there are pairs of CTAs, eight each).
+constexpr size_t kTicketsAt = 256;
+size_t header_bytes(const Plan& plan) { return kTicketsAt + up256((size_t)plan.sms / 2 * 8 * 4); }
+
 size_t hidden_bytes(const cp_gated_ffn_t* p) {
   return up256((size_t)p->T * p->F * (p->dtype == CP_BF16 ? 2 : 4));
 }
 
 size_t fwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
-  return kStatusBytes + hidden_bytes(p) + up256(plan.fwd_partial);
+  return header_bytes(plan) + hidden_bytes(p) + up256(plan.fwd_partial);
 }
 size_t bwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
-  return kStatusBytes + 3 * hidden_bytes(p) + up256(plan.bwd_partial);
+  return header_bytes(plan) + 3 * hidden_bytes(p) + up256(plan.bwd_partial);
 }
 
 cp_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -150,15 +160,21 @@ struct Matrix {
   int64_t rows, cols, stride;
 };
 
+bool make_map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows, const char** err) {
+  // a single row's stride is never used, but has to be whole 16-byte pieces
+  const int64_t stride = x.rows > 1 ? x.stride : (x.cols + 15) / 16 * 16;
+  return make_tmap_matrix(m, x.p, x.rows, x.cols, stride, elem, cols, rows, err);
+}
+
 // A product under construction; failures stick.
 struct Product {
   GemmArgs g = {};
-  JoinArgs j = {};       // what becomes of its shared tiles
   int epilogue;
   bool a_mn, b_mn;
   const char* err = nullptr;
 
-  Product(int epi, bool amn, bool bmn, int M, int N, Share s, int32_t* status, void* partial)
+  Product(int epi, bool amn, bool bmn, int M, int N, Share s, int follows, uint8_t* ws,
+          void* partial)
       : epilogue(epi), a_mn(amn), b_mn(bmn) {
     g.M = M;
     g.N = N;
@@ -167,14 +183,14 @@ struct Product {
     g.whole = s.whole;
     g.shares = s.shares;
     g.partial = static_cast<float*>(partial);
-    g.status = status;
+    g.follows = follows;
+    g.status = reinterpret_cast<int32_t*>(ws);
+    g.tickets = reinterpret_cast<int32_t*>(ws + kTicketsAt);
     g.wait_limit = device_wait_limit();
   }
   void map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows) {
     const char* e = nullptr;
-    // a single row's stride is never used, but has to be whole 16-byte pieces
-    const int64_t stride = x.rows > 1 ? x.stride : (x.cols + 15) / 16 * 16;
-    if (!make_tmap_matrix(m, x.p, x.rows, x.cols, stride, elem, cols, rows, &e) && !err) err = e;
+    if (!make_map(m, x, elem, cols, rows, &e) && !err) err = e;
   }
   void a(int i, const Matrix& m) { map(&g.a[i], m, 2, kGemmK, a_mn ? 64 : kGemmM / 2); }
   void b(int i, const Matrix& m) { map(&g.b[i], m, 2, kGemmK, b_mn ? 64 : kGemmN / 2); }
@@ -186,13 +202,10 @@ struct Product {
     map(m, {p, g.M, g.N, stride}, elem, elem == 4 ? 32 : 64, 32);
   }
   void out(int i, void* p, bool f32 = false) {
-    j.out[i] = p;
     g.out_f32 = f32;
     box(&g.out[i], p, f32 ? 4 : 2, g.N);
   }
   void kept(void* gate, void* up) {
-    j.gate = gate;
-    j.up = up;
     g.keep = gate != nullptr;
     if (!gate) return;
     for (int i = 0; i < 2; ++i) {
@@ -203,8 +216,6 @@ struct Product {
     }
   }
   void gradients(void* dgate, void* dup) {
-    j.dgate = dgate;
-    j.dup = dup;
     box(&g.dgate, dgate, 2, g.N);
     box(&g.dup, dup, 2, g.N);
   }
@@ -212,20 +223,80 @@ struct Product {
   cp_status_t run(const Plan& plan, cudaStream_t st, const char* what) {
     if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
     ENTRY_CUDA(launch_gemm_bf16(g, epilogue, a_mn, b_mn, plan.sms, st), what);
-    if (g.shares > 1) ENTRY_CUDA(launch_gemm_join(g, j, epilogue, st), what);
     return CP_OK;
   }
 };
 
+cp_status_t fwd_rows(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                     const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
+                     cudaStream_t st) {
+  FfnRowsArgs a = {};
+  a.x = x;
+  a.x_stride = p->x_stride;
+  a.w[0] = wg;
+  a.w[1] = wu;
+  a.w_stride[0] = p->w_gate_stride;
+  a.w_stride[1] = p->w_up_stride;
+  a.out = ws + header_bytes(plan);
+  a.gate = gate;
+  a.up = up;
+  a.T = p->T;
+  a.N = p->F;
+  a.K = p->D;
+  a.act = p->activation;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  ENTRY_CUDA(launch_ffn_rows(a, true, plan.sms, st), "gate and up projections");
+  a.x = a.out;
+  a.x_stride = p->F;
+  a.w[0] = a.w[1] = wd;
+  a.w_stride[0] = a.w_stride[1] = p->w_down_stride;
+  a.out = y;
+  a.N = p->D_out;
+  a.K = p->F;
+  ENTRY_CUDA(launch_ffn_rows(a, false, plan.sms, st), "down projection");
+  return CP_OK;
+}
+
+cp_status_t fwd_tokens(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                       const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
+                       cudaStream_t st) {
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  FfnTokensArgs a = {};
+  a.gate = gate;
+  a.up = up;
+  a.T = T;
+  a.tokens = (T + 15) / 16 * 16;
+  a.act = p->activation;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.wait_limit = device_wait_limit();
+  void* h = ws + header_bytes(plan);
+  const char* err = nullptr;
+  if (!make_map(&a.w[0], {wg, F, D, p->w_gate_stride}, 2, kGemmK, 128, &err) ||
+      !make_map(&a.w[1], {wu, F, D, p->w_up_stride}, 2, kGemmK, 128, &err) ||
+      !make_map(&a.x, {x, T, D, p->x_stride}, 2, kGemmK, a.tokens, &err))
+    return entry_fail(CP_ERR_CUDA, std::string("gate and up projections: ") + err);
+  a.out = h;
+  a.N = F;
+  a.K = D;
+  ENTRY_CUDA(launch_ffn_tokens(a, true, plan.sms, st), "gate and up projections");
+  if (!make_map(&a.w[0], {wd, O, F, p->w_down_stride}, 2, kGemmK, 128, &err) ||
+      !make_map(&a.x, {h, T, F, F}, 2, kGemmK, a.tokens, &err))
+    return entry_fail(CP_ERR_CUDA, std::string("down projection: ") + err);
+  a.out = y;
+  a.N = O;
+  a.K = F;
+  ENTRY_CUDA(launch_ffn_tokens(a, false, plan.sms, st), "down projection");
+  return CP_OK;
+}
+
 cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
                      const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
                      cudaStream_t st) {
-  int32_t* status = reinterpret_cast<int32_t*>(ws);
-  void* h = ws + kStatusBytes;
-  void* partial = ws + kStatusBytes + hidden_bytes(p);
+  void* h = ws + header_bytes(plan);
+  void* partial = ws + header_bytes(plan) + hidden_bytes(p);
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  Product gu(GEMM_GLU, false, false, T, F, plan.gate_up, status, partial);
+  Product gu(GEMM_GLU, false, false, T, F, plan.gate_up, FOLLOWS_NONE, ws, partial);
   gu.a(0, {x, T, D, p->x_stride});
   gu.b(0, {wg, F, D, p->w_gate_stride});
   gu.b(1, {wu, F, D, p->w_up_stride});
@@ -234,7 +305,7 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   gu.g.act = p->activation;
   gu.kept(gate, up);
   if ((e = gu.run(plan, st, "gate and up projections")) != CP_OK) return e;
-  Product down(GEMM_STORE, false, false, T, O, plan.down, status, partial);
+  Product down(GEMM_STORE, false, false, T, O, plan.down, FOLLOWS_A, ws, partial);
   down.a(0, {h, T, F, F});
   down.b(0, {wd, O, F, p->w_down_stride});
   down.k(F);
@@ -246,14 +317,13 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
                      const void* wu, const void* wd, const void* gate, const void* up,
                      const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
                      cudaStream_t st) {
-  int32_t* status = reinterpret_cast<int32_t*>(ws);
-  uint8_t* at = ws + kStatusBytes;
+  uint8_t* at = ws + header_bytes(plan);
   void *dg = at, *du = at + hidden_bytes(p), *h = at + 2 * hidden_bytes(p);
   void* partial = at + 3 * hidden_bytes(p);
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   const bool wide = p->grad_dtype == CP_F32;
   cp_status_t e;
-  Product dh(GEMM_DGLU, false, true, T, F, plan.dh, status, partial);
+  Product dh(GEMM_DGLU, false, true, T, F, plan.dh, FOLLOWS_NONE, ws, partial);
   dh.a(0, {dy, T, O, p->dy_stride});
   dh.b(0, {wd, O, F, p->w_down_stride});
   dh.k(O);
@@ -263,7 +333,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   dh.gradients(dg, du);
   if ((e = dh.run(plan, st, "hidden gradients")) != CP_OK) return e;
   if (dx) {   // dg Wg + du Wu as one product, k running through both
-    Product q(GEMM_STORE, false, true, T, D, plan.dx, status, partial);
+    Product q(GEMM_STORE, false, true, T, D, plan.dx, FOLLOWS_A, ws, partial);
     q.a(0, {dg, T, F, F});
     q.a(1, {du, T, F, F});
     q.b(0, {wg, F, D, p->w_gate_stride});
@@ -273,7 +343,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
     if ((e = q.run(plan, st, "input gradient")) != CP_OK) return e;
   }
   if (dwd) {
-    Product q(GEMM_STORE, true, true, O, F, plan.d_down, status, partial);
+    Product q(GEMM_STORE, true, true, O, F, plan.d_down, FOLLOWS_BOTH, ws, partial);
     q.a(0, {dy, T, O, p->dy_stride});
     q.b(0, {h, T, F, F});
     q.k(T);
@@ -282,7 +352,8 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   }
   if (dwg || dwu) {   // both as one product, m running through both
     const bool both = dwg && dwu;
-    Product q(GEMM_STORE, true, true, F, D, both ? plan.d_both : plan.d_in, status, partial);
+    Product q(GEMM_STORE, true, true, F, D, both ? plan.d_both : plan.d_in, FOLLOWS_BOTH, ws,
+              partial);
     q.a(0, {dwg ? dg : du, T, F, F});
     q.out(0, dwg ? dwg : dwu, wide);
     if (both) {
@@ -343,8 +414,8 @@ struct F32 {
 cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
                     const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
                     cudaStream_t st) {
-  void* h = ws + kStatusBytes;
-  const F32 f{reinterpret_cast<float*>(ws + kStatusBytes + hidden_bytes(p)), st};
+  void* h = ws + header_bytes(plan);
+  const F32 f{reinterpret_cast<float*>(ws + header_bytes(plan) + hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   const int64_t n = (int64_t)T * F;
   cp_status_t e;
@@ -369,7 +440,7 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
                     const void* wu, const void* wd, const void* gate, const void* up,
                     const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
                     cudaStream_t st) {
-  uint8_t* at = ws + kStatusBytes;
+  uint8_t* at = ws + header_bytes(plan);
   void *dg = at, *du = at + hidden_bytes(p), *h = at + 2 * hidden_bytes(p);
   const F32 f{reinterpret_cast<float*>(at + 3 * hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
@@ -452,7 +523,10 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if ((e = check_workspace(workspace, ws_bytes, fwd_bytes(desc, plan))) != CP_OK) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  ENTRY_CUDA(cudaMemsetAsync(ws, 0, 8, st), "clear the status word");
+  if (few_rows(desc))
+    return fwd_rows(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
+  ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
+  if (batch_rows(desc)) return fwd_tokens(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   return desc->dtype == CP_BF16 ? fwd_bf16(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st)
                                 : fwd_f32(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   ENTRY_CATCH
@@ -488,7 +562,7 @@ cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, bwd_bytes(desc, plan))) != CP_OK) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  ENTRY_CUDA(cudaMemsetAsync(ws, 0, 8, st), "clear the status word");
+  ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
   return desc->dtype == CP_BF16
              ? bwd_bf16(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
                         dw_down, ws, st)

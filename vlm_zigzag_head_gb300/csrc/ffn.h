@@ -34,6 +34,8 @@ enum : int {
   GEMM_DGLU = 2,    // dh = A B^T: dgate, dup and h from the kept gate and up
 };
 
+enum : int { FOLLOWS_NONE = 0, FOLLOWS_A = 1, FOLLOWS_BOTH = 2 };
+
 // C[M][N] = sum over k of A(m, k) B(n, k).  A tile of either operand is loaded from
 // memory where k runs along a row (K-major) or where m (n) does (MN-major).
 struct GemmArgs {
@@ -47,8 +49,12 @@ struct GemmArgs {
   int k_tiles;         // all k tiles
   int k_split;         // k tiles from here on: a[1], b[1] (k_tiles: none)
   int whole;           // tiles of one unit; each tile after them is `shares` units,
-  int shares;          // which share its k and leave their sums in `partial`
+  int shares;          // which share its k and leave their sums in `partial`; the last
+                       // to finish adds them in order and goes on with the epilogue
   float* partial;      // [tile - whole][share][64][256][4]: columns 4 c .. 4 c + 3 of a row
+  int32_t* tickets;    // [tile - whole][8]: shares finished; zero before and after
+  int follows;         // the launch before is of the same call: this one may start while
+                       // it ends (FOLLOWS_A: its weights, B, do not come from there)
   int out_f32;
   int act;
   int keep;            // GEMM_GLU: write gate and up
@@ -66,15 +72,21 @@ inline size_t partial_bytes(int64_t n, int whole, int shares) {
   return (size_t)(n - whole) * shares * kGemmM * kGemmN * sizeof(float);
 }
 
-// What the epilogue would have done with the tiles that are shared, from their sums.
-struct JoinArgs {
-  void* out[2];        // [M][N]; two where m_split < m_tiles
-  void* gate;          // GEMM_GLU: written (nullable), GEMM_DGLU: read; both planes
+// More rows than that (T <= kBatchRows): the same two forms, with tensor maps of the
+// operands, box {64, 128} of the weights (one in the second form), {64, tokens} of x.
+constexpr int kBatchRows = 64;
+struct FfnTokensArgs {
+  CUtensorMap w[2], x;
+  void* out;
+  void* gate;                // kept planes (nullable)
   void* up;
-  void* dgate;         // [M][N]
-  void* dup;
+  int T, N, K;
+  int tokens;                // T, rounded up to a multiple of 16
+  int act;
+  int32_t* status;
+  long long wait_limit;
 };
-cudaError_t launch_gemm_join(const GemmArgs& g, const JoinArgs& j, int epilogue, cudaStream_t st);
+cudaError_t launch_ffn_tokens(const FfnTokensArgs& a, bool glu, int sms, cudaStream_t st);
 
 // fp32: the sums of the shares of a product (partial [splits][M][N]; gate and up:
 // [2][splits][M][N]) and what its epilogue does.  All arrays [M][N] fp32.
@@ -90,6 +102,24 @@ struct F32JoinArgs {
   float* dup;
 };
 cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st);
+
+// Few rows (T <= kFewRows): out [T][N] = act(x w0^T) (x w1^T), or x w0^T with the two
+// halves of each 32 rows of one weight as w0 and w1.  The second form may start while
+// the launch before it, which writes x, still runs.
+constexpr int kFewRows = 8;
+struct FfnRowsArgs {
+  const void* x;             // [T][K] bf16
+  int64_t x_stride;
+  const void* w[2];          // [N][K] bf16
+  int64_t w_stride[2];
+  void* out;
+  void* gate;                // kept planes (nullable)
+  void* up;
+  int T, N, K;
+  int act;
+  int32_t* status;           // cleared by the first form
+};
+cudaError_t launch_ffn_rows(const FfnRowsArgs& a, bool glu, int sms, cudaStream_t st);
 
 // fp32 products on CUDA cores: partial[split][m][n] = sum over the split's k of
 // A(m, k) B(n, k), an element of A at m * sam + k * sak (one of the strides is 1).

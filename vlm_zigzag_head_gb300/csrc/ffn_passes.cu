@@ -1,10 +1,9 @@
-// The gated feed-forward block beside its tensor-core products: what becomes of tiles
-// whose k was shared, and the fp32 products on CUDA cores.
+// The gated feed-forward block in fp32: its products on CUDA cores, and the passes
+// between them.
 #include <cuda_bf16.h>
 
 #include "ffn.h"
 #include "ffn_act.cuh"
-#include "ffn_tiles.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -12,94 +11,6 @@ namespace cpattn {
 namespace {
 
 using namespace ptx;
-
-// A thread has eight columns of one row of a tile (GEMM_GLU: of gate and of up) and
-// adds their shares in order, so the sums do not depend on timing.  Bound by memory:
-// neighbouring threads read neighbouring rows' 16 bytes.
-template <int kEpi>
-__global__ void __launch_bounds__(256)
-    tile_join_kernel(const __grid_constant__ GemmArgs g, const __grid_constant__ JoinArgs j) {
-  constexpr int kTileN = kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN;
-  const TilePlace t = tile_place(g, g.whole + blockIdx.x);
-  const int second = t.m >= g.m_split;
-  const int row = (t.m - (second ? g.m_split : 0)) * kGemmM + threadIdx.x;
-  const int col = t.n * kTileN + blockIdx.y * 8;
-  if (row >= g.M || col >= g.N) return;   // N is a multiple of 8
-  const float4* part = reinterpret_cast<const float4*>(g.partial) +
-                       (int64_t)blockIdx.x * g.shares * (64 * kGemmM) + threadIdx.x;
-  auto sum = [&](int piece, float (&f)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < g.shares; ++s) {
-      const float4 a = part[(s * 64 + piece) * kGemmM], b = part[(s * 64 + piece + 1) * kGemmM];
-      f[0] += a.x;
-      f[1] += a.y;
-      f[2] += a.z;
-      f[3] += a.w;
-      f[4] += b.x;
-      f[5] += b.y;
-      f[6] += b.z;
-      f[7] += b.w;
-    }
-  };
-  const int64_t at = (int64_t)row * g.N + col;
-  auto put = [&](void* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
-        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                   pack_bf16x2(f[6], f[7]));
-  };
-  const int64_t low = kept_low(g.M, g.N) + row * kept_pitch(g.N) + col;
-  float x[8];
-  sum(blockIdx.y * 2, x);
-  if constexpr (kEpi == GEMM_STORE) {
-    if (g.out_f32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(j.out[second]) + at);
-      p[0] = make_float4(x[0], x[1], x[2], x[3]);
-      p[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      put(j.out[second], x);
-    }
-  } else if constexpr (kEpi == GEMM_GLU) {
-    float u[8], h[8], unused;
-    sum(32 + blockIdx.y * 2, u);
-    if (j.gate != nullptr) {
-      auto keep = [&](void* p, const float (&f)[8]) {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + at) =
-            make_uint4(upper_halves(f[0], f[1]), upper_halves(f[2], f[3]),
-                       upper_halves(f[4], f[5]), upper_halves(f[6], f[7]));
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p) + low) =
-            make_uint2(next_bytes(f[0], f[1], f[2], f[3]), next_bytes(f[4], f[5], f[6], f[7]));
-      };
-      keep(j.gate, x);
-      keep(j.up, u);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = activation<false, true>(x[i], g.act, unused) * u[i];
-    put(j.out[0], h);
-  } else {
-    auto kept = [&](const void* p, float (&f)[8]) {
-      const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at);
-      const uint2 l = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p) + low);
-      const uint32_t hi[4] = {v.x, v.y, v.z, v.w}, lo[2] = {l.x, l.y};
-      rejoin8(hi, lo, f);
-    };
-    float gate[8], up[8], h[8];
-    kept(j.gate, gate);
-    kept(j.up, up);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float da;
-      const float a = activation<true, true>(gate[i], g.act, da);
-      h[i] = a * up[i];
-      gate[i] = x[i] * up[i] * da;
-      up[i] = x[i] * a;
-    }
-    put(j.dgate, gate);
-    put(j.dup, up);
-    put(j.out[0], h);
-  }
-}
 
 __device__ __forceinline__ void add4(float4& v, const float4& w) {
   v.x += w.x;
@@ -254,20 +165,11 @@ void share_tail(int64_t n, int k_tiles, int pairs, int* whole, int* shares) {
   *shares = 1;
   const int tail = (int)(n % pairs);
   if (tail == 0) return;
-  // at least four k tiles a share, and twelve saved: joining costs a launch
+  // at least four k tiles a share, and twelve saved: joining costs a few microseconds
   const int s = pairs / tail < k_tiles / 4 ? pairs / tail : k_tiles / 4;
   if (s < 2 || k_tiles - (k_tiles + s - 1) / s < 12) return;
   *whole = (int)(n - tail);
   *shares = s;
-}
-
-cudaError_t launch_gemm_join(const GemmArgs& g, const JoinArgs& j, int epilogue, cudaStream_t st) {
-  const int tail = g.m_tiles * g.n_tiles - g.whole;
-  const dim3 grid((unsigned)tail, epilogue == GEMM_GLU ? 16 : 32);
-  if (epilogue == GEMM_STORE) tile_join_kernel<GEMM_STORE><<<grid, kGemmM, 0, st>>>(g, j);
-  else if (epilogue == GEMM_GLU) tile_join_kernel<GEMM_GLU><<<grid, kGemmM, 0, st>>>(g, j);
-  else tile_join_kernel<GEMM_DGLU><<<grid, kGemmM, 0, st>>>(g, j);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st) {

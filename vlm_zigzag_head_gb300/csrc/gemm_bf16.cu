@@ -28,7 +28,6 @@
 #include "check.cuh"
 #include "ffn.h"
 #include "ffn_act.cuh"
-#include "ffn_tiles.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -73,6 +72,21 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
+// m tiles whose n tiles are walked together: about square patches of tiles run at a
+// time, which reads the least of A and B.
+constexpr int kGroupM = 8;
+
+struct TilePlace {
+  int m, n;
+};
+__device__ __forceinline__ TilePlace tile_place(const GemmArgs& g, int tile) {
+  const unsigned per_group = kGroupM * g.n_tiles;
+  const unsigned group = (unsigned)tile / per_group, in = (unsigned)tile % per_group;
+  const unsigned first = group * kGroupM;
+  const unsigned rows = min(kGroupM, g.m_tiles - (int)first);
+  return {(int)(first + in % rows), (int)(in / rows)};
+}
+
 // Unit u: a tile, and which of its k tiles.  The issuing thread asks for the k tiles
 // alone: between two tiles the tensor core waits for it.
 struct Work {
@@ -85,12 +99,12 @@ __device__ __forceinline__ Work work_at(const GemmArgs& g, int u) {
           (int)(g.k_tiles * (share + 1) / g.shares)};
 }
 struct Unit {
-  int m, n, slot, k0, k1;
+  int tile, m, n, slot, k0, k1;
 };
 __device__ __forceinline__ Unit unit_at(const GemmArgs& g, int u) {
   const Work w = work_at(g, u);
   const TilePlace t = tile_place(g, w.tile);
-  return {t.m, t.n, w.slot, w.k0, w.k1};
+  return {w.tile, t.m, t.n, w.slot, w.k0, w.k1};
 }
 
 __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
@@ -106,6 +120,27 @@ __device__ __forceinline__ void store_partial(const GemmArgs& g, int slot, int c
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+
+// The same columns of all shares of a tile, added in order.
+__device__ __forceinline__ void load_partials(const GemmArgs& g, int tile, int col, int row,
+                                              float (&f)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = 0.f;
+#pragma unroll 2
+  for (int s = 0; s < g.shares; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(g.partial) +
+                      ((int64_t)((tile - g.whole) * g.shares + s) * (kGemmN / 4) + col / 4) * kGemmM +
+                      row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = __ldcg(p + i * kGemmM);   // written by other CTAs of this launch
+      f[4 * i] += v.x;
+      f[4 * i + 1] += v.y;
+      f[4 * i + 2] += v.z;
+      f[4 * i + 3] += v.w;
+    }
+  }
 }
 
 __device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
@@ -171,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int units = g.whole + (g.m_tiles * g.n_tiles - g.whole) * g.shares;
+  griddep_launch_dependents();   // the next product waits for this one where it must
   volatile int* abort = &bars->abort;
   const long long lim = g.wait_limit;
 
@@ -201,44 +237,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      int j = 0;   // k tiles so far, across units
+      auto load_a = [&](const Unit& t, int k, int st) {
+        const bool second = t.m >= g.m_split;
+        const int src = k >= g.k_split, kk = (k - (src ? g.k_split : 0)) * kGemmK;
+        const int m0 = (t.m - (second ? g.m_split : 0)) * kGemmM + rank * kRows;
+        const CUtensorMap* map = &g.a[second || src];
+        uint8_t* dst = smem + st * 2 * kTile;
+        const uint32_t full = in_first_cta(&bars->full[st]);
+        if (!CP_IN_RANGE(m0, 0, g.M + kRows, g.status, 301)) return;
+        if constexpr (kAMN) {
+          for (int i = 0; i < kRows / 64; ++i)
+            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, m0 + i * 64, kk);
+        } else {
+          tma_load_2d_pair(map, full, dst, kk, m0);
+        }
+      };
+      auto load_b = [&](const Unit& t, int k, int st) {
+        const int src = k >= g.k_split, kk = (k - (src ? g.k_split : 0)) * kGemmK;
+        const int n0 = kEpi == GEMM_GLU ? t.n * kRows : t.n * kGemmN + rank * kRows;
+        const CUtensorMap* map = &g.b[kEpi == GEMM_GLU ? rank : src];   // gate or up
+        uint8_t* dst = smem + st * 2 * kTile + kTile;
+        const uint32_t full = in_first_cta(&bars->full[st]);
+        if (!CP_IN_RANGE(n0, 0, g.N + kRows, g.status, 302)) return;
+        if constexpr (kBMN) {
+          for (int i = 0; i < kRows / 64; ++i)
+            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, n0 + i * 64, kk);
+        } else {
+          tma_load_2d_pair(map, full, dst, kk, n0);
+        }
+      };
+      auto expect = [&](int st) {   // both CTAs' parts
+        if (rank == 0) mbar_expect_tx(&bars->full[st], 4 * kTile);
+      };
+      // the first stages' weights need not wait for the launch before
+      int early = 0;
+      if (g.follows == FOLLOWS_A) {
+        const Unit t = unit_at(g, pair);
+        early = min(kStages, t.k1 - t.k0);
+        for (int i = 0; i < early; ++i) {
+          expect(i);
+          load_b(t, t.k0 + i, i);
+        }
+        griddep_wait();
+        for (int i = 0; i < early; ++i) load_a(t, t.k0 + i, i);
+      } else if (g.follows == FOLLOWS_BOTH) {
+        griddep_wait();
+      }
+      int j = early;   // k tiles so far, across units
       for (int u = pair; u < units && !*abort; u += pairs) {
         const Unit t = unit_at(g, u);
-        const bool second = t.m >= g.m_split;
-        const int m0 = (t.m - (second ? g.m_split : 0)) * kGemmM + rank * kRows;
-        const int n0 = kEpi == GEMM_GLU ? t.n * kRows : t.n * kGemmN + rank * kRows;
-        if (!CP_IN_RANGE(m0, 0, g.M + kRows, g.status, 301) ||
-            !CP_IN_RANGE(n0, 0, g.N + kRows, g.status, 302)) {
-          *abort = 1;
-          break;
-        }
-        for (int k = t.k0; k < t.k1; ++k, ++j) {
+        for (int k = t.k0 + (u == pair ? early : 0); k < t.k1; ++k, ++j) {
           const int st = j % kStages;
           if (j >= kStages &&
               !mbar_wait_cluster(&bars->empty[st], ((j / kStages) - 1) & 1, lim, abort)) {
             record_timeout(g.status, abort, 31);
             break;
           }
-          const int src = k >= g.k_split;
-          const int kk = (k - (src ? g.k_split : 0)) * kGemmK;
-          const CUtensorMap* ma = &g.a[second || src];
-          const CUtensorMap* mb = &g.b[kEpi == GEMM_GLU ? rank : src];   // gate or up
-          uint8_t* pa = smem + st * 2 * kTile;
-          uint8_t* pb = pa + kTile;
-          if (rank == 0) mbar_expect_tx(&bars->full[st], 4 * kTile);   // both CTAs' parts
-          const uint32_t full = in_first_cta(&bars->full[st]);
-          if constexpr (kAMN) {
-            for (int i = 0; i < kRows / 64; ++i)
-              tma_load_2d_pair(ma, full, pa + i * 64 * kGemmK * 2, m0 + i * 64, kk);
-          } else {
-            tma_load_2d_pair(ma, full, pa, kk, m0);
-          }
-          if constexpr (kBMN) {
-            for (int i = 0; i < kRows / 64; ++i)
-              tma_load_2d_pair(mb, full, pb + i * 64 * kGemmK * 2, n0 + i * 64, kk);
-          } else {
-            tma_load_2d_pair(mb, full, pb, kk, n0);
-          }
+          expect(st);
+          load_a(t, k, st);
+          load_b(t, k, st);
         }
       }
       // no load may be on its way when the CTA exits (none is once its tiles' epilogues
@@ -325,6 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++fetched;
       }
     };
+    if (g.follows != FOLLOWS_NONE) griddep_wait();
     fetch_first(pair);
     bool ok = true;
     for (int u = pair; ok && u < units; u += pairs, ++n) {
@@ -340,23 +398,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kGemmN;
       const int second = t.m >= g.m_split;
       const int row0 = first_row(t), tile_row = rank * kRows + quarter * 32 + lane;
+      auto release = [&] {   // the next products may overwrite the accumulator
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(in_first_cta(&bars->acc_empty[s]));
+      };
+      const bool shared = t.slot >= 0;
+      if (shared) {
+        const bool in = row0 + lane < g.M;
+#pragma unroll 1
+        for (int c = 0; c < kGemmN / 64; ++c) {
+          const int col = c * 64 + half * 32;
+          float x[32];
+          load_acc(acc + col, x);
+          if (in) store_partial(g, t.slot, col, tile_row, x);
+          __syncwarp();   // the next load of the accumulator is the whole warp's
+        }
+        release();
+        // these two warps' rows of all shares: the last to get here goes on with them
+        __threadfence();
+        pair_sync();
+        bool last = true;
+        if (issues) {
+          int32_t* ticket = g.tickets + (t.tile - g.whole) * 8 + rank * 4 + quarter;
+          last = atomicAdd(ticket, 1) == g.shares - 1;
+          if (last) *ticket = 0;
+          __threadfence();
+        }
+        if (!named_all(pair_bar, 64, last)) continue;
+      }
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         const int col = c * 64 + half * 32, box_col = t.n * kTileN + c * 64;
         const bool stores = row0 < g.M && box_col < g.N;   // the box is not wholly past the end
         float x[32];
-        load_acc(acc + col, x);
+        auto take = [&](int at, float (&f)[32]) {
+          if (!shared) {
+            load_acc(acc + at, f);
+          } else if (row0 + lane < g.M) {
+            load_partials(g, t.tile, at, tile_row, f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = 0.f;
+          }
+        };
+        take(col, x);
         if constexpr (kEpi == GEMM_GLU) {
           float v[32];
-          load_acc(acc + kTileN + col, v);
-          if (t.slot >= 0) {
-            if (row0 + lane < g.M) {
-              store_partial(g, t.slot, col, tile_row, x);
-              store_partial(g, t.slot, kTileN + col, tile_row, v);
-            }
-            __syncwarp();   // the next load of the accumulator is the whole warp's
-            continue;
-          }
+          take(kTileN + col, v);
           if (issues) bulk_wait_read<0>();   // the boxes' last stores have read them
           pair_sync();
           if (g.keep) {
@@ -379,97 +468,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             bulk_commit();
           }
-        } else {
-          if (t.slot >= 0) {
-            if (row0 + lane < g.M) store_partial(g, t.slot, col, tile_row, x);
-            __syncwarp();
-            continue;
+        } else if constexpr (kEpi == GEMM_STORE) {
+          uint8_t* box = boxes + (g.out_f32 ? half : c & 1) * kBf16Box;
+          if (issues) {
+            if (g.out_f32) bulk_wait_read<0>();
+            else bulk_wait_read<1>();
           }
-          if constexpr (kEpi == GEMM_STORE) {
-            uint8_t* box = boxes + (g.out_f32 ? half : c & 1) * kBf16Box;
-            if (issues) {
-              if (g.out_f32) bulk_wait_read<0>();
-              else bulk_wait_read<1>();
-            }
-            pair_sync();
-            if (g.out_f32) put_f32(box, lane, x);
-            else put_bf16(box, lane, half, x);
-            fence_proxy_async_smem();
-            pair_sync();
-            if (issues) {
-              if (stores) tma_store_2d(&g.out[second], box, box_col, row0);
-              if (stores && g.out_f32 && box_col + 32 < g.N)
-                tma_store_2d(&g.out[second], box + kBf16Box, box_col + 32, row0);
-              bulk_commit();   // one group a chunk, so that the count holds
-            }
+          pair_sync();
+          if (g.out_f32) put_f32(box, lane, x);
+          else put_bf16(box, lane, half, x);
+          fence_proxy_async_smem();
+          pair_sync();
+          if (issues) {
+            if (stores) tma_store_2d(&g.out[second], box, box_col, row0);
+            if (stores && g.out_f32 && box_col + 32 < g.N)
+              tma_store_2d(&g.out[second], box + kBf16Box, box_col + 32, row0);
+            bulk_commit();   // one group a chunk, so that the count holds
+          }
+        } else {
+          if (fetched == got) {   // a shared tile's, or the first after one
+            fetch(t, c);
+            ++fetched;
+          }
+          if (!named_all(pair_bar, 64, mbar_wait(&bars->box[quarter], got & 1, lim, abort))) {
+            if (lane == 0) record_timeout(g.status, abort, 34);
+            ok = false;
+            break;
+          }
+          ++got;
+          uint4 kg[4], ku[4], lg[2], lu[2];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            kg[p] = *piece<128>(boxes, lane, half * 4 + p);
+            ku[p] = *piece<128>(boxes + kBf16Box, lane, half * 4 + p);
+          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            lg[p] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + p);
+            lu[p] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + p);
+          }
+          if (issues) bulk_wait_read<0>();   // the last stores have read their boxes
+          pair_sync();   // all have read: the next chunk may land
+          if (c + 1 < kChunks) {
+            fetch(t, c + 1);
+            ++fetched;
           } else {
-            if (!named_all(pair_bar, 64, mbar_wait(&bars->box[quarter], got & 1, lim, abort))) {
-              if (lane == 0) record_timeout(g.status, abort, 34);
-              ok = false;
-              break;
-            }
-            ++got;
-            uint4 kg[4], ku[4], lg[2], lu[2];
+            fetch_first(u + pairs);
+          }
+          uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
+          const uint32_t* wg = reinterpret_cast<const uint32_t*>(kg);
+          const uint32_t* wu = reinterpret_cast<const uint32_t*>(ku);
+          const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
+          const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              kg[p] = *piece<128>(boxes, lane, half * 4 + p);
-              ku[p] = *piece<128>(boxes + kBf16Box, lane, half * 4 + p);
-            }
+          for (int p = 0; p < 4; ++p) {   // eight columns at a time
+            float gate[8], up[8], h[8];
+            rejoin8(wg + 4 * p, bg + 2 * p, gate);
+            rejoin8(wu + 4 * p, bu + 2 * p, up);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              lg[p] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + p);
-              lu[p] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + p);
+            for (int e = 0; e < 8; ++e) {
+              float da;
+              const float a = activation<true, true>(gate[e], g.act, da), dh = x[8 * p + e];
+              h[e] = a * up[e];
+              gate[e] = dh * up[e] * da;
+              up[e] = dh * a;
             }
-            if (issues) bulk_wait_read<0>();   // the last stores have read their boxes
-            pair_sync();   // all have read: the next chunk may land
-            if (c + 1 < kChunks) {
-              fetch(t, c + 1);
-              ++fetched;
-            } else {
-              fetch_first(u + pairs);
-            }
-            uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
-            const uint32_t* wg = reinterpret_cast<const uint32_t*>(kg);
-            const uint32_t* wu = reinterpret_cast<const uint32_t*>(ku);
-            const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
-            const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {   // eight columns at a time
-              float gate[8], up[8], h[8];
-              rejoin8(wg + 4 * p, bg + 2 * p, gate);
-              rejoin8(wu + 4 * p, bu + 2 * p, up);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float da;
-                const float a = activation<true, true>(gate[e], g.act, da), dh = x[8 * p + e];
-                h[e] = a * up[e];
-                gate[e] = dh * up[e] * da;
-                up[e] = dh * a;
-              }
-              auto put = [&](int which, const float (&f)[8]) {
-                *piece<128>(out + which * kBf16Box, lane, half * 4 + p) =
-                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-              };
-              put(0, gate);
-              put(1, up);
-              put(2, h);
-            }
-            fence_proxy_async_smem();
-            pair_sync();
-            if (issues && stores) {
-              tma_store_2d(&g.dgate, out, box_col, row0);
-              tma_store_2d(&g.dup, out + kBf16Box, box_col, row0);
-              tma_store_2d(&g.out[0], out + 2 * kBf16Box, box_col, row0);
-              bulk_commit();
-            }
+            auto put = [&](int which, const float (&f)[8]) {
+              *piece<128>(out + which * kBf16Box, lane, half * 4 + p) =
+                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+            };
+            put(0, gate);
+            put(1, up);
+            put(2, h);
+          }
+          fence_proxy_async_smem();
+          pair_sync();
+          if (issues && stores) {
+            tma_store_2d(&g.dgate, out, box_col, row0);
+            tma_store_2d(&g.dup, out + kBf16Box, box_col, row0);
+            tma_store_2d(&g.out[0], out + 2 * kBf16Box, box_col, row0);
+            bulk_commit();
           }
         }
       }
       if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(in_first_cta(&bars->acc_empty[s]));
+      if (!shared) release();
     }
     if (issues) {
       int zero = 0;   // a load that nobody waited for (after a wait gave up)
@@ -495,8 +579,17 @@ cudaError_t launch_t(const GemmArgs& g, int sms, cudaStream_t st) {
   const int64_t units = g.whole + ((int64_t)g.m_tiles * g.n_tiles - g.whole) * g.shares;
   if (units < 1 || units > 0x3fffffff) return cudaErrorInvalidConfiguration;
   const int64_t pairs = units < sms / 2 ? units : sms / 2;
-  kernel<<<(unsigned)(2 * pairs), kThreads, smem, st>>>(g);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = g.follows != FOLLOWS_NONE ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, g);
 }
 
 }  // namespace
