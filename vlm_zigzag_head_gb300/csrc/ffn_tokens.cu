@@ -12,7 +12,8 @@
 // of the tokens.
 //
 // Warp roles (192 threads): warp 0 TMA producer, warp 1 TMEM allocation and MMAs (one
-// lane each), warps 2..5 epilogue: thread = weight row = TMEM lane, columns = tokens.
+// lane each), warps 2..5 epilogue: thread = weight row = TMEM lane, columns = tokens; then a
+// warp a token.
 #include <cuda_bf16.h>
 
 #include "check.cuh"
@@ -29,20 +30,19 @@ using namespace ptx;
 constexpr int kThreads = 192;
 constexpr int kRows = 128;                       // of a weight in one tile
 constexpr int kWeightTile = kRows * kGemmK * 2;  // bytes
-constexpr int kMaxTokens = kBatchRows;
 constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 constexpr long long kDrainLimit = 1LL << 24;
 constexpr int kResident = 2;                     // CTAs an SM holds
 
-template <bool kGlu>
+template <bool kGlu, int kTokens>
 struct Layout {
   static constexpr int kMats = kGlu ? 2 : 1;
-  static constexpr int kStages = kGlu ? 2 : 4;
-  static constexpr int kStage = kMats * kWeightTile + kMaxTokens * kGemmK * 2;
+  static constexpr int kStages = !kGlu ? 4 : kTokens <= 32 ? 3 : 2;   // as many as two CTAs have
+  static constexpr int kStage = kMats * kWeightTile + kTokens * kGemmK * 2;
   static constexpr int kBars = kStages * kStage;
   static constexpr int kSmem = kBars + 256 + 1024;   // slack for alignment
   // the sums take the stages' place in the end
-  static_assert(kMats * kMaxTokens * kRows * 4 <= kBars, "shared memory budget");
+  static_assert(kMats * kTokens * kRows * 4 <= kBars, "shared memory budget");
   static_assert(kResident * (kSmem + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -59,20 +59,24 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-__device__ __forceinline__ float peer_load(const float* p, int rank) {   // of another CTA
+// 16 bytes of another CTA's shared memory.
+__device__ __forceinline__ float4 peer_load4(const float* p, int rank) {
   uint32_t at;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
-template <bool kGlu>
+template <bool kGlu, int kTokens>
 __global__ void __launch_bounds__(kThreads, kResident)
     ffn_tokens_kernel(const __grid_constant__ FfnTokensArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  using L = Layout<kGlu>;
+  using L = Layout<kGlu, kTokens>;
   constexpr int kStages = L::kStages, kMats = L::kMats;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -83,7 +87,9 @@ __global__ void __launch_bounds__(kThreads, kResident)
   const int k1 = (int)((int64_t)k_tiles * (share + 1) / shares);
   volatile int* abort = &bars->abort;
   const long long lim = a.wait_limit;
-  constexpr uint32_t kCols = kMats * kMaxTokens;
+  // 32, 64 or 128 columns: the second product's begin half way
+  constexpr int kMatCols = kTokens <= 32 ? 32 : 64;
+  constexpr uint32_t kCols = kMats * kMatCols;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
       auto load_weights = [&](int k) {
         const int st = (k - k0) % kStages;
         uint8_t* dst = smem + st * L::kStage;
-        mbar_expect_tx(&bars->full[st], kMats * kWeightTile + a.tokens * kGemmK * 2);
+        mbar_expect_tx(&bars->full[st], kMats * kWeightTile + kTokens * kGemmK * 2);
         if (!CP_IN_RANGE(n0, 0, a.N, a.status, 303)) return;
         for (int m = 0; m < kMats; ++m)
           tma_load_2d(&a.w[m], &bars->full[st], dst + m * kWeightTile, k * kGemmK, n0);
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(kRows, a.tokens, 0, 0);
+      constexpr uint32_t idesc = idesc_bf16(kRows, kTokens, 0, 0);
       bool ok = true;
       for (int k = k0; k < k1; ++k) {
         const int j = k - k0, st = j % kStages;
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
         for (int i = 0; i < kGemmK / 16; ++i)
 #pragma unroll
           for (int m = 0; m < kMats; ++m)
-            mma_bf16(tmem + m * kMaxTokens, sdesc_sw128(pw + m * kWeightTile + i * 32, 16, 1024),
+            mma_bf16(tmem + m * kMatCols, sdesc_sw128(pw + m * kWeightTile + i * 32, 16, 1024),
                      sdesc_sw128(px + i * 32, 16, 1024), idesc, (k > k0 || i > 0) ? 1u : 0u);
         mma_commit(&bars->empty[st]);
       }
@@ -175,29 +181,9 @@ __global__ void __launch_bounds__(kThreads, kResident)
   }
   // ------------------------------------------------------------ epilogue
   float* red = reinterpret_cast<float*>(smem);   // [matrix][token][row]
-  const int quarter = warp & 3, row = quarter * 32 + lane;
+  const int quarter = warp & 3;
   const bool epilogue = warp >= 2;
   bool ok = true;
-  auto finish = [&](int token, float v0, float v1) {
-    const int n = n0 + row;
-    if (n >= a.N) return;
-    const int64_t at = (int64_t)token * a.N + n;
-    if constexpr (kGlu) {
-      float unused;
-      static_cast<__nv_bfloat16*>(a.out)[at] =
-          __float2bfloat16_rn(activation<false, true>(v0, a.act, unused) * v1);
-      if (a.gate != nullptr) {
-        const int64_t low = kept_low(a.T, a.N) + token * kept_pitch(a.N) + n;
-        const uint32_t g = __float_as_uint(v0), u = __float_as_uint(v1);
-        static_cast<uint16_t*>(a.gate)[at] = (uint16_t)(g >> 16);
-        static_cast<uint16_t*>(a.up)[at] = (uint16_t)(u >> 16);
-        static_cast<uint8_t*>(a.gate)[low] = (uint8_t)(g >> 8);
-        static_cast<uint8_t*>(a.up)[low] = (uint8_t)(u >> 8);
-      }
-    } else {
-      static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v0);
-    }
-  };
   if (epilogue) {
     if (!kGlu) griddep_wait();   // nothing is written before the launch before is done
     ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full, 0, lim, abort));
@@ -205,61 +191,88 @@ __global__ void __launch_bounds__(kThreads, kResident)
     tc_fence_after();
     if (ok) {
       const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < a.T; c += 32) {
-        uint32_t v[2][32];
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) tmem_ld32(acc + m * kMaxTokens + c, v[m]);
-        tmem_ld_wait();
+      for (int c = 0; c < kTokens; c += 32)
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) reg_fence32(v[m]);
+        for (int m = 0; m < kMats; ++m) {
+          uint32_t v[32];
+          tmem_ld32(acc + m * kMatCols + c, v);
+          tmem_ld_wait();
+          reg_fence32(v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (c + i >= a.T) continue;
-          if (shares == 1) {
-            finish(c + i, __uint_as_float(v[0][i]), __uint_as_float(v[kMats - 1][i]));
-          } else {
-#pragma unroll
-            for (int m = 0; m < kMats; ++m)
-              red[(m * kMaxTokens + c + i) * kRows + row] = __uint_as_float(v[m][i]);
-          }
+          for (int i = 0; i < 32; ++i)
+            if (c + i < kTokens)
+              red[(m * kTokens + c + i) * kRows + quarter * 32 + lane] = __uint_as_float(v[i]);
         }
-        __syncwarp();   // the next load of the accumulator is the whole warp's
-      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (shares > 1) {
-    cluster_sync();
-    if (epilogue && ok) {   // the CTAs take tokens in turn
-      for (int token = share; token < a.T; token += shares) {
-        float p[8][kMats], v[2] = {0.f, 0.f};
+  if (shares > 1) cluster_sync();
+  if (epilogue && ok) {
+    // a warp has a token, a lane four weight rows; the CTAs of a cluster take turns
+    const int row = lane * 4, n = n0 + row;
+    for (int token = share + shares * quarter; token < a.T; token += shares * 4) {
+      float4 v[2] = {};
+      auto add = [](float4& s, const float4& p) {
+        s.x += p.x;
+        s.y += p.y;
+        s.z += p.z;
+        s.w += p.w;
+      };
+      if (shares == 1) {
+#pragma unroll
+        for (int m = 0; m < kMats; ++m)
+          v[m] = *reinterpret_cast<const float4*>(&red[(m * kTokens + token) * kRows + row]);
+      } else {
+        float4 p[8][kMats];
 #pragma unroll
         for (int c = 0; c < 8; ++c)   // all on their way before the first is added
 #pragma unroll
           for (int m = 0; m < kMats; ++m)
-            p[c][m] = c < shares ? peer_load(&red[(m * kMaxTokens + token) * kRows + row], c) : 0.f;
+            p[c][m] = c < shares ? peer_load4(&red[(m * kTokens + token) * kRows + row], c)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
 #pragma unroll
-          for (int m = 0; m < kMats; ++m) v[m] += p[c][m];
-        finish(token, v[0], v[1]);
+          for (int m = 0; m < kMats; ++m) add(v[m], p[c][m]);
       }
+      if (n >= a.N) continue;   // N is a multiple of 8
+      const int64_t at = (int64_t)token * a.N + n;
+      float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+      if constexpr (kGlu) {
+        const float u[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+        if (a.gate != nullptr) {
+          const int64_t low = kept_low(a.T, a.N) + token * kept_pitch(a.N) + n;
+          auto keep = [&](void* p, const float (&f)[4]) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) =
+                make_uint2(upper_halves(f[0], f[1]), upper_halves(f[2], f[3]));
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + low) =
+                next_bytes(f[0], f[1], f[2], f[3]);
+          };
+          keep(a.gate, o);
+          keep(a.up, u);
+        }
+        float unused;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = activation<false, true>(o[i], a.act, unused) * u[i];
+      }
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
     }
-    __syncwarp();
-    cluster_sync();   // the others have read this CTA's sums
   }
+  __syncwarp();
+  if (shares > 1) cluster_sync();   // the others have read this CTA's sums
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
   }
 }
 
-template <bool kGlu>
-cudaError_t launch(const FfnTokensArgs& a, int sms, cudaStream_t st) {
-  using L = Layout<kGlu>;
-  auto kernel = ffn_tokens_kernel<kGlu>;
+template <bool kGlu, int kTokens>
+cudaError_t launch_t(const FfnTokensArgs& a, int sms, cudaStream_t st) {
+  using L = Layout<kGlu, kTokens>;
+  auto kernel = ffn_tokens_kernel<kGlu, kTokens>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kSmem);
   if (e != cudaSuccess) return e;
@@ -286,11 +299,23 @@ cudaError_t launch(const FfnTokensArgs& a, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <bool kGlu>
+cudaError_t launch(const FfnTokensArgs& a, int sms, cudaStream_t st) {
+  switch (a.tokens) {
+    case 16: return launch_t<kGlu, 16>(a, sms, st);
+    case 32: return launch_t<kGlu, 32>(a, sms, st);
+    case 48: return launch_t<kGlu, 48>(a, sms, st);
+    case 64: return launch_t<kGlu, 64>(a, sms, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
+static_assert(kBatchRows == 64, "the cases above");
+
 cudaError_t launch_ffn_tokens(const FfnTokensArgs& a, bool glu, int sms, cudaStream_t st) {
-  if (a.T < 1 || a.T > a.tokens || a.tokens > kBatchRows || a.tokens % 16 != 0)
-    return cudaErrorInvalidValue;
+  if (a.T < 1 || a.T > a.tokens) return cudaErrorInvalidValue;
   return glu ? launch<true>(a, sms, st) : launch<false>(a, sms, st);
 }
 
