@@ -63,18 +63,6 @@ int sm_count() {
   return sms;
 }
 
-// Shares of k that a product's tiles are cut into: as many as fit the SMs at once,
-// each of at least four k tiles.
-int share_k(int64_t n_tiles, int k_tiles, int at_once) {
-  if (2 * n_tiles > at_once) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(at_once / n_tiles, k_tiles / 4));
-}
-
-constexpr int kF32K = 16;   // the fp32 kernel's k step; 128 x 128 tiles, two blocks an SM
-int share_k_f32(int64_t M, int64_t N, int64_t K, int sms) {
-  return share_k((int64_t)tiles(M, 128) * tiles(N, 128), tiles(K, 4 * kF32K), 2 * sms);
-}
-
 // Forward calls that the kernels for few rows take, and for a batch of them.
 bool few_rows(const cp_gated_ffn_t* p) { return p->dtype == CP_BF16 && p->T <= kFewRows; }
 bool batch_rows(const cp_gated_ffn_t* p) {
@@ -84,11 +72,11 @@ bool batch_rows(const cp_gated_ffn_t* p) {
 // How the bf16 products' last tiles and the fp32 products' k are shared, and what of
 // the workspace that takes.
 struct Share {
-  int whole, shares;
+  int whole, shares;   // fp32: the tile, and the shares
 };
 struct Plan {
   int sms = 0;
-  Share gate_up, down, dh, d_down, d_in, d_both, dx;   // d_both: d_in of both weights at once
+  Share gate_up, down, dh, d_down, d_in, d_both, dx;   // d_in: one weight, d_both: both
   size_t fwd_partial = 0, bwd_partial = 0;   // bytes
 };
 
@@ -115,17 +103,20 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
     return r;
   }
   // gate and up always go through the workspace, and so does dh
-  auto share = [&](int64_t M, int64_t N, int64_t K, int outputs, bool always, size_t* most) {
-    const Share s{0, share_k_f32(M, N, K, sms)};
+  auto share = [&](int64_t M, int64_t N, int64_t K, int outputs, int phases, bool always,
+                   size_t* most) {
+    Share s;
+    share_f32(M, N, K, outputs, phases, sms, &s.whole, &s.shares);
     if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
     return s;
   };
-  r.gate_up = share(T, F, D, 2, true, &r.fwd_partial);
-  r.down = share(T, O, F, 1, false, &r.fwd_partial);
-  r.dh = share(T, F, O, 1, true, &r.bwd_partial);
-  r.dx = share(T, D, F, 2, false, &r.bwd_partial);
-  r.d_down = share(O, F, T, 1, false, &r.bwd_partial);
-  r.d_in = share(F, D, T, 1, false, &r.bwd_partial);
+  r.gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
+  r.down = share(T, O, F, 1, 1, false, &r.fwd_partial);
+  r.dh = share(T, F, O, 1, 1, true, &r.bwd_partial);
+  r.dx = share(T, D, F, 1, 2, false, &r.bwd_partial);
+  r.d_down = share(O, F, T, 1, 1, false, &r.bwd_partial);
+  r.d_in = share(F, D, T, 1, 1, false, &r.bwd_partial);
+  r.d_both = share(F, D, T, 2, 1, false, &r.bwd_partial);
   return r;
 }
 
@@ -368,72 +359,85 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   return CP_OK;
 }
 
-// fp32: out = A B^T over element strides, its shares joined when there are several.
+// fp32 products, their shares joined where there are several.
 struct F32 {
   float* partial;
   cudaStream_t st;
 
-  cp_status_t shares(const void* a, int64_t sam, int64_t sak, const void* b, int64_t sbn,
-                     int64_t sbk, int M, int N, int K, int splits, float* out, bool accumulate,
-                     const char* what) const {
-    GemmF32Args g;
-    g.a = static_cast<const float*>(a);
-    g.b = static_cast<const float*>(b);
-    g.sam = sam;
-    g.sak = sak;
-    g.sbn = sbn;
-    g.sbk = sbk;
+  // The operands' order in memory: A and B row by row along k, or across it.
+  static GemmF32Args args(int M, int N, int K, int64_t a_stride, bool a_mn, int64_t b_stride,
+                          bool b_mn, const Share& s) {
+    GemmF32Args g = {};
     g.M = M;
     g.N = N;
     g.K = K;
-    g.splits = splits;
-    g.accumulate = accumulate;
-    g.out = out;
+    g.sam = a_mn ? 1 : a_stride;
+    g.sak = a_mn ? a_stride : 1;
+    for (int i = 0; i < 2; ++i) {
+      g.sbn[i] = b_mn ? 1 : b_stride;
+      g.sbk[i] = b_mn ? b_stride : 1;
+    }
+    g.outputs = g.phases = 1;
+    g.tile = s.whole;
+    g.splits = s.shares;
+    return g;
+  }
+  static const float* in(const void* p) { return static_cast<const float*>(p); }
+  // to the workspace, as [outputs][splits][M][N]
+  cp_status_t shares(GemmF32Args& g, const char* what) const {
+    g.out[0] = partial;
+    g.out[1] = partial + (int64_t)g.splits * g.M * g.N;
     ENTRY_CUDA(launch_gemm_f32(g, st), what);
     return CP_OK;
   }
-  cp_status_t sum(int splits, int M, int N, void* out, const char* what) const {
-    F32JoinArgs j = {};
-    j.partial = partial;
-    j.splits = splits;
-    j.n = (int64_t)M * N;
-    j.out = static_cast<float*>(out);
-    ENTRY_CUDA(launch_f32_join(j, GEMM_STORE, st), what);
-    return CP_OK;
-  }
-  cp_status_t product(const void* a, int64_t sam, int64_t sak, const void* b, int64_t sbn,
-                      int64_t sbk, int M, int N, int K, int splits, void* out,
-                      const char* what) const {
-    float* to = splits > 1 ? partial : static_cast<float*>(out);
-    cp_status_t e = shares(a, sam, sak, b, sbn, sbk, M, N, K, splits, to, false, what);
-    if (e != CP_OK || splits == 1) return e;
-    return sum(splits, M, N, out, what);
+  cp_status_t run(GemmF32Args& g, void* out0, void* out1, const char* what) const {
+    void* out[2] = {out0, out1};
+    if (g.splits == 1) {
+      for (int i = 0; i < 2; ++i) g.out[i] = static_cast<float*>(out[i]);
+      ENTRY_CUDA(launch_gemm_f32(g, st), what);
+      return CP_OK;
+    }
+    cp_status_t e = shares(g, what);
+    for (int i = 0; i < g.outputs && e == CP_OK; ++i) {
+      F32JoinArgs j = {};
+      j.partial = g.out[i];
+      j.splits = g.splits;
+      j.n = (int64_t)g.M * g.N;
+      j.out = static_cast<float*>(out[i]);
+      ENTRY_CUDA(launch_f32_join(j, GEMM_STORE, st), what);
+    }
+    return e;
   }
 };
 
 cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
                     const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
                     cudaStream_t st) {
-  void* h = ws + header_bytes(plan);
+  float* h = reinterpret_cast<float*>(ws + header_bytes(plan));
   const F32 f{reinterpret_cast<float*>(ws + header_bytes(plan) + hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
-  const int64_t n = (int64_t)T * F;
   cp_status_t e;
-  if ((e = f.shares(x, p->x_stride, 1, wg, p->w_gate_stride, 1, T, F, D, plan.gate_up.shares, f.partial,
-                    false, "gate projection")) != CP_OK ||
-      (e = f.shares(x, p->x_stride, 1, wu, p->w_up_stride, 1, T, F, D, plan.gate_up.shares,
-                    f.partial + plan.gate_up.shares * n, false, "up projection")) != CP_OK)
-    return e;
+  GemmF32Args g = F32::args(T, F, D, p->x_stride, false, p->w_gate_stride, false, plan.gate_up);
+  for (int i = 0; i < 2; ++i) {
+    g.a[i] = F32::in(x);
+    g.b[i] = F32::in(i ? wu : wg);
+  }
+  g.sbn[1] = p->w_up_stride;
+  g.outputs = 2;
+  if ((e = f.shares(g, "gate and up projections")) != CP_OK) return e;
   F32JoinArgs j = {};
   j.partial = f.partial;
-  j.splits = plan.gate_up.shares;
+  j.splits = g.splits;
   j.n = (int64_t)T * F;
-  j.out = static_cast<float*>(h);
+  j.out = h;
   j.act = p->activation;
   j.gate = static_cast<float*>(gate);
   j.up = static_cast<float*>(up);
   ENTRY_CUDA(launch_f32_join(j, GEMM_GLU, st), "activation");
-  return f.product(h, F, 1, wd, p->w_down_stride, 1, T, O, F, plan.down.shares, y, "down projection");
+  g = F32::args(T, O, F, F, false, p->w_down_stride, false, plan.down);
+  g.a[0] = h;
+  g.b[0] = F32::in(wd);
+  return f.run(g, y, nullptr, "down projection");
 }
 
 cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
@@ -441,44 +445,52 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
                     const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
                     cudaStream_t st) {
   uint8_t* at = ws + header_bytes(plan);
-  void *dg = at, *du = at + hidden_bytes(p), *h = at + 2 * hidden_bytes(p);
+  float* dg = reinterpret_cast<float*>(at);
+  float* du = reinterpret_cast<float*>(at + hidden_bytes(p));
+  float* h = reinterpret_cast<float*>(at + 2 * hidden_bytes(p));
   const F32 f{reinterpret_cast<float*>(at + 3 * hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  if ((e = f.shares(dy, p->dy_stride, 1, wd, 1, p->w_down_stride, T, F, O, plan.dh.shares, f.partial,
-                    false, "hidden gradients")) != CP_OK)
-    return e;
+  GemmF32Args g = F32::args(T, F, O, p->dy_stride, false, p->w_down_stride, true, plan.dh);
+  g.a[0] = F32::in(dy);
+  g.b[0] = F32::in(wd);
+  if ((e = f.shares(g, "hidden gradients")) != CP_OK) return e;
   F32JoinArgs j = {};
   j.partial = f.partial;
-  j.splits = plan.dh.shares;
+  j.splits = g.splits;
   j.n = (int64_t)T * F;
-  j.out = static_cast<float*>(h);
+  j.out = h;
   j.act = p->activation;
   j.gate = static_cast<float*>(const_cast<void*>(gate));
   j.up = static_cast<float*>(const_cast<void*>(up));
-  j.dgate = static_cast<float*>(dg);
-  j.dup = static_cast<float*>(du);
+  j.dgate = dg;
+  j.dup = du;
   ENTRY_CUDA(launch_f32_join(j, GEMM_DGLU, st), "activation's gradient");
-  if (dx) {
-    const int s = plan.dx.shares;
-    const int64_t n = (int64_t)T * D;
-    float* to = s > 1 ? f.partial : static_cast<float*>(dx);
-    if ((e = f.shares(dg, F, 1, wg, 1, p->w_gate_stride, T, D, F, s, to, false,
-                      "input gradient")) != CP_OK ||
-        (e = f.shares(du, F, 1, wu, 1, p->w_up_stride, T, D, F, s, s > 1 ? to + s * n : to, s == 1,
-                      "input gradient")) != CP_OK ||
-        (s > 1 && (e = f.sum(2 * s, T, D, dx, "input gradient's sums")) != CP_OK))
-      return e;
+  if (dx) {   // dg Wg + du Wu as one product, k running through both
+    g = F32::args(T, D, F, F, false, p->w_gate_stride, true, plan.dx);
+    g.a[0] = dg;
+    g.a[1] = du;
+    g.b[0] = F32::in(wg);
+    g.b[1] = F32::in(wu);
+    g.sbk[1] = p->w_up_stride;
+    g.phases = 2;
+    if ((e = f.run(g, dx, nullptr, "input gradient")) != CP_OK) return e;
   }
-  if (dwd && (e = f.product(dy, 1, p->dy_stride, h, 1, F, O, F, T, plan.d_down.shares, dwd,
-                            "down weight's gradient")) != CP_OK)
-    return e;
-  if (dwg && (e = f.product(dg, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in.shares, dwg,
-                            "gate weight's gradient")) != CP_OK)
-    return e;
-  if (dwu && (e = f.product(du, 1, F, x, 1, p->x_stride, F, D, T, plan.d_in.shares, dwu,
-                            "up weight's gradient")) != CP_OK)
-    return e;
+  if (dwd) {
+    g = F32::args(O, F, T, p->dy_stride, true, F, true, plan.d_down);
+    g.a[0] = F32::in(dy);
+    g.b[0] = h;
+    if ((e = f.run(g, dwd, nullptr, "down weight's gradient")) != CP_OK) return e;
+  }
+  if (dwg || dwu) {
+    const bool both = dwg && dwu;
+    g = F32::args(F, D, T, F, true, p->x_stride, true, both ? plan.d_both : plan.d_in);
+    g.a[0] = dwg ? dg : du;
+    g.a[1] = du;
+    g.b[0] = g.b[1] = F32::in(x);
+    g.outputs = both ? 2 : 1;
+    if ((e = f.run(g, dwg ? dwg : dwu, dwu, "gate and up weights' gradients")) != CP_OK) return e;
+  }
   return CP_OK;
 }
 

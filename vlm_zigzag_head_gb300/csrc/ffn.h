@@ -121,16 +121,23 @@ struct FfnRowsArgs {
 };
 cudaError_t launch_ffn_rows(const FfnRowsArgs& a, bool glu, int sms, cudaStream_t st);
 
-// fp32 products on CUDA cores: partial[split][m][n] = sum over the split's k of
-// A(m, k) B(n, k), an element of A at m * sam + k * sak (one of the strides is 1).
+// fp32 products on CUDA cores: out[o][share][m][n] = sum over the share's k of
+// A(m, k) B(n, k), an element of A at m * sam + k * sak (one of the strides is 1, the
+// other a multiple of 4, pointers 16-byte aligned).  Two outputs have operands of their
+// own; with two phases k runs through a[0], b[0] and then a[1], b[1].
 struct GemmF32Args {
-  const float *a, *b;
-  int64_t sam, sak, sbn, sbk;
+  const float *a[2], *b[2];
+  int64_t sam, sak;
+  int64_t sbn[2], sbk[2];   // of b[0], b[1]
   int M, N, K;
+  int outputs, phases;   // 1 or 2; not both 2
+  int tile;              // 64 or 128
   int splits;
-  int accumulate;      // add to what is there (splits == 1)
-  float* out;          // [splits][M][N]
+  float* out[2];         // [splits][M][N]
 };
 cudaError_t launch_gemm_f32(const GemmF32Args& g, cudaStream_t st);
+// Tile and shares of k that fill the GPU.
+void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms, int* tile,
+               int* splits);
 
 }  // namespace cpattn

@@ -66,35 +66,59 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
   }
 }
 
-// 128 x 128 tiles, 256 threads of 8 x 8 sums, k by 16 through shared memory; two
-// multiply-adds an instruction.
-constexpr int kTile = 128, kStep = 16, kPitch = kTile + 4;
+// Tiles of 128 x 128 (256 threads) or 64 x 64 (64 threads), 8 x 8 sums a thread, k by
+// 16 through shared memory, two multiply-adds an instruction.  The smaller tile where
+// the larger ones would leave SMs idle (517 x 1360 by 512: 25 us with 110 blocks of the
+// larger, 10 with 792 of the smaller).
+constexpr int kStep = 16;
 
-__global__ void __launch_bounds__(256) gemm_f32_kernel(const __grid_constant__ GemmF32Args g) {
+template <int kTile>
+__global__ void __launch_bounds__(kTile == 128 ? 256 : 64)
+    gemm_f32_kernel(const __grid_constant__ GemmF32Args g) {
+  constexpr int kSide = kTile / 8, kThreads = kSide * kSide, kPitch = kTile + 4;
+  constexpr int kLoads = kTile * kStep / 4 / kThreads;   // 16-byte pieces a thread loads
   __shared__ __align__(16) float as[2][kStep][kPitch], bs[2][kStep][kPitch];
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int tid = threadIdx.x, tx = tid % kSide, ty = tid / kSide;
   const int m0 = blockIdx.x * kTile, n0 = blockIdx.y * kTile;
-  const int steps = (g.K + kStep - 1) / kStep;
-  const int s0 = (int)((int64_t)steps * blockIdx.z / g.splits);
-  const int s1 = (int)((int64_t)steps * (blockIdx.z + 1) / g.splits);
-  float ra[8], rb[8];
-  // eight elements of one operand's tile: neighbouring threads along its contiguous
-  // direction
-  auto load = [&](const float* p, int64_t sr, int64_t sk, int r0, int rows, int k0, float (&r)[8]) {
+  const int output = blockIdx.z / g.splits, share = blockIdx.z % g.splits;
+  const int steps = (g.K + kStep - 1) / kStep, all = steps * g.phases;
+  const int s0 = (int)((int64_t)all * share / g.splits);
+  const int s1 = (int)((int64_t)all * (share + 1) / g.splits);
+  float4 ra[kLoads], rb[kLoads];
+  // pieces of one operand's tile along its contiguous direction; a piece lies wholly
+  // inside the matrix or outside (widths are multiples of 8)
+  auto load = [&](const float* p, int64_t sr, int64_t sk, int r0, int rows, int k0,
+                  float4 (&r)[kLoads]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = tid + i * 256;
-      const int k = sk == 1 ? e % kStep : e / kTile, row = sk == 1 ? e / kStep : e % kTile;
-      r[i] = row < rows - r0 && k0 + k < g.K ? p[(int64_t)(r0 + row) * sr + (int64_t)(k0 + k) * sk] : 0.f;
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = tid + i * kThreads;
+      const int k = sk == 1 ? e % 4 * 4 : e / (kTile / 4);
+      const int row = sk == 1 ? e / 4 : e % (kTile / 4) * 4;
+      r[i] = row < rows - r0 && k0 + k < g.K
+                 ? *reinterpret_cast<const float4*>(p + (int64_t)(r0 + row) * sr +
+                                                    (int64_t)(k0 + k) * sk)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
-  auto store = [&](float (*t)[kPitch], int64_t sk, const float (&r)[8]) {
+  auto store = [&](float (*t)[kPitch], int64_t sk, const float4 (&r)[kLoads]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = tid + i * 256;
-      const int k = sk == 1 ? e % kStep : e / kTile, row = sk == 1 ? e / kStep : e % kTile;
-      t[k][row] = r[i];
+    for (int i = 0; i < kLoads; ++i) {
+      const int e = tid + i * kThreads;
+      if (sk == 1) {
+        const int k = e % 4 * 4, row = e / 4;
+        t[k][row] = r[i].x;
+        t[k + 1][row] = r[i].y;
+        t[k + 2][row] = r[i].z;
+        t[k + 3][row] = r[i].w;
+      } else {
+        *reinterpret_cast<float4*>(&t[e / (kTile / 4)][e % (kTile / 4) * 4]) = r[i];
+      }
     }
+  };
+  auto fetch = [&](int s) {
+    const int phase = s >= steps, k = (s - phase * steps) * kStep, i = output + phase;
+    load(g.a[i], g.sam, g.sak, m0, g.M, k, ra);
+    load(g.b[i], g.sbn[i], g.sbk[i], n0, g.N, k, rb);
   };
   uint64_t acc[8][4];
 #pragma unroll
@@ -102,25 +126,21 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(const __grid_constant__ G
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[i][c] = 0ull;
   if (s0 < s1) {
-    load(g.a, g.sam, g.sak, m0, g.M, s0 * kStep, ra);
-    load(g.b, g.sbn, g.sbk, n0, g.N, s0 * kStep, rb);
+    fetch(s0);
     store(as[0], g.sak, ra);
-    store(bs[0], g.sbk, rb);
+    store(bs[0], g.sbk[0], rb);
   }
   __syncthreads();
   for (int s = s0; s < s1; ++s) {
     const int cur = (s - s0) & 1;
-    if (s + 1 < s1) {
-      load(g.a, g.sam, g.sak, m0, g.M, (s + 1) * kStep, ra);
-      load(g.b, g.sbn, g.sbk, n0, g.N, (s + 1) * kStep, rb);
-    }
+    if (s + 1 < s1) fetch(s + 1);
 #pragma unroll
     for (int k = 0; k < kStep; ++k) {
-      // rows ty * 4 and 64 + ty * 4 on, columns tx * 4 and 64 + tx * 4 on
+      // rows ty * 4 and half a tile further on, columns tx * 4 and half a tile on
       const float4 a0 = *reinterpret_cast<const float4*>(&as[cur][k][ty * 4]);
-      const float4 a1 = *reinterpret_cast<const float4*>(&as[cur][k][64 + ty * 4]);
+      const float4 a1 = *reinterpret_cast<const float4*>(&as[cur][k][kTile / 2 + ty * 4]);
       const ulonglong2 b0 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][tx * 4]);
-      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][64 + tx * 4]);
+      const ulonglong2 b1 = *reinterpret_cast<const ulonglong2*>(&bs[cur][k][kTile / 2 + tx * 4]);
       const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
       const uint64_t bv[4] = {b0.x, b0.y, b1.x, b1.y};
 #pragma unroll
@@ -132,28 +152,23 @@ __global__ void __launch_bounds__(256) gemm_f32_kernel(const __grid_constant__ G
     }
     if (s + 1 < s1) {
       store(as[cur ^ 1], g.sak, ra);
-      store(bs[cur ^ 1], g.sbk, rb);
+      store(bs[cur ^ 1], g.sbk[0], rb);   // both phases' run the same way
     }
     __syncthreads();
   }
-  float* out = g.out + (int64_t)blockIdx.z * g.M * g.N;
+  float* out = g.out[output] + (int64_t)share * g.M * g.N;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int m = m0 + (i / 4) * 64 + ty * 4 + i % 4;
+    const int m = m0 + (i / 4) * (kTile / 2) + ty * 4 + i % 4;
     if (m >= g.M) continue;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const int n = n0 + c * 64 + tx * 4;
-      if (n >= g.N) continue;   // N is a multiple of 4
+      const int n = n0 + c * (kTile / 2) + tx * 4;
+      if (n >= g.N) continue;   // N is a multiple of 8
       float4 v;
       unpack2(acc[i][2 * c], v.x, v.y);
       unpack2(acc[i][2 * c + 1], v.z, v.w);
-      float4* p = reinterpret_cast<float4*>(out + (int64_t)m * g.N + n);
-      if (g.accumulate) {
-        const float4 w = *p;
-        v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-      }
-      *p = v;
+      *reinterpret_cast<float4*>(out + (int64_t)m * g.N + n) = v;
     }
   }
 }
@@ -181,11 +196,27 @@ cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st)
   return cudaGetLastError();
 }
 
+void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms, int* tile,
+               int* splits) {
+  auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + t - 1) / t) * outputs; };
+  *splits = 1;
+  *tile = tiles(128) >= 2 * sms ? 128 : 64;
+  if (*tile == 128) return;
+  // six blocks of 64 threads an SM, of four steps at least
+  const int64_t steps = (K + kStep - 1) / kStep * phases;
+  int64_t s = 6 * (int64_t)sms / tiles(64);
+  if (s > steps / 4) s = steps / 4;
+  if (s > 64) s = 64;
+  if (s > 1) *splits = (int)s;
+}
+
 cudaError_t launch_gemm_f32(const GemmF32Args& g, cudaStream_t st) {
-  const int64_t nt = ((int64_t)g.N + kTile - 1) / kTile;
-  if (nt > 65535 || g.splits > 65535) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(((int64_t)g.M + kTile - 1) / kTile), (unsigned)nt, (unsigned)g.splits);
-  gemm_f32_kernel<<<grid, 256, 0, st>>>(g);
+  const int64_t nt = ((int64_t)g.N + g.tile - 1) / g.tile;
+  if (nt > 65535 || g.splits * g.outputs > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(((int64_t)g.M + g.tile - 1) / g.tile), (unsigned)nt,
+                  (unsigned)(g.splits * g.outputs));
+  if (g.tile == 128) gemm_f32_kernel<128><<<grid, 256, 0, st>>>(g);
+  else gemm_f32_kernel<64><<<grid, 64, 0, st>>>(g);
   return cudaGetLastError();
 }
 
