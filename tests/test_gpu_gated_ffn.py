@@ -85,7 +85,8 @@ CASES = [(1, 64, 128, 64, "bf16", "silu"), (128, 64, 128, 256, "bf16", "silu"), 
          (1000, 512, 1360, 512, "bf16", "silu"), (3000, 64, 2048, 64, "bf16", "silu"),
          (8, 40, 24, 56, "bf16", "gelu"), (9, 2048, 6144, 2048, "bf16", "silu"), (31, 264, 1000, 1032, "bf16", "silu"),
          (33, 136, 520, 72, "bf16", "gelu_tanh"), (64, 512, 1040, 512, "bf16", "gelu"),
-         (65, 512, 1040, 512, "bf16", "gelu"),
+         (65, 512, 1040, 512, "bf16", "gelu"), (100, 2048, 520, 1000, "bf16", "silu"),
+         (127, 264, 4104, 264, "bf16", "gelu_tanh"),
          (2500, 1536, 768, 1280, "bf16", "gelu_tanh"), (5000, 1024, 1280, 1024, "bf16", "silu"),
          (1, 32, 64, 32, "f32", "silu"), (5, 8, 16, 24, "f32", "gelu"), (129, 136, 264, 72, "f32", "gelu_tanh"),
          (300, 256, 512, 256, "f32", "silu"), (17, 512, 1360, 512, "f32", "gelu"),

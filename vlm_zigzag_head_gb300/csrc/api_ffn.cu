@@ -256,7 +256,7 @@ cp_status_t fwd_tokens(const cp_gated_ffn_t* p, const Plan& plan, const void* x,
   a.gate = gate;
   a.up = up;
   a.T = T;
-  a.tokens = (T + 15) / 16 * 16;
+  a.tokens = T <= 64 ? (T + 15) / 16 * 16 : (T + 31) / 32 * 32;
   a.act = p->activation;
   a.status = reinterpret_cast<int32_t*>(ws);
   a.wait_limit = device_wait_limit();

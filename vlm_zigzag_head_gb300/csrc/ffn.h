@@ -74,14 +74,14 @@ inline size_t partial_bytes(int64_t n, int whole, int shares) {
 
 // More rows than that (T <= kBatchRows): the same two forms, with tensor maps of the
 // operands, box {64, 128} of the weights (one in the second form), {64, tokens} of x.
-constexpr int kBatchRows = 64;
+constexpr int kBatchRows = 128;
 struct FfnTokensArgs {
   CUtensorMap w[2], x;
   void* out;
   void* gate;                // kept planes (nullable)
   void* up;
   int T, N, K;
-  int tokens;                // T, rounded up to a multiple of 16
+  int tokens;                // T, rounded up to 16, 32, 48, 64, 96 or 128
   int act;
   int32_t* status;
   long long wait_limit;

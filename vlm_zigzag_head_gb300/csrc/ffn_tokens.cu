@@ -1,4 +1,4 @@
-// The gated feed-forward block for 9 to 64 rows (decoding a batch of requests).
+// The gated feed-forward block for 9 to 128 rows (decoding a batch of requests).
 //
 // Bound by the weights, which are read once: 6 D F bytes in bf16.  They are the M side
 // of the MMAs, 128 rows of a weight (of both projections, so that gate and up of a
@@ -7,7 +7,7 @@
 // take 76 us for 37 tokens, 4096 x 12288, in five launches; here are two, the second's
 // first weights in flight while the first ends.
 //
-// Two CTAs share an SM, and the CTAs of a cluster share k where there are fewer tiles
+// Two CTAs share an SM (up to 64 tokens), and the CTAs of a cluster share k where there are fewer tiles
 // than that; their sums meet in shared memory in a fixed order, each CTA finishing some
 // of the tokens.
 //
@@ -32,12 +32,13 @@ constexpr int kRows = 128;                       // of a weight in one tile
 constexpr int kWeightTile = kRows * kGemmK * 2;  // bytes
 constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 constexpr long long kDrainLimit = 1LL << 24;
-constexpr int kResident = 2;                     // CTAs an SM holds
 
 template <bool kGlu, int kTokens>
 struct Layout {
   static constexpr int kMats = kGlu ? 2 : 1;
-  static constexpr int kStages = !kGlu ? 4 : kTokens <= 32 ? 3 : 2;   // as many as two CTAs have
+  // CTAs an SM holds, and as many stages as they have
+  static constexpr int kResident = kTokens <= 64 ? 2 : 1;
+  static constexpr int kStages = kResident == 1 ? (kGlu ? 4 : 6) : !kGlu ? 4 : kTokens <= 32 ? 3 : 2;
   static constexpr int kStage = kMats * kWeightTile + kTokens * kGemmK * 2;
   static constexpr int kBars = kStages * kStage;
   static constexpr int kSmem = kBars + 256 + 1024;   // slack for alignment
@@ -47,7 +48,7 @@ struct Layout {
 };
 
 struct Bars {
-  uint64_t full[4], empty[4];
+  uint64_t full[6], empty[6];
   uint64_t acc_full;
   uint64_t drain;
   uint32_t tmem_base;
@@ -72,7 +73,7 @@ __device__ __forceinline__ float4 peer_load4(const float* p, int rank) {
 }
 
 template <bool kGlu, int kTokens>
-__global__ void __launch_bounds__(kThreads, kResident)
+__global__ void __launch_bounds__(kThreads, Layout<kGlu, kTokens>::kResident)
     ffn_tokens_kernel(const __grid_constant__ FfnTokensArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -87,8 +88,8 @@ __global__ void __launch_bounds__(kThreads, kResident)
   const int k1 = (int)((int64_t)k_tiles * (share + 1) / shares);
   volatile int* abort = &bars->abort;
   const long long lim = a.wait_limit;
-  // 32, 64 or 128 columns: the second product's begin half way
-  constexpr int kMatCols = kTokens <= 32 ? 32 : 64;
+  // a power of two of columns: the second product's begin half way
+  constexpr int kMatCols = kTokens <= 32 ? 32 : kTokens <= 64 ? 64 : 128;
   constexpr uint32_t kCols = kMats * kMatCols;
 
   if (threadIdx.x == 0) {
@@ -278,7 +279,7 @@ cudaError_t launch_t(const FfnTokensArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int tiles = (a.N + kRows - 1) / kRows, k_tiles = (a.K + kGemmK - 1) / kGemmK;
   // as many shares of k as run at once, of two k tiles or more
-  int shares = kResident * sms / tiles;
+  int shares = L::kResident * sms / tiles;
   if (shares > k_tiles / 2) shares = k_tiles / 2;
   if (shares > 8) shares = 8;
   if (shares < 1) shares = 1;
@@ -306,13 +307,15 @@ cudaError_t launch(const FfnTokensArgs& a, int sms, cudaStream_t st) {
     case 32: return launch_t<kGlu, 32>(a, sms, st);
     case 48: return launch_t<kGlu, 48>(a, sms, st);
     case 64: return launch_t<kGlu, 64>(a, sms, st);
+    case 96: return launch_t<kGlu, 96>(a, sms, st);
+    case 128: return launch_t<kGlu, 128>(a, sms, st);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-static_assert(kBatchRows == 64, "the cases above");
+static_assert(kBatchRows == 128, "the cases above");
 
 cudaError_t launch_ffn_tokens(const FfnTokensArgs& a, bool glu, int sms, cudaStream_t st) {
   if (a.T < 1 || a.T > a.tokens) return cudaErrorInvalidValue;
