@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
       squares = warp_sum(lane_cols > 0.f ? fmaf(lane_cols * d, d, v.y) : 0.f);
       slot ^= 1;   // the next pass writes the other slot: one barrier a pass
     }
-    const float r = rsqrtf(squares * a.inv_D + a.eps);
+    const float r = __frsqrt_rn(squares * a.inv_D + a.eps);
     if (row < a.T) {
       T* dst = static_cast<T*>(a.y) + row * a.D;
       const uint64_t m2 = pack2(-mean, -mean), r2 = pack2(r, r);

@@ -44,7 +44,7 @@ void rope_fill_angles(const Desc* p, const int32_t* pos, RopeAngles* a) {
   for (int i = 0; i < 64; ++i) a->freq[i] = 0;
   for (int i = 0; i < p->rot_dim / 2; ++i) {
     const double turns = p->inv_freq[i] / 6.283185307179586476925;
-    const double frac = std::ldexp(turns - std::floor(turns), 64);
+    const double frac = (turns - std::floor(turns)) * 18446744073709551616.0;   // exact
     a->freq[i] = frac < 18446744073709551616.0 ? (uint64_t)frac : 0;
   }
 }

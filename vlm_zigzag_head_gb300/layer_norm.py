@@ -47,7 +47,8 @@ def _prepare(x, weight, bias, eps, dy=None):
     for w in (weight, bias):
         if w is None:
             continue
-        if w.shape != x.shape[1:] or w.device != x.device or not w.is_contiguous():
+        if w.dim() != 1 or w.shape[0] != x.shape[1] or w.device != x.device or \
+                not w.is_contiguous():
             raise CpError(2, "weight and bias must be contiguous [D] tensors on x's device")
         w_dtype = _dt(w)
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
@@ -66,18 +67,20 @@ def cp_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5):
     Returns ``(y, mean, rstd)``: y contiguous; mean and rstd fp32, one per row, for
     :func:`cp_layer_norm_bwd`."""
     rows = _rows(x, "x")
-    y, mean, rstd = _launch_fwd(_prepare(rows, weight, bias, eps), rows, weight, bias, x.shape)
-    return y, mean.view(x.shape[:-1]), rstd.view(x.shape[:-1])
+    return _launch_fwd(_prepare(rows, weight, bias, eps), rows, weight, bias, x.shape)
 
 
-def _launch_fwd(f, rows, weight, bias, shape):
+def _launch_fwd(f, rows, weight, bias, shape, stats=True):
     device = rows.device
     y = torch.empty(shape, dtype=rows.dtype, device=device)
-    mean, rstd = torch.empty((2, f.T), dtype=torch.float32, device=device)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty_like(mean)
     with _on_device(device):
         _b.check(_b.lib().cp_layer_norm_fwd(
-            f, rows.data_ptr(), _at(weight), _at(bias), y.data_ptr(), mean.data_ptr(),
-            rstd.data_ptr(), _raw_stream(device)))
+            f, rows.data_ptr(), _at(weight), _at(bias), y.data_ptr(), _at(mean), _at(rstd),
+            _raw_stream(device)))
     return y, mean, rstd
 
 
