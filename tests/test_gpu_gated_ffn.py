@@ -83,7 +83,7 @@ CASES = [(1, 64, 128, 64, "bf16", "silu"), (128, 64, 128, 256, "bf16", "silu"), 
          (257, 520, 1032, 264, "bf16", "silu"), (37, 1024, 2816, 1024, "bf16", "gelu_tanh"),
          (3, 2048, 512, 1000, "bf16", "silu"), (16, 264, 4104, 264, "bf16", "gelu"),
          (1000, 512, 1360, 512, "bf16", "silu"), (3000, 64, 2048, 64, "bf16", "silu"),
-         (8, 40, 24, 56, "bf16", "gelu"), (9, 2048, 6144, 2048, "bf16", "silu"), (31, 264, 1000, 1032, "bf16", "silu"),
+         (8, 40, 24, 56, "bf16", "gelu"), (20, 8, 16, 24, "bf16", "silu"), (9, 2048, 6144, 2048, "bf16", "silu"), (31, 264, 1000, 1032, "bf16", "silu"),
          (33, 136, 520, 72, "bf16", "gelu_tanh"), (64, 512, 1040, 512, "bf16", "gelu"),
          (65, 512, 1040, 512, "bf16", "gelu"), (100, 2048, 520, 1000, "bf16", "silu"),
          (127, 264, 4104, 264, "bf16", "gelu_tanh"),

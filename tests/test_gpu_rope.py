@@ -175,6 +175,11 @@ def test_frequencies():
     assert np.allclose(np.array(p)[turns <= 1], np.array(base)[turns <= 1] / 8, rtol=1e-15)
     assert all(f / 8 <= v <= f * (1 + 1e-12) for f, v in zip(base, p))
     assert cp.rope_frequencies(0) == ()
+    from vlm_zigzag_head_gb300 import rope
+    odd = (np.float32(1.0), 2, np.float64(0.5)) + (0.25,) * 29      # entries of any kind of number
+    f = rope._desc(1, (1, 1, 64), (64, 64, 1), (1, 1, 64), (64, 64, 1), (1,), 1e4, None, None, False,
+                   rope.Frequencies(float(x) for x in odd), 1.0, False)
+    assert [f.inv_freq[i] for i in range(4)] == [1.0, 2.0, 0.5, 0.25]
     for bad in (dict(rot_dim=7), dict(rot_dim=64, scaling="cubic"), dict(rot_dim=64, factor=0.0),
                 dict(rot_dim=64, theta=-1.0), dict(rot_dim=2, scaling="base", factor=2.0),
                 dict(rot_dim=64, scaling="by_parts", low=2.0, high=2.0)):

@@ -188,7 +188,8 @@ def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, theta: fl
     gradients flow to q and k (backward only: forward mode raises).  To capture the backward
     into a graph, call :func:`~vlm_zigzag_head_gb300.cp_rope_bwd`, which involves no leaves."""
     options = (theta, rot_dim, None if sections is None else tuple(sections), interleaved,
-               None if inv_freq is None else tuple(inv_freq), amplitude)
+               inv_freq if inv_freq is None else _rope.Frequencies(float(f) for f in inv_freq),
+               amplitude)
     desc = _rope._prepare(q, k, positions, *options)
     if not _wants_grad(q, k):
         return _rope._launch(_b.lib().cp_rope_fwd, desc, q, k, positions)

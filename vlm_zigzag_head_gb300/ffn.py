@@ -118,6 +118,8 @@ def cp_gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, dy, activation: str = "s
     """Gradient of :func:`cp_gated_ffn_fwd` (``gate``, ``up``: what it kept): ``(dx, dw_gate,
     dw_up, dw_down)``, None where ``wanted`` says so.  dx has x's dtype; the weights'
     gradients have ``grad_dtype``: fp32, or bf16 for bf16 inputs."""
+    if len(wanted) != 4:
+        raise CpError(2, "wanted must say yes or no to dx, dw_gate, dw_up and dw_down")
     rows, g = _rows(x, "x"), _rows(dy, "dy")
     f, sizes = _prepare(rows, w_gate, w_up, w_down, activation,
                         _dt(torch.empty(0, dtype=grad_dtype)), g)

@@ -17,6 +17,11 @@ from . import CpError, _binding as _b, _dt
 from .norm_rope import _check_heads, _on_device, _raw_stream
 
 
+class Frequencies(tuple):
+    """Floats, one a rotated pair: what :func:`rope_frequencies` returns (a call takes them as
+    they are, where it converts each entry of another sequence)."""
+
+
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, *, scaling: str = "none",
                      factor: float = 1.0, trained_length: int = 8192, low: float = 1.0,
                      high: float = 32.0) -> Tuple[float, ...]:
@@ -55,7 +60,7 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, *, scaling: str = "no
         freq = out
     elif scaling not in ("none", "base"):
         raise CpError(1, "scaling must be none, linear, base or by_parts")
-    return tuple(freq)
+    return Frequencies(freq)
 
 
 @functools.lru_cache(maxsize=256)
@@ -145,8 +150,8 @@ def _prepare(q, k, positions, theta, rot_dim, sections, interleaved, inv_freq, a
     f = _desc(_dt(q), tuple(q.shape), q.stride(), tuple(k.shape), k.stride(),
               tuple(positions.shape), float(theta), rot_dim,
               None if sections is None else tuple(int(n) for n in sections), bool(interleaved),
-              inv_freq if inv_freq is None or type(inv_freq) is tuple else
-              tuple(float(x) for x in inv_freq), float(amplitude), bool(inplace))
+              inv_freq if inv_freq is None or type(inv_freq) is Frequencies else
+              Frequencies(float(x) for x in inv_freq), float(amplitude), bool(inplace))
     if inplace and f.T > 0 and not _disjoint(q, k):
         raise CpError(1, "q and k share memory: not in place")
     return f
