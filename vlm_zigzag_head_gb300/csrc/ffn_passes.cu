@@ -67,13 +67,15 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
 }
 
 // Tiles of 128 x 128 (256 threads) or 64 x 64 (64 threads), 8 x 8 sums a thread, k by
-// 16 through shared memory, two multiply-adds an instruction.  The smaller tile where
-// the larger ones would leave SMs idle (517 x 1360 by 512: 25 us with 110 blocks of the
-// larger, 10 with 792 of the smaller).
+// 16 through shared memory, two multiply-adds an instruction.  Bound by the loads from
+// shared memory, whose 64 bytes a thread and k take as long as its 64 multiply-adds: 45
+// to 52 TFLOP/s with the larger tile, 38 to 45 with the smaller (a library's 57 to 64).
+// The smaller one where the larger would leave SMs idle (two products 517 x 1360 by
+// 512: 45 us; the larger tile's 110 blocks took 60).
 constexpr int kStep = 16;
 
 template <int kTile>
-__global__ void __launch_bounds__(kTile == 128 ? 256 : 64)
+__global__ void __launch_bounds__(kTile == 128 ? 256 : 64, kTile == 128 ? 2 : 8)
     gemm_f32_kernel(const __grid_constant__ GemmF32Args g) {
   constexpr int kSide = kTile / 8, kThreads = kSide * kSide, kPitch = kTile + 4;
   constexpr int kLoads = kTile * kStep / 4 / kThreads;   // 16-byte pieces a thread loads
@@ -202,9 +204,9 @@ void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms
   *splits = 1;
   *tile = tiles(128) >= 2 * sms ? 128 : 64;
   if (*tile == 128) return;
-  // six blocks of 64 threads an SM, of four steps at least
+  // eight blocks of 64 threads an SM, of four steps at least
   const int64_t steps = (K + kStep - 1) / kStep * phases;
-  int64_t s = 6 * (int64_t)sms / tiles(64);
+  int64_t s = 8 * (int64_t)sms / tiles(64);
   if (s > steps / 4) s = steps / 4;
   if (s > 64) s = 64;
   if (s > 1) *splits = (int)s;
