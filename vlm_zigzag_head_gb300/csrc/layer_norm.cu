@@ -186,14 +186,31 @@ __device__ __forceinline__ uint64_t inside(uint64_t v, int t, int i, int j, int 
   }
 }
 
+constexpr int kMinThreads = 256;   // of a block whose rows take fewer
+
+// The next row's pieces are copied asynchronously into shared memory by the thread that
+// will use them (so no barrier) while it works on a row: forward 186 us with them held
+// in registers, 183 so (131072 x 2048, bf16; fp32 x 1000 169 and 159), backward 275 and
+// 243, as the registers go to the sums.  More rows ahead gained nothing.
+constexpr int block_threads(int tpr) { return tpr > kMinThreads ? tpr : kMinThreads; }
+__device__ __forceinline__ void copy_async(uint4* dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(in ? 16 : 0)   // zeros past the row
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copy_wait() {   // all rows but the last are there
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-constexpr int kMinThreads = 256;   // of a block whose rows take fewer
-constexpr int block_threads(int tpr) { return tpr > kMinThreads ? tpr : kMinThreads; }
 
 // Persistent blocks: a group of TPR threads takes rows gridDim.x * G apart with its
 // columns' weights in registers (read per row they were twice the traffic of bf16
@@ -226,18 +243,43 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
   const float lane_cols = kWarps > 1 && lane < kWarps ? (float)columns_of(lane) : 0.f;
   uint64_t w[NV][E2], b[NV][E2];
   uint4 raw[NV];
-  auto load = [&](int64_t row) {
-    const T* src = static_cast<const T*>(a.x) + row * a.x_stride;
-    if (row < a.T) {
+  extern __shared__ uint4 ring[];   // [2][NV][threads]
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + grp;
+  int stage = 0;   // of the row to be taken
+  auto stage_at = [&](int s, int i) {
+    return ring + (s * NV + i) * block_threads(TPR) + threadIdx.x;
+  };
+  auto load = [&](int64_t r, int to) {
+    const T* src = static_cast<const T*>(a.x) + r * a.x_stride;
+    if constexpr (kVec) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) raw[i] = load_piece<T, TPR, kVec>(src, t, i, a.D);
+      for (int i = 0; i < NV; ++i) {
+        const int c = column<T, TPR, true>(t, i, 0);
+        if (r < a.T) copy_async(stage_at(to, i), src + (c < a.D ? c : 0), c < a.D);
+      }
+      copy_commit();
+    } else if (r < a.T) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) raw[i] = load_piece<T, TPR, false>(src, t, i, a.D);
     }
+  };
+  // the row's pieces, and the loads of one to come
+  auto take = [&](uint64_t (&x)[NV][E2]) {
+    if constexpr (kVec) {
+      load(row + step, stage ^ 1);
+      copy_wait();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) raw[i] = *stage_at(stage, i);
+      stage ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) widen<T>(raw[i], x[i]);
+    if constexpr (!kVec) load(row + step, 0);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-  const int64_t step = (int64_t)gridDim.x * G;
-  int64_t row = (int64_t)blockIdx.x * G + grp;
-  load(row);
+  load(row, 0);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     load_weights<T, TPR, kVec>(a.w, a.w_bf16, 1.f, t, i, a.D, w[i]);
@@ -250,13 +292,11 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
        first += step, row += step) {
     uint64_t x[NV][E2];
     uint64_t s2 = 0ull;
+    take(x);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      widen<T>(raw[i], x[i]);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < E2; ++j) s2 = add2(s2, x[i][j]);
-    }
-    load(row + step);
     float mean = warp_sum(sum2(s2)) * inv_mine;
     const uint64_t neg = pack2(-mean, -mean);
     uint64_t ss = 0ull;
@@ -298,6 +338,13 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
   }
 }
 
+// bf16 rows of one block of 512 threads come through registers all the same: 282 us for
+// 32768 x 8192, 394 through shared memory (fp32, half the elements a thread: 32768 x 4096
+// 268 and 252).  The widest rows leave no room.
+constexpr bool bwd_ring(int tpr, int elem, bool vec) {
+  return vec && (tpr <= 256 || (tpr == 512 && elem == 4));
+}
+
 // kWide (rows of more than 1024 threads' 8 elements): sums of dw and db in shared
 // memory and no row read ahead, so that a thread's row fits 64 registers.
 template <typename T, int TPR, int NV, bool kVec, bool kWide, int kBlocks>
@@ -309,33 +356,48 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
   constexpr int kWarps = TPR / 32;         // of one row
   constexpr int kCols = TPR * NV * E;
   constexpr int kHeld = kWide ? 1 : NV;
-  extern __shared__ float acc[];           // kWide: [2][kCols]; else [G][2][kCols] at the end
+  extern __shared__ __align__(16) float acc[];   // kWide: [2][kCols]; else [G][2][kCols] at the end
   __shared__ float2 red[2][G][kWarps];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   const int warp = t >> 5, lane = threadIdx.x & 31;
   uint64_t dw[kHeld][E2], db[kHeld][E2], w[kHeld][E2];
   uint4 rx[NV], rd[NV];
   float mean = 0.f, r = 0.f;
-  auto load = [&](int64_t row) {
-    if (row < a.T) {
-      const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-      const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        rx[i] = load_piece<T, TPR, kVec>(x, t, i, a.D);
-        rd[i] = load_piece<T, TPR, kVec>(dy, t, i, a.D);
-      }
-      mean = a.mean[row];
-      r = a.rstd[row];
-    } else {   // a group without a row in the last pass adds nothing
-#pragma unroll
-      for (int i = 0; i < NV; ++i) rx[i] = rd[i] = make_uint4(0, 0, 0, 0);
-      mean = r = 0.f;
-    }
-  };
+  constexpr bool kRing = bwd_ring(TPR, sizeof(T), kVec);   // else rows come straight into registers
+  uint4* ring = reinterpret_cast<uint4*>(acc);   // [2][x, dy][NV][threads]
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t row = (int64_t)blockIdx.x * G + grp;
-  if constexpr (!kWide) load(row);
+  int stage = 0;
+  auto stage_at = [&](int s, int which, int i) {
+    return ring + ((s * 2 + which) * NV + i) * kThreads + threadIdx.x;
+  };
+  auto load = [&](int64_t q, int to) {
+    const T* x = static_cast<const T*>(a.x) + q * a.x_stride;
+    const T* dy = static_cast<const T*>(a.dy) + q * a.dy_stride;
+    if constexpr (kRing) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = column<T, TPR, true>(t, i, 0);
+        if (q < a.T) {
+          copy_async(stage_at(to, 0, i), x + (c < a.D ? c : 0), c < a.D);
+          copy_async(stage_at(to, 1, i), dy + (c < a.D ? c : 0), c < a.D);
+        }
+      }
+      copy_commit();
+    } else {   // a group without a row in the last pass adds nothing
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        rx[i] = q < a.T ? load_piece<T, TPR, kVec>(x, t, i, a.D) : make_uint4(0, 0, 0, 0);
+        rd[i] = q < a.T ? load_piece<T, TPR, kVec>(dy, t, i, a.D) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto load_stats = [&](int64_t q) {
+    mean = q < a.T ? a.mean[q] : 0.f;
+    r = q < a.T ? a.rstd[q] : 0.f;
+  };
+  if constexpr (!kWide) load(row, 0);
+  load_stats(row);
   if constexpr (kWide) {
     for (int c = threadIdx.x; c < 2 * kCols; c += kThreads) acc[c] = 0.f;
     __syncthreads();
@@ -349,7 +411,18 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
   }
   int slot = 0;
   for (int64_t first = (int64_t)blockIdx.x * G; first < a.T; first += step, row += step) {
-    if constexpr (kWide) load(row);
+    if constexpr (kWide) load(row, 0);
+    if constexpr (kRing) {
+      load(row + step, stage ^ 1);
+      copy_wait();
+      const bool in = row < a.T;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        rx[i] = in ? *stage_at(stage, 0, i) : make_uint4(0, 0, 0, 0);
+        rd[i] = in ? *stage_at(stage, 1, i) : make_uint4(0, 0, 0, 0);
+      }
+      stage ^= 1;
+    }
     uint64_t s1 = 0ull, s2 = 0ull;
     uint64_t n[kHeld][E2], g[kHeld][E2];
     const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
@@ -389,7 +462,8 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
       }
     }
     const float rc = r;
-    if constexpr (!kWide) load(row + step);   // in flight during the sums
+    if constexpr (!kWide && !kRing) load(row + step, 0);   // in flight during the sums
+    load_stats(row + step);
     float c1 = warp_sum(sum2(s1)), c2 = warp_sum(sum2(s2));
     if constexpr (kWarps > 1) {
       if (lane == 0) red[slot][grp][warp] = make_float2(c1, c2);
@@ -451,6 +525,8 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
         }
       }
   } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();   // the ring's place is free
     float* own = acc + grp * 2 * kCols;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -535,13 +611,27 @@ int blocks_of(const Shape& s, int64_t T, int sms) {
   return (int)(need < most ? need : most);
 }
 
+constexpr int ring_bytes(const Shape& s, int arrays) {
+  return 2 * arrays * s.nv * block_threads(s.tpr) * 16;
+}
+
+// 48 KB are there unasked, static ones among them.
+template <typename F>
+cudaError_t more_shared(F kernel, int bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <typename T, bool kVec>
 cudaError_t fwd_t(const LayerNormArgs& a, int sms, cudaStream_t st) {
   return by_shape(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
     constexpr Shape s = sizeof(T) == 2 ? kFwdShapes[decltype(i)::value]
                                        : kFwdShapesF32[decltype(i)::value];
-    layer_norm_fwd_kernel<T, s.tpr, s.nv, kVec, s.blocks>
-        <<<blocks_of(s, a.T, sms), block_threads(s.tpr), 0, st>>>(a);
+    auto kernel = layer_norm_fwd_kernel<T, s.tpr, s.nv, kVec, s.blocks>;
+    constexpr int smem = kVec ? ring_bytes(s, 1) : 0;
+    cudaError_t e = more_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks_of(s, a.T, sms), block_threads(s.tpr), smem, st>>>(a);
     return cudaGetLastError();
   });
 }
@@ -552,13 +642,12 @@ cudaError_t bwd_t(const LayerNormArgs& a, int blocks, cudaStream_t st) {
     constexpr Shape s = kBwdShapes[decltype(i)::value];
     constexpr bool kWide = decltype(i)::value >= kBwdWideFrom;
     constexpr int kThreads = block_threads(s.tpr), G = kThreads / s.tpr;
-    constexpr int smem = (kWide || G > 1) ? G * 2 * s.tpr * s.nv * kPiece<T> * 4 : 0;
+    constexpr int sums = (kWide || G > 1) ? G * 2 * s.tpr * s.nv * kPiece<T> * 4 : 0;
+    constexpr int ring = bwd_ring(s.tpr, sizeof(T), kVec) ? ring_bytes(s, 2) : 0;
+    constexpr int smem = sums > ring ? sums : ring;
     auto kernel = layer_norm_bwd_kernel<T, s.tpr, s.nv, kVec, kWide, s.blocks>;
-    if (smem > 48 * 1024) {
-      cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-    }
+    cudaError_t e = more_shared(kernel, smem);
+    if (e != cudaSuccess) return e;
     kernel<<<(unsigned)blocks, kThreads, smem, st>>>(a);
     return cudaGetLastError();
   });
