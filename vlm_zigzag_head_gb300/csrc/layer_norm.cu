@@ -173,19 +173,6 @@ __device__ __forceinline__ void load_weights(const void* w, bool bf16, float non
   for (int j = 0; j < E / 2; ++j) f[j] = pack2(v[2 * j], v[2 * j + 1]);
 }
 
-// A pair with zeros in place of elements past the row (all other values kept).
-template <typename T, int TPR, bool kVec>
-__device__ __forceinline__ uint64_t inside(uint64_t v, int t, int i, int j, int D) {
-  if constexpr (kVec) {
-    return column<T, TPR, true>(t, i, 0) < D ? v : 0ull;
-  } else {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(column<T, TPR, false>(t, i, 2 * j) < D ? a : 0.f,
-                 column<T, TPR, false>(t, i, 2 * j + 1) < D ? b : 0.f);
-  }
-}
-
 constexpr int kMinThreads = 256;   // of a block whose rows take fewer
 
 // The next row's pieces are copied asynchronously into shared memory by the thread that
@@ -304,8 +291,17 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < E2; ++j) {
-        const uint64_t d = inside<T, TPR, kVec>(add2(x[i][j], neg), t, i, j, a.D);
-        ss = fma2(d, d, ss);
+        const uint64_t d = add2(x[i][j], neg);
+        if constexpr (kVec) {   // elements past the row have no square
+          if (column<T, TPR, true>(t, i, 0) < a.D) ss = fma2(d, d, ss);
+        } else {
+          float p, q;
+          unpack2(d, p, q);
+          p = column<T, TPR, false>(t, i, 2 * j) < a.D ? p : 0.f;
+          q = column<T, TPR, false>(t, i, 2 * j + 1) < a.D ? q : 0.f;
+          const uint64_t e = pack2(p, q);
+          ss = fma2(e, e, ss);
+        }
       }
     float squares = warp_sum(sum2(ss));
     if constexpr (kWarps > 1) {
@@ -434,8 +430,8 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
       widen<T>(rd[i], d);
 #pragma unroll
       for (int j = 0; j < E2; ++j) {
-        ni[j] = inside<T, TPR, kVec>(mul2(add2(ni[j], m2), r2), t, i, j, a.D);
-        gi[j] = mul2(d[j], wi[j]);   // past the row: zeros
+        ni[j] = mul2(add2(ni[j], m2), r2);
+        gi[j] = mul2(d[j], wi[j]);   // past the row: zeros, in all sums
         if (!sums) continue;
         s1 = add2(s1, gi[j]);
         s2 = fma2(gi[j], ni[j], s2);
