@@ -192,9 +192,11 @@ __device__ __forceinline__ void copy_wait() {   // all rows but the last are the
   asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
+// Sum over each kLanes neighbouring lanes.
+template <int kLanes = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
   };
   const int mine = columns_of(warp);
   const float inv_mine = mine > 0 ? 1.f / (float)mine : 0.f;
-  const float lane_cols = kWarps > 1 && lane < kWarps ? (float)columns_of(lane) : 0.f;
+  const float lane_cols = kWarps > 1 ? (float)columns_of(lane % kWarps) : 0.f;
   uint64_t w[NV][E2], b[NV][E2];
   uint4 raw[NV];
   extern __shared__ uint4 ring[];   // [2][NV][threads]
@@ -307,12 +309,12 @@ __global__ void __launch_bounds__(block_threads(TPR), kBlocks)
     if constexpr (kWarps > 1) {
       if (lane == 0) red[slot][grp][warp] = make_float2(mean, squares);
       __syncthreads();
-      // lane i has warp i's: the mean of all, then the squares about that (each
+      // a lane has a warp's: the mean of all, then the squares about that (each
       // thread adding all warps' from shared memory measured 3 to 15 % slower)
-      const float2 v = lane < kWarps ? red[slot][grp][lane] : make_float2(0.f, 0.f);
-      mean = warp_sum(v.x * lane_cols) * a.inv_D;
+      const float2 v = red[slot][grp][lane % kWarps];
+      mean = warp_sum<kWarps>(v.x * lane_cols) * a.inv_D;
       const float d = v.x - mean;
-      squares = warp_sum(lane_cols > 0.f ? fmaf(lane_cols * d, d, v.y) : 0.f);
+      squares = warp_sum<kWarps>(lane_cols > 0.f ? fmaf(lane_cols * d, d, v.y) : 0.f);
       slot ^= 1;   // the next pass writes the other slot: one barrier a pass
     }
     const float r = __frsqrt_rn(squares * a.inv_D + a.eps);
