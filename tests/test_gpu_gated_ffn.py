@@ -254,6 +254,32 @@ def test_large_and_tiny_values():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gates_far_out(act, dtype):
+    """Where the activation is 0 or the identity: gates of both signs up to 1e30 give y = u or 0, and
+    gradients that are finite and exact to their roundings."""
+    import vlm_zigzag_head_gb300 as cp
+    D = F = Do = 8
+    for T in (4, 20, 150):
+        x = torch.zeros(T, D, device=DEV)
+        size = torch.logspace(2, 30, T, device=DEV)
+        x[:, 0] = torch.where(torch.arange(T, device=DEV) % 2 == 0, size, -size)   # the gates
+        x[:, 1] = 1.0
+        wg, wu, wd = (torch.zeros(s, device=DEV) for s in ((F, D), (F, D), (Do, F)))
+        wg[0, 0], wu[0, 1], wd[3, 0] = 1.0, 2.0, 1.0
+        x, wg, wu, wd = (t.to(dtype) for t in (x, wg, wu, wd))
+        dy = torch.ones(T, Do, dtype=dtype, device=DEV)
+        y, g, u = cp.cp_gated_ffn_fwd(x, wg, wu, wd, act, keep=True)
+        dx = cp.cp_gated_ffn_bwd(x, wg, wu, wd, g, u, dy, act)[0]
+        gate = to64(x)[:, 0]
+        step = 2 * 2.0 ** (-8 if dtype == torch.bfloat16 else -24)     # h and the result rounded
+        assert np.all(np.abs(to64(y)[:, 3] - 2 * np.maximum(gate, 0)) <= step * np.abs(2 * gate) * (gate > 0))
+        assert np.all(np.abs(to64(dx)[:, 0] - 2 * (gate > 0)) <= 2 * step)
+        assert np.all(np.abs(to64(dx)[:, 1] - 2 * np.maximum(gate, 0)) <= step * np.abs(2 * gate) * (gate > 0))
+
+
+@pytest.mark.gpu
 def test_waits_that_run_out_are_reported():
     """A bounded wait cut to one polling round gives up; the status says so and the next call is exact."""
     cp, x, wg, wu, wd, dy, y, gate, up = _call(8, 600, 512, 1024, 512)

@@ -61,7 +61,8 @@ __device__ __forceinline__ float activation(float g, int act, float& da) {
     constexpr float k = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     const float g2 = g * g;
     s = sigmoid(k * g * fmaf(0.044715f, g2, 1.f));
-    slope = k * fmaf(0.134145f, g2, 1.f);
+    // far out the slope's factor is 0, and an infinite slope would make it NaN
+    slope = k * fmaf(0.134145f, fminf(g2, 1e6f), 1.f);
   }
   const float a = g * s;
   if constexpr (kDerivative) da = fmaf(a - a * s, slope, s);

@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, Layout<kGlu, kTokens>::kResident)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16(kRows, kTokens, 0, 0);
+      // its waits are bounded, and the launch before may take longer than the bound
+      if (!kGlu) griddep_wait();
       bool ok = true;
       for (int k = k0; k < k1; ++k) {
         const int j = k - k0, st = j % kStages;

@@ -312,6 +312,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int j = 0, n = 0;   // k tiles and units so far
       Work t = work_at(g, pair), next = t;
+      // its waits are bounded, and the launch before may take longer than the bound
+      if (g.follows != FOLLOWS_NONE) griddep_wait();
       for (int u = pair; ok && u < units; u += pairs, ++n, t = next) {
         if (u + pairs < units) next = work_at(g, u + pairs);
         const int s = n & 1;
