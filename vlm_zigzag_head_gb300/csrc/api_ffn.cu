@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/cpattn.h"
@@ -57,7 +58,9 @@ cp_status_t check_ptr(const void* p, const char* name) {
 
 int sm_count() {
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
+  // a thread that has not used the device yet (autograd's, say) has no context until it is
+  // set, and tensor maps cannot be made without one
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return sms;
@@ -69,15 +72,65 @@ bool batch_rows(const cp_gated_ffn_t* p) {
   return p->dtype == CP_BF16 && p->T > kFewRows && p->T <= kBatchRows;
 }
 
-// How the bf16 products' last tiles and the fp32 products' k are shared, and what of
-// the workspace that takes.
+// A launch of bf16 products: the width of its tiles and how it is cut into units.  Wide
+// tiles are quicker per product (backward of 4096 rows, 2048 -> 5504, 375 and 594 us),
+// narrow ones where wide ones are too few for the GPU (700 rows, 320 -> 1664, 31 and 23).
+struct Launch {
+  int n = 0, tile_n = 256;
+  GemmCut cut[kGemmProblems] = {};
+  size_t partial = 0;   // bytes
+  bool shared() const { return partial > 0; }
+};
+struct Shape {
+  int64_t M, N;
+  int k_tiles, outputs;
+};
+Launch plan_launch(std::initializer_list<Shape> products, int epilogue, int pairs) {
+  Launch best;
+  double least = 0;
+  for (int tile_n : {256, 128}) {
+    Launch l;
+    l.tile_n = tile_n;
+    for (const Shape& p : products) {
+      if (p.outputs == 0) continue;
+      l.cut[l.n].tiles = (int64_t)p.outputs * tiles(p.M, kGemmM) *
+                         tiles(p.N, epilogue == GEMM_GLU ? tile_n / 2 : tile_n);
+      l.cut[l.n++].k_tiles = p.k_tiles;
+    }
+    const double t = cut_products(l.cut, l.n, pairs, tile_n, epilogue);
+    for (int i = 0; i < l.n; ++i) l.partial += partial_bytes(l.cut[i], tile_n);
+    if (tile_n == 256 || t < least) {
+      best = l;
+      least = t;
+    }
+  }
+  return best;
+}
+
+// The products of a backward pass behind the hidden gradients, those with the longest k
+// first: dx [T][D], k through both weights; `in` weights' gradients [F][D]; that of the
+// down weight [D_out][F].  One launch: alone, each leaves most pairs of CTAs idle in its
+// last round of tiles (the whole pass, 2000 rows, 512 -> 1360, 55 -> 35 us; 2000 rows,
+// 1024 -> 2816, 95 -> 79; 18688 rows, 2048 -> 8192, 2345 -> 2285).
+bool dx_first(const cp_gated_ffn_t* p) { return 2 * tiles(p->F, kGemmK) >= tiles(p->T, kGemmK); }
+Launch plan_gradients(const cp_gated_ffn_t* p, int pairs, bool dx, int in, bool down) {
+  const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
+  const int k_dx = 2 * tiles(F, kGemmK), k = tiles(T, kGemmK);
+  const bool first = dx_first(p);
+  return plan_launch({{T, D, k_dx, dx && first}, {F, D, k, in}, {O, F, k, down},
+                      {T, D, k_dx, dx && !first}},
+                     GEMM_STORE, pairs);
+}
+
 struct Share {
-  int whole, shares;   // fp32: the tile, and the shares
+  int tile, shares;
 };
 struct Plan {
   int sms = 0;
-  Share gate_up, down, dh, d_down, d_in, d_both, dx;   // d_in: one weight, d_both: both
-  size_t fwd_partial = 0, bwd_partial = 0;   // bytes
+  Launch gate_up, down, dh;                                 // bf16
+  Share f32_gate_up, f32_down, f32_dh, d_down, d_in, d_both, dx;   // fp32; d_in: one weight
+  size_t fwd_partial = 0, bwd_partial = 0;                  // bytes
+  int pairs() const { return sms / 2; }
 };
 
 Plan make_plan(const cp_gated_ffn_t* p, int sms) {
@@ -86,33 +139,28 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
   if (sms < 2) return r;
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
   if (p->dtype == CP_BF16) {
-    auto share = [&](int64_t M, int64_t N, int tile_n, int k_tiles, int outputs, size_t* most) {
-      const int64_t n = (int64_t)outputs * tiles(M, kGemmM) * tiles(N, tile_n);
-      Share s;
-      share_tail(n, k_tiles, sms / 2, &s.whole, &s.shares);
-      *most = std::max(*most, s.shares > 1 ? partial_bytes(n, s.whole, s.shares) : 0);
-      return s;
-    };
-    r.gate_up = share(T, F, kGemmN / 2, tiles(D, kGemmK), 1, &r.fwd_partial);
-    r.down = share(T, O, kGemmN, tiles(F, kGemmK), 1, &r.fwd_partial);
-    r.dh = share(T, F, kGemmN, tiles(O, kGemmK), 1, &r.bwd_partial);
-    r.dx = share(T, D, kGemmN, 2 * tiles(F, kGemmK), 1, &r.bwd_partial);
-    r.d_down = share(O, F, kGemmN, tiles(T, kGemmK), 1, &r.bwd_partial);
-    r.d_in = share(F, D, kGemmN, tiles(T, kGemmK), 1, &r.bwd_partial);
-    r.d_both = share(F, D, kGemmN, tiles(T, kGemmK), 2, &r.bwd_partial);
+    r.gate_up = plan_launch({{T, F, tiles(D, kGemmK), 1}}, GEMM_GLU, r.pairs());
+    r.down = plan_launch({{T, O, tiles(F, kGemmK), 1}}, GEMM_STORE, r.pairs());
+    r.dh = plan_launch({{T, F, tiles(O, kGemmK), 1}}, GEMM_DGLU, r.pairs());
+    r.fwd_partial = std::max(r.gate_up.partial, r.down.partial);
+    r.bwd_partial = r.dh.partial;
+    for (int which = 1; which < 12; ++which)   // whichever gradients are wanted
+      r.bwd_partial = std::max(
+          r.bwd_partial,
+          plan_gradients(p, r.pairs(), which & 1, which >> 2, (which >> 1) & 1).partial);
     return r;
   }
   // gate and up always go through the workspace, and so does dh
   auto share = [&](int64_t M, int64_t N, int64_t K, int outputs, int phases, bool always,
                    size_t* most) {
     Share s;
-    share_f32(M, N, K, outputs, phases, sms, &s.whole, &s.shares);
+    share_f32(M, N, K, outputs, phases, sms, &s.tile, &s.shares);
     if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
     return s;
   };
-  r.gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
-  r.down = share(T, O, F, 1, 1, false, &r.fwd_partial);
-  r.dh = share(T, F, O, 1, 1, true, &r.bwd_partial);
+  r.f32_gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
+  r.f32_down = share(T, O, F, 1, 1, false, &r.fwd_partial);
+  r.f32_dh = share(T, F, O, 1, 1, true, &r.bwd_partial);
   r.dx = share(T, D, F, 1, 2, false, &r.bwd_partial);
   r.d_down = share(O, F, T, 1, 1, false, &r.bwd_partial);
   r.d_in = share(F, D, T, 1, 1, false, &r.bwd_partial);
@@ -157,66 +205,90 @@ bool make_map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows, con
   return make_tmap_matrix(m, x.p, x.rows, x.cols, stride, elem, cols, rows, err);
 }
 
-// A product under construction; failures stick.
-struct Product {
+// A launch of products under construction; failures stick.  What is set belongs to the
+// product added last.
+struct Products {
   GemmArgs g = {};
+  const Launch& plan;
   int epilogue;
-  bool a_mn, b_mn;
+  GemmProblem* p = nullptr;
+  int64_t units = 0;
+  int slots = 0, shared = 0;
   const char* err = nullptr;
 
-  Product(int epi, bool amn, bool bmn, int M, int N, Share s, int follows, uint8_t* ws,
-          void* partial)
-      : epilogue(epi), a_mn(amn), b_mn(bmn) {
-    g.M = M;
-    g.N = N;
-    g.m_tiles = g.m_split = tiles(M, kGemmM);
-    g.n_tiles = tiles(N, epi == GEMM_GLU ? kGemmN / 2 : kGemmN);
-    g.whole = s.whole;
-    g.shares = s.shares;
+  Products(int epi, const Launch& l, int follows, uint8_t* ws, void* partial)
+      : plan(l), epilogue(epi) {
     g.partial = static_cast<float*>(partial);
     g.follows = follows;
     g.status = reinterpret_cast<int32_t*>(ws);
     g.tickets = reinterpret_cast<int32_t*>(ws + kTicketsAt);
     g.wait_limit = device_wait_limit();
   }
+  void add(int M, int N, bool a_mn, bool b_mn, int64_t K) {
+    const GemmCut& c = plan.cut[g.problems];
+    p = &g.p[g.problems++];
+    p->M = M;
+    p->N = N;
+    p->a_mn = a_mn;
+    p->b_mn = b_mn;
+    p->m_tiles = p->m_split = tiles(M, kGemmM);
+    p->n_tiles = tiles(N, epilogue == GEMM_GLU ? plan.tile_n / 2 : plan.tile_n);
+    p->k_split = p->k_tiles = tiles(K, kGemmK);
+    p->first = (int)units;
+    p->whole = (int)c.whole;
+    p->shares = c.shares;
+    p->first_slot = slots;
+    p->first_ticket = shared;
+    const int cut = (int)(c.tiles - c.whole);
+    units += c.whole + (int64_t)cut * c.shares;
+    slots += cut * c.shares;
+    shared += cut;
+  }
   void map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows) {
     const char* e = nullptr;
     if (!make_map(m, x, elem, cols, rows, &e) && !err) err = e;
   }
-  void a(int i, const Matrix& m) { map(&g.a[i], m, 2, kGemmK, a_mn ? 64 : kGemmM / 2); }
-  void b(int i, const Matrix& m) { map(&g.b[i], m, 2, kGemmK, b_mn ? 64 : kGemmN / 2); }
-  void k(int64_t K, int phases = 1) {
-    g.k_split = tiles(K, kGemmK);
-    g.k_tiles = phases * g.k_split;
+  void a(int i, const Matrix& m) { map(&p->a[i], m, 2, kGemmK, p->a_mn ? 64 : kGemmM / 2); }
+  void b(int i, const Matrix& m) { map(&p->b[i], m, 2, kGemmK, p->b_mn ? 64 : plan.tile_n / 2); }
+  void box(CUtensorMap* m, void* at, int elem, int64_t stride) {   // what an epilogue moves
+    map(m, {at, p->M, p->N, stride}, elem, elem == 4 ? 32 : 64, 32);
   }
-  void box(CUtensorMap* m, void* p, int elem, int64_t stride) {   // what an epilogue moves
-    map(m, {p, g.M, g.N, stride}, elem, elem == 4 ? 32 : 64, 32);
-  }
-  void out(int i, void* p, bool f32 = false) {
-    g.out_f32 = f32;
-    box(&g.out[i], p, f32 ? 4 : 2, g.N);
+  void out(int i, void* at, bool f32 = false) {
+    p->out_f32 = f32;
+    box(&p->out[i], at, f32 ? 4 : 2, p->N);
   }
   void kept(void* gate, void* up) {
     g.keep = gate != nullptr;
     if (!gate) return;
     for (int i = 0; i < 2; ++i) {
-      uint8_t* p = static_cast<uint8_t*>(i ? up : gate);
+      uint8_t* at = static_cast<uint8_t*>(i ? up : gate);
       CUtensorMap* m = i ? g.up : g.gate;
-      box(&m[0], p, 2, g.N);
-      map(&m[1], {p + kept_low(g.M, g.N), g.M, g.N, kept_pitch(g.N)}, 1, 64, 32);
+      box(&m[0], at, 2, p->N);
+      map(&m[1], {at + kept_low(p->M, p->N), p->M, p->N, kept_pitch(p->N)}, 1, 64, 32);
     }
   }
   void gradients(void* dgate, void* dup) {
-    box(&g.dgate, dgate, 2, g.N);
-    box(&g.dup, dup, 2, g.N);
+    box(&g.dgate, dgate, 2, p->N);
+    box(&g.dup, dup, 2, p->N);
   }
 
-  cp_status_t run(const Plan& plan, cudaStream_t st, const char* what) {
+  cp_status_t run(int sms, cudaStream_t st, const char* what) {
     if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
-    ENTRY_CUDA(launch_gemm_bf16(g, epilogue, a_mn, b_mn, plan.sms, st), what);
+    if (units >= (int64_t)1 << 30) return entry_fail(CP_ERR_SHAPE, "too many tiles");
+    g.units = (int)units;
+    ENTRY_CUDA(launch_gemm_bf16(g, epilogue, plan.tile_n, sms, st), what);
     return CP_OK;
   }
 };
+
+// The header is cleared by the call's first launch itself where that shares no tiles.
+cp_status_t clear_header(const Plan& plan, Products& first, uint8_t* ws, cudaStream_t st) {
+  if (first.plan.shared())
+    ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
+  else
+    first.g.clear = (int)(header_bytes(plan) / 4);
+  return CP_OK;
+}
 
 cp_status_t fwd_rows(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
                      const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
@@ -287,21 +359,22 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   void* partial = ws + header_bytes(plan) + hidden_bytes(p);
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  Product gu(GEMM_GLU, false, false, T, F, plan.gate_up, FOLLOWS_NONE, ws, partial);
+  Products gu(GEMM_GLU, plan.gate_up, FOLLOWS_NONE, ws, partial);
+  gu.add(T, F, false, false, D);
   gu.a(0, {x, T, D, p->x_stride});
   gu.b(0, {wg, F, D, p->w_gate_stride});
   gu.b(1, {wu, F, D, p->w_up_stride});
-  gu.k(D);
   gu.out(0, h);
   gu.g.act = p->activation;
   gu.kept(gate, up);
-  if ((e = gu.run(plan, st, "gate and up projections")) != CP_OK) return e;
-  Product down(GEMM_STORE, false, false, T, O, plan.down, FOLLOWS_A, ws, partial);
+  if ((e = clear_header(plan, gu, ws, st)) != CP_OK) return e;
+  if ((e = gu.run(plan.sms, st, "gate and up projections")) != CP_OK) return e;
+  Products down(GEMM_STORE, plan.down, FOLLOWS_A, ws, partial);
+  down.add(T, O, false, false, F);
   down.a(0, {h, T, F, F});
   down.b(0, {wd, O, F, p->w_down_stride});
-  down.k(F);
   down.out(0, y);
-  return down.run(plan, st, "down projection");
+  return down.run(plan.sms, st, "down projection");
 }
 
 cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
@@ -314,49 +387,49 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   const bool wide = p->grad_dtype == CP_F32;
   cp_status_t e;
-  Product dh(GEMM_DGLU, false, true, T, F, plan.dh, FOLLOWS_NONE, ws, partial);
+  Products dh(GEMM_DGLU, plan.dh, FOLLOWS_NONE, ws, partial);
+  dh.add(T, F, false, true, O);
   dh.a(0, {dy, T, O, p->dy_stride});
   dh.b(0, {wd, O, F, p->w_down_stride});
-  dh.k(O);
   dh.out(0, h);
   dh.g.act = p->activation;
   dh.kept(const_cast<void*>(gate), const_cast<void*>(up));
   dh.gradients(dg, du);
-  if ((e = dh.run(plan, st, "hidden gradients")) != CP_OK) return e;
-  if (dx) {   // dg Wg + du Wu as one product, k running through both
-    Product q(GEMM_STORE, false, true, T, D, plan.dx, FOLLOWS_A, ws, partial);
+  if ((e = clear_header(plan, dh, ws, st)) != CP_OK) return e;
+  if ((e = dh.run(plan.sms, st, "hidden gradients")) != CP_OK) return e;
+
+  const int in = (dwg != nullptr) + (dwu != nullptr);
+  const Launch rest = plan_gradients(p, plan.pairs(), dx, in, dwd);
+  Products q(GEMM_STORE, rest, dx && !in && !dwd ? FOLLOWS_A : FOLLOWS_BOTH, ws, partial);
+  auto input = [&] {   // dg Wg + du Wu as one product, k running through both
+    q.add(T, D, false, true, F);
+    q.p->k_tiles *= 2;
     q.a(0, {dg, T, F, F});
     q.a(1, {du, T, F, F});
     q.b(0, {wg, F, D, p->w_gate_stride});
     q.b(1, {wu, F, D, p->w_up_stride});
-    q.k(F, 2);
     q.out(0, dx);
-    if ((e = q.run(plan, st, "input gradient")) != CP_OK) return e;
-  }
-  if (dwd) {
-    Product q(GEMM_STORE, true, true, O, F, plan.d_down, FOLLOWS_BOTH, ws, partial);
-    q.a(0, {dy, T, O, p->dy_stride});
-    q.b(0, {h, T, F, F});
-    q.k(T);
-    q.out(0, dwd, wide);
-    if ((e = q.run(plan, st, "down weight's gradient")) != CP_OK) return e;
-  }
-  if (dwg || dwu) {   // both as one product, m running through both
-    const bool both = dwg && dwu;
-    Product q(GEMM_STORE, true, true, F, D, both ? plan.d_both : plan.d_in, FOLLOWS_BOTH, ws,
-              partial);
+  };
+  if (dx && dx_first(p)) input();
+  if (in) {   // both weights as one product, m running through both
+    q.add(F, D, true, true, T);
     q.a(0, {dwg ? dg : du, T, F, F});
     q.out(0, dwg ? dwg : dwu, wide);
-    if (both) {
+    if (in == 2) {
       q.a(1, {du, T, F, F});
       q.out(1, dwu, wide);
-      q.g.m_tiles *= 2;
+      q.p->m_tiles *= 2;
     }
     q.b(0, {x, T, D, p->x_stride});
-    q.k(T);
-    if ((e = q.run(plan, st, "gate and up weights' gradients")) != CP_OK) return e;
   }
-  return CP_OK;
+  if (dwd) {
+    q.add(O, F, true, true, T);
+    q.a(0, {dy, T, O, p->dy_stride});
+    q.b(0, {h, T, F, F});
+    q.out(0, dwd, wide);
+  }
+  if (dx && !dx_first(p)) input();
+  return q.run(plan.sms, st, "gradients");
 }
 
 // fp32 products, their shares joined where there are several.
@@ -378,7 +451,7 @@ struct F32 {
       g.sbk[i] = b_mn ? b_stride : 1;
     }
     g.outputs = g.phases = 1;
-    g.tile = s.whole;
+    g.tile = s.tile;
     g.splits = s.shares;
     return g;
   }
@@ -417,7 +490,7 @@ cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   const F32 f{reinterpret_cast<float*>(ws + header_bytes(plan) + hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  GemmF32Args g = F32::args(T, F, D, p->x_stride, false, p->w_gate_stride, false, plan.gate_up);
+  GemmF32Args g = F32::args(T, F, D, p->x_stride, false, p->w_gate_stride, false, plan.f32_gate_up);
   for (int i = 0; i < 2; ++i) {
     g.a[i] = F32::in(x);
     g.b[i] = F32::in(i ? wu : wg);
@@ -434,7 +507,7 @@ cp_status_t fwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   j.gate = static_cast<float*>(gate);
   j.up = static_cast<float*>(up);
   ENTRY_CUDA(launch_f32_join(j, GEMM_GLU, st), "activation");
-  g = F32::args(T, O, F, F, false, p->w_down_stride, false, plan.down);
+  g = F32::args(T, O, F, F, false, p->w_down_stride, false, plan.f32_down);
   g.a[0] = h;
   g.b[0] = F32::in(wd);
   return f.run(g, y, nullptr, "down projection");
@@ -451,7 +524,7 @@ cp_status_t bwd_f32(const cp_gated_ffn_t* p, const Plan& plan, const void* x, co
   const F32 f{reinterpret_cast<float*>(at + 3 * hidden_bytes(p)), st};
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  GemmF32Args g = F32::args(T, F, O, p->dy_stride, false, p->w_down_stride, true, plan.dh);
+  GemmF32Args g = F32::args(T, F, O, p->dy_stride, false, p->w_down_stride, true, plan.f32_dh);
   g.a[0] = F32::in(dy);
   g.b[0] = F32::in(wd);
   if ((e = f.shares(g, "hidden gradients")) != CP_OK) return e;
@@ -537,10 +610,11 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (few_rows(desc))
     return fwd_rows(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
+  if (desc->dtype == CP_BF16 && !batch_rows(desc))
+    return fwd_bf16(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
-  if (batch_rows(desc)) return fwd_tokens(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
-  return desc->dtype == CP_BF16 ? fwd_bf16(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st)
-                                : fwd_f32(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
+  return batch_rows(desc) ? fwd_tokens(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st)
+                          : fwd_f32(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   ENTRY_CATCH
 }
 
@@ -574,12 +648,12 @@ cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, bwd_bytes(desc, plan))) != CP_OK) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (desc->dtype == CP_BF16)
+    return bwd_bf16(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up, dw_down,
+                    ws, st);
   ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
-  return desc->dtype == CP_BF16
-             ? bwd_bf16(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
-                        dw_down, ws, st)
-             : bwd_f32(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
-                       dw_down, ws, st);
+  return bwd_f32(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up, dw_down, ws,
+                 st);
   ENTRY_CATCH
 }
 

@@ -23,14 +23,15 @@ inline __host__ __device__ int64_t kept_pitch(int64_t N) { return (N + 15) / 16 
 inline __host__ __device__ int64_t kept_low(int64_t M, int64_t N) { return M * N * 2; }  // bytes
 inline int64_t kept_bytes(int64_t M, int64_t N) { return kept_low(M, N) + M * kept_pitch(N); }
 
-// Tile of a CTA pair and k step; an epilogue moves boxes of 32 rows and 64 columns (fp32:
-// 32).
-constexpr int kGemmM = 256, kGemmN = 256, kGemmK = 64;
+// Tile of a CTA pair (kGemmM x tile_n, 256 or 128) and k step; an epilogue moves boxes of
+// 32 rows and 64 columns (fp32: 32).
+constexpr int kGemmM = 256, kGemmK = 64;
 
 // What becomes of a tile of products.
 enum : int {
   GEMM_STORE = 0,   // out = A B^T
-  GEMM_GLU = 1,     // two products, gate and up: out = act(gate) up (and both kept)
+  GEMM_GLU = 1,     // two products, gate and up, tile_n / 2 columns of each: out = act(gate)
+                    // up (and both kept)
   GEMM_DGLU = 2,    // dh = A B^T: dgate, dup and h from the kept gate and up
 };
 
@@ -38,38 +39,56 @@ enum : int { FOLLOWS_NONE = 0, FOLLOWS_A = 1, FOLLOWS_BOTH = 2 };
 
 // C[M][N] = sum over k of A(m, k) B(n, k).  A tile of either operand is loaded from
 // memory where k runs along a row (K-major) or where m (n) does (MN-major).
-struct GemmArgs {
-  CUtensorMap a[2], b[2];      // box {64, 128} K-major, {64, 64} MN-major
+struct GemmProblem {
+  CUtensorMap a[2], b[2];      // box {64, 128} (b: {64, tile_n / 2}) K-major, {64, 64} MN-major
   CUtensorMap out[2];          // box {64, 32} bf16, {32, 32} fp32
-  CUtensorMap gate[2], up[2];  // the kept planes, box {64, 32}
-  CUtensorMap dgate, dup;      // GEMM_DGLU: written; h goes to out[0]
+  int a_mn, b_mn;      // MN-major (GEMM_GLU: neither; GEMM_DGLU: B alone)
   int M, N;            // of one output
   int m_tiles, n_tiles;
   int m_split;         // m tiles from here on: a[1], out[1] (m_tiles: none)
   int k_tiles;         // all k tiles
   int k_split;         // k tiles from here on: a[1], b[1] (k_tiles: none)
+  int out_f32;
+  int first;           // number of its first unit in the launch
   int whole;           // tiles of one unit; each tile after them is `shares` units,
   int shares;          // which share its k and leave their sums in `partial`; the last
                        // to finish adds them in order and goes on with the epilogue
-  float* partial;      // [tile - whole][share][64][256][4]: columns 4 c .. 4 c + 3 of a row
-  int32_t* tickets;    // [tile - whole][8]: shares finished; zero before and after
+  int first_slot, first_ticket;   // of its shared tiles
+};
+constexpr int kGemmProblems = 3;
+struct GemmArgs {
+  GemmProblem p[kGemmProblems];   // GEMM_STORE: one to three, their units one after another
+  int problems;
+  int units;           // of all problems, below 2^30
+  CUtensorMap gate[2], up[2];  // the kept planes, box {64, 32}
+  CUtensorMap dgate, dup;      // GEMM_DGLU: written; h goes to out[0]
+  float* partial;      // [slot][tile_n / 4][256][4]: columns 4 c .. 4 c + 3
+  int32_t* tickets;    // [shared tile][8]: shares finished; zero before and after
   int follows;         // the launch before is of the same call: this one may start while
                        // it ends (FOLLOWS_A: its weights, B, do not come from there)
-  int out_f32;
+  int clear;           // words from `status` on, cleared at the start (no shared tiles)
   int act;
   int keep;            // GEMM_GLU: write gate and up
   int32_t* status;
   long long wait_limit;
 };
-// a_mn, b_mn: the operand is MN-major (GEMM_GLU: neither; GEMM_DGLU: B alone).
-cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, bool a_mn, bool b_mn, int sms,
+cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, int tile_n, int sms,
                              cudaStream_t st);
 
-// How many of n tiles run as one unit each, and the shares of the others: the last
-// tiles, too few for all pairs of CTAs at once, are cut along k where that saves time.
-void share_tail(int64_t n, int k_tiles, int pairs, int* whole, int* shares);
-inline size_t partial_bytes(int64_t n, int whole, int shares) {
-  return (size_t)(n - whole) * shares * kGemmM * kGemmN * sizeof(float);
+// How a launch's products are cut into units: the last tiles, too few for all pairs of
+// CTAs at once, along k where that saves time.
+struct GemmCut {
+  int64_t tiles;
+  int k_tiles;
+  int64_t whole;
+  int shares;
+};
+// Sets whole and shares, the products in the order of the launch; returns about the
+// microseconds that the launch takes.
+double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue);
+inline size_t partial_bytes(const GemmCut& p, int tile_n) {
+  return p.shares < 2 ? 0
+                      : (size_t)(p.tiles - p.whole) * p.shares * kGemmM * tile_n * sizeof(float);
 }
 
 // More rows than that (T <= kBatchRows): the same two forms, with tensor maps of the

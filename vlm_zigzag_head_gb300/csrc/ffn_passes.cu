@@ -2,6 +2,8 @@
 // between them.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "ffn.h"
 #include "ffn_act.cuh"
 #include "ptx.cuh"
@@ -177,16 +179,120 @@ __global__ void __launch_bounds__(kTile == 128 ? 256 : 64, kTile == 128 ? 2 : 8)
 
 }  // namespace
 
-void share_tail(int64_t n, int k_tiles, int pairs, int* whole, int* shares) {
-  *whole = (int)n;
-  *shares = 1;
-  const int tail = (int)(n % pairs);
-  if (tail == 0) return;
-  // at least four k tiles a share, and twelve saved: joining costs a few microseconds
-  const int s = pairs / tail < k_tiles / 4 ? pairs / tail : k_tiles / 4;
-  if (s < 2 || k_tiles - (k_tiles + s - 1) / s < 12) return;
-  *whole = (int)(n - tail);
-  *shares = s;
+// What a pair takes for a k tile, in microseconds (one half as wide reads three quarters
+// of the operands for half the products), and for adding up the shares of a tile, which
+// waits for memory once for every two shares of 64 columns.
+static double step_time(int tile_n) { return tile_n == 256 ? 0.29 : 0.22; }
+static double join_time(int shares, int tile_n) { return 1.5 + 0.4 * shares * tile_n / 64; }
+
+// About the time of a launch, its units dealt out to the pairs to and fro.
+static double launch_time(const GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
+  const double step = step_time(tile_n);
+  const double epi = (epilogue == GEMM_STORE ? 2. : 4.) * tile_n / 256;
+  struct {
+    int64_t end;
+    double time;
+  } run[2 * kGemmProblems];   // of equal units
+  int runs = 0;
+  int64_t units = 0;
+  double sum = 0, longest = 0;
+  auto add = [&](int64_t count, double time) {
+    if (count == 0) return;
+    units += count;
+    run[runs++] = {units, time};
+    sum += count * time;
+    longest = std::max(longest, time);
+  };
+  for (int i = 0; i < n; ++i) {
+    add(p[i].whole, p[i].k_tiles * step);
+    if (p[i].shares > 1)
+      add((p[i].tiles - p[i].whole) * p[i].shares,
+          (p[i].k_tiles + p[i].shares - 1) / p[i].shares * step +
+              join_time(p[i].shares, tile_n));
+  }
+  if (units <= pairs) return longest + epi;
+  double time = sum / pairs;
+  if (units <= 2 * pairs) {
+    auto at = [&](int64_t u) {
+      int i = 0;
+      while (i < runs && u >= run[i].end) ++i;
+      return i < runs ? run[i].time : 0.;
+    };
+    auto pair = [&](int64_t i) {   // its first unit and its second
+      if (i >= 0 && i < pairs) time = std::max(time, at(i) + at(2 * pairs - 1 - i));
+    };
+    pair(0);
+    for (int i = 0; i < runs; ++i) {   // where one of the two changes
+      pair(run[i].end);
+      pair(2 * pairs - run[i].end);
+    }
+  } else if (units % pairs != 0) {
+    time += run[runs - 1].time * (1. - (double)(units % pairs) / pairs);
+  }
+  return std::max(time, longest) + epi;
+}
+
+double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
+  int64_t total = 0, work = 0;
+  for (int i = 0; i < n; ++i) {
+    total += p[i].tiles;
+    work += p[i].tiles * p[i].k_tiles;
+    p[i].whole = p[i].tiles;
+    p[i].shares = 1;
+  }
+  double best = launch_time(p, n, pairs, tile_n, epilogue);
+  auto consider = [&](const GemmCut* q) {
+    const double t = launch_time(q, n, pairs, tile_n, epilogue);
+    if (t >= best) return;
+    best = t;
+    std::copy(q, q + n, p);
+  };
+  auto unit_time = [&](const GemmCut& c) {
+    return (c.k_tiles + c.shares - 1) / c.shares * step_time(tile_n) +
+           (c.shares > 1 ? join_time(c.shares, tile_n) : 0.);
+  };
+  GemmCut q[kGemmProblems];
+
+  // The last round's tiles: the product whose units are longest is cut further while that
+  // pays and there are pairs left and four k tiles a share.
+  std::copy(p, p + n, q);
+  int tail[kGemmProblems] = {}, left = (int)(total % pairs), free = pairs - left;
+  for (int i = n - 1; i >= 0; --i) {
+    tail[i] = (int)(p[i].tiles < left ? p[i].tiles : left);
+    left -= tail[i];
+  }
+  for (;;) {
+    int i = -1;
+    for (int j = 0; j < n; ++j)
+      if (tail[j] && (i < 0 || unit_time(q[j]) > unit_time(q[i]))) i = j;
+    if (i < 0 || tail[i] > free || q[i].k_tiles / (q[i].shares + 1) < 4) break;
+    GemmCut more = q[i];
+    ++more.shares;
+    more.whole = more.tiles - tail[i];
+    if (unit_time(more) >= unit_time(q[i])) break;
+    free -= tail[i];
+    q[i] = more;
+  }
+  consider(q);
+
+  // Or every product with more k than a pair's part of the whole work (so that these are
+  // fewer tiles than pairs).
+  const int part = (int)std::min<int64_t>((work + pairs - 1) / pairs, 1 << 30);
+  bool any = false;
+  for (int i = 0; i < n; ++i) {
+    q[i].whole = p[i].tiles;
+    q[i].shares = 1;
+    const int most = std::min((p[i].k_tiles + part - 1) / part, p[i].k_tiles / 4);
+    for (GemmCut more = q[i]; more.shares < most;) {
+      more.whole = 0;
+      ++more.shares;
+      if (unit_time(more) >= unit_time(q[i])) break;
+      q[i] = more;
+      any = true;
+    }
+  }
+  if (any) consider(q);
+  return best;
 }
 
 cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st) {

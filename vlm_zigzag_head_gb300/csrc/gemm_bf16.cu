@@ -4,12 +4,12 @@
 //   C[m][n] = sum_k A(m, k) B(n, k),  bf16 operands, fp32 sums in tensor memory
 //
 // A pair of CTAs shares a tile of 256 x 256 (gate and up: 256 x 128 of each, so that
-// both halves of a pair of columns meet in one epilogue), k goes by 64: each CTA
-// loads 128 rows of A and of B, and the pair's MMAs read both.  Operands come by TMA
-// in the 128-byte swizzle, K-major or MN-major as they lie in memory: no product needs
-// a transposed copy.  The kernel is persistent: pairs walk (tile, share of k) units,
-// and two accumulators in tensor memory let a tile's epilogue run under the next one's
-// products.
+// both halves of a pair of columns meet in one epilogue), or half as wide where that
+// fills the GPU better; k goes by 64: each CTA loads 128 rows of A and half the tile's
+// rows of B, and the pair's MMAs read both.  Operands come by TMA in the 128-byte
+// swizzle, K-major or MN-major as they lie in memory: no product needs a transposed copy.
+// The kernel is persistent: pairs walk (product, tile, share of k) units, and two
+// accumulators in tensor memory let a tile's epilogue run under the next one's products.
 //
 // Warp roles (384 threads):
 //   warp 0       TMA producer (one lane): this CTA's rows of A and B
@@ -38,31 +38,31 @@ using namespace ptx;
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int kRows = kGemmM / 2;                   // of A and B in one CTA
-constexpr int kTile = kRows * kGemmK * 2;           // bytes of one operand's part of a stage
+constexpr int kRows = kGemmM / 2;                   // of A in one CTA
+constexpr int kTileA = kRows * kGemmK * 2;          // bytes of a CTA's part of a stage
 constexpr int kBf16Box = 32 * 64 * 2, kByteBox = 32 * 64;
-constexpr uint32_t kTmemCols = 512;
 constexpr long long kDrainLimit = 1LL << 24;
 constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 // Stages, and the boxes of two warps: two of bf16 (or two halves of fp32); h, gate, up
 // and the low bytes; gate, up, low bytes in, dgate, dup, h out.
-template <int kEpi>
+template <int kEpi, int kN>
 struct Layout {
-  static constexpr int kStages = kEpi == GEMM_STORE ? 6 : kEpi == GEMM_GLU ? 5 : 4;
   static constexpr int kPairBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
                                     : kEpi == GEMM_GLU ? 3 * kBf16Box + 2 * kByteBox
                                                        : 5 * kBf16Box + 2 * kByteBox;
-  static constexpr int kBoxes = kStages * 2 * kTile;
-  static constexpr int kBars = kBoxes + kEpiWarps / 2 * kPairBytes;
+  static constexpr int kTileB = kN / 2 * kGemmK * 2;
+  static constexpr int kStage = kTileA + kTileB;
+  static constexpr int kEpiBytes = kEpiWarps / 2 * kPairBytes;
+  static constexpr int kStages = (224 * 1024 - kEpiBytes) / kStage;   // 4 to 8
+  static constexpr int kBoxes = kStages * kStage;
+  static constexpr int kBars = kBoxes + kEpiBytes;
   static constexpr int kSmem = kBars + 256 + 1024;   // slack for alignment
+  static_assert(kStages <= 8 && kSmem <= 227 * 1024, "shared memory budget");
 };
-static_assert(Layout<GEMM_STORE>::kSmem <= 227 * 1024, "shared memory budget");
-static_assert(Layout<GEMM_GLU>::kSmem <= 227 * 1024, "shared memory budget");
-static_assert(Layout<GEMM_DGLU>::kSmem <= 227 * 1024, "shared memory budget");
 
 struct Bars {
-  uint64_t full[6];        // first CTA: both CTAs' loads of a stage have landed
-  uint64_t empty[6];       // both: the stage's MMAs are done
+  uint64_t full[8];        // first CTA: both CTAs' loads of a stage have landed
+  uint64_t empty[8];       // both: the stage's MMAs are done
   uint64_t acc_full[2];    // both: a tile's products are done
   uint64_t acc_empty[2];   // first CTA: both CTAs' epilogues have read them
   uint64_t box[4];         // GEMM_DGLU: a quarter's boxes have landed
@@ -76,35 +76,48 @@ static_assert(sizeof(Bars) <= 256, "barrier block");
 // time, which reads the least of A and B.
 constexpr int kGroupM = 8;
 
-struct TilePlace {
-  int m, n;
-};
-__device__ __forceinline__ TilePlace tile_place(const GemmArgs& g, int tile) {
-  const unsigned per_group = kGroupM * g.n_tiles;
-  const unsigned group = (unsigned)tile / per_group, in = (unsigned)tile % per_group;
-  const unsigned first = group * kGroupM;
-  const unsigned rows = min(kGroupM, g.m_tiles - (int)first);
-  return {(int)(first + in % rows), (int)(in / rows)};
-}
-
-// Unit u: a tile, and which of its k tiles.  The issuing thread asks for the k tiles
-// alone: between two tiles the tensor core waits for it.
+// Unit u: a tile of a problem, and which of its k tiles.  The issuing thread asks for
+// no more: between two tiles the tensor core waits for it.
 struct Work {
-  int tile, slot, k0, k1;   // slot: of the partial sums, -1 for a whole tile
+  int p, tile, k0, k1;
+  int slot, share, ticket;   // of the partial sums, the slot -1 for a whole tile
 };
 __device__ __forceinline__ Work work_at(const GemmArgs& g, int u) {
-  if (u < g.whole) return {u, -1, 0, g.k_tiles};
-  const unsigned v = u - g.whole, tail = v / g.shares, share = v % g.shares;
-  return {(int)(g.whole + tail), (int)v, (int)(g.k_tiles * share / g.shares),
-          (int)(g.k_tiles * (share + 1) / g.shares)};
+  Work w;
+  w.p = 0;
+  while (w.p + 1 < g.problems && u >= g.p[w.p + 1].first) ++w.p;
+  const GemmProblem& p = g.p[w.p];
+  w.tile = u - p.first;
+  w.slot = -1;
+  w.share = w.ticket = 0;
+  unsigned shares = 1;
+  if (w.tile >= p.whole) {
+    const unsigned v = w.tile - p.whole;
+    shares = p.shares;
+    w.ticket = p.first_ticket + (int)(v / shares);
+    w.share = (int)(v % shares);
+    w.tile = p.whole + (int)(v / shares);
+    w.slot = p.first_slot + (int)v;
+  }
+  const unsigned k_tiles = p.k_tiles;
+  w.k0 = w.share == 0 ? 0 : (int)(k_tiles * w.share / shares);
+  w.k1 = w.share + 1 == (int)shares ? (int)k_tiles : (int)(k_tiles * (w.share + 1) / shares);
+  return w;
 }
-struct Unit {
-  int tile, m, n, slot, k0, k1;
+struct Unit : Work {
+  int m, n;
 };
 __device__ __forceinline__ Unit unit_at(const GemmArgs& g, int u) {
-  const Work w = work_at(g, u);
-  const TilePlace t = tile_place(g, w.tile);
-  return {w.tile, t.m, t.n, w.slot, w.k0, w.k1};
+  Unit t;
+  static_cast<Work&>(t) = work_at(g, u);
+  const GemmProblem& p = g.p[t.p];
+  const unsigned per_group = kGroupM * p.n_tiles;
+  const unsigned group = t.tile / per_group, in = t.tile % per_group;
+  const unsigned first = group * kGroupM;
+  const unsigned rows = min(kGroupM, p.m_tiles - (int)first);
+  t.m = (int)(first + in % rows);
+  t.n = (int)(in / rows);
+  return t;
 }
 
 __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
@@ -113,25 +126,26 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
 }
 
 // 32 columns (pieces 8 c .. 8 c + 7) of tile row `row` into a shared tile's sums.
+template <int kN>
 __device__ __forceinline__ void store_partial(const GemmArgs& g, int slot, int col, int row,
                                               const float (&f)[32]) {
   float4* p = reinterpret_cast<float4*>(g.partial) +
-              ((int64_t)slot * (kGemmN / 4) + col / 4) * kGemmM + row;
+              ((int64_t)slot * (kN / 4) + col / 4) * kGemmM + row;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
-// The same columns of all shares of a tile, added in order.
-__device__ __forceinline__ void load_partials(const GemmArgs& g, int tile, int col, int row,
-                                              float (&f)[32]) {
+// The same columns of all shares of a tile, from slot `slot` on, added in order.
+template <int kN>
+__device__ __forceinline__ void load_partials(const GemmArgs& g, int slot, int shares, int col,
+                                              int row, float (&f)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = 0.f;
 #pragma unroll 2
-  for (int s = 0; s < g.shares; ++s) {
+  for (int s = 0; s < shares; ++s) {
     const float4* p = reinterpret_cast<const float4*>(g.partial) +
-                      ((int64_t)((tile - g.whole) * g.shares + s) * (kGemmN / 4) + col / 4) * kGemmM +
-                      row;
+                      ((int64_t)(slot + s) * (kN / 4) + col / 4) * kGemmM + row;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float4 v = __ldcg(p + i * kGemmM);   // written by other CTAs of this launch
@@ -194,22 +208,27 @@ __device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, int
   }
 }
 
-template <bool kAMN, bool kBMN, int kEpi>
+template <int kEpi, int kN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  using L = Layout<kEpi>;
-  constexpr int kStages = L::kStages;
+  using L = Layout<kEpi, kN>;
+  constexpr int kStages = L::kStages, kRowsB = kN / 2;
+  constexpr uint32_t kTmemCols = 2 * kN;   // two accumulators
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int units = g.whole + (g.m_tiles * g.n_tiles - g.whole) * g.shares;
+  const int units = g.units;
+  // the units are dealt out to and fro: the longest come first
+  auto unit_of = [&](int r) { return r * pairs + (r & 1 ? pairs - 1 - pair : pair); };
   griddep_launch_dependents();   // the next product waits for this one where it must
   volatile int* abort = &bars->abort;
   const long long lim = g.wait_limit;
 
+  if (blockIdx.x == 0)   // long before any wait may give up
+    for (int i = threadIdx.x; i < g.clear; i += kThreads) g.status[i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 1);
@@ -237,56 +256,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      auto load_a = [&](const Unit& t, int k, int st) {
-        const bool second = t.m >= g.m_split;
-        const int src = k >= g.k_split, kk = (k - (src ? g.k_split : 0)) * kGemmK;
-        const int m0 = (t.m - (second ? g.m_split : 0)) * kGemmM + rank * kRows;
-        const CUtensorMap* map = &g.a[second || src];
-        uint8_t* dst = smem + st * 2 * kTile;
+      // Where a unit's operands come from; this thread's time is near the products'
+      // where both operands take two loads a stage, so all that is the same for each
+      // stage stays in registers.
+      struct Source {
+        const CUtensorMap *a, *a_next, *b, *b_next;   // the latter from k_split on
+        int m0, n0, k_split;
+        bool a_mn, b_mn;
+      };
+      auto source = [&](const Unit& t) {
+        const GemmProblem& p = g.p[t.p];
+        const bool second = t.m >= p.m_split;
+        Source f;
+        f.a = &p.a[second];
+        f.a_next = &p.a[1];
+        f.b = &p.b[kEpi == GEMM_GLU ? rank : 0];   // gate or up
+        f.b_next = &p.b[1];
+        f.m0 = (t.m - (second ? p.m_split : 0)) * kGemmM + rank * kRows;
+        f.n0 = kEpi == GEMM_GLU ? t.n * kRowsB : t.n * kN + rank * kRowsB;
+        f.k_split = p.k_split;
+        f.a_mn = p.a_mn;
+        f.b_mn = p.b_mn;
+        if (!CP_IN_RANGE(f.m0, 0, p.M + kRows, g.status, 301)) f.m0 = 0;
+        if (!CP_IN_RANGE(f.n0, 0, p.N + kRows, g.status, 302)) f.n0 = 0;
+        return f;
+      };
+      auto load_a = [&](const Source& f, int k, int st) {
+        const bool next = k >= f.k_split;
+        const int kk = (k - (next ? f.k_split : 0)) * kGemmK;
+        const CUtensorMap* map = next ? f.a_next : f.a;
+        uint8_t* dst = smem + st * L::kStage;
         const uint32_t full = in_first_cta(&bars->full[st]);
-        if (!CP_IN_RANGE(m0, 0, g.M + kRows, g.status, 301)) return;
-        if constexpr (kAMN) {
+        if (f.a_mn) {
+#pragma unroll
           for (int i = 0; i < kRows / 64; ++i)
-            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, m0 + i * 64, kk);
+            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, f.m0 + i * 64, kk);
         } else {
-          tma_load_2d_pair(map, full, dst, kk, m0);
+          tma_load_2d_pair(map, full, dst, kk, f.m0);
         }
       };
-      auto load_b = [&](const Unit& t, int k, int st) {
-        const int src = k >= g.k_split, kk = (k - (src ? g.k_split : 0)) * kGemmK;
-        const int n0 = kEpi == GEMM_GLU ? t.n * kRows : t.n * kGemmN + rank * kRows;
-        const CUtensorMap* map = &g.b[kEpi == GEMM_GLU ? rank : src];   // gate or up
-        uint8_t* dst = smem + st * 2 * kTile + kTile;
+      auto load_b = [&](const Source& f, int k, int st) {
+        const bool next = k >= f.k_split;
+        const int kk = (k - (next ? f.k_split : 0)) * kGemmK;
+        const CUtensorMap* map = next ? f.b_next : f.b;
+        uint8_t* dst = smem + st * L::kStage + kTileA;
         const uint32_t full = in_first_cta(&bars->full[st]);
-        if (!CP_IN_RANGE(n0, 0, g.N + kRows, g.status, 302)) return;
-        if constexpr (kBMN) {
-          for (int i = 0; i < kRows / 64; ++i)
-            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, n0 + i * 64, kk);
+        if (f.b_mn) {
+#pragma unroll
+          for (int i = 0; i < kRowsB / 64; ++i)
+            tma_load_2d_pair(map, full, dst + i * 64 * kGemmK * 2, f.n0 + i * 64, kk);
         } else {
-          tma_load_2d_pair(map, full, dst, kk, n0);
+          tma_load_2d_pair(map, full, dst, kk, f.n0);
         }
       };
       auto expect = [&](int st) {   // both CTAs' parts
-        if (rank == 0) mbar_expect_tx(&bars->full[st], 4 * kTile);
+        if (rank == 0) mbar_expect_tx(&bars->full[st], 2 * L::kStage);
       };
       // the first stages' weights need not wait for the launch before
       int early = 0;
       if (g.follows == FOLLOWS_A) {
         const Unit t = unit_at(g, pair);
+        const Source f = source(t);
         early = min(kStages, t.k1 - t.k0);
         for (int i = 0; i < early; ++i) {
           expect(i);
-          load_b(t, t.k0 + i, i);
+          load_b(f, t.k0 + i, i);
         }
         griddep_wait();
-        for (int i = 0; i < early; ++i) load_a(t, t.k0 + i, i);
+        for (int i = 0; i < early; ++i) load_a(f, t.k0 + i, i);
       } else if (g.follows == FOLLOWS_BOTH) {
         griddep_wait();
       }
       int j = early;   // k tiles so far, across units
-      for (int u = pair; u < units && !*abort; u += pairs) {
-        const Unit t = unit_at(g, u);
-        for (int k = t.k0 + (u == pair ? early : 0); k < t.k1; ++k, ++j) {
+      for (int r = 0; unit_of(r) < units && !*abort; ++r) {
+        const Unit t = unit_at(g, unit_of(r));
+        const Source f = source(t);
+        for (int k = t.k0 + (r == 0 ? early : 0); k < t.k1; ++k, ++j) {
           const int st = j % kStages;
           if (j >= kStages &&
               !mbar_wait_cluster(&bars->empty[st], ((j / kStages) - 1) & 1, lim, abort)) {
@@ -294,8 +339,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           expect(st);
-          load_a(t, k, st);
-          load_b(t, k, st);
+          load_a(f, k, st);
+          load_b(f, k, st);
         }
       }
       // no load may be on its way when the CTA exits (none is once its tiles' epilogues
@@ -308,15 +353,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t idesc = idesc_bf16(kGemmM, kGemmN, kAMN, kBMN);
       bool ok = true;
       int j = 0, n = 0;   // k tiles and units so far
       Work t = work_at(g, pair), next = t;
       // its waits are bounded, and the launch before may take longer than the bound
       if (g.follows != FOLLOWS_NONE) griddep_wait();
-      for (int u = pair; ok && u < units; u += pairs, ++n, t = next) {
-        if (u + pairs < units) next = work_at(g, u + pairs);
+      for (; ok && unit_of(n) < units; ++n, t = next) {
+        if (unit_of(n + 1) < units) next = work_at(g, unit_of(n + 1));
         const int s = n & 1;
+        const int a_mn = g.p[t.p].a_mn, b_mn = g.p[t.p].b_mn;
+        const uint32_t idesc = idesc_bf16(kGemmM, kN, a_mn, b_mn);
+        // 16 k further: 32 bytes along a K-major row, 16 rows of an MN-major box
+        const uint32_t a_step = a_mn ? 2048 : 32, b_step = b_mn ? 2048 : 32;
+        const uint32_t a_lbo = a_mn ? 64 * kGemmK * 2 : 16, b_lbo = b_mn ? 64 * kGemmK * 2 : 16;
         if (n >= 2 && !mbar_wait_cluster(&bars->acc_empty[s], ((n >> 1) - 1) & 1, lim, abort)) {
           ok = false;
           break;
@@ -329,16 +378,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t pa = smem_u32(smem + st * 2 * kTile), pb = pa + kTile;
+          const uint32_t pa = smem_u32(smem + st * L::kStage), pb = pa + kTileA;
 #pragma unroll
-          for (int i = 0; i < kGemmK / 16; ++i) {
-            // 16 k further: 32 bytes along a K-major row, 16 rows of an MN-major box
-            const uint64_t da = kAMN ? sdesc_sw128(pa + i * 2048, 64 * kGemmK * 2, 1024)
-                                     : sdesc_sw128(pa + i * 32, 16, 1024);
-            const uint64_t db = kBMN ? sdesc_sw128(pb + i * 2048, 64 * kGemmK * 2, 1024)
-                                     : sdesc_sw128(pb + i * 32, 16, 1024);
-            mma_bf16_pair(tmem + s * kGemmN, da, db, idesc, (k > t.k0 || i > 0) ? 1u : 0u);
-          }
+          for (int i = 0; i < kGemmK / 16; ++i)
+            mma_bf16_pair(tmem + s * kN, sdesc_sw128(pa + i * a_step, a_lbo, 1024),
+                          sdesc_sw128(pb + i * b_step, b_lbo, 1024), idesc,
+                          (k > t.k0 || i > 0) ? 1u : 0u);
           mma_commit_pair(&bars->empty[st]);
         }
         if (!ok) break;
@@ -359,10 +404,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int pair_bar = 1 + quarter;
     auto pair_sync = [&] { named_sync(pair_bar, 64); };
     uint8_t* boxes = smem + L::kBoxes + quarter * L::kPairBytes;
-    constexpr int kTileN = kEpi == GEMM_GLU ? kGemmN / 2 : kGemmN;
+    constexpr int kTileN = kEpi == GEMM_GLU ? kN / 2 : kN;
     constexpr int kChunks = kTileN / 64;
     auto first_row = [&](const Unit& t) {
-      return (t.m - (t.m >= g.m_split ? g.m_split : 0)) * kGemmM + rank * kRows + quarter * 32;
+      const int split = g.p[t.p].m_split;
+      return (t.m - (t.m >= split ? split : 0)) * kGemmM + rank * kRows + quarter * 32;
     };
     // GEMM_DGLU: the kept gate and up of a chunk, on their way while the one before
     // is worked on
@@ -379,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int n = 0, fetched = 0, got = 0;
     auto fetch_first = [&](int u) {   // the first chunk of unit u, where it is a whole tile
       if constexpr (kEpi == GEMM_DGLU) {
-        if (u >= g.whole) return;
+        if (u >= g.p[0].whole) return;
         fetch(unit_at(g, u), 0);
         ++fetched;
       }
@@ -387,8 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (g.follows != FOLLOWS_NONE) griddep_wait();
     fetch_first(pair);
     bool ok = true;
-    for (int u = pair; ok && u < units; u += pairs, ++n) {
-      const Unit t = unit_at(g, u);
+    for (; ok && unit_of(n) < units; ++n) {
+      const Unit t = unit_at(g, unit_of(n));
       const int s = n & 1;
       // both warps of a box go on, or neither
       if (!named_all(pair_bar, 64,
@@ -397,8 +443,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kGemmN;
-      const int second = t.m >= g.m_split;
+      const GemmProblem& p = g.p[t.p];
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kN;
+      const int second = t.m >= p.m_split;
       const int row0 = first_row(t), tile_row = rank * kRows + quarter * 32 + lane;
       auto release = [&] {   // the next products may overwrite the accumulator
         tc_fence_before();
@@ -407,13 +454,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       const bool shared = t.slot >= 0;
       if (shared) {
-        const bool in = row0 + lane < g.M;
+        const bool in = row0 + lane < p.M;
 #pragma unroll 1
-        for (int c = 0; c < kGemmN / 64; ++c) {
+        for (int c = 0; c < kN / 64; ++c) {
           const int col = c * 64 + half * 32;
           float x[32];
           load_acc(acc + col, x);
-          if (in) store_partial(g, t.slot, col, tile_row, x);
+          if (in) store_partial<kN>(g, t.slot, col, tile_row, x);
           __syncwarp();   // the next load of the accumulator is the whole warp's
         }
         release();
@@ -422,8 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_sync();
         bool last = true;
         if (issues) {
-          int32_t* ticket = g.tickets + (t.tile - g.whole) * 8 + rank * 4 + quarter;
-          last = atomicAdd(ticket, 1) == g.shares - 1;
+          int32_t* ticket = g.tickets + t.ticket * 8 + rank * 4 + quarter;
+          last = atomicAdd(ticket, 1) == p.shares - 1;
           if (last) *ticket = 0;
           __threadfence();
         }
@@ -432,13 +479,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
         const int col = c * 64 + half * 32, box_col = t.n * kTileN + c * 64;
-        const bool stores = row0 < g.M && box_col < g.N;   // the box is not wholly past the end
+        const bool stores = row0 < p.M && box_col < p.N;   // the box is not wholly past the end
         float x[32];
         auto take = [&](int at, float (&f)[32]) {
           if (!shared) {
             load_acc(acc + at, f);
-          } else if (row0 + lane < g.M) {
-            load_partials(g, t.tile, at, tile_row, f);
+          } else if (row0 + lane < p.M) {
+            load_partials<kN>(g, t.slot - t.share, p.shares, at, tile_row, f);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = 0.f;
@@ -461,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           pair_sync();
           if (issues && stores) {
-            tma_store_2d(&g.out[0], boxes, box_col, row0);
+            tma_store_2d(&p.out[0], boxes, box_col, row0);
             if (g.keep) {
               tma_store_2d(&g.gate[0], boxes + kBf16Box, box_col, row0);
               tma_store_2d(&g.up[0], boxes + 2 * kBf16Box, box_col, row0);
@@ -471,20 +518,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         } else if constexpr (kEpi == GEMM_STORE) {
-          uint8_t* box = boxes + (g.out_f32 ? half : c & 1) * kBf16Box;
+          uint8_t* box = boxes + (p.out_f32 ? half : c & 1) * kBf16Box;
           if (issues) {
-            if (g.out_f32) bulk_wait_read<0>();
+            if (p.out_f32 || c == 0) bulk_wait_read<0>();   // the last tile's may be fp32
             else bulk_wait_read<1>();
           }
           pair_sync();
-          if (g.out_f32) put_f32(box, lane, x);
+          if (p.out_f32) put_f32(box, lane, x);
           else put_bf16(box, lane, half, x);
           fence_proxy_async_smem();
           pair_sync();
           if (issues) {
-            if (stores) tma_store_2d(&g.out[second], box, box_col, row0);
-            if (stores && g.out_f32 && box_col + 32 < g.N)
-              tma_store_2d(&g.out[second], box + kBf16Box, box_col + 32, row0);
+            if (stores) tma_store_2d(&p.out[second], box, box_col, row0);
+            if (stores && p.out_f32 && box_col + 32 < p.N)
+              tma_store_2d(&p.out[second], box + kBf16Box, box_col + 32, row0);
             bulk_commit();   // one group a chunk, so that the count holds
           }
         } else {
@@ -500,14 +547,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++got;
           uint4 kg[4], ku[4], lg[2], lu[2];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            kg[p] = *piece<128>(boxes, lane, half * 4 + p);
-            ku[p] = *piece<128>(boxes + kBf16Box, lane, half * 4 + p);
+          for (int q = 0; q < 4; ++q) {
+            kg[q] = *piece<128>(boxes, lane, half * 4 + q);
+            ku[q] = *piece<128>(boxes + kBf16Box, lane, half * 4 + q);
           }
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            lg[p] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + p);
-            lu[p] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + p);
+          for (int q = 0; q < 2; ++q) {
+            lg[q] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + q);
+            lu[q] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + q);
           }
           if (issues) bulk_wait_read<0>();   // the last stores have read their boxes
           pair_sync();   // all have read: the next chunk may land
@@ -515,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fetch(t, c + 1);
             ++fetched;
           } else {
-            fetch_first(u + pairs);
+            fetch_first(unit_of(n + 1));
           }
           uint8_t* out = boxes + 2 * (kBf16Box + kByteBox);
           const uint32_t* wg = reinterpret_cast<const uint32_t*>(kg);
@@ -523,20 +570,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
           const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {   // eight columns at a time
+          for (int q = 0; q < 4; ++q) {   // eight columns at a time
             float gate[8], up[8], h[8];
-            rejoin8(wg + 4 * p, bg + 2 * p, gate);
-            rejoin8(wu + 4 * p, bu + 2 * p, up);
+            rejoin8(wg + 4 * q, bg + 2 * q, gate);
+            rejoin8(wu + 4 * q, bu + 2 * q, up);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float da;
-              const float a = activation<true, true>(gate[e], g.act, da), dh = x[8 * p + e];
+              const float a = activation<true, true>(gate[e], g.act, da), dh = x[8 * q + e];
               h[e] = a * up[e];
               gate[e] = dh * up[e] * da;
               up[e] = dh * a;
             }
             auto put = [&](int which, const float (&f)[8]) {
-              *piece<128>(out + which * kBf16Box, lane, half * 4 + p) =
+              *piece<128>(out + which * kBf16Box, lane, half * 4 + q) =
                   make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
             };
@@ -549,7 +596,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (issues && stores) {
             tma_store_2d(&g.dgate, out, box_col, row0);
             tma_store_2d(&g.dup, out + kBf16Box, box_col, row0);
-            tma_store_2d(&g.out[0], out + 2 * kBf16Box, box_col, row0);
+            tma_store_2d(&p.out[0], out + 2 * kBf16Box, box_col, row0);
             bulk_commit();
           }
         }
@@ -560,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (issues) {
       int zero = 0;   // a load that nobody waited for (after a wait gave up)
       for (; got < fetched; ++got) mbar_wait(&bars->box[quarter], got & 1, kDrainLimit, &zero);
-      bulk_wait_all();
+      bulk_wait_read<0>();   // the boxes may go; the kernel's end waits for the writes
     }
   }
   tc_fence_before();
@@ -572,15 +619,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool kAMN, bool kBMN, int kEpi>
+template <int kEpi, int kN>
 cudaError_t launch_t(const GemmArgs& g, int sms, cudaStream_t st) {
-  auto kernel = gemm_kernel<kAMN, kBMN, kEpi>;
-  constexpr int smem = Layout<kEpi>::kSmem;
+  auto kernel = gemm_kernel<kEpi, kN>;
+  constexpr int smem = Layout<kEpi, kN>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t units = g.whole + ((int64_t)g.m_tiles * g.n_tiles - g.whole) * g.shares;
-  if (units < 1 || units > 0x3fffffff) return cudaErrorInvalidConfiguration;
-  const int64_t pairs = units < sms / 2 ? units : sms / 2;
+  const int pairs = g.units < sms / 2 ? g.units : sms / 2;
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(kThreads);
@@ -596,13 +642,15 @@ cudaError_t launch_t(const GemmArgs& g, int sms, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, bool a_mn, bool b_mn, int sms,
+cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, int tile_n, int sms,
                              cudaStream_t st) {
-  if (epilogue == GEMM_GLU) return launch_t<false, false, GEMM_GLU>(g, sms, st);
-  if (epilogue == GEMM_DGLU) return launch_t<false, true, GEMM_DGLU>(g, sms, st);
-  if (a_mn) return launch_t<true, true, GEMM_STORE>(g, sms, st);
-  return b_mn ? launch_t<false, true, GEMM_STORE>(g, sms, st)
-              : launch_t<false, false, GEMM_STORE>(g, sms, st);
+  if (tile_n != 256 && tile_n != 128) return cudaErrorInvalidValue;
+  const bool wide = tile_n == 256;
+  if (epilogue == GEMM_GLU)
+    return wide ? launch_t<GEMM_GLU, 256>(g, sms, st) : launch_t<GEMM_GLU, 128>(g, sms, st);
+  if (epilogue == GEMM_DGLU)
+    return wide ? launch_t<GEMM_DGLU, 256>(g, sms, st) : launch_t<GEMM_DGLU, 128>(g, sms, st);
+  return wide ? launch_t<GEMM_STORE, 256>(g, sms, st) : launch_t<GEMM_STORE, 128>(g, sms, st);
 }
 
 }  // namespace cpattn
