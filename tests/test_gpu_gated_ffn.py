@@ -111,6 +111,32 @@ def test_matches_oracle(T, D, F, D_out, dtype, act):
         assert all(torch.equal(a, b) for a, b in zip(grads, again))
 
 
+# dx, the two weights' and the down weight's gradients are one launch: dx first with its k shared; all
+# whole in two rounds; dx last, behind fp32 gradients of the weights; a few tiles each; one long product
+ONE_LAUNCH = [(700, 320, 1664, 320, "silu"), (2000, 512, 1360, 520, "gelu"), (6000, 520, 64, 264, "silu"),
+              (30, 512, 1360, 512, "gelu_tanh"), (9000, 1032, 136, 40, "silu"), (400, 64, 8000, 72, "silu"),
+              (150, 1920, 3968, 24, "silu")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,F,D_out,act", ONE_LAUNCH)
+def test_gradients_of_one_launch(T, D, F, D_out, act):
+    import vlm_zigzag_head_gb300 as cp
+    dt = torch.bfloat16
+    x, wg, wu, wd, dy = _inputs(T, D, F, D_out, dt, T + D + F)
+    y, gate, up = cp.cp_gated_ffn_fwd(x, wg, wu, wd, act, keep=True)
+    ws = cp.Workspace()
+    for grad_dtype in (torch.float32, dt):
+        full = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, grad_dtype=grad_dtype, workspace=ws)
+        assert cp.cp_workspace_status(ws) == 0
+        _check((y, *full), x, wg, wu, wd, dy, act, dt, grad_dtype)
+        for wanted in ((True, False, False, True), (True, True, False, False), (False, True, True, True)):
+            some = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, grad_dtype=grad_dtype,
+                                       wanted=list(wanted), workspace=ws)
+            assert cp.cp_workspace_status(ws) == 0
+            _check((y, *some), x, wg, wu, wd, dy, act, dt, grad_dtype)
+
+
 def _call(seed=1, T=70, D=72, F=136, D_out=40, dtype=torch.bfloat16):
     import vlm_zigzag_head_gb300 as cp
     x, wg, wu, wd, dy = _inputs(T, D, F, D_out, dtype, seed)
