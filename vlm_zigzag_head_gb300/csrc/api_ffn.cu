@@ -72,7 +72,10 @@ bool batch_rows(const cp_gated_ffn_t* p) {
   return p->dtype == CP_BF16 && p->T > kFewRows && p->T <= kBatchRows;
 }
 
-// A launch of bf16 products: the width of its tiles and how it is cut into units.  Wide
+// fp32 calls of more rows go through the tensor cores.
+bool split_rows(const cp_gated_ffn_t* p) { return p->dtype == CP_F32 && p->T > kSimtRows; }
+
+// A launch of products: the width of its tiles and how it is cut into units.  bf16: wide
 // tiles are quicker per product (backward of 4096 rows, 2048 -> 5504, 375 and 594 us),
 // narrow ones where wide ones are too few for the GPU (700 rows, 320 -> 1664, 31 and 23).
 struct Launch {
@@ -85,10 +88,12 @@ struct Shape {
   int64_t M, N;
   int k_tiles, outputs;
 };
-Launch plan_launch(std::initializer_list<Shape> products, int epilogue, int pairs) {
+Launch plan_launch(std::initializer_list<Shape> products, int epilogue, int pairs, bool split) {
   Launch best;
   double least = 0;
   for (int tile_n : {256, 128}) {
+    if (split && tile_n != kSplitN) continue;
+    const GemmCost cost = split ? split_cost(epilogue) : gemm_cost(epilogue, tile_n);
     Launch l;
     l.tile_n = tile_n;
     for (const Shape& p : products) {
@@ -97,9 +102,9 @@ Launch plan_launch(std::initializer_list<Shape> products, int epilogue, int pair
                          tiles(p.N, epilogue == GEMM_GLU ? tile_n / 2 : tile_n);
       l.cut[l.n++].k_tiles = p.k_tiles;
     }
-    const double t = cut_products(l.cut, l.n, pairs, tile_n, epilogue);
+    const double t = cut_products(l.cut, l.n, pairs, cost);
     for (int i = 0; i < l.n; ++i) l.partial += partial_bytes(l.cut[i], tile_n);
-    if (tile_n == 256 || t < least) {
+    if (least == 0 || t < least) {
       best = l;
       least = t;
     }
@@ -119,7 +124,7 @@ Launch plan_gradients(const cp_gated_ffn_t* p, int pairs, bool dx, int in, bool 
   const bool first = dx_first(p);
   return plan_launch({{T, D, k_dx, dx && first}, {F, D, k, in}, {O, F, k, down},
                       {T, D, k_dx, dx && !first}},
-                     GEMM_STORE, pairs);
+                     GEMM_STORE, pairs, p->dtype == CP_F32);
 }
 
 struct Share {
@@ -127,8 +132,8 @@ struct Share {
 };
 struct Plan {
   int sms = 0;
-  Launch gate_up, down, dh;                                 // bf16
-  Share f32_gate_up, f32_down, f32_dh, d_down, d_in, d_both, dx;   // fp32; d_in: one weight
+  Launch gate_up, down, dh;                                 // tensor cores
+  Share f32_gate_up, f32_down, f32_dh, d_down, d_in, d_both, dx;   // CUDA cores; d_in: one weight
   size_t fwd_partial = 0, bwd_partial = 0;                  // bytes
   int pairs() const { return sms / 2; }
 };
@@ -138,10 +143,11 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
   r.sms = sms;
   if (sms < 2) return r;
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
-  if (p->dtype == CP_BF16) {
-    r.gate_up = plan_launch({{T, F, tiles(D, kGemmK), 1}}, GEMM_GLU, r.pairs());
-    r.down = plan_launch({{T, O, tiles(F, kGemmK), 1}}, GEMM_STORE, r.pairs());
-    r.dh = plan_launch({{T, F, tiles(O, kGemmK), 1}}, GEMM_DGLU, r.pairs());
+  const bool split = split_rows(p);
+  if (p->dtype == CP_BF16 || split) {
+    r.gate_up = plan_launch({{T, F, tiles(D, kGemmK), 1}}, GEMM_GLU, r.pairs(), split);
+    r.down = plan_launch({{T, O, tiles(F, kGemmK), 1}}, GEMM_STORE, r.pairs(), split);
+    r.dh = plan_launch({{T, F, tiles(O, kGemmK), 1}}, GEMM_DGLU, r.pairs(), split);
     r.fwd_partial = std::max(r.gate_up.partial, r.down.partial);
     r.bwd_partial = r.dh.partial;
     for (int which = 1; which < 12; ++which)   // whichever gradients are wanted
@@ -169,19 +175,28 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
 }
 
 // At the start of a workspace, cleared by every call: the status word, and the tickets
-// of shared tiles (fewer than there are pairs of CTAs, eight each).
+// of shared tiles (fewer than there are pairs of CTAs).
 constexpr size_t kTicketsAt = 256;
-size_t header_bytes(const Plan& plan) { return kTicketsAt + up256((size_t)plan.sms / 2 * 8 * 4); }
+size_t header_bytes(const Plan& plan) { return kTicketsAt + up256((size_t)plan.sms / 2 * kTickets * 4); }
 
+// Three bf16 planes of an fp32 matrix.
+size_t plane_bytes(int64_t rows, int64_t cols) { return up256((size_t)rows * cols * 6); }
 size_t hidden_bytes(const cp_gated_ffn_t* p) {
+  if (split_rows(p)) return plane_bytes(p->T, p->F);
   return up256((size_t)p->T * p->F * (p->dtype == CP_BF16 ? 2 : 4));
+}
+size_t operand_bytes(const cp_gated_ffn_t* p, bool backward) {   // planes of the call's inputs
+  if (!split_rows(p)) return 0;
+  return plane_bytes(p->T, p->D) + 2 * plane_bytes(p->F, p->D) + plane_bytes(p->D_out, p->F) +
+         (backward ? plane_bytes(p->T, p->D_out) : 0);
 }
 
 size_t fwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
-  return header_bytes(plan) + hidden_bytes(p) + up256(plan.fwd_partial);
+  return header_bytes(plan) + hidden_bytes(p) + operand_bytes(p, false) + up256(plan.fwd_partial);
 }
 size_t bwd_bytes(const cp_gated_ffn_t* p, const Plan& plan) {
-  return header_bytes(plan) + 3 * hidden_bytes(p) + up256(plan.bwd_partial);
+  return header_bytes(plan) + 3 * hidden_bytes(p) + operand_bytes(p, true) +
+         up256(plan.bwd_partial);
 }
 
 cp_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -207,19 +222,18 @@ bool make_map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows, con
 
 // A launch of products under construction; failures stick.  What is set belongs to the
 // product added last.
+template <class Args>
 struct Products {
-  GemmArgs g = {};
+  Args g = {};
   const Launch& plan;
   int epilogue;
-  GemmProblem* p = nullptr;
+  decltype(&g.p[0]) p = nullptr;
   int64_t units = 0;
   int slots = 0, shared = 0;
   const char* err = nullptr;
 
-  Products(int epi, const Launch& l, int follows, uint8_t* ws, void* partial)
-      : plan(l), epilogue(epi) {
+  Products(int epi, const Launch& l, uint8_t* ws, void* partial) : plan(l), epilogue(epi) {
     g.partial = static_cast<float*>(partial);
-    g.follows = follows;
     g.status = reinterpret_cast<int32_t*>(ws);
     g.tickets = reinterpret_cast<int32_t*>(ws + kTicketsAt);
     g.wait_limit = device_wait_limit();
@@ -244,12 +258,27 @@ struct Products {
     slots += cut * c.shares;
     shared += cut;
   }
+  int a_rows() const { return p->a_mn ? 64 : kGemmM / 2; }   // of a box
+  int b_rows() const { return p->b_mn ? 64 : plan.tile_n / 2; }
+  cp_status_t ready(const char* what) {
+    if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
+    if (units >= (int64_t)1 << 30) return entry_fail(CP_ERR_SHAPE, "too many tiles");
+    g.units = (int)units;
+    return CP_OK;
+  }
+};
+
+struct Bf16Products : Products<GemmArgs> {
+  Bf16Products(int epi, const Launch& l, int follows, uint8_t* ws, void* partial)
+      : Products(epi, l, ws, partial) {
+    g.follows = follows;
+  }
   void map(CUtensorMap* m, const Matrix& x, int elem, int cols, int rows) {
     const char* e = nullptr;
     if (!make_map(m, x, elem, cols, rows, &e) && !err) err = e;
   }
-  void a(int i, const Matrix& m) { map(&p->a[i], m, 2, kGemmK, p->a_mn ? 64 : kGemmM / 2); }
-  void b(int i, const Matrix& m) { map(&p->b[i], m, 2, kGemmK, p->b_mn ? 64 : plan.tile_n / 2); }
+  void a(int i, const Matrix& m) { map(&p->a[i], m, 2, kGemmK, a_rows()); }
+  void b(int i, const Matrix& m) { map(&p->b[i], m, 2, kGemmK, b_rows()); }
   void box(CUtensorMap* m, void* at, int elem, int64_t stride) {   // what an epilogue moves
     map(m, {at, p->M, p->N, stride}, elem, elem == 4 ? 32 : 64, 32);
   }
@@ -273,16 +302,37 @@ struct Products {
   }
 
   cp_status_t run(int sms, cudaStream_t st, const char* what) {
-    if (err) return entry_fail(CP_ERR_CUDA, std::string(what) + ": " + err);
-    if (units >= (int64_t)1 << 30) return entry_fail(CP_ERR_SHAPE, "too many tiles");
-    g.units = (int)units;
+    const cp_status_t e = ready(what);
+    if (e != CP_OK) return e;
     ENTRY_CUDA(launch_gemm_bf16(g, epilogue, plan.tile_n, sms, st), what);
     return CP_OK;
   }
 };
 
+// Planes of an fp32 matrix of the call.
+struct Planes {
+  void* p;
+  int64_t rows, cols;
+};
+struct SplitProducts : Products<SplitArgs> {
+  SplitProducts(int epi, const Launch& l, uint8_t* ws, void* partial)
+      : Products(epi, l, ws, partial) {}
+  void map(CUtensorMap* m, const Planes& x, int rows) {
+    const char* e = nullptr;
+    if (!make_tmap_planes(m, x.p, x.rows, x.cols, rows, &e) && !err) err = e;
+  }
+  void a(int i, const Planes& m) { map(&p->a[i], m, a_rows()); }
+  void b(int i, const Planes& m) { map(&p->b[i], m, b_rows()); }
+  cp_status_t run(int sms, cudaStream_t st, const char* what) {
+    const cp_status_t e = ready(what);
+    if (e != CP_OK) return e;
+    ENTRY_CUDA(launch_gemm_split(g, epilogue, sms, st), what);
+    return CP_OK;
+  }
+};
+
 // The header is cleared by the call's first launch itself where that shares no tiles.
-cp_status_t clear_header(const Plan& plan, Products& first, uint8_t* ws, cudaStream_t st) {
+cp_status_t clear_header(const Plan& plan, Bf16Products& first, uint8_t* ws, cudaStream_t st) {
   if (first.plan.shared())
     ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
   else
@@ -359,7 +409,7 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   void* partial = ws + header_bytes(plan) + hidden_bytes(p);
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   cp_status_t e;
-  Products gu(GEMM_GLU, plan.gate_up, FOLLOWS_NONE, ws, partial);
+  Bf16Products gu(GEMM_GLU, plan.gate_up, FOLLOWS_NONE, ws, partial);
   gu.add(T, F, false, false, D);
   gu.a(0, {x, T, D, p->x_stride});
   gu.b(0, {wg, F, D, p->w_gate_stride});
@@ -369,7 +419,7 @@ cp_status_t fwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   gu.kept(gate, up);
   if ((e = clear_header(plan, gu, ws, st)) != CP_OK) return e;
   if ((e = gu.run(plan.sms, st, "gate and up projections")) != CP_OK) return e;
-  Products down(GEMM_STORE, plan.down, FOLLOWS_A, ws, partial);
+  Bf16Products down(GEMM_STORE, plan.down, FOLLOWS_A, ws, partial);
   down.add(T, O, false, false, F);
   down.a(0, {h, T, F, F});
   down.b(0, {wd, O, F, p->w_down_stride});
@@ -387,7 +437,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   const int T = p->T, D = p->D, F = p->F, O = p->D_out;
   const bool wide = p->grad_dtype == CP_F32;
   cp_status_t e;
-  Products dh(GEMM_DGLU, plan.dh, FOLLOWS_NONE, ws, partial);
+  Bf16Products dh(GEMM_DGLU, plan.dh, FOLLOWS_NONE, ws, partial);
   dh.add(T, F, false, true, O);
   dh.a(0, {dy, T, O, p->dy_stride});
   dh.b(0, {wd, O, F, p->w_down_stride});
@@ -400,7 +450,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
 
   const int in = (dwg != nullptr) + (dwu != nullptr);
   const Launch rest = plan_gradients(p, plan.pairs(), dx, in, dwd);
-  Products q(GEMM_STORE, rest, dx && !in && !dwd ? FOLLOWS_A : FOLLOWS_BOTH, ws, partial);
+  Bf16Products q(GEMM_STORE, rest, dx && !in && !dwd ? FOLLOWS_A : FOLLOWS_BOTH, ws, partial);
   auto input = [&] {   // dg Wg + du Wu as one product, k running through both
     q.add(T, D, false, true, F);
     q.p->k_tiles *= 2;
@@ -427,6 +477,120 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
     q.a(0, {dy, T, O, p->dy_stride});
     q.b(0, {h, T, F, F});
     q.out(0, dwd, wide);
+  }
+  if (dx && !dx_first(p)) input();
+  return q.run(plan.sms, st, "gradients");
+}
+
+// fp32 on the tensor cores: the inputs' planes in one launch, then the products.
+struct Operands {
+  SplitPass s = {};
+  uint8_t* at;
+
+  Operands(const Plan& plan, uint8_t* ws, size_t hidden) : at(ws + header_bytes(plan) + hidden) {
+    s.status = reinterpret_cast<int32_t*>(ws);
+    s.clear = (int)(header_bytes(plan) / 4);
+  }
+  Planes add(const void* src, int64_t rows, int64_t cols, int64_t stride, bool wanted = true) {
+    const Planes r = {at, rows, cols};
+    at += plane_bytes(rows, cols);
+    if (!wanted) return r;
+    auto& m = s.m[s.n++];
+    m.src = static_cast<const float*>(src);
+    m.planes = static_cast<__nv_bfloat16*>(r.p);
+    m.rows = rows;
+    m.cols = (int)cols;
+    m.stride = rows > 1 ? stride : cols;
+    return r;
+  }
+};
+
+cp_status_t fwd_split(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                      const void* wu, const void* wd, void* y, void* gate, void* up, uint8_t* ws,
+                      cudaStream_t st) {
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  const Planes h = {ws + header_bytes(plan), T, F};
+  Operands in(plan, ws, hidden_bytes(p));
+  const Planes px = in.add(x, T, D, p->x_stride), pg = in.add(wg, F, D, p->w_gate_stride),
+               pu = in.add(wu, F, D, p->w_up_stride), pd = in.add(wd, O, F, p->w_down_stride);
+  void* partial = in.at;
+  ENTRY_CUDA(launch_split(in.s, st), "planes of the inputs");
+  cp_status_t e;
+  SplitProducts gu(GEMM_GLU, plan.gate_up, ws, partial);
+  gu.add(T, F, false, false, D);
+  gu.a(0, px);
+  gu.b(0, pg);
+  gu.b(1, pu);
+  gu.g.act = p->activation;
+  gu.g.gate = static_cast<float*>(gate);
+  gu.g.up = static_cast<float*>(up);
+  gu.g.h = static_cast<__nv_bfloat16*>(h.p);
+  if ((e = gu.run(plan.sms, st, "gate and up projections")) != CP_OK) return e;
+  SplitProducts down(GEMM_STORE, plan.down, ws, partial);
+  down.add(T, O, false, false, F);
+  down.a(0, h);
+  down.b(0, pd);
+  down.p->out[0] = static_cast<float*>(y);
+  return down.run(plan.sms, st, "down projection");
+}
+
+cp_status_t bwd_split(const cp_gated_ffn_t* p, const Plan& plan, const void* x, const void* wg,
+                      const void* wu, const void* wd, const void* gate, const void* up,
+                      const void* dy, void* dx, void* dwg, void* dwu, void* dwd, uint8_t* ws,
+                      cudaStream_t st) {
+  const int T = p->T, D = p->D, F = p->F, O = p->D_out;
+  uint8_t* at = ws + header_bytes(plan);
+  const size_t hidden = hidden_bytes(p);
+  const Planes dg = {at, T, F}, du = {at + hidden, T, F}, h = {at + 2 * hidden, T, F};
+  const int n_in = (dwg != nullptr) + (dwu != nullptr);
+  Operands in(plan, ws, 3 * hidden);
+  const Planes px = in.add(x, T, D, p->x_stride, n_in > 0),
+               pg = in.add(wg, F, D, p->w_gate_stride, dx),
+               pu = in.add(wu, F, D, p->w_up_stride, dx),
+               pd = in.add(wd, O, F, p->w_down_stride), py = in.add(dy, T, O, p->dy_stride);
+  void* partial = in.at;
+  ENTRY_CUDA(launch_split(in.s, st), "planes of the inputs");
+  cp_status_t e;
+  SplitProducts dh(GEMM_DGLU, plan.dh, ws, partial);
+  dh.add(T, F, false, true, O);
+  dh.a(0, py);
+  dh.b(0, pd);
+  dh.g.act = p->activation;
+  dh.g.gate = static_cast<float*>(const_cast<void*>(gate));
+  dh.g.up = static_cast<float*>(const_cast<void*>(up));
+  dh.g.h = static_cast<__nv_bfloat16*>(h.p);
+  dh.g.dgate = static_cast<__nv_bfloat16*>(dg.p);
+  dh.g.dup = static_cast<__nv_bfloat16*>(du.p);
+  if ((e = dh.run(plan.sms, st, "hidden gradients")) != CP_OK) return e;
+
+  const Launch rest = plan_gradients(p, plan.pairs(), dx, n_in, dwd);
+  SplitProducts q(GEMM_STORE, rest, ws, partial);
+  auto input = [&] {
+    q.add(T, D, false, true, F);
+    q.p->k_tiles *= 2;
+    q.a(0, dg);
+    q.a(1, du);
+    q.b(0, pg);
+    q.b(1, pu);
+    q.p->out[0] = static_cast<float*>(dx);
+  };
+  if (dx && dx_first(p)) input();
+  if (n_in) {
+    q.add(F, D, true, true, T);
+    q.a(0, dwg ? dg : du);
+    q.p->out[0] = static_cast<float*>(dwg ? dwg : dwu);
+    if (n_in == 2) {
+      q.a(1, du);
+      q.p->out[1] = static_cast<float*>(dwu);
+      q.p->m_tiles *= 2;
+    }
+    q.b(0, px);
+  }
+  if (dwd) {
+    q.add(O, F, true, true, T);
+    q.a(0, py);
+    q.b(0, h);
+    q.p->out[0] = static_cast<float*>(dwd);
   }
   if (dx && !dx_first(p)) input();
   return q.run(plan.sms, st, "gradients");
@@ -612,6 +776,8 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
     return fwd_rows(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   if (desc->dtype == CP_BF16 && !batch_rows(desc))
     return fwd_bf16(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
+  if (split_rows(desc))
+    return fwd_split(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
   ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
   return batch_rows(desc) ? fwd_tokens(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st)
                           : fwd_f32(desc, plan, x, w_gate, w_up, w_down, y, gate, up, ws, st);
@@ -651,6 +817,9 @@ cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if (desc->dtype == CP_BF16)
     return bwd_bf16(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up, dw_down,
                     ws, st);
+  if (split_rows(desc))
+    return bwd_split(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up,
+                     dw_down, ws, st);
   ENTRY_CUDA(cudaMemsetAsync(ws, 0, header_bytes(plan), st), "clear the status word");
   return bwd_f32(desc, plan, x, w_gate, w_up, w_down, gate, up, dy, dx, dw_gate, dw_up, dw_down, ws,
                  st);

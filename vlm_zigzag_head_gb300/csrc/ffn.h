@@ -2,6 +2,7 @@
 // for fp32) and the passes between them (kernel launchers).
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -14,6 +15,8 @@ enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 // bytes in the swizzle of that size.
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                       int64_t stride, int elem, int box_cols, int box_rows, const char** err);
+bool make_tmap_planes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                      int box_rows, const char** err);
 
 // The projections kept for a bf16 backward are the upper 24 bits of their fp32 values:
 // a plane [M][N] of upper halves (bf16, cut off), then a plane of the bytes below them,
@@ -39,23 +42,26 @@ enum : int { FOLLOWS_NONE = 0, FOLLOWS_A = 1, FOLLOWS_BOTH = 2 };
 
 // C[M][N] = sum over k of A(m, k) B(n, k).  A tile of either operand is loaded from
 // memory where k runs along a row (K-major) or where m (n) does (MN-major).
-struct GemmProblem {
-  CUtensorMap a[2], b[2];      // box {64, 128} (b: {64, tile_n / 2}) K-major, {64, 64} MN-major
-  CUtensorMap out[2];          // box {64, 32} bf16, {32, 32} fp32
+struct GemmTiles {
   int a_mn, b_mn;      // MN-major (GEMM_GLU: neither; GEMM_DGLU: B alone)
   int M, N;            // of one output
   int m_tiles, n_tiles;
   int m_split;         // m tiles from here on: a[1], out[1] (m_tiles: none)
   int k_tiles;         // all k tiles
   int k_split;         // k tiles from here on: a[1], b[1] (k_tiles: none)
-  int out_f32;
   int first;           // number of its first unit in the launch
   int whole;           // tiles of one unit; each tile after them is `shares` units,
   int shares;          // which share its k and leave their sums in `partial`; the last
                        // to finish adds them in order and goes on with the epilogue
   int first_slot, first_ticket;   // of its shared tiles
 };
+struct GemmProblem : GemmTiles {
+  CUtensorMap a[2], b[2];      // box {64, 128} (b: {64, tile_n / 2}) K-major, {64, 64} MN-major
+  CUtensorMap out[2];          // box {64, 32} bf16, {32, 32} fp32
+  int out_f32;
+};
 constexpr int kGemmProblems = 3;
+constexpr int kTickets = 16;   // of a tile (bf16 products: 8 of them)
 struct GemmArgs {
   GemmProblem p[kGemmProblems];   // GEMM_STORE: one to three, their units one after another
   int problems;
@@ -63,7 +69,7 @@ struct GemmArgs {
   CUtensorMap gate[2], up[2];  // the kept planes, box {64, 32}
   CUtensorMap dgate, dup;      // GEMM_DGLU: written; h goes to out[0]
   float* partial;      // [slot][tile_n / 4][256][4]: columns 4 c .. 4 c + 3
-  int32_t* tickets;    // [shared tile][8]: shares finished; zero before and after
+  int32_t* tickets;    // [shared tile][kTickets]: shares finished; zero before and after
   int follows;         // the launch before is of the same call: this one may start while
                        // it ends (FOLLOWS_A: its weights, B, do not come from there)
   int clear;           // words from `status` on, cleared at the start (no shared tiles)
@@ -75,6 +81,42 @@ struct GemmArgs {
 cudaError_t launch_gemm_bf16(const GemmArgs& g, int epilogue, int tile_n, int sms,
                              cudaStream_t st);
 
+// The same for fp32 operands, each as three bf16 planes that add up to it (24 bits):
+// hi, mid, lo, one behind another, rows contiguous.  Tiles of kGemmM x kSplitN.
+constexpr int kSplitN = 128;
+struct SplitProblem : GemmTiles {
+  CUtensorMap a[2], b[2];      // {cols, rows, plane}, boxes as above (tile_n = kSplitN), one plane
+  float* out[2];               // GEMM_STORE
+};
+struct SplitArgs {
+  SplitProblem p[kGemmProblems];
+  int problems, units;
+  float *gate, *up;            // [M][N]: written (GEMM_GLU, nullable), read (GEMM_DGLU)
+  __nv_bfloat16 *h, *dgate, *dup;   // planes [3][M][N]
+  float* partial;              // as above
+  int32_t* tickets;
+  int act;
+  int32_t* status;
+  long long wait_limit;
+};
+constexpr int kSimtRows = 32;   // of calls that stay on CUDA cores
+// Follows the launch before it on the stream, which must be of the same call.
+cudaError_t launch_gemm_split(const SplitArgs& g, int epilogue, int sms, cudaStream_t st);
+
+// Planes of up to five fp32 matrices; clears `clear` words from `status` on.
+struct SplitPass {
+  struct {
+    const float* src;
+    __nv_bfloat16* planes;
+    int64_t rows, stride;
+    int cols;                  // a multiple of 8
+  } m[5];
+  int n;
+  int32_t* status;
+  int clear;
+};
+cudaError_t launch_split(const SplitPass& s, cudaStream_t st);
+
 // How a launch's products are cut into units: the last tiles, too few for all pairs of
 // CTAs at once, along k where that saves time.
 struct GemmCut {
@@ -83,9 +125,18 @@ struct GemmCut {
   int64_t whole;
   int shares;
 };
+// About the microseconds that a pair takes for a k tile and for the last tile's epilogue,
+// and the fewest k tiles of a share.
+struct GemmCost {
+  int tile_n;
+  double step, epilogue;
+  int least_k;
+};
+GemmCost gemm_cost(int epilogue, int tile_n);
+GemmCost split_cost(int epilogue);
 // Sets whole and shares, the products in the order of the launch; returns about the
 // microseconds that the launch takes.
-double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue);
+double cut_products(GemmCut* p, int n, int pairs, const GemmCost& cost);
 inline size_t partial_bytes(const GemmCut& p, int tile_n) {
   return p.shares < 2 ? 0
                       : (size_t)(p.tiles - p.whole) * p.shares * kGemmM * tile_n * sizeof(float);

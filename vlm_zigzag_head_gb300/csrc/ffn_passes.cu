@@ -179,16 +179,24 @@ __global__ void __launch_bounds__(kTile == 128 ? 256 : 64, kTile == 128 ? 2 : 8)
 
 }  // namespace
 
-// What a pair takes for a k tile, in microseconds (one half as wide reads three quarters
-// of the operands for half the products), and for adding up the shares of a tile, which
-// waits for memory once for every two shares of 64 columns.
-static double step_time(int tile_n) { return tile_n == 256 ? 0.29 : 0.22; }
-static double join_time(int shares, int tile_n) { return 1.5 + 0.4 * shares * tile_n / 64; }
+// A tile half as wide reads three quarters of the operands for half the products.
+GemmCost gemm_cost(int epilogue, int tile_n) {
+  return {tile_n, tile_n == 256 ? 0.29 : 0.22,
+          (epilogue == GEMM_STORE ? 2. : 4.) * tile_n / 256, 4};
+}
+// Six products a k tile.
+GemmCost split_cost(int epilogue) {
+  return {kSplitN, 0.95, epilogue == GEMM_STORE ? 2. : 6., 2};
+}
+
+// Adding up the shares of a tile waits for memory once for every two shares of 64 columns.
+static double unit_time(const GemmCut& c, const GemmCost& cost) {
+  return (c.k_tiles + c.shares - 1) / c.shares * cost.step +
+         (c.shares > 1 ? 1.5 + 0.4 * c.shares * cost.tile_n / 64 : 0.);
+}
 
 // About the time of a launch, its units dealt out to the pairs to and fro.
-static double launch_time(const GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
-  const double step = step_time(tile_n);
-  const double epi = (epilogue == GEMM_STORE ? 2. : 4.) * tile_n / 256;
+static double launch_time(const GemmCut* p, int n, int pairs, const GemmCost& cost) {
   struct {
     int64_t end;
     double time;
@@ -204,13 +212,11 @@ static double launch_time(const GemmCut* p, int n, int pairs, int tile_n, int ep
     longest = std::max(longest, time);
   };
   for (int i = 0; i < n; ++i) {
-    add(p[i].whole, p[i].k_tiles * step);
+    add(p[i].whole, p[i].k_tiles * cost.step);
     if (p[i].shares > 1)
-      add((p[i].tiles - p[i].whole) * p[i].shares,
-          (p[i].k_tiles + p[i].shares - 1) / p[i].shares * step +
-              join_time(p[i].shares, tile_n));
+      add((p[i].tiles - p[i].whole) * p[i].shares, unit_time(p[i], cost));
   }
-  if (units <= pairs) return longest + epi;
+  if (units <= pairs) return longest + cost.epilogue;
   double time = sum / pairs;
   if (units <= 2 * pairs) {
     auto at = [&](int64_t u) {
@@ -229,10 +235,10 @@ static double launch_time(const GemmCut* p, int n, int pairs, int tile_n, int ep
   } else if (units % pairs != 0) {
     time += run[runs - 1].time * (1. - (double)(units % pairs) / pairs);
   }
-  return std::max(time, longest) + epi;
+  return std::max(time, longest) + cost.epilogue;
 }
 
-double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
+double cut_products(GemmCut* p, int n, int pairs, const GemmCost& cost) {
   int64_t total = 0, work = 0;
   for (int i = 0; i < n; ++i) {
     total += p[i].tiles;
@@ -240,21 +246,17 @@ double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
     p[i].whole = p[i].tiles;
     p[i].shares = 1;
   }
-  double best = launch_time(p, n, pairs, tile_n, epilogue);
+  double best = launch_time(p, n, pairs, cost);
   auto consider = [&](const GemmCut* q) {
-    const double t = launch_time(q, n, pairs, tile_n, epilogue);
+    const double t = launch_time(q, n, pairs, cost);
     if (t >= best) return;
     best = t;
     std::copy(q, q + n, p);
   };
-  auto unit_time = [&](const GemmCut& c) {
-    return (c.k_tiles + c.shares - 1) / c.shares * step_time(tile_n) +
-           (c.shares > 1 ? join_time(c.shares, tile_n) : 0.);
-  };
   GemmCut q[kGemmProblems];
 
   // The last round's tiles: the product whose units are longest is cut further while that
-  // pays and there are pairs left and four k tiles a share.
+  // pays and there are pairs left and enough k tiles a share.
   std::copy(p, p + n, q);
   int tail[kGemmProblems] = {}, left = (int)(total % pairs), free = pairs - left;
   for (int i = n - 1; i >= 0; --i) {
@@ -264,12 +266,12 @@ double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
   for (;;) {
     int i = -1;
     for (int j = 0; j < n; ++j)
-      if (tail[j] && (i < 0 || unit_time(q[j]) > unit_time(q[i]))) i = j;
-    if (i < 0 || tail[i] > free || q[i].k_tiles / (q[i].shares + 1) < 4) break;
+      if (tail[j] && (i < 0 || unit_time(q[j], cost) > unit_time(q[i], cost))) i = j;
+    if (i < 0 || tail[i] > free || q[i].k_tiles / (q[i].shares + 1) < cost.least_k) break;
     GemmCut more = q[i];
     ++more.shares;
     more.whole = more.tiles - tail[i];
-    if (unit_time(more) >= unit_time(q[i])) break;
+    if (unit_time(more, cost) >= unit_time(q[i], cost)) break;
     free -= tail[i];
     q[i] = more;
   }
@@ -282,11 +284,11 @@ double cut_products(GemmCut* p, int n, int pairs, int tile_n, int epilogue) {
   for (int i = 0; i < n; ++i) {
     q[i].whole = p[i].tiles;
     q[i].shares = 1;
-    const int most = std::min((p[i].k_tiles + part - 1) / part, p[i].k_tiles / 4);
+    const int most = std::min((p[i].k_tiles + part - 1) / part, p[i].k_tiles / cost.least_k);
     for (GemmCut more = q[i]; more.shares < most;) {
       more.whole = 0;
       ++more.shares;
-      if (unit_time(more) >= unit_time(q[i])) break;
+      if (unit_time(more, cost) >= unit_time(q[i], cost)) break;
       q[i] = more;
       any = true;
     }

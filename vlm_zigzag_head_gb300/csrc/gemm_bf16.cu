@@ -28,6 +28,7 @@
 #include "check.cuh"
 #include "ffn.h"
 #include "ffn_act.cuh"
+#include "gemm_units.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -41,8 +42,6 @@ constexpr int kEpiWarps = 8;
 constexpr int kRows = kGemmM / 2;                   // of A in one CTA
 constexpr int kTileA = kRows * kGemmK * 2;          // bytes of a CTA's part of a stage
 constexpr int kBf16Box = 32 * 64 * 2, kByteBox = 32 * 64;
-constexpr long long kDrainLimit = 1LL << 24;
-constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 // Stages, and the boxes of two warps: two of bf16 (or two halves of fp32); h, gate, up
 // and the low bytes; gate, up, low bytes in, dgate, dup, h out.
 template <int kEpi, int kN>
@@ -71,100 +70,6 @@ struct Bars {
   int abort;
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
-
-// m tiles whose n tiles are walked together: about square patches of tiles run at a
-// time, which reads the least of A and B.
-constexpr int kGroupM = 8;
-
-// Unit u: a tile of a problem, and which of its k tiles.  The issuing thread asks for
-// no more: between two tiles the tensor core waits for it.
-struct Work {
-  int p, tile, k0, k1;
-  int slot, share, ticket;   // of the partial sums, the slot -1 for a whole tile
-};
-__device__ __forceinline__ Work work_at(const GemmArgs& g, int u) {
-  Work w;
-  w.p = 0;
-  while (w.p + 1 < g.problems && u >= g.p[w.p + 1].first) ++w.p;
-  const GemmProblem& p = g.p[w.p];
-  w.tile = u - p.first;
-  w.slot = -1;
-  w.share = w.ticket = 0;
-  unsigned shares = 1;
-  if (w.tile >= p.whole) {
-    const unsigned v = w.tile - p.whole;
-    shares = p.shares;
-    w.ticket = p.first_ticket + (int)(v / shares);
-    w.share = (int)(v % shares);
-    w.tile = p.whole + (int)(v / shares);
-    w.slot = p.first_slot + (int)v;
-  }
-  const unsigned k_tiles = p.k_tiles;
-  w.k0 = w.share == 0 ? 0 : (int)(k_tiles * w.share / shares);
-  w.k1 = w.share + 1 == (int)shares ? (int)k_tiles : (int)(k_tiles * (w.share + 1) / shares);
-  return w;
-}
-struct Unit : Work {
-  int m, n;
-};
-__device__ __forceinline__ Unit unit_at(const GemmArgs& g, int u) {
-  Unit t;
-  static_cast<Work&>(t) = work_at(g, u);
-  const GemmProblem& p = g.p[t.p];
-  const unsigned per_group = kGroupM * p.n_tiles;
-  const unsigned group = t.tile / per_group, in = t.tile % per_group;
-  const unsigned first = group * kGroupM;
-  const unsigned rows = min(kGroupM, p.m_tiles - (int)first);
-  t.m = (int)(first + in % rows);
-  t.n = (int)(in / rows);
-  return t;
-}
-
-__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
-  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
-  *abort = 1;
-}
-
-// 32 columns (pieces 8 c .. 8 c + 7) of tile row `row` into a shared tile's sums.
-template <int kN>
-__device__ __forceinline__ void store_partial(const GemmArgs& g, int slot, int col, int row,
-                                              const float (&f)[32]) {
-  float4* p = reinterpret_cast<float4*>(g.partial) +
-              ((int64_t)slot * (kN / 4) + col / 4) * kGemmM + row;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-}
-
-// The same columns of all shares of a tile, from slot `slot` on, added in order.
-template <int kN>
-__device__ __forceinline__ void load_partials(const GemmArgs& g, int slot, int shares, int col,
-                                              int row, float (&f)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = 0.f;
-#pragma unroll 2
-  for (int s = 0; s < shares; ++s) {
-    const float4* p = reinterpret_cast<const float4*>(g.partial) +
-                      ((int64_t)(slot + s) * (kN / 4) + col / 4) * kGemmM + row;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 v = __ldcg(p + i * kGemmM);   // written by other CTAs of this launch
-      f[4 * i] += v.x;
-      f[4 * i + 1] += v.y;
-      f[4 * i + 2] += v.z;
-      f[4 * i + 3] += v.w;
-    }
-  }
-}
-
-__device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
-  uint32_t r[32];
-  tmem_ld32(taddr, r);
-  tmem_ld_wait();
-  reg_fence32(r);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-}
 
 // 16-byte piece p of a lane's row in a box of 64- or 128-byte rows, as TMA's swizzle
 // of that size places it; the eight lanes of a pass meet no bank twice.
@@ -460,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int col = c * 64 + half * 32;
           float x[32];
           load_acc(acc + col, x);
-          if (in) store_partial<kN>(g, t.slot, col, tile_row, x);
+          if (in) store_partial<kN>(g.partial, t.slot, col, tile_row, x);
           __syncwarp();   // the next load of the accumulator is the whole warp's
         }
         release();
@@ -469,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         pair_sync();
         bool last = true;
         if (issues) {
-          int32_t* ticket = g.tickets + t.ticket * 8 + rank * 4 + quarter;
+          int32_t* ticket = g.tickets + t.ticket * kTickets + rank * 4 + quarter;
           last = atomicAdd(ticket, 1) == p.shares - 1;
           if (last) *ticket = 0;
           __threadfence();
@@ -485,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!shared) {
             load_acc(acc + at, f);
           } else if (row0 + lane < p.M) {
-            load_partials<kN>(g, t.slot - t.share, p.shares, at, tile_row, f);
+            load_partials<kN>(g.partial, t.slot - t.share, p.shares, at, tile_row, f);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = 0.f;

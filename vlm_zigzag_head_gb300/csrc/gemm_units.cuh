@@ -1,0 +1,111 @@
+// Work split of the feed-forward products' persistent kernels: units of (product, tile,
+// share of k), and the sums of shared tiles.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ffn.h"
+#include "ptx.cuh"
+
+namespace cpattn {
+
+constexpr long long kDrainLimit = 1LL << 24;
+constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
+
+// m tiles whose n tiles are walked together: about square patches of tiles run at a
+// time, which reads the least of A and B.
+constexpr int kGroupM = 8;
+
+// Unit u: a tile of a problem, and which of its k tiles.  The issuing thread asks for
+// no more: between two tiles the tensor core waits for it.
+struct Work {
+  int p, tile, k0, k1;
+  int slot, share, ticket;   // of the partial sums, the slot -1 for a whole tile
+};
+template <class Args>
+__device__ __forceinline__ Work work_at(const Args& g, int u) {
+  Work w;
+  w.p = 0;
+  while (w.p + 1 < g.problems && u >= g.p[w.p + 1].first) ++w.p;
+  const GemmTiles& p = g.p[w.p];
+  w.tile = u - p.first;
+  w.slot = -1;
+  w.share = w.ticket = 0;
+  unsigned shares = 1;
+  if (w.tile >= p.whole) {
+    const unsigned v = w.tile - p.whole;
+    shares = p.shares;
+    w.ticket = p.first_ticket + (int)(v / shares);
+    w.share = (int)(v % shares);
+    w.tile = p.whole + (int)(v / shares);
+    w.slot = p.first_slot + (int)v;
+  }
+  const unsigned k_tiles = p.k_tiles;
+  w.k0 = w.share == 0 ? 0 : (int)(k_tiles * w.share / shares);
+  w.k1 = w.share + 1 == (int)shares ? (int)k_tiles : (int)(k_tiles * (w.share + 1) / shares);
+  return w;
+}
+struct Unit : Work {
+  int m, n;
+};
+template <class Args>
+__device__ __forceinline__ Unit unit_at(const Args& g, int u) {
+  Unit t;
+  static_cast<Work&>(t) = work_at(g, u);
+  const GemmTiles& p = g.p[t.p];
+  const unsigned per_group = kGroupM * p.n_tiles;
+  const unsigned group = t.tile / per_group, in = t.tile % per_group;
+  const unsigned first = group * kGroupM;
+  const unsigned rows = min(kGroupM, p.m_tiles - (int)first);
+  t.m = (int)(first + in % rows);
+  t.n = (int)(in / rows);
+  return t;
+}
+
+__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
+  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
+  *abort = 1;
+}
+
+// 32 columns (pieces 8 c .. 8 c + 7) of tile row `row` into a shared tile's sums.
+template <int kN>
+__device__ __forceinline__ void store_partial(float* partial, int slot, int col, int row,
+                                              const float (&f)[32]) {
+  float4* p = reinterpret_cast<float4*>(partial) +
+              ((int64_t)slot * (kN / 4) + col / 4) * kGemmM + row;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+}
+
+// The same columns of all shares of a tile, from slot `slot` on, added in order.
+template <int kN>
+__device__ __forceinline__ void load_partials(const float* partial, int slot, int shares, int col,
+                                              int row, float (&f)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = 0.f;
+#pragma unroll 2
+  for (int s = 0; s < shares; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(partial) +
+                      ((int64_t)(slot + s) * (kN / 4) + col / 4) * kGemmM + row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = __ldcg(p + i * kGemmM);   // written by other CTAs of this launch
+      f[4 * i] += v.x;
+      f[4 * i + 1] += v.y;
+      f[4 * i + 2] += v.z;
+      f[4 * i + 3] += v.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
+  uint32_t r[32];
+  ptx::tmem_ld32(taddr, r);
+  ptx::tmem_ld_wait();
+  ptx::reg_fence32(r);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+
+}  // namespace cpattn

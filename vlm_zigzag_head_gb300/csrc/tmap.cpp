@@ -127,4 +127,27 @@ bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t 
   return true;
 }
 
+// Three bf16 planes [rows][cols] one behind another: dims (innermost first) {cols, rows, 3},
+// box {64, box_rows, 1} in the 128-byte swizzle; cols a multiple of 8.
+bool make_tmap_planes(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                      int box_rows, const char** err) {
+  auto fn = encode_fn();
+  if (!fn) {
+    *err = "cuTensorMapEncodeTiled unavailable";
+    return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 3};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)rows * cols * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled failed (planes)";
+    return false;
+  }
+  return true;
+}
+
 }  // namespace cpattn
