@@ -478,8 +478,11 @@ cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const 
  *
  * CP_BF16: tensor cores, sums and activation in fp32; h, dg and du are rounded to
  * bf16 once, as operands of the next product, and the results once; g and u are
- * kept for the backward to 24 bits (2^-15 of the value).  CP_F32: CUDA cores, fp32 throughout.  A NaN or infinity reaches the rows of
- * y, dx and the parts of the weights' gradients that the formulas give it.
+ * kept for the backward to 24 bits (2^-15 of the value).  CP_F32: nothing is rounded
+ * below fp32; beyond 64 rows every factor is three bf16 values that add up to it (to
+ * 2^-110) and the products' sums are in fp32.  A NaN or infinity reaches the rows of y, dx
+ * and the parts of the weights' gradients that the formulas give it (an fp32 infinity as a
+ * NaN).
  *
  *   x [T][D], dy [T][D_out], w_gate, w_up [F][D], w_down [D_out][F]   row strides in
  *                   elements; rows do not overlap (e.g. halves of one [2 F][D] weight)

@@ -323,3 +323,119 @@ def test_waits_that_run_out_are_reported():
     assert all(s in (0, 7) for s in seen) and 7 in seen, seen
     assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws), y)
     assert cp.cp_workspace_status(ws) == 0
+
+
+# ---- fp32 of more than 64 rows: factors as three bf16 values, six products of them
+
+SPLIT = [(65, 72, 136, 40, "silu"), (517, 512, 1360, 512, "gelu"), (700, 2048, 264, 520, "silu"),
+         (2500, 136, 72, 264, "gelu_tanh"), (300, 8, 8, 8, "silu"), (128, 1024, 2816, 1032, "silu"),
+         (1100, 520, 1032, 264, "silu")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,F,D_out,act", SPLIT)
+def test_fp32_of_many_rows(T, D, F, D_out, act):
+    import vlm_zigzag_head_gb300 as cp
+    x, wg, wu, wd, dy = _inputs(T, D, F, D_out, torch.float32, T + D + F)
+    ws = cp.Workspace()
+    y, gate, up = cp.cp_gated_ffn_fwd(x, wg, wu, wd, act, keep=True, workspace=ws)
+    assert cp.cp_workspace_status(ws) == 0
+    assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, act), y)
+    full = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, workspace=ws)
+    assert cp.cp_workspace_status(ws) == 0
+    _check((y, *full), x, wg, wu, wd, dy, act, torch.float32, torch.float32)
+    again = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act)
+    assert all(torch.equal(a, b) for a, b in zip(full, again))
+    for wanted in ((True, False, False, True), (False, True, False, False), (False, False, True, True)):
+        some = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, wanted=list(wanted), workspace=ws)
+        assert cp.cp_workspace_status(ws) == 0
+        _check((y, *some), x, wg, wu, wd, dy, act, torch.float32, torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [72, 200, 520])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 1.0, 2.0 ** 60])
+def test_fp32_keeps_all_digits(n, scale):
+    """Products with a single term that is a value times a power of two give the value's 24 bits:
+    no part of it is lost.  silu(128) = 128 and silu'(128) = 1 in fp32 (e^-128 < 2^-126)."""
+    import vlm_zigzag_head_gb300 as cp
+    g = torch.Generator().manual_seed(n)
+    eye = torch.eye(n, device=DEV)
+    values, dy = ((torch.randn(n, n, generator=g) * scale).to(DEV) for _ in range(2))
+    x, wg, wu = 128 * eye, eye, eye / 16384          # g = 128 on the diagonal, u = 1 / 128, h = 1
+    y, gate, up = cp.cp_gated_ffn_fwd(x, wg, wu, values, keep=True)
+    assert torch.equal(y, values.t())
+    dwd = cp.cp_gated_ffn_bwd(x, wg, wu, values, gate, up, dy, wanted=[False, False, False, True])[3]
+    assert torch.equal(dwd, dy.t())
+    # the down weight an identity: dh = dy, of which the diagonal goes on: dg = dy / 128, du = 128 dy
+    dx, dwg, dwu, _ = cp.cp_gated_ffn_bwd(x, wg, wu, eye, gate, up, dy)
+    diag = torch.diag(torch.diag(dy))
+    assert torch.equal(dx, diag / 64) and torch.equal(dwg, diag) and torch.equal(dwu, diag * 16384)
+    # rows of 24 bits: u = x / 128 where the gates are 128
+    up_w, rows = torch.zeros(n, n + 8, device=DEV), torch.zeros(n, n + 8, device=DEV)
+    gate_w = torch.zeros(n, n + 8, device=DEV)
+    gate_w[:, 0] = 128.0
+    rows[:, 0], rows[:, 8:], up_w[:, 8:] = 1.0, values, eye / 128
+    assert torch.equal(cp.cp_gated_ffn_fwd(rows, gate_w, up_w, eye), values)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_fp32_nonfinite_rows_stay_rows(bad):
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(6, 300, dtype=torch.float32)
+    clean = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy)
+    worse = x.clone()
+    worse[150, 3] = bad
+    yb, gb, ub = cp.cp_gated_ffn_fwd(worse, wg, wu, wd, keep=True)
+    db = cp.cp_gated_ffn_bwd(worse, wg, wu, wd, gb, ub, dy)
+    keep = torch.arange(300, device=DEV) != 150
+    assert not yb[150].isfinite().any() and torch.equal(yb[keep], y[keep])
+    assert not db[0][150].isfinite().any() and torch.equal(db[0][keep], clean[0][keep])
+    assert all(not d.isfinite().all() for d in db[1:])
+
+
+@pytest.mark.gpu
+def test_fp32_streams_graphs_and_strides():
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(5, 400, 264, 768, 128, torch.float32)
+    grads = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy)
+    sides, got = [torch.cuda.Stream() for _ in range(3)], []
+    torch.cuda.synchronize()
+    for s in sides:
+        with torch.cuda.stream(s):
+            r = cp.cp_gated_ffn_fwd(x, wg, wu, wd, keep=True)
+            got.append((r, cp.cp_gated_ffn_bwd(x, wg, wu, wd, r[1], r[2], dy)))
+    torch.cuda.synchronize()
+    for r, g in got:
+        assert torch.equal(r[0], y) and all(torch.equal(a, b) for a, b in zip(g, grads))
+    both = torch.cat([wg, wu])                                      # halves of one weight
+    wide = torch.full((400, 264 + 4), float("nan"), device=DEV)     # rows apart
+    wide[:, :264] = x
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        yg, gg, ug = cp.cp_gated_ffn_fwd(wide[:, :264], both[:768], both[768:], wd, keep=True)
+        out = cp.cp_gated_ffn_bwd(wide[:, :264], both[:768], both[768:], wd, gg, ug, dy)
+    for _ in range(2):
+        for t in (yg, *out):
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, y) and all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+@pytest.mark.gpu
+def test_fp32_waits_that_run_out_are_reported():
+    cp, x, wg, wu, wd, dy, y, gate, up = _call(8, 600, 512, 1024, 512, torch.float32)
+    ws, seen = cp.Workspace(), []
+    cp.cp_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws)
+            try:
+                seen.append(cp.cp_workspace_status(ws))
+            except cp.CpError as e:
+                seen.append(e.status)
+    finally:
+        cp.cp_set_wait_limit(0)
+    assert all(s in (0, 7) for s in seen) and 7 in seen, seen
+    assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws), y)
+    assert cp.cp_workspace_status(ws) == 0

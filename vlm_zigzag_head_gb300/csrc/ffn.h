@@ -99,7 +99,7 @@ struct SplitArgs {
   int32_t* status;
   long long wait_limit;
 };
-constexpr int kSimtRows = 32;   // of calls that stay on CUDA cores
+constexpr int kSimtRows = 64;   // of calls that stay on CUDA cores
 // Follows the launch before it on the stream, which must be of the same call.
 cudaError_t launch_gemm_split(const SplitArgs& g, int epilogue, int sms, cudaStream_t st);
 

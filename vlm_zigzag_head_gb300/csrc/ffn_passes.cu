@@ -1,4 +1,4 @@
-// The gated feed-forward block in fp32: its products on CUDA cores, and the passes
+// The gated feed-forward block in fp32, few rows: its products on CUDA cores, and the passes
 // between them.
 #include <cuda_bf16.h>
 
@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
 // shared memory, whose 64 bytes a thread and k take as long as its 64 multiply-adds: 45
 // to 52 TFLOP/s with the larger tile, 38 to 45 with the smaller (a library's 57 to 64).
 // The smaller one where the larger would leave SMs idle (two products 517 x 1360 by
-// 512: 45 us; the larger tile's 110 blocks took 60).
+// 512: 45 us; the larger tile's 110 blocks took 60).  Calls of more than kSimtRows rows
+// take the tensor cores instead.
 constexpr int kStep = 16;
 
 template <int kTile>

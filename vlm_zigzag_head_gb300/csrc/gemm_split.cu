@@ -8,19 +8,23 @@
 // products of parts the six largest are taken,
 //   hi hi + hi mid + mid hi + mid mid + hi lo + lo hi;
 // the others are below 2^-23 of |A| |B| and of random sign (2^-26 in the mean).  The
-// tensor cores cut their sums off at each step, which grows with k: a chain of 4096 was
-// off by 4e-6 of the result, ordered fp32 sums by 1e-6.  So a chain ends after kChain k,
-// and its sums are added in fp32 registers: 2.3e-7.
+// tensor cores cut their sums off at each step, which grows with the steps: a chain of 4096
+// k was off by 4e-6 of the result, fp32 sums by 1e-6.  So a chain ends after kChain k tiles,
+// and its sums are added in fp32 registers; and the five small products, whose steps would
+// cut off the large one's sum, have sums of their own (together 2.3e-6 at 512 k, apart 2.4e-7, fp32 sums 4e-7; at 4096 k 2.6e-7 and 1.2e-6).
 //
-// Six bf16 products take a third of the time that CUDA cores need at their peak, which
-// shared memory keeps them from (45 TFLOP/s here): see the figures at the launch.
+// Six bf16 products are quicker than one on CUDA cores: 2048 x 2048 x 6144 forward 751 us
+// (1236 TFLOP/s of bf16, 206 of fp32), on CUDA cores 3364.  Up to kSimtRows rows the planes
+// of the weights cost more than that saves (64 rows: forward 161 us and 139; 128 rows: 164
+// and 241; backward 231 and 250, 266 and 444).
 //
 // Pairs of CTAs as in gemm_bf16.cu, tiles of 256 x 128 (gate and up: 64 columns of each).
 // A slot of shared memory holds a 64 deep tile of one plane of A and of B; each of the
 // three pairs of slots of a k tile is loaded once and used by the terms that it completes.
-// Epilogue warps hold 64 sums a thread, a row of 64 columns or 32 of gate and of up, and
-// read and write memory directly: a lane's 128 bytes are a line of its own, and with six
-// products to a k tile there is time for it.
+// Epilogue warps hold 64 sums a thread, a row of 64 columns or 32 of gate and of up.  Shared
+// memory is full, so rows go to memory from registers: four lanes exchange their pieces,
+// and write 64 bytes of a row at a time.  (Each lane its own row instead, 16 bytes in each
+// of 32 lines: hidden gradients of 2048 x 2048 x 6144 466 us, 324 so.)
 #include <cuda_bf16.h>
 
 #include "check.cuh"
@@ -46,7 +50,7 @@ constexpr int kChain = 4;                            // k tiles of one accumulat
 constexpr int kBarsAt = 3 * kDepth * kSlot;
 constexpr int kSmem = kBarsAt + 256 + 1024;          // slack for alignment
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-constexpr uint32_t kTmemCols = 2 * kN;               // two accumulators
+constexpr uint32_t kTmemCols = 4 * kN;   // two accumulators of hi hi, and of the rest
 
 struct Bars {
   uint64_t full[3 * kDepth];   // first CTA: both CTAs' loads of a slot have landed
@@ -59,22 +63,97 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
-// Eight values as three planes' 16-byte pieces.
-__device__ __forceinline__ void split8(const float (&f)[8], uint4 (&plane)[3]) {
-  uint32_t w[3][4];
+// Eight values as a 16-byte piece of their next plane, which is taken off them: cut off
+// (the first) or rounded.
+template <bool kCut>
+__device__ __forceinline__ uint4 next_plane(float* f) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = f[2 * i], b = f[2 * i + 1];
-    w[0][i] = upper_halves(a, b);
-    const float ra = a - __uint_as_float(w[0][i] << 16);
-    const float rb = b - __uint_as_float(w[0][i] & 0xffff0000u);
-    w[1][i] = pack_bf16x2(ra, rb);
-    w[2][i] = pack_bf16x2(ra - __uint_as_float(w[1][i] << 16),
-                          rb - __uint_as_float(w[1][i] & 0xffff0000u));
+    w[i] = kCut ? upper_halves(f[2 * i], f[2 * i + 1]) : pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    f[2 * i] -= __uint_as_float(w[i] << 16);
+    f[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
   }
-#pragma unroll
-  for (int p = 0; p < 3; ++p) plane[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// Piece j of lane i (of four) and piece i of lane j change places.
+__device__ __forceinline__ void exchange4(uint4 (&v)[4], int lane) {
+  auto swap = [&](uint4& low, uint4& high, int bit) {
+    const bool up = lane & bit;
+    uint4 s = up ? low : high;
+    s.x = __shfl_xor_sync(0xffffffffu, s.x, bit);
+    s.y = __shfl_xor_sync(0xffffffffu, s.y, bit);
+    s.z = __shfl_xor_sync(0xffffffffu, s.z, bit);
+    s.w = __shfl_xor_sync(0xffffffffu, s.w, bit);
+    (up ? low : high) = s;
+  };
+  swap(v[0], v[1], 1);
+  swap(v[2], v[3], 1);
+  swap(v[0], v[2], 2);
+  swap(v[1], v[3], 2);
+}
+
+// A store of some lanes without a branch: behind one, the lanes of a warp that has rows
+// past the end went on in two groups (33 x 512 x 1360, hidden gradients 89 us, 64 rows 33).
+__device__ __forceinline__ void store_if(bool on, void* p, const uint4& v) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"((uint32_t)on)
+      : "memory");
+}
+
+// A warp's 32 rows and 16 columns of a matrix [M][N], a row in each lane's registers.
+struct Rows {
+  int row, col, M, N, lane;   // row: the first of the lane's four
+  __device__ __forceinline__ void load(const float* p, float (&f)[16]) const {
+    uint4 v[4];
+    const int c = min(col + 4 * (lane & 3), N - 4);   // what lies past the ends is not used
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<const uint4*>(p + (int64_t)min(row + j, M - 1) * N + c);
+    exchange4(v, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[4 * j] = __uint_as_float(v[j].x);
+      f[4 * j + 1] = __uint_as_float(v[j].y);
+      f[4 * j + 2] = __uint_as_float(v[j].z);
+      f[4 * j + 3] = __uint_as_float(v[j].w);
+    }
+  }
+  __device__ __forceinline__ void store(float* p, const float* f) const {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]),
+                        __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3]));
+    exchange4(v, lane);
+    const int c = col + 4 * (lane & 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      store_if(row + j < M && c < N, p + (int64_t)(row + j) * N + c, v[j]);
+  }
+  // pieces 0, 1 and 2, 3 of the rows into one plane each (the second nullable)
+  __device__ __forceinline__ void store_pieces(__nv_bfloat16* p0, __nv_bfloat16* p1,
+                                               uint4 (&v)[4]) const {
+    exchange4(v, lane);
+    __nv_bfloat16* p = lane & 2 ? p1 : p0;
+    const int c = col + 8 * (lane & 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      store_if(p != nullptr && row + j < M && c < N, p + (int64_t)(row + j) * N + c, v[j]);
+  }
+  // the first two planes, the last one's pieces in lo; f is used up
+  __device__ __forceinline__ void store_planes(__nv_bfloat16* p, float* f, uint4* lo) const {
+    uint4 v[4] = {next_plane<true>(f), next_plane<true>(f + 8)};
+    v[2] = next_plane<false>(f);
+    v[3] = next_plane<false>(f + 8);
+    store_pieces(p, p + (int64_t)M * N, v);
+    lo[0] = next_plane<false>(f);
+    lo[1] = next_plane<false>(f + 8);
+  }
+};
 
 template <int kEpi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -188,11 +267,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tc_fence_after();
           }
           const uint32_t base = smem_u32(smem + st * 3 * kSlot);
-          auto term = [&](int a, int b, bool first) {
+          const uint32_t large = tmem + s * 2 * kN, small = large + kN;
+          auto term = [&](uint32_t acc, int a, int b, bool first) {
             const uint32_t pa = base + a * kSlot, pb = base + b * kSlot + kTileA;
 #pragma unroll
             for (int i = 0; i < kGemmK / 16; ++i)
-              mma_bf16_pair(tmem + s * kN, sdesc_sw128(pa + i * a_step, a_lbo, 1024),
+              mma_bf16_pair(acc, sdesc_sw128(pa + i * a_step, a_lbo, 1024),
                             sdesc_sw128(pb + i * b_step, b_lbo, 1024), idesc,
                             first && i == 0 ? 0u : 1u);
           };
@@ -203,14 +283,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (plane == 0) {
-              term(0, 0, starts);
+              term(large, 0, 0, starts);
             } else if (plane == 1) {
-              term(0, 1, false);
-              term(1, 0, false);
-              term(1, 1, false);
+              term(small, 0, 1, starts);
+              term(small, 1, 0, false);
+              term(small, 1, 1, false);
             } else {
-              term(0, 2, false);
-              term(2, 0, false);
+              term(small, 0, 2, false);
+              term(small, 2, 0, false);
             }
           }
           if (!ok) break;
@@ -243,10 +323,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const SplitProblem& p = g.p[t.p];
       const bool second = t.m >= p.m_split;
       const int row = (t.m - (second ? p.m_split : 0)) * kGemmM + tile_row;
-      const bool in = row < p.M;
-      float x[2][32];
+      const bool any = row - lane < p.M;   // of the warp's rows
+      float x[64];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[0][i] = x[1][i] = 0.f;
+      for (int i = 0; i < 64; ++i) x[i] = 0.f;
       for (int k = t.k0; k < t.k1; k += kChain, ++n) {
         const int s = n & 1;
         if (!__all_sync(0xffffffffu,
@@ -256,23 +336,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * kN;
-        float f[32];
-        load_acc(acc + col0, f);
+        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + s * 2 * kN;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[0][i] += f[i];
-        load_acc(acc + col1, f);
+        for (int part = kN; part >= 0; part -= kN) {
+          float f[32];
+          load_acc(acc + part + col0, f);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[1][i] += f[i];
+          for (int i = 0; i < 32; ++i) x[i] += f[i];
+          load_acc(acc + part + col1, f);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[32 + i] += f[i];
+        }
         tc_fence_before();   // the next products may overwrite the accumulator
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(in_first_cta(&bars->acc_empty[s]));
       }
       if (!ok) break;
+      auto& x0 = *reinterpret_cast<float(*)[32]>(x);
+      auto& x1 = *reinterpret_cast<float(*)[32]>(x + 32);
       if (t.slot >= 0) {
-        if (in) {
-          store_partial<kN>(g.partial, t.slot, col0, tile_row, x[0]);
-          store_partial<kN>(g.partial, t.slot, col1, tile_row, x[1]);
+        if (any) {
+          store_partial<kN>(g.partial, t.slot, col0, tile_row, x0);
+          store_partial<kN>(g.partial, t.slot, col1, tile_row, x1);
         }
         // this warp's rows of all shares: the last to get here goes on with them
         __threadfence();
@@ -285,75 +370,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __threadfence();
         }
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-        if (in) {
-          load_partials<kN>(g.partial, t.slot - t.share, p.shares, col0, tile_row, x[0]);
-          load_partials<kN>(g.partial, t.slot - t.share, p.shares, col1, tile_row, x[1]);
+        if (any) {
+          load_partials<kN>(g.partial, t.slot - t.share, p.shares, col0, tile_row, x0);
+          load_partials<kN>(g.partial, t.slot - t.share, p.shares, col1, tile_row, x1);
         }
       }
-      if (in) {
-        const int64_t line = (int64_t)row * p.N, plane = (int64_t)p.M * p.N;
-        auto eight = [](const float* f, float (&v)[8]) {
-  #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = f[e];
-        };
-        auto put = [](float* q, const float (&v)[8]) {
-          reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<float4*>(q)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        };
-        auto put_planes = [&](__nv_bfloat16* q, const float (&v)[8]) {
-          uint4 w[3];
-          split8(v, w);
-  #pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(q + i * plane) = w[i];
-        };
+      if (!any) continue;
+      // 16 columns at a time; rolled up, since code that runs once per launch and warp is
+      // waited for line by line
+      Rows to = {row - (lane & 3), t.n * kN + half * 64, p.M, p.N, lane};
+      if (kEpi == GEMM_GLU) to.col = t.n * (kN / 2) + half * 32;
+      constexpr int kRounds = kEpi == GEMM_GLU ? 2 : 4;
+#pragma unroll 1
+      for (int c = 0; c < kRounds; ++c, to.col += 16) {
         if constexpr (kEpi == GEMM_GLU) {
-          const int first = t.n * (kN / 2) + half * 32;
-  #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // eight columns at a time; N is a multiple of 8
-            if (first + 8 * q >= p.N) break;
-            const int64_t at = line + first + 8 * q;
-            float gate[8], up[8], unused;
-            eight(x[0] + 8 * q, gate);
-            eight(x[1] + 8 * q, up);
-            if (g.gate != nullptr) {
-              put(g.gate + at, gate);
-              put(g.up + at, up);
-            }
-  #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              gate[e] = activation<false, false>(gate[e], g.act, unused) * up[e];
-            put_planes(g.h + at, gate);
+          if (g.gate != nullptr) {
+            to.store(g.gate, x);
+            to.store(g.up, x + 32);
+          }
+          float unused;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            x[i] = activation<false, false>(x[i], g.act, unused) * x[32 + i];
+          uint4 lo[4] = {};
+          to.store_planes(g.h, x, lo);
+          to.store_pieces(g.h + 2 * (int64_t)p.M * p.N, nullptr, lo);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            x[i] = x[16 + i];
+            x[32 + i] = x[48 + i];
           }
         } else {
-  #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int col = t.n * kN + half * 64 + 8 * q;
-            if (col >= p.N) break;
-            const int64_t at = line + col;
-            float v[8];
-            eight(x[q / 4] + 8 * (q % 4), v);
-            if constexpr (kEpi == GEMM_STORE) {
-              put(p.out[second] + at, v);
-            } else {
-              float gate[8], up[8];
-              *reinterpret_cast<float4*>(gate) = *reinterpret_cast<const float4*>(g.gate + at);
-              *reinterpret_cast<float4*>(gate + 4) = *reinterpret_cast<const float4*>(g.gate + at + 4);
-              *reinterpret_cast<float4*>(up) = *reinterpret_cast<const float4*>(g.up + at);
-              *reinterpret_cast<float4*>(up + 4) = *reinterpret_cast<const float4*>(g.up + at + 4);
-              float h[8];
-  #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float da;
-                const float a = activation<true, false>(gate[e], g.act, da), dh = v[e];
-                h[e] = a * up[e];
-                gate[e] = dh * up[e] * da;
-                up[e] = dh * a;
-              }
-              put_planes(g.dgate + at, gate);
-              put_planes(g.dup + at, up);
-              put_planes(g.h + at, h);
+          if constexpr (kEpi == GEMM_STORE) {
+            to.store(p.out[second], x);
+          } else {
+            float gate[16], up[16];
+            to.load(g.gate, gate);
+            to.load(g.up, up);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float da;
+              const float a = activation<true, false>(gate[i], g.act, da), dh = x[i];
+              x[i] = a * up[i];
+              gate[i] = dh * up[i] * da;
+              up[i] = dh * a;
             }
+            const int64_t last_plane = 2 * (int64_t)p.M * p.N;
+            uint4 lo[4];
+            to.store_planes(g.dgate, gate, lo);
+            to.store_planes(g.dup, up, lo + 2);
+            to.store_pieces(g.dgate + last_plane, g.dup + last_plane, lo);
+            to.store_planes(g.h, x, lo);
+            to.store_pieces(g.h + last_plane, nullptr, lo);
           }
+#pragma unroll
+          for (int i = 0; i < 48; ++i) x[i] = x[16 + i];
         }
       }
       __syncwarp();   // the next loads of an accumulator are the whole warp's
@@ -387,11 +458,10 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     float f[8];
     *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(m.src + at);
     *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(m.src + at + 4);
-    uint4 w[3];
-    split8(f, w);
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint4*>(m.planes + p * n * 8 + i * 8) = w[p];
+    __nv_bfloat16* to = m.planes + i * 8;
+    *reinterpret_cast<uint4*>(to) = next_plane<true>(f);
+    *reinterpret_cast<uint4*>(to + n * 8) = next_plane<false>(f);
+    *reinterpret_cast<uint4*>(to + 2 * n * 8) = next_plane<false>(f);
   }
 }
 

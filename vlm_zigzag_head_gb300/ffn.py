@@ -90,8 +90,9 @@ def _prepare(x, w_gate, w_up, w_down, activation, grad_dtype, dy=None):
 def cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", *, keep: bool = False,
                      workspace: Optional[Workspace] = None):
     """``y = (a(x w_gate^T) * (x w_up^T)) w_down^T`` of the last dimension of ``x [..., D]``
-    (bf16: tensor cores; fp32: CUDA cores), with ``w_gate``/``w_up [F, D]``, ``w_down [D_out,
-    F]`` and ``a`` one of ``"silu"``, ``"gelu"``, ``"gelu_tanh"``.  D, F, D_out: multiples of
+    (fp32 stays fp32: beyond 64 rows on the tensor cores too, as sums of bf16 parts that lose
+    no digit), with ``w_gate``/``w_up [F, D]``, ``w_down [D_out, F]`` and ``a`` one of
+    ``"silu"``, ``"gelu"``, ``"gelu_tanh"``.  D, F, D_out: multiples of
     8; rows of any stride that lie on 16-byte boundaries.  With ``keep`` returns ``(y, gate,
     up)``, the two projections for :func:`cp_gated_ffn_bwd` as byte tensors in the library's
     layout (bf16: to 24 bits).  Without ``workspace`` each call takes one of its own, so calls
