@@ -439,3 +439,48 @@ def test_fp32_waits_that_run_out_are_reported():
     assert all(s in (0, 7) for s in seen) and 7 in seen, seen
     assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, workspace=ws), y)
     assert cp.cp_workspace_status(ws) == 0
+
+
+FEW = [(1, 8, 8, 8, "silu"), (1, 2048, 6144, 2048, "silu"), (2, 120, 136, 40, "gelu"), (3, 264, 1000, 72, "gelu_tanh"),
+       (4, 1032, 264, 2048, "silu"), (5, 512, 1360, 512, "gelu"), (8, 136, 4104, 8, "silu"), (9, 40, 24, 56, "silu"),
+       (16, 512, 72, 1032, "gelu_tanh"), (23, 264, 520, 264, "silu"), (24, 1000, 2048, 128, "gelu"),
+       (25, 264, 520, 264, "silu"), (33, 136, 264, 72, "silu"), (64, 264, 520, 136, "gelu")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,F,D_out,act", FEW)
+def test_fp32_of_few_rows(T, D, F, D_out, act):
+    import vlm_zigzag_head_gb300 as cp
+    x, wg, wu, wd, dy = _inputs(T, D, F, D_out, torch.float32, T + D + F)
+    ws = cp.Workspace()
+    y, gate, up = cp.cp_gated_ffn_fwd(x, wg, wu, wd, act, keep=True, workspace=ws)
+    assert cp.cp_workspace_status(ws) == 0
+    assert torch.equal(cp.cp_gated_ffn_fwd(x, wg, wu, wd, act), y)
+    grads = cp.cp_gated_ffn_bwd(x, wg, wu, wd, gate, up, dy, act, workspace=ws)
+    _check((y, *grads), x, wg, wu, wd, dy, act, torch.float32, torch.float32)
+    # halves of one weight, rows apart, and NaN behind them
+    both, wide = torch.cat([wg, wu]), torch.full((T, D + 8), float("nan"), device=DEV)
+    wide[:, :D] = x
+    assert torch.equal(cp.cp_gated_ffn_fwd(wide[:, :D], both[:F], both[F:], wd, act), y)
+    # a NaN in one row stays there
+    bad, row = x.clone(), T // 2
+    bad[row, D - 1] = float("nan")
+    yb, keep = cp.cp_gated_ffn_fwd(bad, wg, wu, wd, act), torch.arange(T, device=DEV) != T // 2
+    assert yb[row].isnan().all() and torch.equal(yb[keep], y[keep])
+
+
+@pytest.mark.gpu
+def test_fp32_single_tokens_replayed():
+    """One token a step into a captured graph whose input changes, as a decoding loop has it."""
+    cp, x, wg, wu, wd, dy, *_ = _call(9, 6, 512, 1360, 512, torch.float32)
+    want = [cp.cp_gated_ffn_fwd(x[i:i + 1], wg, wu, wd) for i in range(6)]
+    step = x[:1].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = cp.cp_gated_ffn_fwd(cp.cp_gated_ffn_fwd(step, wg, wu, wd), wg, wu, wd)
+    for i in range(6):
+        step.copy_(x[i:i + 1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, cp.cp_gated_ffn_fwd(want[i], wg, wu, wd))

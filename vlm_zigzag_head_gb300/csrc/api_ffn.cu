@@ -67,7 +67,9 @@ int sm_count() {
 }
 
 // Forward calls that the kernels for few rows take, and for a batch of them.
-bool few_rows(const cp_gated_ffn_t* p) { return p->dtype == CP_BF16 && p->T <= kFewRows; }
+bool few_rows(const cp_gated_ffn_t* p) {
+  return p->T <= (p->dtype == CP_BF16 ? kFewRows : kFewRowsF32);
+}
 bool batch_rows(const cp_gated_ffn_t* p) {
   return p->dtype == CP_BF16 && p->T > kFewRows && p->T <= kBatchRows;
 }
@@ -164,8 +166,10 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
     if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
     return s;
   };
-  r.f32_gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
-  r.f32_down = share(T, O, F, 1, 1, false, &r.fwd_partial);
+  if (!few_rows(p)) {
+    r.f32_gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
+    r.f32_down = share(T, O, F, 1, 1, false, &r.fwd_partial);
+  }
   r.f32_dh = share(T, F, O, 1, 1, true, &r.bwd_partial);
   r.dx = share(T, D, F, 1, 2, false, &r.bwd_partial);
   r.d_down = share(O, F, T, 1, 1, false, &r.bwd_partial);
@@ -358,7 +362,8 @@ cp_status_t fwd_rows(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   a.K = p->D;
   a.act = p->activation;
   a.status = reinterpret_cast<int32_t*>(ws);
-  ENTRY_CUDA(launch_ffn_rows(a, true, plan.sms, st), "gate and up projections");
+  auto launch = p->dtype == CP_F32 ? launch_ffn_rows_f32 : launch_ffn_rows;
+  ENTRY_CUDA(launch(a, true, plan.sms, st), "gate and up projections");
   a.x = a.out;
   a.x_stride = p->F;
   a.w[0] = a.w[1] = wd;
@@ -366,7 +371,7 @@ cp_status_t fwd_rows(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   a.out = y;
   a.N = p->D_out;
   a.K = p->F;
-  ENTRY_CUDA(launch_ffn_rows(a, false, plan.sms, st), "down projection");
+  ENTRY_CUDA(launch(a, false, plan.sms, st), "down projection");
   return CP_OK;
 }
 

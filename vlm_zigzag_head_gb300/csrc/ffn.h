@@ -190,6 +190,10 @@ struct FfnRowsArgs {
   int32_t* status;           // cleared by the first form
 };
 cudaError_t launch_ffn_rows(const FfnRowsArgs& a, bool glu, int sms, cudaStream_t st);
+// The same in fp32 (x, weights, out, gate and up), T <= kFewRowsF32; no second weight in
+// the second form.
+constexpr int kFewRowsF32 = 24;
+cudaError_t launch_ffn_rows_f32(const FfnRowsArgs& a, bool glu, int sms, cudaStream_t st);
 
 // fp32 products on CUDA cores: out[o][share][m][n] = sum over the share's k of
 // A(m, k) B(n, k), an element of A at m * sam + k * sak (one of the strides is 1, the

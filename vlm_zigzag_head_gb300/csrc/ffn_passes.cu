@@ -1,5 +1,5 @@
-// The gated feed-forward block in fp32, few rows: its products on CUDA cores, and the passes
-// between them.
+// The gated feed-forward block: work split of its products, and in fp32 the products of
+// up to kSimtRows rows on CUDA cores with the passes between them.
 #include <cuda_bf16.h>
 
 #include <algorithm>
