@@ -11,13 +11,14 @@
 // The kernel is persistent: pairs walk (product, tile, share of k) units, and two
 // accumulators in tensor memory let a tile's epilogue run under the next one's products.
 //
-// Warp roles (384 threads):
+// Warp roles (576 threads):
 //   warp 0       TMA producer (one lane): this CTA's rows of A and B
 //   warp 1       TMEM allocation; in the first CTA lane 0 issues every MMA
-//   warps 4..11  epilogue: TMEM lane quarter w % 4; the two warps of a quarter have
-//                halves of each 64 columns
+//   warps 2..17  epilogue: TMEM lane quarter w % 4; the four warps of a quarter have
+//                16 of each 64 columns each (by eight warps 2048 x 2048 x 6144 forward
+//                103 us, so 99)
 //
-// The epilogue moves boxes of 32 rows x 64 columns through shared memory by TMA, two
+// The epilogue moves boxes of 32 rows x 64 columns through shared memory by TMA, four
 // warps to a box: a thread holds one row, and rows read and written straight from it
 // (16 bytes in each of 32 lines) took longer than the products.
 //
@@ -37,21 +38,24 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 64 + kEpiWarps * 32;
+constexpr int kParts = kEpiWarps / 4;   // warps that share a box
+constexpr int kCols = 64 / kParts;      // of a box in one of them
+constexpr int kBoxThreads = 32 * kParts;
 constexpr int kRows = kGemmM / 2;                   // of A in one CTA
 constexpr int kTileA = kRows * kGemmK * 2;          // bytes of a CTA's part of a stage
 constexpr int kBf16Box = 32 * 64 * 2, kByteBox = 32 * 64;
-// Stages, and the boxes of two warps: two of bf16 (or two halves of fp32); h, gate, up
+// Stages, and the boxes of a quarter's warps: two of bf16 (or two halves of fp32); h, gate, up
 // and the low bytes; gate, up, low bytes in, dgate, dup, h out.
 template <int kEpi, int kN>
 struct Layout {
-  static constexpr int kPairBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
+  static constexpr int kBoxBytes = kEpi == GEMM_STORE  ? 2 * kBf16Box
                                     : kEpi == GEMM_GLU ? 3 * kBf16Box + 2 * kByteBox
                                                        : 5 * kBf16Box + 2 * kByteBox;
   static constexpr int kTileB = kN / 2 * kGemmK * 2;
   static constexpr int kStage = kTileA + kTileB;
-  static constexpr int kEpiBytes = kEpiWarps / 2 * kPairBytes;
+  static constexpr int kEpiBytes = 4 * kBoxBytes;
   static constexpr int kStages = (224 * 1024 - kEpiBytes) / kStage;   // 4 to 8
   static constexpr int kBoxes = kStages * kStage;
   static constexpr int kBars = kBoxes + kEpiBytes;
@@ -80,25 +84,29 @@ __device__ __forceinline__ uint4* piece(uint8_t* box, int lane, int p) {
                                   ((p ^ (lane * kRowBytes / 128 & kSwap)) << 4));
 }
 
-// A lane's 32 columns, the first or second half of a box's (fp32: a box of their own).
-__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, int half, const float (&f)[32]) {
+// A lane's kCols columns, part `part` of a box's (fp32: of two boxes of 32).
+__device__ __forceinline__ void put_bf16(uint8_t* box, int lane, int part,
+                                         const float (&f)[kCols]) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    *piece<128>(box, lane, half * 4 + p) =
+  for (int p = 0; p < kCols / 8; ++p)
+    *piece<128>(box, lane, part * (kCols / 8) + p) =
         make_uint4(pack_bf16x2(f[8 * p], f[8 * p + 1]), pack_bf16x2(f[8 * p + 2], f[8 * p + 3]),
                    pack_bf16x2(f[8 * p + 4], f[8 * p + 5]), pack_bf16x2(f[8 * p + 6], f[8 * p + 7]));
 }
-__device__ __forceinline__ void put_f32(uint8_t* box, int lane, const float (&f)[32]) {
+__device__ __forceinline__ void put_f32(uint8_t* boxes, int lane, int part,
+                                        const float (&f)[kCols]) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p)
-    *piece<128>(box, lane, p) =
+  for (int p = 0; p < kCols / 4; ++p) {
+    const int at = part * (kCols / 4) + p;
+    *piece<128>(boxes + at / 8 * kBf16Box, lane, at % 8) =
         make_uint4(__float_as_uint(f[4 * p]), __float_as_uint(f[4 * p + 1]),
                    __float_as_uint(f[4 * p + 2]), __float_as_uint(f[4 * p + 3]));
+  }
 }
-__device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, int half,
-                                         const float (&f)[32]) {
+__device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, int part,
+                                         const float (&f)[kCols]) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  for (int p = 0; p < kCols / 16; ++p) {
     uint32_t h[8], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -107,9 +115,10 @@ __device__ __forceinline__ void put_kept(uint8_t* hi, uint8_t* lo, int lane, int
       h[2 * i + 1] = upper_halves(v[2], v[3]);
       l[i] = next_bytes(v[0], v[1], v[2], v[3]);
     }
-    *piece<128>(hi, lane, half * 4 + 2 * p) = make_uint4(h[0], h[1], h[2], h[3]);
-    *piece<128>(hi, lane, half * 4 + 2 * p + 1) = make_uint4(h[4], h[5], h[6], h[7]);
-    *piece<64>(lo, lane, half * 2 + p) = make_uint4(l[0], l[1], l[2], l[3]);
+    const int at = part * (kCols / 16) + p;
+    *piece<128>(hi, lane, 2 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *piece<128>(hi, lane, 2 * at + 1) = make_uint4(h[4], h[5], h[6], h[7]);
+    *piece<64>(lo, lane, at) = make_uint4(l[0], l[1], l[2], l[3]);
   }
 }
 
@@ -302,13 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_wait_cluster(&bars->drain, 0, kDrainLimit, &zero);
       }
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const bool issues = half == 0 && lane == 0;   // of the two warps' boxes
-    const int pair_bar = 1 + quarter;
-    auto pair_sync = [&] { named_sync(pair_bar, 64); };
-    uint8_t* boxes = smem + L::kBoxes + quarter * L::kPairBytes;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    const bool issues = part == 0 && lane == 0;   // of the quarter's boxes
+    const int box_bar = 1 + quarter;
+    auto box_sync = [&] { named_sync(box_bar, kBoxThreads); };
+    uint8_t* boxes = smem + L::kBoxes + quarter * L::kBoxBytes;
     constexpr int kTileN = kEpi == GEMM_GLU ? kN / 2 : kN;
     constexpr int kChunks = kTileN / 64;
     auto first_row = [&](const Unit& t) {
@@ -341,8 +350,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (; ok && unit_of(n) < units; ++n) {
       const Unit t = unit_at(g, unit_of(n));
       const int s = n & 1;
-      // both warps of a box go on, or neither
-      if (!named_all(pair_bar, 64,
+      // all warps of a box go on, or none
+      if (!named_all(box_bar, kBoxThreads,
                      mbar_wait_cluster(&bars->acc_full[s], (n >> 1) & 1, lim, abort))) {
         if (lane == 0) record_timeout(g.status, abort, 33);
         break;
@@ -362,16 +371,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool in = row0 + lane < p.M;
 #pragma unroll 1
         for (int c = 0; c < kN / 64; ++c) {
-          const int col = c * 64 + half * 32;
-          float x[32];
+          const int col = c * 64 + part * kCols;
+          float x[kCols];
           load_acc(acc + col, x);
           if (in) store_partial<kN>(g.partial, t.slot, col, tile_row, x);
           __syncwarp();   // the next load of the accumulator is the whole warp's
         }
         release();
-        // these two warps' rows of all shares: the last to get here goes on with them
+        // these warps' rows of all shares: the last to get here goes on with them
         __threadfence();
-        pair_sync();
+        box_sync();
         bool last = true;
         if (issues) {
           int32_t* ticket = g.tickets + t.ticket * kTickets + rank * 4 + quarter;
@@ -379,39 +388,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (last) *ticket = 0;
           __threadfence();
         }
-        if (!named_all(pair_bar, 64, last)) continue;
+        if (!named_all(box_bar, kBoxThreads, last)) continue;
       }
 #pragma unroll 1
       for (int c = 0; c < kChunks; ++c) {
-        const int col = c * 64 + half * 32, box_col = t.n * kTileN + c * 64;
+        const int col = c * 64 + part * kCols, box_col = t.n * kTileN + c * 64;
         const bool stores = row0 < p.M && box_col < p.N;   // the box is not wholly past the end
-        float x[32];
-        auto take = [&](int at, float (&f)[32]) {
+        float x[kCols];
+        auto take = [&](int at, float (&f)[kCols]) {
           if (!shared) {
             load_acc(acc + at, f);
           } else if (row0 + lane < p.M) {
             load_partials<kN>(g.partial, t.slot - t.share, p.shares, at, tile_row, f);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) f[i] = 0.f;
+            for (int i = 0; i < kCols; ++i) f[i] = 0.f;
           }
         };
         take(col, x);
         if constexpr (kEpi == GEMM_GLU) {
-          float v[32];
+          float v[kCols];
           take(kTileN + col, v);
           if (issues) bulk_wait_read<0>();   // the boxes' last stores have read them
-          pair_sync();
+          box_sync();
           if (g.keep) {
-            put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, half, x);
-            put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, half, v);
+            put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, part, x);
+            put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, part, v);
           }
           float unused;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = activation<false, true>(x[i], g.act, unused) * v[i];
-          put_bf16(boxes, lane, half, x);
+          for (int i = 0; i < kCols; ++i) x[i] = activation<false, true>(x[i], g.act, unused) * v[i];
+          put_bf16(boxes, lane, part, x);
           fence_proxy_async_smem();
-          pair_sync();
+          box_sync();
           if (issues && stores) {
             tma_store_2d(&p.out[0], boxes, box_col, row0);
             if (g.keep) {
@@ -423,16 +432,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bulk_commit();
           }
         } else if constexpr (kEpi == GEMM_STORE) {
-          uint8_t* box = boxes + (p.out_f32 ? half : c & 1) * kBf16Box;
+          uint8_t* box = boxes + (p.out_f32 ? 0 : c & 1) * kBf16Box;
           if (issues) {
             if (p.out_f32 || c == 0) bulk_wait_read<0>();   // the last tile's may be fp32
             else bulk_wait_read<1>();
           }
-          pair_sync();
-          if (p.out_f32) put_f32(box, lane, x);
-          else put_bf16(box, lane, half, x);
+          box_sync();
+          if (p.out_f32) put_f32(box, lane, part, x);
+          else put_bf16(box, lane, part, x);
           fence_proxy_async_smem();
-          pair_sync();
+          box_sync();
           if (issues) {
             if (stores) tma_store_2d(&p.out[second], box, box_col, row0);
             if (stores && p.out_f32 && box_col + 32 < p.N)
@@ -444,25 +453,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             fetch(t, c);
             ++fetched;
           }
-          if (!named_all(pair_bar, 64, mbar_wait(&bars->box[quarter], got & 1, lim, abort))) {
+          if (!named_all(box_bar, kBoxThreads, mbar_wait(&bars->box[quarter], got & 1, lim, abort))) {
             if (lane == 0) record_timeout(g.status, abort, 34);
             ok = false;
             break;
           }
           ++got;
-          uint4 kg[4], ku[4], lg[2], lu[2];
+          uint4 kg[kCols / 8], ku[kCols / 8], lg[kCols / 16], lu[kCols / 16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            kg[q] = *piece<128>(boxes, lane, half * 4 + q);
-            ku[q] = *piece<128>(boxes + kBf16Box, lane, half * 4 + q);
+          for (int q = 0; q < kCols / 8; ++q) {
+            kg[q] = *piece<128>(boxes, lane, part * (kCols / 8) + q);
+            ku[q] = *piece<128>(boxes + kBf16Box, lane, part * (kCols / 8) + q);
           }
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            lg[q] = *piece<64>(boxes + 2 * kBf16Box, lane, half * 2 + q);
-            lu[q] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, half * 2 + q);
+          for (int q = 0; q < kCols / 16; ++q) {
+            lg[q] = *piece<64>(boxes + 2 * kBf16Box, lane, part * (kCols / 16) + q);
+            lu[q] = *piece<64>(boxes + 2 * kBf16Box + kByteBox, lane, part * (kCols / 16) + q);
           }
           if (issues) bulk_wait_read<0>();   // the last stores have read their boxes
-          pair_sync();   // all have read: the next chunk may land
+          box_sync();   // all have read: the next chunk may land
           if (c + 1 < kChunks) {
             fetch(t, c + 1);
             ++fetched;
@@ -475,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t* bg = reinterpret_cast<const uint32_t*>(lg);
           const uint32_t* bu = reinterpret_cast<const uint32_t*>(lu);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // eight columns at a time
+          for (int q = 0; q < kCols / 8; ++q) {   // eight columns at a time
             float gate[8], up[8], h[8];
             rejoin8(wg + 4 * q, bg + 2 * q, gate);
             rejoin8(wu + 4 * q, bu + 2 * q, up);
@@ -488,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               up[e] = dh * a;
             }
             auto put = [&](int which, const float (&f)[8]) {
-              *piece<128>(out + which * kBf16Box, lane, half * 4 + q) =
+              *piece<128>(out + which * kBf16Box, lane, part * (kCols / 8) + q) =
                   make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
             };
@@ -497,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             put(2, h);
           }
           fence_proxy_async_smem();
-          pair_sync();
+          box_sync();
           if (issues && stores) {
             tma_store_2d(&g.dgate, out, box_col, row0);
             tma_store_2d(&g.dup, out + kBf16Box, box_col, row0);

@@ -67,29 +67,29 @@ __device__ __forceinline__ void record_timeout(int32_t* status, volatile int* ab
   *abort = 1;
 }
 
-// 32 columns (pieces 8 c .. 8 c + 7) of tile row `row` into a shared tile's sums.
-template <int kN>
+// kCols columns from `col` on of tile row `row` into a shared tile's sums.
+template <int kN, int kCols>
 __device__ __forceinline__ void store_partial(float* partial, int slot, int col, int row,
-                                              const float (&f)[32]) {
+                                              const float (&f)[kCols]) {
   float4* p = reinterpret_cast<float4*>(partial) +
               ((int64_t)slot * (kN / 4) + col / 4) * kGemmM + row;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < kCols / 4; ++i)
     p[i * kGemmM] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
 // The same columns of all shares of a tile, from slot `slot` on, added in order.
-template <int kN>
+template <int kN, int kCols>
 __device__ __forceinline__ void load_partials(const float* partial, int slot, int shares, int col,
-                                              int row, float (&f)[32]) {
+                                              int row, float (&f)[kCols]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = 0.f;
-#pragma unroll 2
+  for (int i = 0; i < kCols; ++i) f[i] = 0.f;
+#pragma unroll 64 / kCols
   for (int s = 0; s < shares; ++s) {
     const float4* p = reinterpret_cast<const float4*>(partial) +
                       ((int64_t)(slot + s) * (kN / 4) + col / 4) * kGemmM + row;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kCols / 4; ++i) {
       const float4 v = __ldcg(p + i * kGemmM);   // written by other CTAs of this launch
       f[4 * i] += v.x;
       f[4 * i + 1] += v.y;
@@ -99,13 +99,15 @@ __device__ __forceinline__ void load_partials(const float* partial, int slot, in
   }
 }
 
-__device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[32]) {
-  uint32_t r[32];
-  ptx::tmem_ld32(taddr, r);
+template <int kCols>
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&f)[kCols]) {
+  uint32_t r[kCols];
+  if constexpr (kCols == 32) ptx::tmem_ld32(taddr, r);
+  else ptx::tmem_ld16(taddr, r);
   ptx::tmem_ld_wait();
-  ptx::reg_fence32(r);
+  ptx::reg_fence(r);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < kCols; ++i) f[i] = __uint_as_float(r[i]);
 }
 
 }  // namespace cpattn
