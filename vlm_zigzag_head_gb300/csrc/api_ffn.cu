@@ -132,30 +132,44 @@ Launch plan_gradients(const cp_gated_ffn_t* p, int pairs, bool dx, int in, bool 
 struct Share {
   int tile, shares;
 };
+enum : int { WANT_FWD = 1, WANT_BWD = 2 };
 struct Plan {
   int sms = 0;
-  Launch gate_up, down, dh;                                 // tensor cores
+  Launch gate_up, down, dh, gradients;                      // tensor cores
   Share f32_gate_up, f32_down, f32_dh, d_down, d_in, d_both, dx;   // CUDA cores; d_in: one weight
   size_t fwd_partial = 0, bwd_partial = 0;                  // bytes
   int pairs() const { return sms / 2; }
 };
 
-Plan make_plan(const cp_gated_ffn_t* p, int sms) {
+// Which gradients a call wants, as plan_gradients takes them.
+struct Wanted {
+  bool dx, down;
+  int in;
+};
+// For one direction; a backward's for the gradients that are wanted, or, without them, as
+// much workspace as any of them takes.
+Plan make_plan(const cp_gated_ffn_t* p, int sms, int direction, const Wanted* wanted = nullptr) {
   Plan r;
   r.sms = sms;
   if (sms < 2) return r;
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
   const bool split = split_rows(p);
   if (p->dtype == CP_BF16 || split) {
-    r.gate_up = plan_launch({{T, F, tiles(D, kGemmK), 1}}, GEMM_GLU, r.pairs(), split);
-    r.down = plan_launch({{T, O, tiles(F, kGemmK), 1}}, GEMM_STORE, r.pairs(), split);
+    if (direction == WANT_FWD) {
+      if (few_rows(p) || batch_rows(p)) return r;
+      r.gate_up = plan_launch({{T, F, tiles(D, kGemmK), 1}}, GEMM_GLU, r.pairs(), split);
+      r.down = plan_launch({{T, O, tiles(F, kGemmK), 1}}, GEMM_STORE, r.pairs(), split);
+      r.fwd_partial = std::max(r.gate_up.partial, r.down.partial);
+      return r;
+    }
     r.dh = plan_launch({{T, F, tiles(O, kGemmK), 1}}, GEMM_DGLU, r.pairs(), split);
-    r.fwd_partial = std::max(r.gate_up.partial, r.down.partial);
     r.bwd_partial = r.dh.partial;
-    for (int which = 1; which < 12; ++which)   // whichever gradients are wanted
-      r.bwd_partial = std::max(
-          r.bwd_partial,
-          plan_gradients(p, r.pairs(), which & 1, which >> 2, (which >> 1) & 1).partial);
+    for (int which = 1; which < 12; ++which) {
+      const Wanted w = wanted ? *wanted : Wanted{(which & 1) != 0, (which >> 1 & 1) != 0, which >> 2};
+      r.gradients = plan_gradients(p, r.pairs(), w.dx, w.in, w.down);
+      r.bwd_partial = std::max(r.bwd_partial, r.gradients.partial);
+      if (wanted) break;
+    }
     return r;
   }
   // gate and up always go through the workspace, and so does dh
@@ -166,9 +180,11 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms) {
     if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
     return s;
   };
-  if (!few_rows(p)) {
+  if (direction == WANT_FWD) {
+    if (few_rows(p)) return r;
     r.f32_gate_up = share(T, F, D, 2, 1, true, &r.fwd_partial);
     r.f32_down = share(T, O, F, 1, 1, false, &r.fwd_partial);
+    return r;
   }
   r.f32_dh = share(T, F, O, 1, 1, true, &r.bwd_partial);
   r.dx = share(T, D, F, 1, 2, false, &r.bwd_partial);
@@ -454,8 +470,7 @@ cp_status_t bwd_bf16(const cp_gated_ffn_t* p, const Plan& plan, const void* x, c
   if ((e = dh.run(plan.sms, st, "hidden gradients")) != CP_OK) return e;
 
   const int in = (dwg != nullptr) + (dwu != nullptr);
-  const Launch rest = plan_gradients(p, plan.pairs(), dx, in, dwd);
-  Bf16Products q(GEMM_STORE, rest, dx && !in && !dwd ? FOLLOWS_A : FOLLOWS_BOTH, ws, partial);
+  Bf16Products q(GEMM_STORE, plan.gradients, dx && !in && !dwd ? FOLLOWS_A : FOLLOWS_BOTH, ws, partial);
   auto input = [&] {   // dg Wg + du Wu as one product, k running through both
     q.add(T, D, false, true, F);
     q.p->k_tiles *= 2;
@@ -568,8 +583,7 @@ cp_status_t bwd_split(const cp_gated_ffn_t* p, const Plan& plan, const void* x, 
   dh.g.dup = static_cast<__nv_bfloat16*>(du.p);
   if ((e = dh.run(plan.sms, st, "hidden gradients")) != CP_OK) return e;
 
-  const Launch rest = plan_gradients(p, plan.pairs(), dx, n_in, dwd);
-  SplitProducts q(GEMM_STORE, rest, ws, partial);
+  SplitProducts q(GEMM_STORE, plan.gradients, ws, partial);
   auto input = [&] {
     q.add(T, D, false, true, F);
     q.p->k_tiles *= 2;
@@ -748,12 +762,12 @@ size_t cp_gated_ffn_kept_size(const cp_gated_ffn_t* desc) {
 
 size_t cp_gated_ffn_fwd_workspace_size(const cp_gated_ffn_t* desc) {
   const int sms = check_desc(desc) == CP_OK ? sm_count() : 0;
-  return sms > 0 ? fwd_bytes(desc, make_plan(desc, sms)) : 0;
+  return sms > 0 ? fwd_bytes(desc, make_plan(desc, sms, WANT_FWD)) : 0;
 }
 
 size_t cp_gated_ffn_bwd_workspace_size(const cp_gated_ffn_t* desc) {
   const int sms = check_desc(desc) == CP_OK ? sm_count() : 0;
-  return sms > 0 ? bwd_bytes(desc, make_plan(desc, sms)) : 0;
+  return sms > 0 ? bwd_bytes(desc, make_plan(desc, sms, WANT_BWD)) : 0;
 }
 
 cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
@@ -772,7 +786,7 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
   if (!aligned_to(gate, 16) || !aligned_to(up, 16))
     return entry_fail(CP_ERR_ALIGNMENT, "gate and up must be 16-byte aligned");
   if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
-  const Plan plan = make_plan(desc, sm_count());
+  const Plan plan = make_plan(desc, sm_count(), WANT_FWD);
   if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, fwd_bytes(desc, plan))) != CP_OK) return e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -815,7 +829,9 @@ cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const vo
     return e;
   if (!dx && !dw_gate && !dw_up && !dw_down) return CP_OK;   // nothing is wanted
   if (!workspace) return entry_fail(CP_ERR_WORKSPACE, "workspace is NULL");
-  const Plan plan = make_plan(desc, sm_count());
+  const Wanted wanted = {dx != nullptr, dw_down != nullptr,
+                         (dw_gate != nullptr) + (dw_up != nullptr)};
+  const Plan plan = make_plan(desc, sm_count(), WANT_BWD, &wanted);
   if (plan.sms < 2) return entry_fail(CP_ERR_CUDA, "no CUDA device");
   if ((e = check_workspace(workspace, ws_bytes, bwd_bytes(desc, plan))) != CP_OK) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -11,12 +11,13 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import CpError, Workspace, _binding as _b, _dt
+from . import CP_BF16, CP_F32, CpError, Workspace, _binding as _b, _dt
 from .layer_norm import _rows
 from .norm_rope import _at, _on_device, _raw_stream
 from .scored import _like, _space
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+_GRAD_DTYPES = {torch.bfloat16: CP_BF16, torch.float32: CP_F32}
 
 
 def _aligned(x: torch.Tensor) -> torch.Tensor:
@@ -65,25 +66,26 @@ def _workspace_bytes(f, sizes, device, backward):
 
 def _prepare(x, w_gate, w_up, w_down, activation, grad_dtype, dy=None):
     """The checked descriptor of rows ``x [T, D]``, with its workspace sizes."""
-    if activation not in ACTIVATIONS:
+    code, hidden, out = ACTIVATIONS.get(activation), w_gate.shape, w_down.shape
+    if code is None:
         raise CpError(1, "activation must be one of %s" % ", ".join(ACTIVATIONS))
-    if w_gate.dim() != 2 or w_down.dim() != 2 or w_gate.shape != w_up.shape or \
-            w_gate.shape[1] != x.shape[1] or w_down.shape[1] != w_gate.shape[0]:
+    if len(hidden) != 2 or len(out) != 2 or hidden != w_up.shape or hidden[1] != x.shape[1] or \
+            out[1] != hidden[0]:
         raise CpError(2, "w_gate and w_up must be [F, D], w_down [D_out, F]")
-    for w in (w_gate, w_up, w_down):
-        if w.dtype != x.dtype:
+    (T, D), F, D_out, dtype, device = x.shape, hidden[0], out[0], x.dtype, x.device
+    strides = []
+    for w, width in ((w_gate, D), (w_up, D), (w_down, F)):
+        if w.dtype != dtype:
             raise CpError(3, "x and the weights must share a dtype")
-        if w.device != x.device:
+        if w.device != device:
             raise CpError(1, "x and the weights must share a device")
-        if w.shape[1] > 1 and w.stride(1) != 1:
+        row, column = w.stride()
+        if width > 1 and column != 1:
             raise CpError(1, "the last dimension of the weights must be contiguous")
-    F, D = w_gate.shape
-    D_out = w_down.shape[0]
-    if dy is not None and (dy.shape != (x.shape[0], D_out) or dy.dtype != x.dtype or
-                           dy.device != x.device):
+        strides.append(row)
+    if dy is not None and (dy.shape != (T, D_out) or dy.dtype != dtype or dy.device != device):
         raise CpError(2, "dy must match y")
-    return _desc(_dt(x), grad_dtype, ACTIVATIONS[activation], x.shape[0], D, F, D_out,
-                 x.stride(0), w_gate.stride(0), w_up.stride(0), w_down.stride(0),
+    return _desc(_dt(x), grad_dtype, code, T, D, F, D_out, x.stride(0), *strides,
                  D_out if dy is None else dy.stride(0))
 
 
@@ -122,8 +124,9 @@ def cp_gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, dy, activation: str = "s
     if len(wanted) != 4:
         raise CpError(2, "wanted must say yes or no to dx, dw_gate, dw_up and dw_down")
     rows, g = _rows(x, "x"), _rows(dy, "dy")
-    f, sizes = _prepare(rows, w_gate, w_up, w_down, activation,
-                        _dt(torch.empty(0, dtype=grad_dtype)), g)
+    if grad_dtype not in _GRAD_DTYPES:
+        raise CpError(3, "dtype %s not supported (bf16 or fp32)" % grad_dtype)
+    f, sizes = _prepare(rows, w_gate, w_up, w_down, activation, _GRAD_DTYPES[grad_dtype], g)
     device = x.device
     for t, name in ((gate, "gate"), (up, "up")):
         _like(t, (_kept_bytes(f, sizes),), torch.uint8, device, name)

@@ -43,22 +43,21 @@ def _desc(dtype, w_dtype, T, D, x_stride, dy_stride, eps):
 
 def _prepare(x, weight, bias, eps, dy=None):
     """The checked descriptor of rows ``x [T, D]``."""
-    w_dtype = CP_F32
+    w_dtype, (T, D), device = CP_F32, x.shape, x.device
     for w in (weight, bias):
         if w is None:
             continue
-        if w.dim() != 1 or w.shape[0] != x.shape[1] or w.device != x.device or \
-                not w.is_contiguous():
+        if w.shape != (D,) or w.device != device or not w.is_contiguous():
             raise CpError(2, "weight and bias must be contiguous [D] tensors on x's device")
         w_dtype = _dt(w)
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise CpError(3, "weight and bias must share a dtype")
     dy_stride = 0
     if dy is not None:
-        if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != x.device:
+        if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != device:
             raise CpError(2, "dy must match x")
         dy_stride = dy.stride(0)
-    return _desc(_dt(x), w_dtype, x.shape[0], x.shape[1], x.stride(0), dy_stride, float(eps))
+    return _desc(_dt(x), w_dtype, T, D, x.stride(0), dy_stride, float(eps))
 
 
 def cp_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5):

@@ -28,7 +28,7 @@ class _on_device:
     """``torch.cuda.device``, free of charge where the device is current already."""
 
     def __init__(self, device):
-        other = torch.cuda.current_device() != device.index
+        other = torch._C._cuda_getDevice() != device.index
         self._guard = torch.cuda.device(device) if other else None
 
     def __enter__(self):
