@@ -69,6 +69,21 @@ __device__ __forceinline__ float activation(float g, int act, float& da) {
   return a;
 }
 
+// Calls f with the activation as a compile-time constant, for loops over several values:
+// a branch at every value keeps them from running side by side (hidden gradients of fp32,
+// 517 x 512 x 1360: the backward 62.5 us with it, 58.8 without; the bf16 ones, whose loads
+// they wait for, 1 % slower without).
+template <int kAct>
+struct Activation {
+  static constexpr int value = kAct;
+};
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  if (act == ACT_SILU) f(Activation<ACT_SILU>());
+  else if (act == ACT_GELU) f(Activation<ACT_GELU>());
+  else f(Activation<ACT_GELU_TANH>());
+}
+
 // The upper 24 bits of two or four fp32 values, in memory order: their upper halves
 // (bf16 planes), and the bytes below them.  Byte permutations alone: rounding to 24
 // bits instead took six instructions a value, and with it the gradient's epilogue

@@ -415,9 +415,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             put_kept(boxes + kBf16Box, boxes + 3 * kBf16Box, lane, part, x);
             put_kept(boxes + 2 * kBf16Box, boxes + 3 * kBf16Box + kByteBox, lane, part, v);
           }
-          float unused;
+          with_activation(g.act, [&](auto act) {
+            float unused;
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) x[i] = activation<false, true>(x[i], g.act, unused) * v[i];
+            for (int i = 0; i < kCols; ++i)
+              x[i] = activation<false, true>(x[i], act.value, unused) * v[i];
+          });
           put_bf16(boxes, lane, part, x);
           fence_proxy_async_smem();
           box_sync();

@@ -388,10 +388,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             to.store(g.gate, x);
             to.store(g.up, x + 32);
           }
-          float unused;
+          with_activation(g.act, [&](auto act) {
+            float unused;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[i] = activation<false, false>(x[i], g.act, unused) * x[32 + i];
+            for (int i = 0; i < 16; ++i)
+              x[i] = activation<false, false>(x[i], act.value, unused) * x[32 + i];
+          });
           uint4 lo[4] = {};
           to.store_planes(g.h, x, lo);
           to.store_pieces(g.h + 2 * (int64_t)p.M * p.N, nullptr, lo);
@@ -407,14 +409,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float gate[16], up[16];
             to.load(g.gate, gate);
             to.load(g.up, up);
+            with_activation(g.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float da;
-              const float a = activation<true, false>(gate[i], g.act, da), dh = x[i];
-              x[i] = a * up[i];
-              gate[i] = dh * up[i] * da;
-              up[i] = dh * a;
-            }
+              for (int i = 0; i < 16; ++i) {
+                float da;
+                const float a = activation<true, false>(gate[i], act.value, da), dh = x[i];
+                x[i] = a * up[i];
+                gate[i] = dh * up[i] * da;
+                up[i] = dh * a;
+              }
+            });
             const int64_t last_plane = 2 * (int64_t)p.M * p.N;
             uint4 lo[4];
             to.store_planes(g.dgate, gate, lo);
