@@ -38,6 +38,7 @@ def _desc(dtype, w_dtype, T, D, x_stride, dy_stride, eps):
     # the stride of a dimension of one element is never used
     f.x_stride, f.dy_stride = (x_stride, dy_stride) if T > 1 else (D, D)
     f.eps = eps
+    f.workspace = {}   # the backward's bytes by device, as they get known
     return f
 
 
@@ -90,8 +91,9 @@ def cp_layer_norm_bwd(x, dy, mean, rstd, weight=None, *, bias_grad: bool = False
     x's dtype.  dx is contiguous in x's dtype, dweight and dbias are fp32 ``[D]``."""
     rows, g = _rows(x, "x"), _rows(dy, "dy")
     f = _prepare(rows, weight, None, 0.0, g)
+    T, device = f.T, x.device
     for s in (mean, rstd):
-        if s.numel() != f.T or s.dtype != torch.float32 or s.device != x.device or \
+        if s.numel() != T or s.dtype != torch.float32 or s.device != device or \
                 not s.is_contiguous():
             raise CpError(2, "mean and rstd must be those of the forward")
     if weight_grad is None:
@@ -102,13 +104,15 @@ def cp_layer_norm_bwd(x, dy, mean, rstd, weight=None, *, bias_grad: bool = False
 def _launch_bwd(f, rows, dy, mean, rstd, weight, input_grad, weight_grad, bias_grad, shape):
     device = rows.device
     dx = torch.empty(shape, dtype=rows.dtype, device=device) if input_grad else None
-    dw, db = (torch.empty(f.D, dtype=torch.float32, device=device) if wanted else None
-              for wanted in (weight_grad, bias_grad))
+    dw = torch.empty(f.D, dtype=torch.float32, device=device) if weight_grad else None
+    db = torch.empty(f.D, dtype=torch.float32, device=device) if bias_grad else None
     lib = _b.lib()
     with _on_device(device):
         ws, nbytes = None, 0
         if weight_grad or bias_grad:
-            nbytes = lib.cp_layer_norm_bwd_workspace_size(f)
+            nbytes = f.workspace.get(device.index)
+            if nbytes is None:
+                nbytes = f.workspace[device.index] = lib.cp_layer_norm_bwd_workspace_size(f)
             ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         _b.check(lib.cp_layer_norm_bwd(
             f, rows.data_ptr(), dy.data_ptr(), _at(weight), mean.data_ptr(), rstd.data_ptr(),
