@@ -17,6 +17,8 @@
 // take about a microsecond a token, 128 tokens of 4096 x 12288 took 66 us, 62.5 so).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "check.cuh"
 #include "ffn.h"
 #include "ffn_act.cuh"
@@ -272,6 +274,33 @@ __global__ void __launch_bounds__(kThreads, Layout<kGlu, kTokens>::kResident)
   }
 }
 
+// How many clusters of `shares` CTAs run at once: a cluster stays within a part of the
+// GPU, and fewer fit than there is room for their CTAs.  (Six CTAs for each of 48 tiles on
+// 304 places left two clusters for a second round: 20 tokens, 2048 x 6144, 22 us, 20 with
+// three; 128 tokens 41 and 26.)  Asked about a kernel that takes the same threads and
+// shared memory: of one that allocates tensor memory the answer is one CTA an SM.
+__global__ void __launch_bounds__(kThreads) places_kernel(int* p) {
+  extern __shared__ int places_smem[];
+  if (p != nullptr) *p = places_smem[threadIdx.x];
+}
+template <bool kGlu, int kTokens>
+cudaError_t clusters_at_once(cudaLaunchConfig_t cfg, int shares, int* clusters) {
+  static std::atomic<int> known[64][9];   // by device and shares: one more, 0 not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* k = dev < 64 ? &known[dev][shares] : nullptr;
+  if (k && k->load() > 0) {
+    *clusters = k->load() - 1;
+    return cudaSuccess;
+  }
+  e = cudaFuncSetAttribute(places_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           227 * 1024);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(clusters, places_kernel, &cfg);
+  if (e == cudaSuccess && k) k->store(*clusters + 1);
+  return e;
+}
+
 template <bool kGlu, int kTokens>
 cudaError_t launch_t(const FfnTokensArgs& a, int sms, cudaStream_t st) {
   using L = Layout<kGlu, kTokens>;
@@ -280,24 +309,35 @@ cudaError_t launch_t(const FfnTokensArgs& a, int sms, cudaStream_t st) {
                                        L::kSmem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.N + kRows - 1) / kRows, k_tiles = (a.K + kGemmK - 1) / kGemmK;
-  // as many shares of k as run at once, of two k tiles or more
-  int shares = L::kResident * sms / tiles;
-  if (shares > k_tiles / 2) shares = k_tiles / 2;
-  if (shares > 8) shares = 8;
-  if (shares < 1) shares = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)tiles, (unsigned)shares);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = (unsigned)shares;
-  attr[0].val.clusterDim.z = 1;
+  auto set_shares = [&](int n) {
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)n);
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = (unsigned)n;
+    attr[0].val.clusterDim.z = 1;
+  };
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  // shares of k, of two k tiles or more, that run at once and leave the busiest SM the least
+  int shares = 1, load = (tiles + sms - 1) / sms;   // CTAs of the busiest SM
+  for (int n = 2; n <= 8 && n <= k_tiles / 2 && n * tiles <= L::kResident * sms; ++n) {
+    const int most = (n * tiles + sms - 1) / sms;
+    if (most * shares > load * n) continue;
+    set_shares(n);
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if ((e = clusters_at_once<kGlu, kTokens>(cfg, n, &clusters)) != cudaSuccess) return e;
+    if (clusters < tiles) continue;
+    shares = n;
+    load = most;
+  }
+  set_shares(shares);
   cfg.numAttrs = kGlu ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
