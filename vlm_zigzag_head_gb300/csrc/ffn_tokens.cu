@@ -7,9 +7,9 @@
 // take 76 us for 37 tokens, 4096 x 12288, in five launches; here are two, the second's
 // first weights in flight while the first ends.
 //
-// Two CTAs share an SM (up to 64 tokens), and the CTAs of a cluster share k where there are fewer tiles
-// than that; their sums meet in shared memory in a fixed order, each CTA finishing some
-// of the tokens.
+// Two CTAs share an SM (up to 64 tokens), and the CTAs of a cluster share k where there
+// are fewer tiles than that; their sums meet in shared memory in a fixed order, each CTA
+// finishing some of the tokens.
 //
 // Warp roles (320 threads): warp 0 TMA producer, warp 1 TMEM allocation and MMAs (one
 // lane each), warps 2..5 sums to shared memory: thread = weight row = TMEM lane, columns =
