@@ -21,7 +21,6 @@ from __future__ import annotations
 from typing import Callable, Optional, Sequence
 
 import torch
-from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
@@ -29,6 +28,7 @@ from . import _binding as _b
 from . import ffn as _ffn
 from . import layer_norm as _layer_norm
 from . import rope as _rope
+from .norm_rope import _wants_grad
 
 
 class CPAttention(torch.autograd.Function):
@@ -88,17 +88,6 @@ def _dense(x: torch.Tensor) -> torch.Tensor:
     """A contiguous, 16-byte aligned tensor (a copy of any other view)."""
     x = x.contiguous()
     return x if x.data_ptr() % 16 == 0 else x.clone()
-
-
-def _wants_grad(*tensors) -> bool:
-    """Whether the call goes through its autograd function: for a backward to follow, or, with
-    a dual tensor, for the function to say that it has no forward-mode rule (a plain call would
-    drop the tangent, which reads as a derivative of zero)."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        return True
-    # no dual tensor outside a level; the private number saves a query per tensor
-    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
-        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 class QKNormRope(torch.autograd.Function):

@@ -11,6 +11,7 @@ import functools
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 from . import CP_F32, CpError, _binding as _b, _dt
 
@@ -22,6 +23,17 @@ def _at(t: Optional[torch.Tensor]):
 def _raw_stream(device) -> int:
     """The current stream's handle (without building a Stream object per call)."""
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _wants_grad(*tensors) -> bool:
+    """Whether autograd has to know of the call: for a backward to follow, or, with a dual
+    tensor, for the autograd function to say that it has no forward-mode rule (a plain call
+    would drop the tangent, which reads as a derivative of zero)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    # no dual tensor outside a level; the private number saves a query per tensor
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 class _on_device:

@@ -14,7 +14,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from . import CpError, _binding as _b, _dt
-from .norm_rope import _check_heads, _on_device, _raw_stream
+from .norm_rope import _check_heads, _on_device, _raw_stream, _wants_grad
 
 
 class Frequencies(tuple):
@@ -142,6 +142,9 @@ def _disjoint(q, k):
 
 def _prepare(q, k, positions, theta, rot_dim, sections, interleaved, inv_freq, amplitude,
              inplace=False):
+    if inplace and _wants_grad(q, k):   # a graph would go on as if nothing had happened
+        raise CpError(1, "q or k is being differentiated: not in place (autograd.rope rotates out "
+                         "of place; detached tensors and no_grad leave the graph)")
     _check_heads(q, "q")
     _check_heads(k, "k", q)
     if positions.dtype != torch.int32 or positions.device != q.device or \
@@ -168,7 +171,8 @@ def cp_rope_fwd(q, k, positions, *, theta: float = 10000.0, rot_dim: Optional[in
     :func:`cp_qk_norm_rope_fwd`; :func:`rope_frequencies` gives ``inv_freq`` for long
     contexts.  ``amplitude`` multiplies the rotated elements; the others are copied.
     Returns contiguous ``(q_out, k_out)``, or with ``inplace`` q and k themselves, written
-    over."""
+    over: refused where autograd would have to know of it (q or k requires grad while gradients
+    are recorded, or carries a forward-mode tangent)."""
     f = _prepare(q, k, positions, theta, rot_dim, sections, interleaved, inv_freq, amplitude,
                  inplace)
     return _launch(_b.lib().cp_rope_fwd, f, q, k, positions, inplace)
@@ -180,7 +184,7 @@ def cp_rope_bwd(dq_out, dk_out, positions, *, theta: float = 10000.0,
                 amplitude: float = 1.0, inplace: bool = False):
     """Gradient of :func:`cp_rope_fwd` (same options; the gradients of its outputs, any token
     and head strides).  Returns contiguous ``(dq, dk)``, or with ``inplace`` its arguments,
-    written over."""
+    written over (refused as in :func:`cp_rope_fwd`)."""
     f = _prepare(dq_out, dk_out, positions, theta, rot_dim, sections, interleaved, inv_freq,
                  amplitude, inplace)
     return _launch(_b.lib().cp_rope_bwd, f, dq_out, dk_out, positions, inplace)
