@@ -151,7 +151,7 @@ struct Wanted {
 Plan make_plan(const cp_gated_ffn_t* p, int sms, int direction, const Wanted* wanted = nullptr) {
   Plan r;
   r.sms = sms;
-  if (sms < 2) return r;
+  if (sms < 2 || p->T == 0) return r;   // without rows there is nothing to launch
   const int64_t T = p->T, D = p->D, F = p->F, O = p->D_out;
   const bool split = split_rows(p);
   if (p->dtype == CP_BF16 || split) {

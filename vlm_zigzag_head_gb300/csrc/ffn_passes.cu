@@ -249,6 +249,7 @@ double cut_products(GemmCut* p, int n, int pairs, const GemmCost& cost) {
     p[i].shares = 1;
   }
   double best = launch_time(p, n, pairs, cost);
+  if (work == 0) return best;   // no rows: nothing to cut
   auto consider = [&](const GemmCut* q) {
     const double t = launch_time(q, n, pairs, cost);
     if (t >= best) return;
@@ -313,7 +314,7 @@ void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms
   auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + t - 1) / t) * outputs; };
   *splits = 1;
   *tile = tiles(128) >= 2 * sms ? 128 : 64;
-  if (*tile == 128) return;
+  if (*tile == 128 || tiles(64) == 0) return;
   // eight blocks of 64 threads an SM, of four steps at least
   const int64_t steps = (K + kStep - 1) / kStep * phases;
   int64_t s = 8 * (int64_t)sms / tiles(64);
