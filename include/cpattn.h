@@ -485,7 +485,8 @@ cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const 
  * NaN).
  *
  *   x [T][D], dy [T][D_out], w_gate, w_up [F][D], w_down [D_out][F]   row strides in
- *                   elements; rows do not overlap (e.g. halves of one [2 F][D] weight)
+ *                   elements; rows do not overlap (e.g. halves of one [2 F][D] weight);
+ *                   with T == 1 those of x and dy are not looked at
  *   y [T][D_out], dx [T][D]   contiguous, dtype; must not overlap an input
  *   gate, up        cp_gated_ffn_kept_size(desc) bytes each: g and u for the backward,
  *                   in the library's own layout, written by the forward (both, or both

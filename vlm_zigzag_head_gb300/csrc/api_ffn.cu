@@ -48,6 +48,18 @@ cp_status_t check_desc(const cp_gated_ffn_t* p) {
   return CP_OK;
 }
 
+// A checked descriptor as the launches take it.  The stride of a single row is not checked and may
+// be anything, 1 among them, which would read as another order of the operand in memory: a
+// contiguous row's instead.
+cp_gated_ffn_t with_strides(const cp_gated_ffn_t* p) {
+  cp_gated_ffn_t d = *p;
+  if (d.T <= 1) {
+    d.x_stride = d.D;
+    d.dy_stride = d.D_out;
+  }
+  return d;
+}
+
 // 16-byte aligned and not NULL.
 cp_status_t check_ptr(const void* p, const char* name) {
   if (!p) return entry_fail(CP_ERR_INVALID_ARG, std::string(name) + " is NULL");
@@ -770,12 +782,13 @@ size_t cp_gated_ffn_bwd_workspace_size(const cp_gated_ffn_t* desc) {
   return sms > 0 ? bwd_bytes(desc, make_plan(desc, sms, WANT_BWD)) : 0;
 }
 
-cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* given, const void* x, const void* w_gate,
                              const void* w_up, const void* w_down, void* y, void* gate, void* up,
                              void* workspace, size_t ws_bytes, void* stream) {
   ENTRY_TRY
-  cp_status_t e = check_desc(desc);
+  cp_status_t e = check_desc(given);
   if (e != CP_OK) return e;
+  const cp_gated_ffn_t d = with_strides(given), *desc = &d;
   if (desc->T == 0) return CP_OK;
   if ((e = check_ptr(x, "x")) != CP_OK || (e = check_ptr(w_gate, "w_gate")) != CP_OK ||
       (e = check_ptr(w_up, "w_up")) != CP_OK || (e = check_ptr(w_down, "w_down")) != CP_OK ||
@@ -803,13 +816,14 @@ cp_status_t cp_gated_ffn_fwd(const cp_gated_ffn_t* desc, const void* x, const vo
   ENTRY_CATCH
 }
 
-cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* desc, const void* x, const void* w_gate,
+cp_status_t cp_gated_ffn_bwd(const cp_gated_ffn_t* given, const void* x, const void* w_gate,
                              const void* w_up, const void* w_down, const void* gate,
                              const void* up, const void* dy, void* dx, void* dw_gate, void* dw_up,
                              void* dw_down, void* workspace, size_t ws_bytes, void* stream) {
   ENTRY_TRY
-  cp_status_t e = check_desc(desc);
+  cp_status_t e = check_desc(given);
   if (e != CP_OK) return e;
+  const cp_gated_ffn_t d = with_strides(given), *desc = &d;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (const void* p : {(const void*)dx, (const void*)dw_gate, (const void*)dw_up,
                         (const void*)dw_down})
