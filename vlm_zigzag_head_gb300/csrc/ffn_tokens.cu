@@ -33,8 +33,6 @@ using namespace ptx;
 constexpr int kWarps = 10, kThreads = kWarps * 32;
 constexpr int kRows = 128;                       // of a weight in one tile
 constexpr int kWeightTile = kRows * kGemmK * 2;  // bytes
-constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
-constexpr long long kDrainLimit = 1LL << 24;
 
 template <bool kGlu, int kTokens>
 struct Layout {
@@ -57,11 +55,6 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
 };
-
-__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
-  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
-  *abort = 1;
-}
 
 // 16 bytes of another CTA's shared memory.
 __device__ __forceinline__ float4 peer_load4(const float* p, int rank) {

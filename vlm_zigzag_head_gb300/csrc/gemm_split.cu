@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int st = j % kDepth;
           if (j >= kDepth &&
               !mbar_wait_cluster(&bars->empty[st], ((j / kDepth) - 1) & 1, lim, abort)) {
-            record_timeout(g.status, abort, 41);
+            record_timeout(g.status, abort, 51);
             break;
           }
           const bool next = k >= k_split;
@@ -302,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) {
-        record_timeout(g.status, abort, 42);
+        record_timeout(g.status, abort, 52);
         // nothing issued by this thread may still be running at exit
         mma_commit_pair(&bars->drain);
         int zero = 0;
@@ -331,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int s = n & 1;
         if (!__all_sync(0xffffffffu,
                         mbar_wait_cluster(&bars->acc_full[s], (n >> 1) & 1, lim, abort))) {
-          if (lane == 0) record_timeout(g.status, abort, 43);
+          if (lane == 0) record_timeout(g.status, abort, 53);
           ok = false;
           break;
         }

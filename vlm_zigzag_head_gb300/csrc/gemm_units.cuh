@@ -4,13 +4,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "check.cuh"
 #include "ffn.h"
 #include "ptx.cuh"
 
 namespace cpattn {
-
-constexpr long long kDrainLimit = 1LL << 24;
-constexpr long long kLandLimit = 1LL << 16;   // milliseconds: a load lands within microseconds
 
 // m tiles whose n tiles are walked together: about square patches of tiles run at a
 // time, which reads the least of A and B.
@@ -60,11 +58,6 @@ __device__ __forceinline__ Unit unit_at(const Args& g, int u) {
   t.m = (int)(first + in % rows);
   t.n = (int)(in / rows);
   return t;
-}
-
-__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
-  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
-  *abort = 1;
 }
 
 // kCols columns from `col` on of tile row `row` into a shared tile's sums.

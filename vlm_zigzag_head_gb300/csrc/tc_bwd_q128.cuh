@@ -83,7 +83,6 @@ constexpr int kQStages = 2;
 constexpr int kLdRows = kBQ + 4;   // lse2 / D box: 128 rows plus alignment slack
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColDP = 128;
-constexpr long long kDrainLimit = 1LL << 24;
 
 template <int D>
 struct Cols {
@@ -178,11 +177,6 @@ __device__ __forceinline__ void tile_of(const Seg* runs, int nseg, int g, TileWa
   }
   q0 = run_qstart(sg);
   t = g - w.base;
-}
-
-__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
-  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
-  *abort = 1;
 }
 
 // The barriers of a producer's loads over N stages: a stage's own one, or its raw

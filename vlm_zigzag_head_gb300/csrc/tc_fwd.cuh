@@ -68,7 +68,6 @@ constexpr uint32_t kTmemCols = 512;
 __device__ __forceinline__ uint32_t col_s(int x) { return x ? 128u : 0u; }
 __device__ __forceinline__ uint32_t col_o(int x) { return x ? 384u : 256u; }
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: stale max may lag by 2^8
-constexpr long long kDrainLimit = 1LL << 24;
 
 template <int D>
 struct Smem {
@@ -145,11 +144,6 @@ __device__ __forceinline__ int item_tiles(const TcFwdArgs& a, const FwdItem& it)
   int n = 0;
   for (int s = 0; s < it.nseg; ++s) n += run_tiles(item_seg(a, it, s), it.q_len);
   return n;
-}
-
-__device__ __forceinline__ void record_timeout(int32_t* status, volatile int* abort, int site) {
-  if (atomicCAS(&status[0], 0, 1) == 0) status[1] = site;
-  *abort = 1;
 }
 
 // Modifies the row's 128 products in place; the scores in log2 units are then
