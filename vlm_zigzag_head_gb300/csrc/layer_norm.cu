@@ -578,30 +578,39 @@ __global__ void __launch_bounds__(kDwWarps * 32)
 struct Shape {
   int tpr, nv, blocks;
 };
-constexpr Shape kFwdShapes[] = {{32, 1, 4},  {32, 2, 3},  {64, 2, 3},  {128, 2, 3},
-                                {256, 2, 3}, {256, 4, 2}, {512, 4, 1}, {1024, 4, 1}};
+constexpr Shape kFwdShapes[] = {{32, 1, 4},  {32, 2, 3},  {64, 2, 3}, {128, 2, 3},
+                                {256, 2, 3}, {256, 4, 2}, {512, 4, 1}};
 // fp32: half the elements a piece, so fewer registers
 constexpr Shape kFwdShapesF32[] = {{32, 1, 4},  {32, 2, 4},  {64, 2, 4},   {128, 2, 4},
                                    {256, 2, 4}, {512, 2, 2}, {1024, 2, 1}, {1024, 4, 1}};
 constexpr Shape kBwdShapes[] = {{32, 1, 3},  {32, 2, 2},  {64, 2, 2},   {128, 2, 2},
-                                {256, 2, 2}, {512, 2, 1}, {1024, 2, 1}, {1024, 4, 1}};
+                                {256, 2, 2}, {512, 2, 1}, {1024, 2, 1}, {1024, 4, 1}};   // last: fp32
 constexpr int kBwdWideFrom = 6;   // shapes with sums in shared memory
 
 // The shape of rows of `pieces` 16-byte pieces: 32, 64, 128, ... at most.
-int shape_of(int pieces) {
+constexpr int shape_of(int pieces) {
   int i = 0;
   while ((32 << i) < pieces) ++i;
   return i;
 }
 
+constexpr int pieces_of(int D, bool bf16) { return bf16 ? (D + 7) / 8 : (D + 3) / 4; }
+
+// The shapes that rows of a type reach.
+template <typename T>
+constexpr int kShapes = shape_of(pieces_of(kLayerNormMaxWidth, sizeof(T) == 2)) + 1;
+template <typename A>
+constexpr int entries(const A&) { return sizeof(A) / sizeof(Shape); }
+static_assert(kShapes<__nv_bfloat16> == entries(kFwdShapes) && kShapes<float> == entries(kFwdShapesF32) &&
+              kShapes<float> == entries(kBwdShapes), "no shape without rows, none missing");
+
 // f(the shape's number as an integral constant)
-template <int I = 0, typename F>
+template <typename T, int I = 0, typename F>
 cudaError_t by_shape(int i, F f) {
-  if constexpr (I < 8) return i == I ? f(std::integral_constant<int, I>{}) : by_shape<I + 1>(i, f);
+  if constexpr (I < kShapes<T>)
+    return i == I ? f(std::integral_constant<int, I>{}) : by_shape<T, I + 1>(i, f);
   else return cudaErrorInvalidValue;
 }
-
-int pieces_of(int D, bool bf16) { return bf16 ? (D + 7) / 8 : (D + 3) / 4; }
 
 int blocks_of(const Shape& s, int64_t T, int sms) {
   const int rows = block_threads(s.tpr) / s.tpr;
@@ -622,7 +631,7 @@ cudaError_t more_shared(F kernel, int bytes) {
 
 template <typename T, bool kVec>
 cudaError_t fwd_t(const LayerNormArgs& a, int sms, cudaStream_t st) {
-  return by_shape(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
+  return by_shape<T>(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
     constexpr Shape s = sizeof(T) == 2 ? kFwdShapes[decltype(i)::value]
                                        : kFwdShapesF32[decltype(i)::value];
     auto kernel = layer_norm_fwd_kernel<T, s.tpr, s.nv, kVec, s.blocks>;
@@ -636,7 +645,7 @@ cudaError_t fwd_t(const LayerNormArgs& a, int sms, cudaStream_t st) {
 
 template <typename T, bool kVec>
 cudaError_t bwd_t(const LayerNormArgs& a, int blocks, cudaStream_t st) {
-  return by_shape(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
+  return by_shape<T>(shape_of(pieces_of(a.D, sizeof(T) == 2)), [&](auto i) {
     constexpr Shape s = kBwdShapes[decltype(i)::value];
     constexpr bool kWide = decltype(i)::value >= kBwdWideFrom;
     constexpr int kThreads = block_threads(s.tpr), G = kThreads / s.tpr;
