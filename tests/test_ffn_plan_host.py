@@ -24,8 +24,8 @@ class Cost(ctypes.Structure):     # GemmCost
 cut = getattr(lib, "_ZN6cpattn12cut_productsEPNS_7GemmCutEiiRKNS_8GemmCostE")
 cut.restype = ctypes.c_double
 cut.argtypes = [ctypes.POINTER(Cut), ctypes.c_int, ctypes.c_int, ctypes.POINTER(Cost)]
-share = getattr(lib, "_ZN6cpattn9share_f32EllliiiPiS0_")
-share.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 3 + [ctypes.POINTER(ctypes.c_int)] * 2
+share = getattr(lib, "_ZN6cpattn9share_f32Ellliii")
+share.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int] * 3
 
 def products(*shapes):
     p = (Cut * 3)()
@@ -33,11 +33,6 @@ def products(*shapes):
         c.tiles, c.k_tiles = tiles, k_tiles
     time = cut(p, len(shapes), 76, ctypes.byref(Cost(256, 0.29, 2.0, 4)))
     return time, [(c.whole, c.shares) for c in p[:len(shapes)]]
-
-def f32(M, N, K, outputs, phases):
-    tile, splits = ctypes.c_int(-1), ctypes.c_int(-1)
-    share(M, N, K, outputs, phases, 152, ctypes.byref(tile), ctypes.byref(splits))
-    return tile.value, splits.value
 
 if sys.argv[2] == "products":
     # no rows: a product of no tiles, and ones of tiles without k
@@ -50,9 +45,8 @@ if sys.argv[2] == "products":
 else:
     for M, N, K, outputs, phases in ((0, 1360, 512, 1, 1), (0, 512, 1360, 1, 2), (1360, 512, 0, 2, 1),
                                      (512, 1360, 0, 1, 1), (0, 512, 0, 1, 1)):
-        tile, splits = f32(M, N, K, outputs, phases)
-        assert tile in (64, 128) and splits == 1, (M, N, K, tile, splits)
-    assert f32(64, 1360, 512, 1, 1)[1] > 1
+        assert share(M, N, K, outputs, phases, 152) == 1, (M, N, K)
+    assert share(64, 1360, 512, 1, 1, 152) > 1
 """
 
 

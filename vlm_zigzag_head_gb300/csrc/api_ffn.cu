@@ -141,14 +141,12 @@ Launch plan_gradients(const cp_gated_ffn_t* p, int pairs, bool dx, int in, bool 
                      GEMM_STORE, pairs, p->dtype == CP_F32);
 }
 
-struct Share {
-  int tile, shares;
-};
 enum : int { WANT_FWD = 1, WANT_BWD = 2 };
 struct Plan {
   int sms = 0;
   Launch gate_up, down, dh, gradients;                      // tensor cores
-  Share f32_gate_up, f32_down, f32_dh, d_down, d_in, d_both, dx;   // CUDA cores; d_in: one weight
+  // shares of k on CUDA cores; d_in: of one weight
+  int f32_gate_up = 1, f32_down = 1, f32_dh = 1, d_down = 1, d_in = 1, d_both = 1, dx = 1;
   size_t fwd_partial = 0, bwd_partial = 0;                  // bytes
   int pairs() const { return sms / 2; }
 };
@@ -187,10 +185,9 @@ Plan make_plan(const cp_gated_ffn_t* p, int sms, int direction, const Wanted* wa
   // gate and up always go through the workspace, and so does dh
   auto share = [&](int64_t M, int64_t N, int64_t K, int outputs, int phases, bool always,
                    size_t* most) {
-    Share s;
-    share_f32(M, N, K, outputs, phases, sms, &s.tile, &s.shares);
-    if (always || s.shares > 1) *most = std::max(*most, (size_t)outputs * s.shares * M * N * 4);
-    return s;
+    const int n = share_f32(M, N, K, outputs, phases, sms);
+    if (always || n > 1) *most = std::max(*most, (size_t)outputs * n * M * N * 4);
+    return n;
   };
   if (direction == WANT_FWD) {
     if (few_rows(p)) return r;
@@ -634,7 +631,7 @@ struct F32 {
 
   // The operands' order in memory: A and B row by row along k, or across it.
   static GemmF32Args args(int M, int N, int K, int64_t a_stride, bool a_mn, int64_t b_stride,
-                          bool b_mn, const Share& s) {
+                          bool b_mn, int shares) {
     GemmF32Args g = {};
     g.M = M;
     g.N = N;
@@ -646,8 +643,7 @@ struct F32 {
       g.sbk[i] = b_mn ? b_stride : 1;
     }
     g.outputs = g.phases = 1;
-    g.tile = s.tile;
-    g.splits = s.shares;
+    g.splits = shares;
     return g;
   }
   static const float* in(const void* p) { return static_cast<const float*>(p); }

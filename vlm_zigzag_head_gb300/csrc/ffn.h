@@ -205,13 +205,11 @@ struct GemmF32Args {
   int64_t sbn[2], sbk[2];   // of b[0], b[1]
   int M, N, K;
   int outputs, phases;   // 1 or 2; not both 2
-  int tile;              // 64 or 128
   int splits;
   float* out[2];         // [splits][M][N]
 };
 cudaError_t launch_gemm_f32(const GemmF32Args& g, cudaStream_t st);
-// Tile and shares of k that fill the GPU.
-void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms, int* tile,
-               int* splits);
+// Shares of k that fill the GPU.
+int share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms);
 
 }  // namespace cpattn

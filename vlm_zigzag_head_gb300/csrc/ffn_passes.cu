@@ -68,19 +68,21 @@ __global__ void __launch_bounds__(256) f32_join_kernel(const __grid_constant__ F
   }
 }
 
-// Tiles of 128 x 128 (256 threads) or 64 x 64 (64 threads), 8 x 8 sums a thread, k by
-// 16 through shared memory, two multiply-adds an instruction.  Bound by the loads from
-// shared memory, whose 64 bytes a thread and k take as long as its 64 multiply-adds: 45
-// to 52 TFLOP/s with the larger tile, 38 to 45 with the smaller (a library's 57 to 64).
-// The smaller one where the larger would leave SMs idle (two products 517 x 1360 by
-// 512: 45 us; the larger tile's 110 blocks took 60).  Calls of more than kSimtRows rows
-// take the tensor cores instead.
+// Tiles of 64 x 64 (64 threads), 8 x 8 sums a thread, k by 16 through shared memory, two
+// multiply-adds an instruction.  Bound by the loads from shared memory, whose 64 bytes a
+// thread and k take as long as its 64 multiply-adds: 64 rows, forward with the joins, 36
+// TFLOP/s (2048 x 6144, 134 us) and 42 (4096 x 12288, 456 us).  Tiles of 128 x 128 where
+// they fill the GPU gained up to 1 % in weights' gradients of 64 rows (4096 x 12288: 562 us,
+// 560 so) and lost 7 to 10 % for 1 to 32 (32 rows 365 and 395) and, half empty, 40 % of the
+// forward beside wide hidden layers (64 x 8192 x 28672: 2063 and 2916).  Calls of more than
+// kSimtRows rows take the tensor cores instead.
 constexpr int kStep = 16;
 
-template <int kTile>
-__global__ void __launch_bounds__(kTile == 128 ? 256 : 64, kTile == 128 ? 2 : 8)
+constexpr int kTile = 64, kSide = kTile / 8, kThreads = kSide * kSide;
+
+__global__ void __launch_bounds__(kThreads, 8)
     gemm_f32_kernel(const __grid_constant__ GemmF32Args g) {
-  constexpr int kSide = kTile / 8, kThreads = kSide * kSide, kPitch = kTile + 4;
+  constexpr int kPitch = kTile + 4;
   constexpr int kLoads = kTile * kStep / 4 / kThreads;   // 16-byte pieces a thread loads
   __shared__ __align__(16) float as[2][kStep][kPitch], bs[2][kStep][kPitch];
   const int tid = threadIdx.x, tx = tid % kSide, ty = tid / kSide;
@@ -309,27 +311,23 @@ cudaError_t launch_f32_join(const F32JoinArgs& j, int epilogue, cudaStream_t st)
   return cudaGetLastError();
 }
 
-void share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms, int* tile,
-               int* splits) {
-  auto tiles = [&](int t) { return ((M + t - 1) / t) * ((N + t - 1) / t) * outputs; };
-  *splits = 1;
-  *tile = tiles(128) >= 2 * sms ? 128 : 64;
-  if (*tile == 128 || tiles(64) == 0) return;
+int share_f32(int64_t M, int64_t N, int64_t K, int outputs, int phases, int sms) {
+  const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile) * outputs;
+  if (tiles == 0) return 1;
   // eight blocks of 64 threads an SM, of four steps at least
   const int64_t steps = (K + kStep - 1) / kStep * phases;
-  int64_t s = 8 * (int64_t)sms / tiles(64);
+  int64_t s = 8 * (int64_t)sms / tiles;
   if (s > steps / 4) s = steps / 4;
   if (s > 64) s = 64;
-  if (s > 1) *splits = (int)s;
+  return s > 1 ? (int)s : 1;
 }
 
 cudaError_t launch_gemm_f32(const GemmF32Args& g, cudaStream_t st) {
-  const int64_t nt = ((int64_t)g.N + g.tile - 1) / g.tile;
+  const int64_t nt = ((int64_t)g.N + kTile - 1) / kTile;
   if (nt > 65535 || g.splits * g.outputs > 65535) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)(((int64_t)g.M + g.tile - 1) / g.tile), (unsigned)nt,
+  const dim3 grid((unsigned)(((int64_t)g.M + kTile - 1) / kTile), (unsigned)nt,
                   (unsigned)(g.splits * g.outputs));
-  if (g.tile == 128) gemm_f32_kernel<128><<<grid, 256, 0, st>>>(g);
-  else gemm_f32_kernel<64><<<grid, 64, 0, st>>>(g);
+  gemm_f32_kernel<<<grid, kThreads, 0, st>>>(g);
   return cudaGetLastError();
 }
 
