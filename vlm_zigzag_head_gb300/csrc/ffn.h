@@ -11,7 +11,7 @@ namespace cpattn {
 enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
 
 // 2-D tensor map over an [rows][cols] matrix of elements of 1, 2 (bf16) or 4 (fp32)
-// bytes with a row stride in elements (whole 16-byte pieces), box rows of 32, 64 or 128
+// bytes with a row stride in elements (whole 16-byte pieces), box rows of 64 or 128
 // bytes in the swizzle of that size.
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                       int64_t stride, int elem, int box_cols, int box_rows, const char** err);

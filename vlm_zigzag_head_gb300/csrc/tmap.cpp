@@ -98,7 +98,7 @@ bool make_tmap_ld(CUtensorMap* map, const void* base, int64_t pitch, int H, int 
 }
 
 // dims (innermost first): {cols, rows}; box {box_cols, box_rows}, whose rows are laid out
-// in the swizzle of their size (32, 64 or 128 bytes).
+// in the swizzle of their size (64 or 128 bytes).
 bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                       int64_t stride, int elem, int box_cols, int box_rows, const char** err) {
   auto fn = encode_fn();
@@ -110,9 +110,8 @@ bool make_tmap_matrix(CUtensorMap* map, const void* base, int64_t rows, int64_t 
                                    : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const int row = box_cols * elem;
-  const CUtensorMapSwizzle swizzle = row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                     : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                 : CU_TENSOR_MAP_SWIZZLE_32B;
+  const CUtensorMapSwizzle swizzle =
+      row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)stride * elem};
   cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
