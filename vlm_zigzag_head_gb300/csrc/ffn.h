@@ -1,5 +1,5 @@
-// Gated feed-forward block: its matrix products (tensor cores for bf16, CUDA cores
-// for fp32) and the passes between them (kernel launchers).
+// Gated feed-forward block: its matrix products (on tensor cores; fp32 ones of up to
+// kSimtRows rows on CUDA cores) and the passes between them (kernel launchers).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -3,10 +3,11 @@
 // Bound by the weights, which are read once: 6 D F bytes in bf16.  A CTA takes 16 rows
 // of each of two matrices (16 hidden units of gate and up, or 32 output columns),
 // which are the M side of mma.sync; the eight tokens are its N side.  (The tiles of 256
-// rows of the large products take 41 us for one token, 2048 x 6144; this takes 13, its
-// bytes 11.  From nine tokens on the older matrix instructions are what bounds it: 83 us
-// for 16 tokens, 4096 x 12288, against 72 by the tiles.)  Two launches, the second's
-// first loads in flight while the first ends.
+// rows of the large products take 41 us for one token, 2048 x 6144; this takes 12 from
+// memory and 11 where L2 holds the weights, whose bytes are 11.3 at a copy's rate.  From
+// nine tokens on the older matrix instructions are what bounds it: 83 us for 16 tokens,
+// 4096 x 12288, where ffn_tokens.cu takes 54.)  Two launches, the second's first loads in
+// flight while the first ends.
 //
 // Operands go from memory straight into fragments: k may be permuted as long as both
 // operands agree, so a lane takes 16 consecutive bytes of a row, eight k, as its

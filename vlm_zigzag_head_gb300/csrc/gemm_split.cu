@@ -13,10 +13,11 @@
 // and its sums are added in fp32 registers; and the five small products, whose steps would
 // cut off the large one's sum, have sums of their own (together 2.3e-6 at 512 k, apart 2.4e-7, fp32 sums 4e-7; at 4096 k 2.6e-7 and 1.2e-6).
 //
-// Six bf16 products are quicker than one on CUDA cores: 2048 x 2048 x 6144 forward 751 us
-// (1236 TFLOP/s of bf16, 206 of fp32), on CUDA cores 3364.  Up to kSimtRows rows the planes
-// of the weights cost more than that saves (64 rows: forward 161 us and 139; 128 rows: 164
-// and 241; backward 231 and 250, 266 and 444).
+// Six bf16 products are quicker than one on CUDA cores: 2048 x 2048 x 6144 forward 761 us
+// (1219 TFLOP/s of bf16, 203 of fp32), on CUDA cores 3364.  Up to kSimtRows rows the planes
+// of the weights cost the forward more than that saves (2048 x 6144, 64 rows: 163 us, on
+// CUDA cores 134; 128 rows: 165 and 238); its backward is about as long either way (64 rows:
+// 229 and 240; 128 rows: 268 and 442).
 //
 // Pairs of CTAs as in gemm_bf16.cu, tiles of 256 x 128 (gate and up: 64 columns of each).
 // A slot of shared memory holds a 64 deep tile of one plane of A and of B; each of the
