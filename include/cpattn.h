@@ -496,7 +496,8 @@ cp_status_t cp_layer_norm_bwd(const cp_layer_norm_t* desc, const void* x, const 
  *   dx, dw_*        NULL: not wanted, and its product is left out
  *   workspace       >= cp_gated_ffn_{fwd,bwd}_workspace_size(desc) bytes, 256-byte
  *                   aligned, of this call's own while it runs; its status word is
- *                   read by cp_workspace_status
+ *                   read by cp_workspace_status, and alone says whether a bounded
+ *                   wait ran out, which leaves results unwritten
  * Every pointer 16-byte aligned, row strides whole 16-byte pieces.  D, F and D_out are
  * multiples of 8; T is any number.  Sums do not depend on timing.  Every call is
  * launches and memsets alone, so it can be captured into a graph.  T == 0: no rows are

@@ -23,7 +23,7 @@ from typing import Callable, Optional, Sequence
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import CpError, ScorePlan, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
+from . import CpError, ScorePlan, Workspace, cp_attn_bwd, cp_attn_fwd, norm_rope, scored
 from . import _binding as _b
 from . import ffn as _ffn
 from . import layer_norm as _layer_norm
@@ -225,13 +225,15 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
 
 
 class GatedFfn(torch.autograd.Function):
-    """``y = GatedFfn.apply(x, w_gate, w_up, w_down, activation)`` on 16-byte aligned rows."""
+    """``y = GatedFfn.apply(x, w_gate, w_up, w_down, activation, workspace)`` on 16-byte aligned
+    rows."""
 
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, w_down, activation):
-        y, gate, up = _ffn.cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation, keep=True)
+    def forward(ctx, x, w_gate, w_up, w_down, activation, workspace):
+        y, gate, up = _ffn.cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation, keep=True,
+                                            workspace=workspace)
         ctx.save_for_backward(x, w_gate, w_up, w_down, gate, up)
-        ctx.activation = activation
+        ctx.activation, ctx.workspace = activation, workspace
         ctx.set_materialize_grads(False)
         return y
 
@@ -239,26 +241,31 @@ class GatedFfn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         if dy is None:   # what used y has no gradient for it
-            return (None,) * 5
+            return (None,) * 6
         # saved tensors may come back elsewhere and with other strides (offloaded, recomputed)
         x, w_gate, w_up, w_down, gate, up = (_ffn._aligned(t) for t in ctx.saved_tensors)
         return (*_ffn.cp_gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, _ffn._aligned(dy),
                                        ctx.activation, grad_dtype=x.dtype,
-                                       wanted=ctx.needs_input_grad[:4]), None)
+                                       wanted=ctx.needs_input_grad[:4],
+                                       workspace=ctx.workspace), None, None)
 
 
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, *,
-              activation: str = "silu"):
+              activation: str = "silu", workspace: Optional[Workspace] = None):
     """Differentiable :func:`~vlm_zigzag_head_gb300.cp_gated_ffn_fwd`: (a(x w_gate^T) * (x
     w_up^T)) w_down^T of the last dimension of ``x [..., D]``, with ``a`` one of ``"silu"``,
     ``"gelu"``, ``"gelu_tanh"``.  Tensors whose rows do not lie on 16-byte boundaries are
     copied.  Gradients flow to x and the weights (backward only: forward mode raises); a
     gradient that is not needed is not computed.  To capture the backward into a graph, call
-    :func:`~vlm_zigzag_head_gb300.cp_gated_ffn_bwd`, which involves no leaves."""
+    :func:`~vlm_zigzag_head_gb300.cp_gated_ffn_bwd`, which involves no leaves.
+
+    With ``workspace`` both directions use it (their calls then belong on one stream), and
+    :func:`~vlm_zigzag_head_gb300.cp_workspace_status` tells of the last of them whether a
+    bounded device wait ran out, which leaves its results unwritten; without one nothing does."""
     x, w_gate, w_up, w_down = (_ffn._aligned(t) for t in (x, w_gate, w_up, w_down))
     if not _wants_grad(x, w_gate, w_up, w_down):
-        return _ffn.cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation)
-    return GatedFfn.apply(x, w_gate, w_up, w_down, activation)
+        return _ffn.cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation, workspace=workspace)
+    return GatedFfn.apply(x, w_gate, w_up, w_down, activation, workspace)
 
 
 class CPAttentionScored(torch.autograd.Function):

@@ -98,7 +98,8 @@ def cp_gated_ffn_fwd(x, w_gate, w_up, w_down, activation: str = "silu", *, keep:
     8; rows of any stride that lie on 16-byte boundaries.  With ``keep`` returns ``(y, gate,
     up)``, the two projections for :func:`cp_gated_ffn_bwd` as byte tensors in the library's
     layout (bf16: to 24 bits).  Without ``workspace`` each call takes one of its own, so calls
-    on several streams may overlap."""
+    on several streams may overlap; whether a bounded device wait ran out, which leaves results
+    unwritten, is known from a caller's workspace alone (:func:`cp_workspace_status`)."""
     rows = _rows(x, "x")
     f, sizes = _prepare(rows, w_gate, w_up, w_down, activation, _dt(rows))
     device, lead = x.device, x.shape[:-1]
@@ -120,7 +121,7 @@ def cp_gated_ffn_bwd(x, w_gate, w_up, w_down, gate, up, dy, activation: str = "s
                      workspace: Optional[Workspace] = None):
     """Gradient of :func:`cp_gated_ffn_fwd` (``gate``, ``up``: what it kept): ``(dx, dw_gate,
     dw_up, dw_down)``, None where ``wanted`` says so.  dx has x's dtype; the weights'
-    gradients have ``grad_dtype``: fp32, or bf16 for bf16 inputs."""
+    gradients have ``grad_dtype``: fp32, or bf16 for bf16 inputs.  ``workspace`` as in the forward."""
     if len(wanted) != 4:
         raise CpError(2, "wanted must say yes or no to dx, dw_gate, dw_up and dw_down")
     rows, g = _rows(x, "x"), _rows(dy, "dy")
